@@ -70,8 +70,23 @@ extern "C" {
  *                            other fp8 format (its Risks name other scale
  *                            granularities as the next modes)
  *
+ *   KVQ_INT4_PER_TOKEN_HEAD  4-bit codes + inline two-level scales, row =
+ *                            D/2 + 16 bytes (D a multiple of 64).  No
+ *                            counterpart on the pages ([P3]'s Risks name
+ *                            other scale granularities as the next modes).
+ *
  * Per-token-head row layout: [D codes][scale: little-endian fp32][12 zero
  * bytes]; the 16-byte pad keeps every row 16-byte aligned.
+ *
+ * 4-bit row layout: [D/2 code bytes][s: little-endian fp32][m_0 .. m_7:
+ * uint8][4 zero bytes].  A row has eight groups of D/8 consecutive dims; the
+ * element of group g with code c stands for s * (m_g * c), c in [-7, 7] and
+ * m_g in [0, 127], so m_g * c is an integer of at most 10 bits (exact in
+ * 16-bit floating point) and all rounding of a dequantised value lies in the
+ * one fp32 scale of its row.  Nibble j (bits 4j .. 4j + 3) of the w-th
+ * little-endian 32-bit code word holds c + 8 of dim 8 w + 2 j for j < 4 and
+ * of dim 8 w + 2 (j - 4) + 1 for j >= 4: masking a word by 0x000F000F << 4k
+ * selects two consecutive dims in the two 16-bit halves.
  */
 typedef enum {
   KVQ_AUTO = 0,
@@ -79,7 +94,8 @@ typedef enum {
   KVQ_FP8_E5M2 = 2,
   KVQ_INT8_PER_TOKEN_HEAD = 3,
   KVQ_FP8_PER_TOKEN_HEAD = 4,
-  KVQ_FP8_E5M2_PER_TOKEN_HEAD = 5
+  KVQ_FP8_E5M2_PER_TOKEN_HEAD = 5,
+  KVQ_INT4_PER_TOKEN_HEAD = 6
 } kvq_dtype_t;
 
 /* Opaque schedule (work list + sizes), owned by the library. */
@@ -87,17 +103,19 @@ typedef struct kvq_sched kvq_sched_t;
 
 /* Parse a kv_cache_dtype string.  Accepts "auto" (the default of [P2]
  * Breakdown item 2), "fp8" (alias of fp8_e4m3), "fp8_e4m3", "fp8_e5m2",
- * "int8_per_token_head", "fp8_per_token_head", "fp8_e5m2_per_token_head".
+ * "int8_per_token_head", "fp8_per_token_head", "fp8_e5m2_per_token_head",
+ * "int4_per_token_head".
  * s == NULL or "" reads as
  * "auto".  Unknown strings: KVQ_E_INVALID_ARG. */
 KVQ_API int kvq_parse_kv_cache_dtype(const char* s, kvq_dtype_t* out);
 
-/* Bytes of one (token, kv_head) cache row: 2*D (AUTO), D (per-tensor fp8)
- * or D+16 (per-token-head).  [P3] Risks: the per-token-head scale is stored
+/* Bytes of one (token, kv_head) cache row: 2*D (AUTO), D (per-tensor fp8),
+ * D+16 (per-token-head) or D/2+16 (4-bit per-token-head).  [P3] Risks: the per-token-head scale is stored
  * inline by padding the head size (here by 16 bytes: the fp32 scale and 12
  * zero bytes, so every row stays 16-byte aligned); [P1] Risks: an fp8 row
  * is half the bytes of a bf16 one.  head_dim must be a positive multiple
- * of 16; KVQ_E_INVALID_ARG otherwise, or for an unknown dtype. */
+ * of 16 (of 64 for the 4-bit rows); KVQ_E_INVALID_ARG otherwise, or for an
+ * unknown dtype. */
 KVQ_API int kvq_cache_row_bytes(kvq_dtype_t dtype, int head_dim, size_t* out);
 
 /* reshape_and_cache -- quantise new K/V tokens into the paged caches.
@@ -125,7 +143,12 @@ KVQ_API int kvq_cache_row_bytes(kvq_dtype_t dtype, int head_dim, size_t* out);
  * Per-token-head: s = amax/qmax in fp32 (qmax 127 for int8, 448 for fp8
  * e4m3, 57344 for fp8 e5m2),
  * code = Q(x / s) (int8: round half to even, clamp [-128,127]); s == 0 gives
- * zero codes.  Inputs must be finite.  num_tokens == 0 is a no-op. */
+ * zero codes.
+ * 4-bit per-token-head: s = amax / 889 (889 = 7 * 127, amax over the row),
+ * m_g = min(127, ceil((amax_g / s) / 7)) (amax_g over group g; 0 when s is),
+ * code = clamp(rint(x / (s * m_g)), -7, 7) (half to even; 0 when s * m_g is
+ * 0), every division and product a correctly rounded fp32 one.
+ * Inputs must be finite.  num_tokens == 0 is a no-op. */
 KVQ_API int kvq_reshape_and_cache(const void* key, const void* value,
                           int64_t num_tokens, int64_t key_stride_tok,
                           int64_t value_stride_tok, int num_heads_kv,
@@ -427,7 +450,8 @@ KVQ_API void kvq_sched_destroy(kvq_sched_t* sched);
 typedef struct {
   int num_req, heads_q, heads_kv, head_dim;
   int dtype;                   /* kvq_dtype_t the schedule was built for      */
-  int kv_elem_bytes;           /* bytes per cached K/V element (1 or 2)       */
+  int kv_elem_bytes;           /* bytes per cached K/V element (1 or 2; 4-bit
+                                  codes count as the byte they share)         */
   int row_bytes;               /* bytes per (token, kv_head) cache row        */
   int causal, window;
   int64_t num_tiles;           /* row tiles: <= 16 (query, head) rows of a kv head */

@@ -9,8 +9,8 @@
 // [block][slot][kv_head][row] and each (token, head) row is handled by
 // D/8 threads, each with one 16-byte load of K and of V (kvq_cache_row.cuh).
 //
-// HBM bound: per element 2 bytes read, 1 byte written (+16 bytes of scale
-// per row per-token-head).
+// HBM bound: per element 2 bytes read, 1 byte written (half a byte for 4-bit
+// codes; +16 bytes of scales per row per-token-head).
 #include <cuda_runtime.h>
 
 #include "kvq_cache_row.cuh"
@@ -101,6 +101,7 @@ int launch_reshape_and_cache(const void* key, const void* value, int64_t num_tok
     KVQ_CACHE_CASE(KVQ_INT8_PER_TOKEN_HEAD)
     KVQ_CACHE_CASE(KVQ_FP8_PER_TOKEN_HEAD)
     KVQ_CACHE_CASE(KVQ_FP8_E5M2_PER_TOKEN_HEAD)
+    KVQ_CACHE_CASE(KVQ_INT4_PER_TOKEN_HEAD)
     default:
       return KVQ_E_UNSUPPORTED;
   }

@@ -47,6 +47,22 @@ __device__ __forceinline__ float absmax8(const uint4 x) {
   return m;
 }
 
+// 4-bit codes: an element's code + 8 under its group's step s * m_g.
+__device__ __forceinline__ uint32_t enc_int4(float x, float step) {
+  const int v = __float2int_rn(__fdiv_rn(x, step));
+  return (uint32_t)(max(-7, min(7, v)) + 8);
+}
+// Eight consecutive elements' code word: element e in nibble e / 2, the odd
+// ones four nibbles up.
+__device__ __forceinline__ uint32_t quantise8_int4(const uint4 x, float step) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t code = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    code |= enc_int4(dev::bf16_lo(w[i]), step) << (4 * i) | enc_int4(dev::bf16_hi(w[i]), step) << (4 * i + 16);
+  return code;
+}
+
 // Writes one row's share (8 elements) of codes, and for per-token-head the
 // scale tail.  TPR threads (a power of two, aligned in the warp) own a row.
 template <int DT, int TPR>
@@ -59,6 +75,33 @@ __device__ __forceinline__ void write_part(const uint4 x, float tensor_scale, ui
     uint32_t lo, hi;
     quantise8<DT>(x, tensor_scale, lo, hi);
     if (active) *reinterpret_cast<uint2*>(row + part * 8) = make_uint2(lo, hi);
+  } else if constexpr (is_int4(DT)) {
+    // A group is D / 8 dims: GT threads of the row.
+    constexpr int GT = TPR / 8;
+    float mg = absmax8(x);
+#pragma unroll
+    for (int off = 1; off < GT; off <<= 1) mg = fmaxf(mg, __shfl_xor_sync(0xffffffffu, mg, off));
+    float m = mg;
+#pragma unroll
+    for (int off = GT; off < TPR; off <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    const float s = __fdiv_rn(m, kInt4Levels);
+    uint32_t mul = 0, code = 0x88888888u;
+    if (s > 0.0f) {
+      mul = (uint32_t)fminf(kInt4MaxMul, ceilf(__fdiv_rn(__fdiv_rn(mg, s), kInt4MaxCode)));
+      const float step = __fmul_rn(s, (float)mul);
+      if (step > 0.0f) code = quantise8_int4(x, step);
+    }
+    // the four multipliers of each half of the row in one word: {s, m_0..3}
+    // and {m_4..7, 0} go out as two 8-byte stores of the halves' first threads
+    uint32_t word = mul << (8 * ((part / GT) & 3));
+    word |= __shfl_xor_sync(0xffffffffu, word, GT);
+    word |= __shfl_xor_sync(0xffffffffu, word, 2 * GT);
+    if (active) {
+      *reinterpret_cast<uint32_t*>(row + part * 4) = code;
+      if (part % (TPR / 2) == 0)
+        *reinterpret_cast<uint2*>(row + kRowCodes / 2 + (part == 0 ? 0 : 8)) =
+            part == 0 ? make_uint2(__float_as_uint(s), word) : make_uint2(word, 0u);
+    }
   } else {
     float m = absmax8(x);
 #pragma unroll

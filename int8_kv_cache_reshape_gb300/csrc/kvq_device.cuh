@@ -106,6 +106,38 @@ __device__ __forceinline__ void word_to_f16x2x2(uint32_t w, uint32_t& lo, uint32
   }
 }
 
+// ---- 4-bit codes -> f16x2 (exact) --------------------------------------------
+// A nibble u = code + 8 left where it lies in the low byte of a 16-bit half is
+// the subnormal f16 u * 2^-24 (bits 0-3) or u * 2^-20 (bits 4-7): one masking
+// and one fused multiply-add give (u - 8) m 2^-15 = u 2^-24 (m 2^9) - 8 m
+// 2^-15 (bits 4-7: u 2^-20 (m 2^5)), an integer of at most 10 bits times
+// 2^-15, so exact.  The users multiply their fp32 sums by kInt4Unit.
+constexpr float kInt4Unit = 32768.0f;
+struct Int4Mul {
+  uint32_t lo, hi, add;  // f16 pairs: m 2^9, m 2^5, -m 2^-12
+};
+__device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+// The multipliers' factors from f16 pairs 1024 + m (m <= 127; all exact).
+__device__ __forceinline__ Int4Mul int4_mul(uint32_t biased) {
+  Int4Mul f;
+  f.hi = fma_f16x2(biased, 0x50005000u, 0xF800F800u);   // 32 x - 32768
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(f.lo) : "r"(f.hi), "r"(0x4C004C00u));  // 16 (32 m)
+  f.add = fma_f16x2(biased, 0x8C008C00u, 0x34003400u);  // -2^-12 x + 2^-2
+  return f;
+}
+// The eight nibbles of a word, pairs of bits (4k, 4k + 16), k = 0..3.
+__device__ __forceinline__ void int4_to_f16x2x4(uint32_t w, const Int4Mul& f, uint32_t (&v)[4]) {
+  const uint32_t w8 = w >> 8;
+  v[0] = fma_f16x2(w & 0x000F000Fu, f.lo, f.add);
+  v[1] = fma_f16x2(w & 0x00F000F0u, f.hi, f.add);
+  v[2] = fma_f16x2(w8 & 0x000F000Fu, f.lo, f.add);
+  v[3] = fma_f16x2(w8 & 0x00F000F0u, f.hi, f.add);
+}
+
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -175,8 +207,31 @@ __device__ __forceinline__ uint4 ldg_stream(const void* p) {
   return v;
 }
 
-// The same without the non-coherent path: for data that other CTAs of the
-// same kernel wrote before a grid barrier.
+// 8- and 4-byte forms of the same.
+__device__ __forceinline__ uint2 ldg_stream8(const void* p) {
+  uint2 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint2 ldg_stream8_coherent(const void* p) {
+  uint2 v;
+  asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint32_t ldg_stream4(const void* p) {
+  uint32_t v;
+  asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint32_t ldg_stream4_coherent(const void* p) {
+  uint32_t v;
+  asm volatile("ld.global.L1::no_allocate.u32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+
+// The 16-byte load without the non-coherent path (as the _coherent forms
+// above): for data that other CTAs of the same kernel wrote before a grid
+// barrier.
 __device__ __forceinline__ uint4 ldg_stream_coherent(const void* p) {
   uint4 v;
   asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"

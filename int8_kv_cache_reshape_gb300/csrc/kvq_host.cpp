@@ -290,11 +290,13 @@ int kvq_parse_kv_cache_dtype(const char* s, kvq_dtype_t* out) {
     *out = KVQ_FP8_E5M2_PER_TOKEN_HEAD;
     return KVQ_OK;
   }
+  if (!std::strcmp(s, "int4_per_token_head")) { *out = KVQ_INT4_PER_TOKEN_HEAD; return KVQ_OK; }
   return KVQ_E_INVALID_ARG;
 }
 
 int kvq_cache_row_bytes(kvq_dtype_t dtype, int head_dim, size_t* out) {
-  if (!out || !kvq::is_valid_dtype(dtype) || head_dim <= 0 || head_dim % 16)
+  if (!out || !kvq::is_valid_dtype(dtype) || head_dim <= 0 ||
+      head_dim % (kvq::is_int4(dtype) ? 64 : 16))
     return KVQ_E_INVALID_ARG;
   *out = (size_t)kvq::row_bytes(dtype, head_dim);
   return KVQ_OK;

@@ -35,14 +35,15 @@ namespace kvq {
 // ---- cache rows --------------------------------------------------------
 KVQ_HD constexpr bool is_per_token_head(int dtype) {
   return dtype == KVQ_INT8_PER_TOKEN_HEAD || dtype == KVQ_FP8_PER_TOKEN_HEAD ||
-         dtype == KVQ_FP8_E5M2_PER_TOKEN_HEAD;
+         dtype == KVQ_FP8_E5M2_PER_TOKEN_HEAD || dtype == KVQ_INT4_PER_TOKEN_HEAD;
 }
-KVQ_HD constexpr bool is_valid_dtype(int dtype) { return dtype >= 0 && dtype <= 5; }
-// The code format of a quantised dtype: KVQ_FP8_E4M3, KVQ_FP8_E5M2 or
-// KVQ_INT8_PER_TOKEN_HEAD (int8 codes).
+KVQ_HD constexpr bool is_valid_dtype(int dtype) { return dtype >= 0 && dtype <= 6; }
+KVQ_HD constexpr bool is_int4(int dtype) { return dtype == KVQ_INT4_PER_TOKEN_HEAD; }
+// The code format of a quantised dtype: KVQ_FP8_E4M3, KVQ_FP8_E5M2,
+// KVQ_INT8_PER_TOKEN_HEAD (int8 codes) or KVQ_INT4_PER_TOKEN_HEAD (4-bit).
 KVQ_HD constexpr int code_format(int dtype) {
   return dtype == KVQ_FP8_E5M2 || dtype == KVQ_FP8_E5M2_PER_TOKEN_HEAD ? KVQ_FP8_E5M2
-         : dtype == KVQ_INT8_PER_TOKEN_HEAD                          ? KVQ_INT8_PER_TOKEN_HEAD
+         : dtype == KVQ_INT8_PER_TOKEN_HEAD || is_int4(dtype)          ? dtype
                                                                       : KVQ_FP8_E4M3;
 }
 // Largest code magnitude a per-token-head scale maps the row's absmax to.
@@ -50,13 +51,23 @@ KVQ_HD constexpr float per_token_head_qmax(int dtype) {
   return dtype == KVQ_INT8_PER_TOKEN_HEAD ? 127.0f
          : dtype == KVQ_FP8_E5M2_PER_TOKEN_HEAD ? 57344.0f : 448.0f;
 }
-// Bytes of one cached K or V element (the KV element size).
+// Bytes of one cached K or V element (the KV element size; a 4-bit code
+// counts as the byte it shares).
 KVQ_HD constexpr int kv_elem_bytes(int dtype) { return dtype == KVQ_AUTO ? 2 : 1; }
-// Bytes of one (token, kv_head) row: codes plus, per-token-head, a 16-byte
-// tail holding the fp32 scale and 12 zero bytes.
-KVQ_HD constexpr int row_bytes(int dtype, int head_dim) {
-  return head_dim * kv_elem_bytes(dtype) + (is_per_token_head(dtype) ? 16 : 0);
+// Bytes of a row's codes (or bf16 values), where its scale tail starts.
+KVQ_HD constexpr int code_bytes(int dtype, int head_dim) {
+  return is_int4(dtype) ? head_dim / 2 : head_dim * kv_elem_bytes(dtype);
 }
+// Bytes of one (token, kv_head) row: codes plus, per-token-head, a 16-byte
+// tail holding the fp32 scale and 12 zero bytes (4-bit: 8 group multipliers
+// and 4 zero bytes).
+KVQ_HD constexpr int row_bytes(int dtype, int head_dim) {
+  return code_bytes(dtype, head_dim) + (is_per_token_head(dtype) ? 16 : 0);
+}
+// 4-bit rows: a row's scale is amax / kInt4Levels, its eight groups of
+// head_dim / 8 dims have integer multipliers up to kInt4MaxMul, codes reach
+// +-kInt4MaxCode (kInt4Levels = kInt4MaxCode * kInt4MaxMul).
+constexpr float kInt4MaxCode = 7.0f, kInt4MaxMul = 127.0f, kInt4Levels = 889.0f;
 KVQ_HD constexpr bool head_dim_supported(int d) { return d == 64 || d == 128 || d == 256; }
 // Dtypes with built attention kernels: all of them (the bf16 "auto" cache
 // reads its rows as they are).
@@ -78,7 +89,7 @@ constexpr int kMinChunksPerWarp = 8;  // smallest segment worth a warp
 // Bytes of one 16-token chunk of K and V codes (plus the per-token-head
 // scale tails) -- what a warp loads per step, straight into registers.
 KVQ_HD constexpr int decode_chunk_bytes(int dtype, int head_dim) {
-  return 2 * kChunkTokens * head_dim * kv_elem_bytes(dtype) +
+  return 2 * kChunkTokens * code_bytes(dtype, head_dim) +
          (is_per_token_head(dtype) ? 32 * 16 : 0);
 }
 // Resident CTAs per SM the kernel is compiled for (register budget): a

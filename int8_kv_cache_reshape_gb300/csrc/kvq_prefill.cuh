@@ -24,8 +24,9 @@
 //     straight into the K and V operand tiles.
 //   * Converter warps (1-3, and 8 up to the copy warp): a thread takes (key,
 //     16 codes) units, loads the codes from global memory one KV tile ahead,
-//     converts them exactly to f16 (every e4m3 / e5m2 / int8 value is an f16
-//     value) and stores them as key-major rows in the 128-byte swizzle into a
+//     converts them exactly to f16 (every e4m3 / e5m2 / int8 value, and every
+//     4-bit code times its group's multiplier, is an f16 value; a 4-bit
+//     unit is 8 code bytes and its multipliers) and stores them as key-major rows in the 128-byte swizzle into a
 //     two-stage K ring and V ring.  K is read by the tensor core K-major, V
 //     MN-major, so neither needs a transpose.  Step i converts K(i) (its
 //     buffer is free once S(i-2) is complete) and then V(i-1) (free once
@@ -86,6 +87,7 @@ struct PrefillGeom {
   static constexpr int kConv = prefill_conv_threads(D);
   static constexpr int kStages = kPrefillStages;
   static constexpr bool kPth = is_per_token_head(DT);
+  static constexpr bool kInt4 = is_int4(DT);
   // CTA pair (kCG = 2): this CTA holds keys [r * kN / 2, (r + 1) * kN / 2) of
   // each K tile (all D dims) and dims [r * D / 2, (r + 1) * D / 2) of each V
   // tile (all kN keys), r its rank in the cluster.
@@ -239,13 +241,20 @@ __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, vol
   }
 }
 
-// 8 codes (two words) -> 8 f16 (four f16x2 words), exact.
+// 8 codes (two words; 4-bit: one word and its group's multiplier) -> 8 f16
+// (four f16x2 words), exact.
 template <int DT>
 __device__ __forceinline__ uint4 codes8_to_f16(uint32_t w0, uint32_t w1) {
-  uint4 h;
-  dev::word_to_f16x2x2<DT>(w0, h.x, h.y);
-  dev::word_to_f16x2x2<DT>(w1, h.z, h.w);
-  return h;
+  if constexpr (is_int4(DT)) {
+    uint32_t v[4];
+    dev::int4_to_f16x2x4(w0, dev::int4_mul(dev::prmt(w1, 0x64646464u, 0x4040u)), v);
+    return make_uint4(v[0], v[1], v[2], v[3]);
+  } else {
+    uint4 h;
+    dev::word_to_f16x2x2<DT>(w0, h.x, h.y);
+    dev::word_to_f16x2x2<DT>(w1, h.z, h.w);
+    return h;
+  }
 }
 
 // This CTA's k-th tile: the longest-first tile list dealt out over the grid
@@ -757,7 +766,18 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
         if (ctid + i * Geo::kConv < kUnits && ((valid >> (n >> 4)) & 1u) && n >= (int)(win & 0xFFFFu) &&
             n < (int)(win >> 16)) {
           const int64_t slot = table[e * 16 + (n >> 4)] + (n & 15);
-          dst[i] = dev::ldg_stream(cache + (slot * p.heads_kv + head) * kRow + (un.code_off[i] & (D - 1)));
+          const uint8_t* row = cache + (slot * p.heads_kv + head) * kRow;
+          const uint32_t dim = un.code_off[i] & (D - 1);
+          if constexpr (Geo::kInt4) {
+            // {dims 0-7, their multiplier, dims 8-15, theirs} of the unit (the
+            // row's tail is a sector its codes' units bring in as well)
+            const uint2 w = dev::ldg_stream8(row + dim / 2);
+            const uint8_t* mul = row + D / 2 + 4 + dim / (D / 8);
+            const uint32_t m0 = __ldg(mul), m1 = D == 64 ? (uint32_t)__ldg(mul + 1) : m0;
+            dst[i] = make_uint4(w.x, m0, w.y, m1);
+          } else {
+            dst[i] = dev::ldg_stream(row + dim);
+          }
         }
       }
       return valid;
@@ -769,7 +789,8 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
       if constexpr (Geo::kPth) {
         const int n = ctid;
         if (n < kN && ((valid >> (n >> 4)) & 1u) && n >= (int)(win & 0xFFFFu) && n < (int)(win >> 16)) {
-          const int64_t off = ((int64_t)(table[e * 16 + (n >> 4)] + (n & 15)) * p.heads_kv + head) * kRow + D;
+          const int64_t off = ((int64_t)(table[e * 16 + (n >> 4)] + (n & 15)) * p.heads_kv + head) * kRow +
+                              code_bytes(DT, D);
           ks = __ldg(reinterpret_cast<const float*>(p.key_cache + off));
           vs = __ldg(reinterpret_cast<const float*>(p.value_cache + off));
         }
@@ -1009,8 +1030,11 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
       const int row_hi = row_valid ? (p.causal ? pos + 1 : t.kv_hi) : 0;  // padding rows see nothing
       const int row_lo = W > 0 ? pos - W + 1 : 0;
       // scores in log2 units (natural units under a soft cap, which converts)
-      const float score_mul = p.sm_scale * q_unscale * (cap > 0.0f ? 1.0f : log2e) *
-                              (Geo::kPth || Geo::kAuto ? 1.0f : p.k_scale);
+      // (4-bit rows enter the MMAs as multiples of 1 / kInt4Unit)
+      const float score_mul = Geo::kInt4
+                                  ? p.sm_scale * dev::kInt4Unit * (cap > 0.0f ? 1.0f : log2e) * q_unscale
+                                  : p.sm_scale * q_unscale * (cap > 0.0f ? 1.0f : log2e) *
+                                        (Geo::kPth || Geo::kAuto ? 1.0f : p.k_scale);
       // ALiBi: this row's slope in log2 units (the bias uses the exact integer
       // distance key - position, added after the soft cap).
       const float al_slope = AL ? p.alibi_slopes[t.kv_head * G + R % G] * log2e : 0.0f;
@@ -1054,7 +1078,8 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
               ev = e;
             }
           }
-          v_mul = ldexpf(1.0f, -ev);
+          // (no positive scale yet: every value so far is zero)
+          v_mul = ev > -1000 ? ldexpf(1.0f, -ev) : 0.0f;
         }
         auto score = [&](auto cap_c, float r) -> float {
           if constexpr (decltype(cap_c)::value)
@@ -1261,7 +1286,8 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
       }
       uint16_t* const dst = out_row(te);
       const float sc = (l_sum > 0.0f ? 1.0f / l_sum : 0.0f) *
-                       (Geo::kPth ? (ev > -1000 ? ldexpf(1.0f, ev) : 0.0f) : Geo::kAuto ? 1.0f : p.v_scale);
+                       (Geo::kPth ? (ev > -1000 ? ldexpf(Geo::kInt4 ? dev::kInt4Unit : 1.0f, ev) : 0.0f)
+                        : Geo::kAuto ? 1.0f : p.v_scale);
       // (the previous tile's bulk copy of this row has read its staging row)
       asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
       const uint32_t orow = base + Geo::kOffOut + (uint32_t)(m * Geo::kOutPitch);
@@ -1410,6 +1436,8 @@ int launch_prefill_d(const AttnParams& p, const PrefillMaps& maps, int dtype, in
       return launch_prefill_instance<KVQ_FP8_PER_TOKEN_HEAD, D, AL>(p, maps, ctas, stream);
     case KVQ_FP8_E5M2_PER_TOKEN_HEAD:
       return launch_prefill_instance<KVQ_FP8_E5M2_PER_TOKEN_HEAD, D, AL>(p, maps, ctas, stream);
+    case KVQ_INT4_PER_TOKEN_HEAD:
+      return launch_prefill_instance<KVQ_INT4_PER_TOKEN_HEAD, D, AL>(p, maps, ctas, stream);
     default:
       return KVQ_E_UNSUPPORTED;
   }

@@ -36,6 +36,13 @@
  *     [P3] Risks applied to the e5m2 format); s == 0 gives all-zero codes.
  *     Row layout:
  *     [D codes][s as little-endian binary32][12 zero bytes].
+ *   - 4-bit rows (no counterpart on the pages; D a multiple of 64): eight
+ *     groups of D/8 dims, s = amax / 889, m_g = min(127, ceil((amax_g / s)
+ *     / 7)), code = clamp(rint(x / (s m_g)), -7, 7), each operation rounded
+ *     to binary32; the value is s * m_g * code.  Row: [D/2 code bytes]
+ *     [s][m_0 .. m_7][4 zero bytes]; byte b of the w-th four code bytes
+ *     holds code + 8 of dims 8 w + 4 b and + 2 (b < 2; low nibble, high
+ *     nibble) or 8 w + 4 (b - 2) + 1 and + 2 (b >= 2).
  *   - Paged layout: cache[block][slot_in_block][kv_head][row bytes].
  *   - Query row i of a request with Q queries and L keys sits at position
  *     L - Q + i; key j is visible iff (!causal || j <= p) and
@@ -56,10 +63,10 @@
 
 /* dtype numbering: 0..2 follow the kv_cache_dtype indices printed in [P2]'s
  * source snippet; 3 and 4 are the per-token-head modes of [P3]; 5 is the
- * per-token-head mode with e5m2 codes. */
+ * per-token-head mode with e5m2 codes; 6 the 4-bit one. */
 enum { KVO_AUTO = 0, KVO_FP8_E4M3 = 1, KVO_FP8_E5M2 = 2,
        KVO_INT8_PER_TOKEN_HEAD = 3, KVO_FP8_PER_TOKEN_HEAD = 4,
-       KVO_FP8_E5M2_PER_TOKEN_HEAD = 5 };
+       KVO_FP8_E5M2_PER_TOKEN_HEAD = 5, KVO_INT4_PER_TOKEN_HEAD = 6 };
 /* fp8 format selector for the scalar codec. */
 enum { KVO_E4M3 = 0, KVO_E5M2 = 1 };
 
@@ -163,6 +170,7 @@ int64_t kvo_row_bytes(int dtype, int head_dim) {
     case KVO_INT8_PER_TOKEN_HEAD:
     case KVO_FP8_PER_TOKEN_HEAD:
     case KVO_FP8_E5M2_PER_TOKEN_HEAD: return (int64_t)head_dim + 16;
+    case KVO_INT4_PER_TOKEN_HEAD: return head_dim % 64 ? -1 : (int64_t)head_dim / 2 + 16;
     default: return -1;
   }
 }
@@ -184,6 +192,45 @@ static float load_f32_le(const uint8_t* p) {
   return f;
 }
 
+/* Byte and shift of the 4-bit code of dim d in its row. */
+static int int4_byte(int d) {
+  int w = d / 8, i = (d % 8) / 2, odd = d % 2; /* nibble i, or i + 4 */
+  return 4 * w + 2 * odd + i / 2;
+}
+static int int4_shift(int d) { return ((d % 8) / 2) % 2 ? 4 : 0; }
+
+static void write_row_int4(const uint16_t* x, int D, uint8_t* row) {
+  float amax = 0.0f, s;
+  memset(row, 0, (size_t)(D / 2 + 16));
+  for (int d = 0; d < D; ++d) {
+    float a = fabsf(bf16_to_float(x[d]));
+    if (a > amax) amax = a;
+  }
+  s = amax / 889.0f;
+  store_f32_le(row + D / 2, s);
+  for (int g = 0; g < 8; ++g) {
+    float gmax = 0.0f, m = 0.0f, step;
+    for (int d = g * D / 8; d < (g + 1) * D / 8; ++d) {
+      float a = fabsf(bf16_to_float(x[d]));
+      if (a > gmax) gmax = a;
+    }
+    if (s > 0.0f) {
+      float r = gmax / s;
+      m = ceilf(r / 7.0f);
+      if (m > 127.0f) m = 127.0f;
+    }
+    row[D / 2 + 4 + g] = (uint8_t)m;
+    step = s * m;
+    for (int d = g * D / 8; d < (g + 1) * D / 8; ++d) {
+      float y = step > 0.0f ? bf16_to_float(x[d]) / step : 0.0f;
+      double c = rint((double)y);
+      if (c > 7.0) c = 7.0;
+      if (c < -7.0) c = -7.0;
+      row[int4_byte(d)] = (uint8_t)(row[int4_byte(d)] | (uint8_t)(((int)c + 8) << int4_shift(d)));
+    }
+  }
+}
+
 /* Quantise one (token, head) row of D bf16 values into `row`. */
 static void write_row(int dtype, const uint16_t* x, int D, float tensor_scale,
                       uint8_t* row) {
@@ -202,6 +249,10 @@ static void write_row(int dtype, const uint16_t* x, int D, float tensor_scale,
       float y = bf16_to_float(x[d]) / tensor_scale;
       row[d] = kvo_fp8_encode(fmt, y);
     }
+    return;
+  }
+  if (dtype == KVO_INT4_PER_TOKEN_HEAD) {
+    write_row_int4(x, D, row);
     return;
   }
   /* per-token-head: dynamic scale from the row's absolute maximum. */
@@ -291,6 +342,14 @@ static void dequant_row(int dtype, const double* dec, const uint8_t* row, int D,
         int8_t c;
         memcpy(&c, &row[d], 1);
         out[d] = (double)c * s;
+      }
+      return;
+    }
+    case KVO_INT4_PER_TOKEN_HEAD: {
+      double s = (double)load_f32_le(row + D / 2);
+      for (int d = 0; d < D; ++d) {
+        int c = (row[int4_byte(d)] >> int4_shift(d)) & 15;
+        out[d] = (double)((c - 8) * (int)row[D / 2 + 4 + d / (D / 8)]) * s;
       }
       return;
     }
