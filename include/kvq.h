@@ -157,6 +157,79 @@ KVQ_API int kvq_reshape_and_cache(const void* key, const void* value,
                           const int64_t* slot_mapping, kvq_dtype_t dtype,
                           float k_scale, float v_scale, void* stream);
 
+/* gather_cache -- read rows of the caches back as the values they stand for
+ * (the inverse of kvq_reshape_and_cache; no counterpart on the pages).  For
+ * callers that need cached rows outside the attention: a shared prefix moved
+ * to a cache of another dtype, a check of what the quantisation kept.
+ *
+ *   key_cache, value_cache, num_blocks, block_size, num_heads_kv, head_dim,
+ *   dtype, k_scale, v_scale   as for kvq_reshape_and_cache.
+ *   slot_mapping      device int64 [num_tokens]: the slot of each output row.
+ *                     Slots < 0 or >= num_blocks*block_size give zero rows.
+ *   out_fp32          0: bf16 outputs; 1: fp32.
+ *   key_out,          device [num_tokens, num_heads_kv, head_dim], heads and
+ *   value_out         dims contiguous; token stride given in elements (>=
+ *                     Hkv*D, multiples of 8); base pointers 16-byte aligned.
+ * value = code * scale in fp32 (4-bit: (m_g * c) * s), one rounding; a bf16
+ * output rounds that value once more.  num_tokens == 0 is a no-op. */
+KVQ_API int kvq_gather_cache(const void* key_cache, const void* value_cache,
+                             int64_t num_blocks, int block_size, int num_heads_kv,
+                             int head_dim, kvq_dtype_t dtype, float k_scale,
+                             float v_scale, const int64_t* slot_mapping,
+                             int64_t num_tokens, int out_fp32, void* key_out,
+                             void* value_out, int64_t key_out_stride_tok,
+                             int64_t value_out_stride_tok, void* stream);
+
+/* build_block_tables -- block tables and slot mapping of a step, built on the
+ * device from the device's request lengths (no counterpart on the pages).
+ * Request r has Q = query_start_loc[r+1] - query_start_loc[r] new tokens, the
+ * last Q of its seq_lens[r] = L positions, and holds the blocks of its first
+ * L - Q positions: entries 0 .. ceil((L-Q) / block_size) - 1 of its table
+ * row.  The call takes the blocks its new positions need from the free list,
+ * stores them in the row, and gives each new token its slot.  With the
+ * lengths on the device, a step captured in a CUDA graph (this call, then
+ * kvq_decode_step) replays with other lengths.
+ *
+ *   num_req             requests (>= 0).
+ *   query_start_loc,    device int32 [num_req+1] (non-decreasing, [0] == 0)
+ *   seq_lens            and [num_req].
+ *   free_blocks,        device int32 [free_capacity]: ids of unused blocks, a
+ *   free_capacity       stack whose top is entry *free_count - 1.
+ *   free_count          device int32: blocks on it (read as within [0,
+ *                       free_capacity]).
+ *   block_table,        device int32 [num_req, block_table_stride].  Only the
+ *   block_table_stride  entries of new blocks are written.
+ *   slot_mapping,       device int64 [num_tokens]; the entries from
+ *   num_tokens          query_start_loc[num_req] on (a padded step) get -1,
+ *                       which kvq_reshape_and_cache skips.
+ *   block_size,         cache geometry (any block_size > 0).
+ *   num_blocks
+ *   free_count_out      device int32: blocks left; may be free_count.
+ *   status              device int32 [4], ZERO-FILLED before its first use:
+ *                       every call stores [0] = blocks that were wanted
+ *                       beyond the free list's end and [1] = requests left
+ *                       out; [2] and [3] are the library's own.  Calls that
+ *                       share it must be ordered on one stream.
+ * The new blocks are taken in (request, position) order from the top of the
+ * stack down, so the assignment is a function of the inputs alone and a host
+ * copy of the lengths predicts it.  When the list runs out, the remaining new
+ * entries are -1 (read as masked keys by the attention), and the tokens in
+ * them, like tokens in blocks whose id lies outside [0, num_blocks), get slot
+ * -1.  A request with Q < 0, Q > L, tokens outside the buffer, or (Q > 0)
+ * more blocks than block_table_stride is left out: slots -1, no blocks
+ * taken.  Freed blocks are pushed back by the caller (stored at *free_count,
+ * which it then advances).  query_start_loc, seq_lens, free_blocks and
+ * free_count are read only; no buffer may overlap another but free_count_out
+ * and free_count.  One kernel launch; allocates nothing. */
+KVQ_API int kvq_build_block_tables(int num_req, const int32_t* query_start_loc,
+                                   const int32_t* seq_lens, const int32_t* free_blocks,
+                                   int64_t free_capacity, const int32_t* free_count,
+                                   int32_t* block_table, int block_table_stride,
+                                   int64_t* slot_mapping, int64_t num_tokens,
+                                   int block_size, int64_t num_blocks,
+                                   int32_t* free_count_out, int32_t* status,
+                                   void* stream);
+
 /* get_scheduler_metadata -- plan one attention call (host only).
  * [P2] Breakdown item 1 and Key source snippet: the scheduler takes
  * kv_cache_dtype so that its tile and scratch sizes come from the KV cache

@@ -329,6 +329,70 @@ int kvq_reshape_and_cache(const void* key, const void* value, int64_t num_tokens
                                        block_size, slot_mapping, dtype, k_scale, v_scale, stream);
 }
 
+int kvq_gather_cache(const void* key_cache, const void* value_cache, int64_t num_blocks,
+                     int block_size, int num_heads_kv, int head_dim, kvq_dtype_t dtype,
+                     float k_scale, float v_scale, const int64_t* slot_mapping,
+                     int64_t num_tokens, int out_fp32, void* key_out, void* value_out,
+                     int64_t key_out_stride_tok, int64_t value_out_stride_tok, void* stream) {
+  if (!kvq::is_valid_dtype(dtype)) return KVQ_E_INVALID_ARG;
+  if (!kvq::head_dim_supported(head_dim)) return KVQ_E_UNSUPPORTED;
+  if (num_tokens < 0 || num_heads_kv <= 0 || num_blocks < 0 || block_size <= 0 ||
+      (out_fp32 != 0 && out_fp32 != 1))
+    return KVQ_E_INVALID_ARG;
+  if (num_tokens == 0) return KVQ_OK;
+  if (!key_cache || !value_cache || !slot_mapping || !key_out || !value_out)
+    return KVQ_E_INVALID_ARG;
+  const int64_t min_stride = (int64_t)num_heads_kv * head_dim;
+  if (key_out_stride_tok < min_stride || value_out_stride_tok < min_stride ||
+      key_out_stride_tok % 8 || value_out_stride_tok % 8)
+    return KVQ_E_INVALID_ARG;
+  if (!aligned(key_cache, 16) || !aligned(value_cache, 16) || !aligned(slot_mapping, 8) ||
+      !aligned(key_out, 16) || !aligned(value_out, 16))
+    return KVQ_E_INVALID_ARG;
+  if (dtype == KVQ_FP8_E4M3 || dtype == KVQ_FP8_E5M2) {
+    if (!(std::isfinite(k_scale) && std::isfinite(v_scale))) return KVQ_E_INVALID_ARG;
+  }
+  kvq::GatherArgs a;
+  a.key_cache = static_cast<const uint8_t*>(key_cache);
+  a.value_cache = static_cast<const uint8_t*>(value_cache);
+  a.num_slots = num_blocks * (int64_t)block_size;
+  a.heads_kv = num_heads_kv;
+  a.slot_mapping = slot_mapping;
+  a.num_tokens = num_tokens;
+  a.key_out = key_out;
+  a.value_out = value_out;
+  a.key_stride = key_out_stride_tok;
+  a.value_stride = value_out_stride_tok;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  return kvq::launch_gather_cache(a, dtype, head_dim, out_fp32 != 0, stream);
+}
+
+int kvq_build_block_tables(int num_req, const int32_t* query_start_loc, const int32_t* seq_lens,
+                           const int32_t* free_blocks, int64_t free_capacity,
+                           const int32_t* free_count, int32_t* block_table,
+                           int block_table_stride, int64_t* slot_mapping, int64_t num_tokens,
+                           int block_size, int64_t num_blocks, int32_t* free_count_out,
+                           int32_t* status, void* stream) {
+  if (num_req < 0 || num_tokens < 0 || free_capacity < 0 || block_size <= 0 || num_blocks < 0)
+    return KVQ_E_INVALID_ARG;
+  // token numbers and the library's block counts are 32-bit
+  if (num_tokens >= ((int64_t)1 << 31) || free_capacity >= ((int64_t)1 << 31))
+    return KVQ_E_UNSUPPORTED;
+  if (!free_count || !free_count_out || !status || (free_capacity > 0 && !free_blocks))
+    return KVQ_E_INVALID_ARG;
+  if (num_req > 0 && (!query_start_loc || !seq_lens || !block_table || block_table_stride <= 0))
+    return KVQ_E_INVALID_ARG;
+  if (num_tokens > 0 && !slot_mapping) return KVQ_E_INVALID_ARG;
+  if (!aligned(query_start_loc, 4) || !aligned(seq_lens, 4) || !aligned(free_blocks, 4) ||
+      !aligned(free_count, 4) || !aligned(block_table, 4) || !aligned(slot_mapping, 8) ||
+      !aligned(free_count_out, 4) || !aligned(status, 4))
+    return KVQ_E_INVALID_ARG;
+  return kvq::launch_block_tables(num_req, query_start_loc, seq_lens, free_blocks, free_capacity,
+                                  free_count, block_table, block_table_stride, slot_mapping,
+                                  num_tokens, block_size, num_blocks, free_count_out, status,
+                                  stream);
+}
 
 void kvq_sched_destroy(kvq_sched_t* s) {
   if (!s) return;

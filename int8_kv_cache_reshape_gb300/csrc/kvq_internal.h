@@ -313,6 +313,25 @@ int launch_reshape_and_cache(const void* key, const void* value,
                              int64_t num_blocks, int block_size,
                              const int64_t* slot_mapping, int dtype,
                              float k_scale, float v_scale, void* stream);
+// gather_cache's arguments; strides in elements per token.
+struct GatherArgs {
+  const uint8_t* key_cache;
+  const uint8_t* value_cache;
+  int64_t num_slots;
+  int heads_kv;
+  const int64_t* slot_mapping;
+  int64_t num_tokens;
+  void* key_out;
+  void* value_out;
+  int64_t key_stride, value_stride;
+  float k_scale, v_scale;
+};
+int launch_gather_cache(const GatherArgs& a, int dtype, int head_dim, bool fp32, void* stream);
+int launch_block_tables(int num_req, const int32_t* query_start_loc, const int32_t* seq_lens,
+                        const int32_t* free_blocks, int64_t free_capacity, const int32_t* free_count,
+                        int32_t* block_table, int block_table_stride, int64_t* slot_mapping,
+                        int64_t num_tokens, int block_size, int64_t num_blocks,
+                        int32_t* free_count_out, int32_t* status, void* stream);
 int launch_decode(const AttnParams& p, int dtype, int head_dim, int ntiles, void* stream);
 // The fused step's kernel (cooperative launch of `warps` / 4 CTAs); `warps`
 // from step_warps().

@@ -1,0 +1,231 @@
+// kvq_tables.cu -- block tables and slot maps of a step, built on the GPU
+// from the request lengths.  No counterpart on the pages (vLLM's scheduler
+// assigns blocks on the host).
+//
+// What it computes: request r has L keys, the last Q of them new, and holds
+// ceil((L - Q) / B) blocks; it needs ceil(L / B).  With new_r the difference
+// and base_r = sum of new_i over i < r, its n-th new logical block takes
+// free[count - 1 - base_r - n], and the new token at position p goes to slot
+// table[r][p / B] * B + p % B.
+//
+// A token's block never depends on another thread's store: an old block comes
+// from the table, a new one straight from the free list, and the thread of
+// the first token in a new block stores the table entry (a new block's first
+// position is always a new token).  So the work is split over tokens alone.
+//
+// One launch, bound by latency: 64 decode tokens move 1.3 KB.  A CTA takes a
+// contiguous run of tokens.  All of a batch's requests that end before its
+// run are summed in one pass (every thread loads its share of the lengths at
+// once: one memory round trip, where a search for the first request takes
+// log2 R dependent ones); the rest are scanned 256 at a time into shared
+// memory, where each token finds its request.
+#include <cuda_runtime.h>
+
+#include "kvq_internal.h"
+
+namespace kvq {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+// Tokens of a CTA's run: four a thread.
+constexpr int kRun = 1024;
+
+struct TableParams {
+  const int32_t* query_start_loc;
+  const int32_t* seq_lens;
+  const int32_t* free_blocks;
+  const int32_t* free_count;
+  int32_t* block_table;
+  int64_t* slot_mapping;
+  int32_t* free_count_out;
+  int32_t* status;
+  int64_t free_capacity, num_tokens, num_blocks;
+  int num_req, width, block_size;
+};
+
+struct Request {
+  int64_t start, end;  // its tokens
+  int first;           // position of its first new token
+  int held, fresh;     // blocks it holds, blocks that begin in this step
+  bool ok;
+};
+
+// Lengths that do not fit (more new tokens than keys, more blocks than the
+// table's width, tokens past the buffer) leave the request out.
+__device__ __forceinline__ Request load_request(const TableParams& p, int r) {
+  Request q;
+  q.start = p.query_start_loc[r];
+  q.end = p.query_start_loc[r + 1];
+  const int64_t L = p.seq_lens[r], n = q.end - q.start, B = p.block_size;
+  q.ok = n >= 0 && L >= n && q.start >= 0 && q.end <= p.num_tokens && (n == 0 || L <= B * p.width);
+  q.first = q.ok ? (int)(L - n) : 0;
+  q.held = q.ok ? (int)((uint32_t)q.first / (uint32_t)B + ((uint32_t)q.first % (uint32_t)B != 0)) : 0;
+  q.fresh = q.ok && n > 0 ? (int)((uint32_t)L / (uint32_t)B + ((uint32_t)L % (uint32_t)B != 0)) - q.held : 0;
+  return q;
+}
+
+__device__ __forceinline__ int64_t warp_sum(int64_t v) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  return v;
+}
+
+__global__ void __launch_bounds__(kThreads) block_tables_kernel(const TableParams p) {
+  __shared__ int64_t part[kWarps], part2[kWarps], base_s[kThreads];
+  __shared__ int32_t part3[kWarps], start_s[kThreads], end_s[kThreads], first_s[kThreads], held_s[kThreads];
+  __shared__ int last_s;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t t0 = (int64_t)blockIdx.x * kRun;
+  const int64_t t1 = min(t0 + kRun, p.num_tokens);
+  const bool last_run = blockIdx.x == gridDim.x - 1;
+  const int64_t count = max((int64_t)0, min((int64_t)*p.free_count, p.free_capacity));
+
+  // requests that end at or before this run, their new blocks, and how many
+  // of them are left out
+  int64_t base = 0;
+  int first_req = 0, bad = 0;
+  if (t0 > 0) {
+    int64_t sum = 0;
+    int n = 0, b = 0;
+    for (int r = tid; r < p.num_req; r += kThreads) {
+      const Request q = load_request(p, r);
+      if (q.end <= t0) {
+        sum += q.fresh;
+        ++n;
+        b += !q.ok;
+      }
+    }
+    sum = warp_sum(sum);
+    const int64_t nb = warp_sum(((int64_t)b << 32) | (int64_t)n);
+    if (lane == 0) {
+      part[warp] = sum;
+      part2[warp] = nb;
+    }
+    __syncthreads();
+    int64_t nbs = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      base += part[w];
+      nbs += part2[w];
+    }
+    first_req = (int)(nbs & 0xFFFFFFFF);
+    bad = (int)(nbs >> 32);
+    __syncthreads();
+  }
+
+  // the rest, kThreads requests at a time (the last run goes through all of
+  // them, for the totals)
+  int64_t t = t0;
+  for (int r0 = first_req; r0 < p.num_req && (t < t1 || last_run); r0 += kThreads) {
+    const int n = min(kThreads, p.num_req - r0);
+    Request q;
+    q.start = q.end = 0;
+    q.first = q.held = q.fresh = 0;
+    q.ok = true;
+    if (tid < n) q = load_request(p, r0 + tid);
+    int64_t incl = q.fresh;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += v;
+    }
+    const int bad_w = __popc(__ballot_sync(0xffffffffu, !q.ok));
+    if (lane == 31) {
+      part[warp] = incl;
+      part3[warp] = bad_w;
+    }
+    start_s[tid] = (int32_t)q.start;
+    end_s[tid] = q.ok ? (int32_t)q.end : (int32_t)q.start;  // a request left out has no tokens
+    first_s[tid] = q.first;
+    held_s[tid] = q.held;
+    __syncthreads();
+    int64_t before = base + incl - q.fresh;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += part[w];
+      base += part[w];
+      bad += part3[w];
+    }
+    base_s[tid] = before;
+    __syncthreads();
+    // the run's tokens up to the next batch's first (the batch's last end)
+    const int64_t stop = min(t1, (int64_t)p.query_start_loc[r0 + n]);
+    for (int64_t k = t + tid; k < stop; k += kThreads) {
+      int lo = 0, hi = n;  // the last request that starts at or before token k
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (start_s[mid] <= k) lo = mid;
+        else hi = mid;
+      }
+      int64_t slot = -1;
+      if (k >= start_s[lo] && k < end_s[lo]) {
+        const uint32_t pos = (uint32_t)(first_s[lo] + (int)(k - start_s[lo]));
+        const uint32_t lb = pos / (uint32_t)p.block_size, off = pos - lb * (uint32_t)p.block_size;
+        int32_t* entry = p.block_table + (int64_t)(r0 + lo) * p.width + lb;
+        int32_t id = -1;
+        if ((int)lb < held_s[lo]) {
+          id = *entry;
+        } else {
+          const int64_t at = base_s[lo] + (int)lb - held_s[lo];
+          if (at < count) id = p.free_blocks[count - 1 - at];
+          if (off == 0) *entry = id;
+        }
+        if (id >= 0 && id < p.num_blocks) slot = (int64_t)id * p.block_size + off;
+      }
+      p.slot_mapping[k] = slot;
+    }
+    t = max(t, stop);
+    __syncthreads();
+  }
+  for (int64_t k = t + tid; k < t1; k += kThreads) p.slot_mapping[k] = -1;
+
+  // Totals: from the CTA of the last run; free_count_out may be free_count,
+  // so it is stored once every CTA has read that (the last to arrive does).
+  if (tid == 0) {
+    const int32_t left = (int32_t)max((int64_t)0, count - base);
+    if (last_run) {
+      p.status[0] = (int32_t)min((int64_t)0x7FFFFFFF, max((int64_t)0, base - count));
+      p.status[1] = bad;
+      if (gridDim.x == 1) *p.free_count_out = left;
+      else p.status[3] = left;
+    }
+    if (gridDim.x > 1) {
+      __threadfence();
+      if (atomicAdd(p.status + 2, 1) == (int)gridDim.x - 1) {
+        __threadfence();
+        *p.free_count_out = __ldcg(p.status + 3);
+        p.status[2] = 0;
+      }
+    }
+  }
+}
+
+}  // namespace
+
+int launch_block_tables(int num_req, const int32_t* query_start_loc, const int32_t* seq_lens,
+                        const int32_t* free_blocks, int64_t free_capacity, const int32_t* free_count,
+                        int32_t* block_table, int block_table_stride, int64_t* slot_mapping,
+                        int64_t num_tokens, int block_size, int64_t num_blocks,
+                        int32_t* free_count_out, int32_t* status, void* stream) {
+  TableParams p;
+  p.query_start_loc = query_start_loc;
+  p.seq_lens = seq_lens;
+  p.free_blocks = free_blocks;
+  p.free_count = free_count;
+  p.block_table = block_table;
+  p.slot_mapping = slot_mapping;
+  p.free_count_out = free_count_out;
+  p.status = status;
+  p.free_capacity = free_capacity;
+  p.num_tokens = num_tokens;
+  p.num_blocks = num_blocks;
+  p.num_req = num_req;
+  p.width = block_table_stride;
+  p.block_size = block_size;
+  const int64_t ctas = num_tokens > kRun ? (num_tokens + kRun - 1) / kRun : 1;
+  block_tables_kernel<<<(unsigned)ctas, kThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+  return cudaGetLastError() == cudaSuccess ? KVQ_OK : KVQ_E_CUDA;
+}
+
+}  // namespace kvq

@@ -78,6 +78,14 @@ lib.kvq_reshape_and_cache.restype = _c.c_int
 lib.kvq_reshape_and_cache.argtypes = [
     _p, _p, _c.c_int64, _c.c_int64, _c.c_int64, _c.c_int, _c.c_int, _p, _p,
     _c.c_int64, _c.c_int, _p, _c.c_int, _c.c_float, _c.c_float, _p]
+lib.kvq_gather_cache.restype = _c.c_int
+lib.kvq_gather_cache.argtypes = [
+    _p, _p, _c.c_int64, _c.c_int, _c.c_int, _c.c_int, _c.c_int, _c.c_float, _c.c_float, _p,
+    _c.c_int64, _c.c_int, _p, _p, _c.c_int64, _c.c_int64, _p]
+lib.kvq_build_block_tables.restype = _c.c_int
+lib.kvq_build_block_tables.argtypes = [
+    _c.c_int, _p, _p, _p, _c.c_int64, _p, _p, _c.c_int, _p, _c.c_int64, _c.c_int, _c.c_int64,
+    _p, _p, _p]
 lib.kvq_get_scheduler_metadata.restype = _c.c_int
 lib.kvq_get_scheduler_metadata.argtypes = [
     _c.c_int, _c.c_int, _c.c_int, _c.c_int, _p, _p, _c.c_int, _c.c_int,
@@ -183,17 +191,120 @@ def cache_row_bytes(kv_cache_dtype, head_dim: int) -> int:
     return out.value
 
 
+def _reshape_and_cache_args(key, value, key_cache, value_cache, slot_mapping, kv_cache_dtype,
+                            k_scale, v_scale, stream):
+    dt = parse_kv_cache_dtype(kv_cache_dtype) if isinstance(kv_cache_dtype, str) else kv_cache_dtype
+    T, H, D = key.shape
+    return (_ptr(key), _ptr(value), T, key.stride(0), value.stride(0), H, D, _ptr(key_cache),
+            _ptr(value_cache), key_cache.shape[0], key_cache.shape[1], _ptr(slot_mapping), dt,
+            float(k_scale), float(v_scale), _stream(stream))
+
+
 def reshape_and_cache(key, value, key_cache, value_cache, slot_mapping, kv_cache_dtype,
                       k_scale: float = 1.0, v_scale: float = 1.0, stream=None) -> None:
     """key/value: bf16 [T, Hkv, D] (token stride may exceed Hkv*D);
     caches: uint8 [NB, B, Hkv, row]; slot_mapping: int64 [T]."""
+    _check(lib.kvq_reshape_and_cache(*_reshape_and_cache_args(
+        key, value, key_cache, value_cache, slot_mapping, kv_cache_dtype, k_scale, v_scale,
+        stream)), "kvq_reshape_and_cache")
+
+
+class Prepared:
+    """One C-ABI call with its arguments marshalled once (pointers, sizes,
+    the stream), for a serving loop that calls it every step on the same
+    buffers: calling the object only crosses into the library.  The tensors
+    behind the pointers must stay alive (and in place) while it is used."""
+
+    def __init__(self, fn, args, what: str):
+        self.fn = fn
+        self.args = tuple(args)
+        self.what = what
+
+    def __call__(self) -> None:
+        _check(self.fn(*self.args), self.what)
+
+
+def _marshalled(fn, args):
+    """The arguments as ctypes values of fn's declared types, converted once."""
+    return [a if isinstance(a, (t, type(None))) else t(a) for t, a in zip(fn.argtypes, args)]
+
+
+def prepare_reshape_and_cache(key, value, key_cache, value_cache, slot_mapping, kv_cache_dtype,
+                              k_scale: float = 1.0, v_scale: float = 1.0, stream=None) -> Prepared:
+    """reshape_and_cache with its arguments marshalled once (see Prepared)."""
+    return Prepared(lib.kvq_reshape_and_cache, _marshalled(
+        lib.kvq_reshape_and_cache, _reshape_and_cache_args(
+            key, value, key_cache, value_cache, slot_mapping, kv_cache_dtype, k_scale, v_scale,
+            stream)), "kvq_reshape_and_cache")
+
+
+def _gather_cache_args(key_cache, value_cache, slot_mapping, key_out, value_out, kv_cache_dtype,
+                       k_scale, v_scale, stream):
+    import torch
     dt = parse_kv_cache_dtype(kv_cache_dtype) if isinstance(kv_cache_dtype, str) else kv_cache_dtype
-    T, H, D = key.shape
-    nb, bs = key_cache.shape[0], key_cache.shape[1]
-    _check(lib.kvq_reshape_and_cache(
-        _ptr(key), _ptr(value), T, key.stride(0), value.stride(0), H, D,
-        _ptr(key_cache), _ptr(value_cache), nb, bs, _ptr(slot_mapping), dt,
-        float(k_scale), float(v_scale), _stream(stream)), "kvq_reshape_and_cache")
+    T, H, D = key_out.shape
+    if key_out.dtype != value_out.dtype or key_out.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("key_out and value_out must both be bfloat16 or both float32")
+    if tuple(value_out.shape) != (T, H, D) or slot_mapping.shape[0] != T:
+        raise ValueError("key_out, value_out and slot_mapping must agree on their rows")
+    return (_ptr(key_cache), _ptr(value_cache), key_cache.shape[0], key_cache.shape[1], H, D, dt,
+            float(k_scale), float(v_scale), _ptr(slot_mapping), T,
+            int(key_out.dtype == torch.float32), _ptr(key_out), _ptr(value_out),
+            key_out.stride(0), value_out.stride(0), _stream(stream))
+
+
+def gather_cache(key_cache, value_cache, slot_mapping, key_out, value_out, kv_cache_dtype,
+                 k_scale: float = 1.0, v_scale: float = 1.0, stream=None) -> None:
+    """Cache rows read back as values: slot_mapping int64 [T]; key_out /
+    value_out bf16 or float32 [T, Hkv, D] (token stride may exceed Hkv*D)."""
+    _check(lib.kvq_gather_cache(*_gather_cache_args(
+        key_cache, value_cache, slot_mapping, key_out, value_out, kv_cache_dtype, k_scale,
+        v_scale, stream)), "kvq_gather_cache")
+
+
+def prepare_gather_cache(key_cache, value_cache, slot_mapping, key_out, value_out, kv_cache_dtype,
+                         k_scale: float = 1.0, v_scale: float = 1.0, stream=None) -> Prepared:
+    """gather_cache with its arguments marshalled once (see Prepared)."""
+    return Prepared(lib.kvq_gather_cache, _marshalled(lib.kvq_gather_cache, _gather_cache_args(
+        key_cache, value_cache, slot_mapping, key_out, value_out, kv_cache_dtype, k_scale,
+        v_scale, stream)), "kvq_gather_cache")
+
+
+def _build_block_tables_args(query_start_loc, seq_lens, free_blocks, free_count, block_table,
+                             slot_mapping, block_size, num_blocks, free_count_out, status, stream):
+    R = seq_lens.shape[0]
+    if query_start_loc.shape[0] != R + 1 or block_table.shape[0] < R:
+        raise ValueError("query_start_loc, seq_lens and block_table must agree on their requests")
+    if status.numel() < 4:
+        raise ValueError("status holds four int32")
+    return (R, _ptr(query_start_loc), _ptr(seq_lens), _ptr(free_blocks), free_blocks.numel(),
+            _ptr(free_count), _ptr(block_table), block_table.stride(0), _ptr(slot_mapping),
+            slot_mapping.numel(), int(block_size), int(num_blocks), _ptr(free_count_out),
+            _ptr(status), _stream(stream))
+
+
+def build_block_tables(query_start_loc, seq_lens, free_blocks, free_count, block_table,
+                       slot_mapping, block_size: int, num_blocks: int, free_count_out, status,
+                       stream=None) -> None:
+    """Block tables and slot mapping of a step on the device: query_start_loc
+    int32 [R + 1], seq_lens int32 [R], free_blocks int32 (a stack of
+    free_count int32 [1] ids), block_table int32 [R, width] (entries of new
+    blocks are stored), slot_mapping int64 (padded entries get -1),
+    free_count_out int32 [1] (may be free_count), status int32 [4],
+    zero-filled before its first use."""
+    _check(lib.kvq_build_block_tables(*_build_block_tables_args(
+        query_start_loc, seq_lens, free_blocks, free_count, block_table, slot_mapping, block_size,
+        num_blocks, free_count_out, status, stream)), "kvq_build_block_tables")
+
+
+def prepare_build_block_tables(query_start_loc, seq_lens, free_blocks, free_count, block_table,
+                               slot_mapping, block_size: int, num_blocks: int, free_count_out,
+                               status, stream=None) -> Prepared:
+    """build_block_tables with its arguments marshalled once (see Prepared)."""
+    return Prepared(lib.kvq_build_block_tables, _marshalled(
+        lib.kvq_build_block_tables, _build_block_tables_args(
+            query_start_loc, seq_lens, free_blocks, free_count, block_table, slot_mapping,
+            block_size, num_blocks, free_count_out, status, stream)), "kvq_build_block_tables")
 
 
 class Sched:
@@ -255,6 +366,20 @@ def get_scheduler_metadata(num_req: int, heads_q: int, heads_kv: int, head_dim: 
     return Sched(h, ws.value)
 
 
+def _attention_args(sched, q, key_cache, value_cache, query_start_loc, seq_lens, block_table,
+                    sm_scale, causal, window, soft_cap, k_scale, v_scale, out, workspace,
+                    kv_cache_dtype, heads_kv, stream, num_blocks, alibi_slopes, sinks):
+    dt = parse_kv_cache_dtype(kv_cache_dtype) if isinstance(kv_cache_dtype, str) else kv_cache_dtype
+    _, Hq, D = q.shape
+    nb = key_cache.shape[0] if num_blocks is None else num_blocks
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    return (sched.handle, Hq, heads_kv, D, dt, _ptr(q), _ptr(key_cache), _ptr(value_cache),
+            _ptr(query_start_loc), _ptr(seq_lens), _ptr(block_table), block_table.stride(0),
+            key_cache.shape[1], nb, float(sm_scale), int(bool(causal)), int(window),
+            float(soft_cap), _ptr(alibi_slopes), _ptr(sinks), float(k_scale), float(v_scale),
+            _ptr(out), _ptr(workspace), ws_bytes, _stream(stream))
+
+
 def attention_with_kv_cache(sched: Sched, q, key_cache, value_cache, query_start_loc,
                             seq_lens, block_table, sm_scale: float, causal: bool,
                             window: int, soft_cap: float, k_scale: float, v_scale: float,
@@ -264,16 +389,25 @@ def attention_with_kv_cache(sched: Sched, q, key_cache, value_cache, query_start
     block_table int32 [R, max_blocks]; query_start_loc / seq_lens device
     int32; workspace: a uint8 device tensor of >= sched.workspace_bytes;
     alibi_slopes / sinks: device float32 [Hq] or None."""
-    dt = parse_kv_cache_dtype(kv_cache_dtype) if isinstance(kv_cache_dtype, str) else kv_cache_dtype
-    _, Hq, D = q.shape
-    nb = key_cache.shape[0] if num_blocks is None else num_blocks
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(lib.kvq_attention_with_kv_cache(
-        sched.handle, Hq, heads_kv, D, dt, _ptr(q), _ptr(key_cache), _ptr(value_cache),
-        _ptr(query_start_loc), _ptr(seq_lens), _ptr(block_table), block_table.stride(0),
-        key_cache.shape[1], nb, float(sm_scale), int(bool(causal)), int(window),
-        float(soft_cap), _ptr(alibi_slopes), _ptr(sinks), float(k_scale), float(v_scale),
-        _ptr(out), _ptr(workspace), ws_bytes, _stream(stream)), "kvq_attention_with_kv_cache")
+    _check(lib.kvq_attention_with_kv_cache(*_attention_args(
+        sched, q, key_cache, value_cache, query_start_loc, seq_lens, block_table, sm_scale,
+        causal, window, soft_cap, k_scale, v_scale, out, workspace, kv_cache_dtype, heads_kv,
+        stream, num_blocks, alibi_slopes, sinks)), "kvq_attention_with_kv_cache")
+
+
+def prepare_attention_with_kv_cache(sched: Sched, q, key_cache, value_cache, query_start_loc,
+                                    seq_lens, block_table, sm_scale: float, causal: bool,
+                                    window: int, soft_cap: float, k_scale: float, v_scale: float,
+                                    out, workspace, kv_cache_dtype, heads_kv: int, stream=None,
+                                    num_blocks=None, alibi_slopes=None, sinks=None) -> Prepared:
+    """attention_with_kv_cache with its arguments marshalled once (see
+    Prepared): the layers of a step, or steps replayed with one schedule,
+    which must stay open too."""
+    return Prepared(lib.kvq_attention_with_kv_cache, _marshalled(
+        lib.kvq_attention_with_kv_cache, _attention_args(
+            sched, q, key_cache, value_cache, query_start_loc, seq_lens, block_table, sm_scale,
+            causal, window, soft_cap, k_scale, v_scale, out, workspace, kv_cache_dtype, heads_kv,
+            stream, num_blocks, alibi_slopes, sinks)), "kvq_attention_with_kv_cache")
 
 
 def attention_with_kv_cache_static_scratch(sched: Sched, q, key_cache, value_cache,
@@ -307,21 +441,6 @@ def decode_step_workspace_size(num_req: int, heads_q: int, heads_kv: int, head_d
                                               max_query_len, int(bool(use_alibi)),
                                               _c.byref(out)), "kvq_decode_step_workspace_size")
     return out.value
-
-
-class Prepared:
-    """One C-ABI call with its arguments marshalled once (pointers, sizes,
-    the stream), for a serving loop that calls it every step on the same
-    buffers: calling the object only crosses into the library.  The tensors
-    behind the pointers must stay alive (and in place) while it is used."""
-
-    def __init__(self, fn, args, what: str):
-        self.fn = fn
-        self.args = tuple(args)
-        self.what = what
-
-    def __call__(self) -> None:
-        _check(self.fn(*self.args), self.what)
 
 
 def _decode_step_args(key, value, slot_mapping, key_cache, value_cache, q, query_start_loc,
