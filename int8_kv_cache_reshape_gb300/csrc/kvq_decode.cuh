@@ -1,5 +1,6 @@
 // kvq_decode.cuh -- split-KV attention over the quantised paged cache for
 // small row tiles (decode: the query token(s) x G heads of one kv head).
+// (The 4-bit cache has a kernel of its own, kvq_decode_int4.cuh.)
 //
 // What it computes: for each packed row (query token, q head) of a tile,
 // o = softmax_j(z_j) v_j over the visible keys j, with
@@ -31,8 +32,7 @@
 //     record ring in shared memory, so no load waits on the block table.
 //   * Tensor cores at the register level: S^T = K Q^T and O^T = V^T P^T as
 //     m16n8k16 f16 MMAs with tokens as M (one chunk), packed rows as N.
-//     Codes convert exactly to f16 (e4m3 / e5m2 / int8 all fit; a 4-bit code
-//     times its group's integer multiplier too, see dev::int4_mul), Q enters
+//     Codes convert exactly to f16 (e4m3 / e5m2 / int8 all fit), Q enters
 //     exactly (a power-of-two shift of its bf16 values), and every scale
 //     stays in fp32: sm_scale, log2(e) and the per-tensor k_scale multiply
 //     the scores, v_scale the output; per-token-head scales multiply score
@@ -57,16 +57,11 @@ namespace kvq {
 template <int DT, int D>
 struct DecodeGeom {
   static constexpr bool kAuto = DT == KVQ_AUTO;  // bf16 rows, bf16 MMAs
-  static constexpr bool kInt4 = is_int4(DT);
-  static constexpr int kCodes = code_bytes(DT, D);
+  static constexpr int kEB = kv_elem_bytes(DT);
   static constexpr int kKsteps = D / 16;     // MMA k-steps over head_dim (QK)
   static constexpr int kMtiles = D / 16;     // MMA m-tiles over head_dim (PV)
-  static constexpr int kKBytes = kCodes / 4 >= 16 ? 16 : kCodes / 4;  // bytes of a K piece
-  static constexpr int kK16 = kCodes / 4 / kKBytes;  // K pieces per lane per row
-  static constexpr int kVBytes = kCodes / 8;   // V bytes per lane per row
-  // consecutive head dims of a quantised K piece: a lane's dims are runs of
-  // kRun, lane c's at 4 kRun i + kRun c
-  static constexpr int kRun = kInt4 ? 2 * kKBytes : 16;
+  static constexpr int kK16 = D * kEB / 64;  // 16-byte K pieces per lane per row
+  static constexpr int kVBytes = D * kEB / 8;  // V bytes per lane per row
   static constexpr int kVPieces = kVBytes >= 16 ? kVBytes / 16 : 1;
   static constexpr int kVSlots = D / 32;     // 16-byte V slots per lane
   static constexpr bool kPth = is_per_token_head(DT);
@@ -83,8 +78,6 @@ template <int DT, int D>
 __device__ __forceinline__ int pv_dim(int mi, int g, int k) {
   if constexpr (DT == KVQ_AUTO) {
     return (mi / 4) * 64 + g * 8 + 2 * (mi % 4) + k;
-  } else if constexpr (is_int4(DT)) {  // the lane's run is the row's group g
-    return g * (D / 8) + 2 * mi + k;
   } else {
     constexpr int run = D / 8 >= 16 ? 16 : D / 8;
     return (mi / 8) * 128 + g * run + 2 * (mi % 8) + k;
@@ -182,8 +175,8 @@ __device__ __forceinline__ void stage_issue(const StepParams& sp, StageLane& st)
   if (!st.on) return;
   const int64_t ctas = gridDim.x > 1 ? gridDim.x - 1 : 1;
   const int64_t cta = gridDim.x > 1 ? blockIdx.x - 1 : 0;
-  st.i0 = cta * kDecodeThreads + threadIdx.x;
-  st.step = ctas * kDecodeThreads;
+  st.i0 = cta * blockDim.x + threadIdx.x;
+  st.step = ctas * blockDim.x;
   st.n16 = sp.stage_bytes >> 4;
   const uint4* src = reinterpret_cast<const uint4*>(sp.stage_src);
 #pragma unroll
@@ -277,14 +270,6 @@ splitkv_decode_kernel(const AttnParams p, const StepParams sp) {
     if constexpr (DEV) return dev::ldg_stream_coherent(a);
     else return dev::ldg_stream(a);
   };
-  auto load8 = [&](const void* a) {
-    if constexpr (DEV) return dev::ldg_stream8_coherent(a);
-    else return dev::ldg_stream8(a);
-  };
-  auto load4 = [&](const void* a) {
-    if constexpr (DEV) return dev::ldg_stream4_coherent(a);
-    else return dev::ldg_stream4(a);
-  };
 
   // ---- this warp's segment of the flat chunk sequence -------------------
   // (host plan: from the schedule's warp table; fused step: equal cuts)
@@ -316,14 +301,13 @@ splitkv_decode_kernel(const AttnParams p, const StepParams sp) {
   // copies: K rows g, g+8 at bytes 64i + 16c (piece i); V rows 2c, 2c+1,
   // 2c+8, 2c+9 at bytes 128i + 16g (8g for head_dim 64); the scale tail of
   // K row g (c=0), K row g+8 (c=1), V row g (c=2) or V row g+8 (c=3).
-  // (4-bit rows of head_dim 64: K at 8c; V runs of 4, 8 or 16 bytes)
-  const uint32_t koff0 = g * rs + Geo::kKBytes * c;
+  const uint32_t koff0 = g * rs + 16 * c;
   const uint32_t koff1 = koff0 + 8 * rs;
   uint32_t voff[4];
 #pragma unroll
   for (int vr = 0; vr < 4; ++vr)
     voff[vr] = (2 * c + (vr & 1) + 8 * (vr >> 1)) * rs + g * (Geo::kVBytes >= 16 ? 16 : Geo::kVBytes);
-  const uint32_t toff = (g + 8 * (c & 1)) * rs + Geo::kCodes;
+  const uint32_t toff = (g + 8 * (c & 1)) * rs + D;
 
   // ---- chunk records: {slot of the chunk's first row (-1: no block),
   // first token, piece, visible-row mask | kv_head << 16}, built by lanes
@@ -436,14 +420,8 @@ splitkv_decode_kernel(const AttnParams p, const StepParams sp) {
     for (int rr = 0; rr < 2; ++rr) {
       const bool lv = (nx_live >> (g + 8 * rr)) & 1u;
 #pragma unroll
-      for (int i = 0; i < Geo::kK16; ++i) {
-        if constexpr (Geo::kKBytes == 8) {
-          const uint2 w = lv ? load8(kchunk + (rr ? koff1 : koff0)) : make_uint2(0, 0);
-          kreg[rr][i] = make_uint4(w.x, w.y, 0, 0);
-        } else {
-          kreg[rr][i] = lv ? load16(kchunk + (rr ? koff1 : koff0) + 64 * i) : make_uint4(0, 0, 0, 0);
-        }
-      }
+      for (int i = 0; i < Geo::kK16; ++i)
+        kreg[rr][i] = lv ? load16(kchunk + (rr ? koff1 : koff0) + 64 * i) : make_uint4(0, 0, 0, 0);
     }
     if constexpr (Geo::kPth) {
       const bool lv = (nx_live >> (g + 8 * (c & 1))) & 1u;
@@ -455,12 +433,7 @@ splitkv_decode_kernel(const AttnParams p, const StepParams sp) {
 #pragma unroll
     for (int vr = 0; vr < 4; ++vr) {
       const bool lv = (nx_live >> (2 * c + (vr & 1) + 8 * (vr >> 1))) & 1u;
-      if constexpr (Geo::kVBytes == 4) {
-        vreg[vr][0] = make_uint4(lv ? load4(vchunk + voff[vr]) : 0u, 0, 0, 0);
-      } else if constexpr (Geo::kVBytes == 8 && Geo::kInt4) {
-        const uint2 w = lv ? load8(vchunk + voff[vr]) : make_uint2(0, 0);
-        vreg[vr][0] = make_uint4(w.x, w.y, 0, 0);
-      } else if constexpr (Geo::kVBytes == 8) {
+      if constexpr (Geo::kVBytes == 8) {
         uint2 w = make_uint2(0, 0);
         if (lv) w = *reinterpret_cast<const uint2*>(vchunk + voff[vr]);
         vreg[vr][0] = make_uint4(w.x, w.y, 0, 0);
@@ -502,8 +475,7 @@ splitkv_decode_kernel(const AttnParams p, const StepParams sp) {
   // Start a piece: Q fragments (B operand of S^T = K Q^T) and masks.  Q
   // enters the MMA exactly: bf16 values scaled by a power of two only (8
   // significant bits fit f16's 11); sm_scale and log2(e) are applied to the
-  // fp32 scores.  Lane c holds dims 64i + 16c + [0, 16) of its rows (4-bit
-  // rows: 128i + 32c + [0, 32), head_dim 64 16c + [0, 16)).
+  // fp32 scores.  Lane c holds dims 64i + 16c + [0, 16) of its rows.
   auto start_piece = [&](int piece) {
     if constexpr (DEV) {
       // The tile's part inside this warp's segment; a cut tile's partial
@@ -569,17 +541,17 @@ splitkv_decode_kernel(const AttnParams p, const StepParams sp) {
       const int R = pc.row0 + (valid ? nr : 0);
       const int tok = q0 + R / G;
       const int head = pc.kv_head * G + R % G;
-      const uint16_t* src = p.q + ((int64_t)tok * p.heads_q + head) * D + Geo::kRun * c;
+      const uint16_t* src = p.q + ((int64_t)tok * p.heads_q + head) * D + 16 * c;
 #pragma unroll
-      for (int i = 0; i < D / 4 / Geo::kRun; ++i) {
+      for (int i = 0; i < Geo::kK16; ++i) {
 #pragma unroll
-        for (int h = 0; h < Geo::kRun / 8; ++h) {
-          const uint4 w = valid ? *reinterpret_cast<const uint4*>(src + 4 * Geo::kRun * i + 8 * h)
+        for (int h = 0; h < 2; ++h) {
+          const uint4 w = valid ? *reinterpret_cast<const uint4*>(src + 64 * i + 8 * h)
                                 : make_uint4(0, 0, 0, 0);
           const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const int e = Geo::kRun * i + 8 * h + 2 * k;
+            const int e = 16 * i + 8 * h + 2 * k;
             qv[t][e] = dev::bf16_lo(ws[k]);
             qv[t][e + 1] = dev::bf16_hi(ws[k]);
             qmax = fmaxf(qmax, fmaxf(fabsf(qv[t][e]), fabsf(qv[t][e + 1])));
@@ -619,9 +591,7 @@ splitkv_decode_kernel(const AttnParams p, const StepParams sp) {
           al_pos[t][k] = pn;
         }
       }
-    // (4-bit rows enter the MMAs as multiples of 1 / kInt4Unit)
-    score_mul = Geo::kInt4 ? base_scale * dev::kInt4Unit * q_unmul
-                           : q_unmul * base_scale * (Geo::kPth || Geo::kAuto ? 1.0f : p.k_scale);
+    score_mul = q_unmul * base_scale * (Geo::kPth || Geo::kAuto ? 1.0f : p.k_scale);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
 #pragma unroll
@@ -643,7 +613,7 @@ splitkv_decode_kernel(const AttnParams p, const StepParams sp) {
         for (int off = 4; off < 32; off <<= 1)
           l_run[t][k] += __shfl_xor_sync(0xffffffffu, l_run[t][k], off);
     const float unit = Geo::kPth && ev > -1000 ? ldexpf(1.0f, ev) : 1.0f;
-    const float vmul = Geo::kInt4 ? dev::kInt4Unit : Geo::kPth || Geo::kAuto ? 1.0f : p.v_scale;
+    const float vmul = Geo::kPth || Geo::kAuto ? 1.0f : p.v_scale;
     // An attention sink joins the normaliser of a whole (uncut) tile here;
     // a cut tile's merge adds it once.  The weights carry 2^-(m_run - 6).
     if (p.sinks && pc.part < 0) {
@@ -664,7 +634,7 @@ splitkv_decode_kernel(const AttnParams p, const StepParams sp) {
         const int nr = 8 * t + 2 * c + k;
         if (nr >= pc.nrows) continue;
         const float l = l_run[t][k];
-        const float sc = (l > 0.0f ? 1.0f / l : 0.0f) * (Geo::kInt4 ? vmul * unit : unit * vmul);
+        const float sc = (l > 0.0f ? 1.0f / l : 0.0f) * unit * vmul;
         const int R = pc.row0 + nr;
         if (pc.part < 0) {
           if (piece_bad) continue;
@@ -734,37 +704,6 @@ splitkv_decode_kernel(const AttnParams p, const StepParams sp) {
       sv0 *= to_ref;
       sv1 *= to_ref;
     }
-    // 4-bit rows: the group multipliers of this lane's codes as f16 factors.
-    // Each quad's four tails (K and V of rows g and g + 8, one per lane) are
-    // transposed in two exchanges, so that lane c has bytes 2c and 2c + 1 of
-    // all four: its two K groups; and for V, another transpose across rows
-    // (the matrix one) gives the pairs of tokens that its V codes form.  At
-    // head_dim 256 a lane's K groups are c and c + 4: its K tails' bytes are
-    // put in that order first.
-    dev::Int4Mul kmul[2][2], vmul4[2];
-    if constexpr (Geo::kInt4) {
-      uint32_t y = treg.y, zw = treg.z;
-      if constexpr (D == 256) {
-        const uint32_t ty = dev::prmt(y, zw, c < 2 ? 0x5140u : 0x3210u);
-        zw = dev::prmt(y, zw, c < 2 ? 0x7362u : 0x7654u);
-        y = ty;
-      }
-      const bool up = c >= 2, odd = c & 1;
-      const uint32_t keep = up ? zw : y;                                      // tail c
-      const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? y : zw, 2);      // tail c ^ 2
-      const uint32_t own = dev::prmt(keep, got, odd ? 0x7632u : 0x5410u);     // c | c ^ 2
-      const uint32_t oth = __shfl_xor_sync(0xffffffffu, dev::prmt(keep, got, odd ? 0x5410u : 0x7632u), 1);
-      const uint32_t even_t = odd ? oth : own, odd_t = odd ? own : oth;       // tails 0, 2 | 1, 3
-      const uint32_t sel_a = up ? 0x4342u : 0x4140u, sel_b = up ? 0x4140u : 0x4342u;
-      const uint32_t one = 0x64646464u;  // f16 1024 + byte
-      const uint32_t k0 = dev::prmt(even_t, one, sel_a), k1 = dev::prmt(odd_t, one, sel_a);
-      kmul[0][0] = dev::int4_mul(dev::prmt(k0, k0, 0x1010u));
-      kmul[0][1] = dev::int4_mul(dev::prmt(k0, k0, 0x3232u));
-      kmul[1][0] = dev::int4_mul(dev::prmt(k1, k1, 0x1010u));
-      kmul[1][1] = dev::int4_mul(dev::prmt(k1, k1, 0x3232u));
-      vmul4[0] = dev::int4_mul(dev::movmatrix_trans(dev::prmt(even_t, one, sel_b)));
-      vmul4[1] = dev::int4_mul(dev::movmatrix_trans(dev::prmt(odd_t, one, sel_b)));
-    }
 
     // S^T = K Q^T : 16 tokens x 8 rows per n-tile; even and odd k-steps in
     // separate accumulators to halve the dependent MMA chain.
@@ -789,23 +728,6 @@ splitkv_decode_kernel(const AttnParams p, const StepParams sp) {
           for (int t = 0; t < NT; ++t) {
             if (w2 & 1) dev::mma_bf16_16816(s2[t], a, qf[t][j][0], qf[t][j][1]);
             else dev::mma_bf16_16816(s[t], a, qf[t][j][0], qf[t][j][1]);
-          }
-        }
-      } else if constexpr (Geo::kInt4) {
-        // a word: 8 dims, two k-steps; the first half of a lane's words is
-        // its first group, the rest its second
-        constexpr int kWords = D / 32;
-#pragma unroll
-        for (int w = 0; w < Geo::kKBytes / 4; ++w) {
-          const int wi = i * (Geo::kKBytes / 4) + w, half = wi >= kWords / 2 ? 1 : 0;
-          uint32_t f[4], f8[4];
-          dev::int4_to_f16x2x4(wg[w], kmul[0][half], f);
-          dev::int4_to_f16x2x4(wg8[w], kmul[1][half], f8);
-          const uint32_t a0[4] = {f[0], f8[0], f[1], f8[1]}, a1[4] = {f[2], f8[2], f[3], f8[3]};
-#pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            dev::mma_f16_16816(s[t], a0, qf[t][2 * wi][0], qf[t][2 * wi][1]);
-            dev::mma_f16_16816(s2[t], a1, qf[t][2 * wi + 1][0], qf[t][2 * wi + 1][1]);
           }
         }
       } else {
@@ -913,7 +835,7 @@ splitkv_decode_kernel(const AttnParams p, const StepParams sp) {
     }
 
     // O^T += V^T P^T : head_dim x 8 rows per n-tile.
-    constexpr int kWords = Geo::kVBytes >= 16 ? 4 : Geo::kVBytes / 4;  // words per row per piece
+    constexpr int kWords = Geo::kVBytes == 8 ? 2 : 4;  // words per row per piece
 #pragma unroll
     for (int vs = 0; vs < Geo::kVPieces; ++vs) {
       uint32_t r0[4], r1[4], r2[4], r3[4];
@@ -939,24 +861,6 @@ splitkv_decode_kernel(const AttnParams p, const StepParams sp) {
           for (int t = 0; t < NT; ++t) {
             dev::mma_bf16_16816(o[t][i], a, pb0[t], pb1[t]);
             dev::mma_bf16_16816(o[t][i], a, pl0[t], pl1[t]);
-          }
-        }
-      } else if constexpr (Geo::kInt4) {
-        // The low halves of word w of rows 2c / 2c + 1 hold the even dims of
-        // its 8, the high halves the odd ones: nibble n of each pairs the two
-        // tokens' codes of dim 8 w + 2 n (+ 1), m-tile 4 w + n's two rows.
-#pragma unroll
-        for (int w = 0; w < kWords; ++w) {
-          uint32_t e01[4], o01[4], e23[4], o23[4];
-          dev::int4_to_f16x2x4(dev::prmt(r0[w], r1[w], 0x5410u), vmul4[0], e01);
-          dev::int4_to_f16x2x4(dev::prmt(r0[w], r1[w], 0x7632u), vmul4[0], o01);
-          dev::int4_to_f16x2x4(dev::prmt(r2[w], r3[w], 0x5410u), vmul4[1], e23);
-          dev::int4_to_f16x2x4(dev::prmt(r2[w], r3[w], 0x7632u), vmul4[1], o23);
-#pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            const uint32_t a[4] = {e01[n], o01[n], e23[n], o23[n]};
-#pragma unroll
-            for (int t = 0; t < NT; ++t) dev::mma_f16_16816(o[t][4 * w + n], a, pb0[t], pb1[t]);
           }
         }
       } else {
@@ -1072,7 +976,6 @@ int launch_step_d(const AttnParams& p, const StepParams& sp, int dtype, int64_t*
     KVQ_STEP_CASE(KVQ_INT8_PER_TOKEN_HEAD)
     KVQ_STEP_CASE(KVQ_FP8_PER_TOKEN_HEAD)
     KVQ_STEP_CASE(KVQ_FP8_E5M2_PER_TOKEN_HEAD)
-    KVQ_STEP_CASE(KVQ_INT4_PER_TOKEN_HEAD)
     default:
       return KVQ_E_UNSUPPORTED;
   }
@@ -1092,7 +995,6 @@ int launch_decode_d(const AttnParams& p, int dtype, int ntiles, cudaStream_t str
     KVQ_DECODE_CASE(KVQ_INT8_PER_TOKEN_HEAD)
     KVQ_DECODE_CASE(KVQ_FP8_PER_TOKEN_HEAD)
     KVQ_DECODE_CASE(KVQ_FP8_E5M2_PER_TOKEN_HEAD)
-    KVQ_DECODE_CASE(KVQ_INT4_PER_TOKEN_HEAD)
     default:
       return KVQ_E_UNSUPPORTED;
   }

@@ -35,14 +35,14 @@ int launch_merge(const AttnParams& p, int head_dim, int64_t num_merges, void* st
   return KVQ_OK;
 }
 
-int launch_merge_step(const AttnParams& p, const StepParams& sp, int head_dim, int64_t warps,
-                      void* stream) {
+int launch_merge_step(const AttnParams& p, const StepParams& sp, int dtype, int head_dim,
+                      int64_t warps, void* stream) {
   if (sp.num_tiles <= 0) return KVQ_OK;
   void (*kern)(AttnParams, StepParams, int64_t);
   switch (head_dim) {
-    case 64: kern = merge_step_kernel<64>; break;
-    case 128: kern = merge_step_kernel<128>; break;
-    case 256: kern = merge_step_kernel<256>; break;
+    case 64: kern = is_int4(dtype) ? merge_step_kernel<64, true> : merge_step_kernel<64, false>; break;
+    case 128: kern = is_int4(dtype) ? merge_step_kernel<128, true> : merge_step_kernel<128, false>; break;
+    case 256: kern = is_int4(dtype) ? merge_step_kernel<256, true> : merge_step_kernel<256, false>; break;
     default: return KVQ_E_UNSUPPORTED;
   }
   cudaLaunchConfig_t cfg = {};
@@ -67,6 +67,8 @@ int launch_merge_step(const AttnParams& p, const StepParams& sp, int head_dim, i
   int launch_decode_d##D##_alibi(const AttnParams&, int, int, void*);                       \
   int launch_step_d##D(const AttnParams&, const StepParams&, int, int64_t*, void*);         \
   int launch_step_d##D##_alibi(const AttnParams&, const StepParams&, int, int64_t*, void*); \
+  int launch_int4_decode_d##D(const AttnParams&, bool, int, void*);                         \
+  int launch_int4_step_d##D(const AttnParams&, const StepParams&, bool, int64_t*, void*);   \
   int launch_prefill_d##D(const AttnParams&, const PrefillMaps&, int, int64_t, void*);      \
   int launch_prefill_d##D##_alibi(const AttnParams&, const PrefillMaps&, int, int64_t, void*);
 KVQ_DECLARE(64)
@@ -77,6 +79,14 @@ KVQ_DECLARE(256)
 int launch_decode(const AttnParams& p, int dtype, int head_dim, int ntiles, void* stream) {
   if (p.num_chunks <= 0) return KVQ_OK;
   const bool al = uses_alibi(p);
+  if (is_int4(dtype)) {
+    switch (head_dim) {
+      case 64: return launch_int4_decode_d64(p, al, ntiles, stream);
+      case 128: return launch_int4_decode_d128(p, al, ntiles, stream);
+      case 256: return launch_int4_decode_d256(p, al, ntiles, stream);
+      default: return KVQ_E_UNSUPPORTED;
+    }
+  }
   switch (head_dim) {
     case 64: return al ? launch_decode_d64_alibi(p, dtype, ntiles, stream)
                        : launch_decode_d64(p, dtype, ntiles, stream);
@@ -91,6 +101,14 @@ int launch_decode(const AttnParams& p, int dtype, int head_dim, int ntiles, void
 namespace {
 int step_dispatch(const AttnParams& p, const StepParams& sp, int dtype, int head_dim, bool al,
                   int64_t* warps, void* stream) {
+  if (is_int4(dtype)) {
+    switch (head_dim) {
+      case 64: return launch_int4_step_d64(p, sp, al, warps, stream);
+      case 128: return launch_int4_step_d128(p, sp, al, warps, stream);
+      case 256: return launch_int4_step_d256(p, sp, al, warps, stream);
+      default: return KVQ_E_UNSUPPORTED;
+    }
+  }
   switch (head_dim) {
     case 64: return al ? launch_step_d64_alibi(p, sp, dtype, warps, stream)
                        : launch_step_d64(p, sp, dtype, warps, stream);
@@ -103,8 +121,9 @@ int step_dispatch(const AttnParams& p, const StepParams& sp, int dtype, int head
 }
 }  // namespace
 
-int step_warps(int dtype, int head_dim, bool alibi, int max_rows, int64_t* warps) {
+int step_warps(int dtype, int heads_kv, int head_dim, bool alibi, int max_rows, int64_t* warps) {
   AttnParams p{};
+  p.heads_kv = heads_kv;
   StepParams sp{};
   sp.max_rows = max_rows;
   *warps = 0;

@@ -1,0 +1,886 @@
+// kvq_decode_int4.cuh -- split-KV attention of small row tiles (decode) over
+// the 4-bit paged cache, and the fused decode step of that cache.
+//
+// What it computes is the attention of kvq_decode.cuh (same masks, soft cap,
+// ALiBi, sinks, partial rows and merge) for rows of D/2 code bytes and a
+// 16-byte tail of scales: k_jd = s_j m_jg c_jd.  m c is an integer of at most
+// 10 bits, so it enters the f16 MMAs exactly; s_j multiplies the fp32 scores
+// (K) and joins the softmax weights (V).
+//
+// GB300 design.  A 4-bit chunk of 16 tokens is 2560 bytes a head at D = 128,
+// so at the memory's rate a warp has some 450 issue slots for it, and a
+// kernel that fetches its rows lane by lane (kvq_decode.cuh) spends more than
+// that (560 instructions, with a quarter of them for loads, and 71 us for
+// the 64-request decode batch).  Here:
+//   * One warp per kv head, all heads of a group side by side in a CTA on the
+//     same chunks (the plan's head lockstep).  A token's rows of all heads
+//     lie next to each other, so the group's chunk is copied into shared
+//     memory by bulk copies of whole tokens (or of the whole chunk), with
+//     no address, predicate or register in the consumers, and several
+//     chunks in flight (kStages of the geometry).
+//   * No producer warp: the warps of a group issue the copies in turn (chunk
+//     k by warp k mod Hg), two chunks behind the ring's end, so that the
+//     wait for the slot's last readers is over before it is asked for.
+//     Records (slots, masks) are prepared by the lanes 32 turns at a time.
+//   * Rows are laid out in shared memory at a pitch of 16 bytes more than a
+//     multiple of 128 and MMA row g is token pi(g) = {0,4,2,6,12,8,14,10}[g]
+//     of the chunk (row g + 8 the token after it): then K's 16-byte reads
+//     (eight lanes: two rows), V's reads (rows pi(2c)) and the tails' all
+//     cover the 32 banks once.  The token order of a softmax is free.
+//   * The lazy reference maximum and the value scales' power-of-two reference
+//     move on one warp vote; the common chunk has no shuffle.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <atomic>
+
+#include "kvq_cache_row.cuh"
+#include "kvq_decode.cuh"
+#include "kvq_device.cuh"
+#include "kvq_internal.h"
+#include "kvq_tcgen05.cuh"
+
+namespace kvq {
+
+template <int D>
+struct Int4Row {
+  static constexpr int kCodes = D / 2;
+  static constexpr int kRow = row_bytes(KVQ_INT4_PER_TOKEN_HEAD, D);
+  static constexpr int kKBytes = D / 8 >= 16 ? 16 : D / 8;  // bytes of a K piece
+  static constexpr int kK16 = D / 8 / kKBytes;              // K pieces per lane per row
+  static constexpr int kKWords = D / 32;                    // K code words per lane per row
+  static constexpr int kVWords = D / 64;                    // V code words per lane per row
+  static constexpr int kRun = 2 * kKBytes;                  // consecutive dims of a K piece
+  static constexpr int kKsteps = D / 16, kMtiles = D / 16;
+  // A lane's 8-dim K words: the first half belongs to its first group, the
+  // rest to its second: groups 2c and 2c + 1 (D = 256: c and c + 4).
+};
+
+namespace i4 {
+
+__device__ __forceinline__ int pi_of(int g) { return (int)((0xAE8C6240u >> (4 * g)) & 15u); }
+
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" :: "r"(bar) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_expect_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" :: "r"(bar), "r"(bytes)
+               : "memory");
+}
+// (sizes and both addresses are multiples of 16 bytes)
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+               :: "r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" :: "r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+// Bounded wait of a whole warp: false on a timeout (about a second), here or
+// in another warp.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort) {
+  if (__all_sync(0xffffffffu, tc::mbar_try_wait(bar, parity))) return true;
+  const long long t0 = clock64();
+  while (true) {
+    if (__all_sync(0xffffffffu, tc::mbar_try_wait(bar, parity))) return true;
+    if (__any_sync(0xffffffffu, *abort != 0u)) return false;
+    if (__any_sync(0xffffffffu, clock64() - t0 > 2000000000LL)) {
+      *abort = 1u;
+      return false;
+    }
+  }
+}
+
+}  // namespace i4
+
+// The fused step's plan: one tile per request (its kv heads share the chunk
+// ranges), by the kernel's first CTA.  A request with more rows than the
+// launch was built for (or more queries than keys) is left out and flags the
+// error word.
+__device__ __forceinline__ void plan_step_int4(const AttnParams& p, const StepParams& sp, int segments) {
+  __shared__ int32_t warp_sums[32];
+  __shared__ int32_t total;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nthr = blockDim.x;
+  const int nt = sp.num_req;
+  const int per = (nt + nthr - 1) / nthr;
+  const int t0 = min(nt, tid * per), t1 = min(nt, t0 + per);
+  auto chunks_of = [&](int r, bool store) {
+    const int Q = sp.in_query_start_loc[r + 1] - sp.in_query_start_loc[r];
+    const int L = sp.in_seq_lens[r];
+    if (Q <= 0 || L < Q || Q > sp.max_rows / p.group) {
+      if (store) {
+        if (Q != 0) atomicExch(p.error_flag, 2);  // (1 is a timeout)
+        sp.tiles[r] = make_int4(0, 0, 0, 0);
+      }
+      return 0;
+    }
+    const int lo = p.window > 0 ? max(0, L - Q - p.window + 1) : 0;
+    if (store) sp.tiles[r] = make_int4(lo / kChunkTokens, lo, L, Q * p.group);
+    return (L - 1) / kChunkTokens + 1 - lo / kChunkTokens;
+  };
+  int local = 0;
+  for (int t = t0; t < t1; ++t) local += chunks_of(t, true);
+  int incl = local;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += v;
+  }
+  if (lane == 31) warp_sums[warp] = incl;
+  __syncthreads();
+  int run = incl - local;
+  for (int w = 0; w < warp; ++w) run += warp_sums[w];
+  const int run0 = run;
+  for (int t = t0; t < t1; ++t) {
+    sp.prefix[t] = run;
+    run += chunks_of(t, false);
+  }
+  if (tid == nthr - 1) {
+    sp.prefix[nt] = run;
+    total = run;
+  }
+  __syncthreads();
+  // Each segment's first tile: segment v starts at floor(v T / S), which lies
+  // in tile t for v in [ceil(f0 S / T), ceil(f1 S / T)).
+  const int64_t T = total, S = int4_step_segments(T, segments);
+  if (T > 0) {
+    int64_t f0 = run0;
+    for (int t = t0; t < t1; ++t) {
+      const int64_t f1 = f0 + chunks_of(t, false);
+      for (int64_t v = (f0 * S + T - 1) / T; v < (f1 * S + T - 1) / T && v < S; ++v)
+        sp.warp_tile[v] = t;
+      f0 = f1;
+    }
+  }
+}
+
+template <int D, int NT, bool AL, bool DEV>
+__global__ void __launch_bounds__(32 * int4_max_warps(D, NT), int4_min_ctas(D, NT))
+int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge) {
+  using Row = Int4Row<D>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint32_t abort_word;
+  const int lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);  // (uniform)
+  const int g = lane >> 2;
+  const int c = lane & 3;
+
+  // The merge of the cut tiles (its own kernel, after this one) may be
+  // scheduled now: it waits for this grid to complete.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  const int grp = warp / ge.hg, j = warp % ge.hg;  // the group, and the warp's head in it
+  const uint32_t sbase = dev::smem_u32(smem) + (uint32_t)(grp * ge.stages * ge.stage_bytes);
+  const uint32_t meta = dev::smem_u32(smem) + (uint32_t)(ge.gpc * ge.stages * ge.stage_bytes) +
+                        (uint32_t)(grp * ge.stages * 32);  // per stage: record (16), full, empty
+  volatile uint32_t* const abort = &abort_word;
+  if (threadIdx.x == 0) {
+    abort_word = 0u;
+    const uint32_t m0 = dev::smem_u32(smem) + (uint32_t)(ge.gpc * ge.stages * ge.stage_bytes);
+    for (int i = 0; i < ge.gpc * ge.stages; ++i) {
+      tc::mbar_init(m0 + 32u * i + 16, 1);
+      tc::mbar_init(m0 + 32u * i + 24, ge.hg);
+    }
+    tc::mbar_fence_init();
+  }
+
+  // ---- the fused step's prologue -------------------------------------------
+  if constexpr (DEV) {
+    StageLane st;
+    stage_issue(sp, st);
+    row::write_rows<KVQ_INT4_PER_TOKEN_HEAD, D>(
+        sp.key, sp.value, sp.num_tokens, sp.key_stride, sp.value_stride, p.heads_kv, sp.key_cache,
+        sp.value_cache, sp.num_slots, sp.slot_mapping, p.k_scale, p.v_scale, blockDim.x, threadIdx.x,
+        blockIdx.x, gridDim.x);
+    stage_finish(sp, st);
+    if (blockIdx.x == 0) plan_step_int4(p, sp, ge.segments);
+    // (the bulk copies below read rows that other CTAs stored: both sides
+    // order their proxies)
+    asm volatile("fence.proxy.async.global;" ::: "memory");
+    if (!grid_barrier(sp.barrier, p.error_flag)) return;
+    asm volatile("fence.proxy.async.global;" ::: "memory");
+  } else {
+    __syncthreads();
+  }
+
+  // ---- this warp's segment of the flat chunk sequence of its head -----------
+  const int glin = blockIdx.x * ge.gpc + grp;  // (segment, head group)
+  const int seg = glin / ge.hsplit, hgrp = glin % ge.hsplit;
+  const int head = hgrp * ge.hg + j;
+  const int gw = seg * p.heads_kv + head;
+  int seg0 = 0, n = 0, first_piece = 0;
+  if constexpr (DEV) {
+    const int64_t T = __ldcg(sp.prefix + sp.num_req);
+    const int S = int4_step_segments(T, ge.segments);
+    if (seg < S) {
+      seg0 = (int)((int64_t)seg * T / S);
+      n = (int)((int64_t)(seg + 1) * T / S) - seg0;
+      if (n > 0) first_piece = __ldcg(sp.warp_tile + seg);
+    }
+  } else if (seg < ge.segments) {
+    const WarpSeg ws = p.warp_seg[gw];
+    seg0 = ws.seg0;
+    n = ws.n;
+    first_piece = ws.piece;
+  }
+  if (n <= 0) return;  // (the whole group: its heads share the chunk range)
+
+  // ---- copies ----------------------------------------------------------------
+  // Chunk k of the segment is copied by warp k mod hg of the group; a lane
+  // holds the record of one of its warp's next 32 turns.
+  const int S = ge.stages, ahead = S - 2;
+  const int cpb = p.block_size / kChunkTokens;
+  const int tok_bytes = p.heads_kv * Row::kRow;       // a token's rows
+  const int copy_bytes = ge.hg * Row::kRow;           // the group's part of them
+  const uint32_t v_off = 16u * ge.pitch;              // V's rows in a stage
+  // Records of this warp's next 32 turns, one per lane: {first slot (-1: no
+  // block), first token, piece relative to the segment's first, live tokens}.
+  // (Filled together; the three dependent loads cost a group of one warp a
+  // few chunks of lead every 32, wider groups nothing.)
+  const uint32_t recs = dev::smem_u32(smem) + (uint32_t)ge.smem - (uint32_t)((warp + 1) * kInt4RecBytes);
+  int cur_piece = first_piece;
+  auto fill_records = [&](int turn0) {
+    const int pos = j + ge.hg * (turn0 + lane);
+    uint4 rec = make_uint4(0xFFFFFFFFu, 0u, 0u, 0u);
+    if (pos < n) {
+      const int flat = seg0 + pos;
+      int chunk, req, lo, hi;
+      if constexpr (DEV) {
+        while (cur_piece + 1 < sp.num_req && __ldcg(sp.prefix + cur_piece + 1) <= flat) ++cur_piece;
+        const int4 ti = __ldcg(sp.tiles + cur_piece);
+        chunk = ti.x + (flat - __ldcg(sp.prefix + cur_piece));
+        req = cur_piece;
+        lo = ti.y;
+        hi = ti.z;
+      } else {
+        while (cur_piece + 1 < p.num_pieces && __ldg(&p.pieces[cur_piece + 1].flat0) <= flat) ++cur_piece;
+        const DecodePiece* pc = p.pieces + cur_piece;
+        chunk = __ldg(&pc->chunk0) + (flat - __ldg(&pc->flat0));
+        req = __ldg(&pc->req);
+        lo = __ldg(&pc->any_lo);
+        hi = __ldg(&pc->any_hi);
+      }
+      // (the fused step's table width is not known on the host: check it
+      // here; the bounds-checked build checks the host plan's positions too)
+      const int lb = chunk / cpb;
+      const bool in_table = lb < p.block_table_stride;
+      if constexpr (KVQ_CHECKED && !DEV)
+        if (!in_table) atomicExch(p.error_flag, 2);
+      int blk = -1;
+      if (!(DEV || KVQ_CHECKED) || in_table) blk = p.block_table[(int64_t)req * p.block_table_stride + lb];
+      const bool ok = blk >= 0 && (int64_t)blk < p.num_blocks;
+      const int tok0 = chunk * kChunkTokens;
+      const int l = min(max(lo - tok0, 0), kChunkTokens), h = min(max(hi - tok0, 0), kChunkTokens);
+      rec.x = ok ? (uint32_t)(blk * p.block_size + (chunk - lb * cpb) * kChunkTokens) : 0xFFFFFFFFu;
+      rec.y = (uint32_t)tok0;
+      rec.z = (uint32_t)(cur_piece - first_piece);
+      rec.w = ok ? ((1u << h) - 1u) & ~((1u << l) - 1u) : 0u;
+    }
+    i4::sts128(recs + 16u * lane, rec);
+    __syncwarp();
+  };
+  int turn = 0;  // this warp's next turn
+  // This warp's next chunk into stage s, whose parity of use is u (first:
+  // the stage has not been used before).
+  auto issue = [&](int s, uint32_t u, bool first) -> bool {
+    if ((turn & 31) == 0) fill_records(turn);
+    const uint32_t full = meta + 32u * s + 16;
+    if (!first && !i4::warp_wait(full + 8, u ^ 1u, abort)) return false;
+    const uint4 rec = dev::lds128(recs + 16u * (turn & 31));
+    const int slot = (int)rec.x;
+    if (lane == 0) {
+      i4::sts128(meta + 32u * s, rec);
+      if (slot >= 0) i4::mbar_arrive_expect_tx(full, 2u * kChunkTokens * copy_bytes);
+      else i4::mbar_arrive(full);
+    }
+    __syncwarp();
+    if (slot >= 0) {
+      const uint32_t dst = sbase + (uint32_t)(s * ge.stage_bytes);
+      if (ge.whole) {  // all heads, packed: one copy for K, one for V
+        if (lane < 2)
+          i4::bulk_load(dst + (lane ? v_off : 0u),
+                        (lane ? p.value_cache : p.key_cache) + (int64_t)slot * tok_bytes,
+                        kChunkTokens * tok_bytes, full);
+      } else {  // lane t: token t's K rows, lane 16 + t: its V rows
+        const int tk = lane & 15;
+        i4::bulk_load(dst + (lane < 16 ? 0u : v_off) + (uint32_t)(tk * ge.pitch),
+                      (lane < 16 ? p.key_cache : p.value_cache) + (int64_t)(slot + tk) * tok_bytes +
+                          hgrp * copy_bytes,
+                      copy_bytes, full);
+      }
+    }
+    ++turn;
+    return true;
+  };
+
+  // ---- per-piece state ---------------------------------------------------------
+  const float log2e = 1.4426950408889634f;
+  const float cap = p.soft_cap;
+  const float base_scale = p.sm_scale * (cap > 0.0f ? 1.0f : log2e) * dev::kInt4Unit;
+  const float cap_l2 = cap * log2e;
+  const float inv_cap = cap > 0.0f ? 1.0f / cap : 0.0f;
+  const int G = p.group;
+  const int W = p.window;
+  int cur = -1;                 // current piece, relative to the segment's first
+  int all_lo = 0, all_hi = 0;   // tokens that all its rows see
+  int len = 0, pos0 = 0, row0 = 0, row_end = 0;  // its keys, first query's position, rows
+  float score_mul = 0.0f;
+  uint32_t qf[NT][Row::kKsteps][2];
+  float o[NT][Row::kMtiles][4];
+  // a row's reference maximum less 6, in log2 units (the weights carry 2^6);
+  // kUnset before its first visible key
+  constexpr float kUnset = -1.0e30f;
+  float m_off[NT][2], l_run[NT][2];
+  // value scales enter as s 2^-ev, ev the exponent of the largest so far
+  int ev = -1000;
+  float sv_lim = 0.0f, to_ref = 0.0f;
+  float al_slope[NT][2];
+  int al_pos[NT][2];
+  const int tok_g = i4::pi_of(g);  // MMA row g's token of a chunk; row g + 8's is the next
+
+  // A piece's descriptor (read again where it is needed: it does not stay in
+  // registers) and its request's first query token.
+  struct Piece {
+    int req, row0, nrows, part, q0;
+    bool bad;  // (bounds-checked build) its rows lie outside q / out
+  };
+  auto piece_at = [&](int rel) {
+    Piece pc;
+    if constexpr (DEV) {
+      // The tile's part inside this segment; a cut tile's partial rows go to
+      // one of the warp's two 16-row slots: 2 gw for the tile the segment
+      // starts in, 2 gw + 1 for the one it ends in.
+      const int r = first_piece + rel;
+      const int f0 = __ldcg(sp.prefix + r), f1 = __ldcg(sp.prefix + r + 1);
+      pc.req = r;
+      pc.row0 = 0;
+      pc.nrows = __ldcg(&sp.tiles[r].w);
+      pc.part = f0 < seg0 || f1 > seg0 + n ? (2 * gw + (f0 <= seg0 ? 0 : 1)) * kTileMaxRows : -1;
+    } else {
+      const DecodePiece* d = p.pieces + first_piece + rel;
+      pc.req = d->req;
+      pc.row0 = d->row0;
+      pc.nrows = d->nrows;
+      pc.part = d->part;
+    }
+    pc.q0 = p.query_start_loc[pc.req];
+    pc.bad = false;
+    if constexpr (KVQ_CHECKED && !DEV) {
+      pc.bad = pc.q0 < 0 || pc.q0 + (pc.row0 + pc.nrows - 1) / G >= p.total_q_tokens;
+      if (pc.bad && lane == 0) atomicExch(p.error_flag, 2);
+    }
+    return pc;
+  };
+  // Start a piece: Q fragments (B operand of S^T = K Q^T) and masks.  Q enters
+  // the MMA exactly: bf16 values scaled by a power of two only.  Lane c holds
+  // dims 4 kRun i + kRun c + [0, kRun) of its rows.
+  auto start_piece = [&](int rel) {
+    const Piece pc = piece_at(rel);
+    const int q0 = pc.q0;
+    const int Q = p.query_start_loc[pc.req + 1] - q0;
+    const int L = p.seq_lens[pc.req];
+    const int p_min = L - Q + pc.row0 / G;
+    const int p_max = L - Q + (pc.row0 + pc.nrows - 1) / G;
+    len = L;
+    pos0 = L - Q;
+    row0 = pc.row0;
+    row_end = pc.row0 + pc.nrows;
+    all_lo = W > 0 ? p_max - W + 1 : 0;
+    all_hi = p.causal ? p_min + 1 : L;
+    float qv[NT][D / 4];
+    float qmax = 0.0f;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int nr = 8 * t + g;
+      const bool valid = nr < pc.nrows && !pc.bad;
+      const int R = pc.row0 + (valid ? nr : 0);
+      const uint16_t* src =
+          p.q + ((int64_t)(q0 + R / G) * p.heads_q + head * G + R % G) * D + Row::kRun * c;
+#pragma unroll
+      for (int i = 0; i < D / 4 / Row::kRun; ++i) {
+#pragma unroll
+        for (int h = 0; h < Row::kRun / 8; ++h) {
+          const uint4 w = valid ? *reinterpret_cast<const uint4*>(src + 4 * Row::kRun * i + 8 * h)
+                                : make_uint4(0, 0, 0, 0);
+          const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int e2 = 0; e2 < 4; ++e2) {
+            const int e = Row::kRun * i + 8 * h + 2 * e2;
+            qv[t][e] = dev::bf16_lo(ws[e2]);
+            qv[t][e + 1] = dev::bf16_hi(ws[e2]);
+            qmax = fmaxf(qmax, fmaxf(fabsf(qv[t][e]), fabsf(qv[t][e + 1])));
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) qmax = fmaxf(qmax, __shfl_xor_sync(0xffffffffu, qmax, off));
+    // Power-of-two shift that puts the largest |q| just under 2^15.
+    int shift = 0;
+    if (qmax > 0.0f && qmax < 3.0e38f) {
+      int e;
+      frexpf(qmax, &e);
+      shift = max(-126, min(126, 15 - e));
+    }
+    const float q_mul = __int_as_float((127 + shift) << 23);
+    const float q_unmul = __int_as_float((127 - shift) << 23);
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int s = 0; s < Row::kKsteps; ++s) {
+        qf[t][s][0] = dev::pack_f16x2(qv[t][4 * s] * q_mul, qv[t][4 * s + 1] * q_mul);
+        qf[t][s][1] = dev::pack_f16x2(qv[t][4 * s + 2] * q_mul, qv[t][4 * s + 3] * q_mul);
+      }
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int nr = min(8 * t + 2 * c + e, pc.nrows - 1);
+        if constexpr (AL) {
+          al_slope[t][e] = p.alibi_slopes[head * G + (pc.row0 + nr) % G] * log2e;
+          al_pos[t][e] = L - Q + (pc.row0 + nr) / G;
+        }
+        m_off[t][e] = kUnset;
+        l_run[t][e] = 0.0f;
+      }
+    score_mul = base_scale * q_unmul;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < Row::kMtiles; ++i) o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.0f;
+    ev = -1000;
+    sv_lim = to_ref = 0.0f;
+  };
+
+  // Finish a piece: its rows' outputs (or partials) straight from the MMA
+  // fragments.
+  auto finish_piece = [&](int rel) {
+    const Piece pc = piece_at(rel);
+    const int q0 = pc.q0;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1)
+          l_run[t][e] += __shfl_xor_sync(0xffffffffu, l_run[t][e], off);
+    const float unit = ev > -1000 ? ldexpf(dev::kInt4Unit, ev) : 1.0f;
+    // An attention sink joins the normaliser of a whole (uncut) tile here;
+    // a cut tile's merge adds it once.
+    if (p.sinks && pc.part < 0) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int nr = min(8 * t + 2 * c + e, pc.nrows - 1);
+          const float sk = p.sinks[head * G + (pc.row0 + nr) % G] * log2e;
+          if (m_off[t][e] > kUnset && sk != -INFINITY)
+            l_run[t][e] += exp2f(fminf(sk - m_off[t][e], 126.0f));
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int nr = 8 * t + 2 * c + e;
+        if (nr >= pc.nrows) continue;
+        const float l = l_run[t][e];
+        const float sc = (l > 0.0f ? 1.0f / l : 0.0f) * unit;
+        const int R = pc.row0 + nr;
+        if (pc.part < 0) {
+          if (pc.bad) continue;
+          uint16_t* dst = p.out + ((int64_t)(q0 + R / G) * p.heads_q + head * G + R % G) * D + g * (D / 8);
+          // (the lane's group of D / 8 dims: m-tile i holds dims 2 i, 2 i + 1)
+#pragma unroll
+          for (int i = 0; i < Row::kMtiles; i += 4)
+            *reinterpret_cast<uint4*>(dst + 2 * i) =
+                make_uint4(dev::pack_bf16x2(o[t][i][e] * sc, o[t][i][e + 2] * sc),
+                           dev::pack_bf16x2(o[t][i + 1][e] * sc, o[t][i + 1][e + 2] * sc),
+                           dev::pack_bf16x2(o[t][i + 2][e] * sc, o[t][i + 2][e + 2] * sc),
+                           dev::pack_bf16x2(o[t][i + 3][e] * sc, o[t][i + 3][e + 2] * sc));
+        } else {
+          float* dst = p.part_o + (int64_t)(pc.part + nr) * D + g * (D / 8);
+#pragma unroll
+          for (int i = 0; i < Row::kMtiles; i += 2)
+            *reinterpret_cast<float4*>(dst + 2 * i) = make_float4(
+                o[t][i][e] * sc, o[t][i][e + 2] * sc, o[t][i + 1][e] * sc, o[t][i + 1][e + 2] * sc);
+          if (g == 0)
+            p.part_lse[pc.part + nr] = l > 0.0f ? m_off[t][e] + 6.0f + log2f(l) : -INFINITY;
+        }
+      }
+  };
+
+  // ---- stream the segment --------------------------------------------------------
+  // Byte offsets, in a stage, of what this lane reads: its K piece of token
+  // pi(g) (row g + 8: a pitch on), that row's tail, and its V codes of tokens
+  // pi(2c) and pi(2c + 1) (rows 2c + 8, 2c + 9: a pitch on).
+  const uint32_t pitch = (uint32_t)ge.pitch;
+  const uint32_t row_g = tok_g * pitch + j * Row::kRow;
+  const uint32_t k_at = row_g + Row::kKBytes * c, t_at = row_g + Row::kCodes;
+  const uint32_t v_at0 = v_off + i4::pi_of(2 * c) * pitch + j * Row::kRow + Row::kVWords * 4 * g;
+  const uint32_t v_at1 = v_off + i4::pi_of(2 * c + 1) * pitch + j * Row::kRow + Row::kVWords * 4 * g;
+  // multiplier bytes of this lane in a tail's two words: 2c and 2c + 1; at D
+  // = 256 its K groups are c and c + 4
+  const bool up = c >= 2;
+  const uint32_t pair_sel = c & 1 ? 0x4342u : 0x4140u;          // (byte, 0x64) twice
+  const uint32_t kpair_sel = (uint32_t)c | 0x40u | ((uint32_t)c << 8) | 0x4000u;
+
+  // Iteration i reads chunk i and has chunk i + ahead copied (the first
+  // `ahead` iterations only copy); the last one finishes the last piece.
+  int st = 0, kst = 0, kw = 0;     // stage of chunk i; stage and warp of chunk i + ahead
+  uint32_t par = 0, kpar = 0;
+  for (int i = -ahead;; ++i) {
+    if (i + ahead < n) {
+      if (kw == j && !issue(kst, kpar, i < 2)) break;
+      if (++kw == ge.hg) kw = 0;
+      if (++kst == S) {
+        kst = 0;
+        kpar ^= 1u;
+      }
+    }
+    if (i < 0) continue;
+    const uint32_t sb = sbase + (uint32_t)(st * ge.stage_bytes);
+    const uint32_t mb = meta + 32u * st;
+    uint4 rec = make_uint4(0u, 0u, 0xFFFFFFFEu, 0u);
+    if (i < n) {
+      if (!i4::warp_wait(mb + 16, par, abort)) break;
+      rec = dev::lds128(mb);
+    }
+    if ((int)rec.z != cur) {
+      if (cur >= 0) finish_piece(cur);
+      if (i == n) return;
+      cur = (int)rec.z;
+      start_piece(cur);
+    }
+    const int tok0 = (int)rec.y;
+
+    // tails: {s, m_0..3, m_4..7} of rows g and g + 8 of K and of V
+    const uint4 tk0 = dev::lds128(sb + t_at), tk1 = dev::lds128(sb + t_at + pitch);
+    const uint4 tv0 = dev::lds128(sb + t_at + v_off), tv1 = dev::lds128(sb + t_at + v_off + pitch);
+    uint4 kc[2][Row::kK16];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int q = 0; q < Row::kK16; ++q) {
+        if constexpr (Row::kKBytes == 8) {
+          const uint2 w = i4::lds64(sb + k_at + h * pitch);
+          kc[h][q] = make_uint4(w.x, w.y, 0, 0);
+        } else {
+          kc[h][q] = dev::lds128(sb + k_at + h * pitch + 64 * q);
+        }
+      }
+    uint32_t vc[4][Row::kVWords];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const uint32_t a = sb + (r & 1 ? v_at1 : v_at0) + (r >= 2 ? pitch : 0u);
+      if constexpr (Row::kVWords == 1) {
+        vc[r][0] = i4::lds32(a);
+      } else if constexpr (Row::kVWords == 2) {
+        const uint2 w = i4::lds64(a);
+        vc[r][0] = w.x;
+        vc[r][1] = w.y;
+      } else {
+        const uint4 w = dev::lds128(a);
+        vc[r][0] = w.x;
+        vc[r][1] = w.y;
+        vc[r][2] = w.z;
+        vc[r][3] = w.w;
+      }
+    }
+    const float sk0 = __uint_as_float(tk0.x), sk1 = __uint_as_float(tk1.x);
+    float sv0 = __uint_as_float(tv0.x), sv1 = __uint_as_float(tv1.x);
+    const uint32_t bias = 0x64646464u;  // f16 1024 + byte
+    // V's multipliers, transposed to the token pairs its codes form
+    uint32_t vm0 = dev::prmt(up ? tv0.z : tv0.y, bias, pair_sel);
+    uint32_t vm1 = dev::prmt(up ? tv1.z : tv1.y, bias, pair_sel);
+    const uint32_t live = rec.w;
+    if (live != 0xFFFFu) {
+      // Tokens outside the piece's keys (or its whole block): whatever the
+      // cache holds there takes no part.  (K's scores are replaced below.)
+      const bool l0 = (live >> tok_g) & 1u, l1 = (live >> (tok_g + 1)) & 1u;
+      sv0 = l0 ? sv0 : 0.0f;
+      sv1 = l1 ? sv1 : 0.0f;
+      vm0 = l0 ? vm0 : 0x64006400u;
+      vm1 = l1 ? vm1 : 0x64006400u;
+    }
+
+    // S^T = K Q^T : 16 tokens x 8 rows per n-tile; even and odd k-steps in
+    // separate accumulators to halve the dependent MMA chain.
+    float s[NT][4], s2[NT][4];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[t][e] = s2[t][e] = 0.0f;
+    {
+      dev::Int4Mul km[2][2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint4 tl = h ? tk1 : tk0;
+        if constexpr (D == 256) {
+          km[h][0] = dev::int4_mul(dev::prmt(tl.y, bias, kpair_sel));
+          km[h][1] = dev::int4_mul(dev::prmt(tl.z, bias, kpair_sel));
+        } else {
+          const uint32_t pr = dev::prmt(up ? tl.z : tl.y, bias, pair_sel);
+          km[h][0] = dev::int4_mul(dev::prmt(pr, pr, 0x1010u));
+          km[h][1] = dev::int4_mul(dev::prmt(pr, pr, 0x3232u));
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < Row::kK16; ++q) {
+        const uint32_t w0[4] = {kc[0][q].x, kc[0][q].y, kc[0][q].z, kc[0][q].w};
+        const uint32_t w1[4] = {kc[1][q].x, kc[1][q].y, kc[1][q].z, kc[1][q].w};
+#pragma unroll
+        for (int w = 0; w < Row::kKBytes / 4; ++w) {
+          const int wi = q * (Row::kKBytes / 4) + w, half = wi >= Row::kKWords / 2 ? 1 : 0;
+          uint32_t f[4], f8[4];
+          dev::int4_to_f16x2x4(w0[w], km[0][half], f);
+          dev::int4_to_f16x2x4(w1[w], km[1][half], f8);
+          const uint32_t a0[4] = {f[0], f8[0], f[1], f8[1]}, a1[4] = {f[2], f8[2], f[3], f8[3]};
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            dev::mma_f16_16816(s[t], a0, qf[t][2 * wi][0], qf[t][2 * wi][1]);
+            dev::mma_f16_16816(s2[t], a1, qf[t][2 * wi + 1][0], qf[t][2 * wi + 1][1]);
+          }
+        }
+      }
+    }
+    // every lane has read the stage
+    __syncwarp();
+    if (lane == 0) i4::mbar_arrive(mb + 24);
+
+    // Scores in log2 units, masks.  The reference of a row moves only when a
+    // score exceeds it by more than 2^8, and the value scales' only when one
+    // is a binade larger (one vote): P = 2^(z - m_run + 6) <= 2^14 fits f16.
+    const bool full = live == 0xFFFFu && tok0 >= all_lo && tok0 + kChunkTokens <= all_hi;
+    const float zm0 = score_mul * sk0, zm1 = score_mul * sk1;
+    float z[NT][4];
+    bool grow = fmaxf(sv0, sv1) >= sv_lim && fmaxf(sv0, sv1) > 0.0f;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float v = (s[t][e] + s2[t][e]) * (e < 2 ? zm0 : zm1);
+        if (cap > 0.0f) v = cap_l2 * dev::tanh_exp(v * inv_cap);
+        if constexpr (AL)  // bias from the exact integer distance, after the cap
+          v = fmaf(al_slope[t][e & 1], (float)(tok0 + tok_g + (e >> 1) - al_pos[t][e & 1]), v);
+        z[t][e] = v;
+      }
+    }
+    if (!full) {
+      // (rare: the edges of a request's keys) the columns' own key ranges
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int pn = pos0 + min(row0 + 8 * t + 2 * c + (e & 1), row_end - 1) / G;
+          const int tok = tok0 + tok_g + (e >> 1);
+          const bool vis = ((live >> (tok_g + (e >> 1))) & 1u) && tok >= (W > 0 ? pn - W + 1 : 0) &&
+                           tok < (p.causal ? pn + 1 : len);
+          z[t][e] = vis ? z[t][e] : -INFINITY;
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      grow |= fmaxf(z[t][0], z[t][2]) > m_off[t][0] + 14.0f;
+      grow |= fmaxf(z[t][1], z[t][3]) > m_off[t][1] + 14.0f;
+    }
+    if (__any_sync(0xffffffffu, grow)) {
+      float mx = fmaxf(sv0, sv1);
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+      float alpha_v = 1.0f;
+      if (mx > 0.0f) {
+        const int e = max(-100, min(100, (int)((__float_as_uint(mx) >> 23) & 0xFFu) - 127));
+        if (e > ev) {
+          alpha_v = ev > -1000 ? ldexpf(1.0f, ev - e) : 0.0f;
+          ev = e;
+          to_ref = ldexpf(1.0f, -e);
+          sv_lim = ldexpf(1.0f, e + 1);
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        float alpha[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float cm = fmaxf(z[t][e], z[t][e + 2]);
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) cm = fmaxf(cm, __shfl_xor_sync(0xffffffffu, cm, off));
+          // (only a row that passed its limit moves)
+          const float mn = cm > m_off[t][e] + 14.0f ? cm - 6.0f : m_off[t][e];
+          alpha[e] = dev::fast_exp2(m_off[t][e] - mn);
+          m_off[t][e] = mn;
+          l_run[t][e] *= alpha[e];
+        }
+#pragma unroll
+        for (int i2 = 0; i2 < Row::kMtiles; ++i2) {
+          o[t][i2][0] *= alpha[0] * alpha_v;
+          o[t][i2][1] *= alpha[1] * alpha_v;
+          o[t][i2][2] *= alpha[0] * alpha_v;
+          o[t][i2][3] *= alpha[1] * alpha_v;
+        }
+      }
+    }
+    sv0 *= to_ref;
+    sv1 *= to_ref;
+    uint32_t pb0[NT], pb1[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const float p0 = dev::fast_exp2(z[t][0] - m_off[t][0]), p1 = dev::fast_exp2(z[t][1] - m_off[t][1]);
+      const float p2 = dev::fast_exp2(z[t][2] - m_off[t][0]), p3 = dev::fast_exp2(z[t][3] - m_off[t][1]);
+      l_run[t][0] += p0 + p2;
+      l_run[t][1] += p1 + p3;
+      // P^T (tokens x rows) -> B operand of O^T = V^T P^T via transposes.
+      pb0[t] = dev::movmatrix_trans(dev::pack_f16x2(p0 * sv0, p1 * sv0));
+      pb1[t] = dev::movmatrix_trans(dev::pack_f16x2(p2 * sv1, p3 * sv1));
+    }
+
+    // O^T += V^T P^T : head_dim x 8 rows per n-tile.  The low halves of word
+    // w of a row hold the even dims of its 8, the high halves the odd ones:
+    // nibble q of each pairs two tokens' codes of dim 8 w + 2 q (+ 1), the
+    // two rows of m-tile 4 w + q.
+    const dev::Int4Mul vf0 = dev::int4_mul(dev::movmatrix_trans(vm0));
+    const dev::Int4Mul vf1 = dev::int4_mul(dev::movmatrix_trans(vm1));
+#pragma unroll
+    for (int w = 0; w < Row::kVWords; ++w) {
+      uint32_t e01[4], o01[4], e23[4], o23[4];
+      dev::int4_to_f16x2x4(dev::prmt(vc[0][w], vc[1][w], 0x5410u), vf0, e01);
+      dev::int4_to_f16x2x4(dev::prmt(vc[0][w], vc[1][w], 0x7632u), vf0, o01);
+      dev::int4_to_f16x2x4(dev::prmt(vc[2][w], vc[3][w], 0x5410u), vf1, e23);
+      dev::int4_to_f16x2x4(dev::prmt(vc[2][w], vc[3][w], 0x7632u), vf1, o23);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t a[4] = {e01[q], o01[q], e23[q], o23[q]};
+#pragma unroll
+        for (int t = 0; t < NT; ++t) dev::mma_f16_16816(o[t][4 * w + q], a, pb0[t], pb1[t]);
+      }
+    }
+
+    if (++st == S) {
+      st = 0;
+      par ^= 1u;
+    }
+  }
+  // A wait was given up: the error word, NaN rows for this and the segment's
+  // remaining pieces, and a bounded wait for what may still be in flight
+  // before the CTA's shared memory is released.
+  if (lane == 0) atomicExch(p.error_flag, 1);
+  for (int rel = max(cur, 0); first_piece + rel < (DEV ? sp.num_req : p.num_pieces); ++rel) {
+    const int f0 = DEV ? __ldcg(sp.prefix + first_piece + rel) : p.pieces[first_piece + rel].flat0;
+    if (f0 >= seg0 + n) break;
+    const Piece pc = piece_at(rel);
+    for (int r = 0; r < pc.nrows && !pc.bad; ++r) {
+      const int R = pc.row0 + r;
+      for (int d = lane; d < D; d += 32) {
+        if (pc.part >= 0) p.part_o[(int64_t)(pc.part + r) * D + d] = NAN;
+        else p.out[((int64_t)(pc.q0 + R / G) * p.heads_q + head * G + R % G) * D + d] = 0x7FC0u;
+      }
+      if (pc.part >= 0 && lane == 0) p.part_lse[pc.part + r] = 0.0f;
+    }
+  }
+  for (int s = 0; s < S; ++s)
+    (void)tc::mbar_wait(meta + 32u * s + 16, s < kst ? kpar : kpar ^ 1u, 200000000LL);
+}
+
+// The launches' shared memory limit, raised once per device.
+inline bool int4_raise_smem(const void* kern, std::atomic<bool>* raised) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  if (dev < kMaxCachedDevices && raised[dev].load(std::memory_order_acquire)) return true;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kInt4MaxSmem) !=
+      cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  if (dev < kMaxCachedDevices) raised[dev].store(true, std::memory_order_release);
+  return true;
+}
+
+template <int D, int NT, bool AL>
+int launch_int4_decode(const AttnParams& p, cudaStream_t stream) {
+  Int4Geom ge = int4_geom(p.heads_kv, D, NT);
+  ge.segments = p.num_warps / p.heads_kv;
+  auto kern = int4_decode_kernel<D, NT, AL, false>;
+  static std::atomic<bool> raised[kMaxCachedDevices];
+  if (!int4_raise_smem(reinterpret_cast<const void*>(kern), raised)) return KVQ_E_CUDA;
+  const int ctas = (ge.segments * ge.hsplit + ge.gpc - 1) / ge.gpc;
+  StepParams none{};
+  kern<<<(unsigned)ctas, 32 * ge.hg * ge.gpc, ge.smem, stream>>>(p, none, ge);
+  return cudaGetLastError() == cudaSuccess ? KVQ_OK : KVQ_E_CUDA;
+}
+
+// The fused step: every CTA resident at once (a cooperative launch), as many
+// as fit on the device; *warps counts segments times kv heads (0 asks for
+// that number instead).
+template <int D, int NT, bool AL>
+int launch_int4_step(const AttnParams& p, const StepParams& sp, int64_t* warps, cudaStream_t stream) {
+  Int4Geom ge = int4_geom(p.heads_kv, D, NT);
+  auto kern = int4_decode_kernel<D, NT, AL, true>;
+  int dev = 0, sms = 0, per_sm = 0;
+  const int threads = 32 * ge.hg * ge.gpc;
+  // resident CTAs per SM of each geometry (a step asks twice, and the query
+  // costs microseconds), by device and kv heads
+  constexpr int kHeads = 64;
+  static std::atomic<int> resident[kMaxCachedDevices][kHeads];
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    cudaGetLastError();
+    return KVQ_E_CUDA;
+  }
+  const bool kept = dev < kMaxCachedDevices && p.heads_kv < kHeads;
+  if (kept) per_sm = resident[dev][p.heads_kv].load(std::memory_order_acquire);
+  if (per_sm <= 0) {
+    static std::atomic<bool> raised[kMaxCachedDevices];
+    if (!int4_raise_smem(reinterpret_cast<const void*>(kern), raised) ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, ge.smem) != cudaSuccess ||
+        per_sm <= 0) {
+      cudaGetLastError();
+      return KVQ_E_CUDA;
+    }
+    if (kept) resident[dev][p.heads_kv].store(per_sm, std::memory_order_release);
+  }
+  const int64_t ctas = (int64_t)sms * per_sm;
+  ge.segments = (int)(ctas * ge.gpc / ge.hsplit);
+  if (ge.segments == 0) return KVQ_E_UNSUPPORTED;  // more head groups than resident
+  const int64_t want = (int64_t)ge.segments * p.heads_kv;
+  if (*warps == 0) {
+    *warps = want;
+    return KVQ_OK;
+  }
+  if (*warps != want) return KVQ_E_INVALID_ARG;
+  AttnParams pp = p;
+  StepParams ss = sp;
+  void* args[] = {&pp, &ss, &ge};
+  if (cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(kern), dim3((unsigned)ctas), dim3(threads),
+                                  args, ge.smem, stream) != cudaSuccess) {
+    cudaGetLastError();
+    return KVQ_E_CUDA;
+  }
+  return KVQ_OK;
+}
+
+template <int D, bool AL>
+int launch_int4_decode_d(const AttnParams& p, int ntiles, cudaStream_t stream) {
+  return ntiles == 1 ? launch_int4_decode<D, 1, AL>(p, stream) : launch_int4_decode<D, 2, AL>(p, stream);
+}
+template <int D, bool AL>
+int launch_int4_step_d(const AttnParams& p, const StepParams& sp, int64_t* warps, cudaStream_t stream) {
+  return sp.max_rows <= 8 ? launch_int4_step<D, 1, AL>(p, sp, warps, stream)
+                          : launch_int4_step<D, 2, AL>(p, sp, warps, stream);
+}
+
+}  // namespace kvq

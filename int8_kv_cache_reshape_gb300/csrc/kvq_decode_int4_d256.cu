@@ -1,0 +1,17 @@
+// kvq_decode_int4_d256.cu -- the 4-bit decode kernels and fused step for
+// head_dim 256 (one translation unit per head_dim and ALiBi setting keeps
+// the build parallel).
+#include "kvq_decode_int4.cuh"
+
+namespace kvq {
+int launch_int4_decode_d256_alibi(const AttnParams& p, int ntiles, void* stream);
+int launch_int4_step_d256_alibi(const AttnParams& p, const StepParams& sp, int64_t* warps, void* stream);
+int launch_int4_decode_d256(const AttnParams& p, bool alibi, int ntiles, void* stream) {
+  return alibi ? launch_int4_decode_d256_alibi(p, ntiles, stream)
+               : launch_int4_decode_d<256, false>(p, ntiles, static_cast<cudaStream_t>(stream));
+}
+int launch_int4_step_d256(const AttnParams& p, const StepParams& sp, bool alibi, int64_t* warps, void* stream) {
+  return alibi ? launch_int4_step_d256_alibi(p, sp, warps, stream)
+               : launch_int4_step_d<256, false>(p, sp, warps, static_cast<cudaStream_t>(stream));
+}
+}  // namespace kvq

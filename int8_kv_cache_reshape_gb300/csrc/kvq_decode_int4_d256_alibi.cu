@@ -1,0 +1,13 @@
+// kvq_decode_int4_d256_alibi.cu -- the 4-bit decode kernels and fused step for
+// head_dim 256 with ALiBi (one translation unit per head_dim and ALiBi setting keeps
+// the build parallel).
+#include "kvq_decode_int4.cuh"
+
+namespace kvq {
+int launch_int4_decode_d256_alibi(const AttnParams& p, int ntiles, void* stream) {
+  return launch_int4_decode_d<256, true>(p, ntiles, static_cast<cudaStream_t>(stream));
+}
+int launch_int4_step_d256_alibi(const AttnParams& p, const StepParams& sp, int64_t* warps, void* stream) {
+  return launch_int4_step_d<256, true>(p, sp, warps, static_cast<cudaStream_t>(stream));
+}
+}  // namespace kvq

@@ -589,7 +589,9 @@ int kvq_get_scheduler_metadata(int num_req, int heads_q, int heads_kv, int head_
   if (const char* env = std::getenv("KVQ_DECODE_WARPS")) forced = std::atoll(env);
   bool lockstep = kvq::row_bytes(dtype, head_dim) % 128 != 0;
   if (const char* env = std::getenv("KVQ_DECODE_LOCKSTEP")) lockstep = std::atoi(env) != 0;
-  lockstep = lockstep && heads_kv > 1;
+  // (the 4-bit decode kernel runs the kv heads of a segment in one CTA)
+  const bool int4 = kvq::is_int4(dtype);
+  lockstep = (lockstep || int4) && heads_kv > 1;
   s->partial_rows = 0;
   s->max_splits = 0;
   int64_t max_pieces = 0, max_merges = 0, num_warps = 0;
@@ -610,6 +612,21 @@ int kvq_get_scheduler_metadata(int num_req, int heads_q, int heads_kv, int head_
       std::stable_sort(tiles[cls].begin(), tiles[cls].end(),
                        [](const Tile& a, const Tile& b) { return a.kv_head < b.kv_head; });
     dl.lockstep = ls;
+    if (int4) {
+      // segments: as many as there are resident groups for, none shorter
+      // than kInt4MinChunks; every segment has a warp per kv head
+      const kvq::Int4Geom ge = kvq::int4_geom(heads_kv, head_dim, cls + 1);
+      const int64_t groups = (int64_t)sms * kvq::int4_min_ctas(head_dim, cls + 1) * ge.gpc;
+      const int64_t chunks = T / heads_kv;
+      int64_t segs = std::min<int64_t>(std::max<int64_t>(1, groups / ge.hsplit),
+                                       ceil_div(chunks, kvq::kInt4MinChunks));
+      if (forced > 0) segs = std::max<int64_t>(1, std::min(ceil_div(forced, heads_kv), chunks));
+      dl.num_warps = (int)(segs * heads_kv);
+      max_pieces += (int64_t)tiles[cls].size() + dl.num_warps - 1;
+      max_merges += (int64_t)tiles[cls].size();
+      num_warps += dl.num_warps;
+      continue;
+    }
     const int64_t max_ctas = (int64_t)sms * kvq::decode_min_ctas(dtype, head_dim, cls + 1);
     int64_t ctas = std::min<int64_t>(max_ctas, std::max<int64_t>(1, ceil_div(T, kvq::kDecodeWarps * kvq::kMinChunksPerWarp)));
     if (forced > 0) ctas = std::max<int64_t>(1, std::min<int64_t>(ceil_div(forced, kvq::kDecodeWarps), ceil_div(T, kvq::kDecodeWarps)));
@@ -859,7 +876,9 @@ int kvq_sched_get_info(const kvq_sched_t* s, kvq_sched_info_t* out) {
   out->max_splits = s->max_splits;
   out->total_query_tokens = s->total_q;
   out->workspace_bytes = s->workspace_bytes;
-  out->decode_smem_bytes = kvq::decode_smem_bytes(s->dtype, s->head_dim);
+  out->decode_smem_bytes = kvq::is_int4(s->dtype)
+                               ? kvq::int4_geom(s->heads_kv, s->head_dim, 1).smem
+                               : kvq::decode_smem_bytes(s->dtype, s->head_dim);
   out->decode_chunk_bytes = (size_t)kvq::decode_chunk_bytes(s->dtype, s->head_dim);
   out->num_prefill_tiles = (int64_t)s->prefill.size();
   out->prefill_smem_bytes =
@@ -1027,7 +1046,8 @@ int kvq_decode_step_workspace_size(int num_req, int heads_q, int heads_kv, int h
   if ((int64_t)max_query_len * G > kvq::kTileMaxRows) return KVQ_E_UNSUPPORTED;
   if ((int64_t)num_req * heads_kv > kvq::kMaxStepTiles) return KVQ_E_UNSUPPORTED;
   int64_t warps = 0;
-  const int rc = kvq::step_warps(dtype, head_dim, use_alibi != 0, step_rows(max_query_len, G), &warps);
+  const int rc = kvq::step_warps(dtype, heads_kv, head_dim, use_alibi != 0,
+                                 step_rows(max_query_len, G), &warps);
   if (rc != KVQ_OK) return rc;
   *workspace_bytes = kvq::step_workspace(num_req * heads_kv, head_dim, warps).total;
   return KVQ_OK;
@@ -1085,7 +1105,7 @@ int decode_step_impl(int num_req, int heads_q, int heads_kv, int head_dim, kvq_d
   const int G = heads_q / heads_kv;
   const int max_rows = step_rows(max_query_len, G);
   int64_t warps = 0;
-  rc = kvq::step_warps(dtype, head_dim, alibi_slopes != nullptr, max_rows, &warps);
+  rc = kvq::step_warps(dtype, heads_kv, head_dim, alibi_slopes != nullptr, max_rows, &warps);
   if (rc != KVQ_OK) return rc;
   const int num_tiles = num_req * heads_kv;
   const kvq::StepWorkspace lay = kvq::step_workspace(num_tiles, head_dim, warps);
@@ -1158,7 +1178,7 @@ int decode_step_impl(int num_req, int heads_q, int heads_kv, int head_dim, kvq_d
   // dependent launch
   rc = kvq::launch_decode_step(p, sp, dtype, head_dim, warps, stream);
   if (rc != KVQ_OK) return rc;
-  return kvq::launch_merge_step(p, sp, head_dim, warps, stream);
+  return kvq::launch_merge_step(p, sp, dtype, head_dim, warps, stream);
 }
 }  // namespace
 

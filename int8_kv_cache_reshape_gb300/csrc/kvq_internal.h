@@ -107,6 +107,78 @@ KVQ_HD constexpr size_t decode_smem_bytes(int dtype, int head_dim) {
   return (size_t)kDecodeWarps * decode_warp_smem(dtype, head_dim);
 }
 
+// ---- split-KV decode over 4-bit rows ---------------------------------------
+// A CTA has `gpc` groups of `hg` warps, one warp per kv head of a group; a
+// group streams one segment of the chunk sequence (the same for all heads:
+// head lockstep) through a ring of `stages` chunks in shared memory, K rows
+// then V rows of 16 tokens at `pitch` bytes a token.
+//
+// Warps per CTA and CTAs per SM, by registers (o, Q fragments and one
+// chunk's codes): 16 warps of 128 registers at head_dim 128 and up to 8 rows
+// a tile, 24 of 80 at head_dim 64, 12 of 168 and 8 of 255 above.
+KVQ_HD constexpr int int4_max_warps(int head_dim, int ntiles) {
+  return (head_dim == 128 && ntiles == 2) || (head_dim == 256 && ntiles == 1) ? 12 : 8;
+}
+KVQ_HD constexpr int int4_min_ctas(int head_dim, int ntiles) {
+  return head_dim == 64 ? (ntiles == 1 ? 3 : 2) : head_dim == 128 && ntiles == 1 ? 2 : 1;
+}
+// Dynamic shared memory of a CTA: its share of the SM's 228 KB.
+constexpr size_t kInt4MaxSmem = 224 * 1024;
+KVQ_HD constexpr size_t int4_smem_budget(int head_dim, int ntiles) {
+  return int4_min_ctas(head_dim, ntiles) == 3   ? 73 * 1024
+         : int4_min_ctas(head_dim, ntiles) == 2 ? 110 * 1024
+                                                : kInt4MaxSmem;
+}
+constexpr int kInt4RecBytes = 32 * 16;  // a warp's chunk records
+struct Int4Geom {
+  int hg, gpc;      // heads (warps) per group, groups per CTA
+  int hsplit;       // head groups: heads_kv / hg
+  int pitch;        // bytes between tokens in a stage
+  int stage_bytes, stages;
+  int whole;        // 1: a chunk's rows are one packed copy (pitch = a token's bytes)
+  int segments;     // cuts of the chunk sequence the launch has groups for
+  size_t smem;
+};
+// Heads per group: of the divisors of heads_kv that fit the CTA's warps, are
+// at least 4 (or all heads) and so copy long runs of a token's bytes, the one
+// that fills most warps, the larger of equals; failing that the largest.
+KVQ_HD constexpr Int4Geom int4_geom(int heads_kv, int head_dim, int ntiles) {
+  Int4Geom ge{};
+  const int maxw = int4_max_warps(head_dim, ntiles);
+  int best = 0;
+  for (int h = 1; h <= maxw && h <= heads_kv; ++h) {
+    if (heads_kv % h) continue;
+    const bool wide = h >= 4 || h == heads_kv;
+    const int warps = maxw / h * h;
+    if (!wide) ge.hg = h;              // (fallback, growing)
+    else if (warps >= best) {
+      best = warps;
+      ge.hg = h;
+    }
+  }
+  ge.gpc = maxw / ge.hg;
+  ge.hsplit = heads_kv / ge.hg;
+  const int row = row_bytes(KVQ_INT4_PER_TOKEN_HEAD, head_dim);
+  const int bytes = ge.hg * row;
+  // long runs at 16 bytes past a multiple of 128 (no bank conflicts); short
+  // ones packed, one copy for all 16 tokens
+  ge.whole = ge.hg == heads_kv && bytes < 256;
+  ge.pitch = ge.whole ? bytes : bytes + (16 + 128 - bytes % 128) % 128;
+  ge.stage_bytes = 2 * kChunkTokens * ge.pitch;
+  const int per_stage = ge.gpc * (ge.stage_bytes + 32), recs = ge.gpc * ge.hg * kInt4RecBytes;
+  const int fit = ((int)int4_smem_budget(head_dim, ntiles) - recs) / per_stage;
+  ge.stages = fit < 8 ? fit : 8;
+  ge.smem = (size_t)ge.stages * per_stage + recs;
+  return ge;
+}
+// Smallest segment worth a group.
+constexpr int kInt4MinChunks = 4;
+// Segments the fused step cuts a sequence of `chunks` into.
+KVQ_HD constexpr int int4_step_segments(int64_t chunks, int segments) {
+  const int64_t most = (chunks + kInt4MinChunks - 1) / kInt4MinChunks;
+  return (int)(most < 1 ? 1 : most < segments ? most : segments);
+}
+
 // ---- tensor-core prefill kernel -----------------------------------------
 // A prefill tile is 128 packed (query token, head) rows of one kv head; its
 // keys stream through in tiles of 64.  Requests whose rows per kv head
@@ -263,6 +335,7 @@ struct StepParams {
   int32_t* prefix;              // [num_tiles + 1]: flat index of each tile's first chunk
   int4* tiles;                  // [num_tiles]: {first chunk, key_lo, key_hi, rows}
   int32_t* warp_tile;           // [warps]: the tile holding each warp's first chunk
+                                // (4-bit rows: of all three, one per request or segment)
   uint32_t* barrier;            // [2]: arrivals, generation (grid barrier)
   int num_req, num_tiles;       // num_tiles = num_req * Hkv
   int max_rows;                 // 8 or 16: rows per tile the launch is built for
@@ -339,15 +412,16 @@ int launch_decode_step(const AttnParams& p, const StepParams& sp, int dtype, int
                        int64_t warps, void* stream);
 // Decode warps of the fused step's grid on the current device (every CTA
 // resident at once) in *warps; KVQ_OK or a KVQ_E_* status.
-int step_warps(int dtype, int head_dim, bool alibi, int max_rows, int64_t* warps);
+int step_warps(int dtype, int heads_kv, int head_dim, bool alibi, int max_rows, int64_t* warps);
 // The merge of the decode's cut tiles (p.merges, one CTA each), after the
 // decode kernels of a host-planned call.
 int launch_merge(const AttnParams& p, int head_dim, int64_t num_merges, void* stream);
 // The fused step's merge of its cut tiles: one CTA per tile of the device
 // plan (tiles left whole return at once), a programmatic dependent of the
-// fused kernel, whose `warps` warps cut the chunk sequence.
-int launch_merge_step(const AttnParams& p, const StepParams& sp, int head_dim, int64_t warps,
-                      void* stream);
+// fused kernel, whose `warps` warps cut the chunk sequence (4-bit rows: warps
+// / heads_kv segments, the kv heads of a request side by side).
+int launch_merge_step(const AttnParams& p, const StepParams& sp, int dtype, int head_dim,
+                      int64_t warps, void* stream);
 // The persistent prefill over p.num_prefill_tiles tiles on `ctas` CTAs
 // (at most one per SM is resident).
 int launch_prefill(const AttnParams& p, const PrefillMaps& maps, int dtype, int head_dim,

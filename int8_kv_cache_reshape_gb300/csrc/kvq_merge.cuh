@@ -165,8 +165,10 @@ __global__ void __launch_bounds__(kMergeThreads) merge_splits_kernel(const AttnP
 // The fused kernel cut its flat chunk sequence into `warps` equal segments;
 // split s is warp w0 + s (one warp per chunk when there are fewer chunks
 // than warps), whose partial rows sit in its second 16-row slot for the
-// tile its segment ends in, and in its first for the one it starts in.
-template <int D>
+// tile its segment ends in, and in its first for the one it starts in.  4-bit
+// rows: the plan has one tile per request, cut into segments that its kv heads
+// share; head h of segment v is warp v * Hkv + h.
+template <int D, bool I4>
 __global__ void __launch_bounds__(kMergeThreads) merge_step_kernel(const AttnParams p, const StepParams sp,
                                                                  int64_t warps) {
   const int t = blockIdx.x;
@@ -175,6 +177,22 @@ __global__ void __launch_bounds__(kMergeThreads) merge_step_kernel(const AttnPar
   // kernel's, read after the wait)
   const int q0 = sp.in_query_start_loc[t / p.heads_kv];
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  if constexpr (I4) {
+    const int r = t / p.heads_kv, h = t % p.heads_kv;
+    const int64_t T = __ldcg(sp.prefix + sp.num_req);
+    const int64_t f0 = __ldcg(sp.prefix + r), f1 = __ldcg(sp.prefix + r + 1);
+    const int4 ti = __ldcg(sp.tiles + r);
+    if (T <= 0 || f1 <= f0) return;
+    const int64_t S = int4_step_segments(T, (int)(warps / p.heads_kv));
+    const int v0 = (int)(((f0 + 1) * S - 1) / T), v1 = (int)((f1 * S - 1) / T);
+    if (v1 == v0) return;  // one piece: written by its warp
+    const int second = (v0 * T) / S < f0 ? 1 : 0;  // v0 starts in an earlier tile
+    const MergeItem m{r, h, 0, ti.w, 0, v1 - v0 + 1, 0, 0};
+    merge_tile<D, true>(p, m, q0, v1 - v0 + 1, [&](int s) {
+      return (2 * ((v0 + s) * p.heads_kv + h) + (s == 0 ? second : 0)) * kTileMaxRows;
+    });
+    return;
+  }
   const int64_t T = __ldcg(sp.prefix + sp.num_tiles);
   const int64_t f0 = __ldcg(sp.prefix + t), f1 = __ldcg(sp.prefix + t + 1);
   if (T <= 0 || f1 <= f0) return;
