@@ -460,7 +460,8 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge) {
 #pragma unroll
       for (int i = 0; i < Row::kMtiles; ++i) o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.0f;
     ev = -1000;
-    sv_lim = to_ref = 0.0f;
+    sv_lim = __uint_as_float(1u);  // (any positive scale moves it)
+    to_ref = 0.0f;
   };
 
   // Finish a piece: its rows' outputs (or partials) straight from the MMA
@@ -618,10 +619,6 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge) {
     // S^T = K Q^T : 16 tokens x 8 rows per n-tile; even and odd k-steps in
     // separate accumulators to halve the dependent MMA chain.
     float s[NT][4], s2[NT][4];
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s[t][e] = s2[t][e] = 0.0f;
     {
       dev::Int4Mul km[2][2];
 #pragma unroll
@@ -649,8 +646,13 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge) {
           const uint32_t a0[4] = {f[0], f8[0], f[1], f8[1]}, a1[4] = {f[2], f8[2], f[3], f8[3]};
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
-            dev::mma_f16_16816(s[t], a0, qf[t][2 * wi][0], qf[t][2 * wi][1]);
-            dev::mma_f16_16816(s2[t], a1, qf[t][2 * wi + 1][0], qf[t][2 * wi + 1][1]);
+            if (wi == 0) {
+              dev::mma_f16_16816_zero(s[t], a0, qf[t][0][0], qf[t][0][1]);
+              dev::mma_f16_16816_zero(s2[t], a1, qf[t][1][0], qf[t][1][1]);
+            } else {
+              dev::mma_f16_16816(s[t], a0, qf[t][2 * wi][0], qf[t][2 * wi][1]);
+              dev::mma_f16_16816(s2[t], a1, qf[t][2 * wi + 1][0], qf[t][2 * wi + 1][1]);
+            }
           }
         }
       }
@@ -659,43 +661,46 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge) {
     __syncwarp();
     if (lane == 0) i4::mbar_arrive(mb + 24);
 
-    // Scores in log2 units, masks.  The reference of a row moves only when a
-    // score exceeds it by more than 2^8, and the value scales' only when one
-    // is a binade larger (one vote): P = 2^(z - m_run + 6) <= 2^14 fits f16.
+    // Weights P = 2^(z - m_off), z the score in log2 units.  A row's reference
+    // moves only when a weight would pass 2^14 (f16's range), the value
+    // scales' only when one is a binade larger: one vote for both.
     const bool full = live == 0xFFFFu && tok0 >= all_lo && tok0 + kChunkTokens <= all_hi;
-    const float zm0 = score_mul * sk0, zm1 = score_mul * sk1;
-    float z[NT][4];
-    bool grow = fmaxf(sv0, sv1) >= sv_lim && fmaxf(sv0, sv1) > 0.0f;
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float v = (s[t][e] + s2[t][e]) * (e < 2 ? zm0 : zm1);
-        if (cap > 0.0f) v = cap_l2 * dev::tanh_exp(v * inv_cap);
-        if constexpr (AL)  // bias from the exact integer distance, after the cap
-          v = fmaf(al_slope[t][e & 1], (float)(tok0 + tok_g + (e >> 1) - al_pos[t][e & 1]), v);
-        z[t][e] = v;
+    const float zm[2] = {score_mul * sk0, score_mul * sk1};
+    auto score = [&](int t, int e) -> float {
+      float v = s[t][e] * zm[e >> 1];
+      if (cap > 0.0f) v = cap_l2 * dev::tanh_exp(v * inv_cap);
+      const int tok = tok0 + tok_g + (e >> 1);
+      if constexpr (AL)  // bias from the exact integer distance, after the cap
+        v = fmaf(al_slope[t][e & 1], (float)(tok - al_pos[t][e & 1]), v);
+      if (!full) {  // (rare: the edges of a request's keys) the column's own keys
+        const int pn = pos0 + min(row0 + 8 * t + 2 * c + (e & 1), row_end - 1) / G;
+        const bool vis = ((live >> (tok_g + (e >> 1))) & 1u) && tok >= (W > 0 ? pn - W + 1 : 0) &&
+                         tok < (p.causal ? pn + 1 : len);
+        v = vis ? v : -INFINITY;
       }
-    }
-    if (!full) {
-      // (rare: the edges of a request's keys) the columns' own key ranges
+      return v;
+    };
+    float x[NT][4], xmax = -INFINITY;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[t][e] += s2[t][e];
+    if (!AL && full && !(cap > 0.0f)) {
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int pn = pos0 + min(row0 + 8 * t + 2 * c + (e & 1), row_end - 1) / G;
-          const int tok = tok0 + tok_g + (e >> 1);
-          const bool vis = ((live >> (tok_g + (e >> 1))) & 1u) && tok >= (W > 0 ? pn - W + 1 : 0) &&
-                           tok < (p.causal ? pn + 1 : len);
-          z[t][e] = vis ? z[t][e] : -INFINITY;
-        }
+        for (int e = 0; e < 4; ++e) x[t][e] = fmaf(s[t][e], zm[e >> 1], -m_off[t][e & 1]);
+    } else {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[t][e] = score(t, e) - m_off[t][e & 1];
     }
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      grow |= fmaxf(z[t][0], z[t][2]) > m_off[t][0] + 14.0f;
-      grow |= fmaxf(z[t][1], z[t][3]) > m_off[t][1] + 14.0f;
-    }
-    if (__any_sync(0xffffffffu, grow)) {
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) xmax = fmaxf(xmax, x[t][e]);
+    if (__any_sync(0xffffffffu, xmax > 14.0f || fmaxf(sv0, sv1) >= sv_lim)) {
       float mx = fmaxf(sv0, sv1);
 #pragma unroll
       for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
@@ -714,14 +719,18 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge) {
         float alpha[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float cm = fmaxf(z[t][e], z[t][e + 2]);
+          const float z0 = score(t, e), z1 = score(t, e + 2);
+          float cm = fmaxf(z0, z1);
 #pragma unroll
           for (int off = 4; off < 32; off <<= 1) cm = fmaxf(cm, __shfl_xor_sync(0xffffffffu, cm, off));
-          // (only a row that passed its limit moves)
+          // (only a row that passed its limit moves: to the chunk's maximum,
+          // whose weight is 2^6)
           const float mn = cm > m_off[t][e] + 14.0f ? cm - 6.0f : m_off[t][e];
           alpha[e] = dev::fast_exp2(m_off[t][e] - mn);
           m_off[t][e] = mn;
           l_run[t][e] *= alpha[e];
+          x[t][e] = z0 - mn;
+          x[t][e + 2] = z1 - mn;
         }
 #pragma unroll
         for (int i2 = 0; i2 < Row::kMtiles; ++i2) {
@@ -737,8 +746,8 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge) {
     uint32_t pb0[NT], pb1[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const float p0 = dev::fast_exp2(z[t][0] - m_off[t][0]), p1 = dev::fast_exp2(z[t][1] - m_off[t][1]);
-      const float p2 = dev::fast_exp2(z[t][2] - m_off[t][0]), p3 = dev::fast_exp2(z[t][3] - m_off[t][1]);
+      const float p0 = dev::fast_exp2(x[t][0]), p1 = dev::fast_exp2(x[t][1]);
+      const float p2 = dev::fast_exp2(x[t][2]), p3 = dev::fast_exp2(x[t][3]);
       l_run[t][0] += p0 + p2;
       l_run[t][1] += p1 + p3;
       // P^T (tokens x rows) -> B operand of O^T = V^T P^T via transposes.
