@@ -67,8 +67,9 @@ int launch_merge_step(const AttnParams& p, const StepParams& sp, int dtype, int 
   int launch_decode_d##D##_alibi(const AttnParams&, int, int, void*);                       \
   int launch_step_d##D(const AttnParams&, const StepParams&, int, int64_t*, void*);         \
   int launch_step_d##D##_alibi(const AttnParams&, const StepParams&, int, int64_t*, void*); \
-  int launch_int4_decode_d##D(const AttnParams&, bool, int, void*);                         \
-  int launch_int4_step_d##D(const AttnParams&, const StepParams&, bool, int64_t*, void*);   \
+  int launch_int4_decode_d##D(const AttnParams&, const PrefillMaps&, bool, int, void*);     \
+  int launch_int4_step_d##D(const AttnParams&, const StepParams&, const PrefillMaps&, bool, \
+                            int64_t*, void*);                                               \
   int launch_prefill_d##D(const AttnParams&, const PrefillMaps&, int, int64_t, void*);      \
   int launch_prefill_d##D##_alibi(const AttnParams&, const PrefillMaps&, int, int64_t, void*);
 KVQ_DECLARE(64)
@@ -76,14 +77,15 @@ KVQ_DECLARE(128)
 KVQ_DECLARE(256)
 #undef KVQ_DECLARE
 
-int launch_decode(const AttnParams& p, int dtype, int head_dim, int ntiles, void* stream) {
+int launch_decode(const AttnParams& p, const PrefillMaps& maps, int dtype, int head_dim, int ntiles,
+                  void* stream) {
   if (p.num_chunks <= 0) return KVQ_OK;
   const bool al = uses_alibi(p);
   if (is_int4(dtype)) {
     switch (head_dim) {
-      case 64: return launch_int4_decode_d64(p, al, ntiles, stream);
-      case 128: return launch_int4_decode_d128(p, al, ntiles, stream);
-      case 256: return launch_int4_decode_d256(p, al, ntiles, stream);
+      case 64: return launch_int4_decode_d64(p, maps, al, ntiles, stream);
+      case 128: return launch_int4_decode_d128(p, maps, al, ntiles, stream);
+      case 256: return launch_int4_decode_d256(p, maps, al, ntiles, stream);
       default: return KVQ_E_UNSUPPORTED;
     }
   }
@@ -99,13 +101,13 @@ int launch_decode(const AttnParams& p, int dtype, int head_dim, int ntiles, void
 }
 
 namespace {
-int step_dispatch(const AttnParams& p, const StepParams& sp, int dtype, int head_dim, bool al,
-                  int64_t* warps, void* stream) {
+int step_dispatch(const AttnParams& p, const StepParams& sp, const PrefillMaps& maps, int dtype,
+                  int head_dim, bool al, int64_t* warps, void* stream) {
   if (is_int4(dtype)) {
     switch (head_dim) {
-      case 64: return launch_int4_step_d64(p, sp, al, warps, stream);
-      case 128: return launch_int4_step_d128(p, sp, al, warps, stream);
-      case 256: return launch_int4_step_d256(p, sp, al, warps, stream);
+      case 64: return launch_int4_step_d64(p, sp, maps, al, warps, stream);
+      case 128: return launch_int4_step_d128(p, sp, maps, al, warps, stream);
+      case 256: return launch_int4_step_d256(p, sp, maps, al, warps, stream);
       default: return KVQ_E_UNSUPPORTED;
     }
   }
@@ -127,12 +129,12 @@ int step_warps(int dtype, int heads_kv, int head_dim, bool alibi, int max_rows, 
   StepParams sp{};
   sp.max_rows = max_rows;
   *warps = 0;
-  return step_dispatch(p, sp, dtype, head_dim, alibi, warps, nullptr);
+  return step_dispatch(p, sp, PrefillMaps{}, dtype, head_dim, alibi, warps, nullptr);
 }
 
-int launch_decode_step(const AttnParams& p, const StepParams& sp, int dtype, int head_dim,
-                       int64_t warps, void* stream) {
-  return step_dispatch(p, sp, dtype, head_dim, uses_alibi(p), &warps, stream);
+int launch_decode_step(const AttnParams& p, const StepParams& sp, const PrefillMaps& maps, int dtype,
+                       int head_dim, int64_t warps, void* stream) {
+  return step_dispatch(p, sp, maps, dtype, head_dim, uses_alibi(p), &warps, stream);
 }
 
 int launch_prefill(const AttnParams& p, const PrefillMaps& maps, int dtype, int head_dim,

@@ -14,19 +14,22 @@
 // the 64-request decode batch).  Here:
 //   * One warp per kv head, all heads of a group side by side in a CTA on the
 //     same chunks (the plan's head lockstep).  A token's rows of all heads
-//     lie next to each other, so the group's chunk is copied into shared
-//     memory by bulk copies of whole tokens (or of the whole chunk), with
-//     no address, predicate or register in the consumers, and several
-//     chunks in flight (kStages of the geometry).
+//     lie next to each other, so 16 tokens of a block are one run of whole
+//     128-byte lines: one bulk tensor copy each for K and V, with no address,
+//     predicate or register in the consumers.  (Copies a token at a time
+//     reached the copy engine's rate, not the memory's: a 640-byte copy
+//     every 40-50 cycles of an SM, 375 us against 243 for 32 x 32768 keys.)
 //   * No producer warp: the warps of a group issue the copies in turn (chunk
 //     k by warp k mod Hg), two chunks behind the ring's end, so that the
 //     wait for the slot's last readers is over before it is asked for.
 //     Records (slots, masks) are prepared by the lanes 32 turns at a time.
-//   * Rows are laid out in shared memory at a pitch of 16 bytes more than a
-//     multiple of 128 and MMA row g is token pi(g) = {0,4,2,6,12,8,14,10}[g]
-//     of the chunk (row g + 8 the token after it): then K's 16-byte reads
-//     (eight lanes: two rows), V's reads (rows pi(2c)) and the tails' all
-//     cover the 32 banks once.  The token order of a softmax is free.
+//   * The copies write the 128-byte swizzle, and MMA row g is token pi(g) =
+//     {0,4,2,6,12,8,14,10}[g] of a half (row g + 8 the token after it): with 8
+//     heads (5 lines a token) K's 16-byte reads (eight lanes: two rows) and
+//     V's (rows pi(2c)) then cover the 32 banks once.  The token order of a
+//     softmax is free.
+//   * A warp takes both halves of a chunk in one go (32 tokens): waits,
+//     records, masks and votes once for two sets of MMAs.
 //   * The lazy reference maximum and the value scales' power-of-two reference
 //     move on one warp vote; the common chunk has no shuffle.
 #pragma once
@@ -68,10 +71,16 @@ __device__ __forceinline__ void mbar_arrive_expect_tx(uint32_t bar, uint32_t byt
   asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" :: "r"(bar), "r"(bytes)
                : "memory");
 }
-// (sizes and both addresses are multiples of 16 bytes)
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-               :: "r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
+__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+      :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* map, int group, int slot, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %3, %4}], "
+      "[%5];"
+      :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(group), "r"(slot), "r"(bar) : "memory");
 }
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
   uint2 v;
@@ -126,8 +135,8 @@ __device__ __forceinline__ void plan_step_int4(const AttnParams& p, const StepPa
       return 0;
     }
     const int lo = p.window > 0 ? max(0, L - Q - p.window + 1) : 0;
-    if (store) sp.tiles[r] = make_int4(lo / kChunkTokens, lo, L, Q * p.group);
-    return (L - 1) / kChunkTokens + 1 - lo / kChunkTokens;
+    if (store) sp.tiles[r] = make_int4(lo / kInt4Chunk, lo, L, Q * p.group);
+    return (L - 1) / kInt4Chunk + 1 - lo / kInt4Chunk;
   };
   int local = 0;
   for (int t = t0; t < t1; ++t) local += chunks_of(t, true);
@@ -166,8 +175,9 @@ __device__ __forceinline__ void plan_step_int4(const AttnParams& p, const StepPa
 }
 
 template <int D, int NT, bool AL, bool DEV>
-__global__ void __launch_bounds__(32 * int4_max_warps(D, NT), int4_min_ctas(D, NT))
-int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge) {
+__global__ void __launch_bounds__(32 * int4_max_warps(D, NT), 1)
+int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge,
+                   const __grid_constant__ PrefillMaps maps) {
   using Row = Int4Row<D>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint32_t abort_word;
@@ -181,17 +191,20 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   const int grp = warp / ge.hg, j = warp % ge.hg;  // the group, and the warp's head in it
-  const uint32_t sbase = dev::smem_u32(smem) + (uint32_t)(grp * ge.stages * ge.stage_bytes);
-  const uint32_t meta = dev::smem_u32(smem) + (uint32_t)(ge.gpc * ge.stages * ge.stage_bytes) +
-                        (uint32_t)(grp * ge.stages * 32);  // per stage: record (16), full, empty
+  // (the swizzle goes by shared-memory addresses: stages on 1 KB)
+  const uint32_t smem0 = (dev::smem_u32(smem) + 1023u) & ~1023u;
+  const uint32_t sbase = smem0 + (uint32_t)(grp * ge.stages * ge.stage_bytes);
+  const uint32_t meta0 = smem0 + (uint32_t)(ge.gpc * ge.stages * ge.stage_bytes);
+  const uint32_t meta = meta0 + (uint32_t)(grp * ge.stages * 32);  // per stage: record (16), full, empty
   volatile uint32_t* const abort = &abort_word;
   if (threadIdx.x == 0) {
     abort_word = 0u;
-    const uint32_t m0 = dev::smem_u32(smem) + (uint32_t)(ge.gpc * ge.stages * ge.stage_bytes);
     for (int i = 0; i < ge.gpc * ge.stages; ++i) {
-      tc::mbar_init(m0 + 32u * i + 16, 1);
-      tc::mbar_init(m0 + 32u * i + 24, ge.hg);
+      tc::mbar_init(meta0 + 32u * i + 16, 1);
+      tc::mbar_init(meta0 + 32u * i + 24, ge.hg);
     }
+    asm volatile("prefetch.tensormap [%0];" :: "l"(reinterpret_cast<uint64_t>(&maps.k)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" :: "l"(reinterpret_cast<uint64_t>(&maps.v)) : "memory");
     tc::mbar_fence_init();
   }
 
@@ -239,21 +252,22 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge) {
   // ---- copies ----------------------------------------------------------------
   // Chunk k of the segment is copied by warp k mod hg of the group; a lane
   // holds the record of one of its warp's next 32 turns.
-  const int S = ge.stages, ahead = S - 2;
-  const int cpb = p.block_size / kChunkTokens;
-  const int tok_bytes = p.heads_kv * Row::kRow;       // a token's rows
-  const int copy_bytes = ge.hg * Row::kRow;           // the group's part of them
-  const uint32_t v_off = 16u * ge.pitch;              // V's rows in a stage
-  // Records of this warp's next 32 turns, one per lane: {first slot (-1: no
-  // block), first token, piece relative to the segment's first, live tokens}.
-  // (Filled together; the three dependent loads cost a group of one warp a
-  // few chunks of lead every 32, wider groups nothing.)
-  const uint32_t recs = dev::smem_u32(smem) + (uint32_t)ge.smem - (uint32_t)((warp + 1) * kInt4RecBytes);
+  const int S = ge.stages, ahead = S - 1;
+  const int tok_bytes = ge.hg * Row::kRow;  // a token's rows of the group
+  const uint32_t v_off = 2u * ge.half_bytes;  // V's rows in a stage
+  // Records of this warp's next kInt4Turns turns, one per lane: {first token, piece
+  // relative to the segment's first, live tokens}, {first slot of each half of
+  // the chunk (-1: none of its keys, or no block)}.
+  // (Filled together; the three dependent loads cost a group of one warp its
+  // lead every 16 chunks, wider groups nothing.)
+  __shared__ uint4 recs_s[int4_max_warps(D, NT)][kInt4Turns][2];
+  const uint32_t recs = dev::smem_u32(recs_s[warp]);
   int cur_piece = first_piece;
   auto fill_records = [&](int turn0) {
     const int pos = j + ge.hg * (turn0 + lane);
-    uint4 rec = make_uint4(0xFFFFFFFFu, 0u, 0u, 0u);
-    if (pos < n) {
+    int slot[2] = {-1, -1}, tok0 = 0, rel = 0;
+    uint32_t live = 0;
+    if (lane < kInt4Turns && pos < n) {
       const int flat = seg0 + pos;
       int chunk, req, lo, hi;
       if constexpr (DEV) {
@@ -271,59 +285,61 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge) {
         lo = __ldg(&pc->any_lo);
         hi = __ldg(&pc->any_hi);
       }
+      tok0 = chunk * kInt4Chunk;
+      rel = cur_piece - first_piece;
       // (the fused step's table width is not known on the host: check it
       // here; the bounds-checked build checks the host plan's positions too)
-      const int lb = chunk / cpb;
-      const bool in_table = lb < p.block_table_stride;
-      if constexpr (KVQ_CHECKED && !DEV)
-        if (!in_table) atomicExch(p.error_flag, 2);
-      int blk = -1;
-      if (!(DEV || KVQ_CHECKED) || in_table) blk = p.block_table[(int64_t)req * p.block_table_stride + lb];
-      const bool ok = blk >= 0 && (int64_t)blk < p.num_blocks;
-      const int tok0 = chunk * kChunkTokens;
-      const int l = min(max(lo - tok0, 0), kChunkTokens), h = min(max(hi - tok0, 0), kChunkTokens);
-      rec.x = ok ? (uint32_t)(blk * p.block_size + (chunk - lb * cpb) * kChunkTokens) : 0xFFFFFFFFu;
-      rec.y = (uint32_t)tok0;
-      rec.z = (uint32_t)(cur_piece - first_piece);
-      rec.w = ok ? ((1u << h) - 1u) & ~((1u << l) - 1u) : 0u;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int tk = tok0 + 16 * u, lb = tk / p.block_size;
+        const int l = min(max(lo - tk, 0), 16), h = min(max(hi - tk, 0), 16);
+        if (h <= l) continue;  // no key of the piece (nor, perhaps, a block)
+        const bool in_table = lb < p.block_table_stride;
+        if constexpr (KVQ_CHECKED && !DEV)
+          if (!in_table) atomicExch(p.error_flag, 2);
+        int blk = -1;
+        if (!(DEV || KVQ_CHECKED) || in_table) blk = p.block_table[(int64_t)req * p.block_table_stride + lb];
+        if (blk >= 0 && (int64_t)blk < p.num_blocks) {
+          slot[u] = blk * p.block_size + (tk - lb * p.block_size);
+          live |= (((1u << h) - 1u) & ~((1u << l) - 1u)) << (16 * u);
+        }
+      }
     }
-    i4::sts128(recs + 16u * lane, rec);
+    if (lane < kInt4Turns) {
+      i4::sts128(recs + 32u * lane, make_uint4((uint32_t)tok0, (uint32_t)rel, live, 0u));
+      i4::sts128(recs + 32u * lane + 16, make_uint4((uint32_t)slot[0], (uint32_t)slot[1], 0u, 0u));
+    }
     __syncwarp();
   };
   int turn = 0;  // this warp's next turn
   // This warp's next chunk into stage s, whose parity of use is u (first:
   // the stage has not been used before).
   auto issue = [&](int s, uint32_t u, bool first) -> bool {
-    if ((turn & 31) == 0) fill_records(turn);
+    if (turn % kInt4Turns == 0) fill_records(turn);
     const uint32_t full = meta + 32u * s + 16;
     if (!first && !i4::warp_wait(full + 8, u ^ 1u, abort)) return false;
-    const uint4 rec = dev::lds128(recs + 16u * (turn & 31));
-    const int slot = (int)rec.x;
+    const uint4 rec = dev::lds128(recs + 32u * (turn % kInt4Turns));
+    const uint2 sl = i4::lds64(recs + 32u * (turn % kInt4Turns) + 16);
+    const int halves = ((int)sl.x >= 0) + ((int)sl.y >= 0);
     if (lane == 0) {
       i4::sts128(meta + 32u * s, rec);
-      if (slot >= 0) i4::mbar_arrive_expect_tx(full, 2u * kChunkTokens * copy_bytes);
+      if (halves) i4::mbar_arrive_expect_tx(full, (uint32_t)(halves * 2 * kChunkTokens * tok_bytes));
       else i4::mbar_arrive(full);
     }
     __syncwarp();
-    if (slot >= 0) {
-      const uint32_t dst = sbase + (uint32_t)(s * ge.stage_bytes);
-      if (ge.whole) {  // all heads, packed: one copy for K, one for V
-        if (lane < 2)
-          i4::bulk_load(dst + (lane ? v_off : 0u),
-                        (lane ? p.value_cache : p.key_cache) + (int64_t)slot * tok_bytes,
-                        kChunkTokens * tok_bytes, full);
-      } else {  // lane t: token t's K rows, lane 16 + t: its V rows
-        const int tk = lane & 15;
-        i4::bulk_load(dst + (lane < 16 ? 0u : v_off) + (uint32_t)(tk * ge.pitch),
-                      (lane < 16 ? p.key_cache : p.value_cache) + (int64_t)(slot + tk) * tok_bytes +
-                          hgrp * copy_bytes,
-                      copy_bytes, full);
-      }
+    // lanes 0-3: K and V of the first half, K and V of the second
+    const int slot = (int)(lane & 2 ? sl.y : sl.x);
+    if (lane < 4 && slot >= 0) {
+      const uint32_t dst = sbase + (uint32_t)(s * ge.stage_bytes) + (lane & 1 ? v_off : 0u) +
+                           (lane & 2 ? (uint32_t)ge.half_bytes : 0u);
+      const CUtensorMap* map = lane & 1 ? &maps.v : &maps.k;
+      // (16 tokens are whole lines: their first line's number is exact)
+      if (ge.hsplit == 1) i4::tma_2d(dst, map, (slot >> 4) * (tok_bytes >> 3), full);
+      else i4::tma_4d(dst, map, hgrp, slot, full);
     }
     ++turn;
     return true;
   };
-
   // ---- per-piece state ---------------------------------------------------------
   const float log2e = 1.4426950408889634f;
   const float cap = p.soft_cap;
@@ -523,14 +539,22 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge) {
   };
 
   // ---- stream the segment --------------------------------------------------------
-  // Byte offsets, in a stage, of what this lane reads: its K piece of token
-  // pi(g) (row g + 8: a pitch on), that row's tail, and its V codes of tokens
-  // pi(2c) and pi(2c + 1) (rows 2c + 8, 2c + 9: a pitch on).
-  const uint32_t pitch = (uint32_t)ge.pitch;
-  const uint32_t row_g = tok_g * pitch + j * Row::kRow;
-  const uint32_t k_at = row_g + Row::kKBytes * c, t_at = row_g + Row::kCodes;
-  const uint32_t v_at0 = v_off + i4::pi_of(2 * c) * pitch + j * Row::kRow + Row::kVWords * 4 * g;
-  const uint32_t v_at1 = v_off + i4::pi_of(2 * c + 1) * pitch + j * Row::kRow + Row::kVWords * 4 * g;
+  // Byte offsets, in a half, of what this lane reads: its K pieces of token
+  // pi(g) and the next one (rows g and g + 8), those rows' tails, and its V
+  // codes of tokens pi(2c), pi(2c + 1) and the ones after them.
+  auto at = [&](int tok, int off) -> uint32_t {
+    const uint32_t o = (uint32_t)(tok * tok_bytes + j * Row::kRow + off);
+    return ge.swizzle ? o ^ ((o >> 3) & 0x70u) : o;
+  };
+  uint32_t k_at[2][Row::kK16], t_at[2], v_at[4];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    t_at[h] = at(tok_g + h, Row::kCodes);
+#pragma unroll
+    for (int q = 0; q < Row::kK16; ++q) k_at[h][q] = at(tok_g + h, Row::kKBytes * c + 64 * q);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) v_at[2 * h + r] = v_off + at(i4::pi_of(2 * c + r) + h, Row::kVWords * 4 * g);
+  }
   // multiplier bytes of this lane in a tail's two words: 2c and 2c + 1; at D
   // = 256 its K groups are c and c + 4
   const bool up = c >= 2;
@@ -543,7 +567,7 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge) {
   uint32_t par = 0, kpar = 0;
   for (int i = -ahead;; ++i) {
     if (i + ahead < n) {
-      if (kw == j && !issue(kst, kpar, i < 2)) break;
+      if (kw == j && !issue(kst, kpar, i < 1)) break;
       if (++kw == ge.hg) kw = 0;
       if (++kst == S) {
         kst = 0;
@@ -553,82 +577,52 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge) {
     if (i < 0) continue;
     const uint32_t sb = sbase + (uint32_t)(st * ge.stage_bytes);
     const uint32_t mb = meta + 32u * st;
-    uint4 rec = make_uint4(0u, 0u, 0xFFFFFFFEu, 0u);
+    uint4 rec = make_uint4(0u, 0xFFFFFFFEu, 0u, 0u);
     if (i < n) {
       if (!i4::warp_wait(mb + 16, par, abort)) break;
       rec = dev::lds128(mb);
     }
-    if ((int)rec.z != cur) {
+    if ((int)rec.y != cur) {
       if (cur >= 0) finish_piece(cur);
       if (i == n) return;
-      cur = (int)rec.z;
+      cur = (int)rec.y;
       start_piece(cur);
     }
-    const int tok0 = (int)rec.y;
+    const int tok0 = (int)rec.x;
 
-    // tails: {s, m_0..3, m_4..7} of rows g and g + 8 of K and of V
-    const uint4 tk0 = dev::lds128(sb + t_at), tk1 = dev::lds128(sb + t_at + pitch);
-    const uint4 tv0 = dev::lds128(sb + t_at + v_off), tv1 = dev::lds128(sb + t_at + v_off + pitch);
-    uint4 kc[2][Row::kK16];
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int q = 0; q < Row::kK16; ++q) {
-        if constexpr (Row::kKBytes == 8) {
-          const uint2 w = i4::lds64(sb + k_at + h * pitch);
-          kc[h][q] = make_uint4(w.x, w.y, 0, 0);
-        } else {
-          kc[h][q] = dev::lds128(sb + k_at + h * pitch + 64 * q);
-        }
-      }
-    uint32_t vc[4][Row::kVWords];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const uint32_t a = sb + (r & 1 ? v_at1 : v_at0) + (r >= 2 ? pitch : 0u);
-      if constexpr (Row::kVWords == 1) {
-        vc[r][0] = i4::lds32(a);
-      } else if constexpr (Row::kVWords == 2) {
-        const uint2 w = i4::lds64(a);
-        vc[r][0] = w.x;
-        vc[r][1] = w.y;
-      } else {
-        const uint4 w = dev::lds128(a);
-        vc[r][0] = w.x;
-        vc[r][1] = w.y;
-        vc[r][2] = w.z;
-        vc[r][3] = w.w;
-      }
-    }
-    const float sk0 = __uint_as_float(tk0.x), sk1 = __uint_as_float(tk1.x);
-    float sv0 = __uint_as_float(tv0.x), sv1 = __uint_as_float(tv1.x);
+    const uint32_t live = rec.z;
+    const bool full = live == 0xFFFFFFFFu && tok0 >= all_lo && tok0 + kInt4Chunk <= all_hi;
     const uint32_t bias = 0x64646464u;  // f16 1024 + byte
-    // V's multipliers, transposed to the token pairs its codes form
-    uint32_t vm0 = dev::prmt(up ? tv0.z : tv0.y, bias, pair_sel);
-    uint32_t vm1 = dev::prmt(up ? tv1.z : tv1.y, bias, pair_sel);
-    const uint32_t live = rec.w;
-    if (live != 0xFFFFu) {
-      // Tokens outside the piece's keys (or its whole block): whatever the
-      // cache holds there takes no part.  (K's scores are replaced below.)
-      const bool l0 = (live >> tok_g) & 1u, l1 = (live >> (tok_g + 1)) & 1u;
-      sv0 = l0 ? sv0 : 0.0f;
-      sv1 = l1 ? sv1 : 0.0f;
-      vm0 = l0 ? vm0 : 0x64006400u;
-      vm1 = l1 ? vm1 : 0x64006400u;
-    }
-
-    // S^T = K Q^T : 16 tokens x 8 rows per n-tile; even and odd k-steps in
-    // separate accumulators to halve the dependent MMA chain.
-    float s[NT][4], s2[NT][4];
-    {
+    // S^T = K Q^T: the two halves of the chunk, 16 tokens x 8 rows per n-tile
+    // each; and what the values' part needs of this stage.
+    float s[2][NT][4], zm[2][2], sv[2][2];
+    uint32_t vm[2][2], vc[2][4][Row::kVWords];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const uint32_t ub = sb + (uint32_t)(u * ge.half_bytes);
+      // tails: {s, m_0..3, m_4..7} of rows g and g + 8
+      const uint4 tk[2] = {dev::lds128(ub + t_at[0]), dev::lds128(ub + t_at[1])};
+      uint4 kc[2][Row::kK16];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int q = 0; q < Row::kK16; ++q) {
+          if constexpr (Row::kKBytes == 8) {
+            const uint2 w = i4::lds64(ub + k_at[h][q]);
+            kc[h][q] = make_uint4(w.x, w.y, 0, 0);
+          } else {
+            kc[h][q] = dev::lds128(ub + k_at[h][q]);
+          }
+        }
       dev::Int4Mul km[2][2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint4 tl = h ? tk1 : tk0;
+        zm[u][h] = score_mul * __uint_as_float(tk[h].x);
         if constexpr (D == 256) {
-          km[h][0] = dev::int4_mul(dev::prmt(tl.y, bias, kpair_sel));
-          km[h][1] = dev::int4_mul(dev::prmt(tl.z, bias, kpair_sel));
+          km[h][0] = dev::int4_mul(dev::prmt(tk[h].y, bias, kpair_sel));
+          km[h][1] = dev::int4_mul(dev::prmt(tk[h].z, bias, kpair_sel));
         } else {
-          const uint32_t pr = dev::prmt(up ? tl.z : tl.y, bias, pair_sel);
+          const uint32_t pr = dev::prmt(up ? tk[h].z : tk[h].y, bias, pair_sel);
           km[h][0] = dev::int4_mul(dev::prmt(pr, pr, 0x1010u));
           km[h][1] = dev::int4_mul(dev::prmt(pr, pr, 0x3232u));
         }
@@ -646,16 +640,49 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge) {
           const uint32_t a0[4] = {f[0], f8[0], f[1], f8[1]}, a1[4] = {f[2], f8[2], f[3], f8[3]};
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
-            if (wi == 0) {
-              dev::mma_f16_16816_zero(s[t], a0, qf[t][0][0], qf[t][0][1]);
-              dev::mma_f16_16816_zero(s2[t], a1, qf[t][1][0], qf[t][1][1]);
-            } else {
-              dev::mma_f16_16816(s[t], a0, qf[t][2 * wi][0], qf[t][2 * wi][1]);
-              dev::mma_f16_16816(s2[t], a1, qf[t][2 * wi + 1][0], qf[t][2 * wi + 1][1]);
-            }
+            if (wi == 0) dev::mma_f16_16816_zero(s[u][t], a0, qf[t][0][0], qf[t][0][1]);
+            else dev::mma_f16_16816(s[u][t], a0, qf[t][2 * wi][0], qf[t][2 * wi][1]);
+            dev::mma_f16_16816(s[u][t], a1, qf[t][2 * wi + 1][0], qf[t][2 * wi + 1][1]);
           }
         }
       }
+      // values: codes of tokens pi(2c), pi(2c + 1) and the ones after them;
+      // scales and multipliers of rows g and g + 8
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const uint32_t a = ub + v_at[r];
+        if constexpr (Row::kVWords == 1) {
+          vc[u][r][0] = i4::lds32(a);
+        } else if constexpr (Row::kVWords == 2) {
+          const uint2 w = i4::lds64(a);
+          vc[u][r][0] = w.x;
+          vc[u][r][1] = w.y;
+        } else {
+          const uint4 w = dev::lds128(a);
+          vc[u][r][0] = w.x;
+          vc[u][r][1] = w.y;
+          vc[u][r][2] = w.z;
+          vc[u][r][3] = w.w;
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint4 tv = dev::lds128(ub + v_off + t_at[h]);
+        sv[u][h] = __uint_as_float(tv.x);
+        vm[u][h] = dev::prmt(up ? tv.z : tv.y, bias, pair_sel);
+      }
+    }
+    if (live != 0xFFFFFFFFu) {
+      // Tokens outside the piece's keys (or in no block): whatever the stage
+      // holds there takes no part.  (Their scores are replaced below.)
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const bool in = (live >> (16 * u + tok_g + h)) & 1u;
+          sv[u][h] = in ? sv[u][h] : 0.0f;
+          vm[u][h] = in ? vm[u][h] : 0x64006400u;
+        }
     }
     // every lane has read the stage
     __syncwarp();
@@ -664,44 +691,45 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge) {
     // Weights P = 2^(z - m_off), z the score in log2 units.  A row's reference
     // moves only when a weight would pass 2^14 (f16's range), the value
     // scales' only when one is a binade larger: one vote for both.
-    const bool full = live == 0xFFFFu && tok0 >= all_lo && tok0 + kChunkTokens <= all_hi;
-    const float zm[2] = {score_mul * sk0, score_mul * sk1};
-    auto score = [&](int t, int e) -> float {
-      float v = s[t][e] * zm[e >> 1];
+    auto score = [&](int u, int t, int e) -> float {
+      float v = s[u][t][e] * zm[u][e >> 1];
       if (cap > 0.0f) v = cap_l2 * dev::tanh_exp(v * inv_cap);
-      const int tok = tok0 + tok_g + (e >> 1);
+      const int at = 16 * u + tok_g + (e >> 1), tok = tok0 + at;
       if constexpr (AL)  // bias from the exact integer distance, after the cap
         v = fmaf(al_slope[t][e & 1], (float)(tok - al_pos[t][e & 1]), v);
       if (!full) {  // (rare: the edges of a request's keys) the column's own keys
         const int pn = pos0 + min(row0 + 8 * t + 2 * c + (e & 1), row_end - 1) / G;
-        const bool vis = ((live >> (tok_g + (e >> 1))) & 1u) && tok >= (W > 0 ? pn - W + 1 : 0) &&
-                         tok < (p.causal ? pn + 1 : len);
+        const bool vis = ((live >> at) & 1u) && tok >= (W > 0 ? pn - W + 1 : 0) && tok < (p.causal ? pn + 1 : len);
         v = vis ? v : -INFINITY;
       }
       return v;
     };
-    float x[NT][4], xmax = -INFINITY;
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s[t][e] += s2[t][e];
+    float x[2][NT][4];
     if (!AL && full && !(cap > 0.0f)) {
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[t][e] = fmaf(s[t][e], zm[e >> 1], -m_off[t][e & 1]);
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[u][t][e] = fmaf(s[u][t][e], zm[u][e >> 1], -m_off[t][e & 1]);
     } else {
 #pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[u][t][e] = score(u, t, e) - m_off[t][e & 1];
+    }
+    float xmax = x[0][0][0];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[t][e] = score(t, e) - m_off[t][e & 1];
-    }
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) xmax = fmaxf(xmax, x[t][e]);
-    if (__any_sync(0xffffffffu, xmax > 14.0f || fmaxf(sv0, sv1) >= sv_lim)) {
-      float mx = fmaxf(sv0, sv1);
+        for (int e = 0; e < 4; ++e) xmax = fmaxf(xmax, x[u][t][e]);
+    const float sv_max = fmaxf(fmaxf(sv[0][0], sv[0][1]), fmaxf(sv[1][0], sv[1][1]));
+    if (__any_sync(0xffffffffu, xmax > 14.0f || sv_max >= sv_lim)) {
+      float mx = sv_max;
 #pragma unroll
       for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
       float alpha_v = 1.0f;
@@ -719,8 +747,10 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge) {
         float alpha[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float z0 = score(t, e), z1 = score(t, e + 2);
-          float cm = fmaxf(z0, z1);
+          float z[4];
+#pragma unroll
+          for (int i2 = 0; i2 < 4; ++i2) z[i2] = score(i2 >> 1, t, e + 2 * (i2 & 1));
+          float cm = fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3]));
 #pragma unroll
           for (int off = 4; off < 32; off <<= 1) cm = fmaxf(cm, __shfl_xor_sync(0xffffffffu, cm, off));
           // (only a row that passed its limit moves: to the chunk's maximum,
@@ -729,8 +759,8 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge) {
           alpha[e] = dev::fast_exp2(m_off[t][e] - mn);
           m_off[t][e] = mn;
           l_run[t][e] *= alpha[e];
-          x[t][e] = z0 - mn;
-          x[t][e + 2] = z1 - mn;
+#pragma unroll
+          for (int i2 = 0; i2 < 4; ++i2) x[i2 >> 1][t][e + 2 * (i2 & 1)] = z[i2] - mn;
         }
 #pragma unroll
         for (int i2 = 0; i2 < Row::kMtiles; ++i2) {
@@ -741,38 +771,41 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge) {
         }
       }
     }
-    sv0 *= to_ref;
-    sv1 *= to_ref;
-    uint32_t pb0[NT], pb1[NT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const float p0 = dev::fast_exp2(x[t][0]), p1 = dev::fast_exp2(x[t][1]);
-      const float p2 = dev::fast_exp2(x[t][2]), p3 = dev::fast_exp2(x[t][3]);
-      l_run[t][0] += p0 + p2;
-      l_run[t][1] += p1 + p3;
-      // P^T (tokens x rows) -> B operand of O^T = V^T P^T via transposes.
-      pb0[t] = dev::movmatrix_trans(dev::pack_f16x2(p0 * sv0, p1 * sv0));
-      pb1[t] = dev::movmatrix_trans(dev::pack_f16x2(p2 * sv1, p3 * sv1));
-    }
 
     // O^T += V^T P^T : head_dim x 8 rows per n-tile.  The low halves of word
     // w of a row hold the even dims of its 8, the high halves the odd ones:
     // nibble q of each pairs two tokens' codes of dim 8 w + 2 q (+ 1), the
     // two rows of m-tile 4 w + q.
-    const dev::Int4Mul vf0 = dev::int4_mul(dev::movmatrix_trans(vm0));
-    const dev::Int4Mul vf1 = dev::int4_mul(dev::movmatrix_trans(vm1));
 #pragma unroll
-    for (int w = 0; w < Row::kVWords; ++w) {
-      uint32_t e01[4], o01[4], e23[4], o23[4];
-      dev::int4_to_f16x2x4(dev::prmt(vc[0][w], vc[1][w], 0x5410u), vf0, e01);
-      dev::int4_to_f16x2x4(dev::prmt(vc[0][w], vc[1][w], 0x7632u), vf0, o01);
-      dev::int4_to_f16x2x4(dev::prmt(vc[2][w], vc[3][w], 0x5410u), vf1, e23);
-      dev::int4_to_f16x2x4(dev::prmt(vc[2][w], vc[3][w], 0x7632u), vf1, o23);
+    for (int u = 0; u < 2; ++u) {
+      const float f0 = sv[u][0] * to_ref, f1 = sv[u][1] * to_ref;
+      uint32_t pb0[NT], pb1[NT];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const uint32_t a[4] = {e01[q], o01[q], e23[q], o23[q]};
+      for (int t = 0; t < NT; ++t) {
+        const float p0 = dev::fast_exp2(x[u][t][0]), p1 = dev::fast_exp2(x[u][t][1]);
+        const float p2 = dev::fast_exp2(x[u][t][2]), p3 = dev::fast_exp2(x[u][t][3]);
+        l_run[t][0] += p0 + p2;
+        l_run[t][1] += p1 + p3;
+        // P^T (tokens x rows) -> B operand of O^T = V^T P^T via transposes.
+        pb0[t] = dev::movmatrix_trans(dev::pack_f16x2(p0 * f0, p1 * f0));
+        pb1[t] = dev::movmatrix_trans(dev::pack_f16x2(p2 * f1, p3 * f1));
+      }
+      // V's multipliers, transposed to the token pairs its codes form
+      const dev::Int4Mul vf0 = dev::int4_mul(dev::movmatrix_trans(vm[u][0]));
+      const dev::Int4Mul vf1 = dev::int4_mul(dev::movmatrix_trans(vm[u][1]));
 #pragma unroll
-        for (int t = 0; t < NT; ++t) dev::mma_f16_16816(o[t][4 * w + q], a, pb0[t], pb1[t]);
+      for (int w = 0; w < Row::kVWords; ++w) {
+        uint32_t e01[4], o01[4], e23[4], o23[4];
+        dev::int4_to_f16x2x4(dev::prmt(vc[u][0][w], vc[u][1][w], 0x5410u), vf0, e01);
+        dev::int4_to_f16x2x4(dev::prmt(vc[u][0][w], vc[u][1][w], 0x7632u), vf0, o01);
+        dev::int4_to_f16x2x4(dev::prmt(vc[u][2][w], vc[u][3][w], 0x5410u), vf1, e23);
+        dev::int4_to_f16x2x4(dev::prmt(vc[u][2][w], vc[u][3][w], 0x7632u), vf1, o23);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t a[4] = {e01[q], o01[q], e23[q], o23[q]};
+#pragma unroll
+          for (int t = 0; t < NT; ++t) dev::mma_f16_16816(o[t][4 * w + q], a, pb0[t], pb1[t]);
+        }
       }
     }
 
@@ -820,7 +853,7 @@ inline bool int4_raise_smem(const void* kern, std::atomic<bool>* raised) {
 }
 
 template <int D, int NT, bool AL>
-int launch_int4_decode(const AttnParams& p, cudaStream_t stream) {
+int launch_int4_decode(const AttnParams& p, const PrefillMaps& maps, cudaStream_t stream) {
   Int4Geom ge = int4_geom(p.heads_kv, D, NT);
   ge.segments = p.num_warps / p.heads_kv;
   auto kern = int4_decode_kernel<D, NT, AL, false>;
@@ -828,7 +861,7 @@ int launch_int4_decode(const AttnParams& p, cudaStream_t stream) {
   if (!int4_raise_smem(reinterpret_cast<const void*>(kern), raised)) return KVQ_E_CUDA;
   const int ctas = (ge.segments * ge.hsplit + ge.gpc - 1) / ge.gpc;
   StepParams none{};
-  kern<<<(unsigned)ctas, 32 * ge.hg * ge.gpc, ge.smem, stream>>>(p, none, ge);
+  kern<<<(unsigned)ctas, 32 * ge.hg * ge.gpc, ge.smem, stream>>>(p, none, ge, maps);
   return cudaGetLastError() == cudaSuccess ? KVQ_OK : KVQ_E_CUDA;
 }
 
@@ -836,7 +869,8 @@ int launch_int4_decode(const AttnParams& p, cudaStream_t stream) {
 // as fit on the device; *warps counts segments times kv heads (0 asks for
 // that number instead).
 template <int D, int NT, bool AL>
-int launch_int4_step(const AttnParams& p, const StepParams& sp, int64_t* warps, cudaStream_t stream) {
+int launch_int4_step(const AttnParams& p, const StepParams& sp, const PrefillMaps& maps, int64_t* warps,
+                     cudaStream_t stream) {
   Int4Geom ge = int4_geom(p.heads_kv, D, NT);
   auto kern = int4_decode_kernel<D, NT, AL, true>;
   int dev = 0, sms = 0, per_sm = 0;
@@ -873,7 +907,8 @@ int launch_int4_step(const AttnParams& p, const StepParams& sp, int64_t* warps, 
   if (*warps != want) return KVQ_E_INVALID_ARG;
   AttnParams pp = p;
   StepParams ss = sp;
-  void* args[] = {&pp, &ss, &ge};
+  PrefillMaps mm = maps;
+  void* args[] = {&pp, &ss, &ge, &mm};
   if (cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(kern), dim3((unsigned)ctas), dim3(threads),
                                   args, ge.smem, stream) != cudaSuccess) {
     cudaGetLastError();
@@ -883,13 +918,15 @@ int launch_int4_step(const AttnParams& p, const StepParams& sp, int64_t* warps, 
 }
 
 template <int D, bool AL>
-int launch_int4_decode_d(const AttnParams& p, int ntiles, cudaStream_t stream) {
-  return ntiles == 1 ? launch_int4_decode<D, 1, AL>(p, stream) : launch_int4_decode<D, 2, AL>(p, stream);
+int launch_int4_decode_d(const AttnParams& p, const PrefillMaps& maps, int ntiles, cudaStream_t stream) {
+  return ntiles == 1 ? launch_int4_decode<D, 1, AL>(p, maps, stream)
+                     : launch_int4_decode<D, 2, AL>(p, maps, stream);
 }
 template <int D, bool AL>
-int launch_int4_step_d(const AttnParams& p, const StepParams& sp, int64_t* warps, cudaStream_t stream) {
-  return sp.max_rows <= 8 ? launch_int4_step<D, 1, AL>(p, sp, warps, stream)
-                          : launch_int4_step<D, 2, AL>(p, sp, warps, stream);
+int launch_int4_step_d(const AttnParams& p, const StepParams& sp, const PrefillMaps& maps, int64_t* warps,
+                       cudaStream_t stream) {
+  return sp.max_rows <= 8 ? launch_int4_step<D, 1, AL>(p, sp, maps, warps, stream)
+                          : launch_int4_step<D, 2, AL>(p, sp, maps, warps, stream);
 }
 
 }  // namespace kvq

@@ -4,14 +4,16 @@
 #include "kvq_decode_int4.cuh"
 
 namespace kvq {
-int launch_int4_decode_d256_alibi(const AttnParams& p, int ntiles, void* stream);
-int launch_int4_step_d256_alibi(const AttnParams& p, const StepParams& sp, int64_t* warps, void* stream);
-int launch_int4_decode_d256(const AttnParams& p, bool alibi, int ntiles, void* stream) {
-  return alibi ? launch_int4_decode_d256_alibi(p, ntiles, stream)
-               : launch_int4_decode_d<256, false>(p, ntiles, static_cast<cudaStream_t>(stream));
+int launch_int4_decode_d256_alibi(const AttnParams& p, const PrefillMaps& maps, int ntiles, void* stream);
+int launch_int4_step_d256_alibi(const AttnParams& p, const StepParams& sp, const PrefillMaps& maps, int64_t* warps,
+                            void* stream);
+int launch_int4_decode_d256(const AttnParams& p, const PrefillMaps& maps, bool alibi, int ntiles, void* stream) {
+  return alibi ? launch_int4_decode_d256_alibi(p, maps, ntiles, stream)
+               : launch_int4_decode_d<256, false>(p, maps, ntiles, static_cast<cudaStream_t>(stream));
 }
-int launch_int4_step_d256(const AttnParams& p, const StepParams& sp, bool alibi, int64_t* warps, void* stream) {
-  return alibi ? launch_int4_step_d256_alibi(p, sp, warps, stream)
-               : launch_int4_step_d<256, false>(p, sp, warps, static_cast<cudaStream_t>(stream));
+int launch_int4_step_d256(const AttnParams& p, const StepParams& sp, const PrefillMaps& maps, bool alibi, int64_t* warps,
+                            void* stream) {
+  return alibi ? launch_int4_step_d256_alibi(p, sp, maps, warps, stream)
+               : launch_int4_step_d<256, false>(p, sp, maps, warps, static_cast<cudaStream_t>(stream));
 }
 }  // namespace kvq

@@ -204,6 +204,38 @@ bool encode_auto_map(CUtensorMap* map, const void* cache, int head_dim, int head
              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Maps of a 4-bit cache's K and V for the decode's bulk tensor copies (see
+// PrefillMaps): half a chunk -- 16 tokens' rows of a group of kv heads -- a
+// copy.
+bool encode_int4_maps(kvq::PrefillMaps* maps, const void* k, const void* v, int head_dim, int heads_kv,
+                      int64_t slots, const kvq::Int4Geom& ge) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint64_t row = (cuuint64_t)kvq::row_bytes(KVQ_INT4_PER_TOKEN_HEAD, head_dim);
+  const cuuint64_t token = row * (cuuint64_t)heads_kv, part = row * (cuuint64_t)ge.hg;
+  const bool all = ge.hsplit == 1;
+  const cuuint64_t unit = ge.swizzle ? 128 : 16;
+  const cuuint64_t dims[4] = {unit, all ? (cuuint64_t)slots * token / 128 : part / unit,
+                              (cuuint64_t)ge.hsplit, (cuuint64_t)slots};
+  const cuuint64_t strides[3] = {unit, part, token};
+  const cuuint32_t box[4] = {(cuuint32_t)unit,
+                             (cuuint32_t)(all ? kvq::kChunkTokens * token / 128 : part / unit), 1u,
+                             (cuuint32_t)kvq::kChunkTokens};
+  const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+  for (int i = 0; i < 2; ++i)
+    if (enc(i ? &maps->v : &maps->k, CU_TENSOR_MAP_DATA_TYPE_UINT8, all ? 2 : 4, const_cast<void*>(i ? v : k),
+            dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            ge.swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return false;
+  return true;
+}
+
+int64_t int4_lines(int64_t num_blocks, int block_size, int heads_kv, int head_dim) {
+  return num_blocks * (int64_t)block_size / 16 * heads_kv *
+         (kvq::row_bytes(KVQ_INT4_PER_TOKEN_HEAD, head_dim) / 8);
+}
+
 int sm_count() {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
@@ -475,6 +507,8 @@ int kvq_get_scheduler_metadata(int num_req, int heads_q, int heads_kv, int head_
     tiles[0].reserve(n_tiles[0]);
     tiles[1].reserve(n_tiles[1]);
   }
+  // tokens of a plan's chunk
+  const int chunk = kvq::is_int4(dtype) ? kvq::kInt4Chunk : kvq::kChunkTokens;
   // A request's row tiles: their key ranges do not depend on the kv head, so
   // each is worked out once and copied for every head (heads outermost).
   std::vector<PrefillTile> row_prefill;
@@ -522,9 +556,9 @@ int kvq_get_scheduler_metadata(int num_req, int heads_q, int heads_kv, int head_
       t.nrows = (int)nrows;
       t.any_hi = s->causal ? p_max + 1 : L;
       t.any_lo = s->window > 0 ? std::max<int64_t>(0, p_min - s->window + 1) : 0;
-      t.c_lo = t.any_lo / kvq::kChunkTokens;
-      t.c_hi = ceil_div(t.any_hi, kvq::kChunkTokens);
-      s->max_chunk = std::max<int32_t>(s->max_chunk, (int32_t)(t.c_hi - 1));
+      t.c_lo = t.any_lo / chunk;
+      t.c_hi = ceil_div(t.any_hi, chunk);
+      s->max_chunk = std::max<int32_t>(s->max_chunk, (int32_t)((t.any_hi - 1) / kvq::kChunkTokens));
       row_tiles.push_back(t);
     }
     for (int h = 0; h < heads_kv; ++h)
@@ -616,7 +650,7 @@ int kvq_get_scheduler_metadata(int num_req, int heads_q, int heads_kv, int head_
       // segments: as many as there are resident groups for, none shorter
       // than kInt4MinChunks; every segment has a warp per kv head
       const kvq::Int4Geom ge = kvq::int4_geom(heads_kv, head_dim, cls + 1);
-      const int64_t groups = (int64_t)sms * kvq::int4_min_ctas(head_dim, cls + 1) * ge.gpc;
+      const int64_t groups = (int64_t)sms * ge.gpc;
       const int64_t chunks = T / heads_kv;
       int64_t segs = std::min<int64_t>(std::max<int64_t>(1, groups / ge.hsplit),
                                        ceil_div(chunks, kvq::kInt4MinChunks));
@@ -934,8 +968,11 @@ int kvq_attention_with_kv_cache(const kvq_sched_t* s, int heads_q, int heads_kv,
     return KVQ_E_INVALID_ARG;
   if (block_size <= 0 || block_size % kvq::kChunkTokens) return KVQ_E_UNSUPPORTED;
   if (num_blocks <= 0 || block_table_stride <= 0) return KVQ_E_INVALID_ARG;
-  // Cache slots are addressed with 32-bit indices.
+  // Cache slots are addressed with 32-bit indices, and so are the 128-byte
+  // lines of a 4-bit cache.
   if (num_blocks * (int64_t)block_size >= ((int64_t)1 << 31)) return KVQ_E_UNSUPPORTED;
+  if (kvq::is_int4(dtype) && int4_lines(num_blocks, block_size, heads_kv, head_dim) >= ((int64_t)1 << 31))
+    return KVQ_E_UNSUPPORTED;
   // The table must hold every logical block the schedule reads.
   const int64_t last_block = ((int64_t)s->max_chunk * kvq::kChunkTokens) / block_size;
   if (last_block >= block_table_stride) return KVQ_E_INVALID_ARG;
@@ -1022,7 +1059,11 @@ int kvq_attention_with_kv_cache(const kvq_sched_t* s, int heads_q, int heads_kv,
     p.warp_seg = reinterpret_cast<const WarpSeg*>(b + s->d_warps_off) + dl.warp_off;
     p.num_chunks = dl.num_chunks;
     p.num_warps = dl.num_warps;
-    const int rc = kvq::launch_decode(p, s->dtype, head_dim, cls + 1, stream);
+    if (kvq::is_int4(s->dtype) &&
+        !encode_int4_maps(&maps, key_cache, value_cache, head_dim, heads_kv, num_blocks * (int64_t)block_size,
+                          kvq::int4_geom(heads_kv, head_dim, cls + 1)))
+      return KVQ_E_CUDA;
+    const int rc = kvq::launch_decode(p, maps, s->dtype, head_dim, cls + 1, stream);
     if (rc != KVQ_OK) return rc;
   }
   return kvq::launch_merge(p, head_dim, s->num_merges, stream);
@@ -1082,6 +1123,8 @@ int decode_step_impl(int num_req, int heads_q, int heads_kv, int head_dim, kvq_d
   if (num_new_tokens < 0 || num_blocks <= 0 || block_table_stride <= 0) return KVQ_E_INVALID_ARG;
   if (block_size <= 0 || block_size % kvq::kChunkTokens) return KVQ_E_UNSUPPORTED;
   if (num_blocks * (int64_t)block_size >= ((int64_t)1 << 31)) return KVQ_E_UNSUPPORTED;
+  if (kvq::is_int4(dtype) && int4_lines(num_blocks, block_size, heads_kv, head_dim) >= ((int64_t)1 << 31))
+    return KVQ_E_UNSUPPORTED;
   if (!key_cache || !value_cache || !q || !out || !query_start_loc || !seq_lens || !block_table ||
       !workspace)
     return KVQ_E_INVALID_ARG;
@@ -1176,7 +1219,13 @@ int decode_step_impl(int num_req, int heads_q, int heads_kv, int head_dim, kvq_d
   }
   // the fused kernel, then the merge of its cut tiles as a programmatic
   // dependent launch
-  rc = kvq::launch_decode_step(p, sp, dtype, head_dim, warps, stream);
+  kvq::PrefillMaps maps;
+  std::memset(&maps, 0, sizeof(maps));
+  if (kvq::is_int4(dtype) &&
+      !encode_int4_maps(&maps, key_cache, value_cache, head_dim, heads_kv, num_blocks * (int64_t)block_size,
+                        kvq::int4_geom(heads_kv, head_dim, max_rows <= 8 ? 1 : 2)))
+    return KVQ_E_CUDA;
+  rc = kvq::launch_decode_step(p, sp, maps, dtype, head_dim, warps, stream);
   if (rc != KVQ_OK) return rc;
   return kvq::launch_merge_step(p, sp, dtype, head_dim, warps, stream);
 }

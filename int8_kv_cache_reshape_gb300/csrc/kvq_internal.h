@@ -89,8 +89,9 @@ constexpr int kMinChunksPerWarp = 8;  // smallest segment worth a warp
 // Bytes of one 16-token chunk of K and V codes (plus the per-token-head
 // scale tails) -- what a warp loads per step, straight into registers.
 KVQ_HD constexpr int decode_chunk_bytes(int dtype, int head_dim) {
-  return 2 * kChunkTokens * code_bytes(dtype, head_dim) +
-         (is_per_token_head(dtype) ? 32 * 16 : 0);
+  return is_int4(dtype) ? 2 * 32 * row_bytes(dtype, head_dim)
+                        : 2 * kChunkTokens * code_bytes(dtype, head_dim) +
+                              (is_per_token_head(dtype) ? 32 * 16 : 0);
 }
 // Resident CTAs per SM the kernel is compiled for (register budget): a
 // bf16 ("auto") chunk is twice the bytes of a code chunk, so its register
@@ -108,71 +109,58 @@ KVQ_HD constexpr size_t decode_smem_bytes(int dtype, int head_dim) {
 }
 
 // ---- split-KV decode over 4-bit rows ---------------------------------------
-// A CTA has `gpc` groups of `hg` warps, one warp per kv head of a group; a
-// group streams one segment of the chunk sequence (the same for all heads:
-// head lockstep) through a ring of `stages` chunks in shared memory, K rows
-// then V rows of 16 tokens at `pitch` bytes a token.
-//
-// Warps per CTA and CTAs per SM, by registers (o, Q fragments and one
-// chunk's codes): 16 warps of 128 registers at head_dim 128 and up to 8 rows
-// a tile, 24 of 80 at head_dim 64, 12 of 168 and 8 of 255 above.
+// A CTA (one per SM) has `gpc` groups of `hg` warps, one warp per kv head of a
+// group; a group streams one segment of the chunk sequence (the same for all
+// heads: head lockstep) through a ring of `stages` chunks of 32 tokens in
+// shared memory: K rows of the two 16-token halves, then V rows, each half
+// `half_bytes` apart and holding the group's rows token by token.
+constexpr int kInt4Chunk = 32;  // tokens of a chunk of the 4-bit plan
+// Warps per CTA, by registers (o, Q fragments and one chunk's codes): 16 of
+// 128 up to head_dim 128 and 8 rows a tile, 12 of 168 and 8 of 255 above.
 KVQ_HD constexpr int int4_max_warps(int head_dim, int ntiles) {
-  return (head_dim == 128 && ntiles == 2) || (head_dim == 256 && ntiles == 1) ? 12 : 8;
+  return head_dim == 64 || (head_dim == 128 && ntiles == 1) ? 16
+         : head_dim == 128 || ntiles == 1                  ? 12
+                                                           : 8;
 }
-KVQ_HD constexpr int int4_min_ctas(int head_dim, int ntiles) {
-  return head_dim == 64 ? (ntiles == 1 ? 3 : 2) : head_dim == 128 && ntiles == 1 ? 2 : 1;
-}
-// Dynamic shared memory of a CTA: its share of the SM's 228 KB.
-constexpr size_t kInt4MaxSmem = 224 * 1024;
-KVQ_HD constexpr size_t int4_smem_budget(int head_dim, int ntiles) {
-  return int4_min_ctas(head_dim, ntiles) == 3   ? 73 * 1024
-         : int4_min_ctas(head_dim, ntiles) == 2 ? 110 * 1024
-                                                : kInt4MaxSmem;
-}
-constexpr int kInt4RecBytes = 32 * 16;  // a warp's chunk records
+constexpr size_t kInt4MaxSmem = 217 * 1024;  // dynamic shared memory of a CTA
+constexpr int kInt4Turns = 16;               // copies a warp prepares at a time
 struct Int4Geom {
   int hg, gpc;      // heads (warps) per group, groups per CTA
   int hsplit;       // head groups: heads_kv / hg
-  int pitch;        // bytes between tokens in a stage
-  int stage_bytes, stages;
-  int whole;        // 1: a chunk's rows are one packed copy (pitch = a token's bytes)
+  int swizzle;      // 1: 16-byte units of a 128-byte line are XORed with its number mod 8
+  int half_bytes, stage_bytes, stages;
   int segments;     // cuts of the chunk sequence the launch has groups for
   size_t smem;
 };
-// Heads per group: of the divisors of heads_kv that fit the CTA's warps, are
-// at least 4 (or all heads) and so copy long runs of a token's bytes, the one
-// that fills most warps, the larger of equals; failing that the largest.
+// All heads in one group where the CTA has the warps and room for two stages
+// (a 16-token half is then one run of whole 128-byte lines); else the largest
+// divisor of heads_kv that fits and makes whole lines of a token's rows; else
+// the largest that fits.
 KVQ_HD constexpr Int4Geom int4_geom(int heads_kv, int head_dim, int ntiles) {
   Int4Geom ge{};
   const int maxw = int4_max_warps(head_dim, ntiles);
-  int best = 0;
-  for (int h = 1; h <= maxw && h <= heads_kv; ++h) {
-    if (heads_kv % h) continue;
-    const bool wide = h >= 4 || h == heads_kv;
-    const int warps = maxw / h * h;
-    if (!wide) ge.hg = h;              // (fallback, growing)
-    else if (warps >= best) {
-      best = warps;
-      ge.hg = h;
-    }
-  }
-  ge.gpc = maxw / ge.hg;
-  ge.hsplit = heads_kv / ge.hg;
   const int row = row_bytes(KVQ_INT4_PER_TOKEN_HEAD, head_dim);
-  const int bytes = ge.hg * row;
-  // long runs at 16 bytes past a multiple of 128 (no bank conflicts); short
-  // ones packed, one copy for all 16 tokens
-  ge.whole = ge.hg == heads_kv && bytes < 256;
-  ge.pitch = ge.whole ? bytes : bytes + (16 + 128 - bytes % 128) % 128;
-  ge.stage_bytes = 2 * kChunkTokens * ge.pitch;
-  const int per_stage = ge.gpc * (ge.stage_bytes + 32), recs = ge.gpc * ge.hg * kInt4RecBytes;
-  const int fit = ((int)int4_smem_budget(head_dim, ntiles) - recs) / per_stage;
+  const size_t room = kInt4MaxSmem - 1024;  // (1 KB to align the stages)
+  for (int h = 1; h <= maxw && h <= heads_kv; ++h) {
+    const int half = (kChunkTokens * h * row + 1023) / 1024 * 1024;
+    const int lines = h == heads_kv || h * row % 128 == 0;
+    if (heads_kv % h || lines < ge.swizzle || 2 * (size_t)(4 * half + 32) > room) continue;
+    ge.hg = h;
+    ge.swizzle = lines;
+    ge.half_bytes = half;
+  }
+  ge.hsplit = heads_kv / ge.hg;
+  ge.stage_bytes = 4 * ge.half_bytes;
+  // as many groups as there are warps for, with two stages at least
+  ge.gpc = maxw / ge.hg;
+  while (ge.gpc > 1 && 2 * (size_t)ge.gpc * (ge.stage_bytes + 32) > room) --ge.gpc;
+  const int fit = (int)(room / ((size_t)ge.gpc * (ge.stage_bytes + 32)));
   ge.stages = fit < 8 ? fit : 8;
-  ge.smem = (size_t)ge.stages * per_stage + recs;
+  ge.smem = (size_t)ge.stages * ge.gpc * (ge.stage_bytes + 32) + 1024;
   return ge;
 }
 // Smallest segment worth a group.
-constexpr int kInt4MinChunks = 4;
+constexpr int kInt4MinChunks = 2;
 // Segments the fused step cuts a sequence of `chunks` into.
 KVQ_HD constexpr int int4_step_segments(int64_t chunks, int segments) {
   const int64_t most = (chunks + kInt4MinChunks - 1) / kInt4MinChunks;
@@ -229,9 +217,12 @@ KVQ_HD constexpr size_t prefill_smem_bytes(int head_dim, int cta_group = 1) {
          (size_t)kPrefillRows * (head_dim * 2 + 16) + 512 + 1024;
 }
 
-// Tensor maps of bf16 ("auto") caches for the prefill's bulk tensor copies:
-// a cache is a rank-3 bf16 tensor {head_dim, kv heads, slots} copied in
-// boxes of {64, 1, 16 slots} in the 128-byte swizzle.
+// Tensor maps of the caches for bulk tensor copies.  bf16 ("auto") rows, the
+// prefill: a rank-3 bf16 tensor {head_dim, kv heads, slots} copied in boxes
+// of {64, 1, 16 slots} in the 128-byte swizzle.  4-bit rows, the decode: a
+// half chunk of a group of kv heads as 128-byte lines in that swizzle (all
+// heads: rank 2 {128, lines}; some: rank 4 {128, lines, groups, slots}), or
+// as 16-byte units without it (rank 4 {16, units, groups, slots}).
 struct PrefillMaps {
   CUtensorMap k, v;
 };
@@ -405,11 +396,14 @@ int launch_block_tables(int num_req, const int32_t* query_start_loc, const int32
                         int32_t* block_table, int block_table_stride, int64_t* slot_mapping,
                         int64_t num_tokens, int block_size, int64_t num_blocks,
                         int32_t* free_count_out, int32_t* status, void* stream);
-int launch_decode(const AttnParams& p, int dtype, int head_dim, int ntiles, void* stream);
+// (maps: the caches of 4-bit rows, encoded for int4_geom(heads_kv, head_dim,
+// ntiles); unused otherwise)
+int launch_decode(const AttnParams& p, const PrefillMaps& maps, int dtype, int head_dim, int ntiles,
+                  void* stream);
 // The fused step's kernel (cooperative launch of `warps` / 4 CTAs); `warps`
 // from step_warps().
-int launch_decode_step(const AttnParams& p, const StepParams& sp, int dtype, int head_dim,
-                       int64_t warps, void* stream);
+int launch_decode_step(const AttnParams& p, const StepParams& sp, const PrefillMaps& maps, int dtype,
+                       int head_dim, int64_t warps, void* stream);
 // Decode warps of the fused step's grid on the current device (every CTA
 // resident at once) in *warps; KVQ_OK or a KVQ_E_* status.
 int step_warps(int dtype, int heads_kv, int head_dim, bool alibi, int max_rows, int64_t* warps);

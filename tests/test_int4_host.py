@@ -26,7 +26,7 @@ def test_name_and_row_bytes():
 def test_plan_sizes_follow_the_row():
     sl, ql = np.array([300], np.int32), np.array([0, 1], np.int32)
     info = kvq.get_scheduler_metadata(1, 32, 8, 128, sl, ql, True, 0, "int4_per_token_head").info()
-    assert info["row_bytes"] == 80 and info["decode_chunk_bytes"] == 2 * 16 * 80
+    assert info["row_bytes"] == 80 and info["decode_chunk_bytes"] == 2 * 32 * 80
 
 
 def _bits(x):
