@@ -114,32 +114,31 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
 }  // namespace i4
 
 // The fused step's plan: one tile per request (its kv heads share the chunk
-// ranges), by the kernel's first CTA.  A request with more rows than the
-// launch was built for (or more queries than keys) is left out and flags the
-// error word.
-__device__ __forceinline__ void plan_step_int4(const AttnParams& p, const StepParams& sp, int segments) {
+// ranges), {first chunk, first key, end, rows}, and the prefix sum of their
+// chunk counts.  A request with more rows than the launch was built for (or
+// more queries than keys) is left out and flags the error word (if `flag`).
+__device__ __forceinline__ void plan_step_int4(const AttnParams& p, const StepParams& sp, int32_t* prefix,
+                                               int4* tiles, bool flag) {
   __shared__ int32_t warp_sums[32];
-  __shared__ int32_t total;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nthr = blockDim.x;
   const int nt = sp.num_req;
   const int per = (nt + nthr - 1) / nthr;
   const int t0 = min(nt, tid * per), t1 = min(nt, t0 + per);
-  auto chunks_of = [&](int r, bool store) {
+  int local = 0;
+  for (int r = t0; r < t1; ++r) {
     const int Q = sp.in_query_start_loc[r + 1] - sp.in_query_start_loc[r];
     const int L = sp.in_seq_lens[r];
+    int4 ti = make_int4(0, 0, 0, 0);
     if (Q <= 0 || L < Q || Q > sp.max_rows / p.group) {
-      if (store) {
-        if (Q != 0) atomicExch(p.error_flag, 2);  // (1 is a timeout)
-        sp.tiles[r] = make_int4(0, 0, 0, 0);
-      }
-      return 0;
+      if (flag && Q != 0) atomicExch(p.error_flag, 2);  // (1 is a timeout)
+    } else {
+      const int lo = p.window > 0 ? max(0, L - Q - p.window + 1) : 0;
+      ti = make_int4(lo / kInt4Chunk, lo, L, Q * p.group);
     }
-    const int lo = p.window > 0 ? max(0, L - Q - p.window + 1) : 0;
-    if (store) sp.tiles[r] = make_int4(lo / kInt4Chunk, lo, L, Q * p.group);
-    return (L - 1) / kInt4Chunk + 1 - lo / kInt4Chunk;
-  };
-  int local = 0;
-  for (int t = t0; t < t1; ++t) local += chunks_of(t, true);
+    tiles[r] = ti;
+    local += ti.z > 0 ? (ti.z - 1) / kInt4Chunk + 1 - ti.x : 0;
+    prefix[r] = local;  // (within this thread's requests, for now)
+  }
   int incl = local;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
@@ -150,28 +149,14 @@ __device__ __forceinline__ void plan_step_int4(const AttnParams& p, const StepPa
   __syncthreads();
   int run = incl - local;
   for (int w = 0; w < warp; ++w) run += warp_sums[w];
-  const int run0 = run;
-  for (int t = t0; t < t1; ++t) {
-    sp.prefix[t] = run;
-    run += chunks_of(t, false);
+  int before = run;
+  for (int r = t0; r < t1; ++r) {
+    const int end = run + prefix[r];
+    prefix[r] = before;
+    before = end;
   }
-  if (tid == nthr - 1) {
-    sp.prefix[nt] = run;
-    total = run;
-  }
+  if (tid == nthr - 1) prefix[nt] = run + local;
   __syncthreads();
-  // Each segment's first tile: segment v starts at floor(v T / S), which lies
-  // in tile t for v in [ceil(f0 S / T), ceil(f1 S / T)).
-  const int64_t T = total, S = int4_step_segments(T, segments);
-  if (T > 0) {
-    int64_t f0 = run0;
-    for (int t = t0; t < t1; ++t) {
-      const int64_t f1 = f0 + chunks_of(t, false);
-      for (int64_t v = (f0 * S + T - 1) / T; v < (f1 * S + T - 1) / T && v < S; ++v)
-        sp.warp_tile[v] = t;
-      f0 = f1;
-    }
-  }
 }
 
 template <int D, int NT, bool AL, bool DEV>
@@ -217,15 +202,30 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge,
         sp.value_cache, sp.num_slots, sp.slot_mapping, p.k_scale, p.v_scale, blockDim.x, threadIdx.x,
         blockIdx.x, gridDim.x);
     stage_finish(sp, st);
-    if (blockIdx.x == 0) plan_step_int4(p, sp, ge.segments);
     // (the bulk copies below read rows that other CTAs stored: both sides
     // order their proxies)
     asm volatile("fence.proxy.async.global;" ::: "memory");
-    if (!grid_barrier(sp.barrier, p.error_flag)) return;
-    asm volatile("fence.proxy.async.global;" ::: "memory");
-  } else {
-    __syncthreads();
   }
+  // The fused step's plan: of up to kInt4PlanReq requests by every CTA for
+  // itself, so that all that leads to the first copies lies before the
+  // grid barrier (unless the inputs are still on their way from the host);
+  // else by the first CTA, for all of them.  The merge reads the first CTA's.
+  __shared__ int32_t prefix_s[DEV ? kInt4PlanReq + 1 : 1];
+  __shared__ int4 tiles_s[DEV ? kInt4PlanReq : 1];
+  const bool own_plan = DEV && sp.num_req <= kInt4PlanReq && sp.stage_bytes == 0;
+  const volatile int32_t* prefix = own_plan ? prefix_s : sp.prefix;
+  const volatile int4* tiles = own_plan ? tiles_s : sp.tiles;
+  auto join_grid = [&]() -> bool {
+    const bool ok = grid_barrier(sp.barrier, p.error_flag);
+    asm volatile("fence.proxy.async.global;" ::: "memory");
+    return ok;
+  };
+  if constexpr (DEV) {
+    if (blockIdx.x == 0) plan_step_int4(p, sp, sp.prefix, sp.tiles, true);
+    if (own_plan) plan_step_int4(p, sp, prefix_s, tiles_s, false);
+    else if (!join_grid()) return;
+  }
+  __syncthreads();
 
   // ---- this warp's segment of the flat chunk sequence of its head -----------
   const int glin = blockIdx.x * ge.gpc + grp;  // (segment, head group)
@@ -234,12 +234,18 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge,
   const int gw = seg * p.heads_kv + head;
   int seg0 = 0, n = 0, first_piece = 0;
   if constexpr (DEV) {
-    const int64_t T = __ldcg(sp.prefix + sp.num_req);
-    const int S = int4_step_segments(T, ge.segments);
-    if (seg < S) {
-      seg0 = (int)((int64_t)seg * T / S);
-      n = (int)((int64_t)(seg + 1) * T / S) - seg0;
-      if (n > 0) first_piece = __ldcg(sp.warp_tile + seg);
+    const int64_t T = prefix[sp.num_req];
+    const int segs = int4_step_segments(T, ge.segments);
+    if (seg < segs) {
+      seg0 = (int)((int64_t)seg * T / segs);
+      n = (int)((int64_t)(seg + 1) * T / segs) - seg0;
+      // the last request whose first chunk is seg0 or an earlier one
+      int hi = sp.num_req;
+      while (hi - first_piece > 1) {
+        const int mid = (first_piece + hi) >> 1;
+        if (prefix[mid] <= seg0) first_piece = mid;
+        else hi = mid;
+      }
     }
   } else if (seg < ge.segments) {
     const WarpSeg ws = p.warp_seg[gw];
@@ -247,7 +253,10 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge,
     n = ws.n;
     first_piece = ws.piece;
   }
-  if (n <= 0) return;  // (the whole group: its heads share the chunk range)
+  if (n <= 0) {  // (the whole group: its heads share the chunk range)
+    if (own_plan) (void)join_grid();
+    return;
+  }
 
   // ---- copies ----------------------------------------------------------------
   // Chunk k of the segment is copied by warp k mod hg of the group; a lane
@@ -271,12 +280,11 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge,
       const int flat = seg0 + pos;
       int chunk, req, lo, hi;
       if constexpr (DEV) {
-        while (cur_piece + 1 < sp.num_req && __ldcg(sp.prefix + cur_piece + 1) <= flat) ++cur_piece;
-        const int4 ti = __ldcg(sp.tiles + cur_piece);
-        chunk = ti.x + (flat - __ldcg(sp.prefix + cur_piece));
+        while (cur_piece + 1 < sp.num_req && prefix[cur_piece + 1] <= flat) ++cur_piece;
+        chunk = tiles[cur_piece].x + (flat - prefix[cur_piece]);
         req = cur_piece;
-        lo = ti.y;
-        hi = ti.z;
+        lo = tiles[cur_piece].y;
+        hi = tiles[cur_piece].z;
       } else {
         while (cur_piece + 1 < p.num_pieces && __ldg(&p.pieces[cur_piece + 1].flat0) <= flat) ++cur_piece;
         const DecodePiece* pc = p.pieces + cur_piece;
@@ -315,7 +323,7 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge,
   // This warp's next chunk into stage s, whose parity of use is u (first:
   // the stage has not been used before).
   auto issue = [&](int s, uint32_t u, bool first) -> bool {
-    if (turn % kInt4Turns == 0) fill_records(turn);
+    if (turn % kInt4Turns == 0 && !(own_plan && turn == 0)) fill_records(turn);
     const uint32_t full = meta + 32u * s + 16;
     if (!first && !i4::warp_wait(full + 8, u ^ 1u, abort)) return false;
     const uint4 rec = dev::lds128(recs + 32u * (turn % kInt4Turns));
@@ -368,7 +376,7 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge,
   // A piece's descriptor (read again where it is needed: it does not stay in
   // registers) and its request's first query token.
   struct Piece {
-    int req, row0, nrows, part, q0;
+    int req, row0, nrows, part, q0, pos0, len;
     bool bad;  // (bounds-checked build) its rows lie outside q / out
   };
   auto piece_at = [&](int rel) {
@@ -378,19 +386,25 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge,
       // one of the warp's two 16-row slots: 2 gw for the tile the segment
       // starts in, 2 gw + 1 for the one it ends in.
       const int r = first_piece + rel;
-      const int f0 = __ldcg(sp.prefix + r), f1 = __ldcg(sp.prefix + r + 1);
+      const int f0 = prefix[r], f1 = prefix[r + 1];
       pc.req = r;
       pc.row0 = 0;
-      pc.nrows = __ldcg(&sp.tiles[r].w);
+      pc.nrows = tiles[r].w;
+      pc.len = tiles[r].z;
+      pc.pos0 = pc.len - pc.nrows / G;
       pc.part = f0 < seg0 || f1 > seg0 + n ? (2 * gw + (f0 <= seg0 ? 0 : 1)) * kTileMaxRows : -1;
+      pc.q0 = p.query_start_loc[r];
     } else {
-      const DecodePiece* d = p.pieces + first_piece + rel;
-      pc.req = d->req;
-      pc.row0 = d->row0;
-      pc.nrows = d->nrows;
-      pc.part = d->part;
+      const int4* d = reinterpret_cast<const int4*>(p.pieces + first_piece + rel);
+      const int4 a = __ldg(d), b = __ldg(d + 1), e = __ldg(d + 2);
+      pc.req = a.x;
+      pc.row0 = a.z;
+      pc.nrows = a.w;
+      pc.part = b.x;
+      pc.len = b.w;  // (all keys its rows see; without causality all keys)
+      pc.q0 = e.z;
+      pc.pos0 = e.w;
     }
-    pc.q0 = p.query_start_loc[pc.req];
     pc.bad = false;
     if constexpr (KVQ_CHECKED && !DEV) {
       pc.bad = pc.q0 < 0 || pc.q0 + (pc.row0 + pc.nrows - 1) / G >= p.total_q_tokens;
@@ -404,16 +418,14 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge,
   auto start_piece = [&](int rel) {
     const Piece pc = piece_at(rel);
     const int q0 = pc.q0;
-    const int Q = p.query_start_loc[pc.req + 1] - q0;
-    const int L = p.seq_lens[pc.req];
-    const int p_min = L - Q + pc.row0 / G;
-    const int p_max = L - Q + (pc.row0 + pc.nrows - 1) / G;
-    len = L;
-    pos0 = L - Q;
+    const int p_min = pc.pos0 + pc.row0 / G;
+    const int p_max = pc.pos0 + (pc.row0 + pc.nrows - 1) / G;
+    len = pc.len;
+    pos0 = pc.pos0;
     row0 = pc.row0;
     row_end = pc.row0 + pc.nrows;
     all_lo = W > 0 ? p_max - W + 1 : 0;
-    all_hi = p.causal ? p_min + 1 : L;
+    all_hi = p.causal ? p_min + 1 : len;
     float qv[NT][D / 4];
     float qmax = 0.0f;
 #pragma unroll
@@ -465,7 +477,7 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge,
         const int nr = min(8 * t + 2 * c + e, pc.nrows - 1);
         if constexpr (AL) {
           al_slope[t][e] = p.alibi_slopes[head * G + (pc.row0 + nr) % G] * log2e;
-          al_pos[t][e] = L - Q + (pc.row0 + nr) / G;
+          al_pos[t][e] = pos0 + (pc.row0 + nr) / G;
         }
         m_off[t][e] = kUnset;
         l_run[t][e] = 0.0f;
@@ -562,11 +574,15 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge,
   const uint32_t kpair_sel = (uint32_t)c | 0x40u | ((uint32_t)c << 8) | 0x4000u;
 
   // Iteration i reads chunk i and has chunk i + ahead copied (the first
-  // `ahead` iterations only copy); the last one finishes the last piece.
+  // `ahead` iterations only copy); the last one finishes the last piece.  The
+  // first piece starts while the first copies are in flight; in the fused
+  // step before the grid barrier (then in an iteration of its own).
   int st = 0, kst = 0, kw = 0;     // stage of chunk i; stage and warp of chunk i + ahead
   uint32_t par = 0, kpar = 0;
-  for (int i = -ahead;; ++i) {
-    if (i + ahead < n) {
+  if (DEV && own_plan) fill_records(0);
+  for (int i = own_plan ? -ahead - 1 : -ahead;; ++i) {
+    const bool before = i < -ahead;
+    if (!before && i + ahead < n) {
       if (kw == j && !issue(kst, kpar, i < 1)) break;
       if (++kw == ge.hg) kw = 0;
       if (++kst == S) {
@@ -574,11 +590,12 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge,
         kpar ^= 1u;
       }
     }
-    if (i < 0) continue;
+    if (!before && i < 0) continue;
     const uint32_t sb = sbase + (uint32_t)(st * ge.stage_bytes);
     const uint32_t mb = meta + 32u * st;
-    uint4 rec = make_uint4(0u, 0xFFFFFFFEu, 0u, 0u);
-    if (i < n) {
+    uint4 rec = make_uint4(0u, 0u, 0u, 0u);
+    if (i == n) rec.y = 0xFFFFFFFEu;
+    else if (i > 0) {
       if (!i4::warp_wait(mb + 16, par, abort)) break;
       rec = dev::lds128(mb);
     }
@@ -587,6 +604,14 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge,
       if (i == n) return;
       cur = (int)rec.y;
       start_piece(cur);
+    }
+    if (before) {
+      if (!join_grid()) return;
+      continue;
+    }
+    if (i == 0) {
+      if (!i4::warp_wait(mb + 16, par, abort)) break;
+      rec = dev::lds128(mb);
     }
     const int tok0 = (int)rec.x;
 
@@ -819,7 +844,7 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge,
   // before the CTA's shared memory is released.
   if (lane == 0) atomicExch(p.error_flag, 1);
   for (int rel = max(cur, 0); first_piece + rel < (DEV ? sp.num_req : p.num_pieces); ++rel) {
-    const int f0 = DEV ? __ldcg(sp.prefix + first_piece + rel) : p.pieces[first_piece + rel].flat0;
+    const int f0 = DEV ? prefix[first_piece + rel] : p.pieces[first_piece + rel].flat0;
     if (f0 >= seg0 + n) break;
     const Piece pc = piece_at(rel);
     for (int r = 0; r < pc.nrows && !pc.bad; ++r) {

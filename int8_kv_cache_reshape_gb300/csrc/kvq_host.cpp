@@ -803,7 +803,8 @@ int kvq_get_scheduler_metadata(int num_req, int heads_q, int heads_kv, int head_
         pc.any_hi = (int32_t)t.any_hi;
         pc.flat0 = (int32_t)lo;
         pc.chunk0 = (int32_t)(t.c_lo + (lo - F));
-        pc.pad0 = pc.pad1 = 0;
+        pc.q0 = query_start_loc_host[t.req];
+        pc.pos0 = seq_lens_host[t.req] - (query_start_loc_host[t.req + 1] - pc.q0);
         if (part >= 0) part += t.nrows;
       }
       max_splits = std::max(max_splits, np);

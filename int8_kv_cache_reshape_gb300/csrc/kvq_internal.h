@@ -122,8 +122,9 @@ KVQ_HD constexpr int int4_max_warps(int head_dim, int ntiles) {
          : head_dim == 128 || ntiles == 1                  ? 12
                                                            : 8;
 }
-constexpr size_t kInt4MaxSmem = 217 * 1024;  // dynamic shared memory of a CTA
+constexpr size_t kInt4MaxSmem = 212 * 1024;  // dynamic shared memory of a CTA
 constexpr int kInt4Turns = 16;               // copies a warp prepares at a time
+constexpr int kInt4PlanReq = 256;            // requests a CTA of the fused step plans for itself
 struct Int4Geom {
   int hg, gpc;      // heads (warps) per group, groups per CTA
   int hsplit;       // head groups: heads_kv / hg
@@ -247,7 +248,8 @@ struct DecodePiece {
   int32_t any_hi;
   int32_t flat0;     // position of the piece's first chunk in its launch's flat sequence
   int32_t chunk0;    // that chunk's 16-token index in the request
-  int32_t pad0, pad1;
+  int32_t q0;        // the request's first query token (query_start_loc[req])
+  int32_t pos0;      // position of its query 0: L - Q
 };
 static_assert(sizeof(DecodePiece) == 48, "DecodePiece layout");
 
@@ -326,7 +328,8 @@ struct StepParams {
   int32_t* prefix;              // [num_tiles + 1]: flat index of each tile's first chunk
   int4* tiles;                  // [num_tiles]: {first chunk, key_lo, key_hi, rows}
   int32_t* warp_tile;           // [warps]: the tile holding each warp's first chunk
-                                // (4-bit rows: of all three, one per request or segment)
+                                // (4-bit rows: prefix and tiles are per request, the
+                                // warps find theirs themselves)
   uint32_t* barrier;            // [2]: arrivals, generation (grid barrier)
   int num_req, num_tiles;       // num_tiles = num_req * Hkv
   int max_rows;                 // 8 or 16: rows per tile the launch is built for
