@@ -176,6 +176,20 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge,
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   const int grp = warp / ge.hg, j = warp % ge.hg;  // the group, and the warp's head in it
+  // ---- this warp's segment of the flat chunk sequence of its head -----------
+  const int glin = blockIdx.x * ge.gpc + grp;  // (segment, head group)
+  const int seg = glin / ge.hsplit, hgrp = glin % ge.hsplit;
+  const int head = hgrp * ge.hg + j;
+  const int gw = seg * p.heads_kv + head;
+  int seg0 = 0, n = 0, first_piece = 0;
+  if constexpr (!DEV) {
+    if (seg < ge.segments) {
+      const WarpSeg ws = p.warp_seg[gw];
+      seg0 = ws.seg0;
+      n = ws.n;
+      first_piece = ws.piece;
+    }
+  }
   // (the swizzle goes by shared-memory addresses: stages on 1 KB)
   const uint32_t smem0 = (dev::smem_u32(smem) + 1023u) & ~1023u;
   const uint32_t sbase = smem0 + (uint32_t)(grp * ge.stages * ge.stage_bytes);
@@ -221,18 +235,20 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge,
     return ok;
   };
   if constexpr (DEV) {
-    if (blockIdx.x == 0) plan_step_int4(p, sp, sp.prefix, sp.tiles, true);
-    if (own_plan) plan_step_int4(p, sp, prefix_s, tiles_s, false);
-    else if (!join_grid()) return;
+    if (own_plan) {
+      plan_step_int4(p, sp, prefix_s, tiles_s, blockIdx.x == 0);
+      if (blockIdx.x == 0)
+        for (int r = threadIdx.x; r <= sp.num_req; r += blockDim.x) {
+          sp.prefix[r] = prefix_s[r];
+          if (r < sp.num_req) sp.tiles[r] = tiles_s[r];
+        }
+    } else {
+      if (blockIdx.x == 0) plan_step_int4(p, sp, sp.prefix, sp.tiles, true);
+      if (!join_grid()) return;
+    }
   }
   __syncthreads();
 
-  // ---- this warp's segment of the flat chunk sequence of its head -----------
-  const int glin = blockIdx.x * ge.gpc + grp;  // (segment, head group)
-  const int seg = glin / ge.hsplit, hgrp = glin % ge.hsplit;
-  const int head = hgrp * ge.hg + j;
-  const int gw = seg * p.heads_kv + head;
-  int seg0 = 0, n = 0, first_piece = 0;
   if constexpr (DEV) {
     const int64_t T = prefix[sp.num_req];
     const int segs = int4_step_segments(T, ge.segments);
@@ -247,16 +263,14 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge,
         else hi = mid;
       }
     }
-  } else if (seg < ge.segments) {
-    const WarpSeg ws = p.warp_seg[gw];
-    seg0 = ws.seg0;
-    n = ws.n;
-    first_piece = ws.piece;
   }
   if (n <= 0) {  // (the whole group: its heads share the chunk range)
     if (own_plan) (void)join_grid();
     return;
   }
+  // Host plans are launched as programmatic dependents of whatever ran before
+  // on the stream: only the plan has been read so far.
+  if constexpr (!DEV) asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // ---- copies ----------------------------------------------------------------
   // Chunk k of the segment is copied by warp k mod hg of the group; a lane
@@ -286,12 +300,20 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge,
         lo = tiles[cur_piece].y;
         hi = tiles[cur_piece].z;
       } else {
-        while (cur_piece + 1 < p.num_pieces && __ldg(&p.pieces[cur_piece + 1].flat0) <= flat) ++cur_piece;
-        const DecodePiece* pc = p.pieces + cur_piece;
-        chunk = __ldg(&pc->chunk0) + (flat - __ldg(&pc->flat0));
-        req = __ldg(&pc->req);
-        lo = __ldg(&pc->any_lo);
-        hi = __ldg(&pc->any_hi);
+        // (a piece's descriptor and the next one's start are read together)
+        while (true) {
+          const int4* d = reinterpret_cast<const int4*>(p.pieces + cur_piece);
+          const int4 a = __ldg(d), b = __ldg(d + 1), e = __ldg(d + 2);
+          const int next = cur_piece + 1 < p.num_pieces ? __ldg(&p.pieces[cur_piece + 1].flat0) : 0x7FFFFFFF;
+          if (flat < next) {
+            chunk = e.y + (flat - e.x);
+            req = a.x;
+            lo = b.z;
+            hi = b.w;
+            break;
+          }
+          ++cur_piece;
+        }
       }
       tok0 = chunk * kInt4Chunk;
       rel = cur_piece - first_piece;
@@ -884,10 +906,24 @@ int launch_int4_decode(const AttnParams& p, const PrefillMaps& maps, cudaStream_
   auto kern = int4_decode_kernel<D, NT, AL, false>;
   static std::atomic<bool> raised[kMaxCachedDevices];
   if (!int4_raise_smem(reinterpret_cast<const void*>(kern), raised)) return KVQ_E_CUDA;
-  const int ctas = (ge.segments * ge.hsplit + ge.gpc - 1) / ge.gpc;
+  // A programmatic dependent of the kernel before it on the stream (it waits
+  // for that one's completion after reading its plan).
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((ge.segments * ge.hsplit + ge.gpc - 1) / ge.gpc));
+  cfg.blockDim = dim3((unsigned)(32 * ge.hg * ge.gpc));
+  cfg.dynamicSmemBytes = ge.smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
   StepParams none{};
-  kern<<<(unsigned)ctas, 32 * ge.hg * ge.gpc, ge.smem, stream>>>(p, none, ge, maps);
-  return cudaGetLastError() == cudaSuccess ? KVQ_OK : KVQ_E_CUDA;
+  if (cudaLaunchKernelEx(&cfg, kern, p, none, ge, maps) != cudaSuccess) {
+    cudaGetLastError();
+    return KVQ_E_CUDA;
+  }
+  return KVQ_OK;
 }
 
 // The fused step: every CTA resident at once (a cooperative launch), as many
