@@ -47,20 +47,69 @@ __device__ __forceinline__ float absmax8(const uint4 x) {
   return m;
 }
 
-// 4-bit codes: an element's code + 8 under its group's step s * m_g.
+// 4-bit codes.  The format's quotients are correctly rounded; a division costs
+// some ten instructions and only decides which integer is nearest, so the
+// codes come from products with reciprocals a little too large and a little
+// too small: rint is monotonic, and where both give the same integer, so does
+// the rounded quotient between them.  Where they differ (a quotient within
+// 2^-19 of halfway) the division decides.
+//
+// Reference form: an element's code + 8 under its group's step s * m_g.
 __device__ __forceinline__ uint32_t enc_int4(float x, float step) {
   const int v = __float2int_rn(__fdiv_rn(x, step));
   return (uint32_t)(max(-7, min(7, v)) + 8);
 }
 // Eight consecutive elements' code word: element e in nibble e / 2, the odd
 // ones four nibbles up.
-__device__ __forceinline__ uint32_t quantise8_int4(const uint4 x, float step) {
+static __device__ __noinline__ uint32_t quantise8_int4_exact(const uint4 x, float step) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
   uint32_t code = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     code |= enc_int4(dev::bf16_lo(w[i]), step) << (4 * i) | enc_int4(dev::bf16_hi(w[i]), step) << (4 * i + 16);
   return code;
+}
+// (|x| <= gmax of every element; step > 0)
+__device__ __forceinline__ uint32_t quantise8_int4(const uint4 x, float gmax, float step) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  const float inv = dev::rcp_approx(step);
+  const float hi = inv * (1.0f + 0x1p-20f), lo = inv * (1.0f - 0x1p-20f);
+  // x * inv + 1.5 2^23 + 8 holds rint(x * inv) + 8 in its lowest bits, on top
+  // of the pattern of 1.5 2^23: the sum of the patterns times 16^j, less the
+  // constant's, is the code word (modulo 2^32)
+  const float magic = 12582912.0f + 8.0f;
+  uint32_t code = 0, differ = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float a = dev::bf16_lo(w[i]), b = dev::bf16_hi(w[i]);
+    const uint32_t a0 = __float_as_uint(fmaf(a, lo, magic)), a1 = __float_as_uint(fmaf(a, hi, magic));
+    const uint32_t b0 = __float_as_uint(fmaf(b, lo, magic)), b1 = __float_as_uint(fmaf(b, hi, magic));
+    differ |= (a0 ^ a1) | (b0 ^ b1);
+    code += a0 * (1u << (4 * i)) + b0 * (1u << (4 * i + 16));
+  }
+  code -= 0x4B400000u * 0x11111111u;
+  // (steps so small that the reciprocal or the clamp matters: a quotient above
+  // 7.25, or none, also goes the exact way)
+  return differ == 0 && gmax * hi < 7.25f ? code : quantise8_int4_exact(x, step);
+}
+// A group's multiplier min(127, ceil((gmax / s) / 7)), the same way.
+__device__ __forceinline__ uint32_t int4_multiplier(float gmax, float rowmax, float s) {
+  const float u = gmax * dev::rcp_approx(s) * (1.0f / kInt4MaxCode);
+  const float near = rintf(u), d = u - near;
+  // (s = rowmax / 889 is far above the subnormals: the largest group is at
+  // 889 / 7 = 127 but for rounding, clamped from above)
+  const bool normal = rowmax > 0x1p-100f;
+  if (normal && gmax == rowmax) return (uint32_t)kInt4MaxMul;
+  if (normal && fabsf(d) > 0x1p-12f) return (uint32_t)(int)fminf(kInt4MaxMul, d > 0.0f ? near + 1.0f : near);
+  return (uint32_t)(int)fminf(kInt4MaxMul, ceilf(__fdiv_rn(__fdiv_rn(gmax, s), kInt4MaxCode)));
+}
+// Magnitudes of 8 bf16 values: the packed maximum.
+__device__ __forceinline__ uint32_t absmax8_packed(const uint4 x) {
+  return dev::max_u16x2(dev::max_u16x2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu),
+                        dev::max_u16x2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
+}
+__device__ __forceinline__ float max_of_packed(uint32_t m) {
+  return __uint_as_float(max(m << 16, m & 0xFFFF0000u));
 }
 
 // Writes one row's share (8 elements) of codes, and for per-token-head the
@@ -78,18 +127,19 @@ __device__ __forceinline__ void write_part(const uint4 x, float tensor_scale, ui
   } else if constexpr (is_int4(DT)) {
     // A group is D / 8 dims: GT threads of the row.
     constexpr int GT = TPR / 8;
-    float mg = absmax8(x);
+    uint32_t mp = absmax8_packed(x);
 #pragma unroll
-    for (int off = 1; off < GT; off <<= 1) mg = fmaxf(mg, __shfl_xor_sync(0xffffffffu, mg, off));
-    float m = mg;
+    for (int off = 1; off < GT; off <<= 1) mp = dev::max_u16x2(mp, __shfl_xor_sync(0xffffffffu, mp, off));
+    const float mg = max_of_packed(mp);
 #pragma unroll
-    for (int off = GT; off < TPR; off <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    for (int off = GT; off < TPR; off <<= 1) mp = dev::max_u16x2(mp, __shfl_xor_sync(0xffffffffu, mp, off));
+    const float m = max_of_packed(mp);
     const float s = __fdiv_rn(m, kInt4Levels);
     uint32_t mul = 0, code = 0x88888888u;
     if (s > 0.0f) {
-      mul = (uint32_t)fminf(kInt4MaxMul, ceilf(__fdiv_rn(__fdiv_rn(mg, s), kInt4MaxCode)));
+      mul = int4_multiplier(mg, m, s);
       const float step = __fmul_rn(s, (float)mul);
-      if (step > 0.0f) code = quantise8_int4(x, step);
+      if (step > 0.0f) code = quantise8_int4(x, mg, step);
     }
     // the four multipliers of each half of the row in one word: {s, m_0..3}
     // and {m_4..7, 0} go out as two 8-byte stores of the halves' first threads
@@ -141,7 +191,8 @@ __device__ __forceinline__ void write_rows(const uint16_t* __restrict__ key,
     const int64_t r = r0 + tid / TPR;
     const bool in_range = r < total_rows;
     const int64_t rr = in_range ? r : total_rows - 1;
-    const int64_t t = rr / heads_kv;
+    // (a 64-bit division costs more than the rest of the addressing)
+    const int64_t t = total_rows <= 0x7FFFFFFF ? (int64_t)((uint32_t)rr / (uint32_t)heads_kv) : rr / heads_kv;
     const int h = (int)(rr - t * heads_kv);
     const int64_t slot = slot_mapping[t];
     const bool active = in_range && slot >= 0 && slot < num_slots;

@@ -82,7 +82,8 @@ gather_cache_kernel(const uint8_t* __restrict__ key_cache, const uint8_t* __rest
   const int part = threadIdx.x % kTpr;
   const int64_t rows = num_tokens * heads_kv, step = (int64_t)gridDim.x * kRowsPerStep;
   for (int64_t r = (int64_t)blockIdx.x * kRowsPerStep + threadIdx.x / kTpr; r < rows; r += step) {
-    const int64_t t = r / heads_kv;
+    // (a 64-bit division costs more than the rest of the row)
+    const int64_t t = rows <= 0x7FFFFFFF ? (int64_t)((uint32_t)r / (uint32_t)heads_kv) : r / heads_kv;
     const int h = (int)(r - t * heads_kv);
     const int64_t slot = slot_mapping[t];
     uint4 k = make_uint4(0, 0, 0, 0), v = k;
