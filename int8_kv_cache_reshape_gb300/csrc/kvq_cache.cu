@@ -7,7 +7,8 @@
 // scale computed on the fly and stored inline).  The CPU design packs rows
 // for AMX tiles; here rows stay in the plain paged layout
 // [block][slot][kv_head][row] and each (token, head) row is handled by
-// D/8 threads, each with one 16-byte load of K and of V (kvq_cache_row.cuh).
+// D/8 threads, each with one 16-byte load of K and of V (kvq_cache_row.cuh;
+// 4-bit rows: D/16 threads with two).
 //
 // HBM bound: per element 2 bytes read, 1 byte written (half a byte for 4-bit
 // codes; +16 bytes of scales per row per-token-head).
@@ -31,9 +32,14 @@ reshape_and_cache_kernel(const uint16_t* __restrict__ key, const uint16_t* __res
                          uint8_t* __restrict__ value_cache, int64_t num_slots,
                          const int64_t* __restrict__ slot_mapping, float k_scale,
                          float v_scale) {
-  row::write_rows<DT, D>(key, value, num_tokens, key_stride, value_stride, heads_kv, key_cache,
-                         value_cache, num_slots, slot_mapping, k_scale, v_scale, kThreads,
-                         threadIdx.x, blockIdx.x, gridDim.x);
+  if constexpr (is_int4(DT))
+    row::write_rows_int4<D>(key, value, num_tokens, key_stride, value_stride, heads_kv, key_cache,
+                            value_cache, num_slots, slot_mapping, kThreads, threadIdx.x, blockIdx.x,
+                            gridDim.x);
+  else
+    row::write_rows<DT, D>(key, value, num_tokens, key_stride, value_stride, heads_kv, key_cache,
+                           value_cache, num_slots, slot_mapping, k_scale, v_scale, kThreads,
+                           threadIdx.x, blockIdx.x, gridDim.x);
 }
 
 template <int DT, int D>
@@ -41,7 +47,7 @@ int launch(const void* key, const void* value, int64_t num_tokens, int64_t key_s
            int64_t value_stride, int heads_kv, void* key_cache, void* value_cache,
            int64_t num_slots, const int64_t* slot_mapping, float k_scale, float v_scale,
            cudaStream_t stream) {
-  constexpr int kRowsPerBlock = kThreads / (D / 8);
+  constexpr int kRowsPerBlock = kThreads / (is_int4(DT) ? D / 16 : D / 8);
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)

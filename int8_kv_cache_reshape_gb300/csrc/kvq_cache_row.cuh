@@ -124,34 +124,6 @@ __device__ __forceinline__ void write_part(const uint4 x, float tensor_scale, ui
     uint32_t lo, hi;
     quantise8<DT>(x, tensor_scale, lo, hi);
     if (active) *reinterpret_cast<uint2*>(row + part * 8) = make_uint2(lo, hi);
-  } else if constexpr (is_int4(DT)) {
-    // A group is D / 8 dims: GT threads of the row.
-    constexpr int GT = TPR / 8;
-    uint32_t mp = absmax8_packed(x);
-#pragma unroll
-    for (int off = 1; off < GT; off <<= 1) mp = dev::max_u16x2(mp, __shfl_xor_sync(0xffffffffu, mp, off));
-    const float mg = max_of_packed(mp);
-#pragma unroll
-    for (int off = GT; off < TPR; off <<= 1) mp = dev::max_u16x2(mp, __shfl_xor_sync(0xffffffffu, mp, off));
-    const float m = max_of_packed(mp);
-    const float s = __fdiv_rn(m, kInt4Levels);
-    uint32_t mul = 0, code = 0x88888888u;
-    if (s > 0.0f) {
-      mul = int4_multiplier(mg, m, s);
-      const float step = __fmul_rn(s, (float)mul);
-      if (step > 0.0f) code = quantise8_int4(x, mg, step);
-    }
-    // the four multipliers of each half of the row in one word: {s, m_0..3}
-    // and {m_4..7, 0} go out as two 8-byte stores of the halves' first threads
-    uint32_t word = mul << (8 * ((part / GT) & 3));
-    word |= __shfl_xor_sync(0xffffffffu, word, GT);
-    word |= __shfl_xor_sync(0xffffffffu, word, 2 * GT);
-    if (active) {
-      *reinterpret_cast<uint32_t*>(row + part * 4) = code;
-      if (part % (TPR / 2) == 0)
-        *reinterpret_cast<uint2*>(row + kRowCodes / 2 + (part == 0 ? 0 : 8)) =
-            part == 0 ? make_uint2(__float_as_uint(s), word) : make_uint2(word, 0u);
-    }
   } else {
     float m = absmax8(x);
 #pragma unroll
@@ -201,6 +173,97 @@ __device__ __forceinline__ void write_rows(const uint16_t* __restrict__ key,
     const int64_t dst = (active ? (slot * heads_kv + h) : 0) * (int64_t)kRow;
     write_part<DT, TPR>(kx, k_scale, key_cache + dst, part, active);
     write_part<DT, TPR>(vx, v_scale, value_cache + dst, part, active);
+  }
+}
+
+// Writes one 4-bit row's share of 16 elements (x0, x1: the first 8, the rest):
+// TPR = D / 16 threads (aligned in the warp) own a row.  A group is D / 8
+// dims: half a share, a share or two.
+template <int D>
+__device__ __forceinline__ void write_part_int4(const uint4 x0, const uint4 x1, uint8_t* row, int part,
+                                                bool active) {
+  constexpr int TPR = D / 16;
+  const uint32_t m0 = absmax8_packed(x0), m1 = absmax8_packed(x1);
+  uint32_t mp = dev::max_u16x2(m0, m1);
+  if constexpr (D == 256) mp = dev::max_u16x2(mp, __shfl_xor_sync(0xffffffffu, mp, 1));
+  const float g0 = max_of_packed(D == 64 ? m0 : mp), g1 = D == 64 ? max_of_packed(m1) : g0;
+#pragma unroll
+  for (int off = D == 256 ? 2 : 1; off < TPR; off <<= 1)
+    mp = dev::max_u16x2(mp, __shfl_xor_sync(0xffffffffu, mp, off));
+  const float m = max_of_packed(mp);
+  const float s = __fdiv_rn(m, kInt4Levels);
+  uint32_t mul0 = 0, mul1 = 0;
+  uint2 code = make_uint2(0x88888888u, 0x88888888u);
+  if (s > 0.0f) {
+    mul0 = int4_multiplier(g0, m, s);
+    mul1 = D == 64 ? int4_multiplier(g1, m, s) : mul0;
+    const float step0 = __fmul_rn(s, (float)mul0), step1 = __fmul_rn(s, (float)mul1);
+    if (step0 > 0.0f) code.x = quantise8_int4(x0, g0, step0);
+    if (step1 > 0.0f) code.y = quantise8_int4(x1, g1, step1);
+  }
+  // the four multipliers of each half of the row in one word: {s, m_0..3} and
+  // {m_4..7, 0} go out as two 8-byte stores of the halves' first threads
+  uint32_t word;
+  if constexpr (D == 64) {
+    word = (mul0 | mul1 << 8) << (16 * (part & 1));
+    word |= __shfl_xor_sync(0xffffffffu, word, 1);
+  } else {
+    constexpr int GT = D / 128;  // threads of a group
+    word = mul0 << (8 * ((part / GT) & 3));
+    word |= __shfl_xor_sync(0xffffffffu, word, GT);
+    word |= __shfl_xor_sync(0xffffffffu, word, 2 * GT);
+  }
+  if (active) {
+    *reinterpret_cast<uint2*>(row + part * 8) = code;
+    if (part % (TPR / 2) == 0)
+      *reinterpret_cast<uint2*>(row + D / 2 + (part == 0 ? 0 : 8)) =
+          part == 0 ? make_uint2(__float_as_uint(s), word) : make_uint2(word, 0u);
+  }
+}
+
+// write_rows for 4-bit rows, 16 elements of K and of V per thread: what is
+// computed per group and row (scale, multiplier, reciprocals, shuffles) is
+// most of the work with 8.
+template <int D>
+__device__ __forceinline__ void write_rows_int4(const uint16_t* __restrict__ key,
+                                                const uint16_t* __restrict__ value, int64_t num_tokens,
+                                                int64_t key_stride, int64_t value_stride, int heads_kv,
+                                                uint8_t* __restrict__ key_cache,
+                                                uint8_t* __restrict__ value_cache, int64_t num_slots,
+                                                const int64_t* __restrict__ slot_mapping, int threads,
+                                                int tid, int64_t first_step, int64_t stride) {
+  constexpr int TPR = D / 16;
+  constexpr int kRow = row_bytes(KVQ_INT4_PER_TOKEN_HEAD, D);
+  const int rows_per_step = threads / TPR;
+  const int part = tid % TPR;
+  const int64_t total_rows = num_tokens * heads_kv;
+  const int64_t step = stride * rows_per_step;
+  // (token, head) of this thread's row, advanced by the step's: one division
+  int64_t r = first_step * rows_per_step + tid / TPR;
+  int64_t t = r / heads_kv;
+  int h = (int)(r - t * heads_kv);
+  const int64_t dt = step / heads_kv;
+  const int dh = (int)(step - dt * heads_kv);
+  for (int64_t r0 = first_step * rows_per_step; r0 < total_rows; r0 += step) {
+    // (threads past the end take part in the shuffles with the last token's
+    // rows and write nothing)
+    const bool in_range = t < num_tokens;
+    const int64_t tt = in_range ? t : num_tokens - 1;
+    const int64_t slot = slot_mapping[tt];
+    const uint16_t* ks = key + tt * key_stride + (int64_t)h * D + part * 16;
+    const uint16_t* vs = value + tt * value_stride + (int64_t)h * D + part * 16;
+    const uint4 k0 = dev::ldg_stream(ks), k1 = dev::ldg_stream(ks + 8);
+    const uint4 v0 = dev::ldg_stream(vs), v1 = dev::ldg_stream(vs + 8);
+    const bool active = in_range && slot >= 0 && slot < num_slots;
+    const int64_t dst = (active ? (slot * heads_kv + h) : 0) * (int64_t)kRow;
+    write_part_int4<D>(k0, k1, key_cache + dst, part, active);
+    write_part_int4<D>(v0, v1, value_cache + dst, part, active);
+    t += dt;
+    h += dh;
+    if (h >= heads_kv) {
+      h -= heads_kv;
+      ++t;
+    }
   }
 }
 

@@ -211,10 +211,9 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge,
   if constexpr (DEV) {
     StageLane st;
     stage_issue(sp, st);
-    row::write_rows<KVQ_INT4_PER_TOKEN_HEAD, D>(
-        sp.key, sp.value, sp.num_tokens, sp.key_stride, sp.value_stride, p.heads_kv, sp.key_cache,
-        sp.value_cache, sp.num_slots, sp.slot_mapping, p.k_scale, p.v_scale, blockDim.x, threadIdx.x,
-        blockIdx.x, gridDim.x);
+    row::write_rows_int4<D>(sp.key, sp.value, sp.num_tokens, sp.key_stride, sp.value_stride, p.heads_kv,
+                            sp.key_cache, sp.value_cache, sp.num_slots, sp.slot_mapping, blockDim.x,
+                            threadIdx.x, blockIdx.x, gridDim.x);
     stage_finish(sp, st);
     // (the bulk copies below read rows that other CTAs stored: both sides
     // order their proxies)

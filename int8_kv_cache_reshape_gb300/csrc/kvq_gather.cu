@@ -6,10 +6,12 @@
 // group's multiplier) converts exactly, so an fp32 output carries one
 // rounding, and a bf16 output is that fp32 value rounded once more.
 //
-// HBM bound, almost all of it the output: a thread stores 16 bytes of K and
-// of V (4 fp32 or 8 bf16 values), so a warp's stores cover whole lines, and
-// loads the 2 to 16 bytes of codes behind them and the row's tail (the same
-// few sectors for all of a row's threads).
+// HBM bound, almost all of it the output.  A thread takes 8 values of K and of
+// V: one code word of a 4-bit row, 8 bytes of an 8-bit one; its fp32 values go
+// out in one 32-byte store each where the outputs' alignment allows (else two
+// of 16), so a warp's stores cover whole lines.  With 4 values a thread the
+// kernel was bound by its instructions (166 for 8 values, 36.1 us for 20,011
+// tokens x 8 heads of 128 as fp32).
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -21,86 +23,102 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// N consecutive values from dim d0 (a multiple of N) of a row.
-template <int DT, int D, int N>
-__device__ __forceinline__ void load_values(const uint8_t* row, int d0, float tensor_scale, float (&v)[N]) {
+// 8 consecutive values, dims 8 part .. 8 part + 7, of a row.
+template <int DT, int D>
+__device__ __forceinline__ void load_values(const uint8_t* row, int part, float tensor_scale, float (&v)[8]) {
   if constexpr (DT == KVQ_AUTO) {
+    const uint4 w = dev::ldg_stream(row + 16 * part);
+    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int i = 0; i < N; i += 4) {
-      const uint2 w = dev::ldg_stream8(row + 2 * (d0 + i));
-      v[i] = dev::bf16_lo(w.x);
-      v[i + 1] = dev::bf16_hi(w.x);
-      v[i + 2] = dev::bf16_lo(w.y);
-      v[i + 3] = dev::bf16_hi(w.y);
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = dev::bf16_lo(x[i]);
+      v[2 * i + 1] = dev::bf16_hi(x[i]);
     }
   } else if constexpr (is_int4(DT)) {
-    // 8 dims a word; N = 4: the two nibbles 2k and 2k + 1 of each half
-    const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(row + (d0 / 8) * 4));
-    const float s = __ldg(reinterpret_cast<const float*>(row + D / 2));
-    const int m = __ldg(row + D / 2 + 4 + d0 / (D / 8));
-    const int k0 = N == 4 ? (d0 & 4) / 2 : 0;
+    const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(row + 4 * part));
+    const uint4 tail = __ldg(reinterpret_cast<const uint4*>(row + D / 2));  // s, m_0..3, m_4..7
+    const int g = part / (D / 64);
+    const float s = __uint_as_float(tail.x);
+    const float m = (float)(((g < 4 ? tail.y : tail.z) >> (8 * (g & 3))) & 0xFFu);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int c = (int)((w >> (4 * (k0 + i / 2) + 16 * (i & 1))) & 15u) - 8;
-      v[i] = s * (float)(m * c);
+    for (int i = 0; i < 8; ++i) {
+      // a nibble below the pattern of 2^23 is 2^23 + code + 8
+      const uint32_t u = ((w >> (4 * (i / 2) + 16 * (i & 1))) & 15u) | 0x4B000000u;
+      v[i] = s * ((__uint_as_float(u) - 8388616.0f) * m);
     }
   } else {
     const float s = is_per_token_head(DT) ? __ldg(reinterpret_cast<const float*>(row + D)) : tensor_scale;
+    const uint2 w = dev::ldg_stream8(row + 8 * part);
+    uint32_t h[4];
+    dev::word_to_f16x2x2<DT>(w.x, h[0], h[1]);
+    dev::word_to_f16x2x2<DT>(w.y, h[2], h[3]);
 #pragma unroll
-    for (int i = 0; i < N; i += 4) {
-      uint32_t lo, hi;
-      dev::word_to_f16x2x2<DT>(__ldg(reinterpret_cast<const uint32_t*>(row + d0 + i)), lo, hi);
-      const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
-      const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-      v[i] = a.x * s;
-      v[i + 1] = a.y * s;
-      v[i + 2] = b.x * s;
-      v[i + 3] = b.y * s;
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+      v[2 * i] = f.x * s;
+      v[2 * i + 1] = f.y * s;
     }
   }
 }
 
-template <int N>
-__device__ __forceinline__ uint4 pack_out(const float (&v)[N]) {
-  if constexpr (N == 4)
-    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
-  else
-    return make_uint4(dev::pack_bf16x2(v[0], v[1]), dev::pack_bf16x2(v[2], v[3]), dev::pack_bf16x2(v[4], v[5]),
-                      dev::pack_bf16x2(v[6], v[7]));
+// How the outputs are stored: bf16; fp32 by 32 bytes; fp32 by 16.
+enum { kOutBf16 = 0, kOutFp32 = 1, kOutFp32Half = 2 };
+template <int OUT>
+__device__ __forceinline__ void store_values(void* out, int64_t at, const float (&v)[8]) {
+  if constexpr (OUT == kOutBf16) {
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at) =
+        make_uint4(dev::pack_bf16x2(v[0], v[1]), dev::pack_bf16x2(v[2], v[3]), dev::pack_bf16x2(v[4], v[5]),
+                   dev::pack_bf16x2(v[6], v[7]));
+  } else {
+    float* o = static_cast<float*>(out) + at;
+    if constexpr (OUT == kOutFp32) {
+      asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                   :: "l"(o), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]),
+                   "f"(v[7]) : "memory");
+    } else {
+      *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<float4*>(o + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    }
+  }
 }
 
-// N: values per 16 output bytes (4: fp32, 8: bf16); D / N threads per row,
-// grid-stride over rows.
-template <int DT, int D, int N>
+// D / 8 threads per row, grid-stride over rows.
+template <int DT, int D, int OUT>
 __global__ void __launch_bounds__(kThreads)
-gather_cache_kernel(const uint8_t* __restrict__ key_cache, const uint8_t* __restrict__ value_cache,
-                    int64_t num_slots, int heads_kv, const int64_t* __restrict__ slot_mapping,
-                    int64_t num_tokens, uint4* __restrict__ key_out, uint4* __restrict__ value_out,
-                    int64_t key_stride, int64_t value_stride, float k_scale, float v_scale) {
-  constexpr int kTpr = D / N, kRowsPerStep = kThreads / kTpr;
+gather_cache_kernel(const GatherArgs a) {
+  constexpr int kTpr = D / 8, kRowsPerStep = kThreads / kTpr;
   constexpr int64_t kRow = row_bytes(DT, D);
   const int part = threadIdx.x % kTpr;
-  const int64_t rows = num_tokens * heads_kv, step = (int64_t)gridDim.x * kRowsPerStep;
-  for (int64_t r = (int64_t)blockIdx.x * kRowsPerStep + threadIdx.x / kTpr; r < rows; r += step) {
-    // (a 64-bit division costs more than the rest of the row)
-    const int64_t t = rows <= 0x7FFFFFFF ? (int64_t)((uint32_t)r / (uint32_t)heads_kv) : r / heads_kv;
-    const int h = (int)(r - t * heads_kv);
-    const int64_t slot = slot_mapping[t];
-    uint4 k = make_uint4(0, 0, 0, 0), v = k;
-    if (slot >= 0 && slot < num_slots) {
-      const int64_t off = (slot * heads_kv + h) * kRow;
-      float a[N], b[N];
-      load_values<DT, D, N>(key_cache + off, part * N, k_scale, a);
-      load_values<DT, D, N>(value_cache + off, part * N, v_scale, b);
-      k = pack_out<N>(a);
-      v = pack_out<N>(b);
+  const int64_t step = (int64_t)gridDim.x * kRowsPerStep;
+  // (token, head) of this thread's row, advanced by the step's: one division
+  const int64_t r = (int64_t)blockIdx.x * kRowsPerStep + threadIdx.x / kTpr;
+  int64_t t = r / a.heads_kv;
+  int h = (int)(r - t * a.heads_kv);
+  const int64_t dt = step / a.heads_kv;
+  const int dh = (int)(step - dt * a.heads_kv);
+  while (t < a.num_tokens) {
+    const int64_t slot = a.slot_mapping[t];
+    float k[8], v[8];
+    if (slot >= 0 && slot < a.num_slots) {
+      const int64_t off = (slot * a.heads_kv + h) * kRow;
+      load_values<DT, D>(a.key_cache + off, part, a.k_scale, k);
+      load_values<DT, D>(a.value_cache + off, part, a.v_scale, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) k[i] = v[i] = 0.0f;
     }
-    key_out[(t * key_stride + (int64_t)h * D) / N + part] = k;
-    value_out[(t * value_stride + (int64_t)h * D) / N + part] = v;
+    store_values<OUT>(a.key_out, t * a.key_stride + (int64_t)h * D + 8 * part, k);
+    store_values<OUT>(a.value_out, t * a.value_stride + (int64_t)h * D + 8 * part, v);
+    t += dt;
+    h += dh;
+    if (h >= a.heads_kv) {
+      h -= a.heads_kv;
+      ++t;
+    }
   }
 }
 
-template <int DT, int D, int N>
+template <int DT, int D, int OUT>
 int launch(const GatherArgs& a, cudaStream_t stream) {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -108,20 +126,20 @@ int launch(const GatherArgs& a, cudaStream_t stream) {
     cudaGetLastError();
     return KVQ_E_CUDA;
   }
-  constexpr int kRowsPerStep = kThreads / (D / N);
+  constexpr int kRowsPerStep = kThreads / (D / 8);
   int64_t blocks = (a.num_tokens * a.heads_kv + kRowsPerStep - 1) / kRowsPerStep;
   const int64_t cap = (int64_t)sms * 8;  // 8 resident 256-thread blocks per SM
   if (blocks > cap) blocks = cap;
-  gather_cache_kernel<DT, D, N><<<(unsigned)blocks, kThreads, 0, stream>>>(
-      a.key_cache, a.value_cache, a.num_slots, a.heads_kv, a.slot_mapping, a.num_tokens,
-      static_cast<uint4*>(a.key_out), static_cast<uint4*>(a.value_out), a.key_stride, a.value_stride,
-      a.k_scale, a.v_scale);
+  gather_cache_kernel<DT, D, OUT><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
   return cudaGetLastError() == cudaSuccess ? KVQ_OK : KVQ_E_CUDA;
 }
 
 template <int DT, int D>
 int launch_n(const GatherArgs& a, bool fp32, cudaStream_t stream) {
-  return fp32 ? launch<DT, D, 4>(a, stream) : launch<DT, D, 8>(a, stream);
+  if (!fp32) return launch<DT, D, kOutBf16>(a, stream);
+  // (token strides are multiples of 8 elements)
+  const bool wide = ((reinterpret_cast<uintptr_t>(a.key_out) | reinterpret_cast<uintptr_t>(a.value_out)) & 31) == 0;
+  return wide ? launch<DT, D, kOutFp32>(a, stream) : launch<DT, D, kOutFp32Half>(a, stream);
 }
 
 template <int DT>

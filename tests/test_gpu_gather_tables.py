@@ -83,6 +83,12 @@ def test_gather_into_strided_rows(cuda_device):
     kvq().prepare_gather_cache(g.kc, g.vc, g.slots, a, b, "int4_per_token_head")()
     assert torch.equal(buf[:, 1:3], a) and torch.equal(buf[:, 4:6], b)
     assert (buf[:, [0, 3, 6]] == 3.0).all()
+    # outputs 16 bytes off a 32-byte border (16-byte stores)
+    flat = torch.full((2 * 50 * 2 * 128 + 16,), 5.0, device=g.dev)
+    c, d = (flat[4 + i * 12800: 4 + (i + 1) * 12800].view(50, 2, 128) for i in range(2))
+    kvq().gather_cache(g.kc, g.vc, g.slots, c, d, "int4_per_token_head")
+    assert torch.equal(c, a) and torch.equal(d, b)
+    assert (flat[:4] == 5.0).all() and (flat[4 + 25600:] == 5.0).all()
     empty = torch.empty((0, 2, 128), device=g.dev)
     kvq().gather_cache(g.kc, g.vc, g.slots[:0], empty, empty, "int4_per_token_head")
 
