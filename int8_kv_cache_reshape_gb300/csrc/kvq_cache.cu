@@ -32,14 +32,18 @@ reshape_and_cache_kernel(const uint16_t* __restrict__ key, const uint16_t* __res
                          uint8_t* __restrict__ value_cache, int64_t num_slots,
                          const int64_t* __restrict__ slot_mapping, float k_scale,
                          float v_scale) {
-  if constexpr (is_int4(DT))
+  if constexpr (is_int4(DT)) {
+    // (a programmatic dependent of whatever ran before on the stream)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     row::write_rows_int4<D>(key, value, num_tokens, key_stride, value_stride, heads_kv, key_cache,
                             value_cache, num_slots, slot_mapping, kThreads, threadIdx.x, blockIdx.x,
                             gridDim.x);
-  else
+  } else {
     row::write_rows<DT, D>(key, value, num_tokens, key_stride, value_stride, heads_kv, key_cache,
                            value_cache, num_slots, slot_mapping, k_scale, v_scale, kThreads,
                            threadIdx.x, blockIdx.x, gridDim.x);
+  }
 }
 
 template <int DT, int D>
@@ -56,6 +60,12 @@ int launch(const void* key, const void* value, int64_t num_tokens, int64_t key_s
   int64_t blocks = (rows + kRowsPerBlock - 1) / kRowsPerBlock;
   const int64_t cap = (int64_t)sms * 8;  // 8 resident 256-thread blocks per SM
   if (blocks > cap) blocks = cap;
+  if constexpr (is_int4(DT))
+    return launch_dependent(reshape_and_cache_kernel<DT, D>, (unsigned)blocks, kThreads, stream,
+                            static_cast<const uint16_t*>(key), static_cast<const uint16_t*>(value),
+                            num_tokens, key_stride, value_stride, heads_kv,
+                            static_cast<uint8_t*>(key_cache), static_cast<uint8_t*>(value_cache), num_slots,
+                            slot_mapping, k_scale, v_scale);
   reshape_and_cache_kernel<DT, D><<<(unsigned)blocks, kThreads, 0, stream>>>(
       static_cast<const uint16_t*>(key), static_cast<const uint16_t*>(value), num_tokens,
       key_stride, value_stride, heads_kv, static_cast<uint8_t*>(key_cache),

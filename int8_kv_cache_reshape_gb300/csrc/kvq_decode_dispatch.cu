@@ -9,13 +9,13 @@ namespace kvq {
 // The merge runs right after the decode kernel on the stream, launched as its
 // programmatic dependent (the decode kernel lets it be scheduled at once; it
 // waits for the decode grid before reading): no launch gap between the two.
-int launch_merge(const AttnParams& p, int head_dim, int64_t num_merges, void* stream) {
+int launch_merge(const AttnParams& p, int dtype, int head_dim, int64_t num_merges, void* stream) {
   if (num_merges <= 0) return KVQ_OK;
   void (*kern)(AttnParams);
   switch (head_dim) {
-    case 64: kern = merge_splits_kernel<64>; break;
-    case 128: kern = merge_splits_kernel<128>; break;
-    case 256: kern = merge_splits_kernel<256>; break;
+    case 64: kern = is_int4(dtype) ? merge_splits_kernel<64, true> : merge_splits_kernel<64, false>; break;
+    case 128: kern = is_int4(dtype) ? merge_splits_kernel<128, true> : merge_splits_kernel<128, false>; break;
+    case 256: kern = is_int4(dtype) ? merge_splits_kernel<256, true> : merge_splits_kernel<256, false>; break;
     default: return KVQ_E_UNSUPPORTED;
   }
   cudaLaunchConfig_t cfg = {};

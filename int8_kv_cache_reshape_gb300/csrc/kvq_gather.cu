@@ -89,6 +89,9 @@ gather_cache_kernel(const GatherArgs a) {
   constexpr int kTpr = D / 8, kRowsPerStep = kThreads / kTpr;
   constexpr int64_t kRow = row_bytes(DT, D);
   const int part = threadIdx.x % kTpr;
+  // (a programmatic dependent of whatever ran before on the stream)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t step = (int64_t)gridDim.x * kRowsPerStep;
   // (token, head) of this thread's row, advanced by the step's: one division
   const int64_t r = (int64_t)blockIdx.x * kRowsPerStep + threadIdx.x / kTpr;
@@ -130,8 +133,7 @@ int launch(const GatherArgs& a, cudaStream_t stream) {
   int64_t blocks = (a.num_tokens * a.heads_kv + kRowsPerStep - 1) / kRowsPerStep;
   const int64_t cap = (int64_t)sms * 8;  // 8 resident 256-thread blocks per SM
   if (blocks > cap) blocks = cap;
-  gather_cache_kernel<DT, D, OUT><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
-  return cudaGetLastError() == cudaSuccess ? KVQ_OK : KVQ_E_CUDA;
+  return launch_dependent(gather_cache_kernel<DT, D, OUT>, (unsigned)blocks, kThreads, stream, a);
 }
 
 template <int DT, int D>

@@ -1067,7 +1067,7 @@ int kvq_attention_with_kv_cache(const kvq_sched_t* s, int heads_q, int heads_kv,
     const int rc = kvq::launch_decode(p, maps, s->dtype, head_dim, cls + 1, stream);
     if (rc != KVQ_OK) return rc;
   }
-  return kvq::launch_merge(p, head_dim, s->num_merges, stream);
+  return kvq::launch_merge(p, dtype, head_dim, s->num_merges, stream);
 }
 
 // ---- the fused decode step ------------------------------------------------

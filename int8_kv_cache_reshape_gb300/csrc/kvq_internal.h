@@ -412,7 +412,7 @@ int launch_decode_step(const AttnParams& p, const StepParams& sp, const PrefillM
 int step_warps(int dtype, int heads_kv, int head_dim, bool alibi, int max_rows, int64_t* warps);
 // The merge of the decode's cut tiles (p.merges, one CTA each), after the
 // decode kernels of a host-planned call.
-int launch_merge(const AttnParams& p, int head_dim, int64_t num_merges, void* stream);
+int launch_merge(const AttnParams& p, int dtype, int head_dim, int64_t num_merges, void* stream);
 // The fused step's merge of its cut tiles: one CTA per tile of the device
 // plan (tiles left whole return at once), a programmatic dependent of the
 // fused kernel, whose `warps` warps cut the chunk sequence (4-bit rows: warps
@@ -423,6 +423,28 @@ int launch_merge_step(const AttnParams& p, const StepParams& sp, int dtype, int 
 // (at most one per SM is resident).
 int launch_prefill(const AttnParams& p, const PrefillMaps& maps, int dtype, int head_dim,
                    int64_t ctas, void* stream);
+#ifdef __CUDACC__
+// Launch a kernel without dynamic shared memory as a programmatic dependent
+// of the kernel before it on the stream: it may be resident before that one
+// ends, and executes griddepcontrol.wait before it touches memory.
+template <class... P, class... A>
+int launch_dependent(void (*kern)(P...), unsigned grid, unsigned threads, void* stream, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kern, P(args)...) != cudaSuccess) {
+    cudaGetLastError();
+    return KVQ_E_CUDA;
+  }
+  return KVQ_OK;
+}
+#endif
 // Whether a launch needs the ALiBi instances of the kernels.
 inline bool uses_alibi(const AttnParams& p) { return p.alibi_slopes != nullptr; }
 }  // namespace kvq

@@ -147,16 +147,19 @@ __device__ __forceinline__ void merge_tile(const AttnParams& p, const MergeItem&
 
 // Host-planned calls: merge item blockIdx.x of the schedule (split s's rows
 // at m.part + s * nrows).
-template <int D>
+template <int D, bool I4>
 __global__ void __launch_bounds__(kMergeThreads) merge_splits_kernel(const AttnParams p) {
   // Launched as a programmatic dependent of the decode kernel: this CTA may
   // be resident before the decode grid ends; the partials are read only once
   // that grid has completed and its writes are visible.  (The merge item and
   // the request's first token come from the host plan and the caller's
-  // inputs, written before the decode kernel started.)
+  // inputs, written before the decode kernel started.  The decode kernel of
+  // 4-bit rows may itself start before the kernel ahead of it has ended: the
+  // caller's input is then read after the wait.)
   const MergeItem m = p.merges[blockIdx.x];
-  const int q0 = p.query_start_loc[m.req];
+  int q0 = I4 ? 0 : p.query_start_loc[m.req];
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  if constexpr (I4) q0 = p.query_start_loc[m.req];
   merge_tile<D, true>(p, m, q0, m.nsplits, [&](int s) { return m.part + s * m.nrows; });
 }
 

@@ -14,11 +14,13 @@
 // position is always a new token).  So the work is split over tokens alone.
 //
 // One launch, bound by latency: 64 decode tokens move 1.3 KB.  A CTA takes a
-// contiguous run of tokens.  All of a batch's requests that end before its
-// run are summed in one pass (every thread loads its share of the lengths at
-// once: one memory round trip, where a search for the first request takes
-// log2 R dependent ones); the rest are scanned 256 at a time into shared
-// memory, where each token finds its request.
+// contiguous run of tokens and finds their requests in shared memory, among
+// all the batch's requests and their prefix sum (up to kAllRequests of them,
+// read and summed by every CTA for itself: two memory round trips from launch
+// to slot).  Larger batches are taken in windows of kAllRequests that start
+// at the run's first request, with the requests before it summed in one pass
+// (every thread loads its share of the lengths at once, where a search for
+// the first request takes log2 R dependent loads).
 #include <cuda_runtime.h>
 
 #include "kvq_internal.h"
@@ -28,8 +30,11 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-// Tokens of a CTA's run: four a thread.
-constexpr int kRun = 1024;
+// Tokens of a CTA's run, four a thread.
+constexpr int kPer = 4;
+constexpr int kRun = kPer * kThreads;
+// Requests held in shared memory, four a thread.
+constexpr int kAllRequests = kPer * kThreads;
 
 struct TableParams {
   const int32_t* query_start_loc;
@@ -72,20 +77,23 @@ __device__ __forceinline__ int64_t warp_sum(int64_t v) {
 }
 
 __global__ void __launch_bounds__(kThreads) block_tables_kernel(const TableParams p) {
-  __shared__ int64_t part[kWarps], part2[kWarps], base_s[kThreads];
-  __shared__ int32_t part3[kWarps], start_s[kThreads], end_s[kThreads], first_s[kThreads], held_s[kThreads];
-  __shared__ int last_s;
+  __shared__ int64_t part[kWarps], part2[kWarps], base_s[kAllRequests];
+  __shared__ int32_t bad_s[kWarps];
+  __shared__ int32_t start_s[kAllRequests], end_s[kAllRequests], first_s[kAllRequests], held_s[kAllRequests];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t t0 = (int64_t)blockIdx.x * kRun;
   const int64_t t1 = min(t0 + kRun, p.num_tokens);
   const bool last_run = blockIdx.x == gridDim.x - 1;
+  // (a programmatic dependent of whatever ran before on the stream)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t count = max((int64_t)0, min((int64_t)*p.free_count, p.free_capacity));
 
-  // requests that end at or before this run, their new blocks, and how many
-  // of them are left out
+  // large batches: the requests that end at or before this run, their new
+  // blocks, and how many of them are left out
   int64_t base = 0;
   int first_req = 0, bad = 0;
-  if (t0 > 0) {
+  if (p.num_req > kAllRequests && t0 > 0) {
     int64_t sum = 0;
     int n = 0, b = 0;
     for (int r = tid; r < p.num_req; r += kThreads) {
@@ -114,83 +122,133 @@ __global__ void __launch_bounds__(kThreads) block_tables_kernel(const TableParam
     __syncthreads();
   }
 
-  // the rest, kThreads requests at a time (the last run goes through all of
-  // them, for the totals)
+  // kAllRequests requests at a time (the last run goes through all of them,
+  // for the totals): thread i takes kPer consecutive ones
   int64_t t = t0;
-  for (int r0 = first_req; r0 < p.num_req && (t < t1 || last_run); r0 += kThreads) {
-    const int n = min(kThreads, p.num_req - r0);
-    Request q;
-    q.start = q.end = 0;
-    q.first = q.held = q.fresh = 0;
-    q.ok = true;
-    if (tid < n) q = load_request(p, r0 + tid);
-    int64_t incl = q.fresh;
+  for (int r0 = first_req; r0 < p.num_req && (t < t1 || last_run); r0 += kAllRequests) {
+    const int n = min(kAllRequests, p.num_req - r0);
+    const int per = (n + kThreads - 1) / kThreads;
+    int64_t local = 0, fresh[kPer];
+    int bad_t = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      fresh[i] = 0;
+      const int at = tid * per + i;
+      if (i < per && at < n) {
+        const Request q = load_request(p, r0 + at);
+        start_s[at] = (int32_t)q.start;
+        end_s[at] = q.ok ? (int32_t)q.end : (int32_t)q.start;  // a request left out has no tokens
+        first_s[at] = q.first;
+        held_s[at] = q.held;
+        fresh[i] = q.fresh;
+        local += q.fresh;
+        bad_t += !q.ok;
+      }
+    }
+    int64_t incl = local;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
       const int64_t v = __shfl_up_sync(0xffffffffu, incl, off);
       if (lane >= off) incl += v;
     }
-    const int bad_w = __popc(__ballot_sync(0xffffffffu, !q.ok));
+    const int bad_w = __reduce_add_sync(0xffffffffu, bad_t);
     if (lane == 31) {
       part[warp] = incl;
-      part3[warp] = bad_w;
+      bad_s[warp] = bad_w;
     }
-    start_s[tid] = (int32_t)q.start;
-    end_s[tid] = q.ok ? (int32_t)q.end : (int32_t)q.start;  // a request left out has no tokens
-    first_s[tid] = q.first;
-    held_s[tid] = q.held;
+    const int64_t next = p.query_start_loc[r0 + n];  // the window's last end
     __syncthreads();
-    int64_t before = base + incl - q.fresh;
+    int64_t before = base + incl - local;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       if (w < warp) before += part[w];
       base += part[w];
-      bad += part3[w];
+      bad += bad_s[w];
     }
-    base_s[tid] = before;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      if (i < per && tid * per + i < n) base_s[tid * per + i] = before;
+      before += fresh[i];
+    }
     __syncthreads();
-    // the run's tokens up to the next batch's first (the batch's last end)
-    const int64_t stop = min(t1, (int64_t)p.query_start_loc[r0 + n]);
-    for (int64_t k = t + tid; k < stop; k += kThreads) {
-      int lo = 0, hi = n;  // the last request that starts at or before token k
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (start_s[mid] <= k) lo = mid;
-        else hi = mid;
-      }
-      int64_t slot = -1;
-      if (k >= start_s[lo] && k < end_s[lo]) {
-        const uint32_t pos = (uint32_t)(first_s[lo] + (int)(k - start_s[lo]));
-        const uint32_t lb = pos / (uint32_t)p.block_size, off = pos - lb * (uint32_t)p.block_size;
-        int32_t* entry = p.block_table + (int64_t)(r0 + lo) * p.width + lb;
-        int32_t id = -1;
-        if ((int)lb < held_s[lo]) {
-          id = *entry;
-        } else {
-          const int64_t at = base_s[lo] + (int)lb - held_s[lo];
-          if (at < count) id = p.free_blocks[count - 1 - at];
-          if (off == 0) *entry = id;
+    const int64_t stop = min(t1, next);
+    // A thread takes per_t consecutive tokens: one search for the first one's
+    // request (the last that starts at or before it), steps for the others
+    // (a search for each: 10.5 against 9.2 us for 893,000 tokens of 37
+    // requests).
+    const int per_t = (int)((stop - t + kThreads - 1) / kThreads);
+    const int64_t k0 = t + (int64_t)tid * per_t;
+    int lo = 0;
+    for (int hi = n; hi - lo > 1;) {
+      const int mid = (lo + hi) >> 1;
+      if (start_s[mid] <= k0) lo = mid;
+      else hi = mid;
+    }
+    int64_t slot[kPer];
+    int32_t* entry[kPer];
+    const int32_t* from[kPer];
+    uint32_t off[kPer];
+    bool fresh_block[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int64_t k = k0 + i;
+      from[i] = nullptr;
+      entry[i] = nullptr;
+      fresh_block[i] = false;
+      off[i] = 0;
+      if (i < per_t && k < stop) {
+        if (i > 0)
+          while (lo + 1 < n && start_s[lo + 1] <= k) ++lo;
+        if (k >= start_s[lo] && k < end_s[lo]) {
+          const uint32_t pos = (uint32_t)(first_s[lo] + (int)(k - start_s[lo]));
+          const uint32_t lb = pos / (uint32_t)p.block_size;
+          off[i] = pos - lb * (uint32_t)p.block_size;
+          entry[i] = p.block_table + (int64_t)(r0 + lo) * p.width + lb;
+          if ((int)lb < held_s[lo]) {
+            from[i] = entry[i];
+          } else {
+            const int64_t at = base_s[lo] + (int)lb - held_s[lo];
+            if (at < count) from[i] = p.free_blocks + (count - 1 - at);
+            fresh_block[i] = off[i] == 0;
+          }
         }
-        if (id >= 0 && id < p.num_blocks) slot = (int64_t)id * p.block_size + off;
       }
-      p.slot_mapping[k] = slot;
+    }
+    int32_t id[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) id[i] = from[i] ? *from[i] : -1;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      slot[i] = id[i] >= 0 && id[i] < p.num_blocks ? (int64_t)id[i] * p.block_size + off[i] : -1;
+      if (fresh_block[i]) *entry[i] = id[i];
+    }
+    if (per_t == kPer && k0 + kPer <= stop && (k0 & 1) == 0 &&
+        ((uintptr_t)p.slot_mapping & 15u) == 0) {
+#pragma unroll
+      for (int i = 0; i < kPer; i += 2)
+        *reinterpret_cast<longlong2*>(p.slot_mapping + k0 + i) = make_longlong2(slot[i], slot[i + 1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (i < per_t && k0 + i < stop) p.slot_mapping[k0 + i] = slot[i];
     }
     t = max(t, stop);
     __syncthreads();
   }
   for (int64_t k = t + tid; k < t1; k += kThreads) p.slot_mapping[k] = -1;
 
-  // Totals: from the CTA of the last run; free_count_out may be free_count,
-  // so it is stored once every CTA has read that (the last to arrive does).
+  // Totals: from the CTA of the last run.  Where free_count_out is free_count,
+  // it is stored once every CTA has read that (the last to arrive does).
   if (tid == 0) {
     const int32_t left = (int32_t)max((int64_t)0, count - base);
+    const bool in_place = p.free_count_out == p.free_count && gridDim.x > 1;
     if (last_run) {
       p.status[0] = (int32_t)min((int64_t)0x7FFFFFFF, max((int64_t)0, base - count));
       p.status[1] = bad;
-      if (gridDim.x == 1) *p.free_count_out = left;
-      else p.status[3] = left;
+      if (in_place) p.status[3] = left;
+      else *p.free_count_out = left;
     }
-    if (gridDim.x > 1) {
+    if (in_place) {
       __threadfence();
       if (atomicAdd(p.status + 2, 1) == (int)gridDim.x - 1) {
         __threadfence();
@@ -224,8 +282,7 @@ int launch_block_tables(int num_req, const int32_t* query_start_loc, const int32
   p.width = block_table_stride;
   p.block_size = block_size;
   const int64_t ctas = num_tokens > kRun ? (num_tokens + kRun - 1) / kRun : 1;
-  block_tables_kernel<<<(unsigned)ctas, kThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
-  return cudaGetLastError() == cudaSuccess ? KVQ_OK : KVQ_E_CUDA;
+  return launch_dependent(block_tables_kernel, (unsigned)ctas, kThreads, stream, p);
 }
 
 }  // namespace kvq
