@@ -177,7 +177,9 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge,
 
   const int grp = warp / ge.hg, j = warp % ge.hg;  // the group, and the warp's head in it
   // ---- this warp's segment of the flat chunk sequence of its head -----------
-  const int glin = blockIdx.x * ge.gpc + grp;  // (segment, head group)
+  // (segment, head group): the SMs first, so that few segments have their
+  // own copy queue and warp schedulers each
+  const int glin = grp * gridDim.x + blockIdx.x;
   const int seg = glin / ge.hsplit, hgrp = glin % ge.hsplit;
   const int head = hgrp * ge.hg + j;
   const int gw = seg * p.heads_kv + head;
@@ -376,6 +378,11 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge,
   const float cap_l2 = cap * log2e;
   const float inv_cap = cap > 0.0f ? 1.0f / cap : 0.0f;
   const int G = p.group;
+  // r / G of a row r < G + kTileMaxRows (exact: r + 1/2 is half a row or more
+  // from a multiple of G).  An integer division here, two for each score of a
+  // piece's last chunk, took 6 us of a step of seven requests.
+  const float inv_g = 1.0f / (float)G;
+  auto div_g = [&](int r) -> int { return (int)(((float)r + 0.5f) * inv_g); };
   const int W = p.window;
   int cur = -1;                 // current piece, relative to the segment's first
   int all_lo = 0, all_hi = 0;   // tokens that all its rows see
@@ -412,7 +419,7 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge,
       pc.row0 = 0;
       pc.nrows = tiles[r].w;
       pc.len = tiles[r].z;
-      pc.pos0 = pc.len - pc.nrows / G;
+      pc.pos0 = pc.len - div_g(pc.nrows);
       pc.part = f0 < seg0 || f1 > seg0 + n ? (2 * gw + (f0 <= seg0 ? 0 : 1)) * kTileMaxRows : -1;
       pc.q0 = p.query_start_loc[r];
     } else {
@@ -423,12 +430,14 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge,
       pc.nrows = a.w;
       pc.part = b.x;
       pc.len = b.w;  // (all keys its rows see; without causality all keys)
-      pc.q0 = e.z;
-      pc.pos0 = e.w;
+      const int skip = pc.row0 > 0 ? pc.row0 / G : 0;  // whole query tokens before it
+      pc.row0 -= skip * G;
+      pc.q0 = e.z + skip;
+      pc.pos0 = e.w + skip;
     }
     pc.bad = false;
     if constexpr (KVQ_CHECKED && !DEV) {
-      pc.bad = pc.q0 < 0 || pc.q0 + (pc.row0 + pc.nrows - 1) / G >= p.total_q_tokens;
+      pc.bad = pc.q0 < 0 || pc.q0 + div_g(pc.row0 + pc.nrows - 1) >= p.total_q_tokens;
       if (pc.bad && lane == 0) atomicExch(p.error_flag, 2);
     }
     return pc;
@@ -439,8 +448,8 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge,
   auto start_piece = [&](int rel) {
     const Piece pc = piece_at(rel);
     const int q0 = pc.q0;
-    const int p_min = pc.pos0 + pc.row0 / G;
-    const int p_max = pc.pos0 + (pc.row0 + pc.nrows - 1) / G;
+    const int p_min = pc.pos0;
+    const int p_max = pc.pos0 + div_g(pc.row0 + pc.nrows - 1);
     len = pc.len;
     pos0 = pc.pos0;
     row0 = pc.row0;
@@ -454,8 +463,9 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge,
       const int nr = 8 * t + g;
       const bool valid = nr < pc.nrows && !pc.bad;
       const int R = pc.row0 + (valid ? nr : 0);
+      const int rq = div_g(R);
       const uint16_t* src =
-          p.q + ((int64_t)(q0 + R / G) * p.heads_q + head * G + R % G) * D + Row::kRun * c;
+          p.q + ((int64_t)(q0 + rq) * p.heads_q + head * G + R - rq * G) * D + Row::kRun * c;
 #pragma unroll
       for (int i = 0; i < D / 4 / Row::kRun; ++i) {
 #pragma unroll
@@ -497,8 +507,9 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge,
       for (int e = 0; e < 2; ++e) {
         const int nr = min(8 * t + 2 * c + e, pc.nrows - 1);
         if constexpr (AL) {
-          al_slope[t][e] = p.alibi_slopes[head * G + (pc.row0 + nr) % G] * log2e;
-          al_pos[t][e] = pos0 + (pc.row0 + nr) / G;
+          const int rq = div_g(pc.row0 + nr);
+          al_slope[t][e] = p.alibi_slopes[head * G + pc.row0 + nr - rq * G] * log2e;
+          al_pos[t][e] = pos0 + rq;
         }
         m_off[t][e] = kUnset;
         l_run[t][e] = 0.0f;
@@ -534,7 +545,7 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge,
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int nr = min(8 * t + 2 * c + e, pc.nrows - 1);
-          const float sk = p.sinks[head * G + (pc.row0 + nr) % G] * log2e;
+          const float sk = p.sinks[head * G + pc.row0 + nr - div_g(pc.row0 + nr) * G] * log2e;
           if (m_off[t][e] > kUnset && sk != -INFINITY)
             l_run[t][e] += exp2f(fminf(sk - m_off[t][e], 126.0f));
         }
@@ -547,10 +558,10 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge,
         if (nr >= pc.nrows) continue;
         const float l = l_run[t][e];
         const float sc = (l > 0.0f ? 1.0f / l : 0.0f) * unit;
-        const int R = pc.row0 + nr;
         if (pc.part < 0) {
           if (pc.bad) continue;
-          uint16_t* dst = p.out + ((int64_t)(q0 + R / G) * p.heads_q + head * G + R % G) * D + g * (D / 8);
+          const int R = pc.row0 + nr, rq = div_g(R);
+          uint16_t* dst = p.out + ((int64_t)(q0 + rq) * p.heads_q + head * G + R - rq * G) * D + g * (D / 8);
           // (the lane's group of D / 8 dims: m-tile i holds dims 2 i, 2 i + 1)
 #pragma unroll
           for (int i = 0; i < Row::kMtiles; i += 4)
@@ -744,7 +755,7 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge,
       if constexpr (AL)  // bias from the exact integer distance, after the cap
         v = fmaf(al_slope[t][e & 1], (float)(tok - al_pos[t][e & 1]), v);
       if (!full) {  // (rare: the edges of a request's keys) the column's own keys
-        const int pn = pos0 + min(row0 + 8 * t + 2 * c + (e & 1), row_end - 1) / G;
+        const int pn = pos0 + div_g(min(row0 + 8 * t + 2 * c + (e & 1), row_end - 1));
         const bool vis = ((live >> at) & 1u) && tok >= (W > 0 ? pn - W + 1 : 0) && tok < (p.causal ? pn + 1 : len);
         v = vis ? v : -INFINITY;
       }
@@ -907,8 +918,15 @@ int launch_int4_decode(const AttnParams& p, const PrefillMaps& maps, cudaStream_
   if (!int4_raise_smem(reinterpret_cast<const void*>(kern), raised)) return KVQ_E_CUDA;
   // A programmatic dependent of the kernel before it on the stream (it waits
   // for that one's completion after reading its plan).
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    cudaGetLastError();
+    return KVQ_E_CUDA;
+  }
+  const int groups = ge.segments * ge.hsplit, least = (groups + ge.gpc - 1) / ge.gpc;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((ge.segments * ge.hsplit + ge.gpc - 1) / ge.gpc));
+  cfg.gridDim = dim3((unsigned)(least > sms ? least : groups < sms ? groups : sms));
   cfg.blockDim = dim3((unsigned)(32 * ge.hg * ge.gpc));
   cfg.dynamicSmemBytes = ge.smem;
   cfg.stream = stream;
