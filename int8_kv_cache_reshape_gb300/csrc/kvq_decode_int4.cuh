@@ -401,6 +401,9 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge,
   int al_pos[NT][2];
   const int tok_g = i4::pi_of(g);  // MMA row g's token of a chunk; row g + 8's is the next
 
+  // 2^e, e in [-126, 127] (-127: zero)
+  auto exp2_int = [](int e) -> float { return __int_as_float((127 + e) << 23); };
+
   // A piece's descriptor (read again where it is needed: it does not stay in
   // registers) and its request's first query token.
   struct Piece {
@@ -536,7 +539,7 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge,
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1)
           l_run[t][e] += __shfl_xor_sync(0xffffffffu, l_run[t][e], off);
-    const float unit = ev > -1000 ? ldexpf(dev::kInt4Unit, ev) : 1.0f;
+    const float unit = ev > -1000 ? dev::kInt4Unit * exp2_int(ev) : 1.0f;
     // An attention sink joins the normaliser of a whole (uncut) tile here;
     // a cut tile's merge adds it once.
     if (p.sinks && pc.part < 0) {
@@ -761,29 +764,31 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge,
       }
       return v;
     };
-    float x[2][NT][4];
-    if (!AL && full && !(cap > 0.0f)) {
+    // (x: the weights' exponents, or, where a score takes more than a product,
+    // the scores until the reference has been settled)
+    const bool plain = !AL && full && !(cap > 0.0f);
+    float x[2][NT][4], xmax = -INFINITY;
+    if (plain) {
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[u][t][e] = fmaf(s[u][t][e], zm[u][e >> 1], -m_off[t][e & 1]);
+          for (int e = 0; e < 4; ++e) {
+            x[u][t][e] = fmaf(s[u][t][e], zm[u][e >> 1], -m_off[t][e & 1]);
+            xmax = fmaxf(xmax, x[u][t][e]);
+          }
     } else {
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[u][t][e] = score(u, t, e) - m_off[t][e & 1];
+          for (int e = 0; e < 4; ++e) {
+            x[u][t][e] = score(u, t, e);
+            xmax = fmaxf(xmax, x[u][t][e] - m_off[t][e & 1]);
+          }
     }
-    float xmax = x[0][0][0];
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) xmax = fmaxf(xmax, x[u][t][e]);
     const float sv_max = fmaxf(fmaxf(sv[0][0], sv[0][1]), fmaxf(sv[1][0], sv[1][1]));
     if (__any_sync(0xffffffffu, xmax > 14.0f || sv_max >= sv_lim)) {
       float mx = sv_max;
@@ -793,10 +798,10 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge,
       if (mx > 0.0f) {
         const int e = max(-100, min(100, (int)((__float_as_uint(mx) >> 23) & 0xFFu) - 127));
         if (e > ev) {
-          alpha_v = ev > -1000 ? ldexpf(1.0f, ev - e) : 0.0f;
+          alpha_v = exp2_int(max(ev - e, -127));
           ev = e;
-          to_ref = ldexpf(1.0f, -e);
-          sv_lim = ldexpf(1.0f, e + 1);
+          to_ref = exp2_int(-e);
+          sv_lim = exp2_int(e + 1);
         }
       }
 #pragma unroll
@@ -806,7 +811,10 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge,
         for (int e = 0; e < 2; ++e) {
           float z[4];
 #pragma unroll
-          for (int i2 = 0; i2 < 4; ++i2) z[i2] = score(i2 >> 1, t, e + 2 * (i2 & 1));
+          for (int i2 = 0; i2 < 4; ++i2) {
+            const int u = i2 >> 1, k = e + 2 * (i2 & 1);
+            z[i2] = plain ? s[u][t][k] * zm[u][k >> 1] : x[u][t][k];
+          }
           float cm = fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3]));
 #pragma unroll
           for (int off = 4; off < 32; off <<= 1) cm = fmaxf(cm, __shfl_xor_sync(0xffffffffu, cm, off));
@@ -827,6 +835,13 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge,
           o[t][i2][3] *= alpha[1] * alpha_v;
         }
       }
+    } else if (!plain) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[u][t][e] -= m_off[t][e & 1];
     }
 
     // O^T += V^T P^T : head_dim x 8 rows per n-tile.  The low halves of word
