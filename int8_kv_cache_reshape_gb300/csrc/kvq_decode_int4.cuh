@@ -270,8 +270,12 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge,
     return;
   }
   // Host plans are launched as programmatic dependents of whatever ran before
-  // on the stream: only the plan has been read so far.
-  if constexpr (!DEV) asm volatile("griddepcontrol.wait;" ::: "memory");
+  // on the stream: only the plan has been read so far.  Where that is the
+  // call's own prefill, nothing here depends on it, and all that it depends on
+  // was done when it started: the decode's CTAs take the SMs that its tail
+  // leaves idle, and wait for its end before their own (so that what follows
+  // the decode follows both).
+  if (!DEV && !p.beside_prefill) asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // ---- copies ----------------------------------------------------------------
   // Chunk k of the segment is copied by warp k mod hg of the group; a lane
@@ -636,7 +640,10 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge,
     }
     if ((int)rec.y != cur) {
       if (cur >= 0) finish_piece(cur);
-      if (i == n) return;
+      if (i == n) {
+        if (!DEV && p.beside_prefill) asm volatile("griddepcontrol.wait;" ::: "memory");
+        return;
+      }
       cur = (int)rec.y;
       start_piece(cur);
     }
@@ -905,6 +912,7 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge,
   }
   for (int s = 0; s < S; ++s)
     (void)tc::mbar_wait(meta + 32u * s + 16, s < kst ? kpar : kpar ^ 1u, 200000000LL);
+  if (!DEV && p.beside_prefill) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // The launches' shared memory limit, raised once per device.

@@ -1051,6 +1051,7 @@ int kvq_attention_with_kv_cache(const kvq_sched_t* s, int heads_q, int heads_kv,
     ctas = std::min<int64_t>(ctas, (int64_t)s->prefill.size());
     const int rc = kvq::launch_prefill(p, maps, s->dtype, head_dim, ctas, stream);
     if (rc != KVQ_OK) return rc;
+    p.beside_prefill = true;
   }
   for (int cls = 0; cls < 2; ++cls) {
     const DecodeLaunch& dl = s->launch[cls];
@@ -1066,6 +1067,7 @@ int kvq_attention_with_kv_cache(const kvq_sched_t* s, int heads_q, int heads_kv,
       return KVQ_E_CUDA;
     const int rc = kvq::launch_decode(p, maps, s->dtype, head_dim, cls + 1, stream);
     if (rc != KVQ_OK) return rc;
+    p.beside_prefill = false;
   }
   return kvq::launch_merge(p, dtype, head_dim, s->num_merges, stream);
 }

@@ -311,6 +311,7 @@ struct AttnParams {
   float sm_scale, soft_cap, k_scale, v_scale;
   const float* alibi_slopes;   // [Hq] or null: score += slope * (key - query position)
   const float* sinks;          // [Hq] or null: one extra logit in the softmax normaliser
+  bool beside_prefill;         // 4-bit decode: the kernel ahead of it is this call's prefill
 };
 
 // ---- fused decode step (cache write + device-built plan + decode) --------

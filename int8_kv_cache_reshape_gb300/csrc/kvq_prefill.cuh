@@ -343,6 +343,8 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
   const uint32_t raw = dev::smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* sm = smem_raw + (base - raw);
+  // (the 4-bit decode of the call may take the SMs that this grid leaves)
+  if constexpr (is_int4(DT)) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
   const int G = p.group;
