@@ -204,7 +204,7 @@ constexpr int kPrefillSlotRing = 4;
 // head_dim 64 (a V half of 32 dims is narrower than the 128-byte swizzle)
 // on single CTAs.
 KVQ_HD constexpr int prefill_cta_group(int dtype, int head_dim) {
-  return KVQ_PREFILL_PAIR && dtype != KVQ_AUTO && head_dim >= 128 ? 2 : 1;
+  return KVQ_PREFILL_PAIR && dtype != KVQ_AUTO && !is_int4(dtype) && head_dim >= 128 ? 2 : 1;
 }
 // Shared memory: 2 x K and 2 x V (keys x D f16 each, halves for a pair); 4 x
 // the tile's key / value scales; 4 x the tile's chunk mask and per-warp

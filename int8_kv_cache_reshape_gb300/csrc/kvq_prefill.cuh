@@ -23,10 +23,10 @@
 //     ahead).  bf16 ("auto") rows: bulk tensor copies (TMA) of the chunks
 //     straight into the K and V operand tiles.
 //   * Converter warps (1-3, and 8 up to the copy warp): a thread takes (key,
-//     16 codes) units, loads the codes from global memory one KV tile ahead,
-//     converts them exactly to f16 (every e4m3 / e5m2 / int8 value, and every
-//     4-bit code times its group's multiplier, is an f16 value; a 4-bit
-//     unit is 8 code bytes and its multipliers) and stores them as key-major rows in the 128-byte swizzle into a
+//     16 codes; 4-bit: 32 and their multipliers) units, loads the codes from
+//     global memory one KV tile ahead, converts them exactly to f16 (every e4m3 /
+//     e5m2 / int8 value, and every 4-bit code times its group's multiplier, is
+//     an f16 value) and stores them as key-major rows in the 128-byte swizzle into a
 //     two-stage K ring and V ring.  K is read by the tensor core K-major, V
 //     MN-major, so neither needs a transpose.  Step i converts K(i) (its
 //     buffer is free once S(i-2) is complete) and then V(i-1) (free once
@@ -241,20 +241,13 @@ __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, vol
   }
 }
 
-// 8 codes (two words; 4-bit: one word and its group's multiplier) -> 8 f16
-// (four f16x2 words), exact.
+// 8 codes (two words) -> 8 f16 (four f16x2 words), exact.
 template <int DT>
 __device__ __forceinline__ uint4 codes8_to_f16(uint32_t w0, uint32_t w1) {
-  if constexpr (is_int4(DT)) {
-    uint32_t v[4];
-    dev::int4_to_f16x2x4(w0, dev::int4_mul(dev::prmt(w1, 0x64646464u, 0x4040u)), v);
-    return make_uint4(v[0], v[1], v[2], v[3]);
-  } else {
-    uint4 h;
-    dev::word_to_f16x2x2<DT>(w0, h.x, h.y);
-    dev::word_to_f16x2x2<DT>(w1, h.z, h.w);
-    return h;
-  }
+  uint4 h;
+  dev::word_to_f16x2x2<DT>(w0, h.x, h.y);
+  dev::word_to_f16x2x2<DT>(w1, h.z, h.w);
+  return h;
 }
 
 // This CTA's k-th tile: the longest-first tile list dealt out over the grid
@@ -727,7 +720,11 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
     // converts its half of each tile: of K, keys [r * kN / 2, (r + 1) * kN / 2)
     // (rows of its K tile); of V, dims [r * D / 2, (r + 1) * D / 2) of every
     // key (columns of its V tile).
-    constexpr int kUnits = kN * D / 16 / CG;
+    // 4-bit rows: a unit is (key, 32 dims), 16 code bytes and the multipliers of
+    // their groups.  A thread keeps its 32 dims, and its units' keys differ by
+    // a multiple of 8, so that its offsets in the operand tile are constants.
+    constexpr bool kInt4 = Geo::kInt4;
+    constexpr int kUnits = kInt4 ? kN * D / 32 : kN * D / 16 / CG;
     constexpr int kSlots = (kUnits + Geo::kConv - 1) / Geo::kConv;
     constexpr int64_t kRow = row_bytes(DT, D);
     struct Units {
@@ -752,15 +749,50 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
       }
       return t;
     };
-    const Units uk = make_units(Geo::kKeysK, D / 16, (int)rank * Geo::kKeysK, 0);
+    struct Code4 {
+      uint4 w;     // four code words
+      uint32_t m;  // their multipliers: bytes 0-3 (D = 64), 0-1 (128), 0 (256)
+    };
+    using Code = std::conditional_t<kInt4, Code4, uint4>;
+    constexpr int kPieces = D / 32, kStepN = Geo::kConv / kPieces;  // (keys between a thread's units)
+    static_assert(!kInt4 || (CG == 1 && Geo::kConv % kPieces == 0 && kStepN % 8 == 0), "4-bit units");
+    const int pc4 = ctid % kPieces, n4 = ctid / kPieces;
+    // A unit's four 16-byte f16 chunks go out in the order i ^ x4, x4 by the
+    // 64-dim block, so that the 8 lanes of a quarter-warp are on 8 bank groups
+    // (D = 128: two keys of 4 pieces; 256: one key of 8; 64: one block).
+    constexpr int kXMask = D == 64 ? 0 : D == 128 ? 2 : 3;
+    const int x4 = D == 128 ? (pc4 >> 1) * 2 : (pc4 >> 1) & kXMask;
+    const uint32_t st4 = (uint32_t)((pc4 >> 1) * kN * 128 + n4 * 128);
+    const uint32_t chunk4 = (uint32_t)((4 * (pc4 & 1)) ^ (n4 & 7) ^ x4);
+    // multiplier selector of words 0 ^ x4 and 1 ^ x4 (f16 1024 + byte in both halves)
+    const uint32_t msel4 = D == 128 && x4 ? 0x4141u : 0x4040u;
+    const Units uk = kInt4 ? Units{} : make_units(Geo::kKeysK, D / 16, (int)rank * Geo::kKeysK, 0);
     const Units uv = CG == 1 ? uk : make_units(kN, Geo::kDimsV / 16, 0, (int)rank * Geo::kDimsV);
     const int32_t* table = reinterpret_cast<const int32_t*>(sm + Geo::kOffSlots);
     // Codes of KV tile g (slot table entry e, kv head `head`, live keys
     // [win & 0xFFFF, win >> 16) of the tile) into registers; returns the
     // tile's chunk mask.
     auto load_codes = [&](const Units& un, const uint8_t* cache, int e, int head, uint32_t win,
-                          uint4 (&dst)[kSlots]) {
+                          Code (&dst)[kSlots]) {
       const uint32_t valid = (uint32_t)table[e * 16 + 15];
+      if constexpr (kInt4) {
+        const uint8_t* from = cache + head * kRow + 16 * pc4;
+#pragma unroll
+        for (int i = 0; i < kSlots; ++i) {
+          dst[i].w = make_uint4(0, 0, 0, 0);
+          dst[i].m = 0;
+          const int n = n4 + i * kStepN;
+          if (n < kN && ((valid >> (n >> 4)) & 1u) && n >= (int)(win & 0xFFFFu) && n < (int)(win >> 16)) {
+            const uint8_t* at = from + (int64_t)(table[e * 16 + (n >> 4)] + (n & 15)) * (p.heads_kv * kRow);
+            dst[i].w = dev::ldg_stream(at);
+            const uint8_t* mul = at - 16 * pc4 + D / 2 + 4;
+            if constexpr (D == 64) dst[i].m = __ldg(reinterpret_cast<const uint32_t*>(mul + 4 * pc4));
+            else if constexpr (D == 128) dst[i].m = __ldg(reinterpret_cast<const uint16_t*>(mul + 2 * pc4));
+            else dst[i].m = __ldg(mul + pc4);
+          }
+        }
+        return valid;
+      } else {
 #pragma unroll
       for (int i = 0; i < kSlots; ++i) {
         dst[i] = make_uint4(0, 0, 0, 0);
@@ -768,21 +800,11 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
         if (ctid + i * Geo::kConv < kUnits && ((valid >> (n >> 4)) & 1u) && n >= (int)(win & 0xFFFFu) &&
             n < (int)(win >> 16)) {
           const int64_t slot = table[e * 16 + (n >> 4)] + (n & 15);
-          const uint8_t* row = cache + (slot * p.heads_kv + head) * kRow;
-          const uint32_t dim = un.code_off[i] & (D - 1);
-          if constexpr (Geo::kInt4) {
-            // {dims 0-7, their multiplier, dims 8-15, theirs} of the unit (the
-            // row's tail is a sector its codes' units bring in as well)
-            const uint2 w = dev::ldg_stream8(row + dim / 2);
-            const uint8_t* mul = row + D / 2 + 4 + dim / (D / 8);
-            const uint32_t m0 = __ldg(mul), m1 = D == 64 ? (uint32_t)__ldg(mul + 1) : m0;
-            dst[i] = make_uint4(w.x, m0, w.y, m1);
-          } else {
-            dst[i] = dev::ldg_stream(row + dim);
-          }
+          dst[i] = dev::ldg_stream(cache + (slot * p.heads_kv + head) * kRow + (un.code_off[i] & (D - 1)));
         }
       }
       return valid;
+      }
     };
     // Per token-head: key ctid's two scales (the fp32 after the codes; 0 for
     // a dead key), loaded with the tile's K codes.
@@ -798,7 +820,45 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
         }
       }
     };
-    auto convert = [&](const Units& un, uint32_t tile, const uint4 (&c)[kSlots]) {
+    auto convert = [&](const Units& un, uint32_t tile, const Code (&c)[kSlots]) {
+      if constexpr (kInt4) {
+#pragma unroll
+        for (int i = 0; i < kSlots; ++i) {
+          if (kN % kStepN != 0 && n4 + i * kStepN >= kN) break;
+          uint32_t w[4] = {c[i].w.x, c[i].w.y, c[i].w.z, c[i].w.w};
+          if constexpr ((kXMask & 2) != 0) {
+            const bool s2 = (x4 & 2) != 0;
+            const uint32_t a0 = s2 ? w[2] : w[0], a1 = s2 ? w[3] : w[1];
+            w[2] = s2 ? w[0] : w[2];
+            w[3] = s2 ? w[1] : w[3];
+            w[0] = a0;
+            w[1] = a1;
+          }
+          if constexpr ((kXMask & 1) != 0) {
+            const bool s1 = (x4 & 1) != 0;
+            const uint32_t a0 = s1 ? w[1] : w[0], a2 = s1 ? w[3] : w[2];
+            w[1] = s1 ? w[0] : w[1];
+            w[3] = s1 ? w[2] : w[3];
+            w[0] = a0;
+            w[2] = a2;
+          }
+          dev::Int4Mul f[4];
+          if constexpr (D == 64) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) f[q] = dev::int4_mul(dev::prmt(c[i].m, 0x64646464u, 0x4040u + 0x101u * q));
+          } else {
+            f[0] = f[1] = dev::int4_mul(dev::prmt(c[i].m, 0x64646464u, msel4));
+            f[2] = f[3] = D == 128 ? dev::int4_mul(dev::prmt(c[i].m, 0x64646464u, msel4 ^ 0x0101u)) : f[0];
+          }
+          const uint32_t at = tile + st4 + (uint32_t)(i * kStepN * 128);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t h[4];
+            dev::int4_to_f16x2x4(w[q], f[q], h);
+            sts128(at + ((chunk4 ^ (uint32_t)q) << 4), make_uint4(h[0], h[1], h[2], h[3]));
+          }
+        }
+      } else {
 #pragma unroll
       for (int i = 0; i < kSlots; ++i) {
         if (ctid + i * Geo::kConv < kUnits) {
@@ -806,6 +866,7 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
           sts128(tile + un.st_first[i], codes8_to_f16<DT>(odd ? c[i].z : c[i].x, odd ? c[i].w : c[i].y));
           sts128(tile + un.st_second[i], codes8_to_f16<DT>(odd ? c[i].x : c[i].z, odd ? c[i].y : c[i].w));
         }
+      }
       }
     };
     // The converted tile is visible to the tensor core (for a pair, the MMAs
@@ -823,7 +884,7 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
     // slot table g is released.
     KvCursor<kN, CG> ck;
     ck.start(p);
-    uint4 ka[kSlots], vb[kSlots];
+    Code ka[kSlots], vb[kSlots];
     float ks_a = 0.0f, vs_a = 0.0f;
     uint32_t valid_a = 0, win_a = 0;
     bool ok = true;
