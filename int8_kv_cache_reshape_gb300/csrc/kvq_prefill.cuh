@@ -971,29 +971,61 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
     const float cap_l2 = cap * log2e;
     const float inv_cap = cap > 0.0f ? 1.0f / cap : 0.0f;
     const int W = p.window;
-    // Output row m of a tile, bf16: D values from `dst` (null: not a row).
-    auto out_row = [&](const PrefillTile& t) -> uint16_t* {
-      if (m >= t.nrows) return nullptr;
-      const int Rr = t.row0 + m;
-      return p.out + ((int64_t)(t.q0 + Rr / G) * p.heads_q + t.kv_head * G + Rr % G) * D;
+    // Tile records: word i of this CTA's tile in lane i, of the pair's other
+    // tile in lane 8 + i; one register each, loaded two tiles ahead (read from
+    // memory where they were used, a tile waited for five round trips).
+    enum { kWordHead = 1, kWordRow0, kWordRows, kWordLo, kWordHi, kWordQ0, kWordPos0 };
+    const int lane = tid & 31;
+    int rec_k = -1;  // the ordinal whose record is on its way in `coming`
+    uint32_t coming = 0;
+    bool more = true;
+    auto fetch_record = [&]() {
+      const int idx = dealt_tile<CG>(++rec_k);
+      more = idx < p.num_prefill_tiles;
+      coming = more && lane < 8 * CG
+                   ? __ldg(reinterpret_cast<const uint32_t*>(p.prefill_tiles + (idx ^ (lane >> 3))) + (lane & 7))
+                   : 0u;
     };
-    // Tiles without keys (an empty key range) get zero rows as they are passed.
-    auto zero_rows = [&](const PrefillTile& t) {
-      uint16_t* dst = out_row(t);
-      if (dst)
-        for (int c = 0; c < D / 8; ++c) reinterpret_cast<uint4*>(dst)[c] = make_uint4(0, 0, 0, 0);
+    auto word = [&](uint32_t rec, int i) -> int { return (int)__shfl_sync(0xffffffffu, rec, i); };
+    // the keys of the tile's run (a pair's: the union of both ranges)
+    auto key_lo = [&](uint32_t rec) -> int {
+      const int lo = word(rec, kWordLo);
+      return CG == 2 ? min(lo, word(rec, 8 + kWordLo)) : lo;
     };
-    // Next tile with keys after ordinal k (k moves to it); false: none.
-    auto next_run = [&](int& k, TileRun<kN>& r) -> bool {
-      while (true) {
-        const int idx = dealt_tile<CG>(++k);
-        if (idx >= p.num_prefill_tiles) return false;
-        PrefillTile x, y;
-        load_tiles<CG>(p, idx, x, y);
-        r.set(x, y);
-        if (r.T > 0) return true;
-        zero_rows(r.t);
+    auto key_hi = [&](uint32_t rec) -> int {
+      const int hi = word(rec, kWordHi);
+      return CG == 2 ? max(hi, word(rec, 8 + kWordHi)) : hi;
+    };
+    // r / G and r % G of a packed row (an integer division costs 30 instructions)
+    const uint32_t gdiv = 0xFFFFFFFFu / (uint32_t)G;
+    auto div_g = [&](int r, int& rem) -> int {
+      uint32_t q = __umulhi((uint32_t)r, gdiv);
+      uint32_t x = (uint32_t)r - q * (uint32_t)G;
+      if (x >= (uint32_t)G) {
+        ++q;
+        x -= (uint32_t)G;
       }
+      rem = (int)x;
+      return (int)q;
+    };
+    // Row m of a tile in q and out: its first element.
+    auto row_at = [&](uint32_t rec) -> int64_t {
+      int rem;
+      const int tok = div_g(word(rec, kWordRow0) + m, rem);
+      return ((int64_t)(word(rec, kWordQ0) + tok) * p.heads_q + word(rec, kWordHead) * G + rem) * D;
+    };
+    // The next tile with keys (false: none); tiles without keys (an empty key
+    // range) get zero rows as they are passed.
+    auto next_record = [&](uint32_t& rec) -> bool {
+      while (more) {
+        rec = coming;
+        fetch_record();
+        if (key_hi(rec) > (key_lo(rec) / kN) * kN) return true;
+        const int64_t at = row_at(rec);
+        if (m < word(rec, kWordRows))
+          for (int c = 0; c < D / 8; ++c) reinterpret_cast<uint4*>(p.out + at)[c] = make_uint4(0, 0, 0, 0);
+      }
+      return false;
     };
     // Q rows of a tile are staged in shared memory a tile ahead: each thread
     // copies its row of the next tile (one bulk copy, completing on the
@@ -1001,14 +1033,14 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
     // from the previous tile's bulk store until this tile's epilogue.  Rows
     // past the tile's end copy nothing.
     const uint32_t srow = base + Geo::kOffOut + (uint32_t)(m * Geo::kOutPitch);
-    auto stage_q = [&](const PrefillTile& t) {
-      const bool valid = m < t.nrows;
+    auto stage_q = [&](uint32_t rec) {
+      const int64_t from = row_at(rec);
+      const bool valid = m < word(rec, kWordRows);
       // (this thread's previous bulk store has read its staging row)
       asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
       mbar_arrive_expect_tx(bar(Geo::kBarQStage), valid ? (uint32_t)(D * 2) : 0u);
       if (valid) {
-        const int Rq = t.row0 + m;
-        const uint16_t* src = p.q + ((int64_t)(t.q0 + Rq / G) * p.heads_q + t.kv_head * G + Rq % G) * D;
+        const uint16_t* src = p.q + from;
         asm volatile(
             "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
             :: "r"(srow), "l"(reinterpret_cast<uint64_t>(src)), "n"(D * 2), "r"(bar(Geo::kBarQStage))
@@ -1028,13 +1060,17 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
       (void)__all_sync(0xffffffffu, wait_or_abort(bar(Geo::kBarQStage), (uint32_t)(n_tile & 1), abort_flag));
       int emax = 0;
       if (valid && !Geo::kAuto) {
+        uint32_t big[4] = {0, 0, 0, 0};  // maxima of |q|'s bits, two a word
 #pragma unroll 8
         for (int c = 0; c < D / 8; ++c) {
           const uint4 x4 = lds128(srow + (uint32_t)(16 * c));
-          const uint32_t x[4] = {x4.x, x4.y, x4.z, x4.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) emax = max(emax, (int)max((x[e] >> 7) & 0xFFu, (x[e] >> 23) & 0xFFu));
+          big[0] = __vmaxu2(big[0], x4.x & 0x7FFF7FFFu);
+          big[1] = __vmaxu2(big[1], x4.y & 0x7FFF7FFFu);
+          big[2] = __vmaxu2(big[2], x4.z & 0x7FFF7FFFu);
+          big[3] = __vmaxu2(big[3], x4.w & 0x7FFF7FFFu);
         }
+        const uint32_t b = __vmaxu2(__vmaxu2(big[0], big[1]), __vmaxu2(big[2], big[3]));
+        emax = (int)(max(b & 0xFFFFu, b >> 16) >> 7);
       }
       // largest |q| < 2^(emax - 126): scaled into [2^13, 2^14)
       const int sh = emax == 0 || Geo::kAuto ? 0 : min(140 - emax, 126);
@@ -1058,39 +1094,33 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
       return ldexpf(1.0f, -sh);
     };
 
-    TileRun<kN> cur;
-    int k = -1;
-    bool have = next_run(k, cur);
-    if (have) stage_q(cur.t);
-    float q_unscale = have ? load_q(cur.t.nrows, 0) : 1.0f;
+    uint32_t rec = 0, rec_next = 0;
+    fetch_record();
+    bool have = next_record(rec);
+    if (have) stage_q(rec);
+    float q_unscale = have ? load_q(word(rec, kWordRows), 0) : 1.0f;
     bool ok = true;
     int g = 0;
     int staged = 0;  // tiles whose Q was staged
     if (have) staged = 1;
     for (int n = 0; have; ++n) {
-      // The next tile with keys (its record is read again when its Q is
-      // staged and after this tile's loop, from L1: only its ordinal stays
-      // in registers).
-      int k2 = k;
-      {
-        TileRun<kN> nxt;
-        if (!next_run(k2, nxt)) k2 = -1;
-      }
+      // The next tile with keys.
+      const bool have_next = next_record(rec_next);
       // the next tile's Q rows into the staging area (free from this
       // thread's previous bulk store until this tile's epilogue)
-      if (k2 >= 0) {
-        stage_q(p.prefill_tiles[dealt_tile<CG>(k2)]);
+      if (have_next) {
+        stage_q(rec_next);
         ++staged;
       }
       float q_next = 1.0f;
-      const PrefillTile& t = cur.t;
-      const int kv_first = cur.kv_first, T = cur.T;
-      const bool row_valid = m < t.nrows;
-      const int R = t.row0 + (row_valid ? m : 0);
-      const int pos = t.pos0 + R / G;
-
+      const int kv_first = (key_lo(rec) / kN) * kN, T = (key_hi(rec) - kv_first + kN - 1) / kN;
+      const bool row_valid = m < word(rec, kWordRows);
+      int row_g;  // the row's head in its group
+      const int pos = word(rec, kWordPos0) + div_g(word(rec, kWordRow0) + (row_valid ? m : 0), row_g);
+      const int head_q = word(rec, kWordHead) * G + row_g;
+      const int own_hi = word(rec, kWordHi);
       // (without causality every row sees the request's L keys: the tile's kv_hi)
-      const int row_hi = row_valid ? (p.causal ? pos + 1 : t.kv_hi) : 0;  // padding rows see nothing
+      const int row_hi = row_valid ? (p.causal ? pos + 1 : own_hi) : 0;  // padding rows see nothing
       const int row_lo = W > 0 ? pos - W + 1 : 0;
       // scores in log2 units (natural units under a soft cap, which converts)
       // (4-bit rows enter the MMAs as multiples of 1 / kInt4Unit)
@@ -1100,7 +1130,7 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
                                         (Geo::kPth || Geo::kAuto ? 1.0f : p.k_scale);
       // ALiBi: this row's slope in log2 units (the bias uses the exact integer
       // distance key - position, added after the soft cap).
-      const float al_slope = AL ? p.alibi_slopes[t.kv_head * G + R % G] * log2e : 0.0f;
+      const float al_slope = AL ? p.alibi_slopes[head_q] * log2e : 0.0f;
       // m_ref: the reference maximum, an integer (log2 units) once set, so
       // that moving it scales weights, O and l by exact powers of two.
       float m_ref = -INFINITY, l_sum = 0.0f;
@@ -1117,7 +1147,7 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
         tc::fence_after_sync();
         // S(g), this tile's last, is complete: Q's tensor memory takes the
         // next tile's Q now, so that its first S runs beside this softmax.
-        if (j == T - 1 && k2 >= 0) q_next = load_q(p.prefill_tiles[dealt_tile<CG>(k2)].nrows, n + 1);
+        if (j == T - 1 && have_next) q_next = load_q(word(rec_next, kWordRows), n + 1);
         const uint32_t tmem_s = tmem + Geo::kColS + (uint32_t)(st * kN) + lane_base;
         // Visible keys n of this row: lo_n <= n < hi_n, in a 16-key chunk
         // that was copied.  Masks are needed unless every row of the warp
@@ -1133,7 +1163,15 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
 #pragma unroll
           for (int w = 0; w < kVMaxSlots; ++w) mb = max(mb, vmaxw[sd * 8 + w]);
           const float smax = __uint_as_float(mb);
-          if (smax > 0.0f) {
+          if constexpr (Geo::kInt4) {
+            if (mb != 0u) {  // 2^e above the largest scale, by its exponent bits
+              const int e = max(-100, min(100, (int)(mb >> 23) - 126));
+              if (e > ev) {
+                if (ev > -1000) alpha = __int_as_float((127 + max(ev - e, -127)) << 23);
+                ev = e;
+              }
+            }
+          } else if (smax > 0.0f) {
             int e;
             (void)frexpf(smax, &e);  // smax < 2^e
             if (e > ev) {
@@ -1142,7 +1180,8 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
             }
           }
           // (no positive scale yet: every value so far is zero)
-          v_mul = ev > -1000 ? ldexpf(1.0f, -ev) : 0.0f;
+          if constexpr (Geo::kInt4) v_mul = ev > -1000 ? __int_as_float((127 - ev) << 23) : 0.0f;
+          else v_mul = ev > -1000 ? ldexpf(1.0f, -ev) : 0.0f;
         }
         auto score = [&](auto cap_c, float r) -> float {
           if constexpr (decltype(cap_c)::value)
@@ -1153,11 +1192,10 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
         // 64 scores from column c0: r in place, the row's maximum of r.  With
         // ALiBi the bias differs per key, so the final scores (log2 units) are
         // stored and maximised instead.
-        auto raw64 = [&](auto full_c, uint32_t* v, int c0) -> float {
+        auto raw64 = [&](uint32_t* v, int c0) -> float {
           const float* skp = sk + sd * kN + c0;
-          const int lo = lo_n - c0, hi = hi_n - c0;
-          const uint32_t cm = cmask >> (c0 >> 4);
           const int dist0 = kv0 + c0 - pos;  // key - position of column c0
+          const float dist0f = (float)dist0;
           float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
   #pragma unroll
           for (int e = 0; e < 64; e += 2) {
@@ -1175,17 +1213,33 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
                 r0 *= score_mul;
                 r1 *= score_mul;
               }
-              r0 = fmaf(al_slope, (float)(dist0 + e), r0);
-              r1 = fmaf(al_slope, (float)(dist0 + e + 1), r1);
-            }
-            if constexpr (!decltype(full_c)::value) {
-              const bool in = (cm >> (e >> 4)) & 1u;
-              r0 = in && e >= lo && e < hi ? r0 : -INFINITY;
-              r1 = in && e + 1 >= lo && e + 1 < hi ? r1 : -INFINITY;
+              // (4-bit: the distance by an addition, exact up to 2^24 keys; a
+              // conversion each goes through the unit of the exponentials)
+              r0 = fmaf(al_slope, Geo::kInt4 ? dist0f + (float)e : (float)(dist0 + e), r0);
+              r1 = fmaf(al_slope, Geo::kInt4 ? dist0f + (float)(e + 1) : (float)(dist0 + e + 1), r1);
             }
             v[e] = __float_as_uint(r0);
             v[e + 1] = __float_as_uint(r1);
             mx4[(e >> 1) & 3] = fmaxf(mx4[(e >> 1) & 3], fmaxf(r0, r1));
+          }
+          if (!full) {
+            // Masked: the round's visible keys, a bit each (comparisons for each
+            // key cost a masked tile more than twice a full one), in a pass of
+            // its own that full tiles do not take.
+            mx4[0] = mx4[1] = mx4[2] = mx4[3] = -INFINITY;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int lo = min(max(lo_n - c0 - 32 * h, 0), 32), hi = min(max(hi_n - c0 - 32 * h, 0), 32);
+              const uint32_t cm = cmask >> ((c0 >> 4) + 2 * h);
+              uint32_t seen = hi > lo ? (0xFFFFFFFFu << lo) & (0xFFFFFFFFu >> (32 - hi)) : 0u;
+              seen &= (cm & 1u ? 0xFFFFu : 0u) | (cm & 2u ? 0xFFFF0000u : 0u);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const float r = (seen >> e) & 1u ? __uint_as_float(v[32 * h + e]) : -INFINITY;
+                v[32 * h + e] = __float_as_uint(r);
+                mx4[e & 3] = fmaxf(mx4[e & 3], r);
+              }
+            }
           }
           return fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
         };
@@ -1240,7 +1294,7 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
           tc::tmem_ld32(tmem_s + c0, *reinterpret_cast<uint32_t(*)[32]>(v));
           tc::tmem_ld32(tmem_s + c0 + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
           tc::tmem_wait_ld();
-          const float mr = full ? raw64(std::true_type{}, v, c0) : raw64(std::false_type{}, v, c0);
+          const float mr = raw64(v, c0);
           // the score is monotonic in r (score_mul > 0, tanh increasing); with
           // ALiBi mr is the largest final score already
           const float mx = AL ? mr : cap > 0.0f ? score(std::true_type{}, mr) : score(std::false_type{}, mr);
@@ -1327,12 +1381,6 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
       if (!ok) break;
       // (the next tile's Q is in tensor memory: loaded at this tile's last
       // KV tile)
-      TileRun<kN> nxt;
-      if (k2 >= 0) {
-        PrefillTile x, y;
-        load_tiles<CG>(p, dealt_tile<CG>(k2), x, y);
-        nxt.set(x, y);
-      }
       // ---- epilogue: O / l -> bf16 rows in shared memory; then O is free
       // for the next tile's first P V, and each row goes to global memory by
       // one bulk copy of its thread (coalesced, asynchronous).
@@ -1341,13 +1389,11 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
       tc::fence_after_sync();
       // An attention sink joins the normaliser (the weights carry
       // 2^-(m_ref - 6)).
-      // (this tile's record again, from L1: not kept in registers over the loop)
-      const PrefillTile te = p.prefill_tiles[dealt_tile<CG>(k)];
-      if (p.sinks && m < te.nrows && m_ref != -INFINITY) {
-        const float skl = p.sinks[te.kv_head * G + (te.row0 + m) % G] * log2e;
+      if (p.sinks && row_valid && m_ref != -INFINITY) {
+        const float skl = p.sinks[head_q] * log2e;
         if (skl != -INFINITY) l_sum += exp2f(fminf(skl - m_ref + 6.0f, 126.0f));
       }
-      uint16_t* const dst = out_row(te);
+      uint16_t* const dst = p.out + row_at(rec);
       const float sc = (l_sum > 0.0f ? 1.0f / l_sum : 0.0f) *
                        (Geo::kPth ? (ev > -1000 ? ldexpf(Geo::kInt4 ? dev::kInt4Unit : 1.0f, ev) : 0.0f)
                         : Geo::kAuto ? 1.0f : p.v_scale);
@@ -1384,15 +1430,14 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
       }
       tc::fence_before_sync();
       warp_arrive_mma<CG>(bar(Geo::kBarOFree), rank);
-      if (dst) {
+      if (row_valid) {
         tc::fence_async_smem();
         asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n\t"
                      "cp.async.bulk.commit_group;"
                      :: "l"(reinterpret_cast<uint64_t>(dst)), "r"(orow), "n"(D * 2) : "memory");
       }
-      cur = nxt;
-      k = k2;
-      have = k2 >= 0;
+      rec = rec_next;
+      have = have_next;
       q_unscale = q_next;
     }
     // The rows' bulk copies are complete before the shared memory goes (and
