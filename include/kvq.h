@@ -255,8 +255,8 @@ KVQ_API int kvq_build_block_tables(int num_req, const int32_t* query_start_loc,
  * otherwise and does not synchronise: the first attention call made with
  * the schedule uploads the plan with an asynchronous copy on that call's
  * stream, ahead of its kernels.  Requests with at most 16
- * (query, head) rows per kv head (decodes) form row tiles whose 16-token KV
- * chunks are cut into equal contiguous segments, one per warp, so long
+ * (query, head) rows per kv head (decodes) form row tiles whose KV chunks
+ * (16 tokens; 32 of 4-bit rows) are cut into equal contiguous segments, one per warp, so long
  * contexts are split along the KV axis and merged.  Requests with more rows
  * (prefills) form 128-row tiles for the tensor-core prefill kernel. */
 KVQ_API int kvq_get_scheduler_metadata(int num_req, int heads_q, int heads_kv,
@@ -530,7 +530,8 @@ typedef struct {
   int64_t num_tiles;           /* row tiles: <= 16 (query, head) rows of a kv head */
   int64_t num_pieces;          /* tile pieces (a tile cut among warps)        */
   int64_t num_merge_items;     /* tiles cut into more than one piece          */
-  int64_t num_chunks;          /* 16-token KV chunks streamed in total        */
+  int64_t num_chunks;          /* KV chunks streamed in total (16 tokens; 32 of
+                                  4-bit rows)                                  */
   int64_t num_decode_warps;    /* warps the chunk sequence is cut among       */
   int64_t max_splits;          /* most pieces of one tile                     */
   int64_t total_query_tokens;
@@ -552,8 +553,8 @@ KVQ_API int kvq_sched_get_info(const kvq_sched_t* sched, kvq_sched_info_t* out);
  * [P2] Breakdown item 1: the schedule is the single source of the tile and
  * scratch sizes the kernels run with; these calls expose it for checking.
  *
- * A decode piece is a run of consecutive 16-token chunks of one row tile
- * (<= 16 packed rows of one kv head), streamed by one warp.  The pieces of a
+ * A decode piece is a run of consecutive chunks (16 tokens; 32 of 4-bit
+ * rows) of one row tile (<= 16 packed rows of one kv head), streamed by one warp.  The pieces of a
  * launch class lie end to end in its flat chunk sequence, which is cut into
  * contiguous segments, one per warp (stream-K: segment w starts at
  * floor(w * chunks / warps)); a tile cut by a segment boundary has several
@@ -563,7 +564,9 @@ KVQ_API int kvq_sched_get_info(const kvq_sched_t* sched, kvq_sched_info_t* out);
  * a warp count that is a multiple of the kv heads (Hkv), every head's run cut
  * at the same chunks, and segment h * (warps / Hkv) + v on warp v * Hkv + h,
  * so the warps reading neighbouring heads' rows of the same tokens -- which
- * share 128-byte lines -- are neighbours and run side by side. */
+ * share 128-byte lines -- are neighbours and run side by side.  4-bit rows are
+ * always in head lockstep, every segment with a warp per kv head: warps / Hkv
+ * segments, the kv heads of segment v on warps v * Hkv .. v * Hkv + Hkv - 1. */
 typedef struct {
   int32_t launch;          /* decode launch class: 0 (tiles of <= 8 rows) or 1 */
   int32_t req, kv_head, row0, nrows;
@@ -571,7 +574,7 @@ typedef struct {
   int32_t merge;           /* merge item of a cut tile; -1: not cut */
   int32_t key_lo, key_hi;  /* keys some row of the tile can see: [key_lo, key_hi) */
   int32_t flat0;           /* the piece's first position in its class's chunk sequence */
-  int32_t chunk0;          /* that chunk's 16-token index within the request */
+  int32_t chunk0;          /* that chunk's index within the request */
   int32_t nchunks;         /* chunks in the piece */
 } kvq_plan_piece_t;
 

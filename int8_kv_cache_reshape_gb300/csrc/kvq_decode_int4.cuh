@@ -19,10 +19,11 @@
 //     predicate or register in the consumers.  (Copies a token at a time
 //     reached the copy engine's rate, not the memory's: a 640-byte copy
 //     every 40-50 cycles of an SM, 375 us against 243 for 32 x 32768 keys.)
-//   * No producer warp: the warps of a group issue the copies in turn (chunk
-//     k by warp k mod Hg), two chunks behind the ring's end, so that the
-//     wait for the slot's last readers is over before it is asked for.
-//     Records (slots, masks) are prepared by the lanes 32 turns at a time.
+//   * No producer warp (a ninth costs as many registers as three more): the
+//     warps of a group issue the copies in turn, chunk k by warp k mod Hg, a
+//     chunk behind the ring's end, so that the wait for the slot's last
+//     readers is over before it is asked for.  Records (slots, masks) are
+//     prepared by the lanes, kInt4Turns turns at a time.
 //   * The copies write the 128-byte swizzle, and MMA row g is token pi(g) =
 //     {0,4,2,6,12,8,14,10}[g] of a half (row g + 8 the token after it): with 8
 //     heads (5 lines a token) K's 16-byte reads (eight lanes: two rows) and
@@ -32,6 +33,10 @@
 //     records, masks and votes once for two sets of MMAs.
 //   * The lazy reference maximum and the value scales' power-of-two reference
 //     move on one warp vote; the common chunk has no shuffle.
+// Measured: 64 requests of 1,024 to 4,096 keys (32 q and 8 kv heads of 128) in
+// 48 us with the merge, 179 MB at 3.7 TB/s (the first data comes 7 us after
+// the launch, the merge takes 4); 32 requests of 32,768 keys in 231 us, 5.8
+// TB/s, 87 % of a plain copy's rate.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -278,8 +283,7 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge,
   if (!DEV && !p.beside_prefill) asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // ---- copies ----------------------------------------------------------------
-  // Chunk k of the segment is copied by warp k mod hg of the group; a lane
-  // holds the record of one of its warp's next 32 turns.
+  // Chunk k of the segment is copied by warp k mod hg of the group.
   const int S = ge.stages, ahead = S - 1;
   const int tok_bytes = ge.hg * Row::kRow;  // a token's rows of the group
   const uint32_t v_off = 2u * ge.half_bytes;  // V's rows in a stage
@@ -382,7 +386,7 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge,
   const float cap_l2 = cap * log2e;
   const float inv_cap = cap > 0.0f ? 1.0f / cap : 0.0f;
   const int G = p.group;
-  // r / G of a row r < G + kTileMaxRows (exact: r + 1/2 is half a row or more
+  // r / G of a tile's row (r < kTileMaxRows; exact: r + 1/2 is half a row or more
   // from a multiple of G).  An integer division here, two for each score of a
   // piece's last chunk, took 6 us of a step of seven requests.
   const float inv_g = 1.0f / (float)G;
@@ -437,10 +441,8 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge,
       pc.nrows = a.w;
       pc.part = b.x;
       pc.len = b.w;  // (all keys its rows see; without causality all keys)
-      const int skip = pc.row0 > 0 ? pc.row0 / G : 0;  // whole query tokens before it
-      pc.row0 -= skip * G;
-      pc.q0 = e.z + skip;
-      pc.pos0 = e.w + skip;
+      pc.q0 = e.z;
+      pc.pos0 = e.w;
     }
     pc.bad = false;
     if constexpr (KVQ_CHECKED && !DEV) {
