@@ -545,7 +545,7 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge,
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1)
           l_run[t][e] += __shfl_xor_sync(0xffffffffu, l_run[t][e], off);
-    const float unit = ev > -1000 ? dev::kInt4Unit * exp2_int(ev) : 1.0f;
+    const float unit = ev > -1000 ? exp2_int(ev) : 1.0f;
     // An attention sink joins the normaliser of a whole (uncut) tile here;
     // a cut tile's merge adds it once.
     if (p.sinks && pc.part < 0) {
@@ -566,7 +566,8 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge,
         const int nr = 8 * t + 2 * c + e;
         if (nr >= pc.nrows) continue;
         const float l = l_run[t][e];
-        const float sc = (l > 0.0f ? 1.0f / l : 0.0f) * unit;
+        // (l >= 2^6: no step of this passes 2^128)
+        const float sc = (l > 0.0f ? dev::kInt4Unit / l : 0.0f) * unit;
         if (pc.part < 0) {
           if (pc.bad) continue;
           const int R = pc.row0 + nr, rq = div_g(R);
@@ -805,7 +806,8 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge,
       for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
       float alpha_v = 1.0f;
       if (mx > 0.0f) {
-        const int e = max(-100, min(100, (int)((__float_as_uint(mx) >> 23) & 0xFFu) - 127));
+        // (a finite row's scale is below 2^119)
+        const int e = max(-126, min(118, (int)((__float_as_uint(mx) >> 23) & 0xFFu) - 127));
         if (e > ev) {
           alpha_v = exp2_int(max(ev - e, -127));
           ev = e;

@@ -1165,7 +1165,7 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
           const float smax = __uint_as_float(mb);
           if constexpr (Geo::kInt4) {
             if (mb != 0u) {  // 2^e above the largest scale, by its exponent bits
-              const int e = max(-100, min(100, (int)(mb >> 23) - 126));
+              const int e = max(-125, min(119, (int)(mb >> 23) - 126));
               if (e > ev) {
                 if (ev > -1000) alpha = __int_as_float((127 + max(ev - e, -127)) << 23);
                 ev = e;
@@ -1394,9 +1394,15 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
         if (skl != -INFINITY) l_sum += exp2f(fminf(skl - m_ref + 6.0f, 126.0f));
       }
       uint16_t* const dst = p.out + row_at(rec);
-      const float sc = (l_sum > 0.0f ? 1.0f / l_sum : 0.0f) *
-                       (Geo::kPth ? (ev > -1000 ? ldexpf(Geo::kInt4 ? dev::kInt4Unit : 1.0f, ev) : 0.0f)
-                        : Geo::kAuto ? 1.0f : p.v_scale);
+      // (4-bit: kInt4Unit 2^ev / l in two factors, since l is 2^5 or more and a
+      // value up to 2^128: 2^up last)
+      const int up = Geo::kInt4 && ev > 100 ? 20 : 0;
+      const float sc_up = Geo::kInt4 ? __int_as_float((127 + up) << 23) : 1.0f;
+      const float sc = (l_sum > 0.0f ? (Geo::kInt4 ? dev::kInt4Unit : 1.0f) / l_sum : 0.0f) *
+                       (Geo::kInt4   ? (ev > -1000 ? __int_as_float((127 + ev - up) << 23) : 0.0f)
+                        : Geo::kPth  ? (ev > -1000 ? ldexpf(1.0f, ev) : 0.0f)
+                        : Geo::kAuto ? 1.0f
+                                     : p.v_scale);
       // (the previous tile's bulk copy of this row has read its staging row)
       asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
       const uint32_t orow = base + Geo::kOffOut + (uint32_t)(m * Geo::kOutPitch);
@@ -1406,11 +1412,14 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
       auto stage32 = [&](const uint32_t (&v)[32], int c0) {
 #pragma unroll
         for (int e = 0; e < 32; e += 8) {
-          uint4 o;
-          o.x = dev::pack_bf16x2(__uint_as_float(v[e]) * sc, __uint_as_float(v[e + 1]) * sc);
-          o.y = dev::pack_bf16x2(__uint_as_float(v[e + 2]) * sc, __uint_as_float(v[e + 3]) * sc);
-          o.z = dev::pack_bf16x2(__uint_as_float(v[e + 4]) * sc, __uint_as_float(v[e + 5]) * sc);
-          o.w = dev::pack_bf16x2(__uint_as_float(v[e + 6]) * sc, __uint_as_float(v[e + 7]) * sc);
+          float f[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            f[i] = __uint_as_float(v[e + i]) * sc;
+            if constexpr (Geo::kInt4) f[i] *= sc_up;
+          }
+          const uint4 o = make_uint4(dev::pack_bf16x2(f[0], f[1]), dev::pack_bf16x2(f[2], f[3]),
+                                     dev::pack_bf16x2(f[4], f[5]), dev::pack_bf16x2(f[6], f[7]));
           sts128(orow + (uint32_t)((c0 + e) * 2), o);
         }
       };

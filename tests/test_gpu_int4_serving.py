@@ -279,3 +279,95 @@ def test_requests_without_new_tokens_and_padded_rows(cuda_device):
     torch.cuda.synchronize()
     assert torch.equal(_bits(out[: -pad]), _bits(want))
     assert torch.all(out[-pad:] == 7.0)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("mul", [2.0 ** 120, 2.0 ** 125, 2.0 ** -110])
+def test_largest_and_smallest_values(cuda_device, D, mul):
+    """Value rows at both ends of bf16's range (scales up to 2^118), whole and
+    cut tiles, decode and prefill rows, among them a request of one key."""
+    wl = W.custom("int4-range", [1, 30, 1, 1, 40], [1, 90, 77, 3000, 40], 8, 2, D, 16, DT, 830 + D)
+    # (|x| < 6: the largest finite bf16 is 2^128 (1 - 2^-8))
+    wl.value = (wl.value.float().clamp(-5.5, 5.5) * mul).to(torch.bfloat16)
+    assert torch.isfinite(wl.value.float()).all()
+    g = GpuRun(wl).write_cache()
+    kc, vc = oracle_cache(wl)
+    assert np.array_equal(g.vc.cpu().numpy(), vc)
+    g.attention()
+    ref, bnd = oracle_reference(wl, kc, vc)
+    out = g.out_f32()
+    assert np.isfinite(out).all()
+    if mul > 1:
+        assert_attention_close(out, ref, wl.name, bnd)
+    else:
+        # the bound of _harness.py, without its absolute floor of 1e-2
+        tol = np.abs(ref) * 2.0 ** -8 + 2 * bnd + 2.0 ** -133
+        assert (np.abs(out - ref) <= tol).all()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_step_at_the_largest_values(cuda_device, D):
+    wl = W.custom("int4-range-step", [1, 2, 1], [1, 90, 3000], 8, 2, D, 16, DT, 840 + D)
+    wl.value = (wl.value.float().clamp(-5.5, 5.5) * 2.0 ** 125).to(torch.bfloat16)
+    Step(wl).run().check(wl.name)
+
+
+def test_caches_at_16_byte_offsets(cuda_device):
+    wl = _mixed(850)
+    want = GpuRun(wl).write_cache().attention()
+    g = GpuRun(wl)
+    n = g.kc.numel()
+    for name in ("kc", "vc"):
+        buf = torch.empty(n + 64, dtype=torch.uint8, device=g.dev)
+        setattr(g, name, buf[16:16 + n].view(want.kc.shape))
+        assert getattr(g, name).data_ptr() % 32 == 16
+    s, ws, write, attn = _prepared(g)
+    write()
+    attn()
+    torch.cuda.synchronize()
+    s.check_device()
+    assert torch.equal(_bits(g.out), _bits(want.out))
+    slots = g.slots
+    assert torch.equal(g.vc.flatten(0, 1)[slots], want.vc.flatten(0, 1)[slots])
+
+
+def test_static_scratch(cuda_device):
+    wl = _mixed(860)
+    want = GpuRun(wl).write_cache().attention()
+    k = kvq()
+    s = k.get_scheduler_metadata(wl.num_req, wl.heads_q, wl.heads_kv, wl.head_dim, wl.seq_lens_t.numpy(),
+                                 wl.query_start_loc.numpy(), wl.causal, wl.window, DT)
+    out = torch.full_like(want.out, float("nan"))
+    k.attention_with_kv_cache_static_scratch(s, want.q, want.kc, want.vc, want.qsl, want.sl, want.bt, wl.sm_scale,
+                                             wl.causal, wl.window, wl.soft_cap, 1.0, 1.0, out, DT, wl.heads_kv)
+    torch.cuda.synchronize()
+    s.check_device()
+    assert torch.equal(_bits(out), _bits(want.out))
+
+
+CHILD = r"""
+import os, sys
+import numpy as np, torch
+sys.path.insert(0, os.environ["KVQ_TEST_DIR"])
+sys.path.insert(0, os.path.dirname(os.environ["KVQ_TEST_DIR"]))
+from int8_kv_cache_reshape_gb300 import kvq
+from test_gpu_int4_serving import Step, GpuRun, _mixed, W, DT
+assert kvq.LIB_PATH.endswith("libkvq_checked.so"), kvq.LIB_PATH
+g = GpuRun(_mixed(870)).write_cache().attention()
+Step(W.custom("int4-checked-step", [1, 2], [500, 70], 8, 2, 128, 16, DT, 871)).run().check("checked step")
+np.save(os.environ["KVQ_OUT"], g.out.view(torch.int16).cpu().numpy())
+"""
+
+
+def test_bounds_checked_build(cuda_device, tmp_path):
+    """The build with the kernels' index checks gives the same bits."""
+    import os
+    import subprocess
+    import sys
+    from int8_kv_cache_reshape_gb300 import build as kvq_build
+    here = os.path.dirname(os.path.abspath(__file__))
+    env = dict(os.environ, KVQ_LIBRARY=str(kvq_build.build(checked=True)), KVQ_TEST_DIR=here,
+               KVQ_OUT=str(tmp_path / "o.npy"))
+    subprocess.run([sys.executable, "-c", CHILD], env=env, check=True, timeout=600)
+    want = GpuRun(_mixed(870)).write_cache().attention()
+    assert np.array_equal(np.load(tmp_path / "o.npy"), want.out.view(torch.int16).cpu().numpy())
