@@ -85,6 +85,9 @@ struct PrefillGeom {
   static constexpr int kN = prefill_keys(D);   // keys per KV tile
   static constexpr int kThreads = prefill_threads(D);
   static constexpr int kConv = prefill_conv_threads(D);
+  // Converter threads of a K or V tile: 4-bit rows have one half of the warps
+  // convert K and the other V (see there).
+  static constexpr int kConvTile = is_int4(DT) ? kConv / 2 : kConv;
   static constexpr int kStages = kPrefillStages;
   static constexpr bool kPth = is_per_token_head(DT);
   static constexpr bool kInt4 = is_int4(DT);
@@ -125,7 +128,7 @@ struct PrefillGeom {
   static_assert(kOffBar % 8 == 0, "mbarrier alignment");
   static_assert((kN + 31) / 32 <= 8 && kSide == 4, "side data space");
   static_assert(kN / 16 <= 15 && (kSlotRing & (kSlotRing - 1)) == 0, "slot table layout");
-  static_assert(kConv >= kN && kConv % 32 == 0, "a converter thread per key, whole warps");
+  static_assert(kConvTile >= kN && kConvTile % 32 == 0, "a converter thread per key, whole warps");
   static_assert((size_t)kBytes + 1024 == prefill_smem_bytes(D, kCG), "smem must follow the geometry");
   static_assert(kCG == 1 || (!kAuto && kDimsV % 64 == 0 && kKeysK % 8 == 0), "pair halves in the swizzle");
   // barrier slots (8 bytes each).  Quantised rows: the copy warp publishes
@@ -357,14 +360,14 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
     for (int s = 0; s < Geo::kStages; ++s) {
       tc::mbar_init(bar(Geo::kBarCodesK + s), 1);
       tc::mbar_init(bar(Geo::kBarCodesV + s), 1);
-      tc::mbar_init(bar(Geo::kBarKFull + s), CG * Geo::kConv / 32);
-      tc::mbar_init(bar(Geo::kBarVFull + s), CG * Geo::kConv / 32);
+      tc::mbar_init(bar(Geo::kBarKFull + s), CG * Geo::kConvTile / 32);
+      tc::mbar_init(bar(Geo::kBarVFull + s), CG * Geo::kConvTile / 32);
       tc::mbar_init(bar(Geo::kBarVEmpty + s), 1);
       tc::mbar_init(bar(Geo::kBarSFull + s), 1);
       tc::mbar_init(bar(Geo::kBarPFull + s), 4 * CG);
     }
     for (int s = 0; s < Geo::kSide; ++s)
-      tc::mbar_init(bar(Geo::kBarSide + s), Geo::kAuto ? 1 : Geo::kConv / 32);
+      tc::mbar_init(bar(Geo::kBarSide + s), Geo::kAuto ? 1 : Geo::kConvTile / 32);
     tc::mbar_init(bar(Geo::kBarODone), 1);
     tc::mbar_init(bar(Geo::kBarOFinal), 1);
     tc::mbar_init(bar(Geo::kBarDrain), 1);
@@ -722,10 +725,10 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
     // key (columns of its V tile).
     // 4-bit rows: a unit is (key, 32 dims), 16 code bytes and the multipliers of
     // their groups.  A thread keeps its 32 dims, and its units' keys differ by
-    // a multiple of 8, so that its offsets in the operand tile are constants.
+    // a multiple of 4, so that its offsets in the operand tile are constants.
     constexpr bool kInt4 = Geo::kInt4;
     constexpr int kUnits = kInt4 ? kN * D / 32 : kN * D / 16 / CG;
-    constexpr int kSlots = (kUnits + Geo::kConv - 1) / Geo::kConv;
+    constexpr int kSlots = (kUnits + Geo::kConvTile - 1) / Geo::kConvTile;
     constexpr int64_t kRow = row_bytes(DT, D);
     struct Units {
       uint32_t code_off[kSlots];  // key in the tile * D + dim in the row
@@ -754,9 +757,10 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
       uint32_t m;  // their multipliers: bytes 0-3 (D = 64), 0-1 (128), 0 (256)
     };
     using Code = std::conditional_t<kInt4, Code4, uint4>;
-    constexpr int kPieces = D / 32, kStepN = Geo::kConv / kPieces;  // (keys between a thread's units)
-    static_assert(!kInt4 || (CG == 1 && Geo::kConv % kPieces == 0 && kStepN % 8 == 0), "4-bit units");
-    const int pc4 = ctid % kPieces, n4 = ctid / kPieces;
+    constexpr int kPieces = D / 32, kStepN = Geo::kConvTile / kPieces;  // (keys between a thread's units)
+    static_assert(!kInt4 || (CG == 1 && Geo::kConvTile % kPieces == 0 && kStepN % 4 == 0), "4-bit units");
+    const int tid4 = ctid % Geo::kConvTile;  // (thread of its half)
+    const int pc4 = tid4 % kPieces, n4 = tid4 / kPieces;
     // A unit's four 16-byte f16 chunks go out in the order i ^ x4, x4 by the
     // 64-dim block, so that the 8 lanes of a quarter-warp are on 8 bank groups
     // (D = 128: two keys of 4 pieces; 256: one key of 8; 64: one block).
@@ -811,7 +815,7 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
     auto load_scales = [&](int e, int head, uint32_t win, uint32_t valid, float& ks, float& vs) {
       ks = vs = 0.0f;
       if constexpr (Geo::kPth) {
-        const int n = ctid;
+        const int n = kInt4 ? tid4 : ctid;
         if (n < kN && ((valid >> (n >> 4)) & 1u) && n >= (int)(win & 0xFFFFu) && n < (int)(win >> 16)) {
           const int64_t off = ((int64_t)(table[e * 16 + (n >> 4)] + (n & 15)) * p.heads_kv + head) * kRow +
                               code_bytes(DT, D);
@@ -855,7 +859,7 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
           for (int q = 0; q < 4; ++q) {
             uint32_t h[4];
             dev::int4_to_f16x2x4(w[q], f[q], h);
-            sts128(at + ((chunk4 ^ (uint32_t)q) << 4), make_uint4(h[0], h[1], h[2], h[3]));
+            sts128(at + ((chunk4 ^ (uint32_t)(q ^ ((i * kStepN) & 4))) << 4), make_uint4(h[0], h[1], h[2], h[3]));
           }
         }
       } else {
@@ -878,12 +882,64 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
       const int klo = min(max(c.cur.lo - kv0, 0), kN), khi = min(max(c.cur.hi - kv0, 0), kN);
       return (uint32_t)klo | ((uint32_t)khi << 16);
     };
+    KvCursor<kN, CG> ck;
+    ck.start(p);
+    if constexpr (kInt4) {
+      // One half of the warps converts K tiles, the other V tiles: a warp's
+      // waits, table reads and arrivals then come once per KV tile for twice
+      // the units (with both kinds in every warp they were 2,000 of a step's
+      // 3,300 cycles at D = 256).  Step g: convert tile g (loaded a step ahead;
+      // its buffer is free once S(g - 2), or P(g - 2) V(g - 2), is complete), load
+      // tile g + 1, after which slot table g + 1 is released.
+      const bool for_v = ctid >= Geo::kConvTile;
+      const uint8_t* const cache = for_v ? p.value_cache : p.key_cache;
+      const uint32_t tiles = base + (for_v ? Geo::kOffV : Geo::kOffK);
+      const int bar_free = for_v ? Geo::kBarVEmpty : Geo::kBarSFull, bar_full = for_v ? Geo::kBarVFull : Geo::kBarKFull;
+      Code c[kSlots];
+      float ks = 0.0f, vs = 0.0f;
+      uint32_t valid = 0;
+      auto load_tile = [&](int g) -> bool {
+        const int e = g & (Geo::kSlotRing - 1);
+        if (!__all_sync(0xffffffffu, wait_or_abort(bar(Geo::kBarSlots + e), (uint32_t)((g / Geo::kSlotRing) & 1),
+                                                   abort_flag)))
+          return false;
+        const uint32_t win = window_of(ck);
+        valid = load_codes(uk, cache, e, ck.cur.t.kv_head, win, c);
+        if (!for_v) load_scales(e, ck.cur.t.kv_head, win, valid, ks, vs);
+        warp_arrive(bar(Geo::kBarSlotsFree + e));
+        return true;
+      };
+      bool ok = !ck.valid || load_tile(0);
+      for (int g = 0; ok && ck.valid; ++g) {
+        const int st = g & 1, sd = g & (Geo::kSide - 1);
+        if (g >= 2 && !__all_sync(0xffffffffu, wait_or_abort(bar(bar_free + st), (uint32_t)(((g >> 1) - 1) & 1),
+                                                             abort_flag)))
+          break;
+        if (!for_v) {
+          // side data for the softmax (as below)
+          if (tid4 == 0) smask[sd] = valid;
+          if ((tid4 & ~31) < kN) {
+            if (tid4 < kN) {
+              sk[sd * kN + tid4] = ks;
+              sv[sd * kN + tid4] = vs;
+            }
+            const float vmax = tid4 < kN ? fmaxf(vs, 0.0f) : 0.0f;  // (a NaN or negative scale is ignored)
+            const uint32_t wmax = __reduce_max_sync(0xffffffffu, __float_as_uint(vmax));
+            if ((tid4 & 31) == 0) vmaxw[sd * 8 + (tid4 >> 5)] = wmax;
+          }
+          warp_arrive(bar(Geo::kBarSide + sd));
+        }
+        convert(uk, tiles + (uint32_t)(st * Geo::kTileBytes), c);
+        fence_operands();
+        warp_arrive(bar(bar_full + st));
+        ck.advance(p);
+        if (ck.valid) ok = load_tile(g + 1);
+      }
+    } else {
     // Step g: convert K(g) (its buffer is free once S(g - 2) is complete)
     // and publish its side data; load K(g + 1); convert V(g - 1) (its buffer
     // is free once P(g - 3) V(g - 3) is complete); load V(g), after which
     // slot table g is released.
-    KvCursor<kN, CG> ck;
-    ck.start(p);
     Code ka[kSlots], vb[kSlots];
     float ks_a = 0.0f, vs_a = 0.0f;
     uint32_t valid_a = 0, win_a = 0;
@@ -957,6 +1013,7 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
       const int e = g & (Geo::kSlotRing - 1);
       (void)load_codes(uv, p.value_cache, e, head_g, win_g, vb);
       warp_arrive(bar(Geo::kBarSlotsFree + e));
+    }
     }
     }
     __syncwarp();
