@@ -760,16 +760,14 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
     constexpr int kPieces = D / 32, kStepN = Geo::kConvTile / kPieces;  // (keys between a thread's units)
     static_assert(!kInt4 || (CG == 1 && Geo::kConvTile % kPieces == 0 && kStepN % 4 == 0), "4-bit units");
     const int tid4 = ctid % Geo::kConvTile;  // (thread of its half)
-    const int pc4 = tid4 % kPieces, n4 = tid4 / kPieces;
-    // A unit's four 16-byte f16 chunks go out in the order i ^ x4, x4 by the
-    // 64-dim block, so that the 8 lanes of a quarter-warp are on 8 bank groups
-    // (D = 128: two keys of 4 pieces; 256: one key of 8; 64: one block).
-    constexpr int kXMask = D == 64 ? 0 : D == 128 ? 2 : 3;
-    const int x4 = D == 128 ? (pc4 >> 1) * 2 : (pc4 >> 1) & kXMask;
+    // Lanes: two pieces of a 64-dim block (a 32-byte sector), four keys, then
+    // the blocks and further keys: the 8 lanes of a quarter-warp store on 8 bank
+    // groups of the swizzle.
+    constexpr int kBlocks = D / 64;
+    const int pc4 = 2 * ((tid4 >> 3) % kBlocks) + (tid4 & 1);
+    const int n4 = ((tid4 >> 1) & 3) + 4 * (tid4 / (8 * kBlocks));
     const uint32_t st4 = (uint32_t)((pc4 >> 1) * kN * 128 + n4 * 128);
-    const uint32_t chunk4 = (uint32_t)((4 * (pc4 & 1)) ^ (n4 & 7) ^ x4);
-    // multiplier selector of words 0 ^ x4 and 1 ^ x4 (f16 1024 + byte in both halves)
-    const uint32_t msel4 = D == 128 && x4 ? 0x4141u : 0x4040u;
+    const uint32_t chunk4 = (uint32_t)((4 * (pc4 & 1)) ^ (n4 & 7));
     const Units uk = kInt4 ? Units{} : make_units(Geo::kKeysK, D / 16, (int)rank * Geo::kKeysK, 0);
     const Units uv = CG == 1 ? uk : make_units(kN, Geo::kDimsV / 16, 0, (int)rank * Geo::kDimsV);
     const int32_t* table = reinterpret_cast<const int32_t*>(sm + Geo::kOffSlots);
@@ -781,18 +779,35 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
       const uint32_t valid = (uint32_t)table[e * 16 + 15];
       if constexpr (kInt4) {
         const uint8_t* from = cache + head * kRow + 16 * pc4;
+        // (the multipliers of dims 32 pc4 .. + 31, from the row's tail)
+        const uint8_t* mul = cache + head * kRow + D / 2 + 4 + (D == 64 ? 4 : D == 128 ? 2 : 1) * pc4;
+        const int tok_bytes = p.heads_kv * (int)kRow;
+        auto load = [&](int i, int slot) {
+          const int64_t off = (int64_t)slot * tok_bytes;
+          dst[i].w = dev::ldg_stream(from + off);
+          if constexpr (D == 64) dst[i].m = __ldg(reinterpret_cast<const uint32_t*>(mul + off));
+          else if constexpr (D == 128) dst[i].m = __ldg(reinterpret_cast<const uint16_t*>(mul + off));
+          else dst[i].m = __ldg(mul + off);
+        };
+        int slot[kSlots];
 #pragma unroll
         for (int i = 0; i < kSlots; ++i) {
-          dst[i].w = make_uint4(0, 0, 0, 0);
-          dst[i].m = 0;
-          const int n = n4 + i * kStepN;
-          if (n < kN && ((valid >> (n >> 4)) & 1u) && n >= (int)(win & 0xFFFFu) && n < (int)(win >> 16)) {
-            const uint8_t* at = from + (int64_t)(table[e * 16 + (n >> 4)] + (n & 15)) * (p.heads_kv * kRow);
-            dst[i].w = dev::ldg_stream(at);
-            const uint8_t* mul = at - 16 * pc4 + D / 2 + 4;
-            if constexpr (D == 64) dst[i].m = __ldg(reinterpret_cast<const uint32_t*>(mul + 4 * pc4));
-            else if constexpr (D == 128) dst[i].m = __ldg(reinterpret_cast<const uint16_t*>(mul + 2 * pc4));
-            else dst[i].m = __ldg(mul + pc4);
+          const int n = min(n4 + i * kStepN, kN - 1);
+          slot[i] = table[e * 16 + (n >> 4)] + (n & 15);
+        }
+        if (valid == (1u << kChunks) - 1u && win == ((uint32_t)kN << 16)) {
+          // (most tiles: every key is live)
+#pragma unroll
+          for (int i = 0; i < kSlots; ++i)
+            if (kN % kStepN == 0 || i + 1 < kSlots || n4 + i * kStepN < kN) load(i, slot[i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < kSlots; ++i) {
+            dst[i].w = make_uint4(0, 0, 0, 0);
+            dst[i].m = 0;
+            const int n = n4 + i * kStepN;
+            if (n < kN && ((valid >> (n >> 4)) & 1u) && n >= (int)(win & 0xFFFFu) && n < (int)(win >> 16))
+              load(i, slot[i]);
           }
         }
         return valid;
@@ -829,30 +844,14 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
 #pragma unroll
         for (int i = 0; i < kSlots; ++i) {
           if (kN % kStepN != 0 && n4 + i * kStepN >= kN) break;
-          uint32_t w[4] = {c[i].w.x, c[i].w.y, c[i].w.z, c[i].w.w};
-          if constexpr ((kXMask & 2) != 0) {
-            const bool s2 = (x4 & 2) != 0;
-            const uint32_t a0 = s2 ? w[2] : w[0], a1 = s2 ? w[3] : w[1];
-            w[2] = s2 ? w[0] : w[2];
-            w[3] = s2 ? w[1] : w[3];
-            w[0] = a0;
-            w[1] = a1;
-          }
-          if constexpr ((kXMask & 1) != 0) {
-            const bool s1 = (x4 & 1) != 0;
-            const uint32_t a0 = s1 ? w[1] : w[0], a2 = s1 ? w[3] : w[2];
-            w[1] = s1 ? w[0] : w[1];
-            w[3] = s1 ? w[2] : w[3];
-            w[0] = a0;
-            w[2] = a2;
-          }
+          const uint32_t w[4] = {c[i].w.x, c[i].w.y, c[i].w.z, c[i].w.w};
           dev::Int4Mul f[4];
           if constexpr (D == 64) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) f[q] = dev::int4_mul(dev::prmt(c[i].m, 0x64646464u, 0x4040u + 0x101u * q));
           } else {
-            f[0] = f[1] = dev::int4_mul(dev::prmt(c[i].m, 0x64646464u, msel4));
-            f[2] = f[3] = D == 128 ? dev::int4_mul(dev::prmt(c[i].m, 0x64646464u, msel4 ^ 0x0101u)) : f[0];
+            f[0] = f[1] = dev::int4_mul(dev::prmt(c[i].m, 0x64646464u, 0x4040u));
+            f[2] = f[3] = D == 128 ? dev::int4_mul(dev::prmt(c[i].m, 0x64646464u, 0x4141u)) : f[0];
           }
           const uint32_t at = tile + st4 + (uint32_t)(i * kStepN * 128);
 #pragma unroll
@@ -905,7 +904,7 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
           return false;
         const uint32_t win = window_of(ck);
         valid = load_codes(uk, cache, e, ck.cur.t.kv_head, win, c);
-        if (!for_v) load_scales(e, ck.cur.t.kv_head, win, valid, ks, vs);
+        if (for_v) load_scales(e, ck.cur.t.kv_head, win, valid, ks, vs);
         warp_arrive(bar(Geo::kBarSlotsFree + e));
         return true;
       };
@@ -915,8 +914,9 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
         if (g >= 2 && !__all_sync(0xffffffffu, wait_or_abort(bar(bar_free + st), (uint32_t)(((g >> 1) - 1) & 1),
                                                              abort_flag)))
           break;
-        if (!for_v) {
-          // side data for the softmax (as below)
+        if (for_v) {
+          // Side data for the softmax in slot g % 4 (its reader, the softmax of
+          // tile g - 4, is done).  From the V half: K's is the one that S waits for.
           if (tid4 == 0) smask[sd] = valid;
           if ((tid4 & ~31) < kN) {
             if (tid4 < kN) {
