@@ -176,6 +176,8 @@ __device__ __forceinline__ void write_rows(const uint16_t* __restrict__ key,
   }
 }
 
+// 4-bit rows, 16 elements a thread (8: 36.7 us for 20,011 tokens x 8 heads of
+// 128; 16: 25.1, 108 MB at 4.3 TB/s, bound by its instructions).
 // Writes one 4-bit row's share of 16 elements (x0, x1: the first 8, the rest):
 // TPR = D / 16 threads (aligned in the warp) own a row.  A group is D / 8
 // dims: half a share, a share or two.

@@ -30,7 +30,8 @@
 //     two-stage K ring and V ring.  K is read by the tensor core K-major, V
 //     MN-major, so neither needs a transpose.  Step i converts K(i) (its
 //     buffer is free once S(i-2) is complete) and then V(i-1) (free once
-//     P(i-3) V(i-3) is).  Per-key scales, the tile's chunk mask and its
+//     P(i-3) V(i-3) is); 4-bit rows have one half of the warps take K and
+//     the other V.  Per-key scales, the tile's chunk mask and its
 //     largest value scale go to one of four side-data slots for the softmax.
 //   * MMA warp (0): one elected lane issues, in a fixed order, S(j+1) and
 //     then O += P(j) V(j), each once its operands are in (blocking waits).
@@ -48,6 +49,12 @@
 //     staging area, free between epilogues) when a tile starts, and moved
 //     into tensor memory once the tile's last S is complete, so that the
 //     next tile's first S runs beside the last softmax.
+//   * Tiles at the edges of a row's keys mask them by a bit per key, in a pass
+//     that whole tiles skip.
+// Measured, 4-bit rows: 4 prompts of 1,024 tokens, 16 q and 2 kv heads of 256, in
+// 65 us (34.4 GFLOP: 0.53 PFLOP/s, 27 % of the measured bf16 rate).  A 64-key
+// tile takes the softmax 2,650 cycles (1,370 of them MMA work) and a tile
+// boundary about 10,000.
 //   * Q enters as f16 exactly: each row is scaled by a power of two that puts
 //     its largest |q| in [2^13, 2^14) (a bf16 significand fits in f16's);
 //     the scale, sm_scale, log2(e) and k_scale (per tensor) or the key's
