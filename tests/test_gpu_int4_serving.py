@@ -371,3 +371,54 @@ def test_bounds_checked_build(cuda_device, tmp_path):
     subprocess.run([sys.executable, "-c", CHILD], env=env, check=True, timeout=600)
     want = GpuRun(_mixed(870)).write_cache().attention()
     assert np.array_equal(np.load(tmp_path / "o.npy"), want.out.view(torch.int16).cpu().numpy())
+
+
+class _Rewrite(Step):
+    """A step whose new rows include rows of the context: every 13th token's,
+    and those of blocks that a second request shares."""
+
+    def __init__(self, wl, every):
+        super().__init__(wl)
+        pick = wl.new_token_mask()
+        pick[::every] = True
+        idx = torch.nonzero(pick).flatten()
+        dev = self.g.dev
+        # garbage (NaN scales) where the step is to write
+        slots = wl.slot_mapping[idx].to(dev)
+        self.g.kc.flatten(0, 1)[slots] = 0xFF
+        self.g.vc.flatten(0, 1)[slots] = 0xFF
+        self.nkey = wl.key[idx].contiguous().to(dev)
+        self.nval = wl.value[idx].contiguous().to(dev)
+        self.nslot = wl.slot_mapping[idx].contiguous().to(dev)
+
+
+@pytest.mark.parametrize("D,every", [(128, 101), (64, 13), (256, 997), (128, 40)])
+def test_step_that_rewrites_its_context(cuda_device, D, every):
+    """Rows written anywhere are seen (fewer and more of them than the kernel
+    looks through)."""
+    for seed in range(3):
+        wl = W.custom("int4-rewrite", [1, 2, 1, 1], [3000, 700, 2048, 40], 32, 8, D, 16, DT, 880 + seed)
+        for _ in range(2):
+            _Rewrite(wl, every).run().check(f"{wl.name} {every}")
+
+
+def test_step_over_shared_blocks(cuda_device):
+    """A new row in a block that another request's table holds too."""
+    wl = W.custom("int4-shared", [1, 1], [520, 520], 8, 2, 128, 16, DT, 890)
+    st = Step(wl)
+    # request 1 reads request 0's blocks: its own new row goes to the same slot
+    st.g.bt[1] = st.g.bt[0]
+    st.nkey[1], st.nval[1], st.nslot[1] = st.nkey[0], st.nval[0], st.nslot[0]
+    st.g.q[1] = st.g.q[0]
+    # (not bit for bit between the two: the step cuts the chunks of the two
+    # requests at different places, so their partial sums join in another order;
+    # each is within the bound of _harness.py of request 0's exact result)
+    kc, vc = oracle_cache(wl)
+    ref, bnd = oracle_reference(wl, kc, vc, tokens=[0])
+    for _ in range(5):
+        st.g.out.fill_(float("nan"))
+        st.run()
+        torch.cuda.synchronize()
+        kvq().decode_step_check(st.ws.t)
+        for r in (0, 1):
+            assert_attention_close(st.g.out_f32([r]), ref, f"request {r}", bnd)
