@@ -225,7 +225,8 @@ __device__ __forceinline__ void write_part_int4(const uint4 x0, const uint4 x1, 
 
 // write_rows for 4-bit rows, 16 elements of K and of V per thread: what is
 // computed per group and row (scale, multiplier, reciprocals, shuffles) is
-// most of the work with 8.
+// most of the work with 8.  (Coherent loads: the kernel may be a programmatic
+// dependent of the one that wrote its inputs.)
 template <int D>
 __device__ __forceinline__ void write_rows_int4(const uint16_t* __restrict__ key,
                                                 const uint16_t* __restrict__ value, int64_t num_tokens,
@@ -251,11 +252,11 @@ __device__ __forceinline__ void write_rows_int4(const uint16_t* __restrict__ key
     // rows and write nothing)
     const bool in_range = t < num_tokens;
     const int64_t tt = in_range ? t : num_tokens - 1;
-    const int64_t slot = slot_mapping[tt];
+    const int64_t slot = __ldcg(slot_mapping + tt);
     const uint16_t* ks = key + tt * key_stride + (int64_t)h * D + part * 16;
     const uint16_t* vs = value + tt * value_stride + (int64_t)h * D + part * 16;
-    const uint4 k0 = dev::ldg_stream(ks), k1 = dev::ldg_stream(ks + 8);
-    const uint4 v0 = dev::ldg_stream(vs), v1 = dev::ldg_stream(vs + 8);
+    const uint4 k0 = dev::ldg_stream_coherent(ks), k1 = dev::ldg_stream_coherent(ks + 8);
+    const uint4 v0 = dev::ldg_stream_coherent(vs), v1 = dev::ldg_stream_coherent(vs + 8);
     const bool active = in_range && slot >= 0 && slot < num_slots;
     const int64_t dst = (active ? (slot * heads_kv + h) : 0) * (int64_t)kRow;
     write_part_int4<D>(k0, k1, key_cache + dst, part, active);

@@ -229,15 +229,9 @@ __device__ __forceinline__ uint4 ldg_stream(const void* p) {
   return v;
 }
 
-// Its 8-byte form.
-__device__ __forceinline__ uint2 ldg_stream8(const void* p) {
-  uint2 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
-  return v;
-}
-
-// The 16-byte load without the non-coherent path: for data that other CTAs
-// of the same kernel wrote before a grid barrier.
+// The same without the non-coherent path: for data that other CTAs of the
+// same kernel wrote before a grid barrier, or that the kernel ahead of a
+// programmatic dependent wrote.
 __device__ __forceinline__ uint4 ldg_stream_coherent(const void* p) {
   uint4 v;
   asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"

@@ -27,7 +27,7 @@ constexpr int kThreads = 256;
 template <int DT, int D>
 __device__ __forceinline__ void load_values(const uint8_t* row, int part, float tensor_scale, float (&v)[8]) {
   if constexpr (DT == KVQ_AUTO) {
-    const uint4 w = dev::ldg_stream(row + 16 * part);
+    const uint4 w = dev::ldg_stream_coherent(row + 16 * part);
     const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -35,8 +35,8 @@ __device__ __forceinline__ void load_values(const uint8_t* row, int part, float 
       v[2 * i + 1] = dev::bf16_hi(x[i]);
     }
   } else if constexpr (is_int4(DT)) {
-    const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(row + 4 * part));
-    const uint4 tail = __ldg(reinterpret_cast<const uint4*>(row + D / 2));  // s, m_0..3, m_4..7
+    const uint32_t w = __ldcg(reinterpret_cast<const uint32_t*>(row + 4 * part));
+    const uint4 tail = __ldcg(reinterpret_cast<const uint4*>(row + D / 2));  // s, m_0..3, m_4..7
     const int g = part / (D / 64);
     const float s = __uint_as_float(tail.x);
     const float m = (float)(((g < 4 ? tail.y : tail.z) >> (8 * (g & 3))) & 0xFFu);
@@ -47,8 +47,8 @@ __device__ __forceinline__ void load_values(const uint8_t* row, int part, float 
       v[i] = s * ((__uint_as_float(u) - 8388616.0f) * m);
     }
   } else {
-    const float s = is_per_token_head(DT) ? __ldg(reinterpret_cast<const float*>(row + D)) : tensor_scale;
-    const uint2 w = dev::ldg_stream8(row + 8 * part);
+    const float s = is_per_token_head(DT) ? __ldcg(reinterpret_cast<const float*>(row + D)) : tensor_scale;
+    const uint2 w = __ldcg(reinterpret_cast<const uint2*>(row + 8 * part));
     uint32_t h[4];
     dev::word_to_f16x2x2<DT>(w.x, h[0], h[1]);
     dev::word_to_f16x2x2<DT>(w.y, h[2], h[3]);
@@ -89,7 +89,8 @@ gather_cache_kernel(const GatherArgs a) {
   constexpr int kTpr = D / 8, kRowsPerStep = kThreads / kTpr;
   constexpr int64_t kRow = row_bytes(DT, D);
   const int part = threadIdx.x % kTpr;
-  // (a programmatic dependent of whatever ran before on the stream)
+  // (a programmatic dependent of whatever ran before on the stream: what that
+  // wrote is read by coherent loads)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t step = (int64_t)gridDim.x * kRowsPerStep;
@@ -100,7 +101,7 @@ gather_cache_kernel(const GatherArgs a) {
   const int64_t dt = step / a.heads_kv;
   const int dh = (int)(step - dt * a.heads_kv);
   while (t < a.num_tokens) {
-    const int64_t slot = a.slot_mapping[t];
+    const int64_t slot = __ldcg(a.slot_mapping + t);
     float k[8], v[8];
     if (slot >= 0 && slot < a.num_slots) {
       const int64_t off = (slot * a.heads_kv + h) * kRow;
