@@ -422,3 +422,77 @@ def test_step_over_shared_blocks(cuda_device):
         kvq().decode_step_check(st.ws.t)
         for r in (0, 1):
             assert_attention_close(st.g.out_f32([r]), ref, f"request {r}", bnd)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_captured_step_with_new_lengths(cuda_device, D):
+    """One captured step replayed, call after call without a synchronisation,
+    for two batches in turn: lengths, tables, slots, new rows and q copied
+    into place on the stream."""
+    lens = ([900, 40, 3200, 300, 1, 1500], [1700, 2, 600, 3100, 45, 900])
+    nb = 700
+    wls = [W.custom(f"int4-replay-{i}", [1] * 6, L, 16, 4, D, 16, DT, 900 + i, token_scale_range=(0.1, 10.0),
+                    num_blocks=nb) for i, L in enumerate(lens)]
+    width = max(w.block_table.shape[1] for w in wls)
+    direct = [Step(w).run() for w in wls]
+    for d, w in zip(direct, wls):
+        d.check(w.name)
+    st = Step(wls[0])
+    g = st.g
+    g.bt = torch.full((6, width), -1, dtype=torch.int32, device=g.dev)
+    g.bt[:, : wls[0].block_table.shape[1]] = wls[0].block_table.to(g.dev)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        st.run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        st.run()
+    src = []
+    for w in wls:
+        s = Step(w)  # (its caches hold the context without the new rows)
+        bt = torch.full((6, width), -1, dtype=torch.int32, device=g.dev)
+        bt[:, : w.block_table.shape[1]] = w.block_table.to(g.dev)
+        src.append((s, bt))
+    got = []
+    torch.cuda.synchronize()
+    for i in (1, 0, 1, 1, 0):
+        s, bt = src[i]
+        g.kc.copy_(s.g.kc), g.vc.copy_(s.g.vc), g.bt.copy_(bt)
+        for n in ("q", "qsl", "sl"):
+            getattr(g, n).copy_(getattr(s.g, n))
+        for n in ("nkey", "nval", "nslot"):
+            getattr(st, n).copy_(getattr(s, n))
+        g.out.fill_(float("nan"))
+        graph.replay()
+        got.append((i, g.out.clone(), g.vc.clone()))
+    torch.cuda.synchronize()
+    kvq().decode_step_check(st.ws.t)
+    for i, out, vc in got:
+        assert torch.equal(_bits(out), _bits(direct[i].g.out))
+        assert torch.equal(vc, direct[i].g.vc)
+
+
+def test_two_schedules_share_a_workspace(cuda_device):
+    """Calls of different batches in turn on one stream and workspace."""
+    parts = []
+    for i, (ql, sl) in enumerate((([1, 1, 2], [3000, 700, 90]), ([1] * 9, [400] * 9), ([60, 1], [200, 2000]))):
+        w = W.custom(f"int4-share-{i}", ql, sl, 16, 4, 128, 16, DT, 920 + i, token_scale_range=(0.1, 10.0))
+        want = GpuRun(w).write_cache().attention().out.clone()
+        g = GpuRun(w).write_cache()
+        k = kvq()
+        s = k.get_scheduler_metadata(w.num_req, 16, 4, 128, w.seq_lens_t.numpy(), w.query_start_loc.numpy(), True,
+                                     w.window, DT)
+        parts.append((g, s, want))
+    ws = torch.zeros(max(s.workspace_bytes for _, s, _ in parts), dtype=torch.uint8, device="cuda:0")
+    for _ in range(20):
+        for g, s, _ in parts:
+            w = g.wl
+            g.out.fill_(float("nan"))
+            kvq().attention_with_kv_cache(s, g.q, g.kc, g.vc, g.qsl, g.sl, g.bt, w.sm_scale, True, w.window,
+                                          w.soft_cap, 1.0, 1.0, g.out, ws, DT, 4)
+    torch.cuda.synchronize()
+    for g, s, want in parts:
+        s.check_device()
+        assert torch.equal(_bits(g.out), _bits(want))
