@@ -398,6 +398,9 @@ KVQ_API int kvq_attention_with_kv_cache_static_scratch(
  *                           before its first use (e.g. cudaMemsetAsync);
  *                           every call leaves it ready for the next.  Calls
  *                           sharing a workspace must be ordered on one stream.
+ * 4-bit rows: kv heads whose rows need more copy groups than the device
+ * holds at once, and caches of 2^31 or more 128-byte lines, are refused
+ * (KVQ_E_UNSUPPORTED; the second by the attention call too).
  * The kernel is a cooperative launch (all its CTAs resident at once, one
  * grid-wide barrier between the cache write and the attention), followed
  * on the stream by the merge of the tiles it cut among warps (a kernel of
