@@ -270,15 +270,34 @@ def prepare_gather_cache(key_cache, value_cache, slot_mapping, key_out, value_ou
         v_scale, stream)), "kvq_gather_cache")
 
 
+def _flat(name, t, dtype, least=0):
+    """t as the library reads it: contiguous, of the dtype, of `least` elements or more."""
+    if t.dtype != dtype or not t.is_contiguous() or t.numel() < least:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of at least {least} elements")
+
+
 def _build_block_tables_args(query_start_loc, seq_lens, free_blocks, free_count, block_table,
                              slot_mapping, block_size, num_blocks, free_count_out, status, stream):
-    R = seq_lens.shape[0]
-    if query_start_loc.shape[0] != R + 1 or block_table.shape[0] < R:
+    import torch
+    R = seq_lens.numel()
+    for name, t, dtype, least in (
+            ("query_start_loc", query_start_loc, torch.int32, R + 1), ("seq_lens", seq_lens, torch.int32, 0),
+            ("free_blocks", free_blocks, torch.int32, 0), ("free_count", free_count, torch.int32, 1),
+            ("slot_mapping", slot_mapping, torch.int64, 0),
+            ("free_count_out", free_count_out, torch.int32, 1), ("status", status, torch.int32, 4)):
+        _flat(name, t, dtype, least)
+    if query_start_loc.numel() != R + 1 or block_table.dim() != 2 or block_table.shape[0] < R:
         raise ValueError("query_start_loc, seq_lens and block_table must agree on their requests")
-    if status.numel() < 4:
-        raise ValueError("status holds four int32")
+    # The library's one stride is both the rows' pitch and their width, so a
+    # view of some columns (a pitch beyond its width) would let a request
+    # store into columns that the caller did not hand over.  (One row has no
+    # pitch.)
+    width = block_table.shape[1]
+    if block_table.dtype != torch.int32 or (width > 1 and block_table.stride(1) != 1) or (
+            R > 1 and block_table.stride(0) != width):
+        raise ValueError("block_table must be int32 rows side by side (not a view of some columns)")
     return (R, _ptr(query_start_loc), _ptr(seq_lens), _ptr(free_blocks), free_blocks.numel(),
-            _ptr(free_count), _ptr(block_table), block_table.stride(0), _ptr(slot_mapping),
+            _ptr(free_count), _ptr(block_table), width, _ptr(slot_mapping),
             slot_mapping.numel(), int(block_size), int(num_blocks), _ptr(free_count_out),
             _ptr(status), _stream(stream))
 
@@ -288,8 +307,9 @@ def build_block_tables(query_start_loc, seq_lens, free_blocks, free_count, block
                        stream=None) -> None:
     """Block tables and slot mapping of a step on the device: query_start_loc
     int32 [R + 1], seq_lens int32 [R], free_blocks int32 (a stack of
-    free_count int32 [1] ids), block_table int32 [R, width] (entries of new
-    blocks are stored), slot_mapping int64 (padded entries get -1),
+    free_count int32 [1] ids), block_table int32 [R, width] (rows side by
+    side; entries of new blocks are stored), slot_mapping int64 (padded
+    entries get -1),
     free_count_out int32 [1] (may be free_count), status int32 [4],
     zero-filled before its first use."""
     _check(lib.kvq_build_block_tables(*_build_block_tables_args(
