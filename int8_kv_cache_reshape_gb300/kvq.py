@@ -9,6 +9,7 @@ there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 
@@ -191,6 +192,18 @@ def cache_row_bytes(kv_cache_dtype, head_dim: int) -> int:
     return out.value
 
 
+@functools.lru_cache(maxsize=None)
+def _row_bytes(dt: int, head_dim: int) -> int:
+    """cache_row_bytes, looked up once."""
+    return cache_row_bytes(dt, head_dim)
+
+
+def _flat(name, t, dtype, least=0):
+    """t as the library reads it: contiguous, of the dtype, of `least` elements or more."""
+    if t.dtype != dtype or not t.is_contiguous() or t.numel() < least:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of at least {least} elements")
+
+
 def _reshape_and_cache_args(key, value, key_cache, value_cache, slot_mapping, kv_cache_dtype,
                             k_scale, v_scale, stream):
     dt = parse_kv_cache_dtype(kv_cache_dtype) if isinstance(kv_cache_dtype, str) else kv_cache_dtype
@@ -245,8 +258,19 @@ def _gather_cache_args(key_cache, value_cache, slot_mapping, key_out, value_out,
     T, H, D = key_out.shape
     if key_out.dtype != value_out.dtype or key_out.dtype not in (torch.bfloat16, torch.float32):
         raise ValueError("key_out and value_out must both be bfloat16 or both float32")
-    if tuple(value_out.shape) != (T, H, D) or slot_mapping.shape[0] != T:
+    if tuple(value_out.shape) != (T, H, D) or tuple(slot_mapping.shape) != (T,):
         raise ValueError("key_out, value_out and slot_mapping must agree on their rows")
+    _flat("slot_mapping", slot_mapping, torch.int64)
+    for t in (key_out, value_out):
+        if T > 0 and (t.stride(2) != 1 or (H > 1 and t.stride(1) != D)):
+            raise ValueError("the heads and dims of key_out and value_out must be contiguous")
+    # The library reads rows of H heads of D dims at the slots of the pool.
+    row = _row_bytes(dt, D)
+    for t in (key_cache, value_cache):
+        if t.dim() != 4 or t.shape[2] != H or t.shape[3] * t.element_size() != row or not t.is_contiguous():
+            raise ValueError(f"the caches must be contiguous [num_blocks, block_size, {H}, {row} bytes]")
+    if key_cache.shape != value_cache.shape:
+        raise ValueError("key_cache and value_cache must have one shape")
     return (_ptr(key_cache), _ptr(value_cache), key_cache.shape[0], key_cache.shape[1], H, D, dt,
             float(k_scale), float(v_scale), _ptr(slot_mapping), T,
             int(key_out.dtype == torch.float32), _ptr(key_out), _ptr(value_out),
@@ -255,8 +279,9 @@ def _gather_cache_args(key_cache, value_cache, slot_mapping, key_out, value_out,
 
 def gather_cache(key_cache, value_cache, slot_mapping, key_out, value_out, kv_cache_dtype,
                  k_scale: float = 1.0, v_scale: float = 1.0, stream=None) -> None:
-    """Cache rows read back as values: slot_mapping int64 [T]; key_out /
-    value_out bf16 or float32 [T, Hkv, D] (token stride may exceed Hkv*D)."""
+    """Cache rows read back as values: caches uint8 [NB, B, Hkv, row];
+    slot_mapping int64 [T]; key_out / value_out bf16 or float32 [T, Hkv, D]
+    (token stride may exceed Hkv*D)."""
     _check(lib.kvq_gather_cache(*_gather_cache_args(
         key_cache, value_cache, slot_mapping, key_out, value_out, kv_cache_dtype, k_scale,
         v_scale, stream)), "kvq_gather_cache")
@@ -268,12 +293,6 @@ def prepare_gather_cache(key_cache, value_cache, slot_mapping, key_out, value_ou
     return Prepared(lib.kvq_gather_cache, _marshalled(lib.kvq_gather_cache, _gather_cache_args(
         key_cache, value_cache, slot_mapping, key_out, value_out, kv_cache_dtype, k_scale,
         v_scale, stream)), "kvq_gather_cache")
-
-
-def _flat(name, t, dtype, least=0):
-    """t as the library reads it: contiguous, of the dtype, of `least` elements or more."""
-    if t.dtype != dtype or not t.is_contiguous() or t.numel() < least:
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of at least {least} elements")
 
 
 def _build_block_tables_args(query_start_loc, seq_lens, free_blocks, free_count, block_table,
