@@ -215,9 +215,11 @@ KVQ_API int kvq_gather_cache(const void* key_cache, const void* value_cache,
  * copy of the lengths predicts it.  When the list runs out, the remaining new
  * entries are -1 (read as masked keys by the attention), and the tokens in
  * them, like tokens in blocks whose id lies outside [0, num_blocks), get slot
- * -1.  A request with Q < 0, Q > L, tokens outside the buffer, or (Q > 0)
- * more blocks than block_table_stride is left out: slots -1, no blocks
- * taken.  Freed blocks are pushed back by the caller (stored at *free_count,
+ * -1.  A request with Q > L, tokens outside the buffer, or (Q > 0) more blocks
+ * than block_table_stride is left out: slots -1, no blocks taken.  Where
+ * query_start_loc decreases it does not say whose a token is: the whole step
+ * is left out (every slot -1, no blocks taken, no entry stored, status[1] =
+ * num_req).  Freed blocks are pushed back by the caller (stored at *free_count,
  * which it then advances).  query_start_loc, seq_lens, free_blocks and
  * free_count are read only; no buffer may overlap another but free_count_out
  * and free_count.  One kernel launch; allocates nothing. */

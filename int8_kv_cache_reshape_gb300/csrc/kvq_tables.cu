@@ -8,6 +8,10 @@
 // free[count - 1 - base_r - n], and the new token at position p goes to slot
 // table[r][p / B] * B + p % B.
 //
+// Starts that decrease leave it open whose a token is, and the searches below
+// expect them sorted: every CTA looks at all of them, and where one decreases the
+// whole step is left out.
+//
 // A token's block never depends on another thread's store: an old block comes
 // from the table, a new one straight from the free list, and the thread of
 // the first token in a new block stores the table entry (a new block's first
@@ -21,8 +25,10 @@
 // at the run's first request, with the requests before it summed in one pass
 // (every thread loads its share of the lengths at once, where a search for
 // the first request takes log2 R dependent loads).  Measured, call after call:
-// 2.9 us for 64 requests, 5.0 for 509 with 28,914 tokens, 8.8 for 893,000
-// tokens of 37 requests (a prefix pass of its own ahead: 4.1, 10.2, 14.3).
+// 3.0 us for 64 requests, 5.1 for 509 with 28,914 tokens, 8.9 for 893,000
+// tokens of 37 requests (a prefix pass of its own ahead: 4.1, 10.2, 14.3).  The
+// check for decreasing starts is 0.1 to 0.2 of each, as a term of the sum, a
+// count of its own or a barrier that votes.
 #include <cuda_runtime.h>
 
 #include "kvq_internal.h"
@@ -37,6 +43,11 @@ constexpr int kPer = 4;
 constexpr int kRun = kPer * kThreads;
 // Requests held in shared memory, four a thread.
 constexpr int kAllRequests = kPer * kThreads;
+
+// Added to the sum of the new blocks for a request that ends before it starts: the
+// sum is then negative.  (It stays below the entries of the block table, less
+// than 2^40; at most 1,024 such terms are added.)
+constexpr int64_t kDecreasing = -((int64_t)1 << 44);
 
 struct TableParams {
   const int32_t* query_start_loc;
@@ -95,18 +106,20 @@ __global__ void __launch_bounds__(kThreads) block_tables_kernel(const TableParam
   // blocks, and how many of them are left out
   int64_t base = 0;
   int first_req = 0, bad = 0;
-  if (p.num_req > kAllRequests && t0 > 0) {
+  if (p.num_req > kAllRequests) {
     int64_t sum = 0;
     int n = 0, b = 0;
+    bool down = false;
     for (int r = tid; r < p.num_req; r += kThreads) {
       const Request q = load_request(p, r);
+      down |= q.end < q.start;
       if (q.end <= t0) {
         sum += q.fresh;
         ++n;
         b += !q.ok;
       }
     }
-    sum = warp_sum(sum);
+    sum = warp_sum(down ? kDecreasing : sum);
     const int64_t nb = warp_sum(((int64_t)b << 32) | (int64_t)n);
     if (lane == 0) {
       part[warp] = sum;
@@ -143,7 +156,7 @@ __global__ void __launch_bounds__(kThreads) block_tables_kernel(const TableParam
         first_s[at] = q.first;
         held_s[at] = q.held;
         fresh[i] = q.fresh;
-        local += q.fresh;
+        local += q.end < q.start ? kDecreasing : q.fresh;
         bad_t += !q.ok;
       }
     }
@@ -173,7 +186,7 @@ __global__ void __launch_bounds__(kThreads) block_tables_kernel(const TableParam
       before += fresh[i];
     }
     __syncthreads();
-    const int64_t stop = min(t1, next);
+    const int64_t stop = base < 0 ? t : min(t1, next);  // (no token's, if the starts decrease)
     // A thread takes per_t consecutive tokens: one search for the first one's
     // request (the last that starts at or before it), steps for the others
     // (a search for each: 10.5 against 9.2 us for 893,000 tokens of 37
@@ -236,6 +249,10 @@ __global__ void __launch_bounds__(kThreads) block_tables_kernel(const TableParam
     }
     t = max(t, stop);
     __syncthreads();
+  }
+  if (base < 0) {
+    base = 0;
+    bad = p.num_req;
   }
   for (int64_t k = t + tid; k < t1; k += kThreads) p.slot_mapping[k] = -1;
 
