@@ -541,7 +541,8 @@ typedef struct {
   int64_t max_splits;          /* most pieces of one tile                     */
   int64_t total_query_tokens;
   size_t workspace_bytes;
-  size_t decode_smem_bytes;    /* dynamic shared memory per decode CTA        */
+  size_t decode_smem_bytes;    /* dynamic shared memory per decode CTA (4-bit
+                                  rows: the most of the classes launched)      */
   size_t decode_chunk_bytes;   /* K+V bytes a warp streams per 16-token chunk */
   int64_t num_prefill_tiles;   /* 128-row tiles of the tensor-core prefill
                                   (CTA pairs: list entries, empty partners

@@ -911,9 +911,15 @@ int kvq_sched_get_info(const kvq_sched_t* s, kvq_sched_info_t* out) {
   out->max_splits = s->max_splits;
   out->total_query_tokens = s->total_q;
   out->workspace_bytes = s->workspace_bytes;
-  out->decode_smem_bytes = kvq::is_int4(s->dtype)
-                               ? kvq::int4_geom(s->heads_kv, s->head_dim, 1).smem
-                               : kvq::decode_smem_bytes(s->dtype, s->head_dim);
+  out->decode_smem_bytes = kvq::decode_smem_bytes(s->dtype, s->head_dim);
+  if (kvq::is_int4(s->dtype)) {
+    // the larger of the classes it launches (of class 0 where it launches none)
+    out->decode_smem_bytes = 0;
+    for (int cls = 1; cls >= 0; --cls)
+      if (s->launch[cls].num_chunks > 0 || (cls == 0 && out->decode_smem_bytes == 0))
+        out->decode_smem_bytes =
+            std::max(out->decode_smem_bytes, kvq::int4_geom(s->heads_kv, s->head_dim, cls + 1).smem);
+  }
   out->decode_chunk_bytes = (size_t)kvq::decode_chunk_bytes(s->dtype, s->head_dim);
   out->num_prefill_tiles = (int64_t)s->prefill.size();
   out->prefill_smem_bytes =
