@@ -596,8 +596,11 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge,
         const int nr = 8 * t + 2 * c + e;
         if (nr >= pc.nrows) continue;
         const float l = l_run[t][e];
-        // (l >= 2^6: no step of this passes 2^128)
-        const float sc = (l > 0.0f ? dev::kInt4Unit / l : 0.0f) * unit;
+        // The value scales' power of two comes last: o / l is of the codes' size,
+        // while 2^15 / l times the smallest scales' power would be subnormal (at l
+        // = 2^30, a few ten thousand keys, it keeps 8 bits).
+        const float sc = l > 0.0f ? dev::kInt4Unit / l : 0.0f;
+        auto val = [&](int i, int h) -> float { return o[t][i][e + 2 * h] * sc * unit; };
         if (pc.part < 0) {
           if (pc.bad) continue;
           const int R = pc.row0 + nr, rq = div_g(R);
@@ -606,16 +609,15 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge,
 #pragma unroll
           for (int i = 0; i < Row::kMtiles; i += 4)
             *reinterpret_cast<uint4*>(dst + 2 * i) =
-                make_uint4(dev::pack_bf16x2(o[t][i][e] * sc, o[t][i][e + 2] * sc),
-                           dev::pack_bf16x2(o[t][i + 1][e] * sc, o[t][i + 1][e + 2] * sc),
-                           dev::pack_bf16x2(o[t][i + 2][e] * sc, o[t][i + 2][e + 2] * sc),
-                           dev::pack_bf16x2(o[t][i + 3][e] * sc, o[t][i + 3][e + 2] * sc));
+                make_uint4(dev::pack_bf16x2(val(i, 0), val(i, 1)), dev::pack_bf16x2(val(i + 1, 0), val(i + 1, 1)),
+                           dev::pack_bf16x2(val(i + 2, 0), val(i + 2, 1)),
+                           dev::pack_bf16x2(val(i + 3, 0), val(i + 3, 1)));
         } else {
           float* dst = p.part_o + (int64_t)(pc.part + nr) * D + g * (D / 8);
 #pragma unroll
           for (int i = 0; i < Row::kMtiles; i += 2)
-            *reinterpret_cast<float4*>(dst + 2 * i) = make_float4(
-                o[t][i][e] * sc, o[t][i][e + 2] * sc, o[t][i + 1][e] * sc, o[t][i + 1][e + 2] * sc);
+            *reinterpret_cast<float4*>(dst + 2 * i) =
+                make_float4(val(i, 0), val(i, 1), val(i + 1, 0), val(i + 1, 1));
           if (g == 0)
             p.part_lse[pc.part + nr] = l > 0.0f ? m_off[t][e] + 6.0f + log2f(l) : -INFINITY;
         }

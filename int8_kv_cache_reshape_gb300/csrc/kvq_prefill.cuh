@@ -1458,9 +1458,10 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
         if (skl != -INFINITY) l_sum += exp2f(fminf(skl - m_ref + 6.0f, 126.0f));
       }
       uint16_t* const dst = p.out + row_at(rec);
-      // (4-bit: kInt4Unit 2^ev / l in two factors, since l is 2^5 or more and a
-      // value up to 2^128: 2^up last)
-      const int up = Geo::kInt4 && ev > 100 ? 20 : 0;
+      // (4-bit: kInt4Unit 2^ev / l in two factors, 2^up last: l is 2^5 or more and
+      // a value up to 2^128; at the other end l reaches 2^30 with some ten
+      // thousand keys, and the one factor would be subnormal)
+      const int up = !Geo::kInt4 ? 0 : ev > 100 ? 20 : ev < -40 && ev > -1000 ? -60 : 0;
       const float sc = (l_sum > 0.0f ? (Geo::kInt4 ? dev::kInt4Unit : 1.0f) / l_sum : 0.0f) *
                        (Geo::kInt4   ? (ev > -1000 ? __int_as_float((127 + ev - up) << 23) : 0.0f)
                         : Geo::kPth  ? (ev > -1000 ? ldexpf(1.0f, ev) : 0.0f)
@@ -1480,7 +1481,7 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
           for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[e + i]) * sc;
           if (Geo::kInt4 && up != 0) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] *= 1048576.0f;
+            for (int i = 0; i < 8; ++i) f[i] *= __int_as_float((127 + up) << 23);
           }
           const uint4 o = make_uint4(dev::pack_bf16x2(f[0], f[1]), dev::pack_bf16x2(f[2], f[3]),
                                      dev::pack_bf16x2(f[4], f[5]), dev::pack_bf16x2(f[6], f[7]));
