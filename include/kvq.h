@@ -294,7 +294,8 @@ KVQ_API int kvq_get_scheduler_metadata(int num_req, int heads_q, int heads_kv,
  *                           [0, num_blocks) read as empty (masked) keys.
  *   block_size, num_blocks  cache geometry; block_size a multiple of 16,
  *                           num_blocks * block_size < 2^31.
- *   sm_scale                score scale (typically 1/sqrt(head_dim)).
+ *   sm_scale                score scale (typically 1/sqrt(head_dim)); any finite
+ *                           number.
  *   soft_cap                > 0: z <- soft_cap * tanh(z / soft_cap) after
  *                           sm_scale; <= 0: off.
  *   alibi_slopes            device fp32 [heads_q] or NULL: z <- z + slope_h *

@@ -1118,7 +1118,10 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
     // significand fits in f16's).  Elements more than about 2^27 below the
     // row's largest land in f16's subnormal range (bits lost) or flush to
     // zero: a Q row with that dynamic range loses them.  bf16 rows ("auto")
-    // enter the bf16 MMA as they are.  Returns the row's 2^-shift.
+    // enter the bf16 MMA as they are.  The score scale's sign enters with Q (a
+    // scale of zero makes it zero), so that the softmax multiplies by a positive
+    // factor: it takes a round's maximum and sets masked scores to -inf before
+    // the product.  Returns the row's 2^-shift.
     auto load_q = [&](int nrows, int n_tile) -> float {
       const bool valid = m < nrows;
       (void)__all_sync(0xffffffffu, wait_or_abort(bar(Geo::kBarQStage), (uint32_t)(n_tile & 1), abort_flag));
@@ -1138,7 +1141,9 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
       }
       // largest |q| < 2^(emax - 126): scaled into [2^13, 2^14)
       const int sh = emax == 0 || Geo::kAuto ? 0 : min(140 - emax, 126);
-      const float up = ldexpf(1.0f, sh);
+      const float qk_scale = Geo::kPth || Geo::kAuto ? p.sm_scale : p.sm_scale * p.k_scale;
+      const float up = ldexpf(qk_scale > 0.0f ? 1.0f : qk_scale < 0.0f ? -1.0f : 0.0f, sh);
+      const uint32_t keep = qk_scale == 0.0f ? 0u : 0xFFFFFFFFu, flip = qk_scale < 0.0f ? 0x80008000u : 0u;
 #pragma unroll 1
       for (int h = 0; h < D / 2; h += 16) {
         uint32_t w[16];
@@ -1148,7 +1153,7 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
           const uint32_t x[4] = {x4.x, x4.y, x4.z, x4.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            w[4 * c + e] = Geo::kAuto ? x[e] : dev::pack_f16x2(dev::bf16_lo(x[e]) * up, dev::bf16_hi(x[e]) * up);
+            w[4 * c + e] = Geo::kAuto ? (x[e] & keep) ^ flip : dev::pack_f16x2(dev::bf16_lo(x[e]) * up, dev::bf16_hi(x[e]) * up);
         }
         tc::tmem_st16(tmem + Geo::kColQ + lane_base + (uint32_t)h, w);
       }
@@ -1188,10 +1193,12 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
       const int row_lo = W > 0 ? pos - W + 1 : 0;
       // scores in log2 units (natural units under a soft cap, which converts)
       // (4-bit rows enter the MMAs as multiples of 1 / kInt4Unit)
-      const float score_mul = Geo::kInt4
-                                  ? p.sm_scale * dev::kInt4Unit * (cap > 0.0f ? 1.0f : log2e) * q_unscale
-                                  : p.sm_scale * q_unscale * (cap > 0.0f ? 1.0f : log2e) *
-                                        (Geo::kPth || Geo::kAuto ? 1.0f : p.k_scale);
+      const float signed_mul = Geo::kInt4
+                                   ? p.sm_scale * dev::kInt4Unit * (cap > 0.0f ? 1.0f : log2e) * q_unscale
+                                   : p.sm_scale * q_unscale * (cap > 0.0f ? 1.0f : log2e) *
+                                         (Geo::kPth || Geo::kAuto ? 1.0f : p.k_scale);
+      // (its sign is Q's; never zero, which times -inf is NaN)
+      const float score_mul = fmaxf(fabsf(signed_mul), 0x1p-126f);
       // ALiBi: this row's slope in log2 units (the bias uses the exact integer
       // distance key - position, added after the soft cap).
       const float al_slope = AL ? p.alibi_slopes[head_q] * log2e : 0.0f;
