@@ -133,7 +133,8 @@ KVQ_API int kvq_cache_row_bytes(kvq_dtype_t dtype, int head_dim, size_t* out);
  *   slot_mapping      device int64 [num_tokens]: token t goes to block
  *                     slot/block_size, position slot%block_size.  Slots < 0
  *                     or >= num_blocks*block_size are skipped (nothing is
- *                     written for that token).
+ *                     written for that token).  Tokens of unequal rows must
+ *                     not share a slot (their rows may mix).
  *   dtype             any kvq_dtype_t.
  *   k_scale, v_scale  per-tensor scales (fp8_e4m3 / fp8_e5m2): code =
  *                     fp8(x / scale) with a correctly rounded fp32 division,
@@ -544,7 +545,8 @@ typedef struct {
   size_t workspace_bytes;
   size_t decode_smem_bytes;    /* dynamic shared memory per decode CTA (4-bit
                                   rows: the most of the classes launched)      */
-  size_t decode_chunk_bytes;   /* K+V bytes a warp streams per 16-token chunk */
+  size_t decode_chunk_bytes;   /* K+V bytes a warp streams per 16-token chunk
+                                  (4-bit rows: of 32 tokens)                  */
   int64_t num_prefill_tiles;   /* 128-row tiles of the tensor-core prefill
                                   (CTA pairs: list entries, empty partners
                                   included; see kvq_plan_prefill_tile_t) */

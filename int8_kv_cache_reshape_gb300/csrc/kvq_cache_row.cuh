@@ -51,8 +51,9 @@ __device__ __forceinline__ float absmax8(const uint4 x) {
 // some ten instructions and only decides which integer is nearest, so the
 // codes come from products with reciprocals a little too large and a little
 // too small: rint is monotonic, and where both give the same integer, so does
-// the rounded quotient between them.  Where they differ (a quotient within
-// 2^-19 of halfway) the division decides.
+// the rounded quotient between them.  Where they differ (a quotient whose
+// distance from halfway is about 2^-20 of itself or less: up to 2^-17, at 6.5)
+// the division decides.
 //
 // Reference form: an element's code + 8 under its group's step s * m_g.
 __device__ __forceinline__ uint32_t enc_int4(float x, float step) {

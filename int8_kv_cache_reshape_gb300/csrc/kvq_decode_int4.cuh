@@ -25,18 +25,24 @@
 //     readers is over before it is asked for.  Records (slots, masks) are
 //     prepared by the lanes, kInt4Turns turns at a time.
 //   * The copies write the 128-byte swizzle, and MMA row g is token pi(g) =
-//     {0,4,2,6,12,8,14,10}[g] of a half (row g + 8 the token after it): with 8
-//     heads (5 lines a token) K's 16-byte reads (eight lanes: two rows) and
-//     V's (rows pi(2c)) then cover the 32 banks once.  The token order of a
-//     softmax is free.
+//     {0,4,2,6,12,8,14,10}[g] of a half (row g + 8 the token after it).  The
+//     order is chosen for 8 heads of 128 (5 lines a token): K's 16-byte reads
+//     (eight lanes: two rows) and V's (rows pi(2c)) of heads 0, 2, 4, 5 and 7
+//     then cover the 32 banks once, the others' take 1.5 to 2 times as many
+//     wavefronts (by address arithmetic; 1, 2 and 4 heads: 1.4 to 2.9 times).
+//     The token order of a softmax is free.
 //   * A warp takes both halves of a chunk in one go (32 tokens): waits,
 //     records, masks and votes once for two sets of MMAs.
 //   * The lazy reference maximum and the value scales' power-of-two reference
 //     move on one warp vote; the common chunk has no shuffle.
 // Measured: 64 requests of 1,024 to 4,096 keys (32 q and 8 kv heads of 128) in
 // 48 us with the merge, 179 MB at 3.7 TB/s (the first data comes 7 us after
-// the launch, the merge takes 4); 32 requests of 32,768 keys in 231 us, 5.8
-// TB/s, 87 % of a plain copy's rate.
+// the launch, the merge takes 4); 32 requests of 32,768 keys (64 q heads) in
+// 229 us, 5.9 TB/s, 88 % of a plain copy's rate.  The same 32 requests in other
+// shapes (8 q heads a kv head): 16 kv heads 463 us (5.8 TB/s), 4 heads 124 (5.4), 2 heads
+// 79 (4.2), 1 head 69 (2.4: three eighths of its stages are padding, 13 groups a
+// CTA issue their own copies); 16 rows a tile 356 (3.8: 8 warps a CTA, twice the
+// MMAs); ALiBi 274 (4.9); head_dim 64 155 (5.2), 256 446 (5.4).
 #pragma once
 
 #include <cuda_runtime.h>

@@ -116,7 +116,11 @@ KVQ_HD constexpr size_t decode_smem_bytes(int dtype, int head_dim) {
 // `half_bytes` apart and holding the group's rows token by token.
 constexpr int kInt4Chunk = 32;  // tokens of a chunk of the 4-bit plan
 // Warps per CTA, by registers (o, Q fragments and one chunk's codes): 16 of
-// 128 up to head_dim 128 and 8 rows a tile, 12 of 168 and 8 of 255 above.
+// 128 up to head_dim 128 and 8 rows a tile, 12 of 168 and 8 of 255 above.  The
+// host-planned instances of head_dim 64, and of 128 with 8 rows, do not spill;
+// 128 with 16 rows stores 120 bytes a thread, 256 stores 116 (8 rows) and 240.
+// The fused step's: 8 and 196 (64, 8 and 16 rows), 100 and 316 (128), 300 and 464
+// (256).
 KVQ_HD constexpr int int4_max_warps(int head_dim, int ntiles) {
   return head_dim == 64 || (head_dim == 128 && ntiles == 1) ? 16
          : head_dim == 128 || ntiles == 1                  ? 12
@@ -124,7 +128,12 @@ KVQ_HD constexpr int int4_max_warps(int head_dim, int ntiles) {
 }
 constexpr size_t kInt4MaxSmem = 212 * 1024;  // dynamic shared memory of a CTA
 constexpr int kInt4Turns = 16;               // copies a warp prepares at a time
-constexpr int kInt4PlanReq = 256;            // requests a CTA of the fused step plans for itself
+// Requests that a CTA of the fused step plans for itself; more are planned by the
+// first CTA for all, ahead of the grid barrier.  Own plans against the first
+// CTA's (requests of 300 keys, 8 q and 2 kv heads of 128): 18.6 / 20.6 us for 16,
+// 20.7 / 22.7 for 64, 24.7 / 27.8 for 200, 30.9 / 35.0 for 256.  The plan takes 5 KB
+// beside kInt4MaxSmem and the records (8 KB); as much again exceeds the 227 KB.
+constexpr int kInt4PlanReq = 256;
 struct Int4Geom {
   int hg, gpc;      // heads (warps) per group, groups per CTA
   int hsplit;       // head groups: heads_kv / hg
@@ -236,7 +245,7 @@ struct PrefillTile {
 };
 static_assert(sizeof(PrefillTile) == 32, "PrefillTile layout");
 
-// One piece of a row tile (32 bytes).
+// One piece of a row tile.
 struct DecodePiece {
   int32_t req;       // request index
   int32_t kv_head;   // kv head
@@ -247,7 +256,7 @@ struct DecodePiece {
   int32_t any_lo;    // keys some row of the tile can see: [any_lo, any_hi)
   int32_t any_hi;
   int32_t flat0;     // position of the piece's first chunk in its launch's flat sequence
-  int32_t chunk0;    // that chunk's 16-token index in the request
+  int32_t chunk0;    // that chunk's index in the request (16 tokens; 32 of 4-bit rows)
   int32_t q0;        // the request's first query token (query_start_loc[req])
   int32_t pos0;      // position of its query 0: L - Q
 };
@@ -404,8 +413,8 @@ int launch_block_tables(int num_req, const int32_t* query_start_loc, const int32
 // ntiles); unused otherwise)
 int launch_decode(const AttnParams& p, const PrefillMaps& maps, int dtype, int head_dim, int ntiles,
                   void* stream);
-// The fused step's kernel (cooperative launch of `warps` / 4 CTAs); `warps`
-// from step_warps().
+// The fused step's kernel, a cooperative launch of every CTA that fits; `warps`
+// from step_warps() (4 a CTA; 4-bit rows: segments times kv heads).
 int launch_decode_step(const AttnParams& p, const StepParams& sp, const PrefillMaps& maps, int dtype,
                        int head_dim, int64_t warps, void* stream);
 // Decode warps of the fused step's grid on the current device (every CTA

@@ -149,3 +149,12 @@ def test_device_lengths_beyond_the_bound(cuda_device, R):
     assert torch.isnan(st.g.out[1:4].float()).all()
     # (the read cleared the word)
     kvq().decode_step_check(st.ws.t)
+
+
+@pytest.mark.parametrize("block", [32, 48, 80, 2176])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_block_sizes(cuda_device, block, D):
+    """Blocks that chunks of 32 tokens straddle, and one block a request."""
+    wl = W.custom(f"int4-step-block-{block}", [1, 2, 1, 1], [1, 700, 97, 2048], 16, 4, D, block, DT, 1040 + D,
+                  window=333, token_scale_range=(0.1, 10.0), extra_blocks=2)
+    Step(wl, *_extras(16, False, True)).run().check(wl.name)
