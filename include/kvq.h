@@ -158,6 +158,49 @@ KVQ_API int kvq_reshape_and_cache(const void* key, const void* value,
                           const int64_t* slot_mapping, kvq_dtype_t dtype,
                           float k_scale, float v_scale, void* stream);
 
+/* rotary_and_cache -- a step's queries and keys rotated by their positions
+ * (rotary position embedding), the keys and values stored in the paged caches
+ * (no counterpart on the pages, whose rows come rotated).  Row p of cos_sin
+ * holds the cosines, then the sines, of position p's rotary_dim / 2 pairs; a
+ * pair (a, b) becomes (a c - b s, b c + a s), each product and sum rounded to
+ * fp32 by itself.  Keys are quantised from their rotated fp32 values, with no
+ * bf16 rounding in between (KVQ_AUTO rounds them once to bf16); queries are
+ * rounded once to bf16.
+ *
+ *   query, key, value   device bf16 [num_tokens, heads, head_dim]; heads and
+ *                       dims contiguous; token strides in elements (>= heads *
+ *                       head_dim, multiples of 8); base pointers 16-byte
+ *                       aligned.
+ *   num_heads_q         0: keys and values only (query, query_out unused).
+ *   positions           device int64 [num_tokens].
+ *   cos_sin             device fp32 [max_position, rotary_dim], contiguous,
+ *                       16-byte aligned.
+ *   rotary_dim          dims rotated, the first of each head: a multiple of 16
+ *                       up to head_dim; the others stay as they are.
+ *   interleaved         0: pair j is dims (j, j + rotary_dim / 2); 1: (2j, 2j+1).
+ *   query_out           device bf16 like query, with its own token stride; may
+ *                       be query itself (same pointer and stride), else they
+ *                       must not overlap.
+ *   key_cache ... v_scale   as for kvq_reshape_and_cache, which stores the same
+ *                       bytes for the same fp32 values.
+ * A token whose slot is outside the pool stores no rows (its query is still
+ * rotated); one whose position is outside [0, max_position) stores no rows and
+ * gets zero query rows.  Inputs, and the rotated values, must be finite.
+ * One kernel launch (a programmatic dependent: it may be resident before the
+ * kernel ahead of it on the stream ends, and reads nothing before then);
+ * allocates nothing.  num_tokens == 0 is a no-op. */
+KVQ_API int kvq_rotary_and_cache(const void* query, const void* key, const void* value,
+                                 int64_t num_tokens, int64_t query_stride_tok,
+                                 int64_t key_stride_tok, int64_t value_stride_tok,
+                                 int num_heads_q, int num_heads_kv, int head_dim,
+                                 const int64_t* positions, const float* cos_sin,
+                                 int64_t max_position, int rotary_dim, int interleaved,
+                                 void* query_out, int64_t query_out_stride_tok,
+                                 void* key_cache, void* value_cache, int64_t num_blocks,
+                                 int block_size, const int64_t* slot_mapping,
+                                 kvq_dtype_t dtype, float k_scale, float v_scale,
+                                 void* stream);
+
 /* gather_cache -- read rows of the caches back as the values they stand for
  * (the inverse of kvq_reshape_and_cache; no counterpart on the pages).  For
  * callers that need cached rows outside the attention: a shared prefix moved
@@ -267,6 +310,52 @@ KVQ_API int kvq_get_scheduler_metadata(int num_req, int heads_q, int heads_kv,
                                const int32_t* query_start_loc_host, int causal,
                                int window, kvq_dtype_t dtype,
                                kvq_sched_t** out, size_t* workspace_bytes);
+
+/* get_shared_prefix_metadata -- plan one causal attention call for a batch
+ * whose requests begin with the same keys (a system prompt, samples of one
+ * document), so that the keys of a shared prefix are read once for all its
+ * requests and not once for each (no counterpart on the pages).  The schedule
+ * goes to kvq_attention_with_kv_cache (causal = 1, the same window) like any
+ * other, with the same results as without sharing up to rounding.
+ *
+ *   num_req ... query_start_loc_host, window, dtype, out, workspace_bytes
+ *                         as for kvq_get_scheduler_metadata.
+ *   num_prefixes,         host int32 [num_prefixes]: keys of each prefix
+ *   prefix_lens_host      (>= 0; it need not end at a block's end).
+ *   request_prefix_host   host int32 [num_req]: the prefix that a request
+ *                         begins with, or -1.  Its length must not exceed L - Q
+ *                         (the new tokens come after it).
+ * The caller vouches that keys 0 .. P - 1 of all requests of a prefix hold the
+ * same rows; they are read through the block-table row of one of them.
+ * Requests of up to 16 (query, head) rows per kv head share; larger ones
+ * (prompts) read their whole context as without a prefix.  A prefix is shared
+ * up to a multiple of 32 keys; a batch that would save few bytes (less
+ * than 24 MB of cache reads) is planned without sharing. */
+KVQ_API int kvq_get_shared_prefix_metadata(int num_req, int heads_q, int heads_kv,
+                                           int head_dim, const int32_t* seq_lens_host,
+                                           const int32_t* query_start_loc_host,
+                                           int num_prefixes, const int32_t* prefix_lens_host,
+                                           const int32_t* request_prefix_host, int window,
+                                           kvq_dtype_t dtype, kvq_sched_t** out,
+                                           size_t* workspace_bytes);
+
+/* get_cross_attention_metadata -- plan one attention call of decoder tokens
+ * to an encoder's keys, cached once per request (no counterpart on the pages,
+ * whose queries are the last positions of their own context).  Every query of
+ * request r sees all encoder_lens_host[r] keys of its block-table row; the two
+ * lengths are independent, and a request without keys gets zero rows.
+ *   num_req ... dtype, out, workspace_bytes   as for
+ *                         kvq_get_scheduler_metadata (but Q may exceed L).
+ *   encoder_lens_host     host int32 [num_req], >= 0.
+ * The schedule goes to kvq_attention_with_kv_cache with causal = 0, window 0 and
+ * the encoder lengths as seq_lens; soft cap and sinks as there; ALiBi slopes
+ * are refused (KVQ_E_UNSUPPORTED: the keys have no position relative to a
+ * query). */
+KVQ_API int kvq_get_cross_attention_metadata(int num_req, int heads_q, int heads_kv,
+                                             int head_dim, const int32_t* encoder_lens_host,
+                                             const int32_t* query_start_loc_host,
+                                             kvq_dtype_t dtype, kvq_sched_t** out,
+                                             size_t* workspace_bytes);
 
 /* attention_with_kv_cache -- varlen causal GQA attention over the paged
  * caches, dequantisation fused into the tiles, online softmax.
@@ -558,6 +647,20 @@ typedef struct {
 
 KVQ_API int kvq_sched_get_info(const kvq_sched_t* sched, kvq_sched_info_t* out);
 
+/* What a schedule of kvq_get_shared_prefix_metadata or
+ * kvq_get_cross_attention_metadata attends as rows against a whole run of keys
+ * (for tests and benchmarks; all zero but smem_bytes for other schedules). */
+typedef struct {
+  int64_t num_units;           /* CTAs: up to 256 rows (128 at head_dim 256) of a
+                                  kv head against a range of keys             */
+  int64_t num_merge_items;     /* row groups merged from their partials       */
+  int64_t num_shared_requests; /* requests that read a prefix with others     */
+  int64_t shared_keys;         /* prefix keys read so, summed over them       */
+  size_t smem_bytes;           /* dynamic shared memory per CTA               */
+} kvq_rect_info_t;
+
+KVQ_API int kvq_sched_get_rect_info(const kvq_sched_t* sched, kvq_rect_info_t* out);
+
 /* ---- the plan, for tests and tools (host copies; no device access) --------
  * [P2] Breakdown item 1: the schedule is the single source of the tile and
  * scratch sizes the kernels run with; these calls expose it for checking.
@@ -580,7 +683,8 @@ typedef struct {
   int32_t launch;          /* decode launch class: 0 (tiles of <= 8 rows) or 1 */
   int32_t req, kv_head, row0, nrows;
   int32_t part;            /* first partial row of the piece in the workspace; -1: writes out */
-  int32_t merge;           /* merge item of a cut tile; -1: not cut */
+  int32_t merge;           /* merge item of a cut tile; -1: not cut, or (part >= 0)
+                              merged with its request's shared prefix */
   int32_t key_lo, key_hi;  /* keys some row of the tile can see: [key_lo, key_hi) */
   int32_t flat0;           /* the piece's first position in its class's chunk sequence */
   int32_t chunk0;          /* that chunk's index within the request */

@@ -1,5 +1,5 @@
 // kvq_decode_dispatch.cu -- head_dim (and ALiBi) dispatch of the split-KV
-// decode and the tensor-core prefill kernels (one translation unit per
+// decode, the tensor-core prefill and the rectangular attention kernels (one translation unit per
 // head_dim and ALiBi setting holds the instances).
 #include "kvq_internal.h"
 #include "kvq_merge.cuh"
@@ -35,6 +35,16 @@ int launch_merge(const AttnParams& p, int dtype, int head_dim, int64_t num_merge
   return KVQ_OK;
 }
 
+int launch_rect_merge(const AttnParams& p, const RectParams& rp, int head_dim, int64_t num_merges, void* stream) {
+  if (num_merges <= 0) return KVQ_OK;
+  switch (head_dim) {
+    case 64: return launch_dependent(merge_rect_kernel<64>, (unsigned)num_merges, kMergeThreads, stream, p, rp);
+    case 128: return launch_dependent(merge_rect_kernel<128>, (unsigned)num_merges, kMergeThreads, stream, p, rp);
+    case 256: return launch_dependent(merge_rect_kernel<256>, (unsigned)num_merges, kMergeThreads, stream, p, rp);
+    default: return KVQ_E_UNSUPPORTED;
+  }
+}
+
 int launch_merge_step(const AttnParams& p, const StepParams& sp, int dtype, int head_dim,
                       int64_t warps, void* stream) {
   if (sp.num_tiles <= 0) return KVQ_OK;
@@ -63,6 +73,7 @@ int launch_merge_step(const AttnParams& p, const StepParams& sp, int dtype, int 
 }
 
 #define KVQ_DECLARE(D)                                                                       \
+  int launch_rect_d##D(const AttnParams&, const RectParams&, int, void*);                    \
   int launch_decode_d##D(const AttnParams&, int, int, void*);                               \
   int launch_decode_d##D##_alibi(const AttnParams&, int, int, void*);                       \
   int launch_step_d##D(const AttnParams&, const StepParams&, int, int64_t*, void*);         \
@@ -135,6 +146,16 @@ int step_warps(int dtype, int heads_kv, int head_dim, bool alibi, int max_rows, 
 int launch_decode_step(const AttnParams& p, const StepParams& sp, const PrefillMaps& maps, int dtype,
                        int head_dim, int64_t warps, void* stream) {
   return step_dispatch(p, sp, maps, dtype, head_dim, uses_alibi(p), &warps, stream);
+}
+
+int launch_rect(const AttnParams& p, const RectParams& rp, int dtype, int head_dim, void* stream) {
+  if (rp.num_units <= 0) return KVQ_OK;
+  switch (head_dim) {
+    case 64: return launch_rect_d64(p, rp, dtype, stream);
+    case 128: return launch_rect_d128(p, rp, dtype, stream);
+    case 256: return launch_rect_d256(p, rp, dtype, stream);
+    default: return KVQ_E_UNSUPPORTED;
+  }
 }
 
 int launch_prefill(const AttnParams& p, const PrefillMaps& maps, int dtype, int head_dim,

@@ -16,6 +16,7 @@
 #include <cstdlib>
 #include <cstring>
 #include <atomic>
+#include <memory>
 #include <mutex>
 #include <new>
 #include <utility>
@@ -27,6 +28,9 @@
 using kvq::DecodePiece;
 using kvq::MergeItem;
 using kvq::PrefillTile;
+using kvq::RectMerge;
+using kvq::RectToken;
+using kvq::RectUnit;
 using kvq::WarpSeg;
 
 // One launch of the split-KV decode kernel: the tiles with one 8-row n-tile
@@ -51,13 +55,18 @@ struct kvq_sched {
   const MergeItem* h_merges;
   int64_t num_pieces, num_merges;
   std::vector<PrefillTile> prefill;
+  // Rows attended against a run of keys as a whole (shared prefixes, encoders).
+  std::vector<RectUnit> units;
+  std::vector<RectToken> tokens;
+  int64_t num_rect_merges, num_shared_requests, shared_keys;
+  bool cross;
   DecodeLaunch launch[2];
   int64_t num_tiles, max_splits, partial_rows;
   int32_t max_chunk;  // highest 16-token chunk index any tile reads
   size_t workspace_bytes;
   void* d_buf;  // device copy: pieces, warp table, merge items, prefill tiles, error word
   size_t d_buf_bytes;
-  size_t d_pieces_off, d_warps_off, d_merges_off, d_prefill_off, d_error_off;
+  size_t d_pieces_off, d_warps_off, d_merges_off, d_prefill_off, d_units_off, d_tokens_off, d_rmerges_off, d_error_off;
   size_t image_bytes;       // bytes of the plan image (host and device copies)
   void* h_image;            // host image (pinned with a device), uploaded by the first attention call
   size_t h_image_bytes;
@@ -293,6 +302,112 @@ struct Tile {
   int64_t c_lo, c_hi, any_lo, any_hi;
 };
 
+// The shared prefixes of a batch (host arrays; see
+// kvq_get_shared_prefix_metadata).
+struct Prefixes {
+  int num;
+  const int32_t* lens;
+  const int32_t* of;  // [num_req]: each request's prefix, or -1
+};
+
+// A row tile of the rectangular attention, the same for every kv head: rows of
+// the tokens from list entry tok0, keys [kv_lo, kv_hi) of request `req`.
+struct RectTile {
+  int req, tok0, row0, nrows;
+  int64_t kv_lo, kv_hi;
+  // filled by plan_rect: KV ranges it is cut into, partials a row has, and the
+  // partial row of (kv head 0, row 0); head h's are h * parts * nrows on
+  int64_t splits, parts, part;
+};
+
+// Time of a unit of `tiles` KV tiles, in microseconds: a fixed part (launch,
+// first keys, Q, the rows' way out) and one for each KV tile, by the row tiles
+// that share it.  Fitted to measured calls; it only decides how the keys are cut.
+constexpr double kRectStart = 5.0;
+double rect_tile_us(int head_dim, bool two) {
+  return head_dim >= 256 ? 1.3 : head_dim >= 128 ? (two ? 1.4 : 0.8) : (two ? 1.1 : 0.6);
+}
+
+// Cut the row tiles' keys among CTAs (one per SM) so that the last one ends
+// early: all units as near as can be to one length, tried for every number
+// of cuts of the longest tile.  Appends the units, longest first, and hands out
+// partial rows from *partial_rows on.  A tile left whole writes out directly if
+// it may (`direct`) and its rows have one O.
+void plan_rect(std::vector<RectTile>& tiles, int heads_kv, int head_dim, int sms, bool direct, int64_t forced,
+               std::vector<RectUnit>* units, int64_t* partial_rows) {
+  const int kN = kvq::prefill_keys(head_dim);
+  auto kv_tiles = [&](const RectTile& t) {
+    return t.kv_hi > t.kv_lo ? ceil_div(t.kv_hi, kN) - t.kv_lo / kN : 0;
+  };
+  // one row tile: its two softmax groups leave a partial each
+  auto pair = [&](const RectTile& t) { return kvq::rect_row_tiles(head_dim) == 2 && t.nrows <= 128; };
+  int64_t most = 0;
+  for (const RectTile& t : tiles) most = std::max(most, kv_tiles(t));
+  if (most == 0) return;
+  int64_t best = most;
+  double best_us = 0.0;
+  for (int64_t cuts = 1, last = 0; cuts <= most; cuts += std::max<int64_t>(1, cuts / 16)) {
+    const int64_t len = ceil_div(most, cuts);  // KV tiles of a unit
+    if (len == last) continue;
+    last = len;
+    double total = 0.0, longest = 0.0;
+    int64_t n = 0, rows = 0;
+    for (const RectTile& t : tiles) {
+      const int64_t T = kv_tiles(t);
+      if (T == 0) continue;
+      const int64_t S = ceil_div(T, len);
+      const double per = rect_tile_us(head_dim, !pair(t) && head_dim < 256);
+      total += (double)heads_kv * ((double)S * kRectStart + (double)T * per);
+      longest = std::max(longest, kRectStart + (double)ceil_div(T, S) * per);
+      n += heads_kv * S;
+      if (!direct || S > 1) rows += heads_kv * S * t.nrows * (pair(t) ? 2 : 1);
+    }
+    const int64_t waves = ceil_div(n, sms);
+    // (partials: written and read once, in L2 mostly)
+    const double us = (waves <= 3 ? (double)waves * longest : total / sms + 0.5 * longest) +
+                      (double)rows * head_dim * 8.0 / 5.0e6;
+    if (best_us == 0.0 || us < best_us) {
+      best_us = us;
+      best = len;
+    }
+  }
+  if (forced > 0) best = forced;
+  struct Range {
+    int64_t tile, s, len;
+  };
+  std::vector<Range> order;
+  for (size_t i = 0; i < tiles.size(); ++i) {
+    RectTile& t = tiles[i];
+    const int64_t T = kv_tiles(t);
+    t.splits = T == 0 ? 0 : ceil_div(T, best);
+    const bool whole = direct && t.splits == 1 && (!pair(t) || T == 1);
+    t.parts = whole ? 0 : t.splits * (pair(t) ? 2 : 1);
+    t.part = *partial_rows;
+    *partial_rows += t.parts * t.nrows * heads_kv;
+    for (int64_t s2 = 0; s2 < t.splits; ++s2)
+      order.push_back(Range{(int64_t)i, s2, (s2 + 1) * T / t.splits - s2 * T / t.splits});
+  }
+  std::stable_sort(order.begin(), order.end(), [](const Range& a, const Range& b) { return a.len > b.len; });
+  for (const Range& r : order) {
+    const RectTile& t = tiles[(size_t)r.tile];
+    const int64_t T = kv_tiles(t), first = t.kv_lo / kN;
+    for (int h = 0; h < heads_kv; ++h) {
+      RectUnit u{};
+      u.kv_head = h;
+      u.row0 = t.row0;
+      u.nrows = t.nrows;
+      u.kv_lo = (int32_t)std::max(t.kv_lo, (first + r.s * T / t.splits) * kN);
+      u.kv_hi = (int32_t)std::min(t.kv_hi, (first + (r.s + 1) * T / t.splits) * kN);
+      u.tok0 = t.tok0;
+      u.req = t.req;
+      const int64_t per_split = t.parts / t.splits;
+      u.part = t.parts == 0 ? -1 : (int32_t)(t.part + (h * t.parts + r.s * per_split) * t.nrows);
+      u.part_stride = t.nrows;
+      units->push_back(u);
+    }
+  }
+}
+
 }  // namespace
 
 extern "C" {
@@ -359,6 +474,77 @@ int kvq_reshape_and_cache(const void* key, const void* value, int64_t num_tokens
   return kvq::launch_reshape_and_cache(key, value, num_tokens, key_stride_tok, value_stride_tok,
                                        num_heads_kv, head_dim, key_cache, value_cache, num_blocks,
                                        block_size, slot_mapping, dtype, k_scale, v_scale, stream);
+}
+
+int kvq_rotary_and_cache(const void* query, const void* key, const void* value, int64_t num_tokens,
+                         int64_t query_stride_tok, int64_t key_stride_tok, int64_t value_stride_tok,
+                         int num_heads_q, int num_heads_kv, int head_dim, const int64_t* positions,
+                         const float* cos_sin, int64_t max_position, int rotary_dim, int interleaved,
+                         void* query_out, int64_t query_out_stride_tok, void* key_cache,
+                         void* value_cache, int64_t num_blocks, int block_size,
+                         const int64_t* slot_mapping, kvq_dtype_t dtype, float k_scale, float v_scale,
+                         void* stream) {
+  if (!kvq::is_valid_dtype(dtype)) return KVQ_E_INVALID_ARG;
+  if (!kvq::head_dim_supported(head_dim)) return KVQ_E_UNSUPPORTED;
+  if (num_tokens < 0 || num_heads_q < 0 || num_heads_kv <= 0 || num_blocks < 0 || block_size <= 0 ||
+      max_position < 0 || (interleaved != 0 && interleaved != 1) || rotary_dim <= 0 || rotary_dim > head_dim)
+    return KVQ_E_INVALID_ARG;
+  if (rotary_dim % 16) return KVQ_E_UNSUPPORTED;
+  if (num_tokens == 0) return KVQ_OK;
+  // (positions outside the table read its first row and use nothing of it)
+  if (max_position == 0) return KVQ_E_INVALID_ARG;
+  if (!key || !value || !positions || !cos_sin || !key_cache || !value_cache || !slot_mapping)
+    return KVQ_E_INVALID_ARG;
+  const int64_t min_stride = (int64_t)num_heads_kv * head_dim, min_q = (int64_t)num_heads_q * head_dim;
+  if (key_stride_tok < min_stride || value_stride_tok < min_stride || key_stride_tok % 8 ||
+      value_stride_tok % 8)
+    return KVQ_E_INVALID_ARG;
+  if (num_heads_q > 0) {
+    if (!query || !query_out || query_stride_tok < min_q || query_out_stride_tok < min_q ||
+        query_stride_tok % 8 || query_out_stride_tok % 8 || !aligned(query, 16) || !aligned(query_out, 16))
+      return KVQ_E_INVALID_ARG;
+    // in place, or apart
+    const char* const q0 = static_cast<const char*>(query);
+    const char* const o0 = static_cast<const char*>(query_out);
+    const int64_t q_bytes = 2 * ((num_tokens - 1) * query_stride_tok + min_q);
+    const int64_t o_bytes = 2 * ((num_tokens - 1) * query_out_stride_tok + min_q);
+    const bool same = q0 == o0 && query_stride_tok == query_out_stride_tok;
+    // (rows of one buffer at one stride, side by side, do not meet either)
+    const int64_t apart = o0 > q0 ? o0 - q0 : q0 - o0;
+    const bool beside = query_stride_tok == query_out_stride_tok && apart % (2 * query_stride_tok) >= 2 * min_q &&
+                        apart % (2 * query_stride_tok) <= 2 * (query_stride_tok - min_q);
+    if (!same && !beside && q0 < o0 + o_bytes && o0 < q0 + q_bytes) return KVQ_E_INVALID_ARG;
+  }
+  if (!aligned(key, 16) || !aligned(value, 16) || !aligned(key_cache, 16) || !aligned(value_cache, 16) ||
+      !aligned(slot_mapping, 8) || !aligned(positions, 8) || !aligned(cos_sin, 16))
+    return KVQ_E_INVALID_ARG;
+  if (dtype == KVQ_FP8_E4M3 || dtype == KVQ_FP8_E5M2) {
+    if (!(std::isfinite(k_scale) && k_scale > 0.0f && std::isfinite(v_scale) && v_scale > 0.0f))
+      return KVQ_E_INVALID_ARG;
+  }
+  kvq::RotaryArgs a;
+  a.query = static_cast<const uint16_t*>(query);
+  a.key = static_cast<const uint16_t*>(key);
+  a.value = static_cast<const uint16_t*>(value);
+  a.num_tokens = num_tokens;
+  a.query_stride = query_stride_tok;
+  a.key_stride = key_stride_tok;
+  a.value_stride = value_stride_tok;
+  a.heads_q = num_heads_q;
+  a.heads_kv = num_heads_kv;
+  a.positions = positions;
+  a.cos_sin = cos_sin;
+  a.max_position = max_position;
+  a.rotary_dim = rotary_dim;
+  a.query_out = static_cast<uint16_t*>(query_out);
+  a.query_out_stride = query_out_stride_tok;
+  a.key_cache = static_cast<uint8_t*>(key_cache);
+  a.value_cache = static_cast<uint8_t*>(value_cache);
+  a.num_slots = num_blocks * (int64_t)block_size;
+  a.slot_mapping = slot_mapping;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  return kvq::launch_rotary_and_cache(a, dtype, head_dim, interleaved != 0, stream);
 }
 
 int kvq_gather_cache(const void* key_cache, const void* value_cache, int64_t num_blocks,
@@ -433,10 +619,15 @@ void kvq_sched_destroy(kvq_sched_t* s) {
   delete s;
 }
 
-int kvq_get_scheduler_metadata(int num_req, int heads_q, int heads_kv, int head_dim,
-                               const int32_t* seq_lens_host, const int32_t* query_start_loc_host,
-                               int causal, int window, kvq_dtype_t dtype, kvq_sched_t** out,
-                               size_t* workspace_bytes) {
+}  // extern "C"
+
+namespace {
+
+// The plan of an attention call: causal or not, with shared prefixes (pre) or
+// against encoders' keys (cross: any number of queries for any number of keys).
+int plan_attention(int num_req, int heads_q, int heads_kv, int head_dim, const int32_t* seq_lens_host,
+                   const int32_t* query_start_loc_host, int causal, int window, kvq_dtype_t dtype,
+                   const Prefixes* pre, bool cross, kvq_sched_t** out, size_t* workspace_bytes) {
   if (!out || !workspace_bytes) return KVQ_E_INVALID_ARG;
   *out = nullptr;
   *workspace_bytes = 0;
@@ -450,10 +641,18 @@ int kvq_get_scheduler_metadata(int num_req, int heads_q, int heads_kv, int head_
   if (num_req > 0 && query_start_loc_host[0] != 0) return KVQ_E_INVALID_ARG;
   for (int r = 0; r < num_req; ++r) {
     const int64_t Q = (int64_t)query_start_loc_host[r + 1] - query_start_loc_host[r];
-    if (Q < 0 || seq_lens_host[r] < 0 || Q > seq_lens_host[r]) return KVQ_E_INVALID_ARG;
+    if (Q < 0 || seq_lens_host[r] < 0 || (!cross && Q > seq_lens_host[r])) return KVQ_E_INVALID_ARG;
+    if (pre) {
+      const int g = pre->of[r];
+      if (g < -1 || g >= pre->num) return KVQ_E_INVALID_ARG;
+      // (a request's new tokens come after the prefix)
+      if (g >= 0 && Q > 0 && pre->lens[g] > seq_lens_host[r] - Q) return KVQ_E_INVALID_ARG;
+    }
   }
 
-  kvq_sched* s = new (std::nothrow) kvq_sched();
+  // (destroyed, its buffers returned, on every way out but the last)
+  std::unique_ptr<kvq_sched, void (*)(kvq_sched*)> owned(new (std::nothrow) kvq_sched(), kvq_sched_destroy);
+  kvq_sched* const s = owned.get();
   if (!s) return KVQ_E_NO_MEMORY;
   s->num_req = num_req;
   s->heads_q = heads_q;
@@ -483,6 +682,143 @@ int kvq_get_scheduler_metadata(int num_req, int heads_q, int heads_kv, int head_
     s->device = -1;
   }
   const int G = s->group;
+  const int sms = have_device ? std::max(1, sm_count()) : kDefaultSmCount;
+  s->cross = cross;
+  s->max_chunk = 0;
+  s->num_rect_merges = s->num_shared_requests = s->shared_keys = 0;
+  s->partial_rows = 0;
+
+  // 0) Shared prefixes: the members' rows of each prefix packed into row tiles
+  //    of whole requests; pre_tile[r] and pre_row[r]: a request's tile and its
+  //    first row there (-1: none).  Requests with more than kTileMaxRows rows
+  //    run whole on the prefill: their work is products, which sharing does
+  //    not save.  What the sharing saves is bytes: (members - 1) times the
+  //    prefix, at the rate of the decode kernel, against the units' fixed time
+  //    and the merge, so a batch that saves less than kPrefixMinBytes stays
+  //    unshared.  KVQ_PREFIX_MIN_BYTES (tests, benchmarks) sets another limit;
+  //    KVQ_RECT_TILES forces the KV tiles of a unit.
+  std::vector<RectTile> rect;
+  std::vector<int> pre_tile;
+  std::vector<int32_t> pre_row;
+  int64_t forced_tiles = 0;
+  if (const char* env = std::getenv("KVQ_RECT_TILES")) forced_tiles = std::atoll(env);
+  if (pre && pre->num > 0) {
+    pre_tile.assign((size_t)num_req, -1);
+    pre_row.assign((size_t)num_req, 0);
+    std::vector<std::vector<int>> members((size_t)pre->num);
+    int64_t saved = 0;
+    for (int r = 0; r < num_req; ++r) {
+      const int g = pre->of[r];
+      const int64_t rows = ((int64_t)query_start_loc_host[r + 1] - query_start_loc_host[r]) * G;
+      if (g >= 0 && rows > 0 && rows <= kvq::kTileMaxRows) members[(size_t)g].push_back(r);
+    }
+    for (int g = 0; g < pre->num; ++g) {
+      const int64_t P = pre->lens[g] / kvq::kPrefixGrain * kvq::kPrefixGrain;
+      if (members[(size_t)g].size() < 2 || P == 0) {
+        members[(size_t)g].clear();
+        continue;
+      }
+      int64_t seen = P;
+      if (s->window > 0) {
+        // (what the request that sees least of the prefix sees)
+        for (int r : members[(size_t)g])
+          seen = std::min<int64_t>(seen, std::max<int64_t>(0, P - std::max<int64_t>(0, (int64_t)seq_lens_host[r] - s->window)));
+      }
+      saved += (int64_t)(members[(size_t)g].size() - 1) * seen * heads_kv * 2 * kvq::row_bytes(dtype, head_dim);
+    }
+    int64_t least = kvq::kPrefixMinBytes;
+    if (const char* env = std::getenv("KVQ_PREFIX_MIN_BYTES")) least = std::atoll(env);
+    if (saved >= least) {
+      const int64_t most_rows = kvq::rect_rows(head_dim);
+      for (int g = 0; g < pre->num; ++g) {
+        const int64_t P = pre->lens[g] / kvq::kPrefixGrain * kvq::kPrefixGrain;
+        RectTile t{};
+        auto flush = [&]() {
+          // (a tile whose rows see none of the prefix has no units)
+          if (t.nrows > 0 && t.kv_lo < t.kv_hi) rect.push_back(t);
+          t.nrows = 0;
+        };
+        for (int r : members[(size_t)g]) {
+          const int64_t Q = (int64_t)query_start_loc_host[r + 1] - query_start_loc_host[r];
+          const int64_t p0 = seq_lens_host[r] - Q;
+          if (t.nrows + Q * G > most_rows) flush();
+          const int64_t lo = s->window > 0 ? std::max<int64_t>(0, p0 - s->window + 1) : 0;
+          if (lo >= P) continue;  // sees none of it
+          if (t.nrows == 0) {
+            t = RectTile{};
+            t.req = r;
+            t.tok0 = (int)s->tokens.size();
+            t.kv_lo = P;
+            t.kv_hi = P;
+          }
+          pre_tile[(size_t)r] = (int)rect.size();
+          pre_row[(size_t)r] = t.nrows;
+          t.nrows += (int)(Q * G);
+          t.kv_lo = std::min(t.kv_lo, lo);
+          for (int64_t i = 0; i < Q; ++i)
+            s->tokens.push_back(RectToken{(int32_t)(query_start_loc_host[r] + i), (int32_t)(p0 + i)});
+          ++s->num_shared_requests;
+        }
+        flush();
+      }
+      for (int r = 0; r < num_req; ++r)
+        if (pre_tile[(size_t)r] >= 0)
+          s->shared_keys += pre->lens[pre->of[r]] / kvq::kPrefixGrain * kvq::kPrefixGrain;
+      plan_rect(rect, heads_kv, head_dim, sms, false, forced_tiles, &s->units, &s->partial_rows);
+    }
+  }
+  auto shared = [&](int r) { return !pre_tile.empty() && pre_tile[(size_t)r] >= 0; };
+  // Encoders: requests of more rows than a decode tile.
+  std::vector<int> cross_req;  // of each tile of `rect`
+  if (cross) {
+    for (int r = 0; r < num_req; ++r) {
+      const int64_t Q = (int64_t)query_start_loc_host[r + 1] - query_start_loc_host[r];
+      const int64_t rows = Q * G, L = seq_lens_host[r];
+      if (rows <= kvq::kTileMaxRows || L == 0) continue;
+      const int tok0 = (int)s->tokens.size();
+      for (int64_t i = 0; i < Q; ++i)
+        s->tokens.push_back(RectToken{(int32_t)(query_start_loc_host[r] + i), (int32_t)(L - Q + i)});
+      for (int64_t row0 = 0; row0 < rows; row0 += kvq::rect_rows(head_dim)) {
+        RectTile t{};
+        t.req = r;
+        t.tok0 = tok0;
+        t.row0 = (int)row0;
+        t.nrows = (int)std::min<int64_t>(kvq::rect_rows(head_dim), rows - row0);
+        t.kv_hi = L;
+        rect.push_back(t);
+      }
+      s->max_chunk = std::max<int32_t>(s->max_chunk, (int32_t)((L - 1) / kvq::kChunkTokens));
+    }
+    plan_rect(rect, heads_kv, head_dim, sms, true, forced_tiles, &s->units, &s->partial_rows);
+  }
+  // Rows that the rectangular merge writes: the shared requests' (one item each
+  // (request, kv head)), the cut encoders' and those without keys.
+  std::vector<RectMerge> rect_merges;
+  if (cross) {
+    auto items = [&](int r, int64_t row0, int64_t nrows, const RectTile* t) {
+      for (int h = 0; h < heads_kv; ++h)
+        for (int64_t x = 0; x < nrows; x += kvq::kTileMaxRows) {
+          RectMerge m{};
+          m.m.req = r;
+          m.m.kv_head = h;
+          m.m.row0 = (int32_t)(row0 + x);
+          m.m.nrows = (int32_t)std::min<int64_t>(kvq::kTileMaxRows, nrows - x);
+          m.q0 = query_start_loc_host[r];
+          if (t) {
+            m.pre_part = (int32_t)(t->part + h * t->parts * t->nrows + x);
+            m.pre_splits = (int32_t)t->parts;
+            m.pre_stride = t->nrows;
+          }
+          rect_merges.push_back(m);
+        }
+    };
+    for (const RectTile& t : rect)
+      if (t.parts > 0) items(t.req, t.row0, t.nrows, &t);
+    for (int r = 0; r < num_req; ++r) {
+      const int64_t rows = ((int64_t)query_start_loc_host[r + 1] - query_start_loc_host[r]) * G;
+      if (rows > 0 && seq_lens_host[r] == 0) items(r, 0, rows, nullptr);
+    }
+  }
 
   // 1) Row tiles: the packed rows (q_index * G + g) of each (request,
   //    kv_head) in tiles of up to 16, each with the chunks its rows can see,
@@ -490,7 +826,6 @@ int kvq_get_scheduler_metadata(int num_req, int heads_q, int heads_kv, int head_
   //    rows of the same cache blocks.  Tiles of up to 8 rows use one MMA
   //    n-tile (class 0), larger ones two (class 1).
   std::vector<Tile> tiles[2];
-  s->max_chunk = 0;
   {
     // capacities first (a prefill of many requests has thousands of tiles)
     size_t n_prefill = 0, n_tiles[2] = {0, 0};
@@ -498,6 +833,7 @@ int kvq_get_scheduler_metadata(int num_req, int heads_q, int heads_kv, int head_
       const int64_t rows = ((int64_t)query_start_loc_host[r + 1] - query_start_loc_host[r]) * G;
       if (rows == 0) continue;
       if (rows > kvq::kTileMaxRows) {
+        if (cross) continue;
         n_prefill += (size_t)heads_kv * (size_t)ceil_div(rows, kvq::kPrefillRows);
       } else {
         n_tiles[rows > 8 ? 1 : 0] += (size_t)heads_kv;
@@ -516,8 +852,9 @@ int kvq_get_scheduler_metadata(int num_req, int heads_q, int heads_kv, int head_
   for (int r = 0; r < num_req; ++r) {
     const int64_t L = seq_lens_host[r];
     const int64_t Q = (int64_t)query_start_loc_host[r + 1] - query_start_loc_host[r];
-    if (Q == 0) continue;
+    if (Q == 0 || L == 0) continue;  // (L = 0: an encoder without keys; its rows are the merge's)
     const int64_t rows = Q * G;
+    if (rows > kvq::kTileMaxRows && cross) continue;  // (the units above)
     if (rows > kvq::kTileMaxRows) {
       // Prefill: 128-row tiles on the tensor cores.
       row_prefill.clear();
@@ -556,6 +893,8 @@ int kvq_get_scheduler_metadata(int num_req, int heads_q, int heads_kv, int head_
       t.nrows = (int)nrows;
       t.any_hi = s->causal ? p_max + 1 : L;
       t.any_lo = s->window > 0 ? std::max<int64_t>(0, p_min - s->window + 1) : 0;
+      // (a shared request's own keys; the prefix ends at a chunk's start)
+      if (shared(r)) t.any_lo = std::max(t.any_lo, rect[(size_t)pre_tile[(size_t)r]].kv_hi);
       t.c_lo = t.any_lo / chunk;
       t.c_hi = ceil_div(t.any_hi, chunk);
       s->max_chunk = std::max<int32_t>(s->max_chunk, (int32_t)((t.any_hi - 1) / kvq::kChunkTokens));
@@ -618,7 +957,6 @@ int kvq_get_scheduler_metadata(int num_req, int heads_q, int heads_kv, int head_
   //      second read of a shared line hits L2.
   //    KVQ_DECODE_WARPS (tests, benchmarks) forces the warp count;
   //    KVQ_DECODE_LOCKSTEP = 0 / 1 forces the order.
-  const int sms = have_device ? std::max(1, sm_count()) : kDefaultSmCount;
   int64_t forced = 0;
   if (const char* env = std::getenv("KVQ_DECODE_WARPS")) forced = std::atoll(env);
   bool lockstep = kvq::row_bytes(dtype, head_dim) % 128 != 0;
@@ -626,7 +964,6 @@ int kvq_get_scheduler_metadata(int num_req, int heads_q, int heads_kv, int head_
   // (the 4-bit decode kernel runs the kv heads of a segment in one CTA)
   const bool int4 = kvq::is_int4(dtype);
   lockstep = (lockstep || int4) && heads_kv > 1;
-  s->partial_rows = 0;
   s->max_splits = 0;
   int64_t max_pieces = 0, max_merges = 0, num_warps = 0;
   for (int cls = 0; cls < 2; ++cls) {
@@ -687,25 +1024,23 @@ int kvq_get_scheduler_metadata(int num_req, int heads_q, int heads_kv, int head_
   s->d_warps_off = kvq::align256((size_t)max_pieces * sizeof(DecodePiece));
   s->d_merges_off = s->d_warps_off + kvq::align256((size_t)num_warps * sizeof(WarpSeg));
   s->d_prefill_off = s->d_merges_off + kvq::align256((size_t)max_merges * sizeof(MergeItem));
-  s->d_error_off = s->d_prefill_off + kvq::align256(s->prefill.size() * sizeof(PrefillTile));
+  s->d_units_off = s->d_prefill_off + kvq::align256(s->prefill.size() * sizeof(PrefillTile));
+  s->d_tokens_off = s->d_units_off + kvq::align256(s->units.size() * sizeof(RectUnit));
+  s->d_rmerges_off = s->d_tokens_off + kvq::align256(s->tokens.size() * sizeof(RectToken));
+  const size_t max_rmerges = rect_merges.size() + (size_t)s->num_shared_requests * (size_t)heads_kv;
+  s->d_error_off = s->d_rmerges_off + kvq::align256(max_rmerges * sizeof(RectMerge));
   const size_t total = s->d_error_off + sizeof(int32_t);
   s->image_bytes = total;
   if (have_device) {
     s->d_buf = pool_get(s->device, total, &s->d_buf_bytes);
-    if (!s->d_buf) {
-      delete s;
-      return KVQ_E_NO_MEMORY;
-    }
+    if (!s->d_buf) return KVQ_E_NO_MEMORY;
     s->h_image = pinned_get(total, &s->h_image_bytes, &s->h_image_pinned);
   } else {
     s->h_image = std::malloc(total);
     s->h_image_bytes = total;
     s->h_image_pinned = false;
   }
-  if (!s->h_image) {
-    kvq_sched_destroy(s);
-    return KVQ_E_NO_MEMORY;
-  }
+  if (!s->h_image) return KVQ_E_NO_MEMORY;
   char* image = static_cast<char*>(s->h_image);
   DecodePiece* const P = reinterpret_cast<DecodePiece*>(image + s->d_pieces_off);
   WarpSeg* const WS = reinterpret_cast<WarpSeg*>(image + s->d_warps_off);
@@ -715,6 +1050,13 @@ int kvq_get_scheduler_metadata(int num_req, int heads_q, int heads_kv, int head_
   s->h_merges = M;
   if (!s->prefill.empty())
     std::memcpy(image + s->d_prefill_off, s->prefill.data(), s->prefill.size() * sizeof(PrefillTile));
+  if (!s->units.empty())
+    std::memcpy(image + s->d_units_off, s->units.data(), s->units.size() * sizeof(RectUnit));
+  if (!s->tokens.empty())
+    std::memcpy(image + s->d_tokens_off, s->tokens.data(), s->tokens.size() * sizeof(RectToken));
+  RectMerge* const RM = reinterpret_cast<RectMerge*>(image + s->d_rmerges_off);
+  if (!rect_merges.empty()) std::memcpy(RM, rect_merges.data(), rect_merges.size() * sizeof(RectMerge));
+  int64_t nrmerges = (int64_t)rect_merges.size();
   std::memset(image + s->d_error_off, 0, sizeof(int32_t));  // the error word starts at zero
 
   // 4) Work decomposition (stream-K): per class, lay the tiles' chunks end
@@ -722,7 +1064,7 @@ int kvq_get_scheduler_metadata(int num_req, int heads_q, int heads_kv, int head_
   //    warp.  A tile cut by a segment boundary becomes several pieces whose
   //    partial rows are merged.  (Counters in locals and stores through plain
   //    pointers into the image: this runs once per planned step.)
-  int64_t npieces = 0, nmerges = 0, nwarps = 0, partial_rows = 0, max_splits = 0;
+  int64_t npieces = 0, nmerges = 0, nwarps = 0, partial_rows = s->partial_rows, max_splits = 0;
   std::vector<int64_t> seg;
   for (int cls = 0; cls < 2; ++cls) {
     DecodeLaunch& dl = s->launch[cls];
@@ -774,7 +1116,24 @@ int kvq_get_scheduler_metadata(int num_req, int heads_q, int heads_kv, int head_
       // the ones handed out so far
       int32_t merge = -1;
       int64_t part = -1;
-      if (np > 1) {
+      if (shared(t.req)) {
+        // its pieces' rows, cut or not, are merged with the prefix's
+        const RectTile& rt = rect[(size_t)pre_tile[(size_t)t.req]];
+        RectMerge& m = RM[nrmerges++];
+        m = RectMerge{};
+        m.m.req = t.req;
+        m.m.kv_head = t.kv_head;
+        m.m.row0 = t.row0;
+        m.m.nrows = t.nrows;
+        m.m.part = (int32_t)partial_rows;
+        m.m.nsplits = (int32_t)np;
+        m.pre_part = (int32_t)(rt.part + t.kv_head * rt.parts * rt.nrows + pre_row[(size_t)t.req] + t.row0);
+        m.pre_splits = (int32_t)rt.parts;
+        m.pre_stride = rt.nrows;
+        m.q0 = query_start_loc_host[t.req];
+        part = partial_rows;
+        partial_rows += np * t.nrows;
+      } else if (np > 1) {
         MergeItem& m = M[nmerges];
         m.req = t.req;
         m.kv_head = t.kv_head;
@@ -815,11 +1174,75 @@ int kvq_get_scheduler_metadata(int num_req, int heads_q, int heads_kv, int head_
   }
   s->num_pieces = npieces;
   s->num_merges = nmerges;
+  s->num_rect_merges = nrmerges;
+  // (partial rows are numbered in 32 bits)
+  if (partial_rows > 0x7FFFFFFF) return KVQ_E_UNSUPPORTED;
   s->partial_rows = partial_rows;
   s->max_splits = max_splits;
   s->workspace_bytes = kvq::workspace_bytes(s->partial_rows, head_dim);
   *workspace_bytes = s->workspace_bytes;
-  *out = s;
+  *out = owned.release();
+  return KVQ_OK;
+}
+
+// The planner with the C++ library's exceptions (a host allocation that failed)
+// as a status.
+int plan_or_status(int num_req, int heads_q, int heads_kv, int head_dim, const int32_t* seq_lens_host,
+                   const int32_t* query_start_loc_host, int causal, int window, kvq_dtype_t dtype,
+                   const Prefixes* pre, bool cross, kvq_sched_t** out, size_t* workspace_bytes) {
+  try {
+    return plan_attention(num_req, heads_q, heads_kv, head_dim, seq_lens_host, query_start_loc_host, causal, window,
+                          dtype, pre, cross, out, workspace_bytes);
+  } catch (...) {
+    return KVQ_E_NO_MEMORY;
+  }
+}
+
+}  // namespace
+
+extern "C" {
+
+int kvq_get_scheduler_metadata(int num_req, int heads_q, int heads_kv, int head_dim,
+                               const int32_t* seq_lens_host, const int32_t* query_start_loc_host,
+                               int causal, int window, kvq_dtype_t dtype, kvq_sched_t** out,
+                               size_t* workspace_bytes) {
+  return plan_or_status(num_req, heads_q, heads_kv, head_dim, seq_lens_host, query_start_loc_host, causal, window,
+                        dtype, nullptr, false, out, workspace_bytes);
+}
+
+int kvq_get_shared_prefix_metadata(int num_req, int heads_q, int heads_kv, int head_dim,
+                                   const int32_t* seq_lens_host, const int32_t* query_start_loc_host,
+                                   int num_prefixes, const int32_t* prefix_lens_host,
+                                   const int32_t* request_prefix_host, int window, kvq_dtype_t dtype,
+                                   kvq_sched_t** out, size_t* workspace_bytes) {
+  if (!out || !workspace_bytes) return KVQ_E_INVALID_ARG;
+  *out = nullptr;
+  *workspace_bytes = 0;
+  if (num_prefixes < 0 || (num_prefixes > 0 && !prefix_lens_host) || (num_req > 0 && !request_prefix_host))
+    return KVQ_E_INVALID_ARG;
+  for (int g = 0; g < num_prefixes; ++g)
+    if (prefix_lens_host[g] < 0) return KVQ_E_INVALID_ARG;
+  const Prefixes pre{num_prefixes, prefix_lens_host, request_prefix_host};
+  return plan_or_status(num_req, heads_q, heads_kv, head_dim, seq_lens_host, query_start_loc_host, 1, window, dtype,
+                        &pre, false, out, workspace_bytes);
+}
+
+int kvq_get_cross_attention_metadata(int num_req, int heads_q, int heads_kv, int head_dim,
+                                     const int32_t* encoder_lens_host,
+                                     const int32_t* query_start_loc_host, kvq_dtype_t dtype,
+                                     kvq_sched_t** out, size_t* workspace_bytes) {
+  return plan_or_status(num_req, heads_q, heads_kv, head_dim, encoder_lens_host, query_start_loc_host, 0, 0, dtype,
+                        nullptr, true, out, workspace_bytes);
+}
+
+int kvq_sched_get_rect_info(const kvq_sched_t* s, kvq_rect_info_t* out) {
+  if (!s || !out) return KVQ_E_INVALID_ARG;
+  std::memset(out, 0, sizeof(*out));
+  out->num_units = (int64_t)s->units.size();
+  out->num_merge_items = s->num_rect_merges;
+  out->num_shared_requests = s->num_shared_requests;
+  out->shared_keys = s->shared_keys;
+  out->smem_bytes = kvq::rect_smem_bytes(s->head_dim);
   return KVQ_OK;
 }
 
@@ -925,7 +1348,8 @@ int kvq_sched_get_info(const kvq_sched_t* s, kvq_sched_info_t* out) {
   out->prefill_smem_bytes =
       kvq::prefill_smem_bytes(s->head_dim, kvq::prefill_cta_group(s->dtype, s->head_dim));
   out->num_kernel_launches = (s->launch[0].num_chunks > 0) + (s->launch[1].num_chunks > 0) +
-                             (s->num_merges > 0) + (!s->prefill.empty());
+                             (s->num_merges > 0) + (!s->prefill.empty()) + (!s->units.empty()) +
+                             (s->num_rect_merges > 0);
   out->prefill_cta_group = kvq::prefill_cta_group(s->dtype, s->head_dim);
   return KVQ_OK;
 }
@@ -962,7 +1386,11 @@ int kvq_attention_with_kv_cache(const kvq_sched_t* s, int heads_q, int heads_kv,
       (int)dtype != s->dtype || (causal ? 1 : 0) != s->causal ||
       (window > 0 ? window : 0) != s->window)
     return KVQ_E_SCHED_MISMATCH;
-  if (s->launch[0].num_chunks + s->launch[1].num_chunks == 0 && s->prefill.empty()) return KVQ_OK;
+  if (s->launch[0].num_chunks + s->launch[1].num_chunks == 0 && s->prefill.empty() && s->units.empty() &&
+      s->num_rect_merges == 0)
+    return KVQ_OK;
+  // (an encoder's keys have no position relative to the queries)
+  if (s->cross && alibi_slopes) return KVQ_E_UNSUPPORTED;
   if (!s->d_buf) return KVQ_E_CUDA;  // planned without a device
   int cur = -1;
   if (cudaGetDevice(&cur) != cudaSuccess) return KVQ_E_CUDA;
@@ -1059,6 +1487,16 @@ int kvq_attention_with_kv_cache(const kvq_sched_t* s, int heads_q, int heads_kv,
     if (rc != KVQ_OK) return rc;
     p.beside_prefill = true;
   }
+  kvq::RectParams rp;
+  rp.units = reinterpret_cast<const RectUnit*>(b + s->d_units_off);
+  rp.tokens = reinterpret_cast<const RectToken*>(b + s->d_tokens_off);
+  rp.merges = reinterpret_cast<const RectMerge*>(b + s->d_rmerges_off);
+  rp.num_units = (int)s->units.size();
+  if (rp.num_units > 0) {
+    const int rc = kvq::launch_rect(p, rp, s->dtype, head_dim, stream);
+    if (rc != KVQ_OK) return rc;
+    p.beside_prefill = true;
+  }
   for (int cls = 0; cls < 2; ++cls) {
     const DecodeLaunch& dl = s->launch[cls];
     if (dl.num_chunks == 0) continue;
@@ -1075,7 +1513,9 @@ int kvq_attention_with_kv_cache(const kvq_sched_t* s, int heads_q, int heads_kv,
     if (rc != KVQ_OK) return rc;
     p.beside_prefill = false;
   }
-  return kvq::launch_merge(p, dtype, head_dim, s->num_merges, stream);
+  const int rc = kvq::launch_merge(p, dtype, head_dim, s->num_merges, stream);
+  if (rc != KVQ_OK) return rc;
+  return kvq::launch_rect_merge(p, rp, head_dim, s->num_rect_merges, stream);
 }
 
 // ---- the fused decode step ------------------------------------------------

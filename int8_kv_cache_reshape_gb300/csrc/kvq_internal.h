@@ -227,6 +227,25 @@ KVQ_HD constexpr size_t prefill_smem_bytes(int head_dim, int cta_group = 1) {
          (size_t)kPrefillRows * (head_dim * 2 + 16) + 512 + 1024;
 }
 
+// ---- attention of many rows to one run of keys (kvq_rect.cuh) ---------------
+// Row tiles of 128 rows a CTA holds, each with an O in tensor memory; threads
+// (an issuing, two converting and a softmax warpgroup per row tile); rows of a unit.
+KVQ_HD constexpr int rect_row_tiles(int head_dim) { return head_dim >= 256 ? 1 : 2; }
+KVQ_HD constexpr int rect_threads(int head_dim) { return 128 * (3 + rect_row_tiles(head_dim)); }
+KVQ_HD constexpr int rect_rows(int head_dim) { return 128 * rect_row_tiles(head_dim); }
+// Shared memory: Q, two K and two V tiles (f16), four slots of per-key scales,
+// value-scale maxima and chunk masks, four slot tables, row scales, barriers; +1
+// KB for 1024-byte alignment.
+KVQ_HD constexpr size_t rect_smem_bytes(int head_dim) {
+  return (size_t)rect_rows(head_dim) * head_dim * 2 + 4 * (size_t)prefill_keys(head_dim) * head_dim * 2 +
+         4 * (size_t)(prefill_keys(head_dim) * 8 + 16 + 4 + 64) + (size_t)rect_rows(head_dim) * 4 + 256 + 1024;
+}
+// A prefix's shared part ends at a multiple of this many keys (both plans'
+// chunks); the rest is read with each request's own keys.
+constexpr int kPrefixGrain = 32;
+// Bytes of cache reads that sharing has to save before a batch is planned so.
+constexpr int64_t kPrefixMinBytes = 24 << 20;
+
 // Tensor maps of the caches for bulk tensor copies.  bf16 ("auto") rows, the
 // prefill: a rank-3 bf16 tensor {head_dim, kv heads, slots} copied in boxes
 // of {64, 1, 16 slots} in the 128-byte swizzle.  4-bit rows, the decode: a
@@ -278,6 +297,36 @@ struct MergeItem {
   int32_t pad0, pad1;
 };
 static_assert(sizeof(MergeItem) == 32, "MergeItem layout");
+
+// One unit of the rectangular attention: rows [row0, row0 + nrows) of the
+// packed rows (token * G + head) of the listed tokens from entry tok0, kv head
+// kv_head, keys [kv_lo, kv_hi) through the block-table row of request `req`.
+struct RectUnit {
+  int32_t kv_head, row0, nrows;
+  int32_t kv_lo, kv_hi;
+  int32_t tok0, req;
+  int32_t part;         // partial row of its row 0 (-1: writes out)
+  int32_t part_stride;  // to the partial rows of the second softmax group (one row tile)
+  int32_t pad[3];
+};
+static_assert(sizeof(RectUnit) == 48, "RectUnit layout");
+struct alignas(8) RectToken {
+  int32_t token, pos;  // row of q and out; position
+};
+// Rows whose partials come from the decode's pieces (m) and from units: split s
+// of the latter at pre_part + s * pre_stride.
+struct RectMerge {
+  MergeItem m;
+  int32_t pre_part, pre_splits, pre_stride;
+  int32_t q0;  // the request's first query token
+};
+static_assert(sizeof(RectMerge) == 48, "RectMerge layout");
+struct RectParams {
+  const RectUnit* units;
+  const RectToken* tokens;
+  const RectMerge* merges;
+  int num_units;
+};
 
 // Workspace layout: partial outputs [P][head_dim] fp32, then partial
 // log2-sum-exp [P] fp32, each 256-byte aligned.
@@ -390,6 +439,26 @@ int launch_reshape_and_cache(const void* key, const void* value,
                              int64_t num_blocks, int block_size,
                              const int64_t* slot_mapping, int dtype,
                              float k_scale, float v_scale, void* stream);
+// rotary_and_cache's arguments; strides in elements per token.
+struct RotaryArgs {
+  const uint16_t* query;
+  const uint16_t* key;
+  const uint16_t* value;
+  int64_t num_tokens, query_stride, key_stride, value_stride;
+  int heads_q, heads_kv;
+  const int64_t* positions;
+  const float* cos_sin;  // [max_position, rotary_dim]: cosines, then sines
+  int64_t max_position;
+  int rotary_dim;
+  uint16_t* query_out;
+  int64_t query_out_stride;
+  uint8_t* key_cache;
+  uint8_t* value_cache;
+  int64_t num_slots;
+  const int64_t* slot_mapping;
+  float k_scale, v_scale;
+};
+int launch_rotary_and_cache(const RotaryArgs& a, int dtype, int head_dim, bool interleaved, void* stream);
 // gather_cache's arguments; strides in elements per token.
 struct GatherArgs {
   const uint8_t* key_cache;
@@ -433,6 +502,9 @@ int launch_merge_step(const AttnParams& p, const StepParams& sp, int dtype, int 
 // (at most one per SM is resident).
 int launch_prefill(const AttnParams& p, const PrefillMaps& maps, int dtype, int head_dim,
                    int64_t ctas, void* stream);
+// The units of a plan (kvq_rect.cuh), and the merge of their rows.
+int launch_rect(const AttnParams& p, const RectParams& rp, int dtype, int head_dim, void* stream);
+int launch_rect_merge(const AttnParams& p, const RectParams& rp, int head_dim, int64_t num_merges, void* stream);
 #ifdef __CUDACC__
 // Launch a kernel without dynamic shared memory as a programmatic dependent
 // of the kernel before it on the stream: it may be resident before that one

@@ -163,6 +163,17 @@ __global__ void __launch_bounds__(kMergeThreads) merge_splits_kernel(const AttnP
   merge_tile<D, true>(p, m, q0, m.nsplits, [&](int s) { return m.part + s * m.nrows; });
 }
 
+// Rows with partials of rectangular units (kvq_rect.cuh) beside those of the
+// decode's pieces, or alone: a shared prefix's, an encoder's.
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) merge_rect_kernel(const AttnParams p, const RectParams rp) {
+  const RectMerge r = rp.merges[blockIdx.x];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  merge_tile<D, true>(p, r.m, r.q0, r.m.nsplits + r.pre_splits, [&](int s) {
+    return s < r.m.nsplits ? r.m.part + s * r.m.nrows : r.pre_part + (s - r.m.nsplits) * r.pre_stride;
+  });
+}
+
 // The fused decode step: tile blockIdx.x (request t / Hkv, kv head t % Hkv)
 // of the device-built plan, if its chunks span more than one warp segment.
 // The fused kernel cut its flat chunk sequence into `warps` equal segments;

@@ -1,0 +1,833 @@
+// kvq_rect.cuh -- attention of many rows to one run of cached keys, without
+// a causal edge inside it: the keys of a prefix that requests share, or an
+// encoder's keys (5th-generation tensor cores, accumulators in tensor memory).
+//
+// What it computes: a unit is up to 256 packed (query token, head) rows of
+// one kv head -- 128 at head_dim 256 -- and a range of keys read through one
+// block-table row.  For each row r: the reference m_r, l_r = sum_j 2^(z_rj -
+// m_r + 6) and o_r = sum_j 2^(z_rj - m_r + 6) v_j / l_r over the range's keys
+// that it sees (all, but for a sliding window), z in log2 units with the scale, the
+// soft cap and the ALiBi bias.  Units that hold all keys of their rows write
+// bf16 rows; others leave (o_r, m_r + log2 l_r) in fp32 for the merge.
+//
+// Why a kernel of its own beside the prefill (kvq_prefill.cuh): a prefix is
+// converted to f16 once per 256 rows, so the converters stay below the MMAs'
+// pace; two row tiles share each KV tile and the tensor core always has the
+// other tile's product to run while one tile's softmax works; the keys
+// of one row tile may be cut among many CTAs, which a causal prefill need not be.
+//
+// Layout (one CTA per SM, one unit per CTA; warpgroups):
+//   0     warp 0 issues the MMAs, warp 1 resolves 16-key chunks through the
+//         block table into slots, up to four KV tiles ahead
+//   1, 2  converters: one group takes K, the other V, each thread 16 codes (4-bit:
+//         32) of a key at a time, loaded into registers a KV tile ahead,
+//         converted exactly to f16 and stored in the 128-byte swizzle into two-stage
+//         rings; bf16 rows are copied as they are (cp.async, dead keys zero)
+//   3, 4  softmax: thread = row = tensor-memory lane (head_dim 256: group 3 only)
+// Items: an item is S = Q K^T of a row tile against a KV tile (kN keys) and then
+// O += P V.  Item i has S buffer i mod 2; P replaces S in it.  The MMA warp
+// issues S(0), S(1), then PV(i), S(i + 2), in order.
+//   two row tiles (129 to 256 rows): item i is row tile i mod 2 and KV tile i / 2
+//   one row tile (up to 128 rows): item i is KV tile i, and the two softmax groups
+//     take every other KV tile with an O of their own (two partials a row):
+//     both S buffers and both groups stay busy
+//   head_dim 256: O takes half of tensor memory; item i is KV tile i, one group
+// Numbers as in the prefill: Q enters as f16 scaled by a power of two per row
+// (bf16 rows: as it is), scales multiply fp32 scores, value scales fold into P against
+// a running power of two, the reference m is an integer that moves when a score
+// exceeds it by 2^8, every sum is fp32.  P is f16 (11 bits; bf16 rows: two bf16
+// numbers, 16 bits): the operand type of the MMA.
+// Every wait is bounded (about a second); a unit that gave up leaves NaN rows and
+// sets the schedule's error word.
+#pragma once
+
+#include "kvq_prefill.cuh"
+
+namespace kvq {
+
+template <int DT, int D>
+struct RectGeom {
+  static constexpr bool kAuto = DT == KVQ_AUTO, kInt4 = is_int4(DT), kPth = is_per_token_head(DT);
+  static constexpr int kRT = rect_row_tiles(D);       // row tiles with an O of their own
+  static constexpr int kM = 128, kN = prefill_keys(D);
+  static constexpr int kThreads = rect_threads(D);
+  static constexpr int kStages = 2, kSide = 4, kSlotRing = 4;
+  static constexpr int kQBytes = kM * D * 2;          // a row tile's Q
+  static constexpr int kTileBytes = kN * D * 2;       // a KV tile's K or V
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffK = kOffQ + kRT * kQBytes;
+  static constexpr int kOffV = kOffK + kStages * kTileBytes;
+  static constexpr int kOffSk = kOffV + kStages * kTileBytes;   // kSide x kN f32
+  static constexpr int kOffSv = kOffSk + kSide * kN * 4;        // kSide x kN f32
+  static constexpr int kOffVMax = kOffSv + kSide * kN * 4;      // kSide x 4 u32
+  static constexpr int kOffSMask = kOffVMax + kSide * 16;       // kSide u32
+  static constexpr int kOffSlots = kOffSMask + kSide * 4;       // kSlotRing x 16 i32
+  static constexpr int kOffQScale = kOffSlots + kSlotRing * 64; // kRT x kM f32
+  static constexpr int kOffBar = kOffQScale + kRT * kM * 4;
+  static constexpr int kBytes = kOffBar + 256;
+  static constexpr int kColO = 0, kColS = kRT * D;
+  static constexpr int kTmemCols = 512;
+  static constexpr int kBarSlots = 0, kBarSlotsFree = 4, kBarSide = 8, kBarKFull = 12, kBarVFull = 14, kBarKEmpty = 16,
+                       kBarVEmpty = 18, kBarSFull = 20, kBarPFull = 22, kBarOFinal = 24, kBarQFull = 26, kBarODone = 28,
+                       kBarDrain = 29, kNumBars = 30;
+  static constexpr int kOffTmemSlot = kOffBar + 8 * kNumBars, kOffAbort = kOffTmemSlot + 4;
+  static_assert(kColS + 2 * kN <= kTmemCols, "tensor memory");
+  static_assert(kQBytes % 1024 == 0 && kTileBytes % 1024 == 0 && kOffBar % 8 == 0 && kOffSk % 16 == 0, "alignment");
+  static_assert(kOffAbort + 4 <= kBytes && (size_t)kBytes + 1024 == rect_smem_bytes(D), "shared memory");
+};
+
+// Registers a thread of each warpgroup, out of the launch's (65,536 / threads,
+// a multiple of 8): 640 x 96 = 61,440 at head_dim 64 and 128, 512 x 128 at 256.
+template <int D>
+struct RectRegs {
+  static constexpr int kIssue = D >= 256 ? 64 : 56, kConvert = D >= 256 ? 104 : 80, kSoftmax = D >= 256 ? 232 : 128;
+  static constexpr int kLaunch = D >= 256 ? 128 : 96;
+  static_assert(kIssue + 2 * kConvert + rect_row_tiles(D) * kSoftmax <= (3 + rect_row_tiles(D)) * kLaunch,
+                "the groups' registers come out of the launch's");
+};
+
+template <int N>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(N));
+}
+
+template <int DT, int D>
+__global__ void __launch_bounds__(rect_threads(D), 1) rect_attention_kernel(const AttnParams p, const RectParams rp) {
+  using Geo = RectGeom<DT, D>;
+  using Regs = RectRegs<D>;
+  constexpr int kM = Geo::kM, kN = Geo::kN, kRT = Geo::kRT;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = dev::smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* const sm = smem_raw + (base - raw);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wg = warp >> 2;
+  const uint32_t bars = base + Geo::kOffBar;
+  auto bar = [&](int i) { return bars + 8u * (uint32_t)i; };
+  volatile uint32_t* const abort_flag = reinterpret_cast<volatile uint32_t*>(sm + Geo::kOffAbort);
+
+  if (tid == 0) {
+    for (int s = 0; s < 4; ++s) {
+      tc::mbar_init(bar(Geo::kBarSlots + s), 1);
+      tc::mbar_init(bar(Geo::kBarSlotsFree + s), 8);
+      tc::mbar_init(bar(Geo::kBarSide + s), 4);
+    }
+    for (int s = 0; s < 2; ++s) {
+      tc::mbar_init(bar(Geo::kBarKFull + s), 4);
+      tc::mbar_init(bar(Geo::kBarVFull + s), 4);
+      tc::mbar_init(bar(Geo::kBarKEmpty + s), 1);
+      tc::mbar_init(bar(Geo::kBarVEmpty + s), 1);
+      tc::mbar_init(bar(Geo::kBarSFull + s), 1);
+      tc::mbar_init(bar(Geo::kBarPFull + s), 4);
+      tc::mbar_init(bar(Geo::kBarOFinal + s), 1);
+      tc::mbar_init(bar(Geo::kBarQFull + s), 4);
+    }
+    tc::mbar_init(bar(Geo::kBarODone), 1);
+    tc::mbar_init(bar(Geo::kBarDrain), 1);
+    *abort_flag = 0u;
+    tc::mbar_fence_init();
+  }
+  if (warp == 0) {
+    tc::tmem_alloc(base + Geo::kOffTmemSlot, Geo::kTmemCols);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + Geo::kOffTmemSlot);
+  // A programmatic dependent of the kernel ahead: nothing that it wrote is
+  // read before this wait, and what comes after this kernel may start only now.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  const RectUnit* const up = rp.units + blockIdx.x;
+  const int nrows = __ldg(&up->nrows), kv_lo = __ldg(&up->kv_lo), kv_hi = __ldg(&up->kv_hi);
+  const int kv_head = __ldg(&up->kv_head);
+  const int kv_first = kv_lo / kN * kN;
+  const int T = (kv_hi - kv_first + kN - 1) / kN;  // KV tiles (one at least)
+  const bool two = kRT == 2 && nrows > kM;          // two row tiles, else one
+  constexpr int kChunks = kN / 16;
+  constexpr uint32_t kAllChunks = (1u << kChunks) - 1u;
+  const int G = p.group;
+
+  if (wg == 0) {
+    regs_down<Regs::kIssue>();
+    if (warp == 0) {
+      // ---- MMA issuer (see the items above) ------------------------------
+      const bool leader = elect_one();
+      constexpr uint32_t idesc_s = Geo::kAuto ? tc::idesc_bf16(kM, kN) : tc::idesc_f16(kM, kN);
+      constexpr uint32_t idesc_o = (Geo::kAuto ? tc::idesc_bf16(kM, D) : tc::idesc_f16(kM, D)) | tc::kBMajorMN;
+      const int n = two ? 2 * T : T;
+      auto tile_of = [&](int i) { return two ? i >> 1 : i; };
+      auto wait = [&](int b, int phase) {
+        return __all_sync(0xffffffffu, wait_or_abort(bar(b), (uint32_t)(phase & 1), abort_flag));
+      };
+      int k_in = -1, v_in = -1;  // KV tiles whose K / V have been waited for
+      auto issue_s = [&](int i) -> bool {
+        const int g = tile_of(i), st = g & 1, qt = two ? i & 1 : 0;
+        if ((i == 0 || (two && i == 1)) && !wait(Geo::kBarQFull + qt, 0)) return false;
+        if (g > k_in) {
+          if (!wait(Geo::kBarKFull + st, g >> 1)) return false;
+          k_in = g;
+        }
+        tc::fence_after_sync();
+        const uint64_t dq = tc::desc_sw128(base + Geo::kOffQ + (uint32_t)(qt * Geo::kQBytes));
+        const uint64_t dk = tc::desc_sw128(base + Geo::kOffK + (uint32_t)(st * Geo::kTileBytes));
+        if (leader) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t qoff = (kk >> 2) * (kM * 128) + (kk & 3) * 32, koff = (kk >> 2) * (kN * 128) + (kk & 3) * 32;
+            // (kind::f16: the instruction descriptor names the 16-bit type)
+            tc::mma_bf16(tmem + Geo::kColS + (uint32_t)((i & 1) * kN), dq + (uint64_t)(qoff >> 4),
+                         dk + (uint64_t)(koff >> 4), idesc_s, kk > 0 ? 1u : 0u);
+          }
+          tc::mma_commit(bar(Geo::kBarSFull + (i & 1)));
+          if (!two || (i & 1)) tc::mma_commit(bar(Geo::kBarKEmpty + st));
+        }
+        __syncwarp();
+        return true;
+      };
+      bool ok = true;
+      int next = 0;
+      for (; next < 2 && next < n && ok; ++next) ok = issue_s(next);
+      for (int i = 0; i < n && ok; ++i) {
+        const int g = tile_of(i), st = g & 1;
+        ok = wait(Geo::kBarPFull + (i & 1), i >> 1);
+        if (ok && g > v_in) {
+          ok = wait(Geo::kBarVFull + st, g >> 1);
+          v_in = g;
+        }
+        if (!ok) break;
+        tc::fence_after_sync();
+        const uint64_t dv = tc::desc_sw128_mn(base + Geo::kOffV + (uint32_t)(st * Geo::kTileBytes), kN * 128, 1024);
+        const uint32_t o = tmem + Geo::kColO + (kRT == 2 ? (uint32_t)((i & 1) * D) : 0u);
+        const uint32_t pcol = tmem + Geo::kColS + (uint32_t)((i & 1) * kN);
+        const bool first = i < kRT;
+        if (leader) {
+#pragma unroll
+          for (int kk = 0; kk < kN / 16; ++kk) {
+            if constexpr (Geo::kAuto) {
+              // P = hi + lo, both bf16: hi of keys c0 .. c0 + 63 in columns c0 ..
+              // c0 + 31, lo in c0 + 32 .. c0 + 63
+              const uint32_t pc = pcol + (uint32_t)(64 * (kk / 4) + 8 * (kk % 4));
+              tc::mma_ts(o, pc, dv + (uint64_t)(kk * (2048 >> 4)), idesc_o, (!first || kk > 0) ? 1u : 0u);
+              tc::mma_ts(o, pc + 32u, dv + (uint64_t)(kk * (2048 >> 4)), idesc_o, 1u);
+            } else {
+              tc::mma_ts(o, pcol + (uint32_t)(kk * 8), dv + (uint64_t)(kk * (2048 >> 4)), idesc_o,
+                         (!first || kk > 0) ? 1u : 0u);
+            }
+          }
+          if (kRT == 1) tc::mma_commit(bar(Geo::kBarODone));
+          if (!two || (i & 1)) tc::mma_commit(bar(Geo::kBarVEmpty + st));
+          if (i + kRT >= n) tc::mma_commit(bar(Geo::kBarOFinal + (kRT == 2 ? i & 1 : 0)));
+        }
+        __syncwarp();
+        if (next < n) ok = issue_s(next++);
+      }
+      if (!ok && leader) {
+        // drain what was issued before the tensor memory is freed
+        tc::mma_commit(bar(Geo::kBarDrain));
+        (void)tc::mbar_wait(bar(Geo::kBarDrain), 0u, 200000000LL);
+      }
+      __syncwarp();
+    } else if (warp == 1) {
+      // ---- slots of the KV tiles' 16-key chunks --------------------------
+      // (entries are loaded a tile ahead; the block size is a multiple of 16;
+      // q = hi32(j floor((2^32 - 1) / B)) is the quotient or one less)
+      const int32_t* const btab = p.block_table + (int64_t)__ldg(&up->req) * p.block_table_stride;
+      const uint32_t bsz = (uint32_t)p.block_size, bdiv = 0xFFFFFFFFu / bsz;
+      int32_t* const table = reinterpret_cast<int32_t*>(sm + Geo::kOffSlots);
+      // lane c < kChunks looks after chunk c
+      auto fetch = [&](int g, int& blk, int& off) {
+        blk = -1;
+        off = 0;
+        const int j0 = kv_first + g * kN + 16 * lane;
+        if (lane < kChunks && g < T && j0 + 16 > kv_lo && j0 < kv_hi) {
+          uint32_t q = __umulhi((uint32_t)j0, bdiv), r = (uint32_t)j0 - q * bsz;
+          if (r >= bsz) {
+            ++q;
+            r -= bsz;
+          }
+          blk = __ldcg(btab + q);
+          off = (int)r;
+        }
+      };
+      int blk, off;
+      fetch(0, blk, off);
+      for (int g = 0; g < T; ++g) {
+        const int e = g & 3;
+        if (g >= 4 && !__all_sync(0xffffffffu, wait_or_abort(bar(Geo::kBarSlotsFree + e), (uint32_t)(((g >> 2) - 1) & 1),
+                                                             abort_flag)))
+          break;
+        const bool in = blk >= 0 && (int64_t)blk < p.num_blocks;
+        const uint32_t mask = __ballot_sync(0xffffffffu, in);
+        if (lane < kChunks) table[e * 16 + lane] = in ? blk * (int)bsz + off : 0;  // < num_blocks * block_size < 2^31
+        if (lane == 15) table[e * 16 + 15] = (int32_t)mask;
+        warp_arrive(bar(Geo::kBarSlots + e));
+        fetch(g + 1, blk, off);
+      }
+      __syncwarp();
+    }
+  } else if (wg <= 2) {
+    // ---- converters: K (group 1) or V (group 2) ----------------------------
+    regs_down<Regs::kConvert>();
+    const bool for_v = wg == 2;
+    const int ct = tid & 127;
+    const uint8_t* const cache = for_v ? p.value_cache : p.key_cache;
+    const uint32_t tiles = base + (for_v ? Geo::kOffV : Geo::kOffK);
+    const int bar_empty = for_v ? Geo::kBarVEmpty : Geo::kBarKEmpty, bar_full = for_v ? Geo::kBarVFull : Geo::kBarKFull;
+    const int32_t* const table = reinterpret_cast<const int32_t*>(sm + Geo::kOffSlots);
+    float* const sk = reinterpret_cast<float*>(sm + Geo::kOffSk);
+    float* const sv = reinterpret_cast<float*>(sm + Geo::kOffSv);
+    uint32_t* const vmaxw = reinterpret_cast<uint32_t*>(sm + Geo::kOffVMax);
+    uint32_t* const smask = reinterpret_cast<uint32_t*>(sm + Geo::kOffSMask);
+    constexpr int64_t kRow = row_bytes(DT, D);
+    const int64_t tok_bytes = (int64_t)p.heads_kv * kRow;
+    const uint8_t* const head_at = cache + kv_head * kRow;
+    auto wait = [&](int b, int phase) {
+      return __all_sync(0xffffffffu, wait_or_abort(bar(b), (uint32_t)(phase & 1), abort_flag));
+    };
+    // the live keys of KV tile g, relative to its first
+    auto live_lo = [&](int g) { return max(kv_lo - (kv_first + g * kN), 0); };
+    auto live_hi = [&](int g) { return min(kv_hi - (kv_first + g * kN), kN); };
+    if constexpr (Geo::kAuto) {
+      // 16-byte pieces of bf16 rows straight into the operand tile; a stage's
+      // copies are in flight while the next stage's are issued
+      constexpr int kPieces = D / 8, kStepN = 128 / kPieces, kCopies = kN / kStepN;
+      const int pc = ct % kPieces, n0 = ct / kPieces;
+      auto done = [&](int g) {
+        tc::fence_async_smem();
+        warp_arrive(bar(bar_full + (g & 1)));
+      };
+      bool ok = true;
+      for (int g = 0; g < T; ++g) {
+        const int e = g & 3, st = g & 1;
+        if (!(ok = wait(Geo::kBarSlots + e, g >> 2))) break;
+        if (g >= 2 && !(ok = wait(bar_empty + st, (g >> 1) - 1))) break;
+        const uint32_t valid = (uint32_t)table[e * 16 + 15];
+        const int lo = live_lo(g), hi = live_hi(g);
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i) {
+          const int nn = n0 + i * kStepN;
+          const bool on = ((valid >> (nn >> 4)) & 1u) && nn >= lo && nn < hi;
+          const int64_t slot = on ? table[e * 16 + (nn >> 4)] + (nn & 15) : 0;
+          dev::cp_async_16(tiles + (uint32_t)(st * Geo::kTileBytes + (pc >> 3) * kN * 128 + nn * 128 +
+                                              (((pc & 7) ^ (nn & 7)) << 4)),
+                           head_at + slot * tok_bytes + 16 * pc, on ? 16 : 0);
+        }
+        dev::cp_async_commit();
+        if (for_v) {
+          if (ct == 0) smask[e] = valid;
+          warp_arrive(bar(Geo::kBarSide + e));
+        }
+        warp_arrive(bar(Geo::kBarSlotsFree + e));
+        if (g > 0) {
+          dev::cp_async_wait<1>();
+          done(g - 1);
+        }
+      }
+      dev::cp_async_wait<0>();
+      if (ok) done(T - 1);
+    } else {
+      // units of (key, 16 codes) or, 4-bit, (key, 32 codes): a thread keeps its piece
+      // of the row, and its keys differ by a multiple of 8 (4-bit: of 16), so that
+      // its offsets in the swizzle are constants
+      constexpr int kPieces = Geo::kInt4 ? D / 32 : D / 16, kStepN = 128 / kPieces, kUnits = kN / kStepN;
+      static_assert(kStepN % 8 == 0 && kN % kStepN == 0, "units");
+      // 4-bit lanes: two pieces of a 64-dim block, four keys, then the blocks and
+      // further keys (a quarter-warp's stores then fall on 8 bank groups); 8-bit: the
+      // pieces of a key side by side, odd 64-dim blocks storing their halves in
+      // the other order
+      constexpr int kBlocks = D / 64;
+      const int pc = Geo::kInt4 ? 2 * ((ct >> 3) % kBlocks) + (ct & 1) : ct % kPieces;
+      const int n0 = Geo::kInt4 ? ((ct >> 1) & 3) + 4 * (ct / (8 * kBlocks)) : ct / kPieces;
+      const bool odd = !Geo::kInt4 && ((pc >> 2) & 1);
+      const uint32_t at0 = Geo::kInt4 ? (uint32_t)((pc >> 1) * kN * 128 + n0 * 128)
+                                      : (uint32_t)((pc >> 2) * kN * 128 + n0 * 128);
+      const uint32_t chunk0 = Geo::kInt4 ? (uint32_t)((4 * (pc & 1)) ^ (n0 & 7))
+                                         : (uint32_t)((2 * (pc & 3) + (odd ? 1 : 0)) ^ (n0 & 7));
+      const uint8_t* const from = head_at + 16 * pc;
+      const uint8_t* const mul = head_at + D / 2 + 4 + (D == 64 ? 4 : D == 128 ? 2 : 1) * pc;
+      uint4 c[kUnits];
+      uint32_t cm[Geo::kInt4 ? kUnits : 1];
+      float ks = 0.0f, vs = 0.0f;
+      uint32_t valid = 0;
+      auto load_tile = [&](int g) -> bool {
+        const int e = g & 3;
+        if (!wait(Geo::kBarSlots + e, g >> 2)) return false;
+        valid = (uint32_t)table[e * 16 + 15];
+        const int lo = live_lo(g), hi = live_hi(g);
+        auto load = [&](int i, int nn) {
+          const int64_t off = (int64_t)(table[e * 16 + (nn >> 4)] + (nn & 15)) * tok_bytes;
+          c[i] = dev::ldg_stream_coherent(from + off);
+          if constexpr (Geo::kInt4) {
+            if constexpr (D == 64) cm[i] = *reinterpret_cast<const uint32_t*>(mul + off);
+            else if constexpr (D == 128) cm[i] = *reinterpret_cast<const uint16_t*>(mul + off);
+            else cm[i] = *(mul + off);
+          }
+        };
+        if (valid == kAllChunks && lo == 0 && hi == kN) {
+#pragma unroll
+          for (int i = 0; i < kUnits; ++i) load(i, n0 + i * kStepN);
+        } else {
+#pragma unroll
+          for (int i = 0; i < kUnits; ++i) {
+            c[i] = make_uint4(0, 0, 0, 0);
+            if constexpr (Geo::kInt4) cm[i] = 0;
+            const int nn = n0 + i * kStepN;
+            if (((valid >> (nn >> 4)) & 1u) && nn >= lo && nn < hi) load(i, nn);
+          }
+        }
+        if constexpr (Geo::kPth) {
+          // (key ct's two scales; 0 for a dead key)
+          ks = vs = 0.0f;
+          if (for_v && ct < kN && ((valid >> (ct >> 4)) & 1u) && ct >= lo && ct < hi) {
+            const int64_t off = (int64_t)(table[e * 16 + (ct >> 4)] + (ct & 15)) * tok_bytes + kv_head * kRow +
+                                code_bytes(DT, D);
+            ks = __ldcg(reinterpret_cast<const float*>(p.key_cache + off));
+            vs = __ldcg(reinterpret_cast<const float*>(p.value_cache + off));
+          }
+        }
+        warp_arrive(bar(Geo::kBarSlotsFree + e));
+        return true;
+      };
+      bool ok = load_tile(0);
+      for (int g = 0; ok && g < T; ++g) {
+        const int st = g & 1, sd = g & 3;
+        if (g >= 2 && !wait(bar_empty + st, (g >> 1) - 1)) break;
+        if (for_v) {
+          // side data for the softmax in slot g mod 4: its last reader, of KV tile
+          // g - 4, is done (P(g - 2) V(g - 2) is complete)
+          if (ct == 0) smask[sd] = valid;
+          if constexpr (Geo::kPth) {
+            if (ct < kN) {
+              sk[sd * kN + ct] = ks;
+              sv[sd * kN + ct] = vs;
+            }
+            const float vmax = fmaxf(vs, 0.0f);  // (a NaN or negative scale is ignored)
+            const uint32_t wmax = __reduce_max_sync(0xffffffffu, __float_as_uint(vmax));
+            if (lane == 0) vmaxw[sd * 4 + (ct >> 5)] = wmax;
+          }
+          warp_arrive(bar(Geo::kBarSide + sd));
+        }
+        const uint32_t tile = tiles + (uint32_t)(st * Geo::kTileBytes) + at0;
+        if constexpr (Geo::kInt4) {
+#pragma unroll
+          for (int i = 0; i < kUnits; ++i) {
+            const uint32_t w[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
+            dev::Int4Mul f[4];
+            if constexpr (D == 64) {
+#pragma unroll
+              for (int q = 0; q < 4; ++q) f[q] = dev::int4_mul(dev::prmt(cm[i], 0x64646464u, 0x4040u + 0x101u * q));
+            } else {
+              f[0] = f[1] = dev::int4_mul(dev::prmt(cm[i], 0x64646464u, 0x4040u));
+              f[2] = f[3] = D == 128 ? dev::int4_mul(dev::prmt(cm[i], 0x64646464u, 0x4141u)) : f[0];
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              uint32_t h[4];
+              dev::int4_to_f16x2x4(w[q], f[q], h);
+              sts128(tile + (uint32_t)(i * kStepN * 128) + ((chunk0 ^ (uint32_t)q) << 4), make_uint4(h[0], h[1], h[2], h[3]));
+            }
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < kUnits; ++i) {
+            const uint32_t at = tile + (uint32_t)(i * kStepN * 128);
+            sts128(at + (chunk0 << 4), codes8_to_f16<DT>(odd ? c[i].z : c[i].x, odd ? c[i].w : c[i].y));
+            sts128(at + ((chunk0 ^ 1u) << 4), codes8_to_f16<DT>(odd ? c[i].x : c[i].z, odd ? c[i].y : c[i].w));
+          }
+        }
+        tc::fence_async_smem();
+        warp_arrive(bar(bar_full + st));
+        if (g + 1 < T) ok = load_tile(g + 1);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ---- softmax -------------------------------------------------------------
+    regs_up<Regs::kSoftmax>();
+    const int t = wg - 3;                    // this group's O and S buffer
+    const int m = tid & 127;                 // row in its tile, tensor-memory lane
+    const int tile = two ? t : 0;            // row tile
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const float log2e = 1.4426950408889634f;
+    const int R = tile * kM + m;             // row of the unit
+    const bool row_valid = R < nrows;
+    // the row's token (its row of q and out, its position) and head
+    const int packed = __ldg(&up->row0) + (row_valid ? R : 0);
+    const int2 token = __ldg(reinterpret_cast<const int2*>(rp.tokens) + __ldg(&up->tok0) + packed / G);
+    const int head_q = kv_head * G + packed % G, pos = token.y;
+    const int64_t row_off = ((int64_t)token.x * p.heads_q + head_q) * D;
+    float* const qscale = reinterpret_cast<float*>(sm + Geo::kOffQScale) + tile * kM;
+    bool ok = true;
+    if (two || t == 0) {
+      // Q of the warp's 32 rows: D / 8 lanes a row, 16 bytes each.  A row enters
+      // as f16 scaled by the power of two that puts its largest |q| in [2^13,
+      // 2^14): exact but for elements 2^27 below that one (subnormals).  The
+      // score scale's sign enters with Q, so that the softmax's factor is positive.
+      constexpr int kLpr = D / 8, kRpi = 32 / kLpr, kBatch = 8;
+      const float qk_scale = Geo::kPth || Geo::kAuto ? p.sm_scale : p.sm_scale * p.k_scale;
+      const float sign = qk_scale > 0.0f ? 1.0f : qk_scale < 0.0f ? -1.0f : 0.0f;
+      const uint32_t keep = qk_scale == 0.0f ? 0u : 0xFFFFFFFFu, flip = qk_scale < 0.0f ? 0x80008000u : 0u;
+      const int sub = lane / kLpr, pc = lane % kLpr;
+      const uint32_t qt = base + Geo::kOffQ + (uint32_t)(tile * Geo::kQBytes + (pc >> 3) * (kM * 128));
+#pragma unroll 1
+      for (int r0 = 0; r0 < 32; r0 += kBatch * kRpi) {
+        uint4 x[kBatch];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+          const int r = (r0 + b * kRpi + sub) & 31;
+          const int64_t off = __shfl_sync(0xffffffffu, row_off, r);
+          const bool live = __shfl_sync(0xffffffffu, (int)row_valid, r) != 0;
+          x[b] = live ? dev::ldg_stream_coherent(p.q + off + 8 * pc) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+          const int r = r0 + b * kRpi + sub;
+          uint32_t w[4] = {x[b].x, x[b].y, x[b].z, x[b].w};
+          if constexpr (Geo::kAuto) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = (w[e] & keep) ^ flip;
+            if (pc == 0 && r < 32) qscale[(warp & 3) * 32 + r] = 1.0f;
+          } else {
+            uint32_t big = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) big = dev::max_u16x2(big, w[e] & 0x7FFF7FFFu);
+#pragma unroll
+            for (int o = 1; o < kLpr; o <<= 1) big = dev::max_u16x2(big, __shfl_xor_sync(0xffffffffu, big, o));
+            const int emax = (int)(max(big & 0xFFFFu, big >> 16) >> 7);  // largest |q| < 2^(emax - 126)
+            const int sh = emax == 0 ? 0 : min(140 - emax, 126);
+            const float f = ldexpf(sign, sh);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = dev::pack_f16x2(dev::bf16_lo(w[e]) * f, dev::bf16_hi(w[e]) * f);
+            if (pc == 0 && r < 32) qscale[(warp & 3) * 32 + r] = ldexpf(1.0f, -sh);
+          }
+          const int row = (warp & 3) * 32 + r;
+          if (r < 32)
+            sts128(qt + (uint32_t)(row * 128 + (((pc & 7) ^ (row & 7)) << 4)), make_uint4(w[0], w[1], w[2], w[3]));
+        }
+      }
+      tc::fence_async_smem();
+      warp_arrive(bar(Geo::kBarQFull + tile));
+    }
+    // (the other group's rows where both take the one row tile)
+    ok = __all_sync(0xffffffffu, wait_or_abort(bar(Geo::kBarQFull + tile), 0u, abort_flag));
+    const float q_unscale = qscale[m];
+
+    const float* const sk = reinterpret_cast<const float*>(sm + Geo::kOffSk);
+    const float* const sv = reinterpret_cast<const float*>(sm + Geo::kOffSv);
+    const uint32_t* const vmaxw = reinterpret_cast<const uint32_t*>(sm + Geo::kOffVMax);
+    const uint32_t* const smask = reinterpret_cast<const uint32_t*>(sm + Geo::kOffSMask);
+    const float cap = p.soft_cap, cap_l2 = cap * log2e, inv_cap = cap > 0.0f ? 1.0f / cap : 0.0f;
+    const bool plain = cap <= 0.0f && p.alibi_slopes == nullptr;
+    const float slope = p.alibi_slopes ? p.alibi_slopes[head_q] * log2e : 0.0f;
+    const int row_hi = row_valid ? kv_hi : 0;  // padding rows see nothing
+    const int row_lo = max(kv_lo, p.window > 0 ? pos - p.window + 1 : 0);
+    // scores in log2 units (natural units under a soft cap); never zero, which times -inf is NaN
+    const float signed_mul = p.sm_scale * (Geo::kInt4 ? dev::kInt4Unit : 1.0f) * q_unscale *
+                             (cap > 0.0f ? 1.0f : log2e) * (Geo::kPth || Geo::kAuto ? 1.0f : p.k_scale);
+    const float score_mul = fmaxf(fabsf(signed_mul), 0x1p-126f);
+    const int count = kRT == 1 || two ? T : (T - t + 1) / 2;  // this group's items
+    const uint32_t tmem_o = tmem + Geo::kColO + (kRT == 2 ? (uint32_t)(t * D) : 0u) + lane_base;
+    float m_ref = -INFINITY, l_sum = 0.0f;
+    int ev = -1000;  // exponent of the value-scale reference (per-token-head)
+    for (int k = 0; ok && k < count; ++k) {
+      const int i = kRT == 1 ? k : 2 * k + t;  // item
+      const int g = two ? k : i;               // KV tile
+      const int st = i & 1, sd = g & 3;
+      const int kv0 = kv_first + g * kN;
+      ok = wait_or_abort(bar(Geo::kBarSFull + st), (uint32_t)((i >> 1) & 1), abort_flag) &&
+           wait_or_abort(bar(Geo::kBarSide + sd), (uint32_t)((g >> 2) & 1), abort_flag);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc::fence_after_sync();
+      const uint32_t tmem_s = tmem + Geo::kColS + (uint32_t)(st * kN) + lane_base;
+      const uint32_t cmask = smask[sd];
+      const int lo_n = row_lo - kv0, hi_n = row_hi - kv0;
+      const bool full = __all_sync(0xffffffffu, lo_n <= 0 && hi_n >= kN) && cmask == kAllChunks;
+      float alpha = 1.0f, v_mul = 1.0f;  // factor of O; 2^-ev
+      if constexpr (Geo::kPth) {
+        const uint4 mb4 = *reinterpret_cast<const uint4*>(vmaxw + sd * 4);
+        const uint32_t mb = max(max(mb4.x, mb4.y), max(mb4.z, mb4.w));
+        if (mb != 0u) {  // 2^e above the largest scale, by its exponent bits
+          const int e = max(-125, min(126, (int)(mb >> 23) - 126));
+          if (e > ev) {
+            if (ev > -1000) alpha = __int_as_float((127 + max(ev - e, -127)) << 23);
+            ev = e;
+          }
+        }
+        v_mul = ev > -1000 ? __int_as_float((127 - ev) << 23) : 0.0f;  // (no positive scale yet: values are zero)
+      }
+      float lsum_tile = 0.0f;
+#pragma unroll 1
+      for (int c0 = 0; c0 < kN; c0 += 64) {
+        uint32_t v[64];
+        tc::tmem_ld32(tmem_s + c0, *reinterpret_cast<uint32_t(*)[32]>(v));
+        tc::tmem_ld32(tmem_s + c0 + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
+        tc::tmem_wait_ld();
+        if constexpr (Geo::kPth) {
+          const float4* const k4 = reinterpret_cast<const float4*>(sk + sd * kN + c0);
+#pragma unroll
+          for (int e = 0; e < 64; e += 4) {
+            const float4 s4 = k4[e / 4];
+            v[e] = __float_as_uint(__uint_as_float(v[e]) * s4.x);
+            v[e + 1] = __float_as_uint(__uint_as_float(v[e + 1]) * s4.y);
+            v[e + 2] = __float_as_uint(__uint_as_float(v[e + 2]) * s4.z);
+            v[e + 3] = __float_as_uint(__uint_as_float(v[e + 3]) * s4.w);
+          }
+        }
+        if (!plain) {  // final scores, in log2 units
+          const int dist = kv0 + c0 - pos;  // key - position of column c0
+#pragma unroll
+          for (int e = 0; e < 64; ++e) {
+            float r = __uint_as_float(v[e]) * score_mul;
+            if (cap > 0.0f) r = cap_l2 * dev::tanh_exp(r * inv_cap);
+            v[e] = __float_as_uint(fmaf(slope, (float)(dist + e), r));
+          }
+        }
+        if (!full) {
+          // masked keys by a bit each
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int lo = min(max(lo_n - c0 - 32 * h, 0), 32), hi = min(max(hi_n - c0 - 32 * h, 0), 32);
+            const uint32_t cm = cmask >> ((c0 >> 4) + 2 * h);
+            uint32_t seen = hi > lo ? (0xFFFFFFFFu << lo) & (0xFFFFFFFFu >> (32 - hi)) : 0u;
+            seen &= (cm & 1u ? 0xFFFFu : 0u) | (cm & 2u ? 0xFFFF0000u : 0u);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!((seen >> e) & 1u)) v[32 * h + e] = 0xFF800000u;  // -inf
+          }
+        }
+        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int e = 0; e < 64; e += 2)
+          mx4[(e >> 1) & 3] = fmaxf(mx4[(e >> 1) & 3], fmaxf(__uint_as_float(v[e]), __uint_as_float(v[e + 1])));
+        const float mr = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+        const float mx = plain ? mr * score_mul : mr;
+        float a = 1.0f;
+        if (mx > m_ref + 8.0f) {
+          const float nref = ceilf(mx);
+          if (m_ref != -INFINITY) a = ldexpf(1.0f, (int)fmaxf(m_ref - nref, -200.0f));
+          m_ref = nref;
+          alpha *= a;
+          l_sum *= a;
+          lsum_tile *= a;
+        }
+        const float ref = m_ref == -INFINITY ? 0.0f : m_ref - 6.0f;
+        const float mul = plain ? score_mul : 1.0f;
+        constexpr int kPw = Geo::kAuto ? 64 : 32;
+        uint32_t pw[kPw];
+        float ls0 = 0.0f, ls1 = 0.0f;
+        const float4* const v4 = reinterpret_cast<const float4*>(sv + sd * kN + c0);
+#pragma unroll
+        for (int e = 0; e < 64; e += 4) {
+          float q[4];
+#pragma unroll
+          for (int b = 0; b < 4; ++b) q[b] = dev::fast_exp2(fmaf(__uint_as_float(v[e + b]), mul, -ref));
+          ls0 += q[0] + q[2];
+          ls1 += q[1] + q[3];
+          if constexpr (Geo::kPth) {
+            const float4 s4 = v4[e / 4];
+            q[0] *= s4.x * v_mul;
+            q[1] *= s4.y * v_mul;
+            q[2] *= s4.z * v_mul;
+            q[3] *= s4.w * v_mul;
+          }
+          if constexpr (Geo::kAuto) {
+#pragma unroll
+            for (int b = 0; b < 4; b += 2) {
+              const uint32_t h = dev::pack_bf16x2(q[b], q[b + 1]);
+              pw[(e + b) / 2] = h;
+              pw[32 + (e + b) / 2] = dev::pack_bf16x2(q[b] - dev::bf16_lo(h), q[b + 1] - dev::bf16_hi(h));
+            }
+          } else {
+            pw[e / 2] = dev::pack_f16x2(q[0], q[1]);
+            pw[e / 2 + 1] = dev::pack_f16x2(q[2], q[3]);
+          }
+        }
+        lsum_tile += ls0 + ls1;
+        const int pcol = Geo::kAuto ? c0 : c0 / 2;
+#pragma unroll
+        for (int h = 0; h < kPw; h += 16)
+          tc::tmem_st16(tmem_s + pcol + h, *reinterpret_cast<uint32_t(*)[16]>(pw + h));
+        if (c0 > 0 && __any_sync(0xffffffffu, a != 1.0f)) {
+          // weights of the earlier round against the new reference
+          tc::tmem_wait_st();
+#pragma unroll 1
+          for (int c = 0; c < pcol; c += 32) {
+            uint32_t w[32];
+            tc::tmem_ld32(tmem_s + c, w);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              if constexpr (Geo::kAuto) {
+                w[e] = dev::pack_bf16x2(dev::bf16_lo(w[e]) * a, dev::bf16_hi(w[e]) * a);
+              } else {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[e]));
+                w[e] = dev::pack_f16x2(f.x * a, f.y * a);
+              }
+            }
+            tc::tmem_st32(tmem_s + c, w);
+          }
+        }
+      }
+      l_sum += lsum_tile;
+      // A moved reference rescales O.  With two Os this group's last P V is
+      // complete: it was issued before the S that this item waited for.  With one,
+      // its completion is waited for.
+      if (k > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
+        if constexpr (kRT == 1) {
+          ok = __all_sync(0xffffffffu, wait_or_abort(bar(Geo::kBarODone), (uint32_t)((k - 1) & 1), abort_flag));
+          if (!ok) break;
+          tc::fence_after_sync();
+        }
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 32) {
+          uint32_t w[32];
+          tc::tmem_ld32(tmem_o + (uint32_t)c0, w);
+          tc::tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * alpha);
+          tc::tmem_st32(tmem_o + (uint32_t)c0, w);
+        }
+      }
+      tc::tmem_wait_st();
+      tc::fence_before_sync();
+      warp_arrive(bar(Geo::kBarPFull + st));
+    }
+    // ---- epilogue: O / l as fp32 partial rows or bf16 rows -------------------
+    if (ok && count > 0) {
+      ok = __all_sync(0xffffffffu, wait_or_abort(bar(Geo::kBarOFinal + (kRT == 2 ? t : 0)), 0u, abort_flag));
+      tc::fence_after_sync();
+    }
+    const int part0 = __ldg(&up->part);
+    // (rows of this group's row tile in the partials: the second group of a
+    // single row tile has its own)
+    const int part = part0 + (two ? tile * kM : t * __ldg(&up->part_stride));
+    const int tile_rows = min(kM, nrows - tile * kM);
+    if (ok && (part0 >= 0 || count > 0)) {
+      if (part0 < 0 && p.sinks && row_valid && m_ref != -INFINITY) {
+        // the sink joins the normaliser here (partial rows: in the merge)
+        const float skl = p.sinks[head_q] * log2e;
+        if (skl != -INFINITY) l_sum += exp2f(fminf(skl - m_ref + 6.0f, 126.0f));
+      }
+      // 2^ev / l in two factors, the second last: 2^ev may be at either end of
+      // the exponents, and l up to 2^6 times 2^8 a key
+      const int up2 = !Geo::kPth ? 0 : ev > 100 ? 20 : ev < -40 && ev > -1000 ? -60 : 0;
+      const float sc = (l_sum > 0.0f ? (Geo::kInt4 ? dev::kInt4Unit : 1.0f) / l_sum : 0.0f) *
+                       (Geo::kPth    ? (ev > -1000 ? __int_as_float((127 + ev - up2) << 23) : 0.0f)
+                        : Geo::kAuto ? 1.0f
+                                     : p.v_scale);
+      const float sc2 = __int_as_float((127 + up2) << 23);
+      if (part0 >= 0 && row_valid) p.part_lse[part + m] = l_sum > 0.0f ? m_ref + log2f(l_sum) : -INFINITY;
+      // The warp's rows go through its part of the Q tiles (no longer read):
+      // D / 2 columns a pass, 16-byte pieces swizzled by the row, then out in
+      // runs of a row.
+      constexpr int kCw = D / 2, kPr = kCw / 4;  // columns of a pass, 16-byte pieces of a row
+      const uint32_t stage = base + Geo::kOffQ + (uint32_t)(t * Geo::kQBytes + (warp & 3) * 32 * kCw * 4);
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll 1
+        for (int c0 = 0; c0 < kCw; c0 += 32) {
+          uint32_t w[32];
+          if (count > 0) {
+            tc::tmem_ld32(tmem_o + (uint32_t)(h * kCw + c0), w);
+            tc::tmem_wait_ld();
+          }
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            float f[4];
+#pragma unroll
+            for (int b = 0; b < 4; ++b) f[b] = count > 0 ? __uint_as_float(w[e + b]) * sc * sc2 : 0.0f;
+            sts128(stage + (uint32_t)(lane * kCw * 4 + ((((c0 + e) >> 2) ^ (lane & 7)) << 4)),
+                   make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])));
+          }
+        }
+        __syncwarp();
+#pragma unroll 4
+        for (int x = lane; x < 32 * kPr; x += 32) {
+          const int r = x / kPr, pc = x % kPr;
+          const uint4 u = lds128(stage + (uint32_t)(r * kCw * 4 + ((pc ^ (r & 7)) << 4)));
+          const int64_t off = __shfl_sync(0xffffffffu, row_off, r);
+          if ((warp & 3) * 32 + r < tile_rows) {
+            if (part0 >= 0)
+              *reinterpret_cast<uint4*>(p.part_o + (int64_t)(part + (warp & 3) * 32 + r) * D + h * kCw + 4 * pc) = u;
+            else
+              *reinterpret_cast<uint2*>(p.out + off + h * kCw + 4 * pc) =
+                  make_uint2(dev::pack_bf16x2(__uint_as_float(u.x), __uint_as_float(u.y)),
+                             dev::pack_bf16x2(__uint_as_float(u.z), __uint_as_float(u.w)));
+          }
+        }
+        __syncwarp();
+      }
+    }
+    tc::fence_before_sync();
+    __syncwarp();
+  }
+
+  __syncthreads();
+  if (warp == 0) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, Geo::kTmemCols);
+  }
+  // A unit that gave up leaves NaN in every row of its output.
+  if (*abort_flag != 0u) {
+    if (tid == 0) atomicExch(p.error_flag, 1);
+    const int part0 = __ldg(&up->part), subs = kRT == 2 && !two ? 2 : 1;
+    for (int x = tid; x < nrows * subs; x += Geo::kThreads) {
+      const int r = x % nrows, packed = __ldg(&up->row0) + r;
+      if (part0 >= 0) {
+        const int64_t at = part0 + r + (int64_t)(x / nrows) * __ldg(&up->part_stride);
+        for (int d = 0; d < D; ++d) p.part_o[at * D + d] = NAN;
+        p.part_lse[at] = 0.0f;
+      } else {
+        const int2 token = __ldg(reinterpret_cast<const int2*>(rp.tokens) + __ldg(&up->tok0) + packed / G);
+        uint16_t* const o = p.out + ((int64_t)token.x * p.heads_q + kv_head * G + packed % G) * D;
+        for (int d = 0; d < D; ++d) o[d] = 0x7FC0u;
+      }
+    }
+  }
+}
+
+template <int DT, int D>
+int launch_rect_instance(const AttnParams& p, const RectParams& rp, cudaStream_t stream) {
+  auto kern = rect_attention_kernel<DT, D>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)rect_smem_bytes(D)) != cudaSuccess)
+    return KVQ_E_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)rp.num_units);
+  cfg.blockDim = dim3((unsigned)rect_threads(D));
+  cfg.dynamicSmemBytes = rect_smem_bytes(D);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kern, p, rp) != cudaSuccess) {
+    cudaGetLastError();
+    return KVQ_E_CUDA;
+  }
+  return KVQ_OK;
+}
+
+// The instances of one head_dim (a translation unit each).
+template <int D>
+int launch_rect_d(const AttnParams& p, const RectParams& rp, int dtype, cudaStream_t stream) {
+  switch (dtype) {
+    case KVQ_AUTO: return launch_rect_instance<KVQ_AUTO, D>(p, rp, stream);
+    case KVQ_FP8_E4M3: return launch_rect_instance<KVQ_FP8_E4M3, D>(p, rp, stream);
+    case KVQ_FP8_E5M2: return launch_rect_instance<KVQ_FP8_E5M2, D>(p, rp, stream);
+    case KVQ_INT8_PER_TOKEN_HEAD: return launch_rect_instance<KVQ_INT8_PER_TOKEN_HEAD, D>(p, rp, stream);
+    case KVQ_FP8_PER_TOKEN_HEAD: return launch_rect_instance<KVQ_FP8_PER_TOKEN_HEAD, D>(p, rp, stream);
+    case KVQ_FP8_E5M2_PER_TOKEN_HEAD: return launch_rect_instance<KVQ_FP8_E5M2_PER_TOKEN_HEAD, D>(p, rp, stream);
+    case KVQ_INT4_PER_TOKEN_HEAD: return launch_rect_instance<KVQ_INT4_PER_TOKEN_HEAD, D>(p, rp, stream);
+    default: return KVQ_E_UNSUPPORTED;
+  }
+}
+
+}  // namespace kvq

@@ -67,6 +67,15 @@ class SchedInfo(ctypes.Structure):
         return {k: getattr(self, k) for k, _ in self._fields_}
 
 
+class RectInfo(ctypes.Structure):
+    _fields_ = [("num_units", ctypes.c_int64), ("num_merge_items", ctypes.c_int64),
+                ("num_shared_requests", ctypes.c_int64), ("shared_keys", ctypes.c_int64),
+                ("smem_bytes", ctypes.c_size_t)]
+
+    def as_dict(self):
+        return {k: getattr(self, k) for k, _ in self._fields_}
+
+
 _c = ctypes
 _p = ctypes.c_void_p
 lib.kvq_status_string.restype = _c.c_char_p
@@ -79,6 +88,11 @@ lib.kvq_reshape_and_cache.restype = _c.c_int
 lib.kvq_reshape_and_cache.argtypes = [
     _p, _p, _c.c_int64, _c.c_int64, _c.c_int64, _c.c_int, _c.c_int, _p, _p,
     _c.c_int64, _c.c_int, _p, _c.c_int, _c.c_float, _c.c_float, _p]
+lib.kvq_rotary_and_cache.restype = _c.c_int
+lib.kvq_rotary_and_cache.argtypes = [
+    _p, _p, _p, _c.c_int64, _c.c_int64, _c.c_int64, _c.c_int64, _c.c_int, _c.c_int, _c.c_int, _p, _p,
+    _c.c_int64, _c.c_int, _c.c_int, _p, _c.c_int64, _p, _p, _c.c_int64, _c.c_int, _p, _c.c_int,
+    _c.c_float, _c.c_float, _p]
 lib.kvq_gather_cache.restype = _c.c_int
 lib.kvq_gather_cache.argtypes = [
     _p, _p, _c.c_int64, _c.c_int, _c.c_int, _c.c_int, _c.c_int, _c.c_float, _c.c_float, _p,
@@ -91,6 +105,16 @@ lib.kvq_get_scheduler_metadata.restype = _c.c_int
 lib.kvq_get_scheduler_metadata.argtypes = [
     _c.c_int, _c.c_int, _c.c_int, _c.c_int, _p, _p, _c.c_int, _c.c_int,
     _c.c_int, _c.POINTER(_p), _c.POINTER(_c.c_size_t)]
+lib.kvq_get_shared_prefix_metadata.restype = _c.c_int
+lib.kvq_get_shared_prefix_metadata.argtypes = [
+    _c.c_int, _c.c_int, _c.c_int, _c.c_int, _p, _p, _c.c_int, _p, _p, _c.c_int,
+    _c.c_int, _c.POINTER(_p), _c.POINTER(_c.c_size_t)]
+lib.kvq_get_cross_attention_metadata.restype = _c.c_int
+lib.kvq_get_cross_attention_metadata.argtypes = [
+    _c.c_int, _c.c_int, _c.c_int, _c.c_int, _p, _p, _c.c_int, _c.POINTER(_p),
+    _c.POINTER(_c.c_size_t)]
+lib.kvq_sched_get_rect_info.restype = _c.c_int
+lib.kvq_sched_get_rect_info.argtypes = [_p, _c.POINTER(RectInfo)]
 lib.kvq_attention_with_kv_cache.restype = _c.c_int
 lib.kvq_attention_with_kv_cache.argtypes = [
     _p, _c.c_int, _c.c_int, _c.c_int, _c.c_int, _p, _p, _p, _p, _p, _p,
@@ -251,6 +275,71 @@ def prepare_reshape_and_cache(key, value, key_cache, value_cache, slot_mapping, 
             stream)), "kvq_reshape_and_cache")
 
 
+def _check_caches(key_cache, value_cache, heads: int, row: int):
+    """The caches as the library reads them: [num_blocks, block_size, heads, row bytes]."""
+    for t in (key_cache, value_cache):
+        if t.dim() != 4 or t.shape[2] != heads or t.shape[3] * t.element_size() != row or not t.is_contiguous():
+            raise ValueError(f"the caches must be contiguous [num_blocks, block_size, {heads}, {row} bytes]")
+    if key_cache.shape != value_cache.shape:
+        raise ValueError("key_cache and value_cache must have one shape")
+
+
+def _rotary_and_cache_args(query, key, value, positions, cos_sin, query_out, key_cache, value_cache,
+                           slot_mapping, kv_cache_dtype, interleaved, k_scale, v_scale, stream):
+    import torch
+    dt = parse_kv_cache_dtype(kv_cache_dtype) if isinstance(kv_cache_dtype, str) else kv_cache_dtype
+    T, H, D = key.shape
+    if (query is None) != (query_out is None):
+        raise ValueError("query and query_out must both be given, or neither")
+    Hq = 0 if query is None else query.shape[1]
+    for name, t, heads in (("query", query, Hq), ("key", key, H), ("value", value, H),
+                           ("query_out", query_out, Hq)):
+        if t is None:
+            continue
+        if t.dtype != torch.bfloat16 or tuple(t.shape) != (T, heads, D):
+            raise ValueError(f"{name} must be bfloat16 [{T}, {heads}, {D}]")
+        if T > 0 and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != D)):
+            raise ValueError(f"the heads and dims of {name} must be contiguous")
+    for name, t in (("positions", positions), ("slot_mapping", slot_mapping)):
+        _flat(name, t, torch.int64)
+        if tuple(t.shape) != (T,):
+            raise ValueError(f"{name} must have one entry a token")
+    if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+        raise ValueError("cos_sin must be contiguous float32 [max_position, rotary_dim]")
+    _check_caches(key_cache, value_cache, H, _row_bytes(dt, D))
+    # (a single token has no stride of its own)
+    pitch = lambda t, heads: t.stride(0) if T > 1 else heads * D  # noqa: E731
+    return (_ptr(query), _ptr(key), _ptr(value), T, 0 if query is None else pitch(query, Hq),
+            pitch(key, H), pitch(value, H), Hq, H, D, _ptr(positions), _ptr(cos_sin),
+            cos_sin.shape[0], cos_sin.shape[1], int(bool(interleaved)), _ptr(query_out),
+            0 if query is None else pitch(query_out, Hq), _ptr(key_cache), _ptr(value_cache),
+            key_cache.shape[0], key_cache.shape[1], _ptr(slot_mapping), dt, float(k_scale),
+            float(v_scale), _stream(stream))
+
+
+def rotary_and_cache(query, key, value, positions, cos_sin, query_out, key_cache, value_cache,
+                     slot_mapping, kv_cache_dtype, interleaved: bool = False, k_scale: float = 1.0,
+                     v_scale: float = 1.0, stream=None) -> None:
+    """Queries and keys rotated by their positions, keys and values stored in
+    the caches: query / query_out bf16 [T, Hq, D] (one tensor, or two; or both
+    None), key / value bf16 [T, Hkv, D] (token strides may exceed the heads);
+    positions, slot_mapping int64 [T]; cos_sin float32 [max_position,
+    rotary_dim], cosines then sines; caches uint8 [NB, B, Hkv, row]."""
+    _check(lib.kvq_rotary_and_cache(*_rotary_and_cache_args(
+        query, key, value, positions, cos_sin, query_out, key_cache, value_cache, slot_mapping,
+        kv_cache_dtype, interleaved, k_scale, v_scale, stream)), "kvq_rotary_and_cache")
+
+
+def prepare_rotary_and_cache(query, key, value, positions, cos_sin, query_out, key_cache,
+                             value_cache, slot_mapping, kv_cache_dtype, interleaved: bool = False,
+                             k_scale: float = 1.0, v_scale: float = 1.0, stream=None) -> Prepared:
+    """rotary_and_cache with its arguments marshalled once (see Prepared)."""
+    return Prepared(lib.kvq_rotary_and_cache, _marshalled(
+        lib.kvq_rotary_and_cache, _rotary_and_cache_args(
+            query, key, value, positions, cos_sin, query_out, key_cache, value_cache, slot_mapping,
+            kv_cache_dtype, interleaved, k_scale, v_scale, stream)), "kvq_rotary_and_cache")
+
+
 def _gather_cache_args(key_cache, value_cache, slot_mapping, key_out, value_out, kv_cache_dtype,
                        k_scale, v_scale, stream):
     import torch
@@ -265,12 +354,7 @@ def _gather_cache_args(key_cache, value_cache, slot_mapping, key_out, value_out,
         if T > 0 and (t.stride(2) != 1 or (H > 1 and t.stride(1) != D)):
             raise ValueError("the heads and dims of key_out and value_out must be contiguous")
     # The library reads rows of H heads of D dims at the slots of the pool.
-    row = _row_bytes(dt, D)
-    for t in (key_cache, value_cache):
-        if t.dim() != 4 or t.shape[2] != H or t.shape[3] * t.element_size() != row or not t.is_contiguous():
-            raise ValueError(f"the caches must be contiguous [num_blocks, block_size, {H}, {row} bytes]")
-    if key_cache.shape != value_cache.shape:
-        raise ValueError("key_cache and value_cache must have one shape")
+    _check_caches(key_cache, value_cache, H, _row_bytes(dt, D))
     return (_ptr(key_cache), _ptr(value_cache), key_cache.shape[0], key_cache.shape[1], H, D, dt,
             float(k_scale), float(v_scale), _ptr(slot_mapping), T,
             int(key_out.dtype == torch.float32), _ptr(key_out), _ptr(value_out),
@@ -358,6 +442,13 @@ class Sched:
         _check(lib.kvq_sched_get_info(self.handle, _c.byref(inf)), "kvq_sched_get_info")
         return inf.as_dict()
 
+    def rect_info(self) -> dict:
+        """What is attended as rows against a whole run of keys
+        (kvq_sched_get_rect_info)."""
+        inf = RectInfo()
+        _check(lib.kvq_sched_get_rect_info(self.handle, _c.byref(inf)), "kvq_sched_get_rect_info")
+        return inf.as_dict()
+
     def plan(self) -> dict:
         """The schedule's plan as numpy arrays (kvq_sched_export_plan)."""
         sz = PlanSizes()
@@ -402,6 +493,52 @@ def get_scheduler_metadata(num_req: int, heads_q: int, heads_kv: int, head_dim: 
         num_req, heads_q, heads_kv, head_dim, _p(sl.ctypes.data), _p(qsl.ctypes.data),
         int(bool(causal)), int(window), dt, _c.byref(h), _c.byref(ws)),
         "kvq_get_scheduler_metadata")
+    return Sched(h, ws.value)
+
+
+def _host_i32(name, v, n: int):
+    """v as a contiguous host int32 array of n entries."""
+    a = np.asarray(v)
+    if a.shape != (n,) or (a.size and not np.issubdtype(a.dtype, np.integer)):
+        raise ValueError(f"{name} must hold {n} integers")
+    if a.size and (a.min() < -2**31 or a.max() >= 2**31):
+        raise ValueError(f"{name} must fit 32 bits")
+    return np.ascontiguousarray(a, dtype=np.int32)
+
+
+def get_shared_prefix_metadata(num_req: int, heads_q: int, heads_kv: int, head_dim: int, seq_lens,
+                               query_start_loc, prefix_lens, request_prefix, window: int,
+                               kv_cache_dtype) -> Sched:
+    """A causal schedule of a batch whose requests begin with shared keys:
+    prefix_lens, the keys of each prefix; request_prefix [num_req], each
+    request's prefix or -1 (host tensors, arrays or lists)."""
+    dt = parse_kv_cache_dtype(kv_cache_dtype) if isinstance(kv_cache_dtype, str) else kv_cache_dtype
+    sl = _host_i32("seq_lens", seq_lens, num_req)
+    qsl = _host_i32("query_start_loc", query_start_loc, num_req + 1)
+    pl = _host_i32("prefix_lens", prefix_lens, len(prefix_lens))
+    of = _host_i32("request_prefix", request_prefix, num_req)
+    h = _p()
+    ws = _c.c_size_t()
+    _check(lib.kvq_get_shared_prefix_metadata(
+        num_req, heads_q, heads_kv, head_dim, _p(sl.ctypes.data), _p(qsl.ctypes.data), pl.size,
+        _p(pl.ctypes.data), _p(of.ctypes.data), int(window), dt, _c.byref(h), _c.byref(ws)),
+        "kvq_get_shared_prefix_metadata")
+    return Sched(h, ws.value)
+
+
+def get_cross_attention_metadata(num_req: int, heads_q: int, heads_kv: int, head_dim: int,
+                                 encoder_lens, query_start_loc, kv_cache_dtype) -> Sched:
+    """A schedule of decoder tokens against encoders' keys of other lengths
+    (host tensors, arrays or lists), for attention_with_kv_cache with causal
+    False, window 0 and the encoder lengths as seq_lens."""
+    dt = parse_kv_cache_dtype(kv_cache_dtype) if isinstance(kv_cache_dtype, str) else kv_cache_dtype
+    el = _host_i32("encoder_lens", encoder_lens, num_req)
+    qsl = _host_i32("query_start_loc", query_start_loc, num_req + 1)
+    h = _p()
+    ws = _c.c_size_t()
+    _check(lib.kvq_get_cross_attention_metadata(
+        num_req, heads_q, heads_kv, head_dim, _p(el.ctypes.data), _p(qsl.ctypes.data), dt,
+        _c.byref(h), _c.byref(ws)), "kvq_get_cross_attention_metadata")
     return Sched(h, ws.value)
 
 
