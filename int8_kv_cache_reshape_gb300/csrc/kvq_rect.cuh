@@ -60,16 +60,17 @@ struct RectGeom {
   static constexpr int kOffSk = kOffV + kStages * kTileBytes;   // kSide x kN f32
   static constexpr int kOffSv = kOffSk + kSide * kN * 4;        // kSide x kN f32
   static constexpr int kOffVMax = kOffSv + kSide * kN * 4;      // kSide x 4 u32
-  static constexpr int kOffSMask = kOffVMax + kSide * 16;       // kSide u32
-  static constexpr int kOffSlots = kOffSMask + kSide * 4;       // kSlotRing x 16 i32
+  static constexpr int kOffSMask = kOffVMax + kSide * 16;       // kSide u32, kSide i32
+  static constexpr int kOffSlots = kOffSMask + kSide * 8;       // kSlotRing x 16 i32
   static constexpr int kOffQScale = kOffSlots + kSlotRing * 64; // kRT x kM f32
   static constexpr int kOffBar = kOffQScale + kRT * kM * 4;
-  static constexpr int kBytes = kOffBar + 256;
+  static constexpr int kBytes = kOffBar + 288;
   static constexpr int kColO = 0, kColS = kRT * D;
   static constexpr int kTmemCols = 512;
   static constexpr int kBarSlots = 0, kBarSlotsFree = 4, kBarSide = 8, kBarKFull = 12, kBarVFull = 14, kBarKEmpty = 16,
-                       kBarVEmpty = 18, kBarSFull = 20, kBarPFull = 22, kBarOFinal = 24, kBarQFull = 26, kBarODone = 28,
-                       kBarDrain = 29, kNumBars = 30;
+                       kBarVEmpty = 18, kBarSFull = 20, kBarPFull = 22, kBarOFinal = 26, kBarQFull = 28, kBarODone = 30,
+                       kBarDrain = 32, kBarVMax = 33, kNumBars = 34;
+  static constexpr int kHalves = kN / 64;  // parts of an item whose P is handed over by itself
   static constexpr int kOffTmemSlot = kOffBar + 8 * kNumBars, kOffAbort = kOffTmemSlot + 4;
   static_assert(kColS + 2 * kN <= kTmemCols, "tensor memory");
   static_assert(kQBytes % 1024 == 0 && kTileBytes % 1024 == 0 && kOffBar % 8 == 0 && kOffSk % 16 == 0, "alignment");
@@ -109,6 +110,26 @@ __global__ void __launch_bounds__(rect_threads(D), 1) rect_attention_kernel(cons
   auto bar = [&](int i) { return bars + 8u * (uint32_t)i; };
   volatile uint32_t* const abort_flag = reinterpret_cast<volatile uint32_t*>(sm + Geo::kOffAbort);
 
+  // (the plan, which no kernel writes, ahead of the wait below)
+  const int4* const rec = reinterpret_cast<const int4*>(rp.units + blockIdx.x);
+  const int4 u0 = __ldg(rec), u1 = __ldg(rec + 1);
+  const int part_stride = __ldg(&rp.units[blockIdx.x].part_stride);
+  const int kv_head = u0.x, row0 = u0.y, nrows = u0.z, kv_lo = u0.w;
+  const int kv_hi = u1.x, tok0 = u1.y, req = u1.z, part0 = u1.w;
+  const int G = p.group;
+  const bool two = kRT == 2 && nrows > kM;  // two row tiles, else one
+  // a softmax thread's row: tile t (one row tile: both groups take it), row m;
+  // its token's row of q and out and position
+  const int t = wg - 3, m = tid & 127, tile = two && wg == 4 ? 1 : 0, R = tile * kM + m;
+  const bool row_valid = wg >= 3 && R < nrows;
+  int2 token = make_int2(0, 0);
+  int row_g = 0;
+  if (row_valid) {
+    const int packed = row0 + R, q = packed / G;
+    row_g = packed - q * G;
+    token = __ldg(reinterpret_cast<const int2*>(rp.tokens) + tok0 + q);
+  }
+
   if (tid == 0) {
     for (int s = 0; s < 4; ++s) {
       tc::mbar_init(bar(Geo::kBarSlots + s), 1);
@@ -121,12 +142,14 @@ __global__ void __launch_bounds__(rect_threads(D), 1) rect_attention_kernel(cons
       tc::mbar_init(bar(Geo::kBarKEmpty + s), 1);
       tc::mbar_init(bar(Geo::kBarVEmpty + s), 1);
       tc::mbar_init(bar(Geo::kBarSFull + s), 1);
-      tc::mbar_init(bar(Geo::kBarPFull + s), 4);
+      tc::mbar_init(bar(Geo::kBarPFull + 2 * s), 4);
+      tc::mbar_init(bar(Geo::kBarPFull + 2 * s + 1), 4);
       tc::mbar_init(bar(Geo::kBarOFinal + s), 1);
       tc::mbar_init(bar(Geo::kBarQFull + s), 4);
+      tc::mbar_init(bar(Geo::kBarODone + s), 1);
     }
-    tc::mbar_init(bar(Geo::kBarODone), 1);
     tc::mbar_init(bar(Geo::kBarDrain), 1);
+    tc::mbar_init(bar(Geo::kBarVMax), 4);
     *abort_flag = 0u;
     tc::mbar_fence_init();
   }
@@ -143,15 +166,10 @@ __global__ void __launch_bounds__(rect_threads(D), 1) rect_attention_kernel(cons
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  const RectUnit* const up = rp.units + blockIdx.x;
-  const int nrows = __ldg(&up->nrows), kv_lo = __ldg(&up->kv_lo), kv_hi = __ldg(&up->kv_hi);
-  const int kv_head = __ldg(&up->kv_head);
   const int kv_first = kv_lo / kN * kN;
   const int T = (kv_hi - kv_first + kN - 1) / kN;  // KV tiles (one at least)
-  const bool two = kRT == 2 && nrows > kM;          // two row tiles, else one
   constexpr int kChunks = kN / 16;
   constexpr uint32_t kAllChunks = (1u << kChunks) - 1u;
-  const int G = p.group;
 
   if (wg == 0) {
     regs_down<Regs::kIssue>();
@@ -195,20 +213,23 @@ __global__ void __launch_bounds__(rect_threads(D), 1) rect_attention_kernel(cons
       for (; next < 2 && next < n && ok; ++next) ok = issue_s(next);
       for (int i = 0; i < n && ok; ++i) {
         const int g = tile_of(i), st = g & 1;
-        ok = wait(Geo::kBarPFull + (i & 1), i >> 1);
+        ok = wait(Geo::kBarPFull + 2 * (i & 1), i >> 1);
         if (ok && g > v_in) {
           ok = wait(Geo::kBarVFull + st, g >> 1);
           v_in = g;
         }
         if (!ok) break;
-        tc::fence_after_sync();
         const uint64_t dv = tc::desc_sw128_mn(base + Geo::kOffV + (uint32_t)(st * Geo::kTileBytes), kN * 128, 1024);
         const uint32_t o = tmem + Geo::kColO + (kRT == 2 ? (uint32_t)((i & 1) * D) : 0u);
         const uint32_t pcol = tmem + Geo::kColS + (uint32_t)((i & 1) * kN);
         const bool first = i < kRT;
-        if (leader) {
 #pragma unroll
-          for (int kk = 0; kk < kN / 16; ++kk) {
+        for (int h = 0; h < Geo::kHalves; ++h) {
+          if (h > 0 && !(ok = wait(Geo::kBarPFull + 2 * (i & 1) + h, i >> 1))) break;
+          tc::fence_after_sync();
+          if (leader) {
+#pragma unroll
+            for (int kk = 4 * h; kk < 4 * h + 4; ++kk) {
             if constexpr (Geo::kAuto) {
               // P = hi + lo, both bf16: hi of keys c0 .. c0 + 63 in columns c0 ..
               // c0 + 31, lo in c0 + 32 .. c0 + 63
@@ -216,11 +237,17 @@ __global__ void __launch_bounds__(rect_threads(D), 1) rect_attention_kernel(cons
               tc::mma_ts(o, pc, dv + (uint64_t)(kk * (2048 >> 4)), idesc_o, (!first || kk > 0) ? 1u : 0u);
               tc::mma_ts(o, pc + 32u, dv + (uint64_t)(kk * (2048 >> 4)), idesc_o, 1u);
             } else {
-              tc::mma_ts(o, pcol + (uint32_t)(kk * 8), dv + (uint64_t)(kk * (2048 >> 4)), idesc_o,
+              tc::mma_ts(o, pcol + (uint32_t)(32 * h + (kk & 3) * 8), dv + (uint64_t)(kk * (2048 >> 4)), idesc_o,
                          (!first || kk > 0) ? 1u : 0u);
             }
+            }
+            // (the softmax waits for it where its reference moves inside an item)
+            if (h == 0) tc::mma_commit(bar(Geo::kBarODone + (kRT == 2 ? i & 1 : 0)));
           }
-          if (kRT == 1) tc::mma_commit(bar(Geo::kBarODone));
+          __syncwarp();
+        }
+        if (!ok) break;
+        if (leader) {
           if (!two || (i & 1)) tc::mma_commit(bar(Geo::kBarVEmpty + st));
           if (i + kRT >= n) tc::mma_commit(bar(Geo::kBarOFinal + (kRT == 2 ? i & 1 : 0)));
         }
@@ -237,7 +264,7 @@ __global__ void __launch_bounds__(rect_threads(D), 1) rect_attention_kernel(cons
       // ---- slots of the KV tiles' 16-key chunks --------------------------
       // (entries are loaded a tile ahead; the block size is a multiple of 16;
       // q = hi32(j floor((2^32 - 1) / B)) is the quotient or one less)
-      const int32_t* const btab = p.block_table + (int64_t)__ldg(&up->req) * p.block_table_stride;
+      const int32_t* const btab = p.block_table + (int64_t)req * p.block_table_stride;
       const uint32_t bsz = (uint32_t)p.block_size, bdiv = 0xFFFFFFFFu / bsz;
       int32_t* const table = reinterpret_cast<int32_t*>(sm + Geo::kOffSlots);
       // lane c < kChunks looks after chunk c
@@ -284,6 +311,7 @@ __global__ void __launch_bounds__(rect_threads(D), 1) rect_attention_kernel(cons
     float* const sv = reinterpret_cast<float*>(sm + Geo::kOffSv);
     uint32_t* const vmaxw = reinterpret_cast<uint32_t*>(sm + Geo::kOffVMax);
     uint32_t* const smask = reinterpret_cast<uint32_t*>(sm + Geo::kOffSMask);
+    int32_t* const sev = reinterpret_cast<int32_t*>(sm + Geo::kOffSMask + Geo::kSide * 4);
     constexpr int64_t kRow = row_bytes(DT, D);
     const int64_t tok_bytes = (int64_t)p.heads_kv * kRow;
     const uint8_t* const head_at = cache + kv_head * kRow;
@@ -354,6 +382,7 @@ __global__ void __launch_bounds__(rect_threads(D), 1) rect_attention_kernel(cons
       uint4 c[kUnits];
       uint32_t cm[Geo::kInt4 ? kUnits : 1];
       float ks = 0.0f, vs = 0.0f;
+      int ev = -1000;  // exponent of the value scales' reference
       uint32_t valid = 0;
       auto load_tile = [&](int g) -> bool {
         const int e = g & 3;
@@ -403,13 +432,23 @@ __global__ void __launch_bounds__(rect_threads(D), 1) rect_attention_kernel(cons
           // g - 4, is done (P(g - 2) V(g - 2) is complete)
           if (ct == 0) smask[sd] = valid;
           if constexpr (Geo::kPth) {
-            if (ct < kN) {
-              sk[sd * kN + ct] = ks;
-              sv[sd * kN + ct] = vs;
-            }
+            // value scales relative to the largest power of two so far, 2^ev
             const float vmax = fmaxf(vs, 0.0f);  // (a NaN or negative scale is ignored)
             const uint32_t wmax = __reduce_max_sync(0xffffffffu, __float_as_uint(vmax));
             if (lane == 0) vmaxw[sd * 4 + (ct >> 5)] = wmax;
+            // (the group's four warps, by a wait that ends like the others)
+            warp_arrive(bar(Geo::kBarVMax));
+            if (!wait(Geo::kBarVMax, g)) break;
+            const uint4 mb4 = *reinterpret_cast<const uint4*>(vmaxw + sd * 4);
+            const uint32_t mb = max(max(mb4.x, mb4.y), max(mb4.z, mb4.w));
+            // (2^e above the largest scale, by its exponent bits)
+            if (mb != 0u) ev = max(ev, max(-125, min(126, (int)(mb >> 23) - 126)));
+            if (ct < kN) {
+              sk[sd * kN + ct] = ks;
+              // (no positive scale yet: values are zero)
+              sv[sd * kN + ct] = ev > -1000 ? vs * __int_as_float((127 - ev) << 23) : 0.0f;
+            }
+            if (ct == 0) sev[sd] = ev;
           }
           warp_arrive(bar(Geo::kBarSide + sd));
         }
@@ -450,65 +489,52 @@ __global__ void __launch_bounds__(rect_threads(D), 1) rect_attention_kernel(cons
   } else {
     // ---- softmax -------------------------------------------------------------
     regs_up<Regs::kSoftmax>();
-    const int t = wg - 3;                    // this group's O and S buffer
-    const int m = tid & 127;                 // row in its tile, tensor-memory lane
-    const int tile = two ? t : 0;            // row tile
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const float log2e = 1.4426950408889634f;
-    const int R = tile * kM + m;             // row of the unit
-    const bool row_valid = R < nrows;
-    // the row's token (its row of q and out, its position) and head
-    const int packed = __ldg(&up->row0) + (row_valid ? R : 0);
-    const int2 token = __ldg(reinterpret_cast<const int2*>(rp.tokens) + __ldg(&up->tok0) + packed / G);
-    const int head_q = kv_head * G + packed % G, pos = token.y;
+    const int head_q = kv_head * G + row_g, pos = token.y;
     const int64_t row_off = ((int64_t)token.x * p.heads_q + head_q) * D;
     float* const qscale = reinterpret_cast<float*>(sm + Geo::kOffQScale) + tile * kM;
     bool ok = true;
     if (two || t == 0) {
-      // Q of the warp's 32 rows: D / 8 lanes a row, 16 bytes each.  A row enters
-      // as f16 scaled by the power of two that puts its largest |q| in [2^13,
-      // 2^14): exact but for elements 2^27 below that one (subnormals).  The
-      // score scale's sign enters with Q, so that the softmax's factor is positive.
-      constexpr int kLpr = D / 8, kRpi = 32 / kLpr, kBatch = 8;
+      // Q of the warp's 32 rows: D / 8 lanes a row, 16 bytes each, up to 16 loads
+      // in flight.  A row enters as f16 scaled by the power of two that puts its
+      // largest |q| in [2^13, 2^14): exact but for elements 2^27 below that one
+      // (subnormals).  The score scale's sign enters with Q, so that the softmax's
+      // factor is positive.
+      constexpr int kLpr = D / 8, kRpi = 32 / kLpr, kBatch = 32 / kRpi < 16 ? 32 / kRpi : 16;
       const float qk_scale = Geo::kPth || Geo::kAuto ? p.sm_scale : p.sm_scale * p.k_scale;
-      const float sign = qk_scale > 0.0f ? 1.0f : qk_scale < 0.0f ? -1.0f : 0.0f;
       const uint32_t keep = qk_scale == 0.0f ? 0u : 0xFFFFFFFFu, flip = qk_scale < 0.0f ? 0x80008000u : 0u;
       const int sub = lane / kLpr, pc = lane % kLpr;
       const uint32_t qt = base + Geo::kOffQ + (uint32_t)(tile * Geo::kQBytes + (pc >> 3) * (kM * 128));
+      const int rows_in = min(32, nrows - tile * kM - (warp & 3) * 32);  // valid rows of the warp
 #pragma unroll 1
       for (int r0 = 0; r0 < 32; r0 += kBatch * kRpi) {
         uint4 x[kBatch];
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
-          const int r = (r0 + b * kRpi + sub) & 31;
+          const int r = r0 + b * kRpi + sub;
           const int64_t off = __shfl_sync(0xffffffffu, row_off, r);
-          const bool live = __shfl_sync(0xffffffffu, (int)row_valid, r) != 0;
-          x[b] = live ? dev::ldg_stream_coherent(p.q + off + 8 * pc) : make_uint4(0, 0, 0, 0);
+          x[b] = r < rows_in ? dev::ldg_stream_coherent(p.q + off + 8 * pc) : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
-          const int r = r0 + b * kRpi + sub;
-          uint32_t w[4] = {x[b].x, x[b].y, x[b].z, x[b].w};
-          if constexpr (Geo::kAuto) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) w[e] = (w[e] & keep) ^ flip;
-            if (pc == 0 && r < 32) qscale[(warp & 3) * 32 + r] = 1.0f;
-          } else {
-            uint32_t big = 0;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) big = dev::max_u16x2(big, w[e] & 0x7FFF7FFFu);
+          const int r = r0 + b * kRpi + sub, row = (warp & 3) * 32 + r;
+          uint32_t w[4] = {(x[b].x & keep) ^ flip, (x[b].y & keep) ^ flip, (x[b].z & keep) ^ flip, (x[b].w & keep) ^ flip};
+          float unscale = 1.0f;
+          if constexpr (!Geo::kAuto) {
+            uint32_t big = dev::max_u16x2(dev::max_u16x2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu),
+                                          dev::max_u16x2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
 #pragma unroll
             for (int o = 1; o < kLpr; o <<= 1) big = dev::max_u16x2(big, __shfl_xor_sync(0xffffffffu, big, o));
             const int emax = (int)(max(big & 0xFFFFu, big >> 16) >> 7);  // largest |q| < 2^(emax - 126)
             const int sh = emax == 0 ? 0 : min(140 - emax, 126);
-            const float f = ldexpf(sign, sh);
+            const float f = __int_as_float((127 + sh) << 23);
+            unscale = __int_as_float((127 - sh) << 23);
 #pragma unroll
             for (int e = 0; e < 4; ++e) w[e] = dev::pack_f16x2(dev::bf16_lo(w[e]) * f, dev::bf16_hi(w[e]) * f);
-            if (pc == 0 && r < 32) qscale[(warp & 3) * 32 + r] = ldexpf(1.0f, -sh);
           }
-          const int row = (warp & 3) * 32 + r;
-          if (r < 32)
-            sts128(qt + (uint32_t)(row * 128 + (((pc & 7) ^ (row & 7)) << 4)), make_uint4(w[0], w[1], w[2], w[3]));
+          if (pc == 0) qscale[row] = unscale;
+          sts128(qt + (uint32_t)(row * 128 + (((pc & 7) ^ (row & 7)) << 4)), make_uint4(w[0], w[1], w[2], w[3]));
         }
       }
       tc::fence_async_smem();
@@ -520,8 +546,8 @@ __global__ void __launch_bounds__(rect_threads(D), 1) rect_attention_kernel(cons
 
     const float* const sk = reinterpret_cast<const float*>(sm + Geo::kOffSk);
     const float* const sv = reinterpret_cast<const float*>(sm + Geo::kOffSv);
-    const uint32_t* const vmaxw = reinterpret_cast<const uint32_t*>(sm + Geo::kOffVMax);
     const uint32_t* const smask = reinterpret_cast<const uint32_t*>(sm + Geo::kOffSMask);
+    const int32_t* const sev = reinterpret_cast<const int32_t*>(sm + Geo::kOffSMask + Geo::kSide * 4);
     const float cap = p.soft_cap, cap_l2 = cap * log2e, inv_cap = cap > 0.0f ? 1.0f / cap : 0.0f;
     const bool plain = cap <= 0.0f && p.alibi_slopes == nullptr;
     const float slope = p.alibi_slopes ? p.alibi_slopes[head_q] * log2e : 0.0f;
@@ -535,6 +561,18 @@ __global__ void __launch_bounds__(rect_threads(D), 1) rect_attention_kernel(cons
     const uint32_t tmem_o = tmem + Geo::kColO + (kRT == 2 ? (uint32_t)(t * D) : 0u) + lane_base;
     float m_ref = -INFINITY, l_sum = 0.0f;
     int ev = -1000;  // exponent of the value-scale reference (per-token-head)
+    // O times alpha (per row), once the P V issued so far are complete
+    auto rescale_o = [&](float alpha) {
+#pragma unroll 1
+      for (int c0 = 0; c0 < D; c0 += 32) {
+        uint32_t w[32];
+        tc::tmem_ld32(tmem_o + (uint32_t)c0, w);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * alpha);
+        tc::tmem_st32(tmem_o + (uint32_t)c0, w);
+      }
+    };
     for (int k = 0; ok && k < count; ++k) {
       const int i = kRT == 1 ? k : 2 * k + t;  // item
       const int g = two ? k : i;               // KV tile
@@ -549,165 +587,142 @@ __global__ void __launch_bounds__(rect_threads(D), 1) rect_attention_kernel(cons
       const uint32_t cmask = smask[sd];
       const int lo_n = row_lo - kv0, hi_n = row_hi - kv0;
       const bool full = __all_sync(0xffffffffu, lo_n <= 0 && hi_n >= kN) && cmask == kAllChunks;
-      float alpha = 1.0f, v_mul = 1.0f;  // factor of O; 2^-ev
+      float alpha = 1.0f;  // factor of O
       if constexpr (Geo::kPth) {
-        const uint4 mb4 = *reinterpret_cast<const uint4*>(vmaxw + sd * 4);
-        const uint32_t mb = max(max(mb4.x, mb4.y), max(mb4.z, mb4.w));
-        if (mb != 0u) {  // 2^e above the largest scale, by its exponent bits
-          const int e = max(-125, min(126, (int)(mb >> 23) - 126));
-          if (e > ev) {
-            if (ev > -1000) alpha = __int_as_float((127 + max(ev - e, -127)) << 23);
-            ev = e;
-          }
+        const int e = sev[sd];
+        if (e > ev) {
+          if (ev > -1000) alpha = __int_as_float((127 + max(ev - e, -127)) << 23);
+          ev = e;
         }
-        v_mul = ev > -1000 ? __int_as_float((127 - ev) << 23) : 0.0f;  // (no positive scale yet: values are zero)
       }
-      float lsum_tile = 0.0f;
 #pragma unroll 1
-      for (int c0 = 0; c0 < kN; c0 += 64) {
+      for (int h = 0; h < Geo::kHalves; ++h) {
+        const int c0 = 64 * h;
         uint32_t v[64];
         tc::tmem_ld32(tmem_s + c0, *reinterpret_cast<uint32_t(*)[32]>(v));
         tc::tmem_ld32(tmem_s + c0 + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
         tc::tmem_wait_ld();
+        uint64_t z[32];  // pairs of scores
         if constexpr (Geo::kPth) {
-          const float4* const k4 = reinterpret_cast<const float4*>(sk + sd * kN + c0);
+          const ulonglong2* const k2 = reinterpret_cast<const ulonglong2*>(sk + sd * kN + c0);
 #pragma unroll
-          for (int e = 0; e < 64; e += 4) {
-            const float4 s4 = k4[e / 4];
-            v[e] = __float_as_uint(__uint_as_float(v[e]) * s4.x);
-            v[e + 1] = __float_as_uint(__uint_as_float(v[e + 1]) * s4.y);
-            v[e + 2] = __float_as_uint(__uint_as_float(v[e + 2]) * s4.z);
-            v[e + 3] = __float_as_uint(__uint_as_float(v[e + 3]) * s4.w);
+          for (int e = 0; e < 32; e += 2) {
+            const ulonglong2 s2 = k2[e / 2];
+            z[e] = dev::mul2(dev::pack2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), s2.x);
+            z[e + 1] = dev::mul2(dev::pack2(__uint_as_float(v[2 * e + 2]), __uint_as_float(v[2 * e + 3])), s2.y);
           }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) z[e] = dev::pack2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
         }
         if (!plain) {  // final scores, in log2 units
           const int dist = kv0 + c0 - pos;  // key - position of column c0
 #pragma unroll
-          for (int e = 0; e < 64; ++e) {
-            float r = __uint_as_float(v[e]) * score_mul;
-            if (cap > 0.0f) r = cap_l2 * dev::tanh_exp(r * inv_cap);
-            v[e] = __float_as_uint(fmaf(slope, (float)(dist + e), r));
+          for (int e = 0; e < 32; ++e) {
+            float2 r = dev::unpack2(z[e]);
+            r.x *= score_mul;
+            r.y *= score_mul;
+            if (cap > 0.0f) {
+              r.x = cap_l2 * dev::tanh_exp(r.x * inv_cap);
+              r.y = cap_l2 * dev::tanh_exp(r.y * inv_cap);
+            }
+            z[e] = dev::pack2(fmaf(slope, (float)(dist + 2 * e), r.x), fmaf(slope, (float)(dist + 2 * e + 1), r.y));
           }
         }
         if (!full) {
           // masked keys by a bit each
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int lo = min(max(lo_n - c0 - 32 * h, 0), 32), hi = min(max(hi_n - c0 - 32 * h, 0), 32);
-            const uint32_t cm = cmask >> ((c0 >> 4) + 2 * h);
+          for (int q = 0; q < 2; ++q) {
+            const int lo = min(max(lo_n - c0 - 32 * q, 0), 32), hi = min(max(hi_n - c0 - 32 * q, 0), 32);
+            const uint32_t cm = cmask >> ((c0 >> 4) + 2 * q);
             uint32_t seen = hi > lo ? (0xFFFFFFFFu << lo) & (0xFFFFFFFFu >> (32 - hi)) : 0u;
             seen &= (cm & 1u ? 0xFFFFu : 0u) | (cm & 2u ? 0xFFFF0000u : 0u);
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (!((seen >> e) & 1u)) v[32 * h + e] = 0xFF800000u;  // -inf
+            for (int e = 0; e < 16; ++e) {
+              const float2 r = dev::unpack2(z[16 * q + e]);
+              z[16 * q + e] = dev::pack2((seen >> (2 * e)) & 1u ? r.x : -INFINITY, (seen >> (2 * e + 1)) & 1u ? r.y : -INFINITY);
+            }
           }
         }
         float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int e = 0; e < 64; e += 2)
-          mx4[(e >> 1) & 3] = fmaxf(mx4[(e >> 1) & 3], fmaxf(__uint_as_float(v[e]), __uint_as_float(v[e + 1])));
-        const float mr = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+        for (int e = 0; e < 32; ++e) {
+          const float2 r = dev::unpack2(z[e]);
+          mx4[e & 3] = dev::max3(mx4[e & 3], r.x, r.y);
+        }
+        const float mr = dev::max3(mx4[0], mx4[1], fmaxf(mx4[2], mx4[3]));
         const float mx = plain ? mr * score_mul : mr;
-        float a = 1.0f;
         if (mx > m_ref + 8.0f) {
           const float nref = ceilf(mx);
-          if (m_ref != -INFINITY) a = ldexpf(1.0f, (int)fmaxf(m_ref - nref, -200.0f));
+          if (m_ref != -INFINITY) {
+            const float a = __int_as_float((127 + (int)fmaxf(m_ref - nref, -127.0f)) << 23);  // (an integer's power)
+            alpha *= a;
+            l_sum *= a;
+          }
           m_ref = nref;
-          alpha *= a;
-          l_sum *= a;
-          lsum_tile *= a;
         }
         const float ref = m_ref == -INFINITY ? 0.0f : m_ref - 6.0f;
-        const float mul = plain ? score_mul : 1.0f;
+        const uint64_t mul2v = dev::pack2(plain ? score_mul : 1.0f, plain ? score_mul : 1.0f);
+        const uint64_t ref2 = dev::pack2(-ref, -ref);
         constexpr int kPw = Geo::kAuto ? 64 : 32;
         uint32_t pw[kPw];
-        float ls0 = 0.0f, ls1 = 0.0f;
-        const float4* const v4 = reinterpret_cast<const float4*>(sv + sd * kN + c0);
+        uint64_t ls[2] = {0ull, 0ull};  // pairs of sums
+        const ulonglong2* const v2 = reinterpret_cast<const ulonglong2*>(sv + sd * kN + c0);
 #pragma unroll
-        for (int e = 0; e < 64; e += 4) {
-          float q[4];
+        for (int e = 0; e < 32; e += 2) {
+          ulonglong2 s2;
+          if constexpr (Geo::kPth) s2 = v2[e / 2];
 #pragma unroll
-          for (int b = 0; b < 4; ++b) q[b] = dev::fast_exp2(fmaf(__uint_as_float(v[e + b]), mul, -ref));
-          ls0 += q[0] + q[2];
-          ls1 += q[1] + q[3];
-          if constexpr (Geo::kPth) {
-            const float4 s4 = v4[e / 4];
-            q[0] *= s4.x * v_mul;
-            q[1] *= s4.y * v_mul;
-            q[2] *= s4.z * v_mul;
-            q[3] *= s4.w * v_mul;
-          }
-          if constexpr (Geo::kAuto) {
-#pragma unroll
-            for (int b = 0; b < 4; b += 2) {
-              const uint32_t h = dev::pack_bf16x2(q[b], q[b + 1]);
-              pw[(e + b) / 2] = h;
-              pw[32 + (e + b) / 2] = dev::pack_bf16x2(q[b] - dev::bf16_lo(h), q[b + 1] - dev::bf16_hi(h));
+          for (int b = 0; b < 2; ++b) {
+            const float2 x = dev::unpack2(dev::fma2(z[e + b], mul2v, ref2));
+            uint64_t q2 = dev::pack2(dev::fast_exp2(x.x), dev::fast_exp2(x.y));
+            ls[b] = dev::add2(ls[b], q2);
+            if constexpr (Geo::kPth) q2 = dev::mul2(q2, b ? s2.y : s2.x);
+            const float2 q = dev::unpack2(q2);
+            if constexpr (Geo::kAuto) {
+              const uint32_t hw = dev::pack_bf16x2(q.x, q.y);
+              pw[e + b] = hw;
+              pw[32 + e + b] = dev::pack_bf16x2(q.x - dev::bf16_lo(hw), q.y - dev::bf16_hi(hw));
+            } else {
+              pw[e + b] = dev::pack_f16x2(q.x, q.y);
             }
-          } else {
-            pw[e / 2] = dev::pack_f16x2(q[0], q[1]);
-            pw[e / 2 + 1] = dev::pack_f16x2(q[2], q[3]);
           }
         }
-        lsum_tile += ls0 + ls1;
-        const int pcol = Geo::kAuto ? c0 : c0 / 2;
+        {
+          const float2 a = dev::unpack2(dev::add2(ls[0], ls[1]));
+          l_sum += a.x + a.y;
+        }
+        // P over the columns that this half read
 #pragma unroll
-        for (int h = 0; h < kPw; h += 16)
-          tc::tmem_st16(tmem_s + pcol + h, *reinterpret_cast<uint32_t(*)[16]>(pw + h));
-        if (c0 > 0 && __any_sync(0xffffffffu, a != 1.0f)) {
-          // weights of the earlier round against the new reference
-          tc::tmem_wait_st();
-#pragma unroll 1
-          for (int c = 0; c < pcol; c += 32) {
-            uint32_t w[32];
-            tc::tmem_ld32(tmem_s + c, w);
-            tc::tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              if constexpr (Geo::kAuto) {
-                w[e] = dev::pack_bf16x2(dev::bf16_lo(w[e]) * a, dev::bf16_hi(w[e]) * a);
-              } else {
-                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[e]));
-                w[e] = dev::pack_f16x2(f.x * a, f.y * a);
-              }
-            }
-            tc::tmem_st32(tmem_s + c, w);
+        for (int q = 0; q < kPw; q += 16)
+          tc::tmem_st16(tmem_s + (Geo::kAuto ? c0 : 32 * h) + q, *reinterpret_cast<uint32_t(*)[16]>(pw + q));
+        // A moved reference rescales O.  With two Os, this group's products up
+        // to the last item are complete (issued before the S that this item waited
+        // for); those of this item's first half, and with one O the last item's,
+        // are waited for.
+        if ((k > 0 || h > 0) && __any_sync(0xffffffffu, alpha != 1.0f)) {
+          if (h > 0 || kRT == 1) {
+            ok = __all_sync(0xffffffffu, wait_or_abort(bar(Geo::kBarODone + (kRT == 2 ? t : 0)),
+                                                       (uint32_t)((kRT == 2 ? k : k - 1) & 1), abort_flag));
+            if (!ok) break;
+            tc::fence_after_sync();
           }
+          rescale_o(alpha);
         }
+        alpha = 1.0f;
+        tc::tmem_wait_st();
+        tc::fence_before_sync();
+        warp_arrive(bar(Geo::kBarPFull + 2 * st + h));
       }
-      l_sum += lsum_tile;
-      // A moved reference rescales O.  With two Os this group's last P V is
-      // complete: it was issued before the S that this item waited for.  With one,
-      // its completion is waited for.
-      if (k > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
-        if constexpr (kRT == 1) {
-          ok = __all_sync(0xffffffffu, wait_or_abort(bar(Geo::kBarODone), (uint32_t)((k - 1) & 1), abort_flag));
-          if (!ok) break;
-          tc::fence_after_sync();
-        }
-#pragma unroll 1
-        for (int c0 = 0; c0 < D; c0 += 32) {
-          uint32_t w[32];
-          tc::tmem_ld32(tmem_o + (uint32_t)c0, w);
-          tc::tmem_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * alpha);
-          tc::tmem_st32(tmem_o + (uint32_t)c0, w);
-        }
-      }
-      tc::tmem_wait_st();
-      tc::fence_before_sync();
-      warp_arrive(bar(Geo::kBarPFull + st));
     }
     // ---- epilogue: O / l as fp32 partial rows or bf16 rows -------------------
     if (ok && count > 0) {
       ok = __all_sync(0xffffffffu, wait_or_abort(bar(Geo::kBarOFinal + (kRT == 2 ? t : 0)), 0u, abort_flag));
       tc::fence_after_sync();
     }
-    const int part0 = __ldg(&up->part);
     // (rows of this group's row tile in the partials: the second group of a
     // single row tile has its own)
-    const int part = part0 + (two ? tile * kM : t * __ldg(&up->part_stride));
+    const int part = part0 + (two ? tile * kM : t * part_stride);
     const int tile_rows = min(kM, nrows - tile * kM);
     if (ok && (part0 >= 0 || count > 0)) {
       if (part0 < 0 && p.sinks && row_valid && m_ref != -INFINITY) {
@@ -777,16 +792,16 @@ __global__ void __launch_bounds__(rect_threads(D), 1) rect_attention_kernel(cons
   // A unit that gave up leaves NaN in every row of its output.
   if (*abort_flag != 0u) {
     if (tid == 0) atomicExch(p.error_flag, 1);
-    const int part0 = __ldg(&up->part), subs = kRT == 2 && !two ? 2 : 1;
+    const int subs = kRT == 2 && !two ? 2 : 1;
     for (int x = tid; x < nrows * subs; x += Geo::kThreads) {
-      const int r = x % nrows, packed = __ldg(&up->row0) + r;
+      const int r = x % nrows, packed = row0 + r;
       if (part0 >= 0) {
-        const int64_t at = part0 + r + (int64_t)(x / nrows) * __ldg(&up->part_stride);
+        const int64_t at = part0 + r + (int64_t)(x / nrows) * part_stride;
         for (int d = 0; d < D; ++d) p.part_o[at * D + d] = NAN;
         p.part_lse[at] = 0.0f;
       } else {
-        const int2 token = __ldg(reinterpret_cast<const int2*>(rp.tokens) + __ldg(&up->tok0) + packed / G);
-        uint16_t* const o = p.out + ((int64_t)token.x * p.heads_q + kv_head * G + packed % G) * D;
+        const int2 to = __ldg(reinterpret_cast<const int2*>(rp.tokens) + tok0 + packed / G);
+        uint16_t* const o = p.out + ((int64_t)to.x * p.heads_q + kv_head * G + packed % G) * D;
         for (int d = 0; d < D; ++d) o[d] = 0x7FC0u;
       }
     }
