@@ -228,10 +228,8 @@ KVQ_HD constexpr size_t prefill_smem_bytes(int head_dim, int cta_group = 1) {
 }
 
 // ---- attention of many rows to one run of keys (kvq_rect.cuh) ---------------
-// Row tiles of 128 rows a CTA holds, each with an O in tensor memory; threads
-// (an issuing, two converting and a softmax warpgroup per row tile); rows of a unit.
+// Row tiles of 128 rows a CTA holds, each with an O in tensor memory; rows of a unit.
 KVQ_HD constexpr int rect_row_tiles(int head_dim) { return head_dim >= 256 ? 1 : 2; }
-KVQ_HD constexpr int rect_threads(int head_dim) { return 128 * (3 + rect_row_tiles(head_dim)); }
 KVQ_HD constexpr int rect_rows(int head_dim) { return 128 * rect_row_tiles(head_dim); }
 // Shared memory: Q, two K and two V tiles (f16), four slots of per-key scales,
 // value-scale maxima and chunk masks, four slot tables, row scales, barriers; +1

@@ -16,14 +16,18 @@
 // other tile's product to run while one tile's softmax works; the keys
 // of one row tile may be cut among many CTAs, which a causal prefill need not be.
 //
-// Layout (one CTA per SM, one unit per CTA; warpgroups):
-//   0     warp 0 issues the MMAs, warp 1 resolves 16-key chunks through the
-//         block table into slots, up to four KV tiles ahead
-//   1, 2  converters: one group takes K, the other V, each thread 16 codes (4-bit:
-//         32) of a key at a time, loaded into registers a KV tile ahead,
-//         converted exactly to f16 and stored in the 128-byte swizzle into two-stage
-//         rings; bf16 rows are copied as they are (cp.async, dead keys zero)
-//   3, 4  softmax: thread = row = tensor-memory lane (head_dim 256: group 3 only)
+// Layout (one CTA per SM, one unit per CTA; 16 warps):
+//   warp 0     issues the MMAs
+//   warp 1     resolves 16-key chunks through the block table into slots, up to
+//              four KV tiles ahead
+//   warps 2, 3 the KV tiles' side data: per-key scales, chunk mask
+//   converters two warps (head_dim 256: four) for K and as many for V, each thread 16
+//              codes (4-bit: 32) of a key at a time, loaded into registers a KV tile
+//              ahead, converted exactly to f16 and stored in the 128-byte swizzle into
+//              two-stage rings; bf16 rows are copied as they are (cp.async, dead keys
+//              zero)
+//   softmax    two warpgroups (head_dim 256: one), thread = row = tensor-memory lane;
+//              a thread holds the item's whole row of scores in registers
 // Items: an item is S = Q K^T of a row tile against a KV tile (kN keys) and then
 // O += P V.  Item i has S buffer i mod 2; P replaces S in it.  The MMA warp
 // issues S(0), S(1), then PV(i), S(i + 2), in order.
@@ -50,7 +54,9 @@ struct RectGeom {
   static constexpr bool kAuto = DT == KVQ_AUTO, kInt4 = is_int4(DT), kPth = is_per_token_head(DT);
   static constexpr int kRT = rect_row_tiles(D);       // row tiles with an O of their own
   static constexpr int kM = 128, kN = prefill_keys(D);
-  static constexpr int kThreads = rect_threads(D);
+  static constexpr int kThreads = 512;
+  static constexpr int kConv = kRT == 2 ? 64 : 128;   // converter threads of K, and of V
+  static constexpr int kSoftWg = kRT == 2 ? 2 : 3;    // first softmax warpgroup
   static constexpr int kStages = 2, kSide = 4, kSlotRing = 4;
   static constexpr int kQBytes = kM * D * 2;          // a row tile's Q
   static constexpr int kTileBytes = kN * D * 2;       // a KV tile's K or V
@@ -60,7 +66,7 @@ struct RectGeom {
   static constexpr int kOffSk = kOffV + kStages * kTileBytes;   // kSide x kN f32
   static constexpr int kOffSv = kOffSk + kSide * kN * 4;        // kSide x kN f32
   static constexpr int kOffVMax = kOffSv + kSide * kN * 4;      // kSide x 4 u32
-  static constexpr int kOffSMask = kOffVMax + kSide * 16;       // kSide u32, kSide i32
+  static constexpr int kOffSMask = kOffVMax + kSide * 16;       // kSide u32 masks, kSide i32 exponents
   static constexpr int kOffSlots = kOffSMask + kSide * 8;       // kSlotRing x 16 i32
   static constexpr int kOffQScale = kOffSlots + kSlotRing * 64; // kRT x kM f32
   static constexpr int kOffBar = kOffQScale + kRT * kM * 4;
@@ -69,7 +75,7 @@ struct RectGeom {
   static constexpr int kTmemCols = 512;
   static constexpr int kBarSlots = 0, kBarSlotsFree = 4, kBarSide = 8, kBarKFull = 12, kBarVFull = 14, kBarKEmpty = 16,
                        kBarVEmpty = 18, kBarSFull = 20, kBarPFull = 22, kBarOFinal = 26, kBarQFull = 28, kBarODone = 30,
-                       kBarDrain = 32, kBarVMax = 33, kNumBars = 34;
+                       kBarDrain = 31, kBarVMax = 32, kNumBars = 33;
   static constexpr int kHalves = kN / 64;  // parts of an item whose P is handed over by itself
   static constexpr int kOffTmemSlot = kOffBar + 8 * kNumBars, kOffAbort = kOffTmemSlot + 4;
   static_assert(kColS + 2 * kN <= kTmemCols, "tensor memory");
@@ -77,13 +83,11 @@ struct RectGeom {
   static_assert(kOffAbort + 4 <= kBytes && (size_t)kBytes + 1024 == rect_smem_bytes(D), "shared memory");
 };
 
-// Registers a thread of each warpgroup, out of the launch's (65,536 / threads,
-// a multiple of 8): 640 x 96 = 61,440 at head_dim 64 and 128, 512 x 128 at 256.
+// Registers a thread of each warpgroup, out of the launch's 512 x 128.
 template <int D>
 struct RectRegs {
-  static constexpr int kIssue = D >= 256 ? 64 : 56, kConvert = D >= 256 ? 104 : 80, kSoftmax = D >= 256 ? 232 : 128;
-  static constexpr int kLaunch = D >= 256 ? 128 : 96;
-  static_assert(kIssue + 2 * kConvert + rect_row_tiles(D) * kSoftmax <= (3 + rect_row_tiles(D)) * kLaunch,
+  static constexpr int kIssue = D >= 256 ? 64 : 40, kConvert = D >= 256 ? 104 : 88, kSoftmax = D >= 256 ? 232 : 192;
+  static_assert(kIssue + (D >= 256 ? 2 : 1) * kConvert + rect_row_tiles(D) * kSoftmax <= 4 * 128,
                 "the groups' registers come out of the launch's");
 };
 
@@ -97,7 +101,7 @@ __device__ __forceinline__ void regs_up() {
 }
 
 template <int DT, int D>
-__global__ void __launch_bounds__(rect_threads(D), 1) rect_attention_kernel(const AttnParams p, const RectParams rp) {
+__global__ void __launch_bounds__(512, 1) rect_attention_kernel(const AttnParams p, const RectParams rp) {
   using Geo = RectGeom<DT, D>;
   using Regs = RectRegs<D>;
   constexpr int kM = Geo::kM, kN = Geo::kN, kRT = Geo::kRT;
@@ -120,8 +124,8 @@ __global__ void __launch_bounds__(rect_threads(D), 1) rect_attention_kernel(cons
   const bool two = kRT == 2 && nrows > kM;  // two row tiles, else one
   // a softmax thread's row: tile t (one row tile: both groups take it), row m;
   // its token's row of q and out and position
-  const int t = wg - 3, m = tid & 127, tile = two && wg == 4 ? 1 : 0, R = tile * kM + m;
-  const bool row_valid = wg >= 3 && R < nrows;
+  const int t = wg - Geo::kSoftWg, m = tid & 127, tile = two && t == 1 ? 1 : 0, R = tile * kM + m;
+  const bool row_valid = t >= 0 && R < nrows;
   int2 token = make_int2(0, 0);
   int row_g = 0;
   if (row_valid) {
@@ -133,12 +137,12 @@ __global__ void __launch_bounds__(rect_threads(D), 1) rect_attention_kernel(cons
   if (tid == 0) {
     for (int s = 0; s < 4; ++s) {
       tc::mbar_init(bar(Geo::kBarSlots + s), 1);
-      tc::mbar_init(bar(Geo::kBarSlotsFree + s), 8);
-      tc::mbar_init(bar(Geo::kBarSide + s), 4);
+      tc::mbar_init(bar(Geo::kBarSlotsFree + s), 2 * Geo::kConv / 32 + 2);
+      tc::mbar_init(bar(Geo::kBarSide + s), 2);
     }
     for (int s = 0; s < 2; ++s) {
-      tc::mbar_init(bar(Geo::kBarKFull + s), 4);
-      tc::mbar_init(bar(Geo::kBarVFull + s), 4);
+      tc::mbar_init(bar(Geo::kBarKFull + s), Geo::kConv / 32);
+      tc::mbar_init(bar(Geo::kBarVFull + s), Geo::kConv / 32);
       tc::mbar_init(bar(Geo::kBarKEmpty + s), 1);
       tc::mbar_init(bar(Geo::kBarVEmpty + s), 1);
       tc::mbar_init(bar(Geo::kBarSFull + s), 1);
@@ -146,10 +150,10 @@ __global__ void __launch_bounds__(rect_threads(D), 1) rect_attention_kernel(cons
       tc::mbar_init(bar(Geo::kBarPFull + 2 * s + 1), 4);
       tc::mbar_init(bar(Geo::kBarOFinal + s), 1);
       tc::mbar_init(bar(Geo::kBarQFull + s), 4);
-      tc::mbar_init(bar(Geo::kBarODone + s), 1);
     }
+    tc::mbar_init(bar(Geo::kBarODone), 1);
     tc::mbar_init(bar(Geo::kBarDrain), 1);
-    tc::mbar_init(bar(Geo::kBarVMax), 4);
+    tc::mbar_init(bar(Geo::kBarVMax), 2);
     *abort_flag = 0u;
     tc::mbar_fence_init();
   }
@@ -171,6 +175,13 @@ __global__ void __launch_bounds__(rect_threads(D), 1) rect_attention_kernel(cons
   constexpr int kChunks = kN / 16;
   constexpr uint32_t kAllChunks = (1u << kChunks) - 1u;
 
+  auto wait = [&](int b, int phase) {  // (of a whole warp)
+    return __all_sync(0xffffffffu, wait_or_abort(bar(b), (uint32_t)(phase & 1), abort_flag));
+  };
+  // the live keys of KV tile g, relative to its first
+  auto live_lo = [&](int g) { return max(kv_lo - (kv_first + g * kN), 0); };
+  auto live_hi = [&](int g) { return min(kv_hi - (kv_first + g * kN), kN); };
+
   if (wg == 0) {
     regs_down<Regs::kIssue>();
     if (warp == 0) {
@@ -180,9 +191,6 @@ __global__ void __launch_bounds__(rect_threads(D), 1) rect_attention_kernel(cons
       constexpr uint32_t idesc_o = (Geo::kAuto ? tc::idesc_bf16(kM, D) : tc::idesc_f16(kM, D)) | tc::kBMajorMN;
       const int n = two ? 2 * T : T;
       auto tile_of = [&](int i) { return two ? i >> 1 : i; };
-      auto wait = [&](int b, int phase) {
-        return __all_sync(0xffffffffu, wait_or_abort(bar(b), (uint32_t)(phase & 1), abort_flag));
-      };
       int k_in = -1, v_in = -1;  // KV tiles whose K / V have been waited for
       auto issue_s = [&](int i) -> bool {
         const int g = tile_of(i), st = g & 1, qt = two ? i & 1 : 0;
@@ -241,8 +249,7 @@ __global__ void __launch_bounds__(rect_threads(D), 1) rect_attention_kernel(cons
                          (!first || kk > 0) ? 1u : 0u);
             }
             }
-            // (the softmax waits for it where its reference moves inside an item)
-            if (h == 0) tc::mma_commit(bar(Geo::kBarODone + (kRT == 2 ? i & 1 : 0)));
+            if (kRT == 1) tc::mma_commit(bar(Geo::kBarODone));
           }
           __syncwarp();
         }
@@ -297,34 +304,90 @@ __global__ void __launch_bounds__(rect_threads(D), 1) rect_attention_kernel(cons
         fetch(g + 1, blk, off);
       }
       __syncwarp();
+    } else {
+      // ---- side data for the softmax, in slot g mod 4 ----------------------
+      // (its last reader, of KV tile g - 4, is done: P(g - 2) V(g - 2) is complete)
+      const int st2 = tid - 64;  // of 64 threads
+      const int32_t* const table = reinterpret_cast<const int32_t*>(sm + Geo::kOffSlots);
+      float* const sk = reinterpret_cast<float*>(sm + Geo::kOffSk);
+      float* const sv = reinterpret_cast<float*>(sm + Geo::kOffSv);
+      uint32_t* const vmaxw = reinterpret_cast<uint32_t*>(sm + Geo::kOffVMax);
+      uint32_t* const smask = reinterpret_cast<uint32_t*>(sm + Geo::kOffSMask);
+      int32_t* const sev = reinterpret_cast<int32_t*>(sm + Geo::kOffSMask + Geo::kSide * 4);
+      constexpr int kKeys = kN / 64;  // keys of a thread
+      constexpr int64_t kRow = row_bytes(DT, D);
+      const int64_t tail = kv_head * kRow + code_bytes(DT, D), tok_bytes = (int64_t)p.heads_kv * kRow;
+      float ks[kKeys], vs[kKeys];
+      uint32_t valid = 0;
+      int ev = -1000;  // exponent of the value scales' reference
+      auto load = [&](int g) -> bool {
+        const int e = g & 3;
+        if (!wait(Geo::kBarSlots + e, g >> 2)) return false;
+        valid = (uint32_t)table[e * 16 + 15];
+        if constexpr (Geo::kPth) {
+          const int lo = live_lo(g), hi = live_hi(g);
+#pragma unroll
+          for (int x = 0; x < kKeys; ++x) {
+            const int nn = st2 + 64 * x;
+            ks[x] = vs[x] = 0.0f;  // (of a dead key)
+            if (((valid >> (nn >> 4)) & 1u) && nn >= lo && nn < hi) {
+              const int64_t off = (int64_t)(table[e * 16 + (nn >> 4)] + (nn & 15)) * tok_bytes + tail;
+              ks[x] = __ldcg(reinterpret_cast<const float*>(p.key_cache + off));
+              vs[x] = __ldcg(reinterpret_cast<const float*>(p.value_cache + off));
+            }
+          }
+        }
+        warp_arrive(bar(Geo::kBarSlotsFree + e));
+        return true;
+      };
+      bool ok = load(0);
+      for (int g = 0; ok && g < T; ++g) {
+        const int sd = g & 3;
+        if (g >= 2 && !wait(Geo::kBarVEmpty + (g & 1), (g >> 1) - 1)) break;
+        if (st2 == 0) smask[sd] = valid;
+        if constexpr (Geo::kPth) {
+          // value scales relative to the largest power of two so far, 2^ev
+          float vmax = 0.0f;  // (a NaN or negative scale is ignored)
+#pragma unroll
+          for (int x = 0; x < kKeys; ++x) vmax = fmaxf(vmax, vs[x]);
+          const uint32_t wmax = __reduce_max_sync(0xffffffffu, __float_as_uint(vmax));
+          if (lane == 0) vmaxw[sd * 4 + (warp & 1)] = wmax;
+          // (both warps, by a wait that ends like the others)
+          warp_arrive(bar(Geo::kBarVMax));
+          if (!wait(Geo::kBarVMax, g)) break;
+          const uint32_t mb = max(vmaxw[sd * 4], vmaxw[sd * 4 + 1]);
+          // (2^e above the largest scale, by its exponent bits)
+          if (mb != 0u) ev = max(ev, max(-125, min(126, (int)(mb >> 23) - 126)));
+          // (no positive scale yet: values are zero)
+          const float to_ref = ev > -1000 ? __int_as_float((127 - ev) << 23) : 0.0f;
+#pragma unroll
+          for (int x = 0; x < kKeys; ++x) {
+            sk[sd * kN + st2 + 64 * x] = ks[x];
+            sv[sd * kN + st2 + 64 * x] = vs[x] * to_ref;
+          }
+          if (st2 == 0) sev[sd] = ev;
+        }
+        warp_arrive(bar(Geo::kBarSide + sd));
+        if (g + 1 < T) ok = load(g + 1);
+      }
+      __syncwarp();
     }
-  } else if (wg <= 2) {
-    // ---- converters: K (group 1) or V (group 2) ----------------------------
+  } else if (wg < Geo::kSoftWg) {
+    // ---- converters: K, then V ---------------------------------------------
     regs_down<Regs::kConvert>();
-    const bool for_v = wg == 2;
-    const int ct = tid & 127;
+    const bool for_v = tid - 128 >= Geo::kConv;
+    const int ct = (tid - 128) % Geo::kConv;
     const uint8_t* const cache = for_v ? p.value_cache : p.key_cache;
     const uint32_t tiles = base + (for_v ? Geo::kOffV : Geo::kOffK);
     const int bar_empty = for_v ? Geo::kBarVEmpty : Geo::kBarKEmpty, bar_full = for_v ? Geo::kBarVFull : Geo::kBarKFull;
     const int32_t* const table = reinterpret_cast<const int32_t*>(sm + Geo::kOffSlots);
-    float* const sk = reinterpret_cast<float*>(sm + Geo::kOffSk);
-    float* const sv = reinterpret_cast<float*>(sm + Geo::kOffSv);
-    uint32_t* const vmaxw = reinterpret_cast<uint32_t*>(sm + Geo::kOffVMax);
-    uint32_t* const smask = reinterpret_cast<uint32_t*>(sm + Geo::kOffSMask);
-    int32_t* const sev = reinterpret_cast<int32_t*>(sm + Geo::kOffSMask + Geo::kSide * 4);
     constexpr int64_t kRow = row_bytes(DT, D);
     const int64_t tok_bytes = (int64_t)p.heads_kv * kRow;
     const uint8_t* const head_at = cache + kv_head * kRow;
-    auto wait = [&](int b, int phase) {
-      return __all_sync(0xffffffffu, wait_or_abort(bar(b), (uint32_t)(phase & 1), abort_flag));
-    };
-    // the live keys of KV tile g, relative to its first
-    auto live_lo = [&](int g) { return max(kv_lo - (kv_first + g * kN), 0); };
-    auto live_hi = [&](int g) { return min(kv_hi - (kv_first + g * kN), kN); };
     if constexpr (Geo::kAuto) {
       // 16-byte pieces of bf16 rows straight into the operand tile; a stage's
       // copies are in flight while the next stage's are issued
-      constexpr int kPieces = D / 8, kStepN = 128 / kPieces, kCopies = kN / kStepN;
+      constexpr int kPieces = D / 8, kStepN = Geo::kConv / kPieces, kCopies = kN / kStepN;
       const int pc = ct % kPieces, n0 = ct / kPieces;
       auto done = [&](int g) {
         tc::fence_async_smem();
@@ -337,7 +400,7 @@ __global__ void __launch_bounds__(rect_threads(D), 1) rect_attention_kernel(cons
         if (g >= 2 && !(ok = wait(bar_empty + st, (g >> 1) - 1))) break;
         const uint32_t valid = (uint32_t)table[e * 16 + 15];
         const int lo = live_lo(g), hi = live_hi(g);
-#pragma unroll
+#pragma unroll 8
         for (int i = 0; i < kCopies; ++i) {
           const int nn = n0 + i * kStepN;
           const bool on = ((valid >> (nn >> 4)) & 1u) && nn >= lo && nn < hi;
@@ -347,10 +410,6 @@ __global__ void __launch_bounds__(rect_threads(D), 1) rect_attention_kernel(cons
                            head_at + slot * tok_bytes + 16 * pc, on ? 16 : 0);
         }
         dev::cp_async_commit();
-        if (for_v) {
-          if (ct == 0) smask[e] = valid;
-          warp_arrive(bar(Geo::kBarSide + e));
-        }
         warp_arrive(bar(Geo::kBarSlotsFree + e));
         if (g > 0) {
           dev::cp_async_wait<1>();
@@ -361,10 +420,12 @@ __global__ void __launch_bounds__(rect_threads(D), 1) rect_attention_kernel(cons
       if (ok) done(T - 1);
     } else {
       // units of (key, 16 codes) or, 4-bit, (key, 32 codes): a thread keeps its piece
-      // of the row, and its keys differ by a multiple of 8 (4-bit: of 16), so that
-      // its offsets in the swizzle are constants
-      constexpr int kPieces = Geo::kInt4 ? D / 32 : D / 16, kStepN = 128 / kPieces, kUnits = kN / kStepN;
-      static_assert(kStepN % 8 == 0 && kN % kStepN == 0, "units");
+      // of the row, and its keys differ by a multiple of 8, so that its offsets in
+      // the swizzle are constants.  In two groups: one is loaded for the next tile
+      // while the other is converted.
+      constexpr int kPieces = Geo::kInt4 ? D / 32 : D / 16, kStepN = Geo::kConv / kPieces, kUnits = kN / kStepN;
+      constexpr int kHalf = kUnits / 2;
+      static_assert(kStepN % 8 == 0 && kN % kStepN == 0 && kUnits % 2 == 0, "units");
       // 4-bit lanes: two pieces of a 64-dim block, four keys, then the blocks and
       // further keys (a quarter-warp's stores then fall on 8 bank groups); 8-bit: the
       // pieces of a key side by side, odd 64-dim blocks storing their halves in
@@ -381,13 +442,11 @@ __global__ void __launch_bounds__(rect_threads(D), 1) rect_attention_kernel(cons
       const uint8_t* const mul = head_at + D / 2 + 4 + (D == 64 ? 4 : D == 128 ? 2 : 1) * pc;
       uint4 c[kUnits];
       uint32_t cm[Geo::kInt4 ? kUnits : 1];
-      float ks = 0.0f, vs = 0.0f;
-      int ev = -1000;  // exponent of the value scales' reference
-      uint32_t valid = 0;
-      auto load_tile = [&](int g) -> bool {
+      // (the slot table of tile g is in)
+      auto load_units = [&](int g, auto group) {
+        constexpr int i0 = decltype(group)::value * kHalf;
         const int e = g & 3;
-        if (!wait(Geo::kBarSlots + e, g >> 2)) return false;
-        valid = (uint32_t)table[e * 16 + 15];
+        const uint32_t valid = (uint32_t)table[e * 16 + 15];
         const int lo = live_lo(g), hi = live_hi(g);
         auto load = [&](int i, int nn) {
           const int64_t off = (int64_t)(table[e * 16 + (nn >> 4)] + (nn & 15)) * tok_bytes;
@@ -400,62 +459,23 @@ __global__ void __launch_bounds__(rect_threads(D), 1) rect_attention_kernel(cons
         };
         if (valid == kAllChunks && lo == 0 && hi == kN) {
 #pragma unroll
-          for (int i = 0; i < kUnits; ++i) load(i, n0 + i * kStepN);
+          for (int i = i0; i < i0 + kHalf; ++i) load(i, n0 + i * kStepN);
         } else {
 #pragma unroll
-          for (int i = 0; i < kUnits; ++i) {
+          for (int i = i0; i < i0 + kHalf; ++i) {
             c[i] = make_uint4(0, 0, 0, 0);
             if constexpr (Geo::kInt4) cm[i] = 0;
             const int nn = n0 + i * kStepN;
             if (((valid >> (nn >> 4)) & 1u) && nn >= lo && nn < hi) load(i, nn);
           }
         }
-        if constexpr (Geo::kPth) {
-          // (key ct's two scales; 0 for a dead key)
-          ks = vs = 0.0f;
-          if (for_v && ct < kN && ((valid >> (ct >> 4)) & 1u) && ct >= lo && ct < hi) {
-            const int64_t off = (int64_t)(table[e * 16 + (ct >> 4)] + (ct & 15)) * tok_bytes + kv_head * kRow +
-                                code_bytes(DT, D);
-            ks = __ldcg(reinterpret_cast<const float*>(p.key_cache + off));
-            vs = __ldcg(reinterpret_cast<const float*>(p.value_cache + off));
-          }
-        }
-        warp_arrive(bar(Geo::kBarSlotsFree + e));
-        return true;
       };
-      bool ok = load_tile(0);
-      for (int g = 0; ok && g < T; ++g) {
-        const int st = g & 1, sd = g & 3;
-        if (g >= 2 && !wait(bar_empty + st, (g >> 1) - 1)) break;
-        if (for_v) {
-          // side data for the softmax in slot g mod 4: its last reader, of KV tile
-          // g - 4, is done (P(g - 2) V(g - 2) is complete)
-          if (ct == 0) smask[sd] = valid;
-          if constexpr (Geo::kPth) {
-            // value scales relative to the largest power of two so far, 2^ev
-            const float vmax = fmaxf(vs, 0.0f);  // (a NaN or negative scale is ignored)
-            const uint32_t wmax = __reduce_max_sync(0xffffffffu, __float_as_uint(vmax));
-            if (lane == 0) vmaxw[sd * 4 + (ct >> 5)] = wmax;
-            // (the group's four warps, by a wait that ends like the others)
-            warp_arrive(bar(Geo::kBarVMax));
-            if (!wait(Geo::kBarVMax, g)) break;
-            const uint4 mb4 = *reinterpret_cast<const uint4*>(vmaxw + sd * 4);
-            const uint32_t mb = max(max(mb4.x, mb4.y), max(mb4.z, mb4.w));
-            // (2^e above the largest scale, by its exponent bits)
-            if (mb != 0u) ev = max(ev, max(-125, min(126, (int)(mb >> 23) - 126)));
-            if (ct < kN) {
-              sk[sd * kN + ct] = ks;
-              // (no positive scale yet: values are zero)
-              sv[sd * kN + ct] = ev > -1000 ? vs * __int_as_float((127 - ev) << 23) : 0.0f;
-            }
-            if (ct == 0) sev[sd] = ev;
-          }
-          warp_arrive(bar(Geo::kBarSide + sd));
-        }
-        const uint32_t tile = tiles + (uint32_t)(st * Geo::kTileBytes) + at0;
-        if constexpr (Geo::kInt4) {
+      auto convert = [&](uint32_t tile, auto group) {
+        constexpr int i0 = decltype(group)::value * kHalf;
 #pragma unroll
-          for (int i = 0; i < kUnits; ++i) {
+        for (int i = i0; i < i0 + kHalf; ++i) {
+          const uint32_t at = tile + (uint32_t)(i * kStepN * 128);
+          if constexpr (Geo::kInt4) {
             const uint32_t w[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
             dev::Int4Mul f[4];
             if constexpr (D == 64) {
@@ -469,20 +489,39 @@ __global__ void __launch_bounds__(rect_threads(D), 1) rect_attention_kernel(cons
             for (int q = 0; q < 4; ++q) {
               uint32_t h[4];
               dev::int4_to_f16x2x4(w[q], f[q], h);
-              sts128(tile + (uint32_t)(i * kStepN * 128) + ((chunk0 ^ (uint32_t)q) << 4), make_uint4(h[0], h[1], h[2], h[3]));
+              sts128(at + ((chunk0 ^ (uint32_t)q) << 4), make_uint4(h[0], h[1], h[2], h[3]));
             }
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < kUnits; ++i) {
-            const uint32_t at = tile + (uint32_t)(i * kStepN * 128);
+          } else {
             sts128(at + (chunk0 << 4), codes8_to_f16<DT>(odd ? c[i].z : c[i].x, odd ? c[i].w : c[i].y));
             sts128(at + ((chunk0 ^ 1u) << 4), codes8_to_f16<DT>(odd ? c[i].x : c[i].z, odd ? c[i].y : c[i].w));
           }
         }
+      };
+      constexpr std::integral_constant<int, 0> first{};
+      constexpr std::integral_constant<int, 1> second{};
+      bool ok = wait(Geo::kBarSlots, 0);
+      if (ok) {
+        load_units(0, first);
+        load_units(0, second);
+        warp_arrive(bar(Geo::kBarSlotsFree));
+      }
+      for (int g = 0; ok && g < T; ++g) {
+        const int st = g & 1, e1 = (g + 1) & 3;
+        const bool more = g + 1 < T;
+        if (g >= 2 && !wait(bar_empty + st, (g >> 1) - 1)) break;
+        const uint32_t tile = tiles + (uint32_t)(st * Geo::kTileBytes) + at0;
+        convert(tile, first);
+        if (more) {
+          if (!wait(Geo::kBarSlots + e1, (g + 1) >> 2)) break;
+          load_units(g + 1, first);
+        }
+        convert(tile, second);
         tc::fence_async_smem();
         warp_arrive(bar(bar_full + st));
-        if (g + 1 < T) ok = load_tile(g + 1);
+        if (more) {
+          load_units(g + 1, second);
+          warp_arrive(bar(Geo::kBarSlotsFree + e1));
+        }
       }
     }
     __syncwarp();
@@ -561,18 +600,6 @@ __global__ void __launch_bounds__(rect_threads(D), 1) rect_attention_kernel(cons
     const uint32_t tmem_o = tmem + Geo::kColO + (kRT == 2 ? (uint32_t)(t * D) : 0u) + lane_base;
     float m_ref = -INFINITY, l_sum = 0.0f;
     int ev = -1000;  // exponent of the value-scale reference (per-token-head)
-    // O times alpha (per row), once the P V issued so far are complete
-    auto rescale_o = [&](float alpha) {
-#pragma unroll 1
-      for (int c0 = 0; c0 < D; c0 += 32) {
-        uint32_t w[32];
-        tc::tmem_ld32(tmem_o + (uint32_t)c0, w);
-        tc::tmem_wait_ld();
-#pragma unroll
-        for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * alpha);
-        tc::tmem_st32(tmem_o + (uint32_t)c0, w);
-      }
-    };
     for (int k = 0; ok && k < count; ++k) {
       const int i = kRT == 1 ? k : 2 * k + t;  // item
       const int g = two ? k : i;               // KV tile
@@ -595,125 +622,139 @@ __global__ void __launch_bounds__(rect_threads(D), 1) rect_attention_kernel(cons
           ev = e;
         }
       }
-#pragma unroll 1
-      for (int h = 0; h < Geo::kHalves; ++h) {
-        const int c0 = 64 * h;
-        uint32_t v[64];
-        tc::tmem_ld32(tmem_s + c0, *reinterpret_cast<uint32_t(*)[32]>(v));
-        tc::tmem_ld32(tmem_s + c0 + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
+      // The row's scores, in pairs, and their maximum.
+      uint64_t z[kN / 2];
+      {
+        uint32_t v[kN];
+#pragma unroll
+        for (int c = 0; c < kN; c += 32) tc::tmem_ld32(tmem_s + c, *reinterpret_cast<uint32_t(*)[32]>(v + c));
         tc::tmem_wait_ld();
-        uint64_t z[32];  // pairs of scores
-        if constexpr (Geo::kPth) {
-          const ulonglong2* const k2 = reinterpret_cast<const ulonglong2*>(sk + sd * kN + c0);
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const ulonglong2 s2 = k2[e / 2];
-            z[e] = dev::mul2(dev::pack2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), s2.x);
-            z[e + 1] = dev::mul2(dev::pack2(__uint_as_float(v[2 * e + 2]), __uint_as_float(v[2 * e + 3])), s2.y);
-          }
-        } else {
+        for (int e = 0; e < kN / 2; ++e) z[e] = dev::pack2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
+      }
+      if constexpr (Geo::kPth) {
+        const ulonglong2* const k2 = reinterpret_cast<const ulonglong2*>(sk + sd * kN);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) z[e] = dev::pack2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
+        for (int e = 0; e < kN / 2; e += 2) {
+          const ulonglong2 s2 = k2[e / 2];
+          z[e] = dev::mul2(z[e], s2.x);
+          z[e + 1] = dev::mul2(z[e + 1], s2.y);
         }
-        if (!plain) {  // final scores, in log2 units
-          const int dist = kv0 + c0 - pos;  // key - position of column c0
+      }
+      if (!plain) {  // final scores, in log2 units
+        const int dist = kv0 - pos;  // key - position of column 0
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            float2 r = dev::unpack2(z[e]);
-            r.x *= score_mul;
-            r.y *= score_mul;
-            if (cap > 0.0f) {
-              r.x = cap_l2 * dev::tanh_exp(r.x * inv_cap);
-              r.y = cap_l2 * dev::tanh_exp(r.y * inv_cap);
-            }
-            z[e] = dev::pack2(fmaf(slope, (float)(dist + 2 * e), r.x), fmaf(slope, (float)(dist + 2 * e + 1), r.y));
+        for (int e = 0; e < kN / 2; ++e) {
+          float2 r = dev::unpack2(z[e]);
+          r.x *= score_mul;
+          r.y *= score_mul;
+          if (cap > 0.0f) {
+            r.x = cap_l2 * dev::tanh_exp(r.x * inv_cap);
+            r.y = cap_l2 * dev::tanh_exp(r.y * inv_cap);
           }
+          z[e] = dev::pack2(fmaf(slope, (float)(dist + 2 * e), r.x), fmaf(slope, (float)(dist + 2 * e + 1), r.y));
         }
-        if (!full) {
-          // masked keys by a bit each
+      }
+      if (!full) {
+        // masked keys by a bit each
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const int lo = min(max(lo_n - c0 - 32 * q, 0), 32), hi = min(max(hi_n - c0 - 32 * q, 0), 32);
-            const uint32_t cm = cmask >> ((c0 >> 4) + 2 * q);
-            uint32_t seen = hi > lo ? (0xFFFFFFFFu << lo) & (0xFFFFFFFFu >> (32 - hi)) : 0u;
-            seen &= (cm & 1u ? 0xFFFFu : 0u) | (cm & 2u ? 0xFFFF0000u : 0u);
+        for (int q = 0; q < kN / 32; ++q) {
+          const int lo = min(max(lo_n - 32 * q, 0), 32), hi = min(max(hi_n - 32 * q, 0), 32);
+          const uint32_t cm = cmask >> (2 * q);
+          uint32_t seen = hi > lo ? (0xFFFFFFFFu << lo) & (0xFFFFFFFFu >> (32 - hi)) : 0u;
+          seen &= (cm & 1u ? 0xFFFFu : 0u) | (cm & 2u ? 0xFFFF0000u : 0u);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float2 r = dev::unpack2(z[16 * q + e]);
-              z[16 * q + e] = dev::pack2((seen >> (2 * e)) & 1u ? r.x : -INFINITY, (seen >> (2 * e + 1)) & 1u ? r.y : -INFINITY);
-            }
+          for (int e = 0; e < 16; ++e) {
+            const float2 r = dev::unpack2(z[16 * q + e]);
+            z[16 * q + e] = dev::pack2((seen >> (2 * e)) & 1u ? r.x : -INFINITY, (seen >> (2 * e + 1)) & 1u ? r.y : -INFINITY);
           }
         }
-        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      }
+      float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const float2 r = dev::unpack2(z[e]);
-          mx4[e & 3] = dev::max3(mx4[e & 3], r.x, r.y);
+      for (int e = 0; e < kN / 2; ++e) {
+        const float2 r = dev::unpack2(z[e]);
+        mx4[e & 3] = dev::max3(mx4[e & 3], r.x, r.y);
+      }
+      const float mr = dev::max3(mx4[0], mx4[1], fmaxf(mx4[2], mx4[3]));
+      const float mx = plain ? mr * score_mul : mr;
+      if (mx > m_ref + 8.0f) {
+        const float nref = ceilf(mx);
+        if (m_ref != -INFINITY) {
+          const float a = __int_as_float((127 + (int)fmaxf(m_ref - nref, -127.0f)) << 23);  // (an integer's power)
+          alpha *= a;
+          l_sum *= a;
         }
-        const float mr = dev::max3(mx4[0], mx4[1], fmaxf(mx4[2], mx4[3]));
-        const float mx = plain ? mr * score_mul : mr;
-        if (mx > m_ref + 8.0f) {
-          const float nref = ceilf(mx);
-          if (m_ref != -INFINITY) {
-            const float a = __int_as_float((127 + (int)fmaxf(m_ref - nref, -127.0f)) << 23);  // (an integer's power)
-            alpha *= a;
-            l_sum *= a;
-          }
-          m_ref = nref;
+        m_ref = nref;
+      }
+      // A moved reference rescales O.  With two Os, this group's products so far
+      // are complete (issued before the S that this item waited for); with one, the
+      // last item's are waited for.
+      if (k > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
+        if constexpr (kRT == 1) {
+          ok = wait(Geo::kBarODone, k - 1);
+          if (!ok) break;
+          tc::fence_after_sync();
         }
-        const float ref = m_ref == -INFINITY ? 0.0f : m_ref - 6.0f;
-        const uint64_t mul2v = dev::pack2(plain ? score_mul : 1.0f, plain ? score_mul : 1.0f);
-        const uint64_t ref2 = dev::pack2(-ref, -ref);
-        constexpr int kPw = Geo::kAuto ? 64 : 32;
-        uint32_t pw[kPw];
-        uint64_t ls[2] = {0ull, 0ull};  // pairs of sums
-        const ulonglong2* const v2 = reinterpret_cast<const ulonglong2*>(sv + sd * kN + c0);
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 16) {
+          uint32_t w[16];
+          tc::tmem_ld16(tmem_o + (uint32_t)c0, w);
+          tc::tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) {
+          for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * alpha);
+          tc::tmem_st16(tmem_o + (uint32_t)c0, w);
+        }
+      }
+      // P = 2^(z - m + 6) in blocks of 32 keys, over columns that the row was read
+      // from; a half (64 keys) is handed over once its stores are complete, which is
+      // looked at a block later.
+      const float ref = m_ref == -INFINITY ? 0.0f : m_ref - 6.0f;
+      const uint64_t mul2v = dev::pack2(plain ? score_mul : 1.0f, plain ? score_mul : 1.0f);
+      const uint64_t ref2 = dev::pack2(-ref, -ref);
+      uint64_t ls[2] = {0ull, 0ull};  // pairs of sums
+      const ulonglong2* const v2 = reinterpret_cast<const ulonglong2*>(sv + sd * kN);
+#pragma unroll
+      for (int q = 0; q < kN / 32; ++q) {
+        uint32_t pw[16], pl[Geo::kAuto ? 16 : 1];
+#pragma unroll
+        for (int e = 0; e < 16; e += 2) {
           ulonglong2 s2;
-          if constexpr (Geo::kPth) s2 = v2[e / 2];
+          if constexpr (Geo::kPth) s2 = v2[8 * q + e / 2];
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
-            const float2 x = dev::unpack2(dev::fma2(z[e + b], mul2v, ref2));
+            const float2 x = dev::unpack2(dev::fma2(z[16 * q + e + b], mul2v, ref2));
             uint64_t q2 = dev::pack2(dev::fast_exp2(x.x), dev::fast_exp2(x.y));
             ls[b] = dev::add2(ls[b], q2);
             if constexpr (Geo::kPth) q2 = dev::mul2(q2, b ? s2.y : s2.x);
-            const float2 q = dev::unpack2(q2);
+            const float2 w = dev::unpack2(q2);
             if constexpr (Geo::kAuto) {
-              const uint32_t hw = dev::pack_bf16x2(q.x, q.y);
-              pw[e + b] = hw;
-              pw[32 + e + b] = dev::pack_bf16x2(q.x - dev::bf16_lo(hw), q.y - dev::bf16_hi(hw));
+              pw[e + b] = dev::pack_bf16x2(w.x, w.y);
+              pl[e + b] = dev::pack_bf16x2(w.x - dev::bf16_lo(pw[e + b]), w.y - dev::bf16_hi(pw[e + b]));
             } else {
-              pw[e + b] = dev::pack_f16x2(q.x, q.y);
+              pw[e + b] = dev::pack_f16x2(w.x, w.y);
             }
           }
         }
-        {
-          const float2 a = dev::unpack2(dev::add2(ls[0], ls[1]));
-          l_sum += a.x + a.y;
+        if (q == 2) {
+          tc::tmem_wait_st();
+          tc::fence_before_sync();
+          warp_arrive(bar(Geo::kBarPFull + 2 * st));
         }
-        // P over the columns that this half read
-#pragma unroll
-        for (int q = 0; q < kPw; q += 16)
-          tc::tmem_st16(tmem_s + (Geo::kAuto ? c0 : 32 * h) + q, *reinterpret_cast<uint32_t(*)[16]>(pw + q));
-        // A moved reference rescales O.  With two Os, this group's products up
-        // to the last item are complete (issued before the S that this item waited
-        // for); those of this item's first half, and with one O the last item's,
-        // are waited for.
-        if ((k > 0 || h > 0) && __any_sync(0xffffffffu, alpha != 1.0f)) {
-          if (h > 0 || kRT == 1) {
-            ok = __all_sync(0xffffffffu, wait_or_abort(bar(Geo::kBarODone + (kRT == 2 ? t : 0)),
-                                                       (uint32_t)((kRT == 2 ? k : k - 1) & 1), abort_flag));
-            if (!ok) break;
-            tc::fence_after_sync();
-          }
-          rescale_o(alpha);
+        if constexpr (Geo::kAuto) {
+          tc::tmem_st16(tmem_s + (uint32_t)(64 * (q / 2) + 16 * (q & 1)), pw);
+          tc::tmem_st16(tmem_s + (uint32_t)(64 * (q / 2) + 32 + 16 * (q & 1)), pl);
+        } else {
+          tc::tmem_st16(tmem_s + (uint32_t)(16 * q), pw);
         }
-        alpha = 1.0f;
-        tc::tmem_wait_st();
-        tc::fence_before_sync();
-        warp_arrive(bar(Geo::kBarPFull + 2 * st + h));
       }
+      {
+        const float2 a = dev::unpack2(dev::add2(ls[0], ls[1]));
+        l_sum += a.x + a.y;
+      }
+      tc::tmem_wait_st();
+      tc::fence_before_sync();
+      warp_arrive(bar(Geo::kBarPFull + 2 * st + Geo::kHalves - 1));
     }
     // ---- epilogue: O / l as fp32 partial rows or bf16 rows -------------------
     if (ok && count > 0) {
@@ -815,7 +856,7 @@ int launch_rect_instance(const AttnParams& p, const RectParams& rp, cudaStream_t
     return KVQ_E_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)rp.num_units);
-  cfg.blockDim = dim3((unsigned)rect_threads(D));
+  cfg.blockDim = dim3(512u);
   cfg.dynamicSmemBytes = rect_smem_bytes(D);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
