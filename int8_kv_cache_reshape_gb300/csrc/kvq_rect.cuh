@@ -29,13 +29,20 @@
 //   softmax    two warpgroups (head_dim 256: one), thread = row = tensor-memory lane;
 //              a thread holds the item's whole row of scores in registers
 // Items: an item is S = Q K^T of a row tile against a KV tile (kN keys) and then
-// O += P V.  Item i has S buffer i mod 2; P replaces S in it.  The MMA warp
-// issues S(0), S(1), then PV(i), S(i + 2), in order.
+// O += P V; the softmax turns S into P.
 //   two row tiles (129 to 256 rows): item i is row tile i mod 2 and KV tile i / 2
 //   one row tile (up to 128 rows): item i is KV tile i, and the two softmax groups
 //     take every other KV tile with an O of their own (two partials a row):
-//     both S buffers and both groups stay busy
+//     both groups stay busy
 //   head_dim 256: O takes half of tensor memory; item i is KV tile i, one group
+// Tensor memory, two softmax groups: two Os, one S and a P for each group.  S is
+// free as soon as a group has read it into registers, so the MMA warp issues
+// S(i + 2) and then PV(i): while a group computes, the tensor core has the other
+// group's products, and the next S of a group is there when it is done.  (With P in S's
+// place -- one S a group, its next S only after its P V -- a 128-key tile of
+// two row tiles took 4,280 cycles, 2,048 of them MMA work.)  One group, and
+// bf16 rows of 128 (P is two numbers, which does not fit): two S buffers, P in place,
+// PV(i) and then S(i + 2).
 // Numbers as in the prefill: Q enters as f16 scaled by a power of two per row
 // (bf16 rows: as it is), scales multiply fp32 scores, value scales fold into P against
 // a running power of two, the reference m is an integer that moves when a score
@@ -70,15 +77,19 @@ struct RectGeom {
   static constexpr int kOffSlots = kOffSMask + kSide * 8;       // kSlotRing x 16 i32
   static constexpr int kOffQScale = kOffSlots + kSlotRing * 64; // kRT x kM f32
   static constexpr int kOffBar = kOffQScale + kRT * kM * 4;
-  static constexpr int kBytes = kOffBar + 288;
-  static constexpr int kColO = 0, kColS = kRT * D;
+  static constexpr int kBytes = kOffBar + 320;
+  static constexpr bool kSplitP = kRT == 2 && !(kAuto && D == 128);  // P beside S
+  static constexpr int kColO = 0, kColS = kRT * D, kColP = kColS + kN, kPCols = kAuto ? kN : kN / 2;
+  // S and P of item i
+  __device__ static constexpr int s_col(int i) { return kSplitP ? kColS : kColS + (i & 1) * kN; }
+  __device__ static constexpr int p_col(int i) { return kSplitP ? kColP + (i & 1) * kPCols : kColS + (i & 1) * kN; }
   static constexpr int kTmemCols = 512;
   static constexpr int kBarSlots = 0, kBarSlotsFree = 4, kBarSide = 8, kBarKFull = 12, kBarVFull = 14, kBarKEmpty = 16,
                        kBarVEmpty = 18, kBarSFull = 20, kBarPFull = 22, kBarOFinal = 26, kBarQFull = 28, kBarODone = 30,
-                       kBarDrain = 31, kBarVMax = 32, kNumBars = 33;
+                       kBarDrain = 32, kBarVMax = 33, kBarSFree = 34, kNumBars = 35;
   static constexpr int kHalves = kN / 64;  // parts of an item whose P is handed over by itself
   static constexpr int kOffTmemSlot = kOffBar + 8 * kNumBars, kOffAbort = kOffTmemSlot + 4;
-  static_assert(kColS + 2 * kN <= kTmemCols, "tensor memory");
+  static_assert((kSplitP ? kColP + 2 * kPCols : kColS + 2 * kN) <= kTmemCols, "tensor memory");
   static_assert(kQBytes % 1024 == 0 && kTileBytes % 1024 == 0 && kOffBar % 8 == 0 && kOffSk % 16 == 0, "alignment");
   static_assert(kOffAbort + 4 <= kBytes && (size_t)kBytes + 1024 == rect_smem_bytes(D), "shared memory");
 };
@@ -150,8 +161,9 @@ __global__ void __launch_bounds__(512, 1) rect_attention_kernel(const AttnParams
       tc::mbar_init(bar(Geo::kBarPFull + 2 * s + 1), 4);
       tc::mbar_init(bar(Geo::kBarOFinal + s), 1);
       tc::mbar_init(bar(Geo::kBarQFull + s), 4);
+      tc::mbar_init(bar(Geo::kBarODone + s), 1);
     }
-    tc::mbar_init(bar(Geo::kBarODone), 1);
+    tc::mbar_init(bar(Geo::kBarSFree), 4);
     tc::mbar_init(bar(Geo::kBarDrain), 1);
     tc::mbar_init(bar(Geo::kBarVMax), 2);
     *abort_flag = 0u;
@@ -195,6 +207,7 @@ __global__ void __launch_bounds__(512, 1) rect_attention_kernel(const AttnParams
       auto issue_s = [&](int i) -> bool {
         const int g = tile_of(i), st = g & 1, qt = two ? i & 1 : 0;
         if ((i == 0 || (two && i == 1)) && !wait(Geo::kBarQFull + qt, 0)) return false;
+        if (Geo::kSplitP && i > 0 && !wait(Geo::kBarSFree, i - 1)) return false;  // S(i - 1) is in registers
         if (g > k_in) {
           if (!wait(Geo::kBarKFull + st, g >> 1)) return false;
           k_in = g;
@@ -207,7 +220,7 @@ __global__ void __launch_bounds__(512, 1) rect_attention_kernel(const AttnParams
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t qoff = (kk >> 2) * (kM * 128) + (kk & 3) * 32, koff = (kk >> 2) * (kN * 128) + (kk & 3) * 32;
             // (kind::f16: the instruction descriptor names the 16-bit type)
-            tc::mma_bf16(tmem + Geo::kColS + (uint32_t)((i & 1) * kN), dq + (uint64_t)(qoff >> 4),
+            tc::mma_bf16(tmem + (uint32_t)Geo::s_col(i), dq + (uint64_t)(qoff >> 4),
                          dk + (uint64_t)(koff >> 4), idesc_s, kk > 0 ? 1u : 0u);
           }
           tc::mma_commit(bar(Geo::kBarSFull + (i & 1)));
@@ -221,6 +234,7 @@ __global__ void __launch_bounds__(512, 1) rect_attention_kernel(const AttnParams
       for (; next < 2 && next < n && ok; ++next) ok = issue_s(next);
       for (int i = 0; i < n && ok; ++i) {
         const int g = tile_of(i), st = g & 1;
+        if (Geo::kSplitP && next < n && !(ok = issue_s(next++))) break;
         ok = wait(Geo::kBarPFull + 2 * (i & 1), i >> 1);
         if (ok && g > v_in) {
           ok = wait(Geo::kBarVFull + st, g >> 1);
@@ -229,7 +243,7 @@ __global__ void __launch_bounds__(512, 1) rect_attention_kernel(const AttnParams
         if (!ok) break;
         const uint64_t dv = tc::desc_sw128_mn(base + Geo::kOffV + (uint32_t)(st * Geo::kTileBytes), kN * 128, 1024);
         const uint32_t o = tmem + Geo::kColO + (kRT == 2 ? (uint32_t)((i & 1) * D) : 0u);
-        const uint32_t pcol = tmem + Geo::kColS + (uint32_t)((i & 1) * kN);
+        const uint32_t pcol = tmem + (uint32_t)Geo::p_col(i);
         const bool first = i < kRT;
 #pragma unroll
         for (int h = 0; h < Geo::kHalves; ++h) {
@@ -249,7 +263,8 @@ __global__ void __launch_bounds__(512, 1) rect_attention_kernel(const AttnParams
                          (!first || kk > 0) ? 1u : 0u);
             }
             }
-            if (kRT == 1) tc::mma_commit(bar(Geo::kBarODone));
+            if (h == Geo::kHalves - 1 && (kRT == 1 || Geo::kSplitP))
+              tc::mma_commit(bar(Geo::kBarODone + (kRT == 2 ? i & 1 : 0)));
           }
           __syncwarp();
         }
@@ -259,7 +274,7 @@ __global__ void __launch_bounds__(512, 1) rect_attention_kernel(const AttnParams
           if (i + kRT >= n) tc::mma_commit(bar(Geo::kBarOFinal + (kRT == 2 ? i & 1 : 0)));
         }
         __syncwarp();
-        if (next < n) ok = issue_s(next++);
+        if (!Geo::kSplitP && next < n) ok = issue_s(next++);
       }
       if (!ok && leader) {
         // drain what was issued before the tensor memory is freed
@@ -343,8 +358,7 @@ __global__ void __launch_bounds__(512, 1) rect_attention_kernel(const AttnParams
       bool ok = load(0);
       for (int g = 0; ok && g < T; ++g) {
         const int sd = g & 3;
-        if (g >= 2 && !wait(Geo::kBarVEmpty + (g & 1), (g >> 1) - 1)) break;
-        if (st2 == 0) smask[sd] = valid;
+        float to_ref = 0.0f;
         if constexpr (Geo::kPth) {
           // value scales relative to the largest power of two so far, 2^ev
           float vmax = 0.0f;  // (a NaN or negative scale is ignored)
@@ -359,7 +373,11 @@ __global__ void __launch_bounds__(512, 1) rect_attention_kernel(const AttnParams
           // (2^e above the largest scale, by its exponent bits)
           if (mb != 0u) ev = max(ev, max(-125, min(126, (int)(mb >> 23) - 126)));
           // (no positive scale yet: values are zero)
-          const float to_ref = ev > -1000 ? __int_as_float((127 - ev) << 23) : 0.0f;
+          to_ref = ev > -1000 ? __int_as_float((127 - ev) << 23) : 0.0f;
+        }
+        if (g >= 2 && !wait(Geo::kBarVEmpty + (g & 1), (g >> 1) - 1)) break;
+        if (st2 == 0) smask[sd] = valid;
+        if constexpr (Geo::kPth) {
 #pragma unroll
           for (int x = 0; x < kKeys; ++x) {
             sk[sd * kN + st2 + 64 * x] = ks[x];
@@ -610,7 +628,7 @@ __global__ void __launch_bounds__(512, 1) rect_attention_kernel(const AttnParams
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc::fence_after_sync();
-      const uint32_t tmem_s = tmem + Geo::kColS + (uint32_t)(st * kN) + lane_base;
+      const uint32_t tmem_s = tmem + (uint32_t)Geo::s_col(i) + lane_base, tmem_p = tmem + (uint32_t)Geo::p_col(i) + lane_base;
       const uint32_t cmask = smask[sd];
       const int lo_n = row_lo - kv0, hi_n = row_hi - kv0;
       const bool full = __all_sync(0xffffffffu, lo_n <= 0 && hi_n >= kN) && cmask == kAllChunks;
@@ -629,6 +647,10 @@ __global__ void __launch_bounds__(512, 1) rect_attention_kernel(const AttnParams
 #pragma unroll
         for (int c = 0; c < kN; c += 32) tc::tmem_ld32(tmem_s + c, *reinterpret_cast<uint32_t(*)[32]>(v + c));
         tc::tmem_wait_ld();
+        if constexpr (Geo::kSplitP) {
+          tc::fence_before_sync();
+          warp_arrive(bar(Geo::kBarSFree));
+        }
 #pragma unroll
         for (int e = 0; e < kN / 2; ++e) z[e] = dev::pack2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
       }
@@ -687,9 +709,14 @@ __global__ void __launch_bounds__(512, 1) rect_attention_kernel(const AttnParams
         }
         m_ref = nref;
       }
-      // A moved reference rescales O.  With two Os, this group's products so far
-      // are complete (issued before the S that this item waited for); with one, the
-      // last item's are waited for.
+      // P beside S: the group's last P V has read P.
+      if constexpr (Geo::kSplitP) {
+        if (k > 0 && !(ok = wait(Geo::kBarODone + t, k - 1))) break;
+        tc::fence_after_sync();
+      }
+      // A moved reference rescales O, once the group's products so far are
+      // complete (with P in S's place and two Os they are: issued before the S that
+      // this item waited for).
       if (k > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
         if constexpr (kRT == 1) {
           ok = wait(Geo::kBarODone, k - 1);
@@ -742,10 +769,10 @@ __global__ void __launch_bounds__(512, 1) rect_attention_kernel(const AttnParams
           warp_arrive(bar(Geo::kBarPFull + 2 * st));
         }
         if constexpr (Geo::kAuto) {
-          tc::tmem_st16(tmem_s + (uint32_t)(64 * (q / 2) + 16 * (q & 1)), pw);
-          tc::tmem_st16(tmem_s + (uint32_t)(64 * (q / 2) + 32 + 16 * (q & 1)), pl);
+          tc::tmem_st16(tmem_p + (uint32_t)(64 * (q / 2) + 16 * (q & 1)), pw);
+          tc::tmem_st16(tmem_p + (uint32_t)(64 * (q / 2) + 32 + 16 * (q & 1)), pl);
         } else {
-          tc::tmem_st16(tmem_s + (uint32_t)(16 * q), pw);
+          tc::tmem_st16(tmem_p + (uint32_t)(16 * q), pw);
         }
       }
       {
