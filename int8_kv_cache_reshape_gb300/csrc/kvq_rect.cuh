@@ -197,8 +197,10 @@ __global__ void __launch_bounds__(512, 1) rect_attention_kernel(const AttnParams
   if (wg == 0) {
     regs_down<Regs::kIssue>();
     if (warp == 0) {
-      // ---- MMA issuer (see the items above) ------------------------------
-      const bool leader = elect_one();
+      // ---- MMA issuer (see the items above): one thread, so that a wait costs
+      // one barrier test and no vote ----------------------------------------
+      if (elect_one()) {
+      auto wait1 = [&](int b, int phase) { return wait_or_abort(bar(b), (uint32_t)(phase & 1), abort_flag); };
       constexpr uint32_t idesc_s = Geo::kAuto ? tc::idesc_bf16(kM, kN) : tc::idesc_f16(kM, kN);
       constexpr uint32_t idesc_o = (Geo::kAuto ? tc::idesc_bf16(kM, D) : tc::idesc_f16(kM, D)) | tc::kBMajorMN;
       const int n = two ? 2 * T : T;
@@ -206,16 +208,16 @@ __global__ void __launch_bounds__(512, 1) rect_attention_kernel(const AttnParams
       int k_in = -1, v_in = -1;  // KV tiles whose K / V have been waited for
       auto issue_s = [&](int i) -> bool {
         const int g = tile_of(i), st = g & 1, qt = two ? i & 1 : 0;
-        if ((i == 0 || (two && i == 1)) && !wait(Geo::kBarQFull + qt, 0)) return false;
-        if (Geo::kSplitP && i > 0 && !wait(Geo::kBarSFree, i - 1)) return false;  // S(i - 1) is in registers
+        if ((i == 0 || (two && i == 1)) && !wait1(Geo::kBarQFull + qt, 0)) return false;
+        if (Geo::kSplitP && i > 0 && !wait1(Geo::kBarSFree, i - 1)) return false;  // S(i - 1) is in registers
         if (g > k_in) {
-          if (!wait(Geo::kBarKFull + st, g >> 1)) return false;
+          if (!wait1(Geo::kBarKFull + st, g >> 1)) return false;
           k_in = g;
         }
         tc::fence_after_sync();
         const uint64_t dq = tc::desc_sw128(base + Geo::kOffQ + (uint32_t)(qt * Geo::kQBytes));
         const uint64_t dk = tc::desc_sw128(base + Geo::kOffK + (uint32_t)(st * Geo::kTileBytes));
-        if (leader) {
+        {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t qoff = (kk >> 2) * (kM * 128) + (kk & 3) * 32, koff = (kk >> 2) * (kN * 128) + (kk & 3) * 32;
@@ -226,7 +228,6 @@ __global__ void __launch_bounds__(512, 1) rect_attention_kernel(const AttnParams
           tc::mma_commit(bar(Geo::kBarSFull + (i & 1)));
           if (!two || (i & 1)) tc::mma_commit(bar(Geo::kBarKEmpty + st));
         }
-        __syncwarp();
         return true;
       };
       bool ok = true;
@@ -235,9 +236,9 @@ __global__ void __launch_bounds__(512, 1) rect_attention_kernel(const AttnParams
       for (int i = 0; i < n && ok; ++i) {
         const int g = tile_of(i), st = g & 1;
         if (Geo::kSplitP && next < n && !(ok = issue_s(next++))) break;
-        ok = wait(Geo::kBarPFull + 2 * (i & 1), i >> 1);
+        ok = wait1(Geo::kBarPFull + 2 * (i & 1), i >> 1);
         if (ok && g > v_in) {
-          ok = wait(Geo::kBarVFull + st, g >> 1);
+          ok = wait1(Geo::kBarVFull + st, g >> 1);
           v_in = g;
         }
         if (!ok) break;
@@ -247,9 +248,9 @@ __global__ void __launch_bounds__(512, 1) rect_attention_kernel(const AttnParams
         const bool first = i < kRT;
 #pragma unroll
         for (int h = 0; h < Geo::kHalves; ++h) {
-          if (h > 0 && !(ok = wait(Geo::kBarPFull + 2 * (i & 1) + h, i >> 1))) break;
+          if (h > 0 && !(ok = wait1(Geo::kBarPFull + 2 * (i & 1) + h, i >> 1))) break;
           tc::fence_after_sync();
-          if (leader) {
+          {
 #pragma unroll
             for (int kk = 4 * h; kk < 4 * h + 4; ++kk) {
             if constexpr (Geo::kAuto) {
@@ -266,20 +267,17 @@ __global__ void __launch_bounds__(512, 1) rect_attention_kernel(const AttnParams
             if (h == Geo::kHalves - 1 && (kRT == 1 || Geo::kSplitP))
               tc::mma_commit(bar(Geo::kBarODone + (kRT == 2 ? i & 1 : 0)));
           }
-          __syncwarp();
         }
         if (!ok) break;
-        if (leader) {
-          if (!two || (i & 1)) tc::mma_commit(bar(Geo::kBarVEmpty + st));
-          if (i + kRT >= n) tc::mma_commit(bar(Geo::kBarOFinal + (kRT == 2 ? i & 1 : 0)));
-        }
-        __syncwarp();
+        if (!two || (i & 1)) tc::mma_commit(bar(Geo::kBarVEmpty + st));
+        if (i + kRT >= n) tc::mma_commit(bar(Geo::kBarOFinal + (kRT == 2 ? i & 1 : 0)));
         if (!Geo::kSplitP && next < n) ok = issue_s(next++);
       }
-      if (!ok && leader) {
+      if (!ok) {
         // drain what was issued before the tensor memory is freed
         tc::mma_commit(bar(Geo::kBarDrain));
         (void)tc::mbar_wait(bar(Geo::kBarDrain), 0u, 200000000LL);
+      }
       }
       __syncwarp();
     } else if (warp == 1) {
