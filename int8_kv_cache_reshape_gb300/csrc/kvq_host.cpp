@@ -360,7 +360,7 @@ void plan_rect(std::vector<RectTile>& tiles, int heads_kv, int head_dim, int sms
       total += (double)heads_kv * ((double)S * kRectStart + (double)T * per);
       longest = std::max(longest, kRectStart + (double)ceil_div(T, S) * per);
       n += heads_kv * S;
-      if (!direct || S > 1) rows += heads_kv * S * t.nrows * (pair(t) ? 2 : 1);
+      if (!direct || S > 1 || pair(t)) rows += heads_kv * S * t.nrows * (pair(t) ? 2 : 1);
     }
     const int64_t waves = ceil_div(n, sms);
     // (partials: written and read once, in L2 mostly)
@@ -380,7 +380,7 @@ void plan_rect(std::vector<RectTile>& tiles, int heads_kv, int head_dim, int sms
     RectTile& t = tiles[i];
     const int64_t T = kv_tiles(t);
     t.splits = T == 0 ? 0 : ceil_div(T, best);
-    const bool whole = direct && t.splits == 1 && (!pair(t) || T == 1);
+    const bool whole = direct && t.splits == 1 && !pair(t);
     t.parts = whole ? 0 : t.splits * (pair(t) ? 2 : 1);
     t.part = *partial_rows;
     *partial_rows += t.parts * t.nrows * heads_kv;

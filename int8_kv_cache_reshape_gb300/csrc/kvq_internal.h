@@ -232,11 +232,11 @@ KVQ_HD constexpr size_t prefill_smem_bytes(int head_dim, int cta_group = 1) {
 KVQ_HD constexpr int rect_row_tiles(int head_dim) { return head_dim >= 256 ? 1 : 2; }
 KVQ_HD constexpr int rect_rows(int head_dim) { return 128 * rect_row_tiles(head_dim); }
 // Shared memory: Q, two K and two V tiles (f16), four slots of per-key scales,
-// value-scale maxima and chunk masks, four slot tables, row scales, barriers; +1
+// chunk masks and value-scale exponents, four slot tables, row scales, barriers; +1
 // KB for 1024-byte alignment.
 KVQ_HD constexpr size_t rect_smem_bytes(int head_dim) {
   return (size_t)rect_rows(head_dim) * head_dim * 2 + 4 * (size_t)prefill_keys(head_dim) * head_dim * 2 +
-         4 * (size_t)(prefill_keys(head_dim) * 8 + 16 + 8 + 64) + (size_t)rect_rows(head_dim) * 4 + 320 + 1024;
+         4 * (size_t)(prefill_keys(head_dim) * 8 + 8 + 64) + (size_t)rect_rows(head_dim) * 4 + 320 + 1024;
 }
 // A prefix's shared part ends at a multiple of this many keys (both plans'
 // chunks); the rest is read with each request's own keys.

@@ -17,10 +17,10 @@
 // of one row tile may be cut among many CTAs, which a causal prefill need not be.
 //
 // Layout (one CTA per SM, one unit per CTA; 16 warps):
-//   warp 0     issues the MMAs
-//   warp 1     resolves 16-key chunks through the block table into slots, up to
+//   warps 0, 1 issue the MMAs, a thread for each softmax group (head_dim 256: warp 0)
+//   warp 2     resolves 16-key chunks through the block table into slots, up to
 //              four KV tiles ahead
-//   warps 2, 3 the KV tiles' side data: per-key scales, chunk mask
+//   warp 3     the KV tiles' side data: per-key scales, chunk mask
 //   converters two warps (head_dim 256: four) for K and as many for V, each thread 16
 //              codes (4-bit: 32) of a key at a time, loaded into registers a KV tile
 //              ahead, converted exactly to f16 and stored in the 128-byte swizzle into
@@ -28,21 +28,20 @@
 //              zero)
 //   softmax    two warpgroups (head_dim 256: one), thread = row = tensor-memory lane;
 //              a thread holds the item's whole row of scores in registers
-// Items: an item is S = Q K^T of a row tile against a KV tile (kN keys) and then
-// O += P V; the softmax turns S into P.
-//   two row tiles (129 to 256 rows): item i is row tile i mod 2 and KV tile i / 2
-//   one row tile (up to 128 rows): item i is KV tile i, and the two softmax groups
-//     take every other KV tile with an O of their own (two partials a row):
-//     both groups stay busy
-//   head_dim 256: O takes half of tensor memory; item i is KV tile i, one group
-// Tensor memory, two softmax groups: two Os, one S and a P for each group.  S is
-// free as soon as a group has read it into registers, so the MMA warp issues
-// S(i + 2) and then PV(i): while a group computes, the tensor core has the other
-// group's products, and the next S of a group is there when it is done.  (With P in S's
-// place -- one S a group, its next S only after its P V -- a 128-key tile of
-// two row tiles took 4,280 cycles, 2,048 of them MMA work.)  One group, and
-// bf16 rows of 128 (P is two numbers, which does not fit): two S buffers, P in place,
-// PV(i) and then S(i + 2).
+// Items: an item is S = Q K^T of a row tile against 64 keys and then O += P V; the
+// softmax turns S into P in place.  A softmax group has its own items, k = 0, 1, ..,
+// and two S buffers, so that S(k + 1) is there when it is done with S(k); S(k + 2)
+// follows P V (k).  Each group's MMAs come from a thread of their own: the
+// barriers and commits of an item take a thread some 700 cycles beside its MMAs,
+// which is 640 cycles' work (one thread for both: 240 us where two take XXX).
+//   two row tiles (129 to 256 rows): each group has a row tile and all keys
+//   one row tile (up to 128 rows): both have its rows and take the halves of each
+//     KV tile, with an O of their own (two partials a row)
+//   head_dim 256: O takes half of tensor memory; one row tile, one group
+// (Items of 128 keys leave no room for a second S: with P in S's place the next S
+// waits for the P V, 4,280 cycles a 128-key tile of two row tiles of which 2,048 are MMA
+// work; with P beside one S of both groups the chain S, load, S is as long.  N = 64
+// reads Q from shared memory twice as often: 2,560 cycles of its bandwidth a tile.)
 // Numbers as in the prefill: Q enters as f16 scaled by a power of two per row
 // (bf16 rows: as it is), scales multiply fp32 scores, value scales fold into P against
 // a running power of two, the reference m is an integer that moves when a score
@@ -72,24 +71,20 @@ struct RectGeom {
   static constexpr int kOffV = kOffK + kStages * kTileBytes;
   static constexpr int kOffSk = kOffV + kStages * kTileBytes;   // kSide x kN f32
   static constexpr int kOffSv = kOffSk + kSide * kN * 4;        // kSide x kN f32
-  static constexpr int kOffVMax = kOffSv + kSide * kN * 4;      // kSide x 4 u32
-  static constexpr int kOffSMask = kOffVMax + kSide * 16;       // kSide u32 masks, kSide i32 exponents
+  static constexpr int kOffSMask = kOffSv + kSide * kN * 4;     // kSide u32 masks, kSide i32 exponents
   static constexpr int kOffSlots = kOffSMask + kSide * 8;       // kSlotRing x 16 i32
   static constexpr int kOffQScale = kOffSlots + kSlotRing * 64; // kRT x kM f32
   static constexpr int kOffBar = kOffQScale + kRT * kM * 4;
   static constexpr int kBytes = kOffBar + 320;
-  static constexpr bool kSplitP = kRT == 2 && !(kAuto && D == 128);  // P beside S
-  static constexpr int kColO = 0, kColS = kRT * D, kColP = kColS + kN, kPCols = kAuto ? kN : kN / 2;
-  // S and P of item i
-  __device__ static constexpr int s_col(int i) { return kSplitP ? kColS : kColS + (i & 1) * kN; }
-  __device__ static constexpr int p_col(int i) { return kSplitP ? kColP + (i & 1) * kPCols : kColS + (i & 1) * kN; }
+  static constexpr int kItem = 64;                    // keys of an item
+  static constexpr int kItems = kN / kItem;           // items of a KV tile
+  static constexpr int kColO = 0, kColS = kRT * D;    // O of each group; its two S (P in place)
   static constexpr int kTmemCols = 512;
   static constexpr int kBarSlots = 0, kBarSlotsFree = 4, kBarSide = 8, kBarKFull = 12, kBarVFull = 14, kBarKEmpty = 16,
-                       kBarVEmpty = 18, kBarSFull = 20, kBarPFull = 22, kBarOFinal = 26, kBarQFull = 28, kBarODone = 30,
-                       kBarDrain = 32, kBarVMax = 33, kBarSFree = 34, kNumBars = 35;
-  static constexpr int kHalves = kN / 64;  // parts of an item whose P is handed over by itself
+                       kBarVEmpty = 18, kBarSFull = 20, kBarPFull = 24, kBarODone = 28, kBarQFull = 30, kBarDrain = 32,
+                       kBarOFinal = 34, kNumBars = 36;
   static constexpr int kOffTmemSlot = kOffBar + 8 * kNumBars, kOffAbort = kOffTmemSlot + 4;
-  static_assert((kSplitP ? kColP + 2 * kPCols : kColS + 2 * kN) <= kTmemCols, "tensor memory");
+  static_assert(kColS + kRT * 2 * kItem <= kTmemCols, "tensor memory");
   static_assert(kQBytes % 1024 == 0 && kTileBytes % 1024 == 0 && kOffBar % 8 == 0 && kOffSk % 16 == 0, "alignment");
   static_assert(kOffAbort + 4 <= kBytes && (size_t)kBytes + 1024 == rect_smem_bytes(D), "shared memory");
 };
@@ -97,10 +92,24 @@ struct RectGeom {
 // Registers a thread of each warpgroup, out of the launch's 512 x 128.
 template <int D>
 struct RectRegs {
-  static constexpr int kIssue = D >= 256 ? 64 : 40, kConvert = D >= 256 ? 104 : 88, kSoftmax = D >= 256 ? 232 : 192;
+  static constexpr int kIssue = 64, kConvert = 104, kSoftmax = D >= 256 ? 232 : 168;
   static_assert(kIssue + (D >= 256 ? 2 : 1) * kConvert + rect_row_tiles(D) * kSoftmax <= 4 * 128,
                 "the groups' registers come out of the launch's");
 };
+
+// wait_or_abort with the second look and the rest out of the way (what the warps
+// run between waits has to stay in the instruction caches).
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile uint32_t* abort) {
+  if (__builtin_expect(tc::mbar_try_wait(bar, parity), 1)) return true;
+  const long long t0 = clock64();
+  while (!tc::mbar_try_wait(bar, parity)) {
+    if (*abort != 0u || clock64() - t0 > 2000000000LL) {  // about a second
+      *abort = 1u;
+      return false;
+    }
+  }
+  return true;
+}
 
 template <int N>
 __device__ __forceinline__ void regs_down() {
@@ -111,7 +120,9 @@ __device__ __forceinline__ void regs_up() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(N));
 }
 
-template <int DT, int D>
+// GEN: with a soft cap or ALiBi (an instance of its own keeps the code of the others
+// small).
+template <int DT, int D, bool GEN>
 __global__ void __launch_bounds__(512, 1) rect_attention_kernel(const AttnParams p, const RectParams rp) {
   using Geo = RectGeom<DT, D>;
   using Regs = RectRegs<D>;
@@ -148,24 +159,21 @@ __global__ void __launch_bounds__(512, 1) rect_attention_kernel(const AttnParams
   if (tid == 0) {
     for (int s = 0; s < 4; ++s) {
       tc::mbar_init(bar(Geo::kBarSlots + s), 1);
-      tc::mbar_init(bar(Geo::kBarSlotsFree + s), 2 * Geo::kConv / 32 + 2);
-      tc::mbar_init(bar(Geo::kBarSide + s), 2);
+      tc::mbar_init(bar(Geo::kBarSlotsFree + s), 2 * Geo::kConv / 32 + 1);
+      tc::mbar_init(bar(Geo::kBarSide + s), 1);
+      tc::mbar_init(bar(Geo::kBarSFull + s), 1);
+      tc::mbar_init(bar(Geo::kBarPFull + s), 4);
     }
     for (int s = 0; s < 2; ++s) {
       tc::mbar_init(bar(Geo::kBarKFull + s), Geo::kConv / 32);
       tc::mbar_init(bar(Geo::kBarVFull + s), Geo::kConv / 32);
-      tc::mbar_init(bar(Geo::kBarKEmpty + s), 1);
-      tc::mbar_init(bar(Geo::kBarVEmpty + s), 1);
-      tc::mbar_init(bar(Geo::kBarSFull + s), 1);
-      tc::mbar_init(bar(Geo::kBarPFull + 2 * s), 4);
-      tc::mbar_init(bar(Geo::kBarPFull + 2 * s + 1), 4);
-      tc::mbar_init(bar(Geo::kBarOFinal + s), 1);
+      tc::mbar_init(bar(Geo::kBarKEmpty + s), kRT);
+      tc::mbar_init(bar(Geo::kBarVEmpty + s), kRT);
       tc::mbar_init(bar(Geo::kBarQFull + s), 4);
       tc::mbar_init(bar(Geo::kBarODone + s), 1);
+      tc::mbar_init(bar(Geo::kBarDrain + s), 1);
+      tc::mbar_init(bar(Geo::kBarOFinal + s), 1);
     }
-    tc::mbar_init(bar(Geo::kBarSFree), 4);
-    tc::mbar_init(bar(Geo::kBarDrain), 1);
-    tc::mbar_init(bar(Geo::kBarVMax), 2);
     *abort_flag = 0u;
     tc::mbar_fence_init();
   }
@@ -188,7 +196,7 @@ __global__ void __launch_bounds__(512, 1) rect_attention_kernel(const AttnParams
   constexpr uint32_t kAllChunks = (1u << kChunks) - 1u;
 
   auto wait = [&](int b, int phase) {  // (of a whole warp)
-    return __all_sync(0xffffffffu, wait_or_abort(bar(b), (uint32_t)(phase & 1), abort_flag));
+    return __all_sync(0xffffffffu, wait_bar(bar(b), (uint32_t)(phase & 1), abort_flag));
   };
   // the live keys of KV tile g, relative to its first
   auto live_lo = [&](int g) { return max(kv_lo - (kv_first + g * kN), 0); };
@@ -196,91 +204,67 @@ __global__ void __launch_bounds__(512, 1) rect_attention_kernel(const AttnParams
 
   if (wg == 0) {
     regs_down<Regs::kIssue>();
-    if (warp == 0) {
-      // ---- MMA issuer (see the items above): one thread, so that a wait costs
-      // one barrier test and no vote ----------------------------------------
+    if (warp < kRT) {
+      // ---- MMA issuer of softmax group `warp` (see the items above): one thread,
+      // so that a wait costs one barrier test and no vote --------------------
       if (elect_one()) {
-      auto wait1 = [&](int b, int phase) { return wait_or_abort(bar(b), (uint32_t)(phase & 1), abort_flag); };
-      constexpr uint32_t idesc_s = Geo::kAuto ? tc::idesc_bf16(kM, kN) : tc::idesc_f16(kM, kN);
-      constexpr uint32_t idesc_o = (Geo::kAuto ? tc::idesc_bf16(kM, D) : tc::idesc_f16(kM, D)) | tc::kBMajorMN;
-      const int n = two ? 2 * T : T;
-      auto tile_of = [&](int i) { return two ? i >> 1 : i; };
-      int k_in = -1, v_in = -1;  // KV tiles whose K / V have been waited for
-      auto issue_s = [&](int i) -> bool {
-        const int g = tile_of(i), st = g & 1, qt = two ? i & 1 : 0;
-        if ((i == 0 || (two && i == 1)) && !wait1(Geo::kBarQFull + qt, 0)) return false;
-        if (Geo::kSplitP && i > 0 && !wait1(Geo::kBarSFree, i - 1)) return false;  // S(i - 1) is in registers
-        if (g > k_in) {
-          if (!wait1(Geo::kBarKFull + st, g >> 1)) return false;
-          k_in = g;
-        }
-        tc::fence_after_sync();
+        auto wait1 = [&](int b, int phase) { return wait_bar(bar(b), (uint32_t)(phase & 1), abort_flag); };
+        constexpr uint32_t idesc_s = Geo::kAuto ? tc::idesc_bf16(kM, Geo::kItem) : tc::idesc_f16(kM, Geo::kItem);
+        constexpr uint32_t idesc_o = (Geo::kAuto ? tc::idesc_bf16(kM, D) : tc::idesc_f16(kM, D)) | tc::kBMajorMN;
+        // the group's items of a KV tile: all, or (one row tile) one of the halves
+        const bool all = kRT == 1 || two;
+        const int qt = two ? warp : 0, count = all ? Geo::kItems * T : T;
         const uint64_t dq = tc::desc_sw128(base + Geo::kOffQ + (uint32_t)(qt * Geo::kQBytes));
-        const uint64_t dk = tc::desc_sw128(base + Geo::kOffK + (uint32_t)(st * Geo::kTileBytes));
-        {
+        const uint32_t s_at = tmem + (uint32_t)(Geo::kColS + warp * 2 * Geo::kItem);
+        const uint32_t o_at = tmem + (uint32_t)(Geo::kColO + warp * D);
+        const uint64_t dk0 = tc::desc_sw128(base + Geo::kOffK), dv0 = tc::desc_sw128_mn(base + Geo::kOffV, kN * 128, 1024);
+        bool ok = wait1(Geo::kBarQFull + qt, 0);
+        for (int k = -2; k < count && ok; ++k) {
+          if (k >= 0) {
+            // O += P V (k)
+            const int g = all ? k / Geo::kItems : k, h = all ? k % Geo::kItems : warp, st = g & 1;
+            if (!(ok = wait1(Geo::kBarPFull + 2 * warp + (k & 1), k >> 1))) break;
+            if ((!all || h == 0) && !(ok = wait1(Geo::kBarVFull + st, g >> 1))) break;
+            tc::fence_after_sync();
+            const uint64_t dv = dv0 + (uint64_t)((st * Geo::kTileBytes + h * Geo::kItem * 128) >> 4);
+            const uint32_t p_at = s_at + (uint32_t)((k & 1) * Geo::kItem);
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t qoff = (kk >> 2) * (kM * 128) + (kk & 3) * 32, koff = (kk >> 2) * (kN * 128) + (kk & 3) * 32;
-            // (kind::f16: the instruction descriptor names the 16-bit type)
-            tc::mma_bf16(tmem + (uint32_t)Geo::s_col(i), dq + (uint64_t)(qoff >> 4),
-                         dk + (uint64_t)(koff >> 4), idesc_s, kk > 0 ? 1u : 0u);
+            for (int kk = 0; kk < Geo::kItem / 16; ++kk) {
+              const uint64_t dvk = dv + (uint64_t)(kk * (2048 >> 4));
+              tc::mma_ts(o_at, p_at + (uint32_t)(kk * 8), dvk, idesc_o, (k > 0 || kk > 0) ? 1u : 0u);
+              // (bf16 rows: P = hi + lo, both bf16, lo 32 columns on)
+              if constexpr (Geo::kAuto) tc::mma_ts(o_at, p_at + (uint32_t)(32 + kk * 8), dvk, idesc_o, 1u);
+            }
+            if (!all || h == Geo::kItems - 1) tc::mma_commit(bar(Geo::kBarVEmpty + st));
+            // (the S after next stands for the others)
+            if (k >= count - 2) tc::mma_commit(bar((k == count - 1 ? Geo::kBarOFinal : Geo::kBarODone) + warp));
           }
-          tc::mma_commit(bar(Geo::kBarSFull + (i & 1)));
-          if (!two || (i & 1)) tc::mma_commit(bar(Geo::kBarKEmpty + st));
-        }
-        return true;
-      };
-      bool ok = true;
-      int next = 0;
-      for (; next < 2 && next < n && ok; ++next) ok = issue_s(next);
-      for (int i = 0; i < n && ok; ++i) {
-        const int g = tile_of(i), st = g & 1;
-        if (Geo::kSplitP && next < n && !(ok = issue_s(next++))) break;
-        ok = wait1(Geo::kBarPFull + 2 * (i & 1), i >> 1);
-        if (ok && g > v_in) {
-          ok = wait1(Geo::kBarVFull + st, g >> 1);
-          v_in = g;
-        }
-        if (!ok) break;
-        const uint64_t dv = tc::desc_sw128_mn(base + Geo::kOffV + (uint32_t)(st * Geo::kTileBytes), kN * 128, 1024);
-        const uint32_t o = tmem + Geo::kColO + (kRT == 2 ? (uint32_t)((i & 1) * D) : 0u);
-        const uint32_t pcol = tmem + (uint32_t)Geo::p_col(i);
-        const bool first = i < kRT;
+          const int k2 = k + 2;
+          if (k2 < count) {
+            // S (k + 2)
+            const int g = all ? k2 / Geo::kItems : k2, h = all ? k2 % Geo::kItems : warp, st = g & 1;
+            if ((!all || h == 0) && !(ok = wait1(Geo::kBarKFull + st, g >> 1))) break;
+            tc::fence_after_sync();
+            const uint64_t dk = dk0 + (uint64_t)((st * Geo::kTileBytes + h * Geo::kItem * 128) >> 4);
 #pragma unroll
-        for (int h = 0; h < Geo::kHalves; ++h) {
-          if (h > 0 && !(ok = wait1(Geo::kBarPFull + 2 * (i & 1) + h, i >> 1))) break;
-          tc::fence_after_sync();
-          {
-#pragma unroll
-            for (int kk = 4 * h; kk < 4 * h + 4; ++kk) {
-            if constexpr (Geo::kAuto) {
-              // P = hi + lo, both bf16: hi of keys c0 .. c0 + 63 in columns c0 ..
-              // c0 + 31, lo in c0 + 32 .. c0 + 63
-              const uint32_t pc = pcol + (uint32_t)(64 * (kk / 4) + 8 * (kk % 4));
-              tc::mma_ts(o, pc, dv + (uint64_t)(kk * (2048 >> 4)), idesc_o, (!first || kk > 0) ? 1u : 0u);
-              tc::mma_ts(o, pc + 32u, dv + (uint64_t)(kk * (2048 >> 4)), idesc_o, 1u);
-            } else {
-              tc::mma_ts(o, pcol + (uint32_t)(32 * h + (kk & 3) * 8), dv + (uint64_t)(kk * (2048 >> 4)), idesc_o,
-                         (!first || kk > 0) ? 1u : 0u);
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t qoff = (kk >> 2) * (kM * 128) + (kk & 3) * 32, koff = (kk >> 2) * (kN * 128) + (kk & 3) * 32;
+              // (kind::f16: the instruction descriptor names the 16-bit type)
+              tc::mma_bf16(s_at + (uint32_t)((k & 1) * Geo::kItem), dq + (uint64_t)(qoff >> 4), dk + (uint64_t)(koff >> 4),
+                           idesc_s, kk > 0 ? 1u : 0u);
             }
-            }
-            if (h == Geo::kHalves - 1 && (kRT == 1 || Geo::kSplitP))
-              tc::mma_commit(bar(Geo::kBarODone + (kRT == 2 ? i & 1 : 0)));
+            tc::mma_commit(bar(Geo::kBarSFull + 2 * warp + (k & 1)));
+            if (!all || h == Geo::kItems - 1) tc::mma_commit(bar(Geo::kBarKEmpty + st));
           }
         }
-        if (!ok) break;
-        if (!two || (i & 1)) tc::mma_commit(bar(Geo::kBarVEmpty + st));
-        if (i + kRT >= n) tc::mma_commit(bar(Geo::kBarOFinal + (kRT == 2 ? i & 1 : 0)));
-        if (!Geo::kSplitP && next < n) ok = issue_s(next++);
-      }
-      if (!ok) {
-        // drain what was issued before the tensor memory is freed
-        tc::mma_commit(bar(Geo::kBarDrain));
-        (void)tc::mbar_wait(bar(Geo::kBarDrain), 0u, 200000000LL);
-      }
+        if (!ok) {
+          // drain what was issued before the tensor memory is freed
+          tc::mma_commit(bar(Geo::kBarDrain + warp));
+          (void)tc::mbar_wait(bar(Geo::kBarDrain + warp), 0u, 200000000LL);
+        }
       }
       __syncwarp();
-    } else if (warp == 1) {
+    } else if (warp == 2) {
       // ---- slots of the KV tiles' 16-key chunks --------------------------
       // (entries are loaded a tile ahead; the block size is a multiple of 16;
       // q = hi32(j floor((2^32 - 1) / B)) is the quotient or one less)
@@ -306,7 +290,7 @@ __global__ void __launch_bounds__(512, 1) rect_attention_kernel(const AttnParams
       fetch(0, blk, off);
       for (int g = 0; g < T; ++g) {
         const int e = g & 3;
-        if (g >= 4 && !__all_sync(0xffffffffu, wait_or_abort(bar(Geo::kBarSlotsFree + e), (uint32_t)(((g >> 2) - 1) & 1),
+        if (g >= 4 && !__all_sync(0xffffffffu, wait_bar(bar(Geo::kBarSlotsFree + e), (uint32_t)(((g >> 2) - 1) & 1),
                                                              abort_flag)))
           break;
         const bool in = blk >= 0 && (int64_t)blk < p.num_blocks;
@@ -317,17 +301,15 @@ __global__ void __launch_bounds__(512, 1) rect_attention_kernel(const AttnParams
         fetch(g + 1, blk, off);
       }
       __syncwarp();
-    } else {
+    } else if (warp == 3) {
       // ---- side data for the softmax, in slot g mod 4 ----------------------
       // (its last reader, of KV tile g - 4, is done: P(g - 2) V(g - 2) is complete)
-      const int st2 = tid - 64;  // of 64 threads
       const int32_t* const table = reinterpret_cast<const int32_t*>(sm + Geo::kOffSlots);
       float* const sk = reinterpret_cast<float*>(sm + Geo::kOffSk);
       float* const sv = reinterpret_cast<float*>(sm + Geo::kOffSv);
-      uint32_t* const vmaxw = reinterpret_cast<uint32_t*>(sm + Geo::kOffVMax);
       uint32_t* const smask = reinterpret_cast<uint32_t*>(sm + Geo::kOffSMask);
       int32_t* const sev = reinterpret_cast<int32_t*>(sm + Geo::kOffSMask + Geo::kSide * 4);
-      constexpr int kKeys = kN / 64;  // keys of a thread
+      constexpr int kKeys = kN / 32;  // keys of a thread
       constexpr int64_t kRow = row_bytes(DT, D);
       const int64_t tail = kv_head * kRow + code_bytes(DT, D), tok_bytes = (int64_t)p.heads_kv * kRow;
       float ks[kKeys], vs[kKeys];
@@ -341,7 +323,7 @@ __global__ void __launch_bounds__(512, 1) rect_attention_kernel(const AttnParams
           const int lo = live_lo(g), hi = live_hi(g);
 #pragma unroll
           for (int x = 0; x < kKeys; ++x) {
-            const int nn = st2 + 64 * x;
+            const int nn = lane + 32 * x;
             ks[x] = vs[x] = 0.0f;  // (of a dead key)
             if (((valid >> (nn >> 4)) & 1u) && nn >= lo && nn < hi) {
               const int64_t off = (int64_t)(table[e * 16 + (nn >> 4)] + (nn & 15)) * tok_bytes + tail;
@@ -353,8 +335,9 @@ __global__ void __launch_bounds__(512, 1) rect_attention_kernel(const AttnParams
         warp_arrive(bar(Geo::kBarSlotsFree + e));
         return true;
       };
-      bool ok = load(0);
-      for (int g = 0; ok && g < T; ++g) {
+      bool ok = true;
+      for (int g = 0; g < T; ++g) {
+        if (!(ok = load(g))) break;
         const int sd = g & 3;
         float to_ref = 0.0f;
         if constexpr (Geo::kPth) {
@@ -362,29 +345,23 @@ __global__ void __launch_bounds__(512, 1) rect_attention_kernel(const AttnParams
           float vmax = 0.0f;  // (a NaN or negative scale is ignored)
 #pragma unroll
           for (int x = 0; x < kKeys; ++x) vmax = fmaxf(vmax, vs[x]);
-          const uint32_t wmax = __reduce_max_sync(0xffffffffu, __float_as_uint(vmax));
-          if (lane == 0) vmaxw[sd * 4 + (warp & 1)] = wmax;
-          // (both warps, by a wait that ends like the others)
-          warp_arrive(bar(Geo::kBarVMax));
-          if (!wait(Geo::kBarVMax, g)) break;
-          const uint32_t mb = max(vmaxw[sd * 4], vmaxw[sd * 4 + 1]);
+          const uint32_t mb = __reduce_max_sync(0xffffffffu, __float_as_uint(vmax));
           // (2^e above the largest scale, by its exponent bits)
           if (mb != 0u) ev = max(ev, max(-125, min(126, (int)(mb >> 23) - 126)));
           // (no positive scale yet: values are zero)
           to_ref = ev > -1000 ? __int_as_float((127 - ev) << 23) : 0.0f;
         }
         if (g >= 2 && !wait(Geo::kBarVEmpty + (g & 1), (g >> 1) - 1)) break;
-        if (st2 == 0) smask[sd] = valid;
+        if (lane == 0) smask[sd] = valid;
         if constexpr (Geo::kPth) {
 #pragma unroll
           for (int x = 0; x < kKeys; ++x) {
-            sk[sd * kN + st2 + 64 * x] = ks[x];
-            sv[sd * kN + st2 + 64 * x] = vs[x] * to_ref;
+            sk[sd * kN + lane + 32 * x] = ks[x];
+            sv[sd * kN + lane + 32 * x] = vs[x] * to_ref;
           }
-          if (st2 == 0) sev[sd] = ev;
+          if (lane == 0) sev[sd] = ev;
         }
         warp_arrive(bar(Geo::kBarSide + sd));
-        if (g + 1 < T) ok = load(g + 1);
       }
       __syncwarp();
     }
@@ -458,31 +435,36 @@ __global__ void __launch_bounds__(512, 1) rect_attention_kernel(const AttnParams
       const uint8_t* const mul = head_at + D / 2 + 4 + (D == 64 ? 4 : D == 128 ? 2 : 1) * pc;
       uint4 c[kUnits];
       uint32_t cm[Geo::kInt4 ? kUnits : 1];
-      // (the slot table of tile g is in)
+      // The codes of tile g's units (its slot table is in).  Dead keys (outside the
+      // range, or in a chunk without a block) read some row of the pool: their scores
+      // are masked; their values are cleared, since an fp8 code may be NaN and a byte
+      // that is no multiplier gives infinities (every int8 code is finite).
       auto load_units = [&](int g, auto group) {
         constexpr int i0 = decltype(group)::value * kHalf;
-        const int e = g & 3;
-        const uint32_t valid = (uint32_t)table[e * 16 + 15];
-        const int lo = live_lo(g), hi = live_hi(g);
-        auto load = [&](int i, int nn) {
-          const int64_t off = (int64_t)(table[e * 16 + (nn >> 4)] + (nn & 15)) * tok_bytes;
+        const int32_t* const slots = table + (g & 3) * 16;
+#pragma unroll
+        for (int i = i0; i < i0 + kHalf; ++i) {
+          const int nn = n0 + i * kStepN;
+          const int64_t off = (int64_t)(slots[nn >> 4] + (nn & 15)) * tok_bytes;
           c[i] = dev::ldg_stream_coherent(from + off);
           if constexpr (Geo::kInt4) {
             if constexpr (D == 64) cm[i] = *reinterpret_cast<const uint32_t*>(mul + off);
             else if constexpr (D == 128) cm[i] = *reinterpret_cast<const uint16_t*>(mul + off);
             else cm[i] = *(mul + off);
           }
-        };
-        if (valid == kAllChunks && lo == 0 && hi == kN) {
+        }
+        if constexpr (code_format(DT) != KVQ_INT8_PER_TOKEN_HEAD) {
+          const uint32_t valid = (uint32_t)slots[15];
+          const int lo = live_lo(g), hi = live_hi(g);
+          if (for_v && (valid != kAllChunks || lo != 0 || hi != kN)) {
 #pragma unroll
-          for (int i = i0; i < i0 + kHalf; ++i) load(i, n0 + i * kStepN);
-        } else {
-#pragma unroll
-          for (int i = i0; i < i0 + kHalf; ++i) {
-            c[i] = make_uint4(0, 0, 0, 0);
-            if constexpr (Geo::kInt4) cm[i] = 0;
-            const int nn = n0 + i * kStepN;
-            if (((valid >> (nn >> 4)) & 1u) && nn >= lo && nn < hi) load(i, nn);
+            for (int i = i0; i < i0 + kHalf; ++i) {
+              const int nn = n0 + i * kStepN;
+              if (!((valid >> (nn >> 4)) & 1u) || nn < lo || nn >= hi) {
+                c[i] = make_uint4(0, 0, 0, 0);
+                if constexpr (Geo::kInt4) cm[i] = 0;
+              }
+            }
           }
         }
       };
@@ -515,25 +497,22 @@ __global__ void __launch_bounds__(512, 1) rect_attention_kernel(const AttnParams
       };
       constexpr std::integral_constant<int, 0> first{};
       constexpr std::integral_constant<int, 1> second{};
-      bool ok = wait(Geo::kBarSlots, 0);
-      if (ok) {
-        load_units(0, first);
-        load_units(0, second);
-        warp_arrive(bar(Geo::kBarSlotsFree));
-      }
-      for (int g = 0; ok && g < T; ++g) {
+      // Step g: convert tile g, load tile g + 1 (from step -1 on).
+      for (int g = -1; g < T; ++g) {
         const int st = g & 1, e1 = (g + 1) & 3;
         const bool more = g + 1 < T;
         if (g >= 2 && !wait(bar_empty + st, (g >> 1) - 1)) break;
         const uint32_t tile = tiles + (uint32_t)(st * Geo::kTileBytes) + at0;
-        convert(tile, first);
+        if (g >= 0) convert(tile, first);
         if (more) {
           if (!wait(Geo::kBarSlots + e1, (g + 1) >> 2)) break;
           load_units(g + 1, first);
         }
-        convert(tile, second);
-        tc::fence_async_smem();
-        warp_arrive(bar(bar_full + st));
+        if (g >= 0) {
+          convert(tile, second);
+          tc::fence_async_smem();
+          warp_arrive(bar(bar_full + st));
+        }
         if (more) {
           load_units(g + 1, second);
           warp_arrive(bar(Geo::kBarSlotsFree + e1));
@@ -551,12 +530,12 @@ __global__ void __launch_bounds__(512, 1) rect_attention_kernel(const AttnParams
     float* const qscale = reinterpret_cast<float*>(sm + Geo::kOffQScale) + tile * kM;
     bool ok = true;
     if (two || t == 0) {
-      // Q of the warp's 32 rows: D / 8 lanes a row, 16 bytes each, up to 16 loads
-      // in flight.  A row enters as f16 scaled by the power of two that puts its
+      // Q of the warp's 32 rows: D / 8 lanes a row, 16 bytes each, eight loads in
+      // flight.  A row enters as f16 scaled by the power of two that puts its
       // largest |q| in [2^13, 2^14): exact but for elements 2^27 below that one
       // (subnormals).  The score scale's sign enters with Q, so that the softmax's
       // factor is positive.
-      constexpr int kLpr = D / 8, kRpi = 32 / kLpr, kBatch = 32 / kRpi < 16 ? 32 / kRpi : 16;
+      constexpr int kLpr = D / 8, kRpi = 32 / kLpr, kBatch = 8;
       const float qk_scale = Geo::kPth || Geo::kAuto ? p.sm_scale : p.sm_scale * p.k_scale;
       const uint32_t keep = qk_scale == 0.0f ? 0u : 0xFFFFFFFFu, flip = qk_scale < 0.0f ? 0x80008000u : 0u;
       const int sub = lane / kLpr, pc = lane % kLpr;
@@ -596,40 +575,41 @@ __global__ void __launch_bounds__(512, 1) rect_attention_kernel(const AttnParams
       warp_arrive(bar(Geo::kBarQFull + tile));
     }
     // (the other group's rows where both take the one row tile)
-    ok = __all_sync(0xffffffffu, wait_or_abort(bar(Geo::kBarQFull + tile), 0u, abort_flag));
+    ok = __all_sync(0xffffffffu, wait_bar(bar(Geo::kBarQFull + tile), 0u, abort_flag));
     const float q_unscale = qscale[m];
 
     const float* const sk = reinterpret_cast<const float*>(sm + Geo::kOffSk);
     const float* const sv = reinterpret_cast<const float*>(sm + Geo::kOffSv);
     const uint32_t* const smask = reinterpret_cast<const uint32_t*>(sm + Geo::kOffSMask);
     const int32_t* const sev = reinterpret_cast<const int32_t*>(sm + Geo::kOffSMask + Geo::kSide * 4);
-    const float cap = p.soft_cap, cap_l2 = cap * log2e, inv_cap = cap > 0.0f ? 1.0f / cap : 0.0f;
-    const bool plain = cap <= 0.0f && p.alibi_slopes == nullptr;
-    const float slope = p.alibi_slopes ? p.alibi_slopes[head_q] * log2e : 0.0f;
+    const float cap = GEN ? p.soft_cap : 0.0f, cap_l2 = cap * log2e, inv_cap = cap > 0.0f ? 1.0f / cap : 0.0f;
+    const float slope = GEN && p.alibi_slopes ? p.alibi_slopes[head_q] * log2e : 0.0f;
     const int row_hi = row_valid ? kv_hi : 0;  // padding rows see nothing
     const int row_lo = max(kv_lo, p.window > 0 ? pos - p.window + 1 : 0);
     // scores in log2 units (natural units under a soft cap); never zero, which times -inf is NaN
     const float signed_mul = p.sm_scale * (Geo::kInt4 ? dev::kInt4Unit : 1.0f) * q_unscale *
                              (cap > 0.0f ? 1.0f : log2e) * (Geo::kPth || Geo::kAuto ? 1.0f : p.k_scale);
     const float score_mul = fmaxf(fabsf(signed_mul), 0x1p-126f);
-    const int count = kRT == 1 || two ? T : (T - t + 1) / 2;  // this group's items
+    // this group's items: all 64-key tiles, or one of the halves of each KV tile
+    const int subs = Geo::kItems * T, count = kRT == 1 || two ? subs : subs / 2;
     const uint32_t tmem_o = tmem + Geo::kColO + (kRT == 2 ? (uint32_t)(t * D) : 0u) + lane_base;
     float m_ref = -INFINITY, l_sum = 0.0f;
     int ev = -1000;  // exponent of the value-scale reference (per-token-head)
     for (int k = 0; ok && k < count; ++k) {
-      const int i = kRT == 1 ? k : 2 * k + t;  // item
-      const int g = two ? k : i;               // KV tile
-      const int st = i & 1, sd = g & 3;
-      const int kv0 = kv_first + g * kN;
-      ok = wait_or_abort(bar(Geo::kBarSFull + st), (uint32_t)((i >> 1) & 1), abort_flag) &&
-           wait_or_abort(bar(Geo::kBarSide + sd), (uint32_t)((g >> 2) & 1), abort_flag);
+      const int u = kRT == 1 || two ? k : 2 * k + t;  // 64-key tile
+      const int g = u / Geo::kItems, h = u % Geo::kItems;
+      const int b = 2 * t + (k & 1), sd = g & 3;
+      const int kv0 = kv_first + u * Geo::kItem;
+      ok = wait_bar(bar(Geo::kBarSFull + b), (uint32_t)((k >> 1) & 1), abort_flag) &&
+           wait_bar(bar(Geo::kBarSide + sd), (uint32_t)((g >> 2) & 1), abort_flag);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc::fence_after_sync();
-      const uint32_t tmem_s = tmem + (uint32_t)Geo::s_col(i) + lane_base, tmem_p = tmem + (uint32_t)Geo::p_col(i) + lane_base;
-      const uint32_t cmask = smask[sd];
+      const uint32_t tmem_s = tmem + (uint32_t)(Geo::kColS + b * Geo::kItem) + lane_base;
+      const uint32_t cmask = (smask[sd] >> (4 * h)) & 0xFu;  // 16-key chunks of the item
+      const int side = sd * kN + h * Geo::kItem;
       const int lo_n = row_lo - kv0, hi_n = row_hi - kv0;
-      const bool full = __all_sync(0xffffffffu, lo_n <= 0 && hi_n >= kN) && cmask == kAllChunks;
+      const bool full = __all_sync(0xffffffffu, lo_n <= 0 && hi_n >= Geo::kItem) && cmask == 0xFu;
       float alpha = 1.0f;  // factor of O
       if constexpr (Geo::kPth) {
         const int e = sev[sd];
@@ -639,32 +619,28 @@ __global__ void __launch_bounds__(512, 1) rect_attention_kernel(const AttnParams
         }
       }
       // The row's scores, in pairs, and their maximum.
-      uint64_t z[kN / 2];
+      uint64_t z[32];
       {
-        uint32_t v[kN];
-#pragma unroll
-        for (int c = 0; c < kN; c += 32) tc::tmem_ld32(tmem_s + c, *reinterpret_cast<uint32_t(*)[32]>(v + c));
+        uint32_t v[64];
+        tc::tmem_ld32(tmem_s, *reinterpret_cast<uint32_t(*)[32]>(v));
+        tc::tmem_ld32(tmem_s + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
         tc::tmem_wait_ld();
-        if constexpr (Geo::kSplitP) {
-          tc::fence_before_sync();
-          warp_arrive(bar(Geo::kBarSFree));
-        }
 #pragma unroll
-        for (int e = 0; e < kN / 2; ++e) z[e] = dev::pack2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
+        for (int e = 0; e < 32; ++e) z[e] = dev::pack2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
       }
       if constexpr (Geo::kPth) {
-        const ulonglong2* const k2 = reinterpret_cast<const ulonglong2*>(sk + sd * kN);
+        const ulonglong2* const k2 = reinterpret_cast<const ulonglong2*>(sk + side);
 #pragma unroll
-        for (int e = 0; e < kN / 2; e += 2) {
+        for (int e = 0; e < 32; e += 2) {
           const ulonglong2 s2 = k2[e / 2];
           z[e] = dev::mul2(z[e], s2.x);
           z[e + 1] = dev::mul2(z[e + 1], s2.y);
         }
       }
-      if (!plain) {  // final scores, in log2 units
+      if constexpr (GEN) {  // final scores, in log2 units
         const int dist = kv0 - pos;  // key - position of column 0
 #pragma unroll
-        for (int e = 0; e < kN / 2; ++e) {
+        for (int e = 0; e < 32; ++e) {
           float2 r = dev::unpack2(z[e]);
           r.x *= score_mul;
           r.y *= score_mul;
@@ -678,7 +654,7 @@ __global__ void __launch_bounds__(512, 1) rect_attention_kernel(const AttnParams
       if (!full) {
         // masked keys by a bit each
 #pragma unroll
-        for (int q = 0; q < kN / 32; ++q) {
+        for (int q = 0; q < 2; ++q) {
           const int lo = min(max(lo_n - 32 * q, 0), 32), hi = min(max(hi_n - 32 * q, 0), 32);
           const uint32_t cm = cmask >> (2 * q);
           uint32_t seen = hi > lo ? (0xFFFFFFFFu << lo) & (0xFFFFFFFFu >> (32 - hi)) : 0u;
@@ -692,12 +668,12 @@ __global__ void __launch_bounds__(512, 1) rect_attention_kernel(const AttnParams
       }
       float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int e = 0; e < kN / 2; ++e) {
+      for (int e = 0; e < 32; ++e) {
         const float2 r = dev::unpack2(z[e]);
         mx4[e & 3] = dev::max3(mx4[e & 3], r.x, r.y);
       }
       const float mr = dev::max3(mx4[0], mx4[1], fmaxf(mx4[2], mx4[3]));
-      const float mx = plain ? mr * score_mul : mr;
+      const float mx = GEN ? mr : mr * score_mul;
       if (mx > m_ref + 8.0f) {
         const float nref = ceilf(mx);
         if (m_ref != -INFINITY) {
@@ -707,20 +683,12 @@ __global__ void __launch_bounds__(512, 1) rect_attention_kernel(const AttnParams
         }
         m_ref = nref;
       }
-      // P beside S: the group's last P V has read P.
-      if constexpr (Geo::kSplitP) {
-        if (k > 0 && !(ok = wait(Geo::kBarODone + t, k - 1))) break;
-        tc::fence_after_sync();
-      }
-      // A moved reference rescales O, once the group's products so far are
-      // complete (with P in S's place and two Os they are: issued before the S that
-      // this item waited for).
+      // A moved reference rescales O, once the group's last P V is complete: S(k + 1)
+      // was issued after it; the last item's has a barrier.
       if (k > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
-        if constexpr (kRT == 1) {
-          ok = wait(Geo::kBarODone, k - 1);
-          if (!ok) break;
-          tc::fence_after_sync();
-        }
+        ok = k + 1 < count ? wait(Geo::kBarSFull + 2 * t + ((k + 1) & 1), (k + 1) >> 1) : wait(Geo::kBarODone + t, 0);
+        if (!ok) break;
+        tc::fence_after_sync();
 #pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += 16) {
           uint32_t w[16];
@@ -731,47 +699,36 @@ __global__ void __launch_bounds__(512, 1) rect_attention_kernel(const AttnParams
           tc::tmem_st16(tmem_o + (uint32_t)c0, w);
         }
       }
-      // P = 2^(z - m + 6) in blocks of 32 keys, over columns that the row was read
-      // from; a half (64 keys) is handed over once its stores are complete, which is
-      // looked at a block later.
+      // P = 2^(z - m + 6), over the columns that the row was read from
       const float ref = m_ref == -INFINITY ? 0.0f : m_ref - 6.0f;
-      const uint64_t mul2v = dev::pack2(plain ? score_mul : 1.0f, plain ? score_mul : 1.0f);
+      const uint64_t mul2v = dev::pack2(GEN ? 1.0f : score_mul, GEN ? 1.0f : score_mul);
       const uint64_t ref2 = dev::pack2(-ref, -ref);
       uint64_t ls[2] = {0ull, 0ull};  // pairs of sums
-      const ulonglong2* const v2 = reinterpret_cast<const ulonglong2*>(sv + sd * kN);
+      const ulonglong2* const v2 = reinterpret_cast<const ulonglong2*>(sv + side);
 #pragma unroll
-      for (int q = 0; q < kN / 32; ++q) {
+      for (int q = 0; q < 2; ++q) {
         uint32_t pw[16], pl[Geo::kAuto ? 16 : 1];
 #pragma unroll
         for (int e = 0; e < 16; e += 2) {
           ulonglong2 s2;
           if constexpr (Geo::kPth) s2 = v2[8 * q + e / 2];
 #pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            const float2 x = dev::unpack2(dev::fma2(z[16 * q + e + b], mul2v, ref2));
+          for (int y = 0; y < 2; ++y) {
+            const float2 x = dev::unpack2(dev::fma2(z[16 * q + e + y], mul2v, ref2));
             uint64_t q2 = dev::pack2(dev::fast_exp2(x.x), dev::fast_exp2(x.y));
-            ls[b] = dev::add2(ls[b], q2);
-            if constexpr (Geo::kPth) q2 = dev::mul2(q2, b ? s2.y : s2.x);
+            ls[y] = dev::add2(ls[y], q2);
+            if constexpr (Geo::kPth) q2 = dev::mul2(q2, y ? s2.y : s2.x);
             const float2 w = dev::unpack2(q2);
             if constexpr (Geo::kAuto) {
-              pw[e + b] = dev::pack_bf16x2(w.x, w.y);
-              pl[e + b] = dev::pack_bf16x2(w.x - dev::bf16_lo(pw[e + b]), w.y - dev::bf16_hi(pw[e + b]));
+              pw[e + y] = dev::pack_bf16x2(w.x, w.y);
+              pl[e + y] = dev::pack_bf16x2(w.x - dev::bf16_lo(pw[e + y]), w.y - dev::bf16_hi(pw[e + y]));
             } else {
-              pw[e + b] = dev::pack_f16x2(w.x, w.y);
+              pw[e + y] = dev::pack_f16x2(w.x, w.y);
             }
           }
         }
-        if (q == 2) {
-          tc::tmem_wait_st();
-          tc::fence_before_sync();
-          warp_arrive(bar(Geo::kBarPFull + 2 * st));
-        }
-        if constexpr (Geo::kAuto) {
-          tc::tmem_st16(tmem_p + (uint32_t)(64 * (q / 2) + 16 * (q & 1)), pw);
-          tc::tmem_st16(tmem_p + (uint32_t)(64 * (q / 2) + 32 + 16 * (q & 1)), pl);
-        } else {
-          tc::tmem_st16(tmem_p + (uint32_t)(16 * q), pw);
-        }
+        tc::tmem_st16(tmem_s + (uint32_t)(16 * q), pw);
+        if constexpr (Geo::kAuto) tc::tmem_st16(tmem_s + (uint32_t)(32 + 16 * q), pl);
       }
       {
         const float2 a = dev::unpack2(dev::add2(ls[0], ls[1]));
@@ -779,18 +736,19 @@ __global__ void __launch_bounds__(512, 1) rect_attention_kernel(const AttnParams
       }
       tc::tmem_wait_st();
       tc::fence_before_sync();
-      warp_arrive(bar(Geo::kBarPFull + 2 * st + Geo::kHalves - 1));
+      warp_arrive(bar(Geo::kBarPFull + b));
     }
     // ---- epilogue: O / l as fp32 partial rows or bf16 rows -------------------
-    if (ok && count > 0) {
-      ok = __all_sync(0xffffffffu, wait_or_abort(bar(Geo::kBarOFinal + (kRT == 2 ? t : 0)), 0u, abort_flag));
+    if (ok) {
+      // (one row tile: the rows go out through the Q tile that both groups' MMAs read)
+      ok = wait(Geo::kBarOFinal + t, 0) && (kRT == 1 || two || t == 1 || wait(Geo::kBarOFinal + 1, 0));
       tc::fence_after_sync();
     }
     // (rows of this group's row tile in the partials: the second group of a
     // single row tile has its own)
     const int part = part0 + (two ? tile * kM : t * part_stride);
     const int tile_rows = min(kM, nrows - tile * kM);
-    if (ok && (part0 >= 0 || count > 0)) {
+    if (ok) {
       if (part0 < 0 && p.sinks && row_valid && m_ref != -INFINITY) {
         // the sink joins the normaliser here (partial rows: in the merge)
         const float skl = p.sinks[head_q] * log2e;
@@ -815,15 +773,13 @@ __global__ void __launch_bounds__(512, 1) rect_attention_kernel(const AttnParams
 #pragma unroll 1
         for (int c0 = 0; c0 < kCw; c0 += 32) {
           uint32_t w[32];
-          if (count > 0) {
-            tc::tmem_ld32(tmem_o + (uint32_t)(h * kCw + c0), w);
-            tc::tmem_wait_ld();
-          }
+          tc::tmem_ld32(tmem_o + (uint32_t)(h * kCw + c0), w);
+          tc::tmem_wait_ld();
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
             float f[4];
 #pragma unroll
-            for (int b = 0; b < 4; ++b) f[b] = count > 0 ? __uint_as_float(w[e + b]) * sc * sc2 : 0.0f;
+            for (int b = 0; b < 4; ++b) f[b] = __uint_as_float(w[e + b]) * sc * sc2;
             sts128(stage + (uint32_t)(lane * kCw * 4 + ((((c0 + e) >> 2) ^ (lane & 7)) << 4)),
                    make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])));
           }
@@ -876,7 +832,8 @@ __global__ void __launch_bounds__(512, 1) rect_attention_kernel(const AttnParams
 
 template <int DT, int D>
 int launch_rect_instance(const AttnParams& p, const RectParams& rp, cudaStream_t stream) {
-  auto kern = rect_attention_kernel<DT, D>;
+  auto kern = p.soft_cap > 0.0f || p.alibi_slopes ? rect_attention_kernel<DT, D, true>
+                                                  : rect_attention_kernel<DT, D, false>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)rect_smem_bytes(D)) != cudaSuccess)
     return KVQ_E_CUDA;
   cudaLaunchConfig_t cfg = {};
