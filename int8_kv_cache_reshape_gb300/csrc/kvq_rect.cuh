@@ -92,7 +92,7 @@ struct RectGeom {
 // Registers a thread of each warpgroup, out of the launch's 512 x 128.
 template <int D>
 struct RectRegs {
-  static constexpr int kIssue = 64, kConvert = 104, kSoftmax = D >= 256 ? 232 : 168;
+  static constexpr int kIssue = D >= 256 ? 96 : 104, kConvert = 104, kSoftmax = D >= 256 ? 208 : 152;
   static_assert(kIssue + (D >= 256 ? 2 : 1) * kConvert + rect_row_tiles(D) * kSoftmax <= 4 * 128,
                 "the groups' registers come out of the launch's");
 };
