@@ -236,7 +236,7 @@ KVQ_HD constexpr int rect_rows(int head_dim) { return 128 * rect_row_tiles(head_
 // KB for 1024-byte alignment.
 KVQ_HD constexpr size_t rect_smem_bytes(int head_dim) {
   return (size_t)rect_rows(head_dim) * head_dim * 2 + 4 * (size_t)prefill_keys(head_dim) * head_dim * 2 +
-         4 * (size_t)(prefill_keys(head_dim) * 8 + 8 + 64) + (size_t)rect_rows(head_dim) * 4 + 320 + 1024;
+         4 * (size_t)(prefill_keys(head_dim) * 8 + 8 + 64) + 128 * 4 + 320 + 1024;
 }
 // A prefix's shared part ends at a multiple of this many keys (both plans'
 // chunks); the rest is read with each request's own keys.

@@ -73,8 +73,8 @@ struct RectGeom {
   static constexpr int kOffSv = kOffSk + kSide * kN * 4;        // kSide x kN f32
   static constexpr int kOffSMask = kOffSv + kSide * kN * 4;     // kSide u32 masks, kSide i32 exponents
   static constexpr int kOffSlots = kOffSMask + kSide * 8;       // kSlotRing x 16 i32
-  static constexpr int kOffQScale = kOffSlots + kSlotRing * 64; // kRT x kM f32
-  static constexpr int kOffBar = kOffQScale + kRT * kM * 4;
+  static constexpr int kOffQScale = kOffSlots + kSlotRing * 64; // kM f32 (of one row tile)
+  static constexpr int kOffBar = kOffQScale + kM * 4;
   static constexpr int kBytes = kOffBar + 320;
   static constexpr int kItem = 64;                    // keys of an item
   static constexpr int kItems = kN / kItem;           // items of a KV tile
@@ -156,25 +156,18 @@ __global__ void __launch_bounds__(512, 1) rect_attention_kernel(const AttnParams
     token = __ldg(reinterpret_cast<const int2*>(rp.tokens) + tok0 + q);
   }
 
-  if (tid == 0) {
-    for (int s = 0; s < 4; ++s) {
-      tc::mbar_init(bar(Geo::kBarSlots + s), 1);
-      tc::mbar_init(bar(Geo::kBarSlotsFree + s), 2 * Geo::kConv / 32 + 1);
-      tc::mbar_init(bar(Geo::kBarSide + s), 1);
-      tc::mbar_init(bar(Geo::kBarSFull + s), 1);
-      tc::mbar_init(bar(Geo::kBarPFull + s), 4);
-    }
-    for (int s = 0; s < 2; ++s) {
-      tc::mbar_init(bar(Geo::kBarKFull + s), Geo::kConv / 32);
-      tc::mbar_init(bar(Geo::kBarVFull + s), Geo::kConv / 32);
-      tc::mbar_init(bar(Geo::kBarKEmpty + s), kRT);
-      tc::mbar_init(bar(Geo::kBarVEmpty + s), kRT);
-      tc::mbar_init(bar(Geo::kBarQFull + s), 4);
-      tc::mbar_init(bar(Geo::kBarODone + s), 1);
-      tc::mbar_init(bar(Geo::kBarDrain + s), 1);
-      tc::mbar_init(bar(Geo::kBarOFinal + s), 1);
-    }
-    *abort_flag = 0u;
+  // (a barrier a thread: code that runs once is fetched line by line, some 250
+  // cycles each)
+  if (tid < Geo::kNumBars) {
+    const int arrivals = tid >= Geo::kBarSlotsFree && tid < Geo::kBarSide  ? 2 * Geo::kConv / 32 + 1
+                         : tid >= Geo::kBarKFull && tid < Geo::kBarKEmpty  ? Geo::kConv / 32
+                         : tid >= Geo::kBarKEmpty && tid < Geo::kBarSFull  ? kRT
+                         : (tid >= Geo::kBarPFull && tid < Geo::kBarODone) ||
+                                   (tid >= Geo::kBarQFull && tid < Geo::kBarDrain)
+                             ? 4
+                             : 1;
+    tc::mbar_init(bar(tid), (uint32_t)arrivals);
+    if (tid == 0) *abort_flag = 0u;
     tc::mbar_fence_init();
   }
   if (warp == 0) {
@@ -527,56 +520,69 @@ __global__ void __launch_bounds__(512, 1) rect_attention_kernel(const AttnParams
     const float log2e = 1.4426950408889634f;
     const int head_q = kv_head * G + row_g, pos = token.y;
     const int64_t row_off = ((int64_t)token.x * p.heads_q + head_q) * D;
-    float* const qscale = reinterpret_cast<float*>(sm + Geo::kOffQScale) + tile * kM;
+    float* const qscale = reinterpret_cast<float*>(sm + Geo::kOffQScale);
+    float q_unscale = 1.0f;  // 2^-shift of the row's Q
     bool ok = true;
     if (two || t == 0) {
-      // Q of the warp's 32 rows: D / 8 lanes a row, 16 bytes each, eight loads in
-      // flight.  A row enters as f16 scaled by the power of two that puts its
-      // largest |q| in [2^13, 2^14): exact but for elements 2^27 below that one
-      // (subnormals).  The score scale's sign enters with Q, so that the softmax's
-      // factor is positive.
-      constexpr int kLpr = D / 8, kRpi = 32 / kLpr, kBatch = 8;
+      // Q of the warp's 32 rows: copied where they belong in the operand tile (D / 8
+      // lanes a row), then each thread scales its row in place.  A row enters as
+      // f16 scaled by the power of two that puts its largest |q| in [2^13, 2^14):
+      // exact but for elements 2^27 below that one (subnormals); bf16 rows stay as
+      // they are.  The score scale's sign enters with Q, so that the softmax's
+      // factor is positive.  (Short loops: unrolled loads and shuffles took 9,700
+      // cycles here, most of them instruction fetches.)
+      constexpr int kLpr = D / 8, kRpi = 32 / kLpr;
       const float qk_scale = Geo::kPth || Geo::kAuto ? p.sm_scale : p.sm_scale * p.k_scale;
       const uint32_t keep = qk_scale == 0.0f ? 0u : 0xFFFFFFFFu, flip = qk_scale < 0.0f ? 0x80008000u : 0u;
-      const int sub = lane / kLpr, pc = lane % kLpr;
-      const uint32_t qt = base + Geo::kOffQ + (uint32_t)(tile * Geo::kQBytes + (pc >> 3) * (kM * 128));
-      const int rows_in = min(32, nrows - tile * kM - (warp & 3) * 32);  // valid rows of the warp
-#pragma unroll 1
-      for (int r0 = 0; r0 < 32; r0 += kBatch * kRpi) {
-        uint4 x[kBatch];
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-          const int r = r0 + b * kRpi + sub;
-          const int64_t off = __shfl_sync(0xffffffffu, row_off, r);
-          x[b] = r < rows_in ? dev::ldg_stream_coherent(p.q + off + 8 * pc) : make_uint4(0, 0, 0, 0);
+      const uint32_t qt = base + Geo::kOffQ + (uint32_t)(tile * Geo::kQBytes);
+      const int pc = lane % kLpr, wrow = (warp & 3) * 32;
+#pragma unroll 2
+      for (int r0 = 0; r0 < 32; r0 += kRpi) {
+        const int r = r0 + lane / kLpr;
+        const int64_t off = __shfl_sync(0xffffffffu, row_off, r);
+        const bool live = tile * kM + wrow + r < nrows;
+        dev::cp_async_16(qt + (uint32_t)((pc >> 3) * (kM * 128) + (wrow + r) * 128 + (((pc & 7) ^ (r & 7)) << 4)),
+                         p.q + off + 8 * pc, live ? 16 : 0);
+      }
+      dev::cp_async_commit();
+      dev::cp_async_wait<0>();
+      __syncwarp();
+      const uint32_t mine = qt + (uint32_t)(m * 128);
+      auto piece = [&](int c) { return mine + (uint32_t)((c >> 3) * (kM * 128) + (((c & 7) ^ (m & 7)) << 4)); };
+      if (!Geo::kAuto || qk_scale <= 0.0f) {
+        float f = 1.0f;
+        if constexpr (!Geo::kAuto) {
+          uint32_t big = 0;
+#pragma unroll 4
+          for (int c = 0; c < D / 8; ++c) {
+            const uint4 x = lds128(piece(c));
+            big = dev::max_u16x2(big, dev::max_u16x2(dev::max_u16x2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu),
+                                                     dev::max_u16x2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu)));
+          }
+          const int emax = (int)(max(big & 0xFFFFu, big >> 16) >> 7);  // largest |q| < 2^(emax - 126)
+          const int sh = emax == 0 ? 0 : min(140 - emax, 126);
+          f = __int_as_float((127 + sh) << 23);
+          q_unscale = __int_as_float((127 - sh) << 23);
+          qscale[m] = q_unscale;
         }
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-          const int r = r0 + b * kRpi + sub, row = (warp & 3) * 32 + r;
-          uint32_t w[4] = {(x[b].x & keep) ^ flip, (x[b].y & keep) ^ flip, (x[b].z & keep) ^ flip, (x[b].w & keep) ^ flip};
-          float unscale = 1.0f;
+#pragma unroll 2
+        for (int c = 0; c < D / 8; ++c) {
+          uint4 x = lds128(piece(c));
+          uint32_t w[4] = {(x.x & keep) ^ flip, (x.y & keep) ^ flip, (x.z & keep) ^ flip, (x.w & keep) ^ flip};
           if constexpr (!Geo::kAuto) {
-            uint32_t big = dev::max_u16x2(dev::max_u16x2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu),
-                                          dev::max_u16x2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
-#pragma unroll
-            for (int o = 1; o < kLpr; o <<= 1) big = dev::max_u16x2(big, __shfl_xor_sync(0xffffffffu, big, o));
-            const int emax = (int)(max(big & 0xFFFFu, big >> 16) >> 7);  // largest |q| < 2^(emax - 126)
-            const int sh = emax == 0 ? 0 : min(140 - emax, 126);
-            const float f = __int_as_float((127 + sh) << 23);
-            unscale = __int_as_float((127 - sh) << 23);
 #pragma unroll
             for (int e = 0; e < 4; ++e) w[e] = dev::pack_f16x2(dev::bf16_lo(w[e]) * f, dev::bf16_hi(w[e]) * f);
           }
-          if (pc == 0) qscale[row] = unscale;
-          sts128(qt + (uint32_t)(row * 128 + (((pc & 7) ^ (row & 7)) << 4)), make_uint4(w[0], w[1], w[2], w[3]));
+          sts128(piece(c), make_uint4(w[0], w[1], w[2], w[3]));
         }
       }
       tc::fence_async_smem();
       warp_arrive(bar(Geo::kBarQFull + tile));
     }
-    // (the other group's rows where both take the one row tile)
-    ok = __all_sync(0xffffffffu, wait_bar(bar(Geo::kBarQFull + tile), 0u, abort_flag));
-    const float q_unscale = qscale[m];
+    if (!two && t == 1) {  // (the first group's rows)
+      ok = wait(Geo::kBarQFull, 0);
+      if constexpr (!Geo::kAuto) q_unscale = qscale[m];
+    }
 
     const float* const sk = reinterpret_cast<const float*>(sm + Geo::kOffSk);
     const float* const sv = reinterpret_cast<const float*>(sm + Geo::kOffSv);
@@ -767,6 +773,7 @@ __global__ void __launch_bounds__(512, 1) rect_attention_kernel(const AttnParams
       // D / 2 columns a pass, 16-byte pieces swizzled by the row, then out in
       // runs of a row.
       constexpr int kCw = D / 2, kPr = kCw / 4;  // columns of a pass, 16-byte pieces of a row
+      const int wr = (warp & 3) * 32;
       const uint32_t stage = base + Geo::kOffQ + (uint32_t)(t * Geo::kQBytes + (warp & 3) * 32 * kCw * 4);
 #pragma unroll 1
       for (int h = 0; h < 2; ++h) {
@@ -785,18 +792,28 @@ __global__ void __launch_bounds__(512, 1) rect_attention_kernel(const AttnParams
           }
         }
         __syncwarp();
+        if (part0 >= 0) {
+          // (the partial rows of a warp lie side by side)
+          float* const to = p.part_o + (int64_t)(part + wr) * D + h * kCw;
 #pragma unroll 4
-        for (int x = lane; x < 32 * kPr; x += 32) {
-          const int r = x / kPr, pc = x % kPr;
-          const uint4 u = lds128(stage + (uint32_t)(r * kCw * 4 + ((pc ^ (r & 7)) << 4)));
-          const int64_t off = __shfl_sync(0xffffffffu, row_off, r);
-          if ((warp & 3) * 32 + r < tile_rows) {
-            if (part0 >= 0)
-              *reinterpret_cast<uint4*>(p.part_o + (int64_t)(part + (warp & 3) * 32 + r) * D + h * kCw + 4 * pc) = u;
-            else
-              *reinterpret_cast<uint2*>(p.out + off + h * kCw + 4 * pc) =
-                  make_uint2(dev::pack_bf16x2(__uint_as_float(u.x), __uint_as_float(u.y)),
-                             dev::pack_bf16x2(__uint_as_float(u.z), __uint_as_float(u.w)));
+          for (int x = lane; x < 32 * kPr; x += 32) {
+            const int r = x / kPr, pc = x % kPr;
+            const uint4 u = lds128(stage + (uint32_t)(r * kCw * 4 + ((pc ^ (r & 7)) << 4)));
+            if (wr + r < tile_rows) *reinterpret_cast<uint4*>(to + r * D + 4 * pc) = u;
+          }
+        } else {
+#pragma unroll 2
+          for (int x = lane; x < 16 * kPr; x += 32) {
+            const int r = x / (kPr / 2), pc = 2 * (x % (kPr / 2));
+            const uint4 u = lds128(stage + (uint32_t)(r * kCw * 4 + ((pc ^ (r & 7)) << 4)));
+            const uint4 v = lds128(stage + (uint32_t)(r * kCw * 4 + (((pc + 1) ^ (r & 7)) << 4)));
+            const int64_t off = __shfl_sync(0xffffffffu, row_off, r);
+            if (wr + r < tile_rows)
+              *reinterpret_cast<uint4*>(p.out + off + h * kCw + 4 * pc) =
+                  make_uint4(dev::pack_bf16x2(__uint_as_float(u.x), __uint_as_float(u.y)),
+                             dev::pack_bf16x2(__uint_as_float(u.z), __uint_as_float(u.w)),
+                             dev::pack_bf16x2(__uint_as_float(v.x), __uint_as_float(v.y)),
+                             dev::pack_bf16x2(__uint_as_float(v.z), __uint_as_float(v.w)));
           }
         }
         __syncwarp();
