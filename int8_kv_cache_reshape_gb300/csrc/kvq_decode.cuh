@@ -899,6 +899,11 @@ splitkv_decode_kernel(const AttnParams p, const StepParams sp) {
     }
   }
   if (cur >= 0) finish_piece();
+  // Beside the call's rectangular attention: what waits for this grid waits for
+  // that one too.  (One CTA is enough, and the others leave their places to the
+  // rest of the grid.)
+  if constexpr (!DEV)
+    if (p.beside_rect && blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // Launch one instance (used by the per-head_dim translation units).
@@ -910,6 +915,26 @@ int launch_decode_instance(const AttnParams& p, cudaStream_t stream) {
       cudaSuccess)
     return KVQ_E_CUDA;
   StepParams none{};
+  if (p.beside_rect) {
+    // A programmatic dependent of the call's rectangular attention, which lets it
+    // start once the kernels ahead of both have ended: it takes the SMs that that grid
+    // leaves, and reads nothing of it.
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(p.num_warps / kDecodeWarps));
+    cfg.blockDim = dim3(kDecodeThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kern, p, none) != cudaSuccess) {
+      cudaGetLastError();
+      return KVQ_E_CUDA;
+    }
+    return KVQ_OK;
+  }
   kern<<<(unsigned)(p.num_warps / kDecodeWarps), kDecodeThreads, smem, stream>>>(p, none);
   return cudaGetLastError() == cudaSuccess ? KVQ_OK : KVQ_E_CUDA;
 }

@@ -35,12 +35,30 @@ int launch_merge(const AttnParams& p, int dtype, int head_dim, int64_t num_merge
   return KVQ_OK;
 }
 
-int launch_rect_merge(const AttnParams& p, const RectParams& rp, int head_dim, int64_t num_merges, void* stream) {
-  if (num_merges <= 0) return KVQ_OK;
+namespace {
+template <int D, int PARTS, int BATCH>
+int rect_merge(const AttnParams& p, const RectParams& rp, const RectMergePlan& m, void* stream) {
+  // (eight warps, fewer where an item's rows need fewer)
+  const unsigned rows = (unsigned)(m.most_rows < 8 / PARTS ? m.most_rows : 8 / PARTS);
+  return launch_dependent(merge_rect_kernel<D, PARTS, BATCH>, (unsigned)m.items, 32u * PARTS * rows, stream, p, rp);
+}
+template <int D>
+int rect_merge_d(const AttnParams& p, const RectParams& rp, const RectMergePlan& m, void* stream) {
+  // Warps a row: as many as have partials to read, while all rows' warps are on
+  // the device at once (32 an SM at the kernel's registers).
+  const int64_t room = (int64_t)m.sms * 32 / (m.rows > 0 ? m.rows : 1);
+  if (m.most_splits > 16 && room >= 4) return rect_merge<D, 4, 8>(p, rp, m, stream);
+  if (m.most_splits > 8 && room >= 2) return rect_merge<D, 2, 8>(p, rp, m, stream);
+  return rect_merge<D, 1, 8>(p, rp, m, stream);
+}
+}  // namespace
+
+int launch_rect_merge(const AttnParams& p, const RectParams& rp, int head_dim, const RectMergePlan& m, void* stream) {
+  if (m.items <= 0) return KVQ_OK;
   switch (head_dim) {
-    case 64: return launch_dependent(merge_rect_kernel<64>, (unsigned)num_merges, kMergeThreads, stream, p, rp);
-    case 128: return launch_dependent(merge_rect_kernel<128>, (unsigned)num_merges, kMergeThreads, stream, p, rp);
-    case 256: return launch_dependent(merge_rect_kernel<256>, (unsigned)num_merges, kMergeThreads, stream, p, rp);
+    case 64: return rect_merge_d<64>(p, rp, m, stream);
+    case 128: return rect_merge_d<128>(p, rp, m, stream);
+    case 256: return rect_merge_d<256>(p, rp, m, stream);
     default: return KVQ_E_UNSUPPORTED;
   }
 }

@@ -312,10 +312,10 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge,
   }
   // Host plans are launched as programmatic dependents of whatever ran before
   // on the stream: only the plan has been read so far.  Where that is the
-  // call's own prefill, nothing here depends on it, and all that it depends on
-  // was done when it started: the decode's CTAs take the SMs that its tail
-  // leaves idle, and wait for its end before their own (so that what follows
-  // the decode follows both).
+  // call's own prefill or rectangular attention, nothing here depends on it, and
+  // all that it depends on was done when it started: the decode's CTAs take the
+  // SMs that it leaves, and the first waits for its end before its own (so that what
+  // follows the decode follows both; its first group always has chunks).
   if (!DEV && !p.beside_prefill) asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // ---- copies ----------------------------------------------------------------
@@ -682,7 +682,7 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge,
     if ((int)rec.y != cur) {
       if (cur >= 0) finish_piece(cur);
       if (i == n) {
-        if (!DEV && p.beside_prefill) asm volatile("griddepcontrol.wait;" ::: "memory");
+        if (!DEV && p.beside_prefill && blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
         return;
       }
       cur = (int)rec.y;
@@ -954,7 +954,7 @@ int4_decode_kernel(const AttnParams p, const StepParams sp, const Int4Geom ge,
   }
   for (int s = 0; s < S; ++s)
     (void)tc::mbar_wait(meta + 32u * s + 16, s < kst ? kpar : kpar ^ 1u, 200000000LL);
-  if (!DEV && p.beside_prefill) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!DEV && p.beside_prefill && blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // The launches' shared memory limit, raised once per device.

@@ -59,6 +59,7 @@ struct kvq_sched {
   std::vector<RectUnit> units;
   std::vector<RectToken> tokens;
   int64_t num_rect_merges, num_shared_requests, shared_keys;
+  kvq::RectMergePlan rect_merge;
   bool cross;
   DecodeLaunch launch[2];
   int64_t num_tiles, max_splits, partial_rows;
@@ -320,21 +321,26 @@ struct RectTile {
   int64_t splits, parts, part;
 };
 
-// Time of a unit of `tiles` KV tiles, in microseconds: a fixed part (launch,
-// first keys, Q, the rows' way out) and one for each KV tile, by the row tiles
-// that share it.  Fitted to measured calls; it only decides how the keys are cut.
-constexpr double kRectStart = 5.0;
-double rect_tile_us(int head_dim, bool two) {
-  return head_dim >= 256 ? 1.3 : head_dim >= 128 ? (two ? 1.4 : 0.8) : (two ? 1.1 : 0.6);
+// Time of a unit, in microseconds: a fixed part (first instructions, plan, first
+// keys, Q, the rows' way out) and one for each KV tile, by the row tiles that share
+// it; of a decode of so many bytes on so many SMs; and what it takes when it does
+// not fit beside the units.  Measured; they only decide how the keys are cut.
+constexpr double kRectStart = 8.0, kDecodeStart = 8.0, kDecodeBytesPerUs = 30.0e3, kDecodeBehind = 15.0;
+double rect_tile_us(int dtype, int head_dim, bool two) {
+  const double us = head_dim >= 256 ? 1.5 : head_dim >= 128 ? (two ? 1.95 : 1.2) : (two ? 1.4 : 0.9);
+  return kvq::is_per_token_head(dtype) ? 1.25 * us : us;
 }
 
 // Cut the row tiles' keys among CTAs (one per SM) so that the last one ends
 // early: all units as near as can be to one length, tried for every number
-// of cuts of the longest tile.  Appends the units, longest first, and hands out
+// of cuts of the longest tile.  The decode beside them (beside_bytes of cache) takes
+// the SMs that the units leave: few long units then cost less than many short
+// ones.  Returns the SMs left for it where it is best cut to fit there, else 0.  Appends the units, longest first, and hands out
 // partial rows from *partial_rows on.  A tile left whole writes out directly if
 // it may (`direct`) and its rows have one O.
-void plan_rect(std::vector<RectTile>& tiles, int heads_kv, int head_dim, int sms, bool direct, int64_t forced,
-               std::vector<RectUnit>* units, int64_t* partial_rows) {
+int plan_rect(std::vector<RectTile>& tiles, int dtype, int heads_kv, int head_dim, int sms, bool direct,
+              int64_t beside_bytes, int64_t forced,
+              std::vector<RectUnit>* units, int64_t* partial_rows) {
   const int kN = kvq::prefill_keys(head_dim);
   auto kv_tiles = [&](const RectTile& t) {
     return t.kv_hi > t.kv_lo ? ceil_div(t.kv_hi, kN) - t.kv_lo / kN : 0;
@@ -343,11 +349,12 @@ void plan_rect(std::vector<RectTile>& tiles, int heads_kv, int head_dim, int sms
   auto pair = [&](const RectTile& t) { return kvq::rect_row_tiles(head_dim) == 2 && t.nrows <= 128; };
   int64_t most = 0;
   for (const RectTile& t : tiles) most = std::max(most, kv_tiles(t));
-  if (most == 0) return;
+  if (most == 0) return 0;
   int64_t best = most;
   double best_us = 0.0;
+  int best_left = 0;
   for (int64_t cuts = 1, last = 0; cuts <= most; cuts += std::max<int64_t>(1, cuts / 16)) {
-    const int64_t len = ceil_div(most, cuts);  // KV tiles of a unit
+    const int64_t len = forced > 0 ? forced : ceil_div(most, cuts);  // KV tiles of a unit
     if (len == last) continue;
     last = len;
     double total = 0.0, longest = 0.0;
@@ -356,7 +363,7 @@ void plan_rect(std::vector<RectTile>& tiles, int heads_kv, int head_dim, int sms
       const int64_t T = kv_tiles(t);
       if (T == 0) continue;
       const int64_t S = ceil_div(T, len);
-      const double per = rect_tile_us(head_dim, !pair(t) && head_dim < 256);
+      const double per = rect_tile_us(dtype, head_dim, !pair(t) && head_dim < 256);
       total += (double)heads_kv * ((double)S * kRectStart + (double)T * per);
       longest = std::max(longest, kRectStart + (double)ceil_div(T, S) * per);
       n += heads_kv * S;
@@ -364,14 +371,20 @@ void plan_rect(std::vector<RectTile>& tiles, int heads_kv, int head_dim, int sms
     }
     const int64_t waves = ceil_div(n, sms);
     // (partials: written and read once, in L2 mostly)
-    const double us = (waves <= 3 ? (double)waves * longest : total / sms + 0.5 * longest) +
-                      (double)rows * head_dim * 8.0 / 5.0e6;
+    // the decode on the SMs left, or among and behind the units
+    const int64_t left = beside_bytes > 0 ? std::max<int64_t>(0, sms - n) : 0;
+    const double all = (total + (double)beside_bytes / kDecodeBytesPerUs) / sms;
+    const double beside = std::max(longest, kDecodeStart + (double)beside_bytes / ((double)left * kDecodeBytesPerUs));
+    const double behind = (waves <= 3 ? std::max((double)waves * longest, all) : all + 0.5 * longest) +
+                          (beside_bytes > 0 ? kDecodeBehind : 0.0);
+    const bool fits = left > 0 && beside <= behind;
+    const double us = (fits ? beside : behind) + (double)rows * head_dim * 8.0 / 5.0e6;
     if (best_us == 0.0 || us < best_us) {
       best_us = us;
       best = len;
+      best_left = fits ? (int)left : 0;
     }
   }
-  if (forced > 0) best = forced;
   struct Range {
     int64_t tile, s, len;
   };
@@ -406,6 +419,7 @@ void plan_rect(std::vector<RectTile>& tiles, int heads_kv, int head_dim, int sms
       units->push_back(u);
     }
   }
+  return best_left;
 }
 
 }  // namespace
@@ -702,6 +716,16 @@ int plan_attention(int num_req, int heads_q, int heads_kv, int head_dim, const i
   std::vector<int32_t> pre_row;
   int64_t forced_tiles = 0;
   if (const char* env = std::getenv("KVQ_RECT_TILES")) forced_tiles = std::atoll(env);
+  // (cache bytes of the decode beside the units, and the SMs that are left for it)
+  int64_t beside_bytes = 0;
+  int decode_sms = 0;
+  for (int r = 0; (pre || cross) && r < num_req; ++r) {
+    const int64_t Q = (int64_t)query_start_loc_host[r + 1] - query_start_loc_host[r], L = seq_lens_host[r];
+    if (Q == 0 || Q * G > kvq::kTileMaxRows) continue;
+    int64_t lo = s->window > 0 ? std::max<int64_t>(0, L - Q - s->window + 1) : 0;
+    if (pre && pre->of[r] >= 0) lo = std::max<int64_t>(lo, pre->lens[pre->of[r]]);
+    beside_bytes += (L - lo) * heads_kv * 2 * kvq::row_bytes(dtype, head_dim);
+  }
   if (pre && pre->num > 0) {
     pre_tile.assign((size_t)num_req, -1);
     pre_row.assign((size_t)num_req, 0);
@@ -764,7 +788,8 @@ int plan_attention(int num_req, int heads_q, int heads_kv, int head_dim, const i
       for (int r = 0; r < num_req; ++r)
         if (pre_tile[(size_t)r] >= 0)
           s->shared_keys += pre->lens[pre->of[r]] / kvq::kPrefixGrain * kvq::kPrefixGrain;
-      plan_rect(rect, heads_kv, head_dim, sms, false, forced_tiles, &s->units, &s->partial_rows);
+      decode_sms = plan_rect(rect, dtype, heads_kv, head_dim, sms, false, beside_bytes, forced_tiles, &s->units,
+                             &s->partial_rows);
     }
   }
   auto shared = [&](int r) { return !pre_tile.empty() && pre_tile[(size_t)r] >= 0; };
@@ -789,7 +814,8 @@ int plan_attention(int num_req, int heads_q, int heads_kv, int head_dim, const i
       }
       s->max_chunk = std::max<int32_t>(s->max_chunk, (int32_t)((L - 1) / kvq::kChunkTokens));
     }
-    plan_rect(rect, heads_kv, head_dim, sms, true, forced_tiles, &s->units, &s->partial_rows);
+    decode_sms = plan_rect(rect, dtype, heads_kv, head_dim, sms, true, beside_bytes, forced_tiles, &s->units,
+                           &s->partial_rows);
   }
   // Rows that the rectangular merge writes: the shared requests' (one item each
   // (request, kv head)), the cut encoders' and those without keys.
@@ -966,6 +992,15 @@ int plan_attention(int num_req, int heads_q, int heads_kv, int head_dim, const i
   lockstep = (lockstep || int4) && heads_kv > 1;
   s->max_splits = 0;
   int64_t max_pieces = 0, max_merges = 0, num_warps = 0;
+  // Beside units, the decode is cut for the SMs that they leave (two classes: by
+  // their chunks).
+  int64_t chunks_of[2] = {0, 0};
+  for (int cls = 0; cls < 2; ++cls)
+    for (const Tile& t : tiles[cls]) chunks_of[cls] += t.c_hi - t.c_lo;
+  auto sms_for = [&](int cls) -> int64_t {
+    if (decode_sms == 0) return sms;
+    return std::max<int64_t>(1, (int64_t)decode_sms * chunks_of[cls] / (chunks_of[0] + chunks_of[1]));
+  };
   for (int cls = 0; cls < 2; ++cls) {
     DecodeLaunch& dl = s->launch[cls];
     int64_t T = 0;
@@ -987,7 +1022,7 @@ int plan_attention(int num_req, int heads_q, int heads_kv, int head_dim, const i
       // segments: as many as there are resident groups for, none shorter
       // than kInt4MinChunks; every segment has a warp per kv head
       const kvq::Int4Geom ge = kvq::int4_geom(heads_kv, head_dim, cls + 1);
-      const int64_t groups = (int64_t)sms * ge.gpc;
+      const int64_t groups = sms_for(cls) * ge.gpc;
       const int64_t chunks = T / heads_kv;
       int64_t segs = std::min<int64_t>(std::max<int64_t>(1, groups / ge.hsplit),
                                        ceil_div(chunks, kvq::kInt4MinChunks));
@@ -998,7 +1033,7 @@ int plan_attention(int num_req, int heads_q, int heads_kv, int head_dim, const i
       num_warps += dl.num_warps;
       continue;
     }
-    const int64_t max_ctas = (int64_t)sms * kvq::decode_min_ctas(dtype, head_dim, cls + 1);
+    const int64_t max_ctas = sms_for(cls) * kvq::decode_min_ctas(dtype, head_dim, cls + 1);
     int64_t ctas = std::min<int64_t>(max_ctas, std::max<int64_t>(1, ceil_div(T, kvq::kDecodeWarps * kvq::kMinChunksPerWarp)));
     if (forced > 0) ctas = std::max<int64_t>(1, std::min<int64_t>(ceil_div(forced, kvq::kDecodeWarps), ceil_div(T, kvq::kDecodeWarps)));
     int64_t W = ctas * kvq::kDecodeWarps;
@@ -1175,6 +1210,12 @@ int plan_attention(int num_req, int heads_q, int heads_kv, int head_dim, const i
   s->num_pieces = npieces;
   s->num_merges = nmerges;
   s->num_rect_merges = nrmerges;
+  s->rect_merge = kvq::RectMergePlan{nrmerges, 0, 1, 0, sms};
+  for (int64_t i = 0; i < nrmerges; ++i) {
+    s->rect_merge.rows += RM[i].m.nrows;
+    s->rect_merge.most_rows = std::max(s->rect_merge.most_rows, (int)RM[i].m.nrows);
+    s->rect_merge.most_splits = std::max(s->rect_merge.most_splits, (int)(RM[i].m.nsplits + RM[i].pre_splits));
+  }
   // (partial rows are numbered in 32 bits)
   if (partial_rows > 0x7FFFFFFF) return KVQ_E_UNSUPPORTED;
   s->partial_rows = partial_rows;
@@ -1496,6 +1537,7 @@ int kvq_attention_with_kv_cache(const kvq_sched_t* s, int heads_q, int heads_kv,
     const int rc = kvq::launch_rect(p, rp, s->dtype, head_dim, stream);
     if (rc != KVQ_OK) return rc;
     p.beside_prefill = true;
+    p.beside_rect = true;
   }
   for (int cls = 0; cls < 2; ++cls) {
     const DecodeLaunch& dl = s->launch[cls];
@@ -1515,7 +1557,7 @@ int kvq_attention_with_kv_cache(const kvq_sched_t* s, int heads_q, int heads_kv,
   }
   const int rc = kvq::launch_merge(p, dtype, head_dim, s->num_merges, stream);
   if (rc != KVQ_OK) return rc;
-  return kvq::launch_rect_merge(p, rp, head_dim, s->num_rect_merges, stream);
+  return kvq::launch_rect_merge(p, rp, head_dim, s->rect_merge, stream);
 }
 
 // ---- the fused decode step ------------------------------------------------

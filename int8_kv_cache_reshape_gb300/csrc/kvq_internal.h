@@ -319,6 +319,12 @@ struct RectMerge {
   int32_t q0;  // the request's first query token
 };
 static_assert(sizeof(RectMerge) == 48, "RectMerge layout");
+// What the merge's launch is chosen by.
+struct RectMergePlan {
+  int64_t items, rows;         // merge items, rows of all of them
+  int most_rows, most_splits;  // of an item; partials of a row
+  int sms;
+};
 struct RectParams {
   const RectUnit* units;
   const RectToken* tokens;
@@ -368,6 +374,8 @@ struct AttnParams {
   const float* alibi_slopes;   // [Hq] or null: score += slope * (key - query position)
   const float* sinks;          // [Hq] or null: one extra logit in the softmax normaliser
   bool beside_prefill;         // 4-bit decode: the kernel ahead of it is this call's prefill
+  bool beside_rect;            // decode: the kernel ahead of it is this call's rectangular
+                               // attention, or another decode beside that one
 };
 
 // ---- fused decode step (cache write + device-built plan + decode) --------
@@ -502,7 +510,7 @@ int launch_prefill(const AttnParams& p, const PrefillMaps& maps, int dtype, int 
                    int64_t ctas, void* stream);
 // The units of a plan (kvq_rect.cuh), and the merge of their rows.
 int launch_rect(const AttnParams& p, const RectParams& rp, int dtype, int head_dim, void* stream);
-int launch_rect_merge(const AttnParams& p, const RectParams& rp, int head_dim, int64_t num_merges, void* stream);
+int launch_rect_merge(const AttnParams& p, const RectParams& rp, int head_dim, const RectMergePlan& m, void* stream);
 #ifdef __CUDACC__
 // Launch a kernel without dynamic shared memory as a programmatic dependent
 // of the kernel before it on the stream: it may be resident before that one

@@ -165,13 +165,114 @@ __global__ void __launch_bounds__(kMergeThreads) merge_splits_kernel(const AttnP
 
 // Rows with partials of rectangular units (kvq_rect.cuh) beside those of the
 // decode's pieces, or alone: a shared prefix's, an encoder's.
-template <int D>
-__global__ void __launch_bounds__(kMergeThreads) merge_rect_kernel(const AttnParams p, const RectParams rp) {
+// PARTS warps a row, a lane D / 32 dims of it: each warp takes every PARTS-th
+// partial, BATCH loads in flight beside the log-sum-exps (a lane each), and the
+// warps' sums are added in shared memory.  Few rows of many partials (a prefix cut
+// among all SMs): 2 or 4 warps, so that a row is one or two round trips to L2; many
+// rows of few partials: one.  The CTAs wait for the grid ahead in any case: they run
+// through the code once before, with every access switched off, so that its
+// instructions are there (some 250 cycles for each 128 bytes of code otherwise, more
+// than the work).
+template <int D, int PARTS, int BATCH>
+__global__ void __launch_bounds__(256) merge_rect_kernel(const AttnParams p, const RectParams rp) {
+  constexpr int kDims = D / 32, kRows = 8 / PARTS;
+  __shared__ float sums[PARTS > 1 ? kRows : 1][PARTS][PARTS > 1 ? D : 1];
   const RectMerge r = rp.merges[blockIdx.x];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  merge_tile<D, true>(p, r.m, r.q0, r.m.nsplits + r.pre_splits, [&](int s) {
-    return s < r.m.nsplits ? r.m.part + s * r.m.nrows : r.pre_part + (s - r.m.nsplits) * r.pre_stride;
-  });
+  const int lane = threadIdx.x & 31, slot = (threadIdx.x >> 5) / PARTS, part = (threadIdx.x >> 5) % PARTS;
+  const int at_once = blockDim.x / (32 * PARTS);
+  const int ns = r.m.nsplits + r.pre_splits, G = p.group;
+  for (int n0 = -at_once; n0 < r.m.nrows; n0 += at_once) {
+    if (n0 == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int n = n0 + slot;
+    const bool live = n0 >= 0 && n < r.m.nrows;
+    auto row_of = [&](int s) -> int64_t {
+      return (s < r.m.nsplits ? r.m.part + s * r.m.nrows : r.pre_part + (s - r.m.nsplits) * r.pre_stride) + n;
+    };
+    const int R = r.m.row0 + (live ? n : 0), head = r.m.kv_head * G + R % G;
+    // the largest log-sum-exp; a sink is one more
+    const float sink = p.sinks ? fmaf(p.sinks[head], 1.4426950408889634f, 6.0f) : -INFINITY;
+    float lse = live && lane < ns ? __ldcg(p.part_lse + row_of(lane)) : -INFINITY, M = lse;
+    for (int s = lane + 32; live && s < ns; s += 32) M = fmaxf(M, __ldcg(p.part_lse + row_of(s)));
+    float o[kDims], sum = 0.0f;
+#pragma unroll
+    for (int d = 0; d < kDims; ++d) o[d] = 0.0f;
+    int s0 = 0;
+    do {  // this warp's splits s0 + part, + 4, ..
+      if (s0 > 0) lse = live && s0 + lane < ns ? __ldcg(p.part_lse + row_of(s0 + lane)) : -INFINITY;
+      const bool mine = lane < BATCH * PARTS;  // (the batch's splits)
+      float v[BATCH][kDims];
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
+        const int s = s0 + part + PARTS * i;
+        const float* const from = p.part_o + row_of(s) * D + lane * kDims;
+#pragma unroll
+        for (int d = 0; d < kDims; ++d) v[i][d] = 0.0f;
+        if (live && s < ns) {
+          if constexpr (kDims == 2) {
+            const float2 x = __ldcg(reinterpret_cast<const float2*>(from));
+            v[i][0] = x.x, v[i][1] = x.y;
+          } else {
+#pragma unroll
+            for (int d = 0; d < kDims; d += 4) {
+              const float4 x = __ldcg(reinterpret_cast<const float4*>(from + d));
+              v[i][d] = x.x, v[i][d + 1] = x.y, v[i][d + 2] = x.z, v[i][d + 3] = x.w;
+            }
+          }
+        }
+      }
+      if (s0 == 0) {
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+        M = fmaxf(M, sink);
+      }
+      const float w = !mine || lse == -INFINITY ? 0.0f : exp2f(lse - M);
+      sum += w;
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
+        const float wi = __shfl_sync(0xffffffffu, w, part + PARTS * i);
+#pragma unroll
+        for (int d = 0; d < kDims; ++d) o[d] = fmaf(wi, v[i][d], o[d]);
+      }
+      s0 += BATCH * PARTS;
+    } while (s0 < ns);
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+    if (sink != -INFINITY) sum += exp2f(sink - M);
+    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;  // (a row that sees no key: zeros)
+    bool in_range = true;
+    if constexpr (KVQ_CHECKED) {
+      in_range = p.total_q_tokens <= 0 || (r.q0 >= 0 && r.q0 + R / G < p.total_q_tokens);
+      if (live && !in_range && lane == 0) atomicExch(p.error_flag, 2);
+    }
+    uint16_t* const dst = p.out + ((int64_t)(r.q0 + R / G) * p.heads_q + head) * D;
+    if constexpr (PARTS == 1) {
+      uint32_t w[kDims / 2];
+#pragma unroll
+      for (int d = 0; d < kDims / 2; ++d) w[d] = dev::pack_bf16x2(o[2 * d] * inv, o[2 * d + 1] * inv);
+      if (live && in_range) {
+        uint16_t* const to = dst + lane * kDims;
+        if constexpr (kDims == 2) *reinterpret_cast<uint32_t*>(to) = w[0];
+        else if constexpr (kDims == 4) *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
+        else *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    } else {
+      // dims of a lane: kDims side by side, kept 32 apart in shared memory
+#pragma unroll
+      for (int d = 0; d < kDims; ++d) sums[slot][part][lane + 32 * d] = o[d] * inv;
+      __syncthreads();
+      for (int e = 32 * part + lane; e < D / 2; e += 32 * PARTS) {
+        const int d0 = 2 * e, l = d0 / kDims, d = d0 % kDims;
+        float a = 0.0f, b = 0.0f;
+#pragma unroll
+        for (int q = 0; q < PARTS; ++q) {
+          a += sums[slot][q][l + 32 * d];
+          b += sums[slot][q][l + 32 * (d + 1)];
+        }
+        if (live && in_range) *reinterpret_cast<uint32_t*>(dst + d0) = dev::pack_bf16x2(a, b);
+      }
+      __syncthreads();
+    }
+  }
 }
 
 // The fused decode step: tile blockIdx.x (request t / Hkv, kv head t % Hkv)
