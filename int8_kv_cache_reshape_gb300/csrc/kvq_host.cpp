@@ -325,7 +325,7 @@ struct RectTile {
 // keys, Q, the rows' way out) and one for each KV tile, by the row tiles that share
 // it; of a decode of so many bytes on so many SMs; and what it takes when it does
 // not fit beside the units.  Measured; they only decide how the keys are cut.
-constexpr double kRectStart = 8.0, kDecodeStart = 8.0, kDecodeBytesPerUs = 30.0e3, kDecodeBehind = 15.0;
+constexpr double kRectStart = 8.0, kDecodeStart = 8.0, kDecodeBytesPerUs = 30.0e3, kDecodeBehind = 15.0, kMergeStart = 5.0;
 double rect_tile_us(int dtype, int head_dim, bool two) {
   const double us = head_dim >= 256 ? 1.5 : head_dim >= 128 ? (two ? 1.95 : 1.2) : (two ? 1.4 : 0.9);
   return kvq::is_per_token_head(dtype) ? 1.25 * us : us;
@@ -357,7 +357,7 @@ int plan_rect(std::vector<RectTile>& tiles, int dtype, int heads_kv, int head_di
     const int64_t len = forced > 0 ? forced : ceil_div(most, cuts);  // KV tiles of a unit
     if (len == last) continue;
     last = len;
-    double total = 0.0, longest = 0.0;
+    double total = 0.0, longest = 0.0, shortest = 1.0e30;
     int64_t n = 0, rows = 0;
     for (const RectTile& t : tiles) {
       const int64_t T = kv_tiles(t);
@@ -366,6 +366,7 @@ int plan_rect(std::vector<RectTile>& tiles, int dtype, int heads_kv, int head_di
       const double per = rect_tile_us(dtype, head_dim, !pair(t) && head_dim < 256);
       total += (double)heads_kv * ((double)S * kRectStart + (double)T * per);
       longest = std::max(longest, kRectStart + (double)ceil_div(T, S) * per);
+      shortest = std::min(shortest, kRectStart + (double)(T / S) * per);
       n += heads_kv * S;
       if (!direct || S > 1 || pair(t)) rows += heads_kv * S * t.nrows * (pair(t) ? 2 : 1);
     }
@@ -375,10 +376,13 @@ int plan_rect(std::vector<RectTile>& tiles, int dtype, int heads_kv, int head_di
     const int64_t left = beside_bytes > 0 ? std::max<int64_t>(0, sms - n) : 0;
     const double all = (total + (double)beside_bytes / kDecodeBytesPerUs) / sms;
     const double beside = std::max(longest, kDecodeStart + (double)beside_bytes / ((double)left * kDecodeBytesPerUs));
-    const double behind = (waves <= 3 ? std::max((double)waves * longest, all) : all + 0.5 * longest) +
-                          (beside_bytes > 0 ? kDecodeBehind : 0.0);
+    // (units of one length run in waves; of several, longest first, they fill up)
+    const double units_us = shortest > 0.9 * longest ? (double)waves * longest
+                            : n <= sms               ? longest
+                                                     : std::max(longest, total / sms + 0.5 * total / (double)n);
+    const double behind = std::max(units_us, all) + (beside_bytes > 0 ? kDecodeBehind : 0.0);
     const bool fits = left > 0 && beside <= behind;
-    const double us = (fits ? beside : behind) + (double)rows * head_dim * 8.0 / 5.0e6;
+    const double us = (fits ? beside : behind) + (rows > 0 ? kMergeStart : 0.0) + (double)rows * head_dim * 8.0 / 5.0e6;
     if (best_us == 0.0 || us < best_us) {
       best_us = us;
       best = len;
@@ -1034,7 +1038,9 @@ int plan_attention(int num_req, int heads_q, int heads_kv, int head_dim, const i
       continue;
     }
     const int64_t max_ctas = sms_for(cls) * kvq::decode_min_ctas(dtype, head_dim, cls + 1);
-    int64_t ctas = std::min<int64_t>(max_ctas, std::max<int64_t>(1, ceil_div(T, kvq::kDecodeWarps * kvq::kMinChunksPerWarp)));
+    // (beside units: SMs stand by, and shared tiles are merged in any case)
+    const int64_t least = decode_sms > 0 ? kvq::kMinChunksBeside : kvq::kMinChunksPerWarp;
+    int64_t ctas = std::min<int64_t>(max_ctas, std::max<int64_t>(1, ceil_div(T, kvq::kDecodeWarps * least)));
     if (forced > 0) ctas = std::max<int64_t>(1, std::min<int64_t>(ceil_div(forced, kvq::kDecodeWarps), ceil_div(T, kvq::kDecodeWarps)));
     int64_t W = ctas * kvq::kDecodeWarps;
     if (ls && W >= heads_kv) {

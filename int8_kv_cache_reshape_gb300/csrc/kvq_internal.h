@@ -85,6 +85,7 @@ constexpr int kDecodeThreads = 32 * kDecodeWarps;
 constexpr int kTileMaxRows = 16;
 constexpr int kRecordRing = 32;       // per-warp ring of chunk records (16 B each)
 constexpr int kMinChunksPerWarp = 8;  // smallest segment worth a warp
+constexpr int kMinChunksBeside = 3;   // the same beside rectangular units
 
 // Bytes of one 16-token chunk of K and V codes (plus the per-token-head
 // scale tails) -- what a warp loads per step, straight into registers.
