@@ -1068,7 +1068,7 @@ int plan_attention(int num_req, int heads_q, int heads_kv, int head_dim, const i
   s->d_units_off = s->d_prefill_off + kvq::align256(s->prefill.size() * sizeof(PrefillTile));
   s->d_tokens_off = s->d_units_off + kvq::align256(s->units.size() * sizeof(RectUnit));
   s->d_rmerges_off = s->d_tokens_off + kvq::align256(s->tokens.size() * sizeof(RectToken));
-  const size_t max_rmerges = rect_merges.size() + (size_t)s->num_shared_requests * (size_t)heads_kv;
+  const size_t max_rmerges = rect_merges.size() + (pre || cross ? tiles[0].size() + tiles[1].size() : 0);
   s->d_error_off = s->d_rmerges_off + kvq::align256(max_rmerges * sizeof(RectMerge));
   const size_t total = s->d_error_off + sizeof(int32_t);
   s->image_bytes = total;
@@ -1157,9 +1157,9 @@ int plan_attention(int num_req, int heads_q, int heads_kv, int head_dim, const i
       // the ones handed out so far
       int32_t merge = -1;
       int64_t part = -1;
-      if (shared(t.req)) {
-        // its pieces' rows, cut or not, are merged with the prefix's
-        const RectTile& rt = rect[(size_t)pre_tile[(size_t)t.req]];
+      if (shared(t.req) || (np > 1 && (pre || cross))) {
+        // a shared request's pieces' rows, cut or not, are merged with the prefix's;
+        // the other cut tiles of such a plan by the same launch
         RectMerge& m = RM[nrmerges++];
         m = RectMerge{};
         m.m.req = t.req;
@@ -1168,9 +1168,12 @@ int plan_attention(int num_req, int heads_q, int heads_kv, int head_dim, const i
         m.m.nrows = t.nrows;
         m.m.part = (int32_t)partial_rows;
         m.m.nsplits = (int32_t)np;
-        m.pre_part = (int32_t)(rt.part + t.kv_head * rt.parts * rt.nrows + pre_row[(size_t)t.req] + t.row0);
-        m.pre_splits = (int32_t)rt.parts;
-        m.pre_stride = rt.nrows;
+        if (shared(t.req)) {
+          const RectTile& rt = rect[(size_t)pre_tile[(size_t)t.req]];
+          m.pre_part = (int32_t)(rt.part + t.kv_head * rt.parts * rt.nrows + pre_row[(size_t)t.req] + t.row0);
+          m.pre_splits = (int32_t)rt.parts;
+          m.pre_stride = rt.nrows;
+        }
         m.q0 = query_start_loc_host[t.req];
         part = partial_rows;
         partial_rows += np * t.nrows;

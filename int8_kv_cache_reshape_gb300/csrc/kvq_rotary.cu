@@ -16,7 +16,8 @@
 // elements of an 8-dim thread, and a row's codes leave as 16-byte stores.  The
 // other half of a pair comes from a lane of the row by shuffles of packed
 // bf16.  A unit of threads takes kQHeads query heads of a token, whose cos and
-// sin stay in registers, or one kv head's K and V rows; K/V units come first.
+// sin stay in registers, or one kv head's K and V rows; the two kinds are mixed, since one
+// is bound by memory and the other by its instructions.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -31,32 +32,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kQHeads = 4;  // query heads of a unit
 
-// cos and sin of a thread's 16 dims: of dim e (halves) or pair e / 2 (interleaved).
-template <bool IL>
-struct Angles {
-  static constexpr int kN = IL ? 4 : 8;  // values of an 8-dim piece
-  float c[2][kN], s[2][kN];
-  int kind[2];  // of the piece: 0 first of its pairs, 1 second, 2 not rotated
-  // piece q = 2 part + h of 8 dims; R8 = rotated dims / 16 (pieces of a half)
-  __device__ __forceinline__ void load(const float* row, int part, int R8) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int q = 2 * part + h;
-      kind[h] = q < R8 ? 0 : q < 2 * R8 ? 1 : 2;
-      const int j = IL ? 4 * q : 8 * (q < R8 ? q : q - R8);
-      const float4* c4 = reinterpret_cast<const float4*>(row + j);
-      const float4* s4 = reinterpret_cast<const float4*>(row + 8 * R8 + j);
-#pragma unroll
-      for (int i = 0; i < kN / 4; ++i) {
-        const float4 a = kind[h] < 2 ? c4[i] : make_float4(1.0f, 1.0f, 1.0f, 1.0f);
-        const float4 b = kind[h] < 2 ? s4[i] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        c[h][4 * i] = a.x, c[h][4 * i + 1] = a.y, c[h][4 * i + 2] = a.z, c[h][4 * i + 3] = a.w;
-        s[h][4 * i] = b.x, s[h][4 * i + 1] = b.y, s[h][4 * i + 2] = b.z, s[h][4 * i + 3] = b.w;
-      }
-    }
-  }
-};
-
 __device__ __forceinline__ void unpack8(const uint4 x, float* f) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
@@ -66,41 +41,70 @@ __device__ __forceinline__ void unpack8(const uint4 x, float* f) {
   }
 }
 
+// cos and sin of a thread's 16 dims, two dims a register pair.  With the other
+// half of a pair beside each dim, a rotated dim is x c + y t: t is -s for the
+// first of a pair and s for the second, so the sum rounds as the difference
+// does, and a product serves two dims.
+template <bool IL>
+struct Angles {
+  uint64_t c[2][4], t[2][4];
+  bool turned[2];  // the 8-dim piece is rotated
+  // piece q = 2 part + h; R8 = rotated dims / 16 (pieces of a half)
+  __device__ __forceinline__ void load(const float* row, int part, int R8) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int q = 2 * part + h;
+      turned[h] = q < 2 * R8;
+      if constexpr (IL) {
+        const int j = turned[h] ? 4 * q : 0;
+        const float4 a = *reinterpret_cast<const float4*>(row + j);
+        const float4 b = *reinterpret_cast<const float4*>(row + 8 * R8 + j);
+        c[h][0] = dev::pack2(a.x, a.x), c[h][1] = dev::pack2(a.y, a.y);
+        c[h][2] = dev::pack2(a.z, a.z), c[h][3] = dev::pack2(a.w, a.w);
+        t[h][0] = dev::pack2(-b.x, b.x), t[h][1] = dev::pack2(-b.y, b.y);
+        t[h][2] = dev::pack2(-b.z, b.z), t[h][3] = dev::pack2(-b.w, b.w);
+      } else {
+        const int j = turned[h] ? 8 * (q < R8 ? q : q - R8) : 0;
+        const ulonglong2* const c2 = reinterpret_cast<const ulonglong2*>(row + j);
+        const ulonglong2* const s2 = reinterpret_cast<const ulonglong2*>(row + 8 * R8 + j);
+        const uint64_t flip = q < R8 ? 0x8000000080000000ull : 0ull;
+        const ulonglong2 a = c2[0], b = c2[1], d = s2[0], e = s2[1];
+        c[h][0] = a.x, c[h][1] = a.y, c[h][2] = b.x, c[h][3] = b.y;
+        t[h][0] = d.x ^ flip, t[h][1] = d.y ^ flip, t[h][2] = e.x ^ flip, t[h][3] = e.y ^ flip;
+      }
+    }
+  }
+};
+
 // The thread's 16 dims x[0], x[1] (8 each), rotated.  Every lane of the warp
 // calls it (shuffles).  Halves: piece q's other half is piece q -+ R8, the
 // words of lane (q -+ R8) / 2's piece of parity (q -+ R8) % 2, the same for all lanes.
 template <int TPR, bool IL>
 __device__ __forceinline__ void rotate16(const uint4 (&x)[2], const Angles<IL>& a, int part, int R8, float* f) {
-  unpack8(x[0], f);
-  unpack8(x[1], f + 8);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    float* const g = f + 8 * h;
+    const uint32_t w[4] = {x[h].x, x[h].y, x[h].z, x[h].w};
+    uint32_t o[4];
     if constexpr (IL) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float u = g[2 * i], v = g[2 * i + 1], c = a.c[h][i], s = a.s[h][i];
-        if (a.kind[h] < 2) {
-          g[2 * i] = __fsub_rn(__fmul_rn(u, c), __fmul_rn(v, s));
-          g[2 * i + 1] = __fadd_rn(__fmul_rn(v, c), __fmul_rn(u, s));
-        }
-      }
+      for (int i = 0; i < 4; ++i) o[i] = dev::prmt(w[i], 0u, 0x1032u);  // the other of the pair
     } else {
       const int q = 2 * part + h;
-      const int from = (a.kind[h] == 0 ? q + R8 : a.kind[h] == 1 ? q - R8 : q) >> 1;
+      const int from = (q < R8 ? q + R8 : q < 2 * R8 ? q - R8 : q) >> 1;
       const uint4 mine = (R8 & 1) ? x[h ^ 1] : x[h];
-      uint4 o;
-      o.x = __shfl_sync(0xffffffffu, mine.x, from, TPR);
-      o.y = __shfl_sync(0xffffffffu, mine.y, from, TPR);
-      o.z = __shfl_sync(0xffffffffu, mine.z, from, TPR);
-      o.w = __shfl_sync(0xffffffffu, mine.w, from, TPR);
-      float y[8];
-      unpack8(o, y);
+      o[0] = __shfl_sync(0xffffffffu, mine.x, from, TPR);
+      o[1] = __shfl_sync(0xffffffffu, mine.y, from, TPR);
+      o[2] = __shfl_sync(0xffffffffu, mine.z, from, TPR);
+      o[3] = __shfl_sync(0xffffffffu, mine.w, from, TPR);
+    }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float p = __fmul_rn(g[i], a.c[h][i]), r = __fmul_rn(y[i], a.s[h][i]);
-        if (a.kind[h] < 2) g[i] = a.kind[h] == 0 ? __fsub_rn(p, r) : __fadd_rn(p, r);
-      }
+    for (int i = 0; i < 4; ++i) {
+      const uint64_t v = dev::pack2(dev::bf16_lo(w[i]), dev::bf16_hi(w[i]));
+      const uint64_t y = dev::pack2(dev::bf16_lo(o[i]), dev::bf16_hi(o[i]));
+      // (scalar sums: a packed sum of packed products comes back fused)
+      const float2 p = dev::unpack2(dev::mul2(v, a.c[h][i])), r = dev::unpack2(dev::mul2(y, a.t[h][i]));
+      f[8 * h + 2 * i] = a.turned[h] ? __fadd_rn(p.x, r.x) : dev::bf16_lo(w[i]);
+      f[8 * h + 2 * i + 1] = a.turned[h] ? __fadd_rn(p.y, r.y) : dev::bf16_hi(w[i]);
     }
   }
 }
@@ -125,10 +129,23 @@ __device__ __forceinline__ uint2 codes8(const float* f, float s) {
   const float inv = dev::rcp_approx(s);
   const float lo = inv * (1.0f - 0x1p-22f), hi = inv * (1.0f + 0x1p-22f);
   uint32_t c[4], differ = 0;
+  if constexpr (F == KVQ_INT8_PER_TOKEN_HEAD) {
+    // x lo + 1.5 2^23 holds rint(x lo) in its lowest byte (|x| <= 127 s up to rounding:
+    // nothing to clamp)
+    uint32_t b[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    c[i] = code2<F>(f[2 * i] * lo, f[2 * i + 1] * lo);
-    differ |= c[i] ^ code2<F>(f[2 * i] * hi, f[2 * i + 1] * hi);
+    for (int i = 0; i < 8; ++i) {
+      b[i] = __float_as_uint(fmaf(f[i], lo, 12582912.0f));
+      differ |= b[i] ^ __float_as_uint(fmaf(f[i], hi, 12582912.0f));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = dev::prmt(b[2 * i], b[2 * i + 1], 0x0040u) & 0xFFFFu;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      c[i] = code2<F>(f[2 * i] * lo, f[2 * i + 1] * lo);
+      differ |= c[i] ^ code2<F>(f[2 * i] * hi, f[2 * i + 1] * hi);
+    }
   }
   if (differ != 0 || !(s > 0x1p-120f && s < 0x1p120f))
     return codes8_exact<F>(make_float4(f[0], f[1], f[2], f[3]), make_float4(f[4], f[5], f[6], f[7]), s);
@@ -234,7 +251,7 @@ __device__ __forceinline__ void store_row(const float* f, float tensor_scale, ui
 }
 
 template <int DT, int D, bool IL>
-__global__ void __launch_bounds__(kThreads) rotary_and_cache_kernel(const RotaryArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) rotary_and_cache_kernel(const RotaryArgs a, uint64_t share) {
   constexpr int TPR = D / 16, kUnits = 32 / TPR;  // threads of a row, units of a warp
   constexpr int kRow = row_bytes(DT, D);
   // (a programmatic dependent of whatever ran before on the stream)
@@ -245,24 +262,48 @@ __global__ void __launch_bounds__(kThreads) rotary_and_cache_kernel(const Rotary
   const int64_t warps = (int64_t)gridDim.x * (kThreads / 32);
   const int64_t T = a.num_tokens;
   const int qblocks = (a.heads_q + kQHeads - 1) / kQHeads;
-  // warps' worth of K/V units, then of query units
+  // Warps' worth of K/V units spread evenly among those of query units: of the
+  // first w, floor(w share / 2^32) are K/V units (share: their part of all,
+  // rounded up, times 2^32).
   const int64_t kv_w = (T * a.heads_kv + kUnits - 1) / kUnits, q_w = (T * qblocks + kUnits - 1) / kUnits;
-  for (int64_t w = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); w < kv_w + q_w; w += warps) {
-    const bool is_kv = w < kv_w;
-    const uint32_t per = (uint32_t)(is_kv ? a.heads_kv : qblocks);
-    const int64_t u = (is_kv ? w : w - kv_w) * kUnits + lane / TPR;
+  // A unit's token, head (or block of heads), position and slot, one unit ahead: the
+  // table row's address waits for the position.
+  struct Unit {
+    int64_t t, pos, slot;
+    int b;
+    bool is_kv, in_range;
+  };
+  auto unit_of = [&](int64_t w) {
+    Unit x;
+    const int64_t kv0 = (int64_t)(((uint64_t)w * share) >> 32);
+    x.is_kv = (int64_t)(((uint64_t)(w + 1) * share) >> 32) > kv0;
+    const uint32_t per = (uint32_t)(x.is_kv ? a.heads_kv : qblocks);
+    const int64_t u = (x.is_kv ? kv0 : w - kv0) * kUnits + lane / TPR;
     const int64_t tu = u <= 0x7FFFFFFF ? (int64_t)((uint32_t)u / per) : u / per;
     // (threads past the end take part in the shuffles with the last token's
     // rows and store nothing)
-    const bool in_range = tu < T;
-    const int64_t t = in_range ? tu : T - 1;
-    const int b = in_range ? (int)(u - tu * per) : 0;
-    const int64_t pos = __ldcg(a.positions + t);
-    const bool known = pos >= 0 && pos < a.max_position;
-    const float* const angles = a.cos_sin + (known ? pos : 0) * a.rotary_dim;
+    x.in_range = tu < T;
+    x.t = x.in_range ? tu : T - 1;
+    x.b = x.in_range ? (int)(u - tu * per) : 0;
+    x.pos = __ldcg(a.positions + x.t);
+    x.slot = x.is_kv ? __ldcg(a.slot_mapping + x.t) : 0;
+    return x;
+  };
+  const int64_t all = kv_w + q_w;
+  int64_t w = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  if (w >= all) return;
+  Unit next = unit_of(w);
+  for (; w < all; w += warps) {
+    const Unit cur = next;
+    if (w + warps < all) next = unit_of(w + warps);
+    const int64_t t = cur.t;
+    const int b = cur.b;
+    const bool in_range = cur.in_range, is_kv = cur.is_kv;
+    const bool known = cur.pos >= 0 && cur.pos < a.max_position;
+    const float* const angles = a.cos_sin + (known ? cur.pos : 0) * a.rotary_dim;
     Angles<IL> ang;
     if (is_kv) {
-      const int64_t slot = __ldcg(a.slot_mapping + t);
+      const int64_t slot = cur.slot;
       const uint16_t* ks = a.key + t * a.key_stride + (int64_t)b * D + part * 16;
       const uint16_t* vs = a.value + t * a.value_stride + (int64_t)b * D + part * 16;
       const uint4 k[2] = {dev::ldg_stream_coherent(ks), dev::ldg_stream_coherent(ks + 8)};
@@ -310,11 +351,15 @@ int launch(const RotaryArgs& a, bool interleaved, void* stream) {
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return KVQ_E_CUDA;
   constexpr int kUnits = 32 / (D / 16);
-  const int64_t warps = (a.num_tokens * a.heads_kv + kUnits - 1) / kUnits +
-                        (a.num_tokens * ((a.heads_q + kQHeads - 1) / kQHeads) + kUnits - 1) / kUnits;
-  const int64_t blocks = std::min<int64_t>((warps + kThreads / 32 - 1) / (kThreads / 32), (int64_t)sms * 8);
-  return interleaved ? launch_dependent(rotary_and_cache_kernel<DT, D, true>, (unsigned)blocks, kThreads, stream, a)
-                     : launch_dependent(rotary_and_cache_kernel<DT, D, false>, (unsigned)blocks, kThreads, stream, a);
+  const int64_t kv_w = (a.num_tokens * a.heads_kv + kUnits - 1) / kUnits;
+  const int64_t warps = kv_w + (a.num_tokens * ((a.heads_q + kQHeads - 1) / kQHeads) + kUnits - 1) / kUnits;
+  // (2^31 warps read terabytes; the kernel's products stay within 64 bits)
+  if (warps >= ((int64_t)1 << 31)) return KVQ_E_UNSUPPORTED;
+  const uint64_t share = (((uint64_t)kv_w << 32) + (uint64_t)warps - 1) / (uint64_t)warps;
+  const int64_t blocks = std::min<int64_t>((warps + kThreads / 32 - 1) / (kThreads / 32), (int64_t)sms * 2);
+  return interleaved
+             ? launch_dependent(rotary_and_cache_kernel<DT, D, true>, (unsigned)blocks, kThreads, stream, a, share)
+             : launch_dependent(rotary_and_cache_kernel<DT, D, false>, (unsigned)blocks, kThreads, stream, a, share);
 }
 
 template <int DT>
