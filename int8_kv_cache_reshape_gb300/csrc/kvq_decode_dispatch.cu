@@ -40,7 +40,11 @@ template <int D, int PARTS, int BATCH>
 int rect_merge(const AttnParams& p, const RectParams& rp, const RectMergePlan& m, void* stream) {
   // (eight warps, fewer where an item's rows need fewer)
   const unsigned rows = (unsigned)(m.most_rows < 8 / PARTS ? m.most_rows : 8 / PARTS);
-  return launch_dependent(merge_rect_kernel<D, PARTS, BATCH>, (unsigned)m.items, 32u * PARTS * rows, stream, p, rp);
+  // (few items: a CTA for each of an item's turns)
+  const int turns = (m.most_rows + (int)rows - 1) / (int)rows;
+  const int ctas = m.items * turns <= (int64_t)m.sms * 8 ? turns : 1;
+  return launch_dependent(merge_rect_kernel<D, PARTS, BATCH>, (unsigned)(m.items * ctas), 32u * PARTS * rows, stream, p,
+                          rp, ctas);
 }
 template <int D>
 int rect_merge_d(const AttnParams& p, const RectParams& rp, const RectMergePlan& m, void* stream) {

@@ -174,17 +174,20 @@ __global__ void __launch_bounds__(kMergeThreads) merge_splits_kernel(const AttnP
 // instructions are there (some 250 cycles for each 128 bytes of code otherwise, more
 // than the work).
 template <int D, int PARTS, int BATCH>
-__global__ void __launch_bounds__(256) merge_rect_kernel(const AttnParams p, const RectParams rp) {
+__global__ void __launch_bounds__(256) merge_rect_kernel(const AttnParams p, const RectParams rp, int ctas_of_item) {
   constexpr int kDims = D / 32, kRows = 8 / PARTS;
   __shared__ float sums[PARTS > 1 ? kRows : 1][PARTS][PARTS > 1 ? D : 1];
-  const RectMerge r = rp.merges[blockIdx.x];
+  const int item = (int)blockIdx.x / ctas_of_item;
+  const RectMerge r = rp.merges[item];
   const int lane = threadIdx.x & 31, slot = (threadIdx.x >> 5) / PARTS, part = (threadIdx.x >> 5) % PARTS;
-  const int at_once = blockDim.x / (32 * PARTS);
+  // rows of the item that this CTA takes: its first, and the step to its next
+  const int at_once = blockDim.x / (32 * PARTS), first = ((int)blockIdx.x - item * ctas_of_item) * at_once;
+  const int step = ctas_of_item * at_once;
   const int ns = r.m.nsplits + r.pre_splits, G = p.group;
-  for (int n0 = -at_once; n0 < r.m.nrows; n0 += at_once) {
-    if (n0 == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+  for (int n0 = first - step; n0 < r.m.nrows; n0 += step) {
+    if (n0 == first) asm volatile("griddepcontrol.wait;" ::: "memory");
     const int n = n0 + slot;
-    const bool live = n0 >= 0 && n < r.m.nrows;
+    const bool live = n0 >= first && n < r.m.nrows;
     auto row_of = [&](int s) -> int64_t {
       return (s < r.m.nsplits ? r.m.part + s * r.m.nrows : r.pre_part + (s - r.m.nsplits) * r.pre_stride) + n;
     };
