@@ -329,8 +329,8 @@ KVQ_API int kvq_get_scheduler_metadata(int num_req, int heads_q, int heads_kv,
  * same rows; they are read through the block-table row of one of them.
  * Requests of up to 16 (query, head) rows per kv head share; larger ones
  * (prompts) read their whole context as without a prefix.  A prefix is shared
- * up to a multiple of 32 keys; a batch that would save few bytes (less
- * than 24 MB of cache reads) is planned without sharing. */
+ * up to a multiple of 32 keys, and from two requests on; a batch of 4-bit rows
+ * that would save less than 18 MB of cache reads is planned without sharing. */
 KVQ_API int kvq_get_shared_prefix_metadata(int num_req, int heads_q, int heads_kv,
                                            int head_dim, const int32_t* seq_lens_host,
                                            const int32_t* query_start_loc_host,

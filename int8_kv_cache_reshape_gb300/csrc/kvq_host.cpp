@@ -710,10 +710,13 @@ int plan_attention(int num_req, int heads_q, int heads_kv, int head_dim, const i
   //    of whole requests; pre_tile[r] and pre_row[r]: a request's tile and its
   //    first row there (-1: none).  Requests with more than kTileMaxRows rows
   //    run whole on the prefill: their work is products, which sharing does
-  //    not save.  What the sharing saves is bytes: (members - 1) times the
-  //    prefix, at the rate of the decode kernel, against the units' fixed time
-  //    and the merge, so a batch that saves less than kPrefixMinBytes stays
-  //    unshared.  KVQ_PREFIX_MIN_BYTES (tests, benchmarks) sets another limit;
+  //    not save.  What sharing saves is cache reads, (members - 1) times the
+  //    prefix; it costs the units' fixed time and a merge of every row.  For two
+  //    requests and 128 keys already it wins on all rows but 4-bit ones (12 against
+  //    16 us at 32 / 8 heads of 128), whose decode reads half the bytes at a higher
+  //    rate: 12 against 11 us for 1 MB saved, 15 against 15 for 18 MB, 18 against
+  //    26 for 81 MB, so below kPrefixMinBytes4 they stay unshared.
+  //    KVQ_PREFIX_MIN_BYTES (tests, benchmarks) sets another limit for all rows;
   //    KVQ_RECT_TILES forces the KV tiles of a unit.
   std::vector<RectTile> rect;
   std::vector<int> pre_tile;
@@ -754,7 +757,7 @@ int plan_attention(int num_req, int heads_q, int heads_kv, int head_dim, const i
       }
       saved += (int64_t)(members[(size_t)g].size() - 1) * seen * heads_kv * 2 * kvq::row_bytes(dtype, head_dim);
     }
-    int64_t least = kvq::kPrefixMinBytes;
+    int64_t least = kvq::is_int4(dtype) ? kvq::kPrefixMinBytes4 : 0;
     if (const char* env = std::getenv("KVQ_PREFIX_MIN_BYTES")) least = std::atoll(env);
     if (saved >= least) {
       const int64_t most_rows = kvq::rect_rows(head_dim);

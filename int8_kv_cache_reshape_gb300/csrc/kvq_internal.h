@@ -242,8 +242,8 @@ KVQ_HD constexpr size_t rect_smem_bytes(int head_dim) {
 // A prefix's shared part ends at a multiple of this many keys (both plans'
 // chunks); the rest is read with each request's own keys.
 constexpr int kPrefixGrain = 32;
-// Bytes of cache reads that sharing has to save before a batch is planned so.
-constexpr int64_t kPrefixMinBytes = 24 << 20;
+// Bytes of 4-bit cache reads that sharing has to save before a batch is planned so.
+constexpr int64_t kPrefixMinBytes4 = 18 << 20;
 
 // Tensor maps of the caches for bulk tensor copies.  bf16 ("auto") rows, the
 // prefill: a rank-3 bf16 tensor {head_dim, kv heads, slots} copied in boxes

@@ -16,7 +16,7 @@ DTYPES = ["auto", "fp8_e4m3", "fp8_e5m2", "int8_per_token_head", "fp8_per_token_
 
 @pytest.fixture(autouse=True)
 def share_everything(monkeypatch):
-    """Batches as small as these would not be shared."""
+    """4-bit batches as small as these would not be shared."""
     monkeypatch.setenv("KVQ_PREFIX_MIN_BYTES", "0")
 
 
@@ -94,10 +94,11 @@ def test_same_result_as_without_sharing(cuda_device):
 
 def test_small_batches_are_planned_without_sharing(cuda_device, monkeypatch):
     monkeypatch.delenv("KVQ_PREFIX_MIN_BYTES")
-    wl = shared_workload([256], [0] * 4, [3, 4, 5, 6], [1] * 4, 8, 2, 128, 16, "int8_per_token_head", 2)
-    g = _run(wl)
-    assert g.rect["num_units"] == 0 and g.rect["num_shared_requests"] == 0
-    compare(g, "unshared")
+    for dtype, shared in (("int4_per_token_head", 0), ("int8_per_token_head", 4)):
+        wl = shared_workload([256], [0] * 4, [3, 4, 5, 6], [1] * 4, 8, 2, 128, 16, dtype, 2)
+        g = _run(wl)
+        assert g.rect["num_shared_requests"] == shared and (g.rect["num_units"] > 0) == (shared > 0)
+        compare(g, dtype)
 
 
 def test_blocks_that_are_missing_from_the_table(cuda_device):
