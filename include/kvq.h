@@ -169,8 +169,8 @@ KVQ_API int kvq_reshape_and_cache(const void* key, const void* value,
  *
  *   query, key, value   device bf16 [num_tokens, heads, head_dim]; heads and
  *                       dims contiguous; token strides in elements (>= heads *
- *                       head_dim, multiples of 8); base pointers 16-byte
- *                       aligned.
+ *                       head_dim, multiples of 8, below 2^31); base pointers
+ *                       16-byte aligned.
  *   num_heads_q         0: keys and values only (query, query_out unused).
  *   positions           device int64 [num_tokens].
  *   cos_sin             device fp32 [max_position, rotary_dim], contiguous,
@@ -179,8 +179,9 @@ KVQ_API int kvq_reshape_and_cache(const void* key, const void* value,
  *                       up to head_dim; the others stay as they are.
  *   interleaved         0: pair j is dims (j, j + rotary_dim / 2); 1: (2j, 2j+1).
  *   query_out           device bf16 like query, with its own token stride; may
- *                       be query itself (same pointer and stride), else they
- *                       must not overlap.
+ *                       be query itself (same pointer and stride), else its
+ *                       rows must not meet those of query; nor those of key
+ *                       and value, or the caches.
  *   key_cache ... v_scale   as for kvq_reshape_and_cache, which stores the same
  *                       bytes for the same fp32 values.
  * A token whose slot is outside the pool stores no rows (its query is still

@@ -513,25 +513,30 @@ int kvq_rotary_and_cache(const void* query, const void* key, const void* value, 
   if (max_position == 0) return KVQ_E_INVALID_ARG;
   if (!key || !value || !positions || !cos_sin || !key_cache || !value_cache || !slot_mapping)
     return KVQ_E_INVALID_ARG;
+  // (products of a token count and a stride stay within 64 bits)
+  if (num_tokens > INT32_MAX) return KVQ_E_UNSUPPORTED;
   const int64_t min_stride = (int64_t)num_heads_kv * head_dim, min_q = (int64_t)num_heads_q * head_dim;
-  if (key_stride_tok < min_stride || value_stride_tok < min_stride || key_stride_tok % 8 ||
-      value_stride_tok % 8)
-    return KVQ_E_INVALID_ARG;
+  auto bad_stride = [](int64_t stride, int64_t least) { return stride < least || stride > INT32_MAX || stride % 8; };
+  if (bad_stride(key_stride_tok, min_stride) || bad_stride(value_stride_tok, min_stride)) return KVQ_E_INVALID_ARG;
   if (num_heads_q > 0) {
-    if (!query || !query_out || query_stride_tok < min_q || query_out_stride_tok < min_q ||
-        query_stride_tok % 8 || query_out_stride_tok % 8 || !aligned(query, 16) || !aligned(query_out, 16))
+    if (!query || !query_out || bad_stride(query_stride_tok, min_q) || bad_stride(query_out_stride_tok, min_q) ||
+        !aligned(query, 16) || !aligned(query_out, 16))
       return KVQ_E_INVALID_ARG;
-    // in place, or apart
-    const char* const q0 = static_cast<const char*>(query);
-    const char* const o0 = static_cast<const char*>(query_out);
-    const int64_t q_bytes = 2 * ((num_tokens - 1) * query_stride_tok + min_q);
-    const int64_t o_bytes = 2 * ((num_tokens - 1) * query_out_stride_tok + min_q);
-    const bool same = q0 == o0 && query_stride_tok == query_out_stride_tok;
-    // (rows of one buffer at one stride, side by side, do not meet either)
-    const int64_t apart = o0 > q0 ? o0 - q0 : q0 - o0;
-    const bool beside = query_stride_tok == query_out_stride_tok && apart % (2 * query_stride_tok) >= 2 * min_q &&
-                        apart % (2 * query_stride_tok) <= 2 * (query_stride_tok - min_q);
-    if (!same && !beside && q0 < o0 + o_bytes && o0 < q0 + q_bytes) return KVQ_E_INVALID_ARG;
+    // query_out's rows meet no row of an input: behind one another, or side by side
+    // in one buffer at one stride; or they are the queries' own
+    auto meets = [&](const void* rows, int64_t stride, int64_t width) {
+      const int64_t o0 = (int64_t)(uintptr_t)query_out, x0 = (int64_t)(uintptr_t)rows;
+      if (x0 >= o0 + 2 * ((num_tokens - 1) * query_out_stride_tok + min_q) ||
+          o0 >= x0 + 2 * ((num_tokens - 1) * stride + width))
+        return false;
+      if (stride != query_out_stride_tok || num_tokens == 1) return true;
+      const int64_t d = ((o0 - x0) % (2 * stride) + 2 * stride) % (2 * stride);
+      return d < 2 * width || d + 2 * min_q > 2 * stride;
+    };
+    const bool in_place = query == query_out && (query_stride_tok == query_out_stride_tok || num_tokens == 1);
+    if ((!in_place && meets(query, query_stride_tok, min_q)) || meets(key, key_stride_tok, min_stride) ||
+        meets(value, value_stride_tok, min_stride))
+      return KVQ_E_INVALID_ARG;
   }
   if (!aligned(key, 16) || !aligned(value, 16) || !aligned(key_cache, 16) || !aligned(value_cache, 16) ||
       !aligned(slot_mapping, 8) || !aligned(positions, 8) || !aligned(cos_sin, 16))

@@ -193,14 +193,14 @@ __global__ void __launch_bounds__(256) merge_rect_kernel(const AttnParams p, con
     };
     const int R = r.m.row0 + (live ? n : 0), head = r.m.kv_head * G + R % G;
     // the largest log-sum-exp; a sink is one more
-    const float sink = p.sinks ? fmaf(p.sinks[head], 1.4426950408889634f, 6.0f) : -INFINITY;
+    const float sink = live && p.sinks ? fmaf(p.sinks[head], 1.4426950408889634f, 6.0f) : -INFINITY;
     float lse = live && lane < ns ? __ldcg(p.part_lse + row_of(lane)) : -INFINITY, M = lse;
     for (int s = lane + 32; live && s < ns; s += 32) M = fmaxf(M, __ldcg(p.part_lse + row_of(s)));
     float o[kDims], sum = 0.0f;
 #pragma unroll
     for (int d = 0; d < kDims; ++d) o[d] = 0.0f;
     int s0 = 0;
-    do {  // this warp's splits s0 + part, + 4, ..
+    do {  // this warp's splits s0 + part, + PARTS, .. (BATCH of them)
       if (s0 > 0) lse = live && s0 + lane < ns ? __ldcg(p.part_lse + row_of(s0 + lane)) : -INFINITY;
       const bool mine = lane < BATCH * PARTS;  // (the batch's splits)
       float v[BATCH][kDims];

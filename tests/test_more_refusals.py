@@ -84,6 +84,11 @@ GOOD = [A, 2 * A, 3 * A, 5, 512, 256, 256, 4, 2, 128, 4 * A, 5 * A, 9, 64, 0, 6 
     # queries written over queries that are still to be read
     ({15: A + 256}, kvq.E_INVALID_ARG), ({15: A, 16: 1024}, kvq.E_INVALID_ARG),
     ({4: 1024, 16: 1024, 15: A + 256}, kvq.E_INVALID_ARG), ({4: 1024, 16: 1024, 15: A - 512}, kvq.E_INVALID_ARG),
+    # over keys or values: between their rows, over the last, a single token's
+    ({15: 2 * A - 512}, kvq.E_INVALID_ARG), ({15: 3 * A + 4 * 512}, kvq.E_INVALID_ARG),
+    ({16: 1024, 4: 1024, 5: 1024, 15: A + 1024, 1: A + 2048 - 16}, kvq.E_INVALID_ARG),
+    ({3: 1, 15: 2 * A + 496}, kvq.E_INVALID_ARG),
+    ({3: 1 << 31}, kvq.E_UNSUPPORTED), ({4: 1 << 31}, kvq.E_INVALID_ARG), ({6: 1 << 40}, kvq.E_INVALID_ARG),
 ])
 def test_rotary_arguments(changes, status):
     args = list(GOOD)
