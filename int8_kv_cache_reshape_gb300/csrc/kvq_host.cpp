@@ -337,7 +337,7 @@ double rect_tile_us(int dtype, int head_dim, bool two) {
 // the SMs that the units leave: few long units then cost less than many short
 // ones.  Returns the SMs left for it where it is best cut to fit there, else 0.  Appends the units, longest first, and hands out
 // partial rows from *partial_rows on.  A tile left whole writes out directly if
-// it may (`direct`) and its rows have one O.
+// it may (`direct`).
 int plan_rect(std::vector<RectTile>& tiles, int dtype, int heads_kv, int head_dim, int sms, bool direct,
               int64_t beside_bytes, int64_t forced,
               std::vector<RectUnit>* units, int64_t* partial_rows) {
@@ -368,7 +368,7 @@ int plan_rect(std::vector<RectTile>& tiles, int dtype, int heads_kv, int head_di
       longest = std::max(longest, kRectStart + (double)ceil_div(T, S) * per);
       shortest = std::min(shortest, kRectStart + (double)(T / S) * per);
       n += heads_kv * S;
-      if (!direct || S > 1 || pair(t)) rows += heads_kv * S * t.nrows * (pair(t) ? 2 : 1);
+      if (!direct || S > 1) rows += heads_kv * S * t.nrows * (pair(t) ? 2 : 1);
     }
     const int64_t waves = ceil_div(n, sms);
     // (partials: written and read once, in L2 mostly)
@@ -397,7 +397,7 @@ int plan_rect(std::vector<RectTile>& tiles, int dtype, int heads_kv, int head_di
     RectTile& t = tiles[i];
     const int64_t T = kv_tiles(t);
     t.splits = T == 0 ? 0 : ceil_div(T, best);
-    const bool whole = direct && t.splits == 1 && !pair(t);
+    const bool whole = direct && t.splits == 1;
     t.parts = whole ? 0 : t.splits * (pair(t) ? 2 : 1);
     t.part = *partial_rows;
     *partial_rows += t.parts * t.nrows * heads_kv;

@@ -37,7 +37,8 @@
 // 235 us with one thread for both, 215 us with two).
 //   two row tiles (129 to 256 rows): each group has a row tile and all keys
 //   one row tile (up to 128 rows): both have its rows and take the halves of each
-//     KV tile, with an O of their own (two partials a row)
+//     KV tile, with an O of their own: two partials a row, or, where the unit holds
+//     all keys, joined through shared memory
 //   head_dim 256: O takes half of tensor memory; one row tile, one group
 // (Items of 128 keys leave no room for a second S: with P in S's place the next S
 // waits for the P V, 4,280 cycles a 128-key tile of two row tiles of which 2,048 are MMA
@@ -746,17 +747,19 @@ __global__ void __launch_bounds__(512, 1) rect_attention_kernel(const AttnParams
       warp_arrive(bar(Geo::kBarPFull + b));
     }
     // ---- epilogue: O / l as fp32 partial rows or bf16 rows -------------------
+    const bool join = kRT == 2 && !two && part0 < 0;  // one row tile, all its keys
     if (ok) {
-      // (one row tile: the rows go out through the Q tile that both groups' MMAs read)
-      ok = wait(Geo::kBarOFinal + t, 0) && (kRT == 1 || two || t == 1 || wait(Geo::kBarOFinal + 1, 0));
+      // (one row tile: the rows go out through the Q tile that both groups' MMAs read,
+      // and are joined in the K tiles)
+      ok = wait(Geo::kBarOFinal + t, 0) && (kRT == 1 || two || (t == 1 && !join) || wait(Geo::kBarOFinal + 1 - t, 0));
       tc::fence_after_sync();
     }
     // (rows of this group's row tile in the partials: the second group of a
     // single row tile has its own)
     const int part = part0 + (two ? tile * kM : t * part_stride);
     const int tile_rows = min(kM, nrows - tile * kM);
-    if (ok) {
-      if (part0 < 0 && p.sinks && row_valid && m_ref != -INFINITY) {
+    {
+      if (part0 < 0 && !join && p.sinks && row_valid && m_ref != -INFINITY) {
         // the sink joins the normaliser here (partial rows: in the merge)
         const float skl = p.sinks[head_q] * log2e;
         if (skl != -INFINITY) l_sum += exp2f(fminf(skl - m_ref + 6.0f, 126.0f));
@@ -769,7 +772,42 @@ __global__ void __launch_bounds__(512, 1) rect_attention_kernel(const AttnParams
                         : Geo::kAuto ? 1.0f
                                      : p.v_scale);
       const float sc2 = __int_as_float((127 + up2) << 23);
-      if (part0 >= 0 && row_valid) p.part_lse[part + m] = l_sum > 0.0f ? m_ref + log2f(l_sum) : -INFINITY;
+      const float lse = l_sum > 0.0f ? m_ref + log2f(l_sum) : -INFINITY;
+      if (ok && part0 >= 0 && row_valid) p.part_lse[part + m] = lse;
+      float own = 1.0f, other = 0.0f;  // weights of the row's two halves
+      const uint32_t join_at = base + Geo::kOffK + (uint32_t)(m * D * 4);
+      auto join_piece = [&](int c) { return join_at + (uint32_t)((c ^ (m & 7)) << 4); };
+      if (kRT == 2 && join) {
+        // the second group's normalised rows and their log-sum-exps, through the K and V
+        // tiles (no longer read), to the same row's thread of the first
+        float* const lse_of = reinterpret_cast<float*>(sm + Geo::kOffV);
+        if (t == 1) {
+          lse_of[m] = lse;
+#pragma unroll 1
+          for (int c0 = 0; ok && c0 < D; c0 += 32) {
+            uint32_t w[32];
+            tc::tmem_ld32(tmem_o + (uint32_t)c0, w);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * sc * sc2);
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              sts128(join_piece((c0 + e) >> 2), make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]));
+          }
+        }
+        asm volatile("bar.sync 1, 256;" ::: "memory");  // (both groups come here, whatever gave up)
+        if (t == 0) {
+          const float second = lse_of[m];
+          const float sink = p.sinks && row_valid ? fmaf(p.sinks[head_q], log2e, 6.0f) : -INFINITY;
+          const float M = dev::max3(lse, second, sink), at = M == -INFINITY ? 0.0f : M;
+          own = exp2f(lse - at);
+          other = exp2f(second - at);
+          const float sum = own + other + exp2f(sink - at);
+          const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;  // (a row that sees no key: zeros)
+          own *= inv;
+          other *= inv;
+        }
+      }
       // The warp's rows go through its part of the Q tiles (no longer read):
       // D / 2 columns a pass, 16-byte pieces swizzled by the row, then out in
       // runs of a row.
@@ -777,7 +815,7 @@ __global__ void __launch_bounds__(512, 1) rect_attention_kernel(const AttnParams
       const int wr = (warp & 3) * 32;
       const uint32_t stage = base + Geo::kOffQ + (uint32_t)(t * Geo::kQBytes + (warp & 3) * 32 * kCw * 4);
 #pragma unroll 1
-      for (int h = 0; h < 2; ++h) {
+      for (int h = ok && !(join && t == 1) ? 0 : 2; h < 2; ++h) {
 #pragma unroll 1
         for (int c0 = 0; c0 < kCw; c0 += 32) {
           uint32_t w[32];
@@ -788,6 +826,13 @@ __global__ void __launch_bounds__(512, 1) rect_attention_kernel(const AttnParams
             float f[4];
 #pragma unroll
             for (int b = 0; b < 4; ++b) f[b] = __uint_as_float(w[e + b]) * sc * sc2;
+            if (kRT == 2 && join) {
+              const uint4 y = lds128(join_piece((h * kCw + c0 + e) >> 2));
+              f[0] = fmaf(__uint_as_float(y.x), other, f[0] * own);
+              f[1] = fmaf(__uint_as_float(y.y), other, f[1] * own);
+              f[2] = fmaf(__uint_as_float(y.z), other, f[2] * own);
+              f[3] = fmaf(__uint_as_float(y.w), other, f[3] * own);
+            }
             sts128(stage + (uint32_t)(lane * kCw * 4 + ((((c0 + e) >> 2) ^ (lane & 7)) << 4)),
                    make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])));
           }
