@@ -47,21 +47,21 @@ PROFILED_TRAFFIC = {
     # (workload, kv cache dtype, part of a mixed batch): DRAM bytes read +
     # written by that kernel in one launch, from the ncu capture in `profile`
     # (its "traffic" command; taken while the listed sources hashed to `sha1`).
-    (2, "fp8_e4m3", None): {"bytes": 361.342720e6 + 4.627456e6,
+    (2, "fp8_e4m3", None): {"bytes": 361.369344e6 + 4.377856e6,
                             "profile": "profiles/splitkv_decode_decode_batch.md",
-                            "sources": ['kvq_decode.cuh', 'kvq_device.cuh', 'kvq_internal.h'], "sha1": "4ad871a35ebf166baed2e4589c08ee20104881b9"},
-    (5, "fp8_e5m2", None): {"bytes": 269.839616e6 + 4.492032e6,
+                            "sources": ['kvq_decode.cuh', 'kvq_device.cuh', 'kvq_internal.h'], "sha1": "7f450eb17709a02400c70911fd7f1bbd37b4cca8"},
+    (5, "fp8_e5m2", None): {"bytes": 269.841664e6 + 4.427776e6,
                             "profile": "profiles/splitkv_decode_long_context.md",
-                            "sources": ['kvq_decode.cuh', 'kvq_device.cuh', 'kvq_internal.h'], "sha1": "4ad871a35ebf166baed2e4589c08ee20104881b9"},
-    (4, "int8_per_token_head", "decode"): {"bytes": 484.947968e6 + 5.318144e6,
+                            "sources": ['kvq_decode.cuh', 'kvq_device.cuh', 'kvq_internal.h'], "sha1": "7f450eb17709a02400c70911fd7f1bbd37b4cca8"},
+    (4, "int8_per_token_head", "decode"): {"bytes": 484.947200e6 + 4.939520e6,
                                            "profile": "profiles/mixed_batch_int8_per_token_head.md",
-                                           "sources": ['kvq_decode.cuh', 'kvq_device.cuh', 'kvq_internal.h'], "sha1": "4ad871a35ebf166baed2e4589c08ee20104881b9"},
-    (4, "int8_per_token_head", "prefill"): {"bytes": 369.595392e6 + 88.673536e6,
+                                           "sources": ['kvq_decode.cuh', 'kvq_device.cuh', 'kvq_internal.h'], "sha1": "7f450eb17709a02400c70911fd7f1bbd37b4cca8"},
+    (4, "int8_per_token_head", "prefill"): {"bytes": 362.588416e6 + 88.787712e6,
                                             "profile": "profiles/mixed_batch_int8_per_token_head.md",
-                                            "sources": ['kvq_prefill.cuh', 'kvq_tcgen05.cuh', 'kvq_device.cuh', 'kvq_internal.h'], "sha1": "a8a57d86397cd1906d39d9bb7e061bf821da9de5"},
-    (3, "fp8_e4m3", None): {"bytes": 37.951488e6 + 0.287232e6,
+                                            "sources": ['kvq_prefill.cuh', 'kvq_tcgen05.cuh', 'kvq_device.cuh', 'kvq_internal.h'], "sha1": "b3cb7484531848c1673962fe04967a2203dbd699"},
+    (3, "fp8_e4m3", None): {"bytes": 37.880064e6 + 0.311552e6,
                             "profile": "profiles/prefill_attention_large_prefill.md",
-                            "sources": ['kvq_prefill.cuh', 'kvq_tcgen05.cuh', 'kvq_device.cuh', 'kvq_internal.h'], "sha1": "a8a57d86397cd1906d39d9bb7e061bf821da9de5"},
+                            "sources": ['kvq_prefill.cuh', 'kvq_tcgen05.cuh', 'kvq_device.cuh', 'kvq_internal.h'], "sha1": "b3cb7484531848c1673962fe04967a2203dbd699"},
 }
 
 

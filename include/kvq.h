@@ -366,7 +366,8 @@ KVQ_API int kvq_get_cross_attention_metadata(int num_req, int heads_q, int heads
  * use_sink); [P3] Breakdown item 3 (_prepare_kv_tile: per-token-head
  * dequantisation in the tile).
  *
- *   sched                   from kvq_get_scheduler_metadata.
+ *   sched                   from kvq_get_scheduler_metadata, or from the calls
+ *                           for shared prefixes and encoders above.
  *   heads_q, heads_kv,      what the caller believes the caches and q hold;
  *   head_dim, dtype         they, causal and window must equal the values
  *                           the schedule was built for, else
