@@ -18,9 +18,10 @@
 // bf16.  A unit of threads takes kQHeads query heads of a token, whose cos and
 // sin stay in registers, or one kv head's K and V rows; the two kinds are mixed, since one
 // is bound by memory and the other by its instructions.
-// 20,011 tokens of 32 / 8 heads of 128: 86 us for 4-bit rows (446 MB, 5.2 TB/s: 0.76 of a
-// measured copy; 93 us with the kinds one after the other), 89 us int8 and fp8, 83 us
-// bf16; what is left above the copy's 66 to 74 us is latency and the codes' instructions.
+// 20,011 tokens of 32 / 8 heads of 128: 80 us for 4-bit rows (446 MB, 5.6 TB/s: 0.82 of a
+// measured copy; 93 us with the kinds one after the other, 86 us without the fetches into
+// L2 a unit ahead), 82 us int8 and fp8, 81 us bf16; what is left above the copy's 66 to 74 us is
+// latency and the codes' instructions.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -253,8 +254,11 @@ __device__ __forceinline__ void store_row(const float* f, float tensor_scale, ui
   }
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* at) { asm volatile("prefetch.global.L2 [%0];" :: "l"(at)); }
+
 template <int DT, int D, bool IL>
-__global__ void __launch_bounds__(kThreads, 2) rotary_and_cache_kernel(const RotaryArgs a, uint64_t share) {
+__global__ void __launch_bounds__(kThreads, 2) rotary_and_cache_kernel(const RotaryArgs a, uint64_t share,
+                                                                       bool from_memory) {
   constexpr int TPR = D / 16, kUnits = 32 / TPR;  // threads of a row, units of a warp
   constexpr int kRow = row_bytes(DT, D);
   // (a programmatic dependent of whatever ran before on the stream)
@@ -298,7 +302,22 @@ __global__ void __launch_bounds__(kThreads, 2) rotary_and_cache_kernel(const Rot
   Unit next = unit_of(w);
   for (; w < all; w += warps) {
     const Unit cur = next;
-    if (w + warps < all) next = unit_of(w + warps);
+    if (w + warps < all) {
+      next = unit_of(w + warps);
+      if (from_memory) {
+        if (next.is_kv) {
+          const int64_t at = (int64_t)next.b * D + part * 16;
+          prefetch_l2(a.key + next.t * a.key_stride + at);
+          prefetch_l2(a.value + next.t * a.value_stride + at);
+        } else {
+          const int h0 = next.b * kQHeads, nh = min(kQHeads, a.heads_q - h0);
+          const uint16_t* const qs = a.query + next.t * a.query_stride + (int64_t)h0 * D + part * 16;
+#pragma unroll
+          for (int i = 0; i < kQHeads; ++i)
+            if (i < nh) prefetch_l2(qs + i * D);
+        }
+      }
+    }
     const int64_t t = cur.t;
     const int b = cur.b;
     const bool in_range = cur.in_range, is_kv = cur.is_kv;
@@ -360,9 +379,15 @@ int launch(const RotaryArgs& a, bool interleaved, void* stream) {
   if (warps >= ((int64_t)1 << 31)) return KVQ_E_UNSUPPORTED;
   const uint64_t share = (((uint64_t)kv_w << 32) + (uint64_t)warps - 1) / (uint64_t)warps;
   const int64_t blocks = std::min<int64_t>((warps + kThreads / 32 - 1) / (kThreads / 32), (int64_t)sms * 2);
+  // The next unit's rows are fetched into L2 a unit ahead where they are not there
+  // already, as a projection's output is up to about half of it: 20,011 tokens of 32 / 8
+  // heads of 128 (246 MB) take 80 us in place of 86 (4-bit rows; int8 82 / 89), but 4,099 of
+  // 16 / 2 heads of 256 (42 MB) 14.9 in place of 13.6.
+  const int64_t in_bytes = 2 * a.num_tokens * ((int64_t)a.heads_q + 2 * a.heads_kv) * D;
+  const bool from_memory = in_bytes > (64 << 20);
   return interleaved
-             ? launch_dependent(rotary_and_cache_kernel<DT, D, true>, (unsigned)blocks, kThreads, stream, a, share)
-             : launch_dependent(rotary_and_cache_kernel<DT, D, false>, (unsigned)blocks, kThreads, stream, a, share);
+             ? launch_dependent(rotary_and_cache_kernel<DT, D, true>, (unsigned)blocks, kThreads, stream, a, share, from_memory)
+             : launch_dependent(rotary_and_cache_kernel<DT, D, false>, (unsigned)blocks, kThreads, stream, a, share, from_memory);
 }
 
 template <int DT>
