@@ -194,3 +194,28 @@ def test_on_another_stream_and_replayed(cuda_device):
         graph.replay()
         torch.cuda.synchronize()
         c.check(c.out.t.cpu().view(torch.int16).numpy())
+
+
+@pytest.mark.parametrize("dtype", ["auto", "int8_per_token_head", "int4_per_token_head"])
+def test_large_batches_are_stored_as_small_ones(cuda_device, dtype):
+    """A batch of more than 64 MB of rows against its two halves, bit for bit."""
+    T, Hq, H, D = 6001, 40, 8, 128
+    g = torch.Generator(device=cuda_device).manual_seed(4)
+    qkv = torch.randn((T, Hq + 2 * H, D), generator=g, device=cuda_device).to(torch.bfloat16)
+    assert qkv.numel() * 2 > 64 << 20 and qkv.numel() < 64 << 20
+    pos = torch.randint(0, 3000, (T,), generator=g, device=cuda_device)
+    table = torch.from_numpy(R.cos_sin_table(3000, D)).to(cuda_device)
+    slots = torch.randperm(T + 15, generator=g, device=cuda_device)[:T]
+    slots[::97] = -1
+    row = kvq().cache_row_bytes(dtype, D)
+    got = []
+    for parts in ([(0, T)], [(0, 3000), (3000, T)]):
+        kc, vc = (torch.full((T // 16 + 1, 16, H, row), FILL, dtype=torch.uint8, device=cuda_device) for _ in range(2))
+        out = torch.full((T, Hq, D), float("nan"), dtype=torch.bfloat16, device=cuda_device)
+        for a, b in parts:
+            x = qkv[a:b]
+            kvq().rotary_and_cache(x[:, :Hq], x[:, Hq:Hq + H], x[:, Hq + H:], pos[a:b], table, out[a:b], kc, vc,
+                                   slots[a:b], dtype)
+        got.append((kc, vc, out.view(torch.int16)))
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    assert not torch.isnan(out).any()
