@@ -1,6 +1,6 @@
 // kvq_decode_dispatch.cu -- head_dim (and ALiBi) dispatch of the split-KV
-// decode, the tensor-core prefill and the rectangular attention kernels (one translation unit per
-// head_dim and ALiBi setting holds the instances).
+// decode, the tensor-core prefill and the rectangular attention kernels (one
+// translation unit per head_dim and ALiBi setting holds the instances).
 #include "kvq_internal.h"
 #include "kvq_merge.cuh"
 

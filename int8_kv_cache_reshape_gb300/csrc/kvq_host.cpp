@@ -333,11 +333,11 @@ double rect_tile_us(int dtype, int head_dim, bool two) {
 
 // Cut the row tiles' keys among CTAs (one per SM) so that the last one ends
 // early: all units as near as can be to one length, tried for every number
-// of cuts of the longest tile.  The decode beside them (beside_bytes of cache) takes
-// the SMs that the units leave: few long units then cost less than many short
-// ones.  Returns the SMs left for it where it is best cut to fit there, else 0.  Appends the units, longest first, and hands out
-// partial rows from *partial_rows on.  A tile left whole writes out directly if
-// it may (`direct`).
+// of cuts of the longest tile.  The decode beside them (beside_bytes of cache)
+// takes the SMs that the units leave: few long units then cost less than many
+// short ones.  Returns the SMs left for it where it is best cut to fit there,
+// else 0.  Appends the units, longest first, and hands out partial rows from
+// *partial_rows on.  A tile left whole writes out directly if it may (`direct`).
 int plan_rect(std::vector<RectTile>& tiles, int dtype, int heads_kv, int head_dim, int sms, bool direct,
               int64_t beside_bytes, int64_t forced,
               std::vector<RectUnit>* units, int64_t* partial_rows) {
