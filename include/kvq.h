@@ -327,7 +327,9 @@ KVQ_API int kvq_get_scheduler_metadata(int num_req, int heads_q, int heads_kv,
  *                         begins with, or -1.  Its length must not exceed L - Q
  *                         (the new tokens come after it).
  * The caller vouches that keys 0 .. P - 1 of all requests of a prefix hold the
- * same rows; they are read through the block-table row of one of them.
+ * same rows (with a window: those of them that a request's queries see); they are
+ * read through the block-table row of one of them, which sees all that is read,
+ * so a request's entries wholly behind its window are not used here either.
  * Requests of up to 16 (query, head) rows per kv head share; larger ones
  * (prompts) read their whole context as without a prefix.  A prefix is shared
  * up to a multiple of 32 keys, and from two requests on; a batch of 4-bit rows

@@ -782,7 +782,6 @@ int plan_attention(int num_req, int heads_q, int heads_kv, int head_dim, const i
           if (lo >= P) continue;  // sees none of it
           if (t.nrows == 0) {
             t = RectTile{};
-            t.req = r;
             t.tok0 = (int)s->tokens.size();
             t.kv_lo = P;
             t.kv_hi = P;
@@ -790,7 +789,13 @@ int plan_attention(int num_req, int heads_q, int heads_kv, int head_dim, const i
           pre_tile[(size_t)r] = (int)rect.size();
           pre_row[(size_t)r] = t.nrows;
           t.nrows += (int)(Q * G);
-          t.kv_lo = std::min(t.kv_lo, lo);
+          // The tile reads the table row of the request whose window begins first: the
+          // others may no longer hold blocks behind their own windows.  (lo < P here,
+          // so the tile's first request is taken.)
+          if (lo < t.kv_lo) {
+            t.kv_lo = lo;
+            t.req = r;
+          }
           for (int64_t i = 0; i < Q; ++i)
             s->tokens.push_back(RectToken{(int32_t)(query_start_loc_host[r] + i), (int32_t)(p0 + i)});
           ++s->num_shared_requests;
