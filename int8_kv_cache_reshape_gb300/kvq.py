@@ -322,7 +322,8 @@ def rotary_and_cache(query, key, value, positions, cos_sin, query_out, key_cache
                      v_scale: float = 1.0, stream=None) -> None:
     """Queries and keys rotated by their positions, keys and values stored in
     the caches: query / query_out bf16 [T, Hq, D] (one tensor, or two; or both
-    None), key / value bf16 [T, Hkv, D] (token strides may exceed the heads);
+    None), key / value bf16 [T, Hkv, D] (token strides may exceed the heads;
+    attention calls take query_out only where its rows lie side by side);
     positions, slot_mapping int64 [T]; cos_sin float32 [max_position,
     rotary_dim], cosines then sines; caches uint8 [NB, B, Hkv, row]."""
     _check(lib.kvq_rotary_and_cache(*_rotary_and_cache_args(
@@ -542,10 +543,22 @@ def get_cross_attention_metadata(num_req: int, heads_q: int, heads_kv: int, head
     return Sched(h, ws.value)
 
 
+def _check_rows(q, out):
+    """q and out as the attention calls read and write them: all heads' rows side by
+    side (the library takes no stride for them; a slice of a fused projection,
+    rotated in place or not, is copied by .contiguous() first)."""
+    import torch
+    if q.dim() != 3 or q.dtype != torch.bfloat16 or not q.is_contiguous():
+        raise ValueError("q must be contiguous bfloat16 [tokens, heads, head_dim]")
+    if out is not None and (out.dtype != torch.bfloat16 or not out.is_contiguous()):
+        raise ValueError("out must be contiguous bfloat16 [tokens, heads, head_dim]")
+
+
 def _attention_args(sched, q, key_cache, value_cache, query_start_loc, seq_lens, block_table,
                     sm_scale, causal, window, soft_cap, k_scale, v_scale, out, workspace,
                     kv_cache_dtype, heads_kv, stream, num_blocks, alibi_slopes, sinks):
     dt = parse_kv_cache_dtype(kv_cache_dtype) if isinstance(kv_cache_dtype, str) else kv_cache_dtype
+    _check_rows(q, out)
     _, Hq, D = q.shape
     nb = key_cache.shape[0] if num_blocks is None else num_blocks
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
@@ -561,7 +574,7 @@ def attention_with_kv_cache(sched: Sched, q, key_cache, value_cache, query_start
                             window: int, soft_cap: float, k_scale: float, v_scale: float,
                             out, workspace, kv_cache_dtype, heads_kv: int, stream=None,
                             num_blocks=None, alibi_slopes=None, sinks=None) -> None:
-    """q / out: bf16 [sum Q, Hq, D]; caches uint8 [NB, B, Hkv, row];
+    """q / out: contiguous bf16 [sum Q, Hq, D]; caches uint8 [NB, B, Hkv, row];
     block_table int32 [R, max_blocks]; query_start_loc / seq_lens device
     int32; workspace: a uint8 device tensor of >= sched.workspace_bytes;
     alibi_slopes / sinks: device float32 [Hq] or None."""
@@ -598,6 +611,7 @@ def attention_with_kv_cache_static_scratch(sched: Sched, q, key_cache, value_cac
     For callers that cannot allocate device memory; calls must not overlap
     on the GPU."""
     dt = parse_kv_cache_dtype(kv_cache_dtype) if isinstance(kv_cache_dtype, str) else kv_cache_dtype
+    _check_rows(q, out)
     _, Hq, D = q.shape
     nb = key_cache.shape[0] if num_blocks is None else num_blocks
     _check(lib.kvq_attention_with_kv_cache_static_scratch(
@@ -624,6 +638,7 @@ def _decode_step_args(key, value, slot_mapping, key_cache, value_cache, q, query
                       v_scale, out, workspace, kv_cache_dtype, heads_kv, alibi_slopes, sinks,
                       stream, num_blocks):
     dt = parse_kv_cache_dtype(kv_cache_dtype) if isinstance(kv_cache_dtype, str) else kv_cache_dtype
+    _check_rows(q, out)
     _, Hq, D = q.shape
     T = key.shape[0]
     nb = key_cache.shape[0] if num_blocks is None else num_blocks
@@ -643,8 +658,8 @@ def decode_step(key, value, slot_mapping, key_cache, value_cache, q, query_start
                 k_scale: float, v_scale: float, out, workspace, kv_cache_dtype, heads_kv: int,
                 alibi_slopes=None, sinks=None, stream=None, num_blocks=None) -> None:
     """kvq_decode_step: the new rows key/value bf16 [T, Hkv, D] with their
-    slot_mapping int64 [T]; q / out bf16 [sum Q, Hq, D]; query_start_loc,
-    seq_lens int32 device; workspace: a zero-filled uint8 device tensor of
+    slot_mapping int64 [T]; q / out contiguous bf16 [sum Q, Hq, D];
+    query_start_loc, seq_lens int32 device; workspace: a zero-filled uint8 device tensor of
     >= decode_step_workspace_size(...) bytes."""
     _check(lib.kvq_decode_step(*_decode_step_args(
         key, value, slot_mapping, key_cache, value_cache, q, query_start_loc, seq_lens,
