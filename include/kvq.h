@@ -180,8 +180,8 @@ KVQ_API int kvq_reshape_and_cache(const void* key, const void* value,
  *   interleaved         0: pair j is dims (j, j + rotary_dim / 2); 1: (2j, 2j+1).
  *   query_out           device bf16 like query, with its own token stride; may
  *                       be query itself (same pointer and stride), else its
- *                       rows must not meet those of query; nor those of key
- *                       and value, or the caches.
+ *                       rows must not meet those of query; nor, in either case,
+ *                       those of key and value, or the caches (refused).
  *   key_cache ... v_scale   as for kvq_reshape_and_cache, which stores the same
  *                       bytes for the same fp32 values.
  * A token whose slot is outside the pool stores no rows (its query is still

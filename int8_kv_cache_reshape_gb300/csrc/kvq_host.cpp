@@ -537,6 +537,15 @@ int kvq_rotary_and_cache(const void* query, const void* key, const void* value, 
     if ((!in_place && meets(query, query_stride_tok, min_q)) || meets(key, key_stride_tok, min_stride) ||
         meets(value, value_stride_tok, min_stride))
       return KVQ_E_INVALID_ARG;
+    // nor a pool: the first row that ends behind its start does not begin before its end
+    const __int128 pool = (__int128)num_blocks * block_size * num_heads_kv * kvq::row_bytes(dtype, head_dim);
+    auto in_pool = [&](const void* cache) {
+      const int64_t o0 = (int64_t)(uintptr_t)query_out, c0 = (int64_t)(uintptr_t)cache;
+      const int64_t pitch = 2 * query_out_stride_tok, width = 2 * min_q;
+      const int64_t row = o0 + width > c0 ? 0 : (c0 - o0 - width) / pitch + 1;
+      return row < num_tokens && o0 + row * pitch < c0 + pool;
+    };
+    if (in_pool(key_cache) || in_pool(value_cache)) return KVQ_E_INVALID_ARG;
   }
   if (!aligned(key, 16) || !aligned(value, 16) || !aligned(key_cache, 16) || !aligned(value_cache, 16) ||
       !aligned(slot_mapping, 8) || !aligned(positions, 8) || !aligned(cos_sin, 16))
