@@ -924,11 +924,22 @@ int launch_decode_instance(const AttnParams& p, cudaStream_t stream) {
     cfg.blockDim = dim3(kDecodeThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    // An SM that a unit leaves while others run keeps the unit's split of L1 and shared
+    // memory (228 KB of the latter) for a CTA that states no preference; what is left
+    // of L1 holds few of the decode's loads in flight, and its CTAs there ran 2.4
+    // times as long as the others.  64 requests of 8,192 int8 keys of their own, two of them
+    // behind 32 shared ones, 32 / 8 heads of 128: 614 us, 241 with the preference (242 planned
+    // without sharing).
+    static_assert(decode_min_ctas(DT, D, NT) * (decode_smem_bytes(DT, D) + 1024) * 100 <=
+                      (size_t)kDecodeCarveout * (228 << 10),
+                  "the preference holds an SM's CTAs");
+    attr[1].id = cudaLaunchAttributePreferredSharedMemoryCarveout;
+    attr[1].val.sharedMemCarveout = kDecodeCarveout;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     if (cudaLaunchKernelEx(&cfg, kern, p, none) != cudaSuccess) {
       cudaGetLastError();
       return KVQ_E_CUDA;

@@ -108,6 +108,9 @@ KVQ_HD constexpr size_t decode_warp_smem(int dtype, int head_dim) {
 KVQ_HD constexpr size_t decode_smem_bytes(int dtype, int head_dim) {
   return (size_t)kDecodeWarps * decode_warp_smem(dtype, head_dim);
 }
+// Shared memory that a decode beside units prefers of an SM's 228 KB, in percent: its
+// CTAs' (a KB of each is the system's), the rest is L1.
+constexpr int kDecodeCarveout = 6;
 
 // ---- split-KV decode over 4-bit rows ---------------------------------------
 // A CTA (one per SM) has `gpc` groups of `hg` warps, one warp per kv head of a

@@ -1,0 +1,80 @@
+"""The decode beside the units of a shared prefix: requests whose own contexts are
+long.  Its CTAs on SMs that units held before have to run like the others."""
+import numpy as np
+import pytest
+import torch
+
+from int8_kv_cache_reshape_gb300 import kvq
+
+pytestmark = pytest.mark.gpu
+
+HQ, HKV, D, B = 32, 8, 128, 16
+
+
+def _calls(dtype, P, own, new, sharers, device):
+    """One batch planned with its prefix and without: (call, schedule) of each."""
+    R = len(own)
+    lens = np.array([P + n for n in own], np.int32)
+    need = [-(-int(n) // B) for n in lens]
+    gen = torch.Generator(device).manual_seed(1)
+    shape = (sum(need), B, HKV, kvq.cache_row_bytes(dtype, D))
+    if dtype == "auto":
+        kc = torch.randn((*shape[:3], D), generator=gen, device=device).to(torch.bfloat16).view(torch.uint8)
+    else:       # (int8 rows of one scale, 2^-6)
+        kc = torch.randint(0, 100, shape, generator=gen, dtype=torch.uint8, device=device)
+        kc[..., D:D + 4] = torch.tensor([0, 0, 128, 60], dtype=torch.uint8, device=device)
+    vc = kc.flip(0)
+    bt = torch.zeros((R, max(need)), dtype=torch.int32, device=device)
+    blocks = torch.randperm(sum(need), generator=gen, device=device).to(torch.int32)
+    for r, n in enumerate(need):
+        bt[r, :n] = blocks[sum(need[:r]):sum(need[:r + 1])]
+    bt[:sharers, :P // B] = bt[0, :P // B]
+    starts = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    q = torch.randn((int(starts[-1]), HQ, D), generator=gen, device=device).to(torch.bfloat16)
+    qsl, sl = torch.from_numpy(starts).to(device), torch.from_numpy(lens).to(device)
+    of = [0 if r < sharers else -1 for r in range(R)]
+    runs = []
+    for s in (kvq.get_shared_prefix_metadata(R, HQ, HKV, D, lens, starts, [P], of, 0, dtype),
+              kvq.get_scheduler_metadata(R, HQ, HKV, D, lens, starts, True, 0, dtype)):
+        out = torch.full_like(q, float("nan"))
+        ws = torch.empty(max(256, s.workspace_bytes), dtype=torch.uint8, device=device)
+        call = kvq.prepare_attention_with_kv_cache(s, q, kc, vc, qsl, sl, bt, D ** -0.5, True, 0, 0.0, 1.0, 1.0, out, ws,
+                                                   dtype, HKV)
+        runs.append((call, s, out, (ws, q, kc, vc, qsl, sl, bt)))
+    return runs
+
+
+def _us(call, n=20):
+    times = []
+    for _ in range(5):
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        call()
+        a.record()
+        for _ in range(n):
+            call()
+        b.record()
+        torch.cuda.synchronize()
+        times.append(1e3 * a.elapsed_time(b) / n)
+    return sorted(times)[2]
+
+
+@pytest.mark.parametrize("dtype,P,own,new,sharers", [
+    ("int8_per_token_head", 32, [8192] * 64, [1] * 64, 2),      # few units, a long decode on all SMs
+    ("int8_per_token_head", 2048, [8192] * 64, [1] * 64, 64),
+    ("auto", 32, [3072] * 64, [1] * 64, 2),
+    ("int8_per_token_head", 2048, [2048] * 64, [1, 3] * 32, 64),  # both row classes
+])
+def test_a_long_decode_beside_short_units(cuda_device, dtype, P, own, new, sharers):
+    """Sharing saves reads here or next to none; it must not cost half as much again
+    (CTAs behind a unit on its SM took 2.4 times as long as the others: 1.8 to 2.5 times
+    the unshared call)."""
+    (a, sa, oa, _), (b, sb, ob, _) = runs = _calls(dtype, P, own, new, sharers, cuda_device)
+    assert sa.rect_info()["num_units"] > 0 and sb.rect_info()["num_units"] == 0
+    shared, unshared = _us(a), _us(b)
+    for _, s, _, _ in runs:
+        s.check_device()
+        s.close()
+    # both are within half a bf16 step (2^-9 of the value) plus their fp32 sums of the exact result
+    x, y = oa.double(), ob.double()
+    assert (x - y).abs().max() <= 2.0 ** -7 * y.abs().max()
+    assert shared <= 1.5 * unshared, f"{shared:.0f} us with the prefix shared, {unshared:.0f} us without"
