@@ -990,6 +990,10 @@ int launch_int4_decode(const AttnParams& p, const PrefillMaps& maps, cudaStream_
     return KVQ_E_CUDA;
   }
   const int groups = ge.segments * ge.hsplit, least = (groups + ge.gpc - 1) / ge.gpc;
+  // (beside units a CTA an SM that they leave: one more would wait for a unit to end.
+  // 64 requests, 16 of them behind 2,048 keys and all of some 1,000 of their own, 16 / 4 heads
+  // of 256: 78 us with a CTA for every SM of the device, 55 so)
+  if (p.decode_sms > 0 && p.decode_sms < sms) sms = p.decode_sms;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(least > sms ? least : groups < sms ? groups : sms));
   cfg.blockDim = dim3((unsigned)(32 * ge.hg * ge.gpc));

@@ -41,6 +41,7 @@ struct DecodeLaunch {
   int64_t warp_off = 0;    // its first entry of the warp table
   int64_t num_chunks = 0;  // length of its flat chunk sequence
   int num_warps = 0;       // warps the sequence is cut among
+  int sms = 0;             // SMs that it is cut for (0: all)
   bool lockstep = false;   // every kv head of a request cut at the same chunks
 };
 
@@ -1033,6 +1034,7 @@ int plan_attention(int num_req, int heads_q, int heads_kv, int head_dim, const i
     for (const Tile& t : tiles[cls]) T += t.c_hi - t.c_lo;
     dl.num_chunks = T;
     if (T == 0) continue;
+    if (decode_sms > 0) dl.sms = (int)sms_for(cls);
     // Head-major order when every request has one tile per kv head in this
     // class (row tiles of up to 16 rows: always, for decodes).
     bool ls = lockstep && tiles[cls].size() % (size_t)heads_kv == 0;
@@ -1578,6 +1580,7 @@ int kvq_attention_with_kv_cache(const kvq_sched_t* s, int heads_q, int heads_kv,
     p.warp_seg = reinterpret_cast<const WarpSeg*>(b + s->d_warps_off) + dl.warp_off;
     p.num_chunks = dl.num_chunks;
     p.num_warps = dl.num_warps;
+    p.decode_sms = dl.sms;
     if (kvq::is_int4(s->dtype) &&
         !encode_int4_maps(&maps, key_cache, value_cache, head_dim, heads_kv, num_blocks * (int64_t)block_size,
                           kvq::int4_geom(heads_kv, head_dim, cls + 1)))

@@ -364,6 +364,7 @@ struct AttnParams {
   const struct WarpSeg* warp_seg;  // per warp: its segment and the piece of its first chunk
   int64_t num_chunks;          // length of the launch's flat chunk sequence
   int num_warps;               // warps it is cut among (grid * kDecodeWarps)
+  int decode_sms;              // SMs it is cut for, beside units (0: all)
   const MergeItem* merges;
   const PrefillTile* prefill_tiles;
   int32_t num_prefill_tiles;

@@ -1,5 +1,5 @@
 """The decode beside the units of a shared prefix: requests whose own contexts are
-long.  Its CTAs on SMs that units held before have to run like the others."""
+long.  Times are compared with those of the same batch planned without sharing."""
 import numpy as np
 import pytest
 import torch
@@ -11,7 +11,7 @@ pytestmark = pytest.mark.gpu
 HQ, HKV, D, B = 32, 8, 128, 16
 
 
-def _calls(dtype, P, own, new, sharers, device):
+def _calls(dtype, P, own, new, sharers, device, HQ=HQ, HKV=HKV, D=D):
     """One batch planned with its prefix and without: (call, schedule) of each."""
     R = len(own)
     lens = np.array([P + n for n in own], np.int32)
@@ -20,9 +20,11 @@ def _calls(dtype, P, own, new, sharers, device):
     shape = (sum(need), B, HKV, kvq.cache_row_bytes(dtype, D))
     if dtype == "auto":
         kc = torch.randn((*shape[:3], D), generator=gen, device=device).to(torch.bfloat16).view(torch.uint8)
-    else:       # (int8 rows of one scale, 2^-6)
+    else:       # (rows of one scale, 2^-6; 4-bit ones of multipliers of 50)
         kc = torch.randint(0, 100, shape, generator=gen, dtype=torch.uint8, device=device)
-        kc[..., D:D + 4] = torch.tensor([0, 0, 128, 60], dtype=torch.uint8, device=device)
+        at = D // 2 if dtype == "int4_per_token_head" else D
+        kc[..., at:at + 4] = torch.tensor([0, 0, 128, 60], dtype=torch.uint8, device=device)
+        kc[..., at + 4:at + 12] = 50
     vc = kc.flip(0)
     bt = torch.zeros((R, max(need)), dtype=torch.int32, device=device)
     blocks = torch.randperm(sum(need), generator=gen, device=device).to(torch.int32)
@@ -58,6 +60,20 @@ def _us(call, n=20):
     return sorted(times)[2]
 
 
+def _compare(runs):
+    """Times of the shared and the unshared call, whose results agree."""
+    (a, sa, oa, _), (b, sb, ob, _) = runs
+    assert sa.rect_info()["num_units"] > 0 and sb.rect_info()["num_units"] == 0
+    times = _us(a), _us(b)
+    for _, s, _, _ in runs:
+        s.check_device()
+        s.close()
+    # both are within half a bf16 step (2^-9 of the value) plus their fp32 sums of the exact result
+    x, y = oa.double(), ob.double()
+    assert (x - y).abs().max() <= 2.0 ** -7 * y.abs().max()
+    return times
+
+
 @pytest.mark.parametrize("dtype,P,own,new,sharers", [
     ("int8_per_token_head", 32, [8192] * 64, [1] * 64, 2),      # few units, a long decode on all SMs
     ("int8_per_token_head", 2048, [8192] * 64, [1] * 64, 64),
@@ -68,13 +84,15 @@ def test_a_long_decode_beside_short_units(cuda_device, dtype, P, own, new, share
     """Sharing saves reads here or next to none; it must not cost half as much again
     (CTAs behind a unit on its SM took 2.4 times as long as the others: 1.8 to 2.5 times
     the unshared call)."""
-    (a, sa, oa, _), (b, sb, ob, _) = runs = _calls(dtype, P, own, new, sharers, cuda_device)
-    assert sa.rect_info()["num_units"] > 0 and sb.rect_info()["num_units"] == 0
-    shared, unshared = _us(a), _us(b)
-    for _, s, _, _ in runs:
-        s.check_device()
-        s.close()
-    # both are within half a bf16 step (2^-9 of the value) plus their fp32 sums of the exact result
-    x, y = oa.double(), ob.double()
-    assert (x - y).abs().max() <= 2.0 ** -7 * y.abs().max()
+    shared, unshared = _compare(_calls(dtype, P, own, new, sharers, cuda_device))
     assert shared <= 1.5 * unshared, f"{shared:.0f} us with the prefix shared, {unshared:.0f} us without"
+
+
+@pytest.mark.parametrize("D,HQ,HKV,P,own,sharers", [(256, 16, 4, 2048, 1000, 16), (256, 16, 4, 8192, 8000, 16),
+                                                    (64, 8, 2, 4096, 2000, 64)])
+def test_a_4_bit_decode_on_the_sms_that_units_leave(cuda_device, D, HQ, HKV, P, own, sharers):
+    """It is cut for those SMs: with a CTA for each SM of the device the last ones
+    waited for whole units (1.3 to 1.4 times the time)."""
+    runs = _calls("int4_per_token_head", P, [own // 2 + 16 * r for r in range(64)], [1] * 64, sharers, cuda_device, HQ, HKV, D)
+    shared, unshared = _compare(runs)
+    assert shared <= 1.15 * unshared, f"{shared:.0f} us with the prefix shared, {unshared:.0f} us without"
