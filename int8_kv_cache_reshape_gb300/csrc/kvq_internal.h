@@ -378,7 +378,8 @@ struct AttnParams {
   float sm_scale, soft_cap, k_scale, v_scale;
   const float* alibi_slopes;   // [Hq] or null: score += slope * (key - query position)
   const float* sinks;          // [Hq] or null: one extra logit in the softmax normaliser
-  bool beside_prefill;         // 4-bit decode: the kernel ahead of it is this call's prefill
+  bool beside_prefill;         // 4-bit decode: the kernel ahead of it is this call's prefill or one
+                               // that beside_rect names
   bool beside_rect;            // decode: the kernel ahead of it is this call's rectangular
                                // attention, or another decode beside that one
 };

@@ -96,3 +96,11 @@ def test_a_4_bit_decode_on_the_sms_that_units_leave(cuda_device, D, HQ, HKV, P, 
     runs = _calls("int4_per_token_head", P, [own // 2 + 16 * r for r in range(64)], [1] * 64, sharers, cuda_device, HQ, HKV, D)
     shared, unshared = _compare(runs)
     assert shared <= 1.15 * unshared, f"{shared:.0f} us with the prefix shared, {unshared:.0f} us without"
+
+
+def test_both_classes_of_a_4_bit_decode(cuda_device):
+    """Tiles of 4 and of 12 rows a kv head, each class cut for its part of the SMs left:
+    one class after the other took 1.3 times the unshared call, 1.8 times both together."""
+    runs = _calls("int4_per_token_head", 2048, [2048] * 64, [1, 3] * 32, 64, cuda_device)
+    shared, unshared = _compare(runs)
+    assert shared <= unshared, f"{shared:.0f} us with the prefix shared, {unshared:.0f} us without"
