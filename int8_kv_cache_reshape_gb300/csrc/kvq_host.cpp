@@ -324,12 +324,22 @@ struct RectTile {
 
 // Time of a unit, in microseconds: a fixed part (first instructions, plan, first
 // keys, Q, the rows' way out) and one for each KV tile, by the row tiles that share
-// it; of a decode of so many bytes on so many SMs; and what it takes when it does
-// not fit beside the units.  Measured; they only decide how the keys are cut.
-constexpr double kRectStart = 8.0, kDecodeStart = 8.0, kDecodeBytesPerUs = 30.0e3, kDecodeBehind = 15.0, kMergeStart = 5.0;
+// it; of a decode of so many bytes on so many SMs.  Measured (a KV tile's by units of 16
+// and of 64 of them, alone; beside a decode it takes about a fifth longer); they only
+// decide how the keys are cut.
+constexpr double kRectStart = 8.0, kDecodeStart = 8.0, kMergeStart = 5.0, kTileBeside = 1.2;
 double rect_tile_us(int dtype, int head_dim, bool two) {
-  const double us = head_dim >= 256 ? 1.5 : head_dim >= 128 ? (two ? 1.95 : 1.2) : (two ? 1.4 : 0.9);
-  return kvq::is_per_token_head(dtype) ? 1.25 * us : us;
+  // per-tensor fp8 rows, 8- and 4-bit rows with scales, bf16 rows
+  static constexpr double us[5][3] = {
+      {1.15, 1.30, 1.60}, {1.70, 2.30, 2.40},  // head_dim 64, one row tile and two
+      {1.90, 2.20, 2.40}, {2.10, 2.55, 3.55},  // 128
+      {1.45, 1.60, 1.65},                      // 256
+  };
+  const int kind = dtype == KVQ_AUTO ? 2 : kvq::is_per_token_head(dtype) ? 1 : 0;
+  return us[head_dim >= 256 ? 4 : 2 * (head_dim >= 128) + two][kind];
+}
+double decode_us(double bytes, int dtype, int64_t sms) {
+  return kDecodeStart + bytes / ((double)sms * (dtype == KVQ_AUTO ? 34.0e3 : 32.0e3));
 }
 
 // Cut the row tiles' keys among CTAs (one per SM) so that the last one ends
@@ -373,15 +383,19 @@ int plan_rect(std::vector<RectTile>& tiles, int dtype, int heads_kv, int head_di
     }
     const int64_t waves = ceil_div(n, sms);
     // (partials: written and read once, in L2 mostly)
-    // the decode on the SMs left, or among and behind the units
+    // The decode on the SMs left, or on all: its segments are equal, so one behind a
+    // unit on its SM ends a whole decode later than the unit.  (64 requests of some 8,300
+    // int8 keys, two of them with 8,192 in common, 32 / 8 heads of 128: 381 us with the decode
+    // on all SMs behind 8 units, 246 with it beside them, 243 without sharing.)
     const int64_t left = beside_bytes > 0 ? std::max<int64_t>(0, sms - n) : 0;
-    const double all = (total + (double)beside_bytes / kDecodeBytesPerUs) / sms;
-    const double beside = std::max(longest, kDecodeStart + (double)beside_bytes / ((double)left * kDecodeBytesPerUs));
+    const double beside = left > 0 ? std::max(kRectStart + (longest - kRectStart) * kTileBeside,
+                                              decode_us((double)beside_bytes, dtype, left))
+                                   : 0.0;
     // (units of one length run in waves; of several, longest first, they fill up)
     const double units_us = shortest > 0.9 * longest ? (double)waves * longest
                             : n <= sms               ? longest
                                                      : std::max(longest, total / sms + 0.5 * total / (double)n);
-    const double behind = std::max(units_us, all) + (beside_bytes > 0 ? kDecodeBehind : 0.0);
+    const double behind = units_us + (beside_bytes > 0 ? decode_us((double)beside_bytes, dtype, sms) : 0.0);
     const bool fits = left > 0 && beside <= behind;
     const double us = (fits ? beside : behind) + (rows > 0 ? kMergeStart : 0.0) + (double)rows * head_dim * 8.0 / 5.0e6;
     if (best_us == 0.0 || us < best_us) {
