@@ -49,8 +49,10 @@ int rect_merge(const AttnParams& p, const RectParams& rp, const RectMergePlan& m
 template <int D>
 int rect_merge_d(const AttnParams& p, const RectParams& rp, const RectMergePlan& m, void* stream) {
   // Warps a row: as many as have partials to read, while all rows' warps are on
-  // the device at once (32 an SM at the kernel's registers).
-  const int64_t room = (int64_t)m.sms * 32 / (m.rows > 0 ? m.rows : 1);
+  // the device at once.  (Calls of 8-bit rows behind 8,192 keys, 4 / 2 / 1 warps a row: head_dim
+  // 128, 512 rows 24.1 / 24.6 / 25.7 us, 1,216 rows 36.7 / 33.9 / 34.4, 2,048 rows 47.8 / 44.6 /
+  // 43.0; head_dim 256, 256 rows 23.5 / 24.8 / 26.7, 1,536 rows 64.7 / 61.8 / 59.2.)
+  const int64_t room = (int64_t)m.sms * 8 * rect_merge_ctas(D) / (m.rows > 0 ? m.rows : 1);
   if (m.most_splits > 16 && room >= 4) return rect_merge<D, 4, 8>(p, rp, m, stream);
   if (m.most_splits > 8 && room >= 2) return rect_merge<D, 2, 8>(p, rp, m, stream);
   return rect_merge<D, 1, 8>(p, rp, m, stream);

@@ -173,6 +173,10 @@ __global__ void __launch_bounds__(kMergeThreads) merge_splits_kernel(const AttnP
 // through the code once before, with every access switched off, so that its
 // instructions are there (some 250 cycles for each 128 bytes of code otherwise, more
 // than the work).
+// CTAs of 2 or 4 warps a row that an SM holds (60, 75 and 115 registers a thread).  Not
+// a launch bound: with one, a warp a row at head_dim 128 takes 77 registers in place of 64,
+// 4,096 rows 67 us in place of 65.
+constexpr int rect_merge_ctas(int head_dim) { return head_dim >= 256 ? 2 : head_dim >= 128 ? 3 : 4; }
 template <int D, int PARTS, int BATCH>
 __global__ void __launch_bounds__(256) merge_rect_kernel(const AttnParams p, const RectParams rp, int ctas_of_item) {
   constexpr int kDims = D / 32, kRows = 8 / PARTS;
