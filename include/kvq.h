@@ -333,7 +333,8 @@ KVQ_API int kvq_get_scheduler_metadata(int num_req, int heads_q, int heads_kv,
  * Requests of up to 16 (query, head) rows per kv head share; larger ones
  * (prompts) read their whole context as without a prefix.  A prefix is shared
  * up to a multiple of 32 keys, and from two requests on; a batch of 4-bit rows
- * that would save less than 18 MB of cache reads is planned without sharing. */
+ * that would save less than 18 MB of cache reads is planned without sharing.
+ * (Two or three requests behind tens of thousands of keys are faster unshared.) */
 KVQ_API int kvq_get_shared_prefix_metadata(int num_req, int heads_q, int heads_kv,
                                            int head_dim, const int32_t* seq_lens_host,
                                            const int32_t* query_start_loc_host,
@@ -401,16 +402,20 @@ KVQ_API int kvq_get_cross_attention_metadata(int num_req, int heads_q, int heads
  *                           sum_j e^z_j) (use_sink of [P2]).
  *   k_scale, v_scale        per-tensor scales (per-tensor fp8 only), folded
  *                           into the scores and the output.
- *   out                     device bf16 [sum Q, heads_q, head_dim].
+ *   out                     device bf16 [sum Q, heads_q, head_dim], contiguous,
+ *                           16-byte aligned.
  *   workspace               device scratch of >= the scheduler's
  *                           workspace_bytes (256-byte aligned; may be NULL
  *                           when that is 0).  Calls sharing one workspace
  *                           or one schedule must be ordered on one stream.
  * Query row i of a request sits at position L - Q + i; key j is visible iff
- * (!causal || j <= p) and (window <= 0 || p - j < window).  The call
- * launches the prefill kernel (if the schedule has prefill tiles), the decode
- * kernel of each row-tile class, and the merge of the cut decode tiles (the
- * schedule's num_kernel_launches), in that order on `stream`.  A kernel that
+ * (!causal || j <= p) and (window <= 0 || p - j < window).  On `stream` the call
+ * launches, of what its schedule holds (num_kernel_launches of it): the prefill
+ * kernel; the units of shared prefixes or encoders; the decode kernel of each
+ * row-tile class (beside the units where there are any: it is resident before
+ * they end, and ends after them); and one merge, of the cut decode tiles or, for
+ * schedules of shared prefixes and encoders, of those together with the units'
+ * rows.  A kernel that
  * gives up one of its bounded waits writes NaN rows and sets the schedule's
  * error word (kvq_sched_check_device). */
 KVQ_API int kvq_attention_with_kv_cache(const kvq_sched_t* sched, int heads_q,

@@ -740,11 +740,13 @@ int plan_attention(int num_req, int heads_q, int heads_kv, int head_dim, const i
   //    first row there (-1: none).  Requests with more than kTileMaxRows rows
   //    run whole on the prefill: their work is products, which sharing does
   //    not save.  What sharing saves is cache reads, (members - 1) times the
-  //    prefix; it costs the units' fixed time and a merge of every row.  For two
-  //    requests and 128 keys already it wins on all rows but 4-bit ones (12 against
-  //    16 us at 32 / 8 heads of 128), whose decode reads half the bytes at a higher
-  //    rate: 12 against 11 us for 1 MB saved, 15 against 15 for 18 MB, 18 against
-  //    26 for 81 MB, so below kPrefixMinBytes4 they stay unshared.
+  //    prefix; it costs the units' fixed time and a merge of every row.  At 32 / 8
+  //    heads of 128 and 60 to 200 own keys two requests behind 128 keys win already on
+  //    all rows but 4-bit ones (12 against 16 us), and four behind 32,768 (57 against
+  //    62; two there lose, 54 against 41).  4-bit rows' decode reads half the bytes at a
+  //    higher rate: 12 against 11 us for 1 MB saved, 15 against 15 for 18 MB, 16 against
+  //    26 for 81 MB, so below kPrefixMinBytes4 they stay unshared.  Before own contexts of
+  //    up to 12,000 keys a prefix that saves little costs up to a tenth of the call.
   //    KVQ_PREFIX_MIN_BYTES (tests, benchmarks) sets another limit for all rows;
   //    KVQ_RECT_TILES forces the KV tiles of a unit.
   std::vector<RectTile> rect;

@@ -380,9 +380,10 @@ int launch(const RotaryArgs& a, bool interleaved, void* stream) {
   const uint64_t share = (((uint64_t)kv_w << 32) + (uint64_t)warps - 1) / (uint64_t)warps;
   const int64_t blocks = std::min<int64_t>((warps + kThreads / 32 - 1) / (kThreads / 32), (int64_t)sms * 2);
   // The next unit's rows are fetched into L2 a unit ahead where they are not there
-  // already, as a projection's output is up to about half of it: 20,011 tokens of 32 / 8
-  // heads of 128 (246 MB) take 80 us in place of 86 (4-bit rows; int8 82 / 89), but 4,099 of
-  // 16 / 2 heads of 256 (42 MB) 14.9 in place of 13.6.
+  // already, as a projection's output is up to about half of it.  Without / with, int8 rows:
+  // 32 / 8 heads of 128, 42 MB 16.6 / 16.7 us, 64 MB 24.6 / 24.1, 100 MB 39.7 / 37.1, 246 MB 91
+  // / 83; 16 / 16 of 64, 42 MB 17.9 / 17.6, 64 MB 27.5 / 26.0; 16 / 2 of 256, 64 MB 23.7 / 24.5,
+  // 100 MB 37.7 / 37.0: the sides meet between 42 and 90 MB.
   const int64_t in_bytes = 2 * a.num_tokens * ((int64_t)a.heads_q + 2 * a.heads_kv) * D;
   const bool from_memory = in_bytes > (64 << 20);
   return interleaved
