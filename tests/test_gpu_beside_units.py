@@ -77,7 +77,7 @@ def _compare(runs):
 @pytest.mark.parametrize("dtype,P,own,new,sharers", [
     ("int8_per_token_head", 32, [8192] * 64, [1] * 64, 2),      # few units, a long decode on all SMs
     ("int8_per_token_head", 2048, [8192] * 64, [1] * 64, 64),
-    ("auto", 32, [3072] * 64, [1] * 64, 2),
+    ("auto", 32, [3000] * 64, [1] * 64, 2),
     ("int8_per_token_head", 2048, [2048] * 64, [1, 3] * 32, 64),  # both row classes
 ])
 def test_a_long_decode_beside_short_units(cuda_device, dtype, P, own, new, sharers):
